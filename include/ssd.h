@@ -347,6 +347,161 @@ int ssd_scan_set_config(const ssd_shape* shape, const ssd_scan_config* config);
  * table entry exists, 0 if not, -SSD_ERR_INVALID_ARG for a bad shape. */
 int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
 
+/* Layer operators around the scan.  The pages name no kernels for them; they
+ * are what a layer needs beside the scan and the gated norm: the short causal
+ * convolution in front of it, the selective scan of layers with a decay per
+ * channel and state, one token of each for decoding, and the residual / norm
+ * step between layers.
+ *
+ * Sequences of unequal lengths: `lengths` (batch) int32 device memory or NULL.
+ * Positions from lengths[b] on (clamped to [0, seqlen]) are padding: their
+ * outputs and gradients are 0, the final state is the one after lengths[b]
+ * positions, and a length of 0 carries the initial state through.
+ *
+ * State caches of the single-token calls: `state` holds nslots states, and
+ * slots (batch) int32 device memory names each batch row's.  A row whose slot
+ * is negative or >= nslots is empty: its output is 0 and no state is touched.  A
+ * slot may be named once per call.  slots NULL: row b uses slot b.
+ *
+ * Row strides are the elements between consecutive positions (batch rows in
+ * the single-token calls) of an input that is a column range of a wider
+ * tensor, batch strides those between its batch rows; a row stride of 0 means
+ * dense (the batch stride is then ignored).  Everything else is dense and row-major.  Pointers
+ * must be aligned to their element size; 16-byte alignment of pointers and
+ * rows lets the kernels use wide accesses.  bf16 inputs give bf16 or f32
+ * outputs, f32 inputs f32 ones (else SSD_ERR_UNSUPPORTED).  Every call is
+ * asynchronous on `stream`, waits for nothing on the device, and returns
+ * SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE (workspace NULL,
+ * misaligned or too small) or SSD_ERR_CUDA.  All sums over rows, positions or
+ * channels are taken in a fixed order in f32: repeated calls give bit-identical
+ * results. */
+
+/* Causal depthwise convolution over the last `width` positions, in channels:
+ *   u[t, c] = bias[c] + sum_{k < width} w[c, k] x[t - width + 1 + k, c]
+ *   y = u * sigmoid(u) if silu, else u
+ * x before position 0 is init_state (batch, width - 1, channels), oldest
+ * first, or 0.  x (batch, seqlen, channels) in_dtype, w (channels, width) f32,
+ * bias (channels) f32 or NULL, y (batch, seqlen, channels) out_dtype;
+ * final_state (batch, width - 1, channels) in_dtype or NULL: the last
+ * width - 1 inputs.  2 <= width <= 4.  init_state and final_state must not
+ * overlap. */
+typedef struct {
+  int64_t batch, seqlen, channels, width;
+  int64_t x_row_stride, x_batch_stride;
+  int32_t silu;
+  int32_t in_dtype;  /* x, states, dy                */
+  int32_t out_dtype; /* y; dx and dinit_state        */
+} ssd_conv_shape;
+
+int ssd_causal_conv_fwd(const ssd_conv_shape* shape, const void* x, const float* w,
+                        const float* bias, const void* init_state, const int32_t* lengths, void* y,
+                        void* final_state, void* stream);
+
+/* Gradients of <dy, y> + <dfinal_state, final_state>: dx (dense) and
+ * dinit_state in out_dtype, dw (channels, width) and dbias (channels) f32.
+ * dfinal_state (in_dtype), dbias and dinit_state may be NULL.  Workspace of
+ * ssd_causal_conv_workspace_size bytes (0 for a rejected shape), caller-owned. */
+size_t ssd_causal_conv_workspace_size(const ssd_conv_shape* shape);
+int ssd_causal_conv_bwd(const ssd_conv_shape* shape, const void* x, const float* w,
+                        const float* bias, const void* init_state, const int32_t* lengths,
+                        const void* dy, const void* dfinal_state, void* dx, float* dw,
+                        float* dbias, void* dinit_state, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* One token (shape->seqlen 1): x, y (batch, channels); state (nslots,
+ * width - 1, channels) in_dtype, read and shifted by one in place. */
+int ssd_causal_conv_step(const ssd_conv_shape* shape, const void* x, void* state, const float* w,
+                         const float* bias, const int32_t* slots, int64_t nslots, void* y,
+                         void* stream);
+
+/* Selective scan: for channel d of group g(d) = d / (channels / ngroups), with
+ * delta = softplus(dt + dt_bias) (softplus(v) = v above 20),
+ *   h[n] <- exp(delta A[d, n]) h[n] + delta x B[g, n]
+ *   y     = sum_n C[g, n] h[n] + D[d] x,   out = y z sigmoid(z), or y without z.
+ * x, dt, z (batch, seqlen, channels), B, C (batch, seqlen, ngroups, dstate)
+ * in_dtype; dt_bias, D (channels) f32 or NULL; A (channels, dstate) f32;
+ * init_states, final_states (batch, channels, dstate) f32 or NULL; out (batch,
+ * seqlen, channels) out_dtype.  channels a multiple of ngroups, dstate <= 64
+ * (<= 256 in ssd_selective_step), seqlen at most 2^21.  Workspace of the size
+ * query's bytes (0 for a rejected shape), 16-byte aligned, caller-owned. */
+typedef struct {
+  int64_t batch, seqlen, channels, dstate, ngroups;
+  int64_t z_row_stride, b_row_stride, c_row_stride;
+  int64_t z_batch_stride, b_batch_stride, c_batch_stride;
+  int32_t in_dtype;  /* x, dt, B, C, z, dout     */
+  int32_t out_dtype; /* out; dx, ddt and dz      */
+} ssd_selective_shape;
+
+size_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_shape* shape);
+int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, const void* dt,
+                           const float* dt_bias, const float* A, const void* B, const void* C,
+                           const float* D, const void* z, const float* init_states,
+                           const int32_t* lengths, void* out, float* final_states,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of <dout, out> + <dfinal_states, final_states>, from the forward's
+ * inputs (the states are formed again): dx, ddt, dz (dense, out_dtype; dz with
+ * z), dA (channels, dstate), dB, dC (batch, seqlen, ngroups, dstate), dD,
+ * ddt_bias (channels), dinit_states f32.  dfinal_states, dD, ddt_bias and
+ * dinit_states may be NULL. */
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_shape* shape);
+int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, const void* dt,
+                           const float* dt_bias, const float* A, const void* B, const void* C,
+                           const float* D, const void* z, const float* init_states,
+                           const int32_t* lengths, const void* dout, const float* dfinal_states,
+                           void* dx, void* ddt, float* dA, float* dB, float* dC, float* dD,
+                           void* dz, float* ddt_bias, float* dinit_states, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* One token of the selective scan (shape->seqlen 1): x, dt, z, y (batch,
+ * channels), B, C (batch, ngroups, dstate); state (nslots, channels, dstate)
+ * f32, updated in place. */
+int ssd_selective_step(const ssd_selective_shape* shape, const void* x, const void* dt,
+                       const float* dt_bias, const float* A, const void* B, const void* C,
+                       const float* D, const void* z, float* state, const int32_t* slots,
+                       int64_t nslots, void* y, void* stream);
+
+/* One token of ssd_fwd's scan: x, y (batch, nheads, headdim), dt (batch,
+ * nheads), B, C (batch, ngroups, dstate); state (nslots, nheads, headdim,
+ * dstate) f32, updated in place.  shape->seqlen and chunk_size are ignored. */
+int ssd_step(const ssd_shape* shape, const void* x, const void* dt, const float* dt_bias,
+             const float* A, const void* B, const void* C, const float* D, float* state,
+             const int32_t* slots, int64_t nslots, void* y, void* stream);
+
+/* Block norm, the step between two layers: with a layer's output o, the
+ * residual r and rstd(v) = 1 / sqrt(mean(v^2) + eps) over a row,
+ *   t = o rstd(o) w_post (w_post NULL: t = o)
+ *   r' = r + scale * gate * t,   h = r' rstd(r') w_pre
+ * r, r' (rows, features) res_dtype; o, h (rows, features) in_dtype; w_pre,
+ * w_post (features) f32; gate (ngates, features) f32, row i using gate row
+ * i / (rows / ngates) (one row: shared by all; one per sequence; one per row),
+ * or NULL with ngates 0.  h is formed from r' before r' is rounded.
+ * features <= 8192; rows a multiple of ngates; res_dtype f32 when in_dtype is.
+ * r' may be written over r and h over o. */
+typedef struct {
+  int64_t rows, features, ngates;
+  float eps, scale;
+  int32_t in_dtype;  /* o, h, dh, do                  */
+  int32_t res_dtype; /* residual, residual_out and their gradients */
+} ssd_block_norm_shape;
+
+int ssd_block_norm_fwd(const ssd_block_norm_shape* shape, const void* residual, const void* o,
+                       const float* w_pre, const float* w_post, const float* gate,
+                       void* residual_out, void* h, void* stream);
+
+/* Gradients of <dh, h> + <dresidual_out, r'> from the forward's inputs:
+ * dresidual (res_dtype), d_o (in_dtype), dw_pre, dw_post (features), dgate
+ * (ngates, features) f32.  dresidual_out may be NULL (zero).  dw_post and
+ * dgate are required exactly when w_post and gate are given.  Workspace of
+ * ssd_block_norm_workspace_size bytes, 16-byte aligned, caller-owned; its size
+ * depends on the current device's SM count. */
+size_t ssd_block_norm_workspace_size(const ssd_block_norm_shape* shape);
+int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, const void* o,
+                       const float* w_pre, const float* w_post, const float* gate, const void* dh,
+                       const void* dresidual_out, void* dresidual, void* d_o, float* dw_pre,
+                       float* dw_post, float* dgate, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 /* Diagnostic: one tcgen05 tile product on the current device,
  * D[128][nn] = A[128][k] * B[nn][k]^T (A, B bf16 row-major, D f32 row-major,
  * all device memory), with A and B staged in shared memory K-major (0) or

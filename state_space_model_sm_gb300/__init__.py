@@ -417,3 +417,17 @@ def profile_read(max_kernels: int = 64) -> dict:
 def launch_count() -> int:
     """Kernels launched by libssd in this process so far."""
     return int(_native.load().ssd_launch_count())
+
+
+_LAYER_OPS = ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
+              "selective_scan_bwd", "selective_step", "ssd_step", "block_norm_fwd",
+              "block_norm_bwd")
+
+
+def __getattr__(name):
+    """The layer operators (``layer_ops``), loaded with torch on first use."""
+    if name in _LAYER_OPS:
+        from . import layer_ops
+        globals().update({k: getattr(layer_ops, k) for k in _LAYER_OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

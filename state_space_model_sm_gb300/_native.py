@@ -109,9 +109,36 @@ class NormConfig(ctypes.Structure):
                 ("ctas_per_sm", ctypes.c_int32)]
 
 
+class ConvShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_row_stride", ctypes.c_int64), ("x_batch_stride", ctypes.c_int64),
+                ("silu", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class SelectiveShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("z_row_stride", ctypes.c_int64),
+                ("b_row_stride", ctypes.c_int64), ("c_row_stride", ctypes.c_int64),
+                ("z_batch_stride", ctypes.c_int64), ("b_batch_stride", ctypes.c_int64),
+                ("c_batch_stride", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class BlockNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("features", ctypes.c_int64),
+                ("ngates", ctypes.c_int64), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _SP = ctypes.POINTER(Shape)
 _NP = ctypes.POINTER(NormShape)
+_CP = ctypes.POINTER(ConvShape)
+_EP = ctypes.POINTER(SelectiveShape)
+_BP = ctypes.POINTER(BlockNormShape)
 SIGNATURES = {
     "ssd_fwd_workspace_size": ([_SP], ctypes.c_size_t),
     "ssd_bwd_workspace_size": ([_SP], ctypes.c_size_t),
@@ -144,6 +171,19 @@ SIGNATURES = {
     "ssd_bwd_dinit": ([_SP] + [_VP] * 7 + [_VP, ctypes.c_size_t, _VP], ctypes.c_int),
     "ssd_state_scan": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                         _VP, _VP, _VP, _VP], ctypes.c_int),
+    "ssd_causal_conv_fwd": ([_CP] + [_VP] * 8, ctypes.c_int),
+    "ssd_causal_conv_workspace_size": ([_CP], ctypes.c_size_t),
+    "ssd_causal_conv_bwd": ([_CP] + [_VP] * 12 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_causal_conv_step": ([_CP] + [_VP] * 5 + [ctypes.c_int64, _VP, _VP], ctypes.c_int),
+    "ssd_selective_scan_fwd_workspace_size": ([_EP], ctypes.c_size_t),
+    "ssd_selective_scan_fwd": ([_EP] + [_VP] * 13 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_selective_scan_bwd_workspace_size": ([_EP], ctypes.c_size_t),
+    "ssd_selective_scan_bwd": ([_EP] + [_VP] * 22 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_selective_step": ([_EP] + [_VP] * 10 + [ctypes.c_int64, _VP, _VP], ctypes.c_int),
+    "ssd_step": ([_SP] + [_VP] * 9 + [ctypes.c_int64, _VP, _VP], ctypes.c_int),
+    "ssd_block_norm_workspace_size": ([_BP], ctypes.c_size_t),
+    "ssd_block_norm_fwd": ([_BP] + [_VP] * 8, ctypes.c_int),
+    "ssd_block_norm_bwd": ([_BP] + [_VP] * 13 + [ctypes.c_size_t, _VP], ctypes.c_int),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,396 @@
+"""The operators a layer needs around the scan: the short causal convolution,
+the selective scan (a decay per channel and state), one token of each scan for
+decoding, and the residual / norm step between layers.
+
+Bindings of the same names as ``include/ssd.h`` declares (without the prefix):
+they check the tensors, allocate outputs and workspace, and pass pointers and
+the current stream.  Inputs are float32 or bfloat16 CUDA tensors; parameters
+(weights, biases, A, D) and scan states are float32.  Every call is
+asynchronous and its results are ordered on the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native
+
+_CODE = {torch.float32: 0, torch.bfloat16: 1}  # ssd_dtype
+_F32 = torch.float32
+
+
+def _fail(fn, status):
+    from . import SSDError
+    raise SSDError(fn, status)
+
+
+def _code(dtype):
+    c = _CODE.get(dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    return c
+
+
+def _lead(t, name, ndim):
+    """The call's first tensor: its rank, device and type."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    return t.device
+
+
+def _check(t, name, shape, dtype, device):
+    """Shape, type, device and density of t; its address (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, shape, lead, dtype, device):
+    """As _check for an input that may be a column range of a wider tensor: the
+    ``lead`` leading dimensions (batch, or batch and position) may be strided, the
+    others are dense.  Returns (address, elements between rows, elements between
+    batch rows); a row stride of 0 stands for a dense tensor."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0, 0
+    dense, stride = 1, t.stride()
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and stride[i] != dense:
+            raise ValueError(f"{name}: columns must be contiguous")
+        dense *= shape[i]
+    row = stride[lead - 1] if shape[lead - 1] > 1 else dense
+    if row < dense:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr(), row, stride[0]
+
+
+def _output(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, shape, dtype, device)
+    return t
+
+
+def _scratch(nbytes, device, workspace):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on {device}")
+    return workspace
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+# --------------------------------------------------------- causal convolution
+
+def _conv_inputs(x, w, bias, ndim, silu, out_dtype):
+    dev = _lead(x, "x", ndim)
+    C = x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError("w must be (channels, width)")
+    K = w.shape[1]
+    batch, T = x.shape[0], (x.shape[1] if ndim == 3 else 1)
+    xp, xs, xb = _rows(x, "x", x.shape, ndim - 1, x.dtype, dev)
+    wp = _check(w, "w", (C, K), _F32, dev)
+    bp = _check(bias, "bias", (C,), _F32, dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    shape = _native.ConvShape(batch, T, C, K, xs, xb, 1 if silu else 0, _code(x.dtype),
+                              _code(out_dtype))
+    return dev, shape, (batch, T, C, K), out_dtype, xp, wp, bp
+
+
+def causal_conv_fwd(x, w, bias=None, init_state=None, lengths=None, silu: bool = True,
+                    out_dtype=None, return_final_state: bool = True, y=None, final_state=None):
+    """y, final_state = the causal depthwise convolution of x over the last
+    ``width`` positions, with SiLU unless ``silu=False`` (``ssd_causal_conv_fwd``).
+
+    x (batch, seqlen, channels), may be a column range of a wider tensor; w
+    (channels, width) with width 2 to 4 and bias (channels,) float32; init_state
+    (batch, width - 1, channels) in x's type: the inputs before position 0;
+    lengths (batch,) int32: positions from lengths[b] on are padding.
+    final_state is the state after lengths[b] positions, which
+    ``causal_conv_step`` goes on from.  y is in ``out_dtype`` (x's type)."""
+    lib = _native.load()
+    dev, shape, (B, T, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 3, silu, out_dtype)
+    ip = _check(init_state, "init_state", (B, K - 1, C), x.dtype, dev)
+    lp = _check(lengths, "lengths", (B,), torch.int32, dev)
+    y = _output(y, "y", (B, T, C), odt, dev)
+    if return_final_state:
+        final_state = _output(final_state, "final_state", (B, K - 1, C), x.dtype, dev)
+    else:
+        final_state = None
+    st = lib.ssd_causal_conv_fwd(shape, xp, wp, bp, ip, lp, y.data_ptr(), _at(final_state),
+                                 _stream(dev))
+    if st:
+        _fail("ssd_causal_conv_fwd", st)
+    return y, final_state
+
+
+def causal_conv_bwd(x, w, bias, dy, init_state=None, lengths=None, silu: bool = True,
+                    dfinal_state=None, out_dtype=None, workspace=None, out=None):
+    """Gradients of <dy, y> + <dfinal_state, final_state> of ``causal_conv_fwd``
+    (``ssd_causal_conv_bwd``): a dict with dx (``out_dtype``, x's type by default),
+    dw and dbias (float32) and, with init_state, dinit_state (``out_dtype``)."""
+    lib = _native.load()
+    dev, shape, (B, T, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 3, silu, out_dtype)
+    ip = _check(init_state, "init_state", (B, K - 1, C), x.dtype, dev)
+    lp = _check(lengths, "lengths", (B,), torch.int32, dev)
+    gp = _check(dy, "dy", (B, T, C), x.dtype, dev)
+    fp = _check(dfinal_state, "dfinal_state", (B, K - 1, C), x.dtype, dev)
+    got = {} if out is None else out
+    out = dict(dx=_output(got.get("dx"), "dx", (B, T, C), odt, dev),
+               dw=_output(got.get("dw"), "dw", (C, K), _F32, dev),
+               dbias=_output(got.get("dbias"), "dbias", (C,), _F32, dev))
+    if init_state is not None:
+        out["dinit_state"] = _output(got.get("dinit_state"), "dinit_state", (B, K - 1, C), odt, dev)
+    nbytes = lib.ssd_causal_conv_workspace_size(shape)
+    ws = _scratch(max(nbytes, 1), dev, workspace)
+    st = lib.ssd_causal_conv_bwd(shape, xp, wp, bp, ip, lp, gp, fp, out["dx"].data_ptr(),
+                                 out["dw"].data_ptr(), out["dbias"].data_ptr(),
+                                 _at(out.get("dinit_state")), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream(dev))
+    if st:
+        _fail("ssd_causal_conv_bwd", st)
+    return out
+
+
+def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_dtype=None, y=None):
+    """One token of ``causal_conv_fwd`` (``ssd_causal_conv_step``): x, y (batch,
+    channels); state (nslots, width - 1, channels) in x's type, updated in place.
+    slots (batch,) int32 names each row's state; a negative one marks an empty
+    row, whose output is 0."""
+    lib = _native.load()
+    dev, shape, (B, _, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 2, silu, out_dtype)
+    sp = _check(state, "state", (state.shape[0], K - 1, C), x.dtype, dev)
+    lp = _check(slots, "slots", (B,), torch.int32, dev)
+    y = _output(y, "y", (B, C), odt, dev)
+    st = lib.ssd_causal_conv_step(shape, xp, sp, wp, bp, lp, state.shape[0], y.data_ptr(),
+                                  _stream(dev))
+    if st:
+        _fail("ssd_causal_conv_step", st)
+    return y
+
+
+# ------------------------------------------------------------- selective scan
+
+def _sel_inputs(x, dt, dt_bias, A, B, C, D, z, ndim, out_dtype):
+    dev = _lead(x, "x", ndim)
+    if B.dim() != ndim + 1 or A.dim() != 2:
+        raise ValueError("A must be (channels, dstate), B and C (..., ngroups, dstate)")
+    lead = x.shape[:-1]
+    ch, N, G = x.shape[-1], A.shape[1], B.shape[-2]
+    xd = x.dtype
+    gn = tuple(lead) + (G, N)
+    bp, bs, bb = _rows(B, "B", gn, ndim - 1, xd, dev)
+    cp, cs, cb = _rows(C, "C", gn, ndim - 1, xd, dev)
+    zp, zs, zb = _rows(z, "z", x.shape, ndim - 1, xd, dev)
+    ptrs = (_check(x, "x", x.shape, xd, dev), _check(dt, "dt", x.shape, xd, dev),
+            _check(dt_bias, "dt_bias", (ch,), _F32, dev), _check(A, "A", (ch, N), _F32, dev),
+            bp, cp, _check(D, "D", (ch,), _F32, dev), zp)
+    out_dtype = xd if out_dtype is None else out_dtype
+    T = lead[1] if ndim == 3 else 1
+    shape = _native.SelectiveShape(lead[0], T, ch, N, G, zs, bs, cs, zb, bb, cb, _code(xd),
+                                   _code(out_dtype))
+    return dev, shape, (lead[0], T, ch, N, G), out_dtype, ptrs
+
+
+def selective_scan_fwd(x, dt, dt_bias, A, B, C, D=None, z=None, init_states=None, lengths=None,
+                       out_dtype=None, return_final_states: bool = True, workspace=None, out=None,
+                       final_states=None):
+    """out, final_states = the selective scan of x (``ssd_selective_scan_fwd``):
+    h <- exp(delta A) h + delta x B with delta = softplus(dt + dt_bias) per channel,
+    y = C . h + D x, times silu(z) when z is given.
+
+    x, dt, z (batch, seqlen, channels); B, C (batch, seqlen, ngroups, dstate) (z, B
+    and C may be column ranges of wider tensors); A (channels, dstate), dt_bias and D
+    (channels,), init_states (batch, channels, dstate) float32; lengths (batch,)
+    int32: positions from lengths[b] on are padding.  dstate <= 64.  final_states
+    is what ``selective_step`` goes on from."""
+    lib = _native.load()
+    dev, shape, (Bt, T, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 3, out_dtype)
+    ip = _check(init_states, "init_states", (Bt, ch, N), _F32, dev)
+    lp = _check(lengths, "lengths", (Bt,), torch.int32, dev)
+    out = _output(out, "out", (Bt, T, ch), odt, dev)
+    if return_final_states:
+        final_states = _output(final_states, "final_states", (Bt, ch, N), _F32, dev)
+    else:
+        final_states = None
+    nbytes = lib.ssd_selective_scan_fwd_workspace_size(shape)
+    ws = _scratch(max(nbytes, 1), dev, workspace)
+    st = lib.ssd_selective_scan_fwd(shape, *p, ip, lp, out.data_ptr(), _at(final_states),
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
+    if st:
+        _fail("ssd_selective_scan_fwd", st)
+    return out, final_states
+
+
+def selective_scan_bwd(x, dt, dt_bias, A, B, C, D, z, dout, init_states=None, lengths=None,
+                       dfinal_states=None, out_dtype=None, workspace=None, out=None):
+    """Gradients of <dout, out> + <dfinal_states, final_states> of
+    ``selective_scan_fwd`` (``ssd_selective_scan_bwd``): a dict with dx, ddt and,
+    with z, dz in ``out_dtype`` (x's type), and dA, dB, dC, dD, ddt_bias and, with
+    init_states, dinit_states in float32."""
+    lib = _native.load()
+    dev, shape, (Bt, T, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 3, out_dtype)
+    ip = _check(init_states, "init_states", (Bt, ch, N), _F32, dev)
+    lp = _check(lengths, "lengths", (Bt,), torch.int32, dev)
+    gp = _check(dout, "dout", (Bt, T, ch), x.dtype, dev)
+    fp = _check(dfinal_states, "dfinal_states", (Bt, ch, N), _F32, dev)
+    want = [("dx", (Bt, T, ch), odt), ("ddt", (Bt, T, ch), odt), ("dA", (ch, N), _F32),
+            ("dB", (Bt, T, G, N), _F32), ("dC", (Bt, T, G, N), _F32), ("dD", (ch,), _F32),
+            ("ddt_bias", (ch,), _F32)]
+    if z is not None:
+        want.append(("dz", (Bt, T, ch), odt))
+    if init_states is not None:
+        want.append(("dinit_states", (Bt, ch, N), _F32))
+    got = {} if out is None else out
+    out = {k: _output(got.get(k), k, s, t, dev) for k, s, t in want}
+    nbytes = lib.ssd_selective_scan_bwd_workspace_size(shape)
+    ws = _scratch(max(nbytes, 1), dev, workspace)
+    st = lib.ssd_selective_scan_bwd(
+        shape, *p, ip, lp, gp, fp, *(_at(out.get(k)) for k in (
+            "dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinit_states")),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
+    if st:
+        _fail("ssd_selective_scan_bwd", st)
+    return out
+
+
+def selective_step(x, dt, dt_bias, A, B, C, state, D=None, z=None, slots=None, out_dtype=None, y=None):
+    """One token of ``selective_scan_fwd`` (``ssd_selective_step``): x, dt, z, y
+    (batch, channels); B, C (batch, ngroups, dstate); state (nslots, channels,
+    dstate) float32, updated in place; slots as in ``causal_conv_step``."""
+    lib = _native.load()
+    dev, shape, (Bt, _, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 2, out_dtype)
+    sp = _check(state, "state", (state.shape[0], ch, N), _F32, dev)
+    lp = _check(slots, "slots", (Bt,), torch.int32, dev)
+    y = _output(y, "y", (Bt, ch), odt, dev)
+    st = lib.ssd_selective_step(shape, *p, sp, lp, state.shape[0], y.data_ptr(), _stream(dev))
+    if st:
+        _fail("ssd_selective_step", st)
+    return y
+
+
+def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None, y=None):
+    """One token of ``ssd_fwd``'s scan (``ssd_step``): x, y (batch, nheads, headdim),
+    dt (batch, nheads), B, C (batch, ngroups, dstate); A, dt_bias, D (nheads,) and
+    state (nslots, nheads, headdim, dstate) float32, the state updated in place;
+    slots as in ``causal_conv_step``.  y is in ``out_dtype`` (x's type)."""
+    lib = _native.load()
+    dev = _lead(x, "x", 3)
+    if B.dim() != 3:
+        raise ValueError("B and C must be (batch, ngroups, dstate)")
+    Bt, H, P = x.shape
+    G, N = B.shape[1:]
+    xd = x.dtype
+    odt = xd if out_dtype is None else out_dtype
+    shape = _native.Shape(Bt, 1, H, P, N, G, 1, _code(xd), _code(odt))
+    xp = _check(x, "x", x.shape, xd, dev)
+    dp = _check(dt, "dt", (Bt, H), xd, dev)
+    tp = _check(dt_bias, "dt_bias", (H,), _F32, dev)
+    ap = _check(A, "A", (H,), _F32, dev)
+    bp = _check(B, "B", (Bt, G, N), xd, dev)
+    cp = _check(C, "C", (Bt, G, N), xd, dev)
+    kp = _check(D, "D", (H,), _F32, dev)
+    sp = _check(state, "state", (state.shape[0], H, P, N), _F32, dev)
+    lp = _check(slots, "slots", (Bt,), torch.int32, dev)
+    y = _output(y, "y", (Bt, H, P), odt, dev)
+    st = lib.ssd_step(shape, xp, dp, tp, ap, bp, cp, kp, sp, lp, state.shape[0], y.data_ptr(),
+                      _stream(dev))
+    if st:
+        _fail("ssd_step", st)
+    return y
+
+
+# ------------------------------------------------------------------ block norm
+
+def _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps):
+    if residual.dim() < 1 or not residual.is_cuda:
+        raise ValueError("residual must be a CUDA tensor (..., features)")
+    dev, F = residual.device, residual.shape[-1]
+    rows = residual.numel() // F if F else 0
+    ptrs = (_check(residual, "residual", residual.shape, residual.dtype, dev),
+            _check(o, "o", residual.shape, o.dtype, dev),
+            _check(w_pre, "w_pre", (F,), _F32, dev), _check(w_post, "w_post", (F,), _F32, dev),
+            None if gate is None else _check(gate, "gate", (gate.numel() // F if F else 0, F),
+                                             _F32, dev))
+    ng = 0 if gate is None else gate.shape[0]
+    if gate is not None and (ng < 1 or rows % ng != 0):
+        raise ValueError(f"gate: {ng} gate rows do not divide {rows} rows")
+    shape = _native.BlockNormShape(rows, F, ng, float(eps), float(scale), _code(o.dtype),
+                                   _code(residual.dtype))
+    return dev, shape, F, ptrs
+
+
+def block_norm_fwd(residual, o, w_pre, w_post=None, gate=None, scale: float = 1.0,
+                   eps: float = 1e-5, residual_out=None, h=None):
+    """residual_out, h of the step between two layers (``ssd_block_norm_fwd``):
+    residual_out = residual + scale * gate * t, with t = rmsnorm(o) * w_post (o itself
+    without w_post), and h = rmsnorm(residual_out) * w_pre, the next layer's input.
+
+    residual (..., features) float32 or bfloat16; o of its shape, bfloat16 or
+    float32 (float32 needs a float32 residual); w_pre, w_post (features,) float32;
+    gate (ngates, features) float32: one row for all, one per sequence or one per
+    row, each covering rows / ngates consecutive rows.  residual_out may be
+    ``residual`` and h may be ``o`` (in place)."""
+    lib = _native.load()
+    dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
+    residual_out = _output(residual_out, "residual_out", residual.shape, residual.dtype, dev)
+    h = _output(h, "h", o.shape, o.dtype, dev)
+    st = lib.ssd_block_norm_fwd(shape, *p, residual_out.data_ptr(), h.data_ptr(), _stream(dev))
+    if st:
+        _fail("ssd_block_norm_fwd", st)
+    return residual_out, h
+
+
+def block_norm_bwd(residual, o, w_pre, w_post, gate, dh, dresidual_out=None, scale: float = 1.0,
+                   eps: float = 1e-5, workspace=None, out=None):
+    """Gradients of <dh, h> + <dresidual_out, residual_out> of ``block_norm_fwd``
+    from its inputs (``ssd_block_norm_bwd``): a dict with dresidual (residual's type),
+    do (o's type), dw_pre and, with w_post and gate, dw_post and dgate (float32)."""
+    lib = _native.load()
+    dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
+    hp = _check(dh, "dh", o.shape, o.dtype, dev)
+    rp = _check(dresidual_out, "dresidual_out", residual.shape, residual.dtype, dev)
+    want = [("dresidual", residual.shape, residual.dtype), ("do", o.shape, o.dtype),
+            ("dw_pre", (F,), _F32)]
+    if w_post is not None:
+        want.append(("dw_post", (F,), _F32))
+    if gate is not None:
+        want.append(("dgate", gate.shape, _F32))
+    got = {} if out is None else out
+    out = {k: _output(got.get(k), k, s, t, dev) for k, s, t in want}
+    nbytes = lib.ssd_block_norm_workspace_size(shape)
+    ws = _scratch(max(nbytes, 1), dev, workspace)
+    st = lib.ssd_block_norm_bwd(shape, *p, hp, rp, *(_at(out.get(k)) for k in (
+        "dresidual", "do", "dw_pre", "dw_post", "dgate")), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(dev))
+    if st:
+        _fail("ssd_block_norm_bwd", st)
+    return out
