@@ -97,28 +97,90 @@ __device__ __forceinline__ float ex2(float v) {  // 2^v (MUFU, ~2 ulp; 0 below 2
   return r;
 }
 
-// 1 / (1 + e^-v): e^-v = inf for v < -88 gives exactly 0.
-__device__ __forceinline__ float sigmoid(float v) {
-  return __fdividef(1.f, 1.f + ex2(-v * kLog2e));
+__device__ __forceinline__ float rcp(float v) {  // 1 / v (MUFU, 1 ulp; 0 for inf)
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// softplus(v) = log(1 + e^v), v itself above 20.  With e = e^-|v| it is
-// max(v, 0) + log(1 + e), and log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3:
-// the series 2 s (1 + s^2/3 + s^4/5 + ...) up to s^14 / 15 leaves less than
-// s^16 / 17 < 2e-9 of it.  Steps are typically 1e-3 to 1e-1, where 1 + e in fp32
-// would round away what the logarithm needs; this form keeps ~5e-7 relative.
+// 1 / (1 + e^-v): e^-v = inf for v < -88 gives exactly 0.
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+
+// softplus(v) = log(1 + e^v).  With e = e^-|v| it is max(v, 0) + log(1 + e), and
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3.  atanh(s) / s as a polynomial in
+// q = s^2 on [0, 1/9], interpolated at the Chebyshev nodes: degree 4 is within
+// 8e-9.  Steps are typically 1e-3 to 1e-1, where 1 + e in fp32 would round away
+// what the logarithm needs; this form keeps ~5e-7 relative everywhere (above 20
+// it is v, as e vanishes against v).
+constexpr float kAtanh1 = 0.3333316147327423f, kAtanh2 = 0.20012298226356506f,
+                kAtanh3 = 0.13982579112052917f, kAtanh4 = 0.14078889787197113f;
 __device__ __forceinline__ float softplus(float v) {
   const float e = ex2(-fabsf(v) * kLog2e);
-  const float s = __fdividef(e, 2.f + e), q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
+  const float s = e * rcp(2.f + e), q = s * s;
+  float p = fmaf(kAtanh4, q, kAtanh3);
+  p = fmaf(p, q, kAtanh2);
+  p = fmaf(p, q, kAtanh1);
   p = fmaf(p, q, 1.f);
-  return v > 20.f ? v : fmaxf(v, 0.f) + 2.f * s * p;
+  return fmaf(s + s, p, fmaxf(v, 0.f));
+}
+
+// Pairs, for the packed fp32 instructions (one issue for two operations).
+__device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return __ffma2_rn(a, b, c);
+}
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  return rcp_2(add2(f2(1.f), ex2_2(mul2(v, f2(-kLog2e)))));
+}
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 e = ex2_2(mul2(make_float2(fabsf(v.x), fabsf(v.y)), f2(-kLog2e)));
+  const float2 s = mul2(e, rcp_2(add2(f2(2.f), e))), q = mul2(s, s);
+  float2 p = fma2(f2(kAtanh4), q, f2(kAtanh3));
+  p = fma2(p, q, f2(kAtanh2));
+  p = fma2(p, q, f2(kAtanh1));
+  p = fma2(p, q, f2(1.f));
+  return fma2(add2(s, s), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
+// Two adjacent elements as one access where WIDE (their address is then
+// aligned to both), else as two; `two` says whether there is a second one.
+template <typename T>
+struct alignas(2 * sizeof(T)) Two {
+  T a, b;
+};
+template <typename T, bool WIDE>
+__device__ __forceinline__ Two<T> ld_two(const T* p, bool two) {
+  if constexpr (WIDE) return *reinterpret_cast<const Two<T>*>(p);
+  Two<T> r;
+  r.a = p[0];
+  r.b = p[two ? 1 : 0];
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(const Two<float>& r) { return make_float2(r.a, r.b); }
+__device__ __forceinline__ float2 unpack2(const Two<__nv_bfloat16>& r) {
+  return __bfloat1622float2(__halves2bfloat162(r.a, r.b));
+}
+template <bool WIDE>
+__device__ __forceinline__ void st_two(float* p, float2 v, bool two) {
+  if constexpr (WIDE) {
+    *reinterpret_cast<float2*>(p) = v;
+  } else {
+    p[0] = v.x;
+    if (two) p[1] = v.y;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void st_two(__nv_bfloat16* p, float2 v, bool two) {
+  if constexpr (WIDE) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(v);
+  } else {
+    p[0] = __float2bfloat16_rn(v.x);
+    if (two) p[1] = __float2bfloat16_rn(v.y);
+  }
 }
 
 }  // namespace lm

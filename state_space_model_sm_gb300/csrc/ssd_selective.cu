@@ -10,19 +10,23 @@
 //
 // The sequence is cut into chunks that run in parallel, since B x channels
 // alone leaves most of the machine idle:
-//     k_sel_state    each chunk's state from zero, and the sum of its deltas
-//     k_sel_combine  the state entering each chunk (decays exp(A sum delta))
-//     k_sel_scan     each chunk again from its state, with the outputs
+//     k_sel_scan<.., false>  each chunk's state from zero, and the sum of its deltas
+//     k_sel_combine          the state entering each chunk (decays exp(A sum delta))
+//     k_sel_scan<.., true>   each chunk again from its state, with the outputs
 // and in the backward
-//     k_sel_state    also each chunk's adjoint at its start, from zero after it:
+//     k_sel_state    the states as above and, for each group of chunks, the
+//                    adjoint at its start, from zero after it:
 //                    sum_t exp(A (delta_1 + .. + delta_t)) C_t dy_t
-//     k_sel_combine  also the adjoint entering each chunk from the right
-//     k_sel_bwd      the gradients of a chunk
+//     k_sel_combine  also the adjoint entering each group from the right
+//     k_sel_bwd      the gradients of a group, chunk by chunk from its end
 //     k_sel_bc, k_sel_params  fixed-order sums of dB, dC and of dA, dD, ddt_bias
-// A warp owns CL = 32 / SL channel lanes (times CPT channels each) and SL
-// state lanes of SPT states each, all in registers; the sum over the states of
-// an output is mostly lane-local.
+// A lane owns two adjacent channels and SPT of their states, in registers; SL
+// lanes share a channel's states where it has more, the other 32 / SL lane
+// positions are channel pairs.  The arithmetic is in packed pairs (two states),
+// so an element costs one exponential and two to three issues.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "layer_math.cuh"
 #include "ssd_internal.h"
@@ -35,7 +39,8 @@ using bf16 = __nv_bfloat16;
 
 struct SelDims {
   int B, T, D, N, G, DG;  // DG: channels per group
-  int L, nc;              // chunk length and count
+  int L, nc;              // a block's positions, and how many such ranges
+  int nh;                 // chunks with a state each (the backward has several a range)
   int ctiles;             // blocks' channel tiles per group
   int64_t zs, bs, cs;     // elements between positions of z, B, C
   int64_t zb, bb, cb;     // and between their batch rows
@@ -54,262 +59,435 @@ __device__ __forceinline__ int sel_len(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// A block's place: batch row, group, chunk and first channel of the group.
+// A block's place: batch row, group of channels, chunk and first channel.
 struct Place {
-  int b, g, c, q0;
+  int b, g, c, q0, ct;
 };
 __device__ __forceinline__ Place place(const SelDims& d, int channels) {
   Place p;
   int i = blockIdx.x;
-  const int ct = i % d.ctiles;
+  p.ct = i % d.ctiles;
   i /= d.ctiles;
   p.g = i % d.G;
   p.b = i / d.G;
   p.c = blockIdx.y;
-  p.q0 = ct * channels;
+  p.q0 = p.ct * channels;
   return p;
 }
 
-// Rows [t0, t0 + nt) of B (and C) of one group as fp32 in shared memory,
-// padded with zeros to NP states and past position n.
-template <typename Tin, int NP>
-__device__ __forceinline__ void stage_rows(float* dst, const Tin* src, int64_t stride, int N,
-                                           int t0, int nt, int n) {
-  for (int i = threadIdx.x; i < nt * NP; i += blockDim.x) {
-    const int t = i / NP, k = i - t * NP;
-    dst[i] = (k < N && t0 + t < n) ? to_f(src[(int64_t)(t0 + t) * stride + k]) : 0.f;
-  }
-}
-
-constexpr int kTile = 32;  // positions of B and C staged at a time
-
-// Sum over the state lanes (lane = sl * CL + cl).
+// A lane's channel pair.  Lanes past the group's channels (on false) are
+// pointed at its first channel, so their loads stay in bounds; their results
+// are not written.
+struct Pair {
+  int sl, cl, ch;  // state lane, channel lane, first channel
+  bool on, two;
+};
 template <int SL>
-__device__ __forceinline__ float sum_states(float v) {
-#pragma unroll
-  for (int o = 32 / SL; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ Pair lane_pair(const SelDims& d, const Place& p, int warp) {
+  constexpr int CL = 32 / SL;
+  Pair r;
+  const int lane = threadIdx.x & 31;
+  r.sl = lane / CL;
+  r.cl = lane % CL;
+  const int q = p.q0 + (warp * CL + r.cl) * 2;
+  r.on = q < d.DG;
+  r.two = q + 1 < d.DG;
+  r.ch = p.g * d.DG + (r.on ? q : 0);
+  return r;
 }
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kU = 4;  // positions whose inputs are loaded ahead together
+
+// B (and C) of one group in shared memory as fp32, NP states a position
+// (zeros past N and past position n), TT positions at a time: fetched into
+// registers while the tile before is used, then stored.
+template <typename Tin, int NP, int TT, int NT>
+struct RowTile {
+  static constexpr int kPer = (TT * NP + NT - 1) / NT;
+  Tin v[kPer];
+  __device__ __forceinline__ void fetch(const Tin* src, int64_t stride, int N, int t0, int n) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = threadIdx.x + i * NT, t = e / NP, k = e % NP;
+      v[i] = (t < TT && k < N && t0 + t < n) ? src[(int64_t)(t0 + t) * stride + k] : from_f<Tin>(0.f);
+    }
+  }
+  __device__ __forceinline__ void store(float* dst) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = threadIdx.x + i * NT;
+      if (e < TT * NP) dst[e] = to_f(v[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
 
 constexpr int kFwdWarps = 4;
+constexpr int kFwdBlocksPerSm = 3;
+constexpr int kFwdThreads = 32 * kFwdWarps;
 
 // Forward pass over one chunk.  OUT: with the outputs, from the state
 // hin (B, nc, D, N) (or init when there is one chunk); else the chunk's state
 // from zero into hin and its delta sum into sumd (B, nc, D).
-template <typename Tin, typename Tout, int SPT, int SL, int CPT, bool OUT>
-__global__ void __launch_bounds__(32 * kFwdWarps)
+template <typename Tin, typename Tout, int SPT, int SL, bool WIDE, bool OUT>
+__global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
     k_sel_scan(SelIn in, const float* __restrict__ init, float* __restrict__ hin,
                float* __restrict__ sumd, Tout* __restrict__ out, float* __restrict__ final_state,
                SelDims d) {
-  constexpr int CL = 32 / SL, NP = SPT * SL, CW = CL * CPT;
-  __shared__ __align__(16) float sB[kTile * NP], sC[OUT ? kTile * NP : 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sl = lane / CL, cl = lane % CL;
-  const Place p = place(d, CW * kFwdWarps);
+  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, TT = NP > 16 ? 512 / NP : 32;
+  __shared__ __align__(16) float sB[2][TT * NP], sC[2][OUT ? TT * NP : 4];
+  griddep_launch_dependents();
+  if (d.nc > 1 && OUT) griddep_wait();
+  const int warp = threadIdx.x >> 5;
+  const Place p = place(d, CL * 2 * kFwdWarps);
+  const Pair ln = lane_pair<SL>(d, p, warp);
   const int n = sel_len(in.lengths, p.b, d.T);
-  const int64_t row0 = (int64_t)p.b * d.T;
-  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D;
-  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D;
-  const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb : nullptr;
-  const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + (int64_t)p.g * d.N;
-  const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + (int64_t)p.g * d.N;
+  const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), nt = max(min(t1, n) - t0, 0);
+  const int64_t row0 = (int64_t)p.b * d.T + t0;
+  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D + ln.ch;
+  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D + ln.ch;
+  const Tin* z =
+      OUT && in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + ln.ch : nullptr;
+  const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
+  const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
+  if (OUT) out += row0 * d.D + ln.ch;
 
-  int ch[CPT];
-  bool on[CPT];
-  float a2[CPT][SPT], h[CPT][SPT], bias[CPT], skip[CPT], sd[CPT];
+  float2 a2[2][K2], h[2][K2], bias = f2(0.f), skip = f2(0.f), sd = f2(0.f);
+  if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
+  if (OUT && in.D) skip = make_float2(in.D[ln.ch], in.D[ln.ch + (ln.two ? 1 : 0)]);
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    const int q = p.q0 + warp * CW + j * CL + cl;
-    on[j] = q < d.DG;
-    ch[j] = p.g * d.DG + (on[j] ? q : 0);
-    bias[j] = in.dt_bias && on[j] ? in.dt_bias[ch[j]] : 0.f;
-    skip[j] = in.D && on[j] ? in.D[ch[j]] : 0.f;
-    sd[j] = 0.f;
+  for (int j = 0; j < 2; ++j) {
+    const bool on = j ? ln.two : ln.on;
+    const int ch = ln.ch + j;
     const float* h0 = nullptr;
-    if (OUT && on[j]) {
+    if (OUT && on) {
       if (d.nc > 1)
-        h0 = hin + (((int64_t)p.b * d.nc + p.c) * d.D + ch[j]) * d.N;
+        h0 = hin + (((int64_t)p.b * d.nc + p.c) * d.D + ch) * d.N;
       else if (init)
-        h0 = init + ((int64_t)p.b * d.D + ch[j]) * d.N;
+        h0 = init + ((int64_t)p.b * d.D + ch) * d.N;
     }
+    const float* A = on ? in.A + (int64_t)ch * d.N : nullptr;
 #pragma unroll
-    for (int k = 0; k < SPT; ++k) {
-      const int s = sl * SPT + k;
-      a2[j][k] = on[j] && s < d.N ? in.A[(int64_t)ch[j] * d.N + s] * kLog2e : 0.f;
-      h[j][k] = h0 && s < d.N ? h0[s] : 0.f;
+    for (int k = 0; k < K2; ++k) {
+      const int s = ln.sl * SPT + 2 * k;
+      a2[j][k].x = A && s < d.N ? A[s] * kLog2e : 0.f;
+      a2[j][k].y = A && s + 1 < d.N ? A[s + 1] * kLog2e : 0.f;
+      h[j][k].x = h0 && s < d.N ? h0[s] : 0.f;
+      h[j][k].y = h0 && s + 1 < d.N ? h0[s + 1] : 0.f;
     }
   }
-  const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), tv = min(t1, n);
-  for (int tb = t0; tb < tv; tb += kTile) {
-    __syncthreads();
-    stage_rows<Tin, NP>(sB, Bm, d.bs, d.N, tb, kTile, tv);
-    if (OUT) stage_rows<Tin, NP>(sC, Cm, d.cs, d.N, tb, kTile, tv);
-    __syncthreads();
-    const int te = min(kTile, tv - tb);
-    for (int t = 0; t < te; ++t) {
+  Two<Tin> rx[kU], rd[kU], rz[kU];
+  auto fetch = [&](int t) {  // positions t .. t + kU - 1, the last one repeated past the end
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) {
-        const int64_t at = (int64_t)(tb + t) * d.D + ch[j];
-        const float xv = to_f(x[at]);
-        const float delta = softplus(to_f(dt[at]) + bias[j]);
-        const float dtx = delta * xv;
-        sd[j] += delta;
-        float y = 0.f;
+    for (int u = 0; u < kU; ++u) {
+      const int64_t at = min(t + u, nt - 1);
+      rx[u] = ld_two<Tin, WIDE>(x + at * d.D, ln.two);
+      rd[u] = ld_two<Tin, WIDE>(dt + at * d.D, ln.two);
+      if (OUT && z) rz[u] = ld_two<Tin, WIDE>(z + at * d.zs, ln.two);
+    }
+  };
+  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  int buf = 0;
+  if (nt > 0) {
+    fetch(0);
+    tB.fetch(Bm, d.bs, d.N, 0, nt);
+    if (OUT) tC.fetch(Cm, d.cs, d.N, 0, nt);
+    tB.store(sB[0]);
+    if (OUT) tC.store(sC[0]);
+    __syncthreads();
+  }
+  for (int tb = 0; tb < nt; tb += TT) {
+    const bool more = tb + TT < nt;
+    if (more) {
+      tB.fetch(Bm, d.bs, d.N, tb + TT, nt);
+      if (OUT) tC.fetch(Cm, d.cs, d.N, tb + TT, nt);
+    }
+    const int te = min(TT, nt - tb);
+    for (int tu = 0; tu < te; tu += kU) {
+      float2 xv[kU], dl[kU], gate[kU];
 #pragma unroll
-        for (int k = 0; k < SPT; ++k) {
-          h[j][k] = fmaf(ex2(delta * a2[j][k]), h[j][k], dtx * sB[t * NP + sl * SPT + k]);
-          if (OUT) y = fmaf(h[j][k], sC[t * NP + sl * SPT + k], y);
+      for (int u = 0; u < kU; ++u) {
+        xv[u] = unpack2(rx[u]);
+        dl[u] = softplus2(add2(unpack2(rd[u]), bias));
+        if (OUT && z) {
+          const float2 zv = unpack2(rz[u]);
+          gate[u] = mul2(zv, sigmoid2(zv));
         }
-        if (OUT) {
-          y = sum_states<SL>(y);
-          if (sl == 0 && on[j]) {
-            y = fmaf(skip[j], xv, y);
-            if (z) {
-              const float zv = to_f(z[(int64_t)(tb + t) * d.zs + ch[j]]);
-              y *= zv * sigmoid(zv);
+      }
+      if (tb + tu + kU < nt) fetch(tb + tu + kU);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (tu + u < te) {
+          const float4* Bv = reinterpret_cast<const float4*>(sB[buf] + (tu + u) * NP + ln.sl * SPT);
+          const float4* Cv = reinterpret_cast<const float4*>(sC[buf] + (tu + u) * NP + ln.sl * SPT);
+          const float2 dtx = mul2(dl[u], xv[u]);
+          if (!OUT) sd = add2(sd, dl[u]);
+          float2 y[2] = {f2(0.f), f2(0.f)};
+#pragma unroll
+          for (int q = 0; q < SPT / 4; ++q) {
+            const float4 b4 = Bv[q];
+            float4 c4;
+            if (OUT) c4 = Cv[q];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int k = 2 * q + i;
+              const float2 bk = i ? hi2(b4) : lo2(b4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
+              }
             }
-            out[row0 * d.D + at] = from_f<Tout>(y);
+          }
+          if (OUT) {
+            float2 yv = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+#pragma unroll
+            for (int o = CL; o < 32; o <<= 1) {
+              yv.x += __shfl_xor_sync(0xffffffffu, yv.x, o);
+              yv.y += __shfl_xor_sync(0xffffffffu, yv.y, o);
+            }
+            yv = fma2(skip, xv[u], yv);
+            if (z) yv = mul2(yv, gate[u]);
+            if (ln.on && ln.sl == 0) st_two<WIDE>(out + (int64_t)(tb + tu + u) * d.D, yv, ln.two);
           }
         }
       }
     }
+    if (more) {
+      buf ^= 1;
+      tB.store(sB[buf]);
+      if (OUT) tC.store(sC[buf]);
+      __syncthreads();
+    }
   }
+  if (!ln.on) return;
+  if (OUT && ln.sl == 0)
+    for (int t = nt; t < t1 - t0; ++t) st_two<WIDE>(out + (int64_t)t * d.D, f2(0.f), ln.two);
+  if (!OUT && ln.sl == 0) {
+    float* s = sumd + ((int64_t)p.b * d.nc + p.c) * d.D + ln.ch;
+    s[0] = sd.x;
+    if (ln.two) s[1] = sd.y;
+  }
+  if (OUT && (!final_state || p.c != d.nc - 1)) return;
 #pragma unroll
-  for (int j = 0; j < CPT; ++j) {
-    if (!on[j]) continue;
-    if (OUT) {
-      if (sl == 0)
-        for (int t = max(t0, tv); t < t1; ++t)
-          out[(row0 + t) * d.D + ch[j]] = from_f<Tout>(0.f);
-      if (final_state && p.c == d.nc - 1)
+  for (int j = 0; j < 2; ++j) {
+    if (j && !ln.two) break;
+    float* o = OUT ? final_state + ((int64_t)p.b * d.D + ln.ch + j) * d.N
+                   : hin + (((int64_t)p.b * d.nc + p.c) * d.D + ln.ch + j) * d.N;
 #pragma unroll
-        for (int k = 0; k < SPT; ++k)
-          if (sl * SPT + k < d.N)
-            final_state[((int64_t)p.b * d.D + ch[j]) * d.N + sl * SPT + k] = h[j][k];
-    } else {
-      const int64_t at = ((int64_t)p.b * d.nc + p.c) * d.D + ch[j];
-      if (sl == 0) sumd[at] = sd[j];
-#pragma unroll
-      for (int k = 0; k < SPT; ++k)
-        if (sl * SPT + k < d.N) hin[at * d.N + sl * SPT + k] = h[j][k];
+    for (int k = 0; k < K2; ++k) {
+      const int s = ln.sl * SPT + 2 * k;
+      if (s < d.N) o[s] = h[j][k].x;
+      if (s + 1 < d.N) o[s + 1] = h[j][k].y;
     }
   }
 }
 
-// The backward's first pass: each chunk's state from zero (hin), its delta
-// sum and its adjoint at its start from zero after it (gin).  Running products
-// of the decays give the adjoint in the forward direction, from the same
-// exponentials.
-template <typename Tin, int SPT, int SL>
-__global__ void __launch_bounds__(32 * kFwdWarps)
+constexpr int kBwdL = 32;  // positions of a backward chunk
+
+// The backward's first pass over a group of chunks: each chunk's state from zero
+// (hin) and delta sum, and the group's adjoint at its start from zero after it
+// (gin).  Running products of the decays give the adjoint in the forward
+// direction, from the same exponentials.
+template <typename Tin, int SPT, int SL, bool WIDE>
+__global__ void __launch_bounds__(kFwdThreads)
     k_sel_state(SelIn in, const Tin* __restrict__ dout, float* __restrict__ hin,
                 float* __restrict__ gin, float* __restrict__ sumd, SelDims d) {
-  constexpr int CL = 32 / SL, NP = SPT * SL, CW = CL;
-  __shared__ __align__(16) float sB[kTile * NP], sC[kTile * NP];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sl = lane / CL, cl = lane % CL;
-  const Place p = place(d, CW * kFwdWarps);
+  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, TT = NP > 16 ? 512 / NP : 32;
+  static_assert(kBwdL % TT == 0, "a chunk is whole tiles");
+  __shared__ __align__(16) float sB[2][TT * NP], sC[2][TT * NP];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5;
+  const Place p = place(d, CL * 2 * kFwdWarps);
+  const Pair ln = lane_pair<SL>(d, p, warp);
   const int n = sel_len(in.lengths, p.b, d.T);
-  const int64_t row0 = (int64_t)p.b * d.T;
-  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D;
-  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D;
-  const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb : nullptr;
-  const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + (int64_t)p.g * d.N;
-  const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + (int64_t)p.g * d.N;
-  dout += row0 * d.D;
-  const int q = p.q0 + warp * CW + cl;
-  const bool on = q < d.DG;
-  const int ch = p.g * d.DG + (on ? q : 0);
-  const float bias = in.dt_bias && on ? in.dt_bias[ch] : 0.f;
-  float a2[SPT], h[SPT], pr[SPT], gl[SPT], sd = 0.f;
+  const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), nt = max(min(t1, n) - t0, 0);
+  const int64_t row0 = (int64_t)p.b * d.T + t0;
+  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D + ln.ch;
+  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D + ln.ch;
+  const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + ln.ch : nullptr;
+  const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
+  const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
+  dout += row0 * d.D + ln.ch;
+
+  float2 a2[2][K2], h[2][K2], pr[2][K2], gl[2][K2], bias = f2(0.f), sd = f2(0.f);
+  if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
 #pragma unroll
-  for (int k = 0; k < SPT; ++k) {
-    const int s = sl * SPT + k;
-    a2[k] = on && s < d.N ? in.A[(int64_t)ch * d.N + s] * kLog2e : 0.f;
-    h[k] = gl[k] = 0.f;
-    pr[k] = 1.f;
-  }
-  const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), tv = min(t1, n);
-  for (int tb = t0; tb < tv; tb += kTile) {
-    __syncthreads();
-    stage_rows<Tin, NP>(sB, Bm, d.bs, d.N, tb, kTile, tv);
-    stage_rows<Tin, NP>(sC, Cm, d.cs, d.N, tb, kTile, tv);
-    __syncthreads();
-    const int te = min(kTile, tv - tb);
-    for (int t = 0; t < te; ++t) {
-      const int64_t at = (int64_t)(tb + t) * d.D + ch;
-      const float delta = softplus(to_f(dt[at]) + bias);
-      const float dtx = delta * to_f(x[at]);
-      float dy = to_f(dout[at]);
-      if (z) {
-        const float zv = to_f(z[(int64_t)(tb + t) * d.zs + ch]);
-        dy *= zv * sigmoid(zv);
-      }
-      sd += delta;
+  for (int j = 0; j < 2; ++j) {
+    const float* A = (j ? ln.two : ln.on) ? in.A + (int64_t)(ln.ch + j) * d.N : nullptr;
 #pragma unroll
-      for (int k = 0; k < SPT; ++k) {
-        const float a = ex2(delta * a2[k]);
-        h[k] = fmaf(a, h[k], dtx * sB[t * NP + sl * SPT + k]);
-        pr[k] *= a;
-        gl[k] = fmaf(pr[k], dy * sC[t * NP + sl * SPT + k], gl[k]);
-      }
+    for (int k = 0; k < K2; ++k) {
+      const int s = ln.sl * SPT + 2 * k;
+      a2[j][k].x = A && s < d.N ? A[s] * kLog2e : 0.f;
+      a2[j][k].y = A && s + 1 < d.N ? A[s + 1] * kLog2e : 0.f;
+      h[j][k] = gl[j][k] = f2(0.f);
+      pr[j][k] = f2(1.f);
     }
   }
-  if (!on) return;
-  const int64_t at = ((int64_t)p.b * d.nc + p.c) * d.D + ch;
-  if (sl == 0) sumd[at] = sd;
+  auto write = [&](float* dst, int64_t at, float2 (&v)[2][K2]) {  // at: row of (.., D)
+    if (!ln.on) return;
 #pragma unroll
-  for (int k = 0; k < SPT; ++k)
-    if (sl * SPT + k < d.N) {
-      hin[at * d.N + sl * SPT + k] = h[k];
-      gin[at * d.N + sl * SPT + k] = gl[k];
+    for (int j = 0; j < 2; ++j) {
+      if (j && !ln.two) break;
+      float* o = dst + (at * d.D + ln.ch + j) * d.N;
+#pragma unroll
+      for (int k = 0; k < K2; ++k) {
+        const int s = ln.sl * SPT + 2 * k;
+        if (s < d.N) o[s] = v[j][k].x;
+        if (s + 1 < d.N) o[s + 1] = v[j][k].y;
+      }
     }
+  };
+  Two<Tin> rx[kU], rd[kU], rz[kU], rg[kU];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t at = min(t + u, nt - 1);
+      rx[u] = ld_two<Tin, WIDE>(x + at * d.D, ln.two);
+      rd[u] = ld_two<Tin, WIDE>(dt + at * d.D, ln.two);
+      rg[u] = ld_two<Tin, WIDE>(dout + at * d.D, ln.two);
+      if (z) rz[u] = ld_two<Tin, WIDE>(z + at * d.zs, ln.two);
+    }
+  };
+  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  int buf = 0;
+  if (nt > 0) {
+    fetch(0);
+    tB.fetch(Bm, d.bs, d.N, 0, nt);
+    tC.fetch(Cm, d.cs, d.N, 0, nt);
+    tB.store(sB[0]);
+    tC.store(sC[0]);
+    __syncthreads();
+  }
+  const int64_t c0 = (int64_t)p.b * d.nh + t0 / kBwdL;  // the group's first chunk
+  for (int tb = 0; tb < t1 - t0; tb += TT) {
+    const bool more = tb + TT < nt;
+    if (more) {
+      tB.fetch(Bm, d.bs, d.N, tb + TT, nt);
+      tC.fetch(Cm, d.cs, d.N, tb + TT, nt);
+    }
+    const int te = min(TT, nt - tb);
+    for (int tu = 0; tu < te; tu += kU) {
+      float2 xv[kU], dl[kU], dy[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        xv[u] = unpack2(rx[u]);
+        dl[u] = softplus2(add2(unpack2(rd[u]), bias));
+        dy[u] = unpack2(rg[u]);
+        if (z) {
+          const float2 zv = unpack2(rz[u]);
+          dy[u] = mul2(dy[u], mul2(zv, sigmoid2(zv)));
+        }
+      }
+      if (tb + tu + kU < nt) fetch(tb + tu + kU);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (tu + u < te) {
+          const float4* Bv = reinterpret_cast<const float4*>(sB[buf] + (tu + u) * NP + ln.sl * SPT);
+          const float4* Cv = reinterpret_cast<const float4*>(sC[buf] + (tu + u) * NP + ln.sl * SPT);
+          const float2 dtx = mul2(dl[u], xv[u]);
+          sd = add2(sd, dl[u]);
+#pragma unroll
+          for (int q = 0; q < SPT / 4; ++q) {
+            const float4 b4 = Bv[q], c4 = Cv[q];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int k = 2 * q + i;
+              const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                pr[j][k] = mul2(pr[j][k], a);
+                gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
+              }
+            }
+          }
+        }
+      }
+    }
+    if ((tb + TT) % kBwdL == 0 || tb + TT >= t1 - t0) {  // a chunk ends
+      const int64_t at = c0 + tb / kBwdL;
+      write(hin, at, h);
+      if (ln.on && ln.sl == 0) {
+        sumd[at * d.D + ln.ch] = sd.x;
+        if (ln.two) sumd[at * d.D + ln.ch + 1] = sd.y;
+      }
+      sd = f2(0.f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < K2; ++k) h[j][k] = f2(0.f);
+    }
+    if (more) {
+      buf ^= 1;
+      tB.store(sB[buf]);
+      tC.store(sC[buf]);
+      __syncthreads();
+    }
+  }
+  write(gin, (int64_t)p.b * d.nc + p.c, gl);
 }
 
-// hin: each chunk's own state -> the state entering it, in place:
-// H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1): each chunk's own
-// adjoint at its start -> the adjoint entering it from the right:
-// G_c = gin_c + exp(A sumd_c) G_{c+1}.  One thread per (b, d, n).
+// hin (B, nh, D, N): each chunk's own state -> the state entering it, in place:
+// H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1; B, nc, D, N, groups
+// of `per` chunks): each group's own adjoint at its start -> the adjoint
+// entering it from the right: G_c = gin_c + exp(A sum of its sumd) G_{c+1}.  One
+// thread per (b, d, n), kC chunks' loads ahead of the chain.
 __global__ void __launch_bounds__(256)
     k_sel_combine(const float* __restrict__ A, const float* __restrict__ init,
                   const float* __restrict__ dfinal, float* __restrict__ hin,
-                  float* __restrict__ gin, const float* __restrict__ sumd, SelDims d) {
+                  float* __restrict__ gin, const float* __restrict__ sumd, SelDims d, int per) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t DN = (int64_t)d.D * d.N, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= d.B * DN) return;
   const int b = (int)(i / DN);
   const int64_t dn = i - b * DN;
   const int ch = (int)(dn / d.N);
   const float a2 = A[dn] * kLog2e;
-  const bool rev = blockIdx.y == 1;
-  float* v = (rev ? gin : hin) + (int64_t)b * d.nc * DN + dn;
-  const float* sm = sumd + (int64_t)b * d.nc * d.D + ch;
-  const float* start = rev ? dfinal : init;
-  float acc = start ? start[i] : 0.f;
-  constexpr int U = 4;
-  for (int c0 = 0; c0 < d.nc; c0 += U) {
-    float e[U], s[U];
+  const float* sm = sumd + (int64_t)b * d.nh * d.D + ch;
+  constexpr int kC = 8;
+  if (blockIdx.y == 0) {
+    float* v = hin + (int64_t)b * d.nh * DN + dn;
+    float acc = init ? init[i] : 0.f;
+    for (int c0 = 0; c0 < d.nh; c0 += kC) {
+      float e[kC], s[kC];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = rev ? d.nc - 1 - c0 - u : c0 + u;
-      const bool in = c0 + u < d.nc;
-      // the last chunk's own state is not needed (the forward writes none)
-      s[u] = in && c0 + u < d.nc - 1 ? v[c * DN] : 0.f;
-      e[u] = in ? sm[(int64_t)c * d.D] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = rev ? d.nc - 1 - c0 - u : c0 + u;
-      if (c0 + u < d.nc) {
-        v[c * DN] = acc;
-        acc = fmaf(ex2(e[u] * a2), acc, s[u]);
+      for (int u = 0; u < kC; ++u) {  // (the last chunk's own state is not needed)
+        const bool in = c0 + u < d.nh - 1;
+        s[u] = in ? v[(c0 + u) * DN] : 0.f;
+        e[u] = in ? sm[(int64_t)(c0 + u) * d.D] : 0.f;
       }
+#pragma unroll
+      for (int u = 0; u < kC; ++u)
+        if (c0 + u < d.nh) {
+          v[(c0 + u) * DN] = acc;
+          acc = fmaf(ex2(e[u] * a2), acc, s[u]);
+        }
+    }
+  } else {
+    float* v = gin + (int64_t)b * d.nc * DN + dn;
+    float acc = dfinal ? dfinal[i] : 0.f;
+    for (int c = d.nc - 1; c >= 0; --c) {
+      const float own = v[c * DN];
+      float e = 0.f;
+      for (int k = c * per; k < min(d.nh, (c + 1) * per); ++k) e += sm[(int64_t)k * d.D];
+      v[c * DN] = acc;
+      acc = fmaf(ex2(e * a2), acc, own);
     }
   }
 }
 
-// Sums v[0 .. NV) over the CL lanes cl of a state lane.  Halving exchanges: at
-// each step a lane keeps one half of the values and sends the other to the
-// lane that keeps that one, so lane cl ends with the totals
-// [cl * NV / CL, (cl + 1) * NV / CL) in v[0 ..]; with fewer values than lanes,
-// CL / NV consecutive lanes end with the total cl / (CL / NV).
+// Sums v[0 .. NV) over CL lanes cl.  Halving exchanges: at each step a lane
+// keeps one half of the values and sends the other to the lane that keeps that
+// one, so lane cl ends with the totals [cl * NV / CL, (cl + 1) * NV / CL) in
+// v[0 ..]; with fewer values than lanes, CL / NV consecutive lanes end with the
+// total cl / (CL / NV).
 template <int NV, int CL>
 __device__ __forceinline__ void reduce_lanes(float (&v)[NV], int cl) {
   int half = NV / 2;
@@ -331,189 +509,325 @@ __device__ __forceinline__ void reduce_lanes(float (&v)[NV], int cl) {
   }
 }
 
-constexpr int kBwdL = 32, kBwdTS = 4, kBwdWarps = 4;
+constexpr int kBwdTS = 4, kBwdWarps = 4, kBwdThreads = 32 * kBwdWarps;
 constexpr int kBwdTiles = kBwdL / kBwdTS;
 
 template <int SPT, int SL>
 struct BwdSmem {
-  static constexpr int NP = SPT * SL, CW = 32 / SL;
+  static constexpr int NP = SPT * SL, CL = 32 / SL;
   float B[kBwdL * NP], C[kBwdL * NP];
-  float red[kBwdWarps][kBwdTS][2 * NP];
-  float delta[kBwdWarps][kBwdL][CW], dy[kBwdWarps][kBwdL][CW], x[kBwdWarps][kBwdL][CW];
-  float start[kBwdWarps][kBwdTiles][SPT][32];
+  float red[2][kBwdWarps][kBwdTS][2 * NP];
+  float2 delta[kBwdWarps][kBwdL][CL], dtx[kBwdWarps][kBwdL][CL], dy[kBwdWarps][kBwdL][CL];
+  float4 start[kBwdWarps][kBwdTiles - 1][2][SPT / 4][32];
 };
 
-// Gradients of one chunk of kBwdL positions.  With the state and the adjoint
-// that enter it known, the warp walks forward once, keeping the state at every
-// kBwdTS-th position, then backward tile by tile: the tile's states are formed
-// again into registers, and at each position
+// Gradients of a group of chunks, from its last chunk to its first.  With the
+// state that enters a chunk known, the warp walks forward once, keeping the
+// state at every kBwdTS-th position, then backward tile by tile: the tile's
+// states are formed again into registers, and at each position
 //     g = C dy + a_next g_next,  w = (a g) h_prev
 //     dA += delta w,  ddelta = sum_n (A w + x g B),  dx = delta sum_n g B + D dy
 //     dB_t += delta x g,  dC_t += dy h   (sums over the group's channels).
-// The last two are sums over lanes: halving exchanges leave each lane one
-// total (31 shuffles for 32 values), the block's warps are added in shared
-// memory, and each block writes its part (B, T, G, ctiles, 2 N).
-template <typename Tin, typename Tout, int SPT, int SL>
-__global__ void __launch_bounds__(32 * kBwdWarps)
+// The last two are sums over lanes by halving exchanges, one exchange a value.
+// The first exchange needs no selects: a lane in the upper half of the channel
+// lanes holds its two groups of four states in the other order, so what it
+// keeps and what it sends sit in the same registers in every lane.  The
+// block's warps are then added in shared memory, and each block writes its
+// part (B, T, G, ctiles, 2 N).
+template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
+__global__ void __launch_bounds__(kBwdThreads, 2)
     k_sel_bwd(SelIn in, const Tin* __restrict__ dout, const float* __restrict__ hin,
               const float* __restrict__ gin, Tout* __restrict__ dx, Tout* __restrict__ ddt,
               Tout* __restrict__ dz, float* __restrict__ bcpart, float* __restrict__ dApart,
               float* __restrict__ ppart, float* __restrict__ dinit, SelDims d) {
-  constexpr int CL = 32 / SL, NP = SPT * SL, CW = CL, NV = 2 * SPT;
+  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, Q = SPT / 4;
+  static_assert(SL >= 2 && Q <= 2, "a lane finishes one of its two channels");
   extern __shared__ __align__(16) unsigned char raw_smem[];
   BwdSmem<SPT, SL>& sm = *reinterpret_cast<BwdSmem<SPT, SL>*>(raw_smem);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sl = lane / CL, cl = lane % CL;
-  const Place p = place(d, CW * kBwdWarps);
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place p = place(d, CL * 2 * kBwdWarps);
+  const Pair ln = lane_pair<SL>(d, p, warp);
+  const int sl = ln.sl, cl = ln.cl;
+  const int swap = Q == 2 && cl >= CL / 2 ? 1 : 0;  // order of the state groups
   const int n = sel_len(in.lengths, p.b, d.T);
-  const int64_t row0 = (int64_t)p.b * d.T;
-  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D;
-  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D;
+  const int64_t rowb = (int64_t)p.b * d.T;
+  const Tin* x = static_cast<const Tin*>(in.x) + rowb * d.D;
+  const Tin* dt = static_cast<const Tin*>(in.dt) + rowb * d.D;
   const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb : nullptr;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + (int64_t)p.g * d.N;
-  dout += row0 * d.D;
-  const int t0 = p.c * kBwdL, t1 = min(d.T, t0 + kBwdL), tv = min(t1, n);
-  const int qw = p.q0 + warp * CW, q = qw + cl;
-  const bool on = q < d.DG;
-  const int ch = p.g * d.DG + (on ? q : 0);
-  const float bias = in.dt_bias && on ? in.dt_bias[ch] : 0.f;
+  dout += rowb * d.D;
 
-  // one lane in SL computes a (position, channel)'s delta, x and dy
-  stage_rows<Tin, NP>(sm.B, Bm, d.bs, d.N, t0, kBwdL, tv);
-  stage_rows<Tin, NP>(sm.C, Cm, d.cs, d.N, t0, kBwdL, tv);
-  for (int t = sl; t < kBwdL; t += SL) {
-    float dl = 0.f, xv = 0.f, dy = 0.f;
-    if (on && t0 + t < tv) {
-      const int64_t at = (int64_t)(t0 + t) * d.D + ch;
-      xv = to_f(x[at]);
-      dl = softplus(to_f(dt[at]) + bias);
-      dy = to_f(dout[at]);
-      if (z) {
-        const float zv = to_f(z[(int64_t)(t0 + t) * d.zs + ch]);
-        dy *= zv * sigmoid(zv);
-      }
-    }
-    sm.delta[warp][t][cl] = dl;
-    sm.x[warp][t][cl] = xv;
-    sm.dy[warp][t][cl] = dy;
-  }
-  __syncthreads();
+  // the channel that this lane finishes: the pair's first or second
+  const int fj = sl & 1, fch = ln.ch + fj;
+  const bool fon = sl < 2 && (fj ? ln.two : ln.on);
+  const int fld = fj && !ln.two ? ln.ch : fch;  // where it loads from
+  const float fbias = in.dt_bias ? in.dt_bias[fld] : 0.f, fskip = in.D ? in.D[fld] : 0.f;
+  float2 bias = f2(0.f);
+  if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
 
-  float a2[SPT], h[SPT], gc[SPT], dA[SPT];
-  const int64_t cat = ((int64_t)p.b * d.nc + p.c) * d.D + ch;
+  // register pair k of a lane: states st(k), st(k) + 1
+  auto st = [&](int k) { return sl * SPT + ((k >> 1) ^ swap) * 4 + (k & 1) * 2; };
+  float2 a2[2][K2], h[2][K2], gc[2][K2], dA[2][K2];
+  const int64_t gat = ((int64_t)p.b * d.nc + p.c) * d.D + ln.ch;  // row of (B, nc, D)
 #pragma unroll
-  for (int k = 0; k < SPT; ++k) {
-    const int s = sl * SPT + k;
-    const bool ok = on && s < d.N;
-    a2[k] = ok ? in.A[(int64_t)ch * d.N + s] * kLog2e : 0.f;
-    h[k] = ok ? hin[cat * d.N + s] : 0.f;
-    gc[k] = ok ? gin[cat * d.N + s] : 0.f;
-    dA[k] = 0.f;
-  }
-  for (int t = 0; t < kBwdL; ++t) {
-    if (t % kBwdTS == 0) {
+  for (int j = 0; j < 2; ++j) {
+    const bool on = j ? ln.two : ln.on;
 #pragma unroll
-      for (int k = 0; k < SPT; ++k) sm.start[warp][t / kBwdTS][k][lane] = h[k];
-      if (t == kBwdL - kBwdTS) break;
+    for (int k = 0; k < K2; ++k) {
+      const int s = st(k);
+      const bool o0 = on && s < d.N, o1 = on && s + 1 < d.N;
+      const float* A = in.A + (int64_t)(ln.ch + j) * d.N + s;
+      const float* G = gin + (gat + j) * d.N + s;
+      a2[j][k] = make_float2(o0 ? A[0] * kLog2e : 0.f, o1 ? A[1] * kLog2e : 0.f);
+      gc[j][k] = make_float2(o0 ? G[0] : 0.f, o1 ? G[1] : 0.f);
+      dA[j][k] = f2(0.f);
     }
-    const float dl = sm.delta[warp][t][cl], dtx = dl * sm.x[warp][t][cl];
-#pragma unroll
-    for (int k = 0; k < SPT; ++k)
-      h[k] = fmaf(ex2(dl * a2[k]), h[k], dtx * sm.B[t * NP + sl * SPT + k]);
   }
-  const float skip = in.D && on ? in.D[ch] : 0.f;
   float dD = 0.f, dbias = 0.f;
-  for (int tile = kBwdTiles - 1; tile >= 0; --tile) {
-    float hs[kBwdTS][SPT];
-#pragma unroll
-    for (int k = 0; k < SPT; ++k) h[k] = sm.start[warp][tile][k][lane];
-#pragma unroll
-    for (int u = 0; u < kBwdTS; ++u) {
-      const int t = tile * kBwdTS + u;
-      const float dl = sm.delta[warp][t][cl], dtx = dl * sm.x[warp][t][cl];
-      float y = 0.f;
-#pragma unroll
-      for (int k = 0; k < SPT; ++k) {
-        h[k] = fmaf(ex2(dl * a2[k]), h[k], dtx * sm.B[t * NP + sl * SPT + k]);
-        hs[u][k] = h[k];
-        y = fmaf(h[k], sm.C[t * NP + sl * SPT + k], y);
-      }
-      if (z) {
-        y = sum_states<SL>(y);
-        if (sl == u % SL && on && t0 + t < t1) {
-          float o = 0.f;
-          if (t0 + t < tv) {
-            const float zv = to_f(z[(int64_t)(t0 + t) * d.zs + ch]), sg = sigmoid(zv);
-            y = fmaf(skip, sm.x[warp][t][cl], y);
-            o = to_f(dout[(int64_t)(t0 + t) * d.D + ch]) * y * sg * (1.f + zv * (1.f - sg));
+  int ph = 0;
+  const int cfirst = p.c * (d.L / kBwdL), clast = min(d.nh, cfirst + d.L / kBwdL) - 1;
+  for (int c = clast; c >= cfirst; --c) {
+    const int t0 = c * kBwdL, t1 = min(d.T, t0 + kBwdL), nt = max(min(t1, n) - t0, 0);
+    __syncthreads();  // the chunk after this one is done with B, C and its own staging
+    {
+      RowTile<Tin, NP, kBwdL, kBwdThreads> tB, tC;
+      tB.fetch(Bm + t0 * d.bs, d.bs, d.N, 0, nt);
+      tC.fetch(Cm + t0 * d.cs, d.cs, d.N, 0, nt);
+      // lane -> (position sl + SL i, pair cl): delta, delta x and dy, once
+#pragma unroll 4
+      for (int t = sl; t < kBwdL; t += SL) {
+        float2 dl = f2(0.f), xd = f2(0.f), dy = f2(0.f);
+        if (ln.on && t < nt) {
+          const int64_t at = (int64_t)(t0 + t) * d.D + ln.ch;
+          const Two<Tin> rx = ld_two<Tin, WIDE>(x + at, ln.two);
+          const Two<Tin> rd = ld_two<Tin, WIDE>(dt + at, ln.two);
+          const Two<Tin> rg = ld_two<Tin, WIDE>(dout + at, ln.two);
+          dl = softplus2(add2(unpack2(rd), bias));
+          xd = mul2(dl, unpack2(rx));
+          dy = unpack2(rg);
+          if (z) {
+            const float2 zv =
+                unpack2(ld_two<Tin, WIDE>(z + (int64_t)(t0 + t) * d.zs + ln.ch, ln.two));
+            dy = mul2(dy, mul2(zv, sigmoid2(zv)));
           }
-          dz[(row0 + t0 + t) * d.D + ch] = from_f<Tout>(o);
+          if (!ln.two) dl.y = xd.y = dy.y = 0.f;
+        }
+        sm.delta[warp][t][cl] = dl;
+        sm.dtx[warp][t][cl] = xd;
+        sm.dy[warp][t][cl] = dy;
+      }
+      tB.store(sm.B);
+      tC.store(sm.C);
+    }
+    const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
+    auto enter = [&]() {  // h = the state entering the chunk
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool on = j ? ln.two : ln.on;
+#pragma unroll
+        for (int k = 0; k < K2; ++k) {
+          const int s = st(k);
+          const float* H = hin + (hat + j) * d.N + s;
+          h[j][k] = make_float2(on && s < d.N ? H[0] : 0.f, on && s + 1 < d.N ? H[1] : 0.f);
         }
       }
-    }
-#pragma unroll
-    for (int u = kBwdTS - 1; u >= 0; --u) {
-      const int t = tile * kBwdTS + u;
-      const float dl = sm.delta[warp][t][cl], xv = sm.x[warp][t][cl], dy = sm.dy[warp][t][cl];
-      const float dtx = dl * xv;
-      float v[NV], gb = 0.f, aw = 0.f;
-#pragma unroll
-      for (int k = 0; k < SPT; ++k) {
-        const float Bk = sm.B[t * NP + sl * SPT + k], Ck = sm.C[t * NP + sl * SPT + k];
-        const float g = fmaf(Ck, dy, gc[k]);
-        gc[k] = ex2(dl * a2[k]) * g;
-        const float w = gc[k] * (u > 0 ? hs[u > 0 ? u - 1 : 0][k] : sm.start[warp][tile][k][lane]);
-        dA[k] = fmaf(dl, w, dA[k]);
-        aw = fmaf(a2[k], w, aw);
-        gb = fmaf(g, Bk, gb);
-        v[k] = dtx * g;
-        v[SPT + k] = dy * hs[u][k];
-      }
-      reduce_lanes<NV, CL>(v, cl);
-      constexpr int kPer = NV > CL ? NV / CL : 1;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int idx = cl * NV / CL + i;  // < SPT: dB, else dC, of this state lane
-        sm.red[warp][u][(idx / SPT) * NP + sl * SPT + idx % SPT] = v[i];
-      }
-      gb = sum_states<SL>(gb);
-      aw = sum_states<SL>(aw) * 0.6931471805599453f;  // a2 = A log2(e)
-      if (sl == u % SL && on && t0 + t < t1) {
-        const int64_t at = (int64_t)(t0 + t) * d.D + ch;
-        float dv = 0.f;
-        if (t0 + t < tv) dv = fmaf(xv, gb, aw) * sigmoid(to_f(dt[at]) + bias);
-        dx[row0 * d.D + at] = from_f<Tout>(fmaf(dl, gb, skip * dy));
-        ddt[row0 * d.D + at] = from_f<Tout>(dv);
-        dD = fmaf(dy, xv, dD);
-        dbias += dv;
-      }
-    }
+    };
+    enter();
     __syncthreads();
-    const int ct = p.q0 / (CW * kBwdWarps);
-    for (int i = threadIdx.x; i < kBwdTS * 2 * NP; i += blockDim.x) {
-      const int u = i / (2 * NP), e = i - u * (2 * NP), s = e % NP, t = t0 + tile * kBwdTS + u;
-      if (s < d.N && t < t1) {
-        float a = 0.f;
+    const float4* const sBv = reinterpret_cast<const float4*>(sm.B);
+    const float4* const sCv = reinterpret_cast<const float4*>(sm.C);
+    auto at4 = [&](int t, int q) { return (t * NP + sl * SPT) / 4 + (q ^ swap); };
+    auto step = [&](int t) {  // h at position t from h at t - 1
+      const float2 dl = sm.delta[warp][t][cl], xd = sm.dtx[warp][t][cl];
 #pragma unroll
-        for (int wv = 0; wv < kBwdWarps; ++wv) a += sm.red[wv][u][e];
-        bcpart[(((row0 + t) * d.G + p.g) * d.ctiles + ct) * (2 * d.N) + (e / NP) * d.N + s] = a;
+      for (int q = 0; q < Q; ++q) {
+        const float4 b4 = sBv[at4(t, q)];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = 2 * q + i;
+            const float2 a = ex2_2(mul2(f2(j ? dl.y : dl.x), a2[j][k]));
+            h[j][k] = fma2(a, h[j][k], mul2(f2(j ? xd.y : xd.x), i ? hi2(b4) : lo2(b4)));
+          }
       }
+    };
+    for (int tile = 1; tile < kBwdTiles; ++tile) {
+#pragma unroll
+      for (int u = 0; u < kBwdTS; ++u) step((tile - 1) * kBwdTS + u);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          sm.start[warp][tile - 1][j][q][lane] =
+              make_float4(h[j][2 * q].x, h[j][2 * q].y, h[j][2 * q + 1].x, h[j][2 * q + 1].y);
     }
-    __syncthreads();
+    for (int tile = kBwdTiles - 1; tile >= 0; --tile) {
+      const int tb = tile * kBwdTS;
+      auto begin = [&]() {  // h = the state entering the tile
+        if (tile == 0) {
+          enter();
+          return;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const float4 v = sm.start[warp][tile - 1][j][q][lane];
+            h[j][2 * q] = lo2(v);
+            h[j][2 * q + 1] = hi2(v);
+          }
+      };
+      // inputs of the positions that this lane finishes
+      float fx[kBwdTS], fdt[kBwdTS], fg[kBwdTS], fz[kBwdTS];
+#pragma unroll
+      for (int u = 0; u < kBwdTS; ++u) {
+        const bool in = fon && tb + u < nt;
+        const int64_t t = t0 + tb + u;
+        fx[u] = in ? to_f(x[t * d.D + fld]) : 0.f;
+        fdt[u] = in ? to_f(dt[t * d.D + fld]) : 0.f;
+        if (z) {
+          fg[u] = in ? to_f(dout[t * d.D + fld]) : 0.f;
+          fz[u] = in ? to_f(z[t * d.zs + fld]) : 0.f;
+        }
+      }
+      // a lane's pair of sums -> the sum of the channel it finishes, over its SL lanes
+      auto finish = [&](float2 v) {
+        float r = (fj ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, fj ? v.x : v.y, CL);
+#pragma unroll
+        for (int o = 2 * CL; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        return r;
+      };
+      float2 hs[kBwdTS][2][K2];
+      begin();
+#pragma unroll
+      for (int u = 0; u < kBwdTS; ++u) {
+        step(tb + u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < K2; ++k) hs[u][j][k] = h[j][k];
+        if (z) {
+          float2 y[2] = {f2(0.f), f2(0.f)};
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const float4 c4 = sCv[at4(tb + u, q)];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              y[j] = fma2(h[j][2 * q], lo2(c4), y[j]);
+              y[j] = fma2(h[j][2 * q + 1], hi2(c4), y[j]);
+            }
+          }
+          const float yv =
+              fmaf(fskip, fx[u], finish(make_float2(y[0].x + y[0].y, y[1].x + y[1].y)));
+          if (fon && tb + u < t1 - t0) {
+            const float sg = sigmoid(fz[u]);
+            dz[(rowb + t0 + tb + u) * d.D + fch] =
+                from_f<Tout>(fg[u] * yv * sg * (1.f + fz[u] * (1.f - sg)));
+          }
+        }
+      }
+      begin();
+#pragma unroll
+      for (int u = kBwdTS - 1; u >= 0; --u) {
+        const int t = tb + u;
+        const float2 dl = sm.delta[warp][t][cl], xd = sm.dtx[warp][t][cl], dy = sm.dy[warp][t][cl];
+        float2 gb[2] = {f2(0.f), f2(0.f)}, aw[2] = {f2(0.f), f2(0.f)}, vB[K2], vC[K2];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const float4 b4 = sBv[at4(t, q)], c4 = sCv[at4(t, q)];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int k = 2 * q + i;
+            const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 dlj = f2(j ? dl.y : dl.x);
+              const float2 g = fma2(ck, f2(j ? dy.y : dy.x), gc[j][k]);
+              gc[j][k] = mul2(ex2_2(mul2(dlj, a2[j][k])), g);
+              const float2 w = mul2(gc[j][k], u > 0 ? hs[u > 0 ? u - 1 : 0][j][k] : h[j][k]);
+              dA[j][k] = fma2(dlj, w, dA[j][k]);
+              aw[j] = fma2(a2[j][k], w, aw[j]);
+              gb[j] = fma2(g, bk, gb[j]);
+              if (j == 0) {
+                vB[k] = mul2(f2(xd.x), g);
+                vC[k] = mul2(f2(dy.x), hs[u][0][k]);
+              } else {
+                vB[k] = fma2(f2(xd.y), g, vB[k]);
+                vC[k] = fma2(f2(dy.y), hs[u][1][k], vC[k]);
+              }
+            }
+          }
+        }
+        float v[8];  // four states of dB and of dC
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (Q == 2) {
+            const float2 ob = make_float2(__shfl_xor_sync(0xffffffffu, vB[2 + i].x, CL / 2),
+                                          __shfl_xor_sync(0xffffffffu, vB[2 + i].y, CL / 2));
+            const float2 oc = make_float2(__shfl_xor_sync(0xffffffffu, vC[2 + i].x, CL / 2),
+                                          __shfl_xor_sync(0xffffffffu, vC[2 + i].y, CL / 2));
+            vB[i] = add2(vB[i], ob);
+            vC[i] = add2(vC[i], oc);
+          }
+          v[2 * i] = vB[i].x, v[2 * i + 1] = vB[i].y;
+          v[4 + 2 * i] = vC[i].x, v[4 + 2 * i + 1] = vC[i].y;
+        }
+        constexpr int RL = Q == 2 ? CL / 2 : CL;  // lanes left to add over
+        reduce_lanes<8, RL>(v, cl % RL);
+        constexpr int kPer = 8 > RL ? 8 / RL : 1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int e = (cl % RL) * 8 / RL + i;  // < 4: dB, else dC
+          sm.red[ph][warp][u][(e >> 2) * NP + sl * SPT + swap * 4 + (e & 3)] = v[i];
+        }
+        const float fgb = finish(make_float2(gb[0].x + gb[0].y, gb[1].x + gb[1].y));
+        const float faw = finish(make_float2(aw[0].x + aw[0].y, aw[1].x + aw[1].y)) * kLn2;
+        if (fon && t < t1 - t0) {
+          const int64_t at = (rowb + t0 + t) * d.D + fch;
+          const float fdl = fj ? dl.y : dl.x, fdy = fj ? dy.y : dy.x;
+          float dv = 0.f;
+          if (t < nt) dv = fmaf(fx[u], fgb, faw) * sigmoid(fdt[u] + fbias);
+          dx[at] = from_f<Tout>(fmaf(fdl, fgb, fskip * fdy));
+          ddt[at] = from_f<Tout>(dv);
+          dD = fmaf(fdy, fx[u], dD);
+          dbias += dv;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kBwdTS * 2 * NP; i += kBwdThreads) {
+        const int u = i / (2 * NP), e = i % (2 * NP), s = e % NP;
+        if (s < d.N && tb + u < t1 - t0) {
+          float a = 0.f;
+#pragma unroll
+          for (int wv = 0; wv < kBwdWarps; ++wv) a += sm.red[ph][wv][u][e];
+          bcpart[(((rowb + t0 + tb + u) * d.G + p.g) * d.ctiles + p.ct) * (2 * d.N) +
+                 (e / NP) * d.N + s] = a;
+        }
+      }
+      ph ^= 1;
+    }
   }
-  dD = sum_states<SL>(dD);
-  dbias = sum_states<SL>(dbias);
-  if (!on) return;
-  if (sl == 0) {
-    ppart[cat * 2] = dD;
-    ppart[cat * 2 + 1] = dbias;
+  if (fon) {
+    const int64_t at = ((int64_t)p.b * d.nc + p.c) * d.D + fch;
+    ppart[at * 2] = dD;
+    ppart[at * 2 + 1] = dbias;
   }
 #pragma unroll
-  for (int k = 0; k < SPT; ++k) {
-    const int s = sl * SPT + k;
-    if (s < d.N) {
-      dApart[cat * d.N + s] = dA[k];
-      if (dinit && p.c == 0) dinit[((int64_t)p.b * d.D + ch) * d.N + s] = gc[k];
+  for (int j = 0; j < 2; ++j) {
+    if (!(j ? ln.two : ln.on)) continue;
+    float* a = dApart + (gat + j) * d.N;
+    float* gi = dinit && p.c == 0 ? dinit + ((int64_t)p.b * d.D + ln.ch + j) * d.N : nullptr;
+#pragma unroll
+    for (int k = 0; k < K2; ++k) {
+      const int s = st(k);
+      if (s < d.N) a[s] = dA[j][k].x;
+      if (s + 1 < d.N) a[s + 1] = dA[j][k].y;
+      if (gi && s < d.N) gi[s] = gc[j][k].x;
+      if (gi && s + 1 < d.N) gi[s + 1] = gc[j][k].y;
     }
   }
 }
@@ -522,6 +836,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
 __global__ void __launch_bounds__(256)
     k_sel_bc(const float* __restrict__ part, float* __restrict__ dB, float* __restrict__ dC,
              int64_t rows, int ctiles, int N) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= rows * 2 * N) return;
   const int64_t r = i / (2 * N);
@@ -542,6 +858,7 @@ __global__ void __launch_bounds__(256)
                  float* __restrict__ dA, float* __restrict__ dD, float* __restrict__ dbias,
                  int parts, int64_t DN, int D, int blocksA) {
   __shared__ float red[8][32];
+  griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool isA = (int)blockIdx.x < blocksA;
   const int64_t w = isA ? DN : 2 * (int64_t)D;
@@ -596,28 +913,38 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
   return SSD_OK;
 }
 
-int state_lanes(int N) { return N > 32 ? 4 : N > 16 ? 2 : 1; }
-constexpr int kCPT = 2;
-
-// Forward chunks: as many as give about 12 warps per SM, at least two
-// staged tiles long; one chunk (no state pass) where the channels fill half of
-// that by themselves.
+// Forward ranges: as many as fill the machine once (kFwdBlocksPerSm blocks an
+// SM), each at least 64 positions; one (no state pass) where the channels fill
+// half of it by themselves.
 void fwd_chunks(SelDims* d) {
-  const int chans = 32 / state_lanes(d->N) * kCPT * kFwdWarps;
-  d->ctiles = ceil_div(d->DG, chans);
+  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
+  d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   const int64_t blocks = (int64_t)d->B * d->G * d->ctiles;
-  int64_t nc = 3 * 152 / blocks;
-  const int64_t most = ceil_div(d->T, 2 * kTile);
+  int64_t nc = kFwdBlocksPerSm * 152 / blocks;
+  const int64_t most = ceil_div(d->T, 64);
   if (nc > most) nc = most;
   if (nc < 2) nc = 1;
-  d->L = ceil_div(ceil_div(d->T, nc), kTile) * kTile;
-  d->nc = ceil_div(d->T, d->L);
+  d->L = ceil_div(ceil_div(d->T, nc), 32) * 32;
+  d->nc = d->nh = ceil_div(d->T, d->L);
 }
 
+// Backward: the two passes have their own channel tiles (first: as the
+// forward; main: SPT 8 states a lane).  Ranges of whole chunks, as many as give
+// the main pass about four waves of its two blocks an SM.
+int bwd_main_tiles(const SelDims& d) {
+  const int sl = d.N > 32 ? 8 : d.N > 16 ? 4 : 2;
+  return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);
+}
 void bwd_chunks(SelDims* d) {
-  d->ctiles = ceil_div(d->DG, 32 / state_lanes(d->N) * kBwdWarps);
-  d->L = kBwdL;
-  d->nc = ceil_div(d->T, kBwdL);
+  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
+  d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
+  d->nh = ceil_div(d->T, kBwdL);
+  const int64_t blocks = (int64_t)d->B * d->G * bwd_main_tiles(*d);
+  int64_t ranges = ceil_div(4 * 2 * 152, blocks);
+  if (ranges > d->nh) ranges = d->nh;
+  const int per = ceil_div(d->nh, ranges);
+  d->L = per * kBwdL;
+  d->nc = ceil_div(d->nh, per);
 }
 
 struct SelBwdWs {
@@ -633,13 +960,13 @@ SelBwdWs bwd_ws(const SelDims& d, void* base) {
     off = align_up(off + n * sizeof(float), 256);
     return p;
   };
-  const size_t cd = (size_t)d.B * d.nc * d.D;
-  w.hin = take(cd * d.N);
+  const size_t cd = (size_t)d.B * d.nc * d.D, hd = (size_t)d.B * d.nh * d.D;
+  w.hin = take(hd * d.N);
   w.gin = take(cd * d.N);
-  w.sumd = take(cd);
+  w.sumd = take(hd);
   w.dA = take(cd * d.N);
   w.pp = take(cd * 2);
-  w.bc = take((size_t)d.B * d.T * d.G * d.ctiles * 2 * d.N);
+  w.bc = take((size_t)d.B * d.T * d.G * bwd_main_tiles(d) * 2 * d.N);
   w.total = off;
   return w;
 }
@@ -652,25 +979,31 @@ cudaError_t combine(const SelDims& d, const float* A, const float* init, const f
                     float* hin, float* gin, const float* sumd, cudaStream_t s) {
   const int64_t n = (int64_t)d.B * d.D * d.N;
   const dim3 grid((unsigned)((n + 255) / 256), gin ? 2 : 1);
-  SSD_LAUNCH("k_sel_combine", s,
-             k_sel_combine<<<grid, 256, 0, s>>>(A, init, dfinal, hin, gin, sumd, d));
-  return cudaGetLastError();
+  cudaError_t e;
+  SSD_LAUNCH("k_sel_combine", s, e = launch_pdl(k_sel_combine, grid, 256, 0, s, A, init, dfinal,
+                                                hin, gin, sumd, d, d.L / kBwdL));
+  return e;
 }
 
-template <typename Tin, typename Tout, int SPT, int SL>
+template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
 int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out, float* fin,
                 float* hin, float* sumd, cudaStream_t s) {
+  Tout* const o = static_cast<Tout*>(out);
   if (d.nc > 1) {
     SSD_LAUNCH("k_sel_chunk_state", s,
-               k_sel_scan<Tin, Tout, SPT, SL, kCPT, false>
-               <<<sel_grid(d, d.nc - 1), 32 * kFwdWarps, 0, s>>>(in, nullptr, hin, sumd, nullptr,
-                                                                 nullptr, d));
+               k_sel_scan<Tin, Tout, SPT, SL, WIDE, false>
+               <<<sel_grid(d, d.nc - 1), kFwdThreads, 0, s>>>(in, nullptr, hin, sumd, nullptr,
+                                                              nullptr, d));
     if (combine(d, in.A, init, nullptr, hin, nullptr, sumd, s) != cudaSuccess) return SSD_ERR_CUDA;
+    cudaError_t e;
+    SSD_LAUNCH("k_sel_scan", s,
+               e = launch_pdl(k_sel_scan<Tin, Tout, SPT, SL, WIDE, true>, sel_grid(d, d.nc),
+                              kFwdThreads, 0, s, in, init, hin, sumd, o, fin, d));
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
   }
   SSD_LAUNCH("k_sel_scan", s,
-             k_sel_scan<Tin, Tout, SPT, SL, kCPT, true>
-             <<<sel_grid(d, d.nc), 32 * kFwdWarps, 0, s>>>(in, init, hin, nullptr,
-                                                           static_cast<Tout*>(out), fin, d));
+             k_sel_scan<Tin, Tout, SPT, SL, WIDE, true>
+             <<<sel_grid(d, 1), kFwdThreads, 0, s>>>(in, init, hin, sumd, o, fin, d));
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -681,41 +1014,58 @@ struct SelGrads {
   float *ddt_bias, *dinit;
 };
 
-template <typename Tin, typename Tout, int SPT, int SL>
+// SPT, SL: the first pass's states and state lanes; the main pass has half the
+// states a lane (its live set is three times as large) on twice the lanes.
+template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
 int sel_backward(const SelDims& d, const SelIn& in, const float* init, const void* dout,
                  const float* dfinal, const SelGrads& g, const SelBwdWs& w, cudaStream_t s) {
   const Tin* go = static_cast<const Tin*>(dout);
   SSD_LAUNCH("k_sel_state", s,
-             k_sel_state<Tin, SPT, SL><<<sel_grid(d, d.nc), 32 * kFwdWarps, 0, s>>>(
+             k_sel_state<Tin, SPT, SL, WIDE><<<sel_grid(d, d.nc), kFwdThreads, 0, s>>>(
                  in, go, w.hin, w.gin, w.sumd, d));
   if (combine(d, in.A, init, dfinal, w.hin, w.gin, w.sumd, s) != cudaSuccess) return SSD_ERR_CUDA;
-  auto kern = k_sel_bwd<Tin, Tout, SPT, SL>;
-  constexpr size_t smem = sizeof(BwdSmem<SPT, SL>);
+  SelDims m = d;
+  m.ctiles = bwd_main_tiles(d);
+  auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2, WIDE>;
+  constexpr size_t smem = sizeof(BwdSmem<SPT / 2, SL * 2>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return SSD_ERR_CUDA;
+  cudaError_t e;
   SSD_LAUNCH("k_sel_bwd", s,
-             kern<<<sel_grid(d, d.nc), 32 * kBwdWarps, smem, s>>>(
-                 in, go, w.hin, w.gin, static_cast<Tout*>(g.dx), static_cast<Tout*>(g.ddt),
-                 static_cast<Tout*>(g.dz), w.bc, w.dA, w.pp, g.dinit, d));
+             e = launch_pdl(kern, sel_grid(m, m.nc), kBwdThreads, smem, s, in, go, w.hin, w.gin,
+                            static_cast<Tout*>(g.dx), static_cast<Tout*>(g.ddt),
+                            static_cast<Tout*>(g.dz), w.bc, w.dA, w.pp, g.dinit, m));
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
   const int64_t rows = (int64_t)d.B * d.T * d.G, DN = (int64_t)d.D * d.N;
   SSD_LAUNCH("k_sel_bc", s,
-             k_sel_bc<<<(unsigned)((rows * 2 * d.N + 255) / 256), 256, 0, s>>>(
-                 w.bc, g.dB, g.dC, rows, d.ctiles, d.N));
+             e = launch_pdl(k_sel_bc, (unsigned)((rows * 2 * d.N + 255) / 256), 256, 0, s, w.bc,
+                            g.dB, g.dC, rows, m.ctiles, d.N));
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
   const int ba = ceil_div(DN, 32), bp = ceil_div(2 * (int64_t)d.D, 32);
   SSD_LAUNCH("k_sel_params", s,
-             k_sel_params<<<ba + bp, 256, 0, s>>>(w.dA, w.pp, g.dA, g.dD, g.ddt_bias, d.B * d.nc,
-                                                  DN, d.D, ba));
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+             e = launch_pdl(k_sel_params, ba + bp, 256, 0, s, w.dA, w.pp, g.dA, g.dD, g.ddt_bias,
+                            d.B * d.nc, DN, d.D, ba));
+  return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 // The instantiation for a state count and a pair of types.
+template <int V>
+using Int = std::integral_constant<int, V>;
 template <typename F>
-int by_states(int N, F&& f) {
-  if (N <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-  if (N <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  if (N <= 32) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+int by_states(int N, bool wide, F&& f) {
+  auto go = [&](auto spt, auto sl) {
+    return wide ? f(spt, sl, std::true_type{}) : f(spt, sl, std::false_type{});
+  };
+  if (N <= 8) return go(Int<8>{}, Int<1>{});
+  if (N <= 16) return go(Int<16>{}, Int<1>{});
+  if (N <= 32) return go(Int<16>{}, Int<2>{});
+  return go(Int<16>{}, Int<4>{});
+}
+
+// Whether channel pairs can be accessed as one element of twice the size.
+bool pairs_ok(const void* p, int64_t row, int64_t batch, int esize) {
+  return vec_ok(p, row, esize, 2) && vec_ok(p, batch, esize, 2);
 }
 
 bool off(const void* p, int esize) {
@@ -770,12 +1120,14 @@ int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, cons
       align_up((size_t)d.B * d.nc * d.D * d.N * sizeof(float), 256));
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return by_states(d.N, [&](auto spt, auto sl) {
-    if (ie == 4)
-      return sel_forward<float, float, spt(), sl()>(d, in, init_states, out, final_states, hin, sumd, s);
-    if (oe == 4)
-      return sel_forward<bf16, float, spt(), sl()>(d, in, init_states, out, final_states, hin, sumd, s);
-    return sel_forward<bf16, bf16, spt(), sl()>(d, in, init_states, out, final_states, hin, sumd, s);
+  const bool wide = d.DG % 2 == 0 && pairs_ok(x, d.D, 0, ie) && pairs_ok(dt, d.D, 0, ie) &&
+                    pairs_ok(out, d.D, 0, oe) && (!z || pairs_ok(z, d.zs, d.zb, ie));
+  return by_states(d.N, wide, [&](auto spt, auto sl, auto w) {
+#define SSD_GO(TI, TO)                                                                      \
+  sel_forward<TI, TO, spt(), sl(), w()>(d, in, init_states, out, final_states, hin, sumd, s)
+    if (ie == 4) return SSD_GO(float, float);
+    return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
+#undef SSD_GO
   });
 }
 
@@ -806,12 +1158,14 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const SelGrads g{dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit_states};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return by_states(d.N, [&](auto spt, auto sl) {
-    if (ie == 4)
-      return sel_backward<float, float, spt(), sl()>(d, in, init_states, dout, dfinal_states, g, w, s);
-    if (oe == 4)
-      return sel_backward<bf16, float, spt(), sl()>(d, in, init_states, dout, dfinal_states, g, w, s);
-    return sel_backward<bf16, bf16, spt(), sl()>(d, in, init_states, dout, dfinal_states, g, w, s);
+  const bool wide = d.DG % 2 == 0 && pairs_ok(x, d.D, 0, ie) && pairs_ok(dt, d.D, 0, ie) &&
+                    pairs_ok(dout, d.D, 0, ie) && (!z || pairs_ok(z, d.zs, d.zb, ie));
+  return by_states(d.N, wide, [&](auto spt, auto sl, auto wd) {
+#define SSD_GO(TI, TO)                                                                      \
+  sel_backward<TI, TO, spt(), sl(), wd()>(d, in, init_states, dout, dfinal_states, g, w, s)
+    if (ie == 4) return SSD_GO(float, float);
+    return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
+#undef SSD_GO
   });
 }
 
