@@ -146,15 +146,15 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   return fma2(add2(s, s), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
-// Two adjacent elements as one access where WIDE (their address is then
+// Two adjacent elements as one access where wide (their address is then
 // aligned to both), else as two; `two` says whether there is a second one.
 template <typename T>
 struct alignas(2 * sizeof(T)) Two {
   T a, b;
 };
-template <typename T, bool WIDE>
-__device__ __forceinline__ Two<T> ld_two(const T* p, bool two) {
-  if constexpr (WIDE) return *reinterpret_cast<const Two<T>*>(p);
+template <typename T>
+__device__ __forceinline__ Two<T> ld_two(const T* p, bool two, bool wide) {
+  if (wide) return *reinterpret_cast<const Two<T>*>(p);
   Two<T> r;
   r.a = p[0];
   r.b = p[two ? 1 : 0];
@@ -164,22 +164,16 @@ __device__ __forceinline__ float2 unpack2(const Two<float>& r) { return make_flo
 __device__ __forceinline__ float2 unpack2(const Two<__nv_bfloat16>& r) {
   return __bfloat1622float2(__halves2bfloat162(r.a, r.b));
 }
-template <bool WIDE>
-__device__ __forceinline__ void st_two(float* p, float2 v, bool two) {
-  if constexpr (WIDE) {
-    *reinterpret_cast<float2*>(p) = v;
+template <typename T>
+__device__ __forceinline__ void st_two(T* p, float2 v, bool two, bool wide) {
+  if (wide) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(p) = v;
+    else
+      *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(v);
   } else {
-    p[0] = v.x;
-    if (two) p[1] = v.y;
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ void st_two(__nv_bfloat16* p, float2 v, bool two) {
-  if constexpr (WIDE) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(v);
-  } else {
-    p[0] = __float2bfloat16_rn(v.x);
-    if (two) p[1] = __float2bfloat16_rn(v.y);
+    p[0] = from_f<T>(v.x);
+    if (two) p[1] = from_f<T>(v.y);
   }
 }
 

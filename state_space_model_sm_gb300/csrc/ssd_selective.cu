@@ -42,6 +42,9 @@ struct SelDims {
   int L, nc;              // a block's positions, and how many such ranges
   int nh;                 // chunks with a state each (the backward has several a range)
   int ctiles;             // blocks' channel tiles per group
+  int mode;               // how the rings copy (bytes: 16; 2: pairs; 1: elements)
+  int v4;                 // state rows can be accessed 16 bytes at a time
+  int wide;               // channel pairs can be read and written as one element
   int64_t zs, bs, cs;     // elements between positions of z, B, C
   int64_t zb, bb, cb;     // and between their batch rows
 };
@@ -97,7 +100,16 @@ __device__ __forceinline__ Pair lane_pair(const SelDims& d, const Place& p, int 
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kU = 4;  // positions whose inputs are loaded ahead together
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+                 : "memory");
+}
 
 // B (and C) of one group in shared memory as fp32, NP states a position
 // (zeros past N and past position n), TT positions at a time: fetched into
@@ -125,20 +137,145 @@ struct RowTile {
 __device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
 __device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
 
+// A warp's ring of its inputs: kStage positions of its channels for NI tensors a
+// stage, kStages stages, filled by cp.async ahead of the computation (no
+// registers held, and nothing the compiler can sink to the loads' use).
+// Where rows are 16-byte aligned a copy moves 16 bytes; else pairs are copied by
+// 4 or 8 bytes, and odd bf16 rows by element through registers.
+constexpr int kStage = 8, kStages = 3;
+constexpr int kU = 4;  // positions whose steps and gates are formed together
+
+template <typename Tin, int CL, int NI>
+struct Ring {
+  static constexpr int CW = 2 * CL, kTensor = kStage * CW, kOne = NI * kTensor;
+  static constexpr int kElems = kStages * kOne;  // of one warp
+  Tin* buf;
+  const Tin* src[NI];  // position 0 of the range, the warp's first channel
+  int64_t row[NI];     // elements between positions; NULL sources are skipped
+  int nt, nq, lane, mode;
+
+  // stage s of the range into its slot; positions past nt, and channels past nq
+  // are left as zeros or as they are (their results are never written)
+  __device__ __forceinline__ void fill(int s) {
+    Tin* const dst0 = buf + (s % kStages) * kOne;
+    const int t0 = s * kStage;
+    if (t0 < nt) {
+      if (mode == 16) {
+        constexpr int V = 16 / sizeof(Tin), R = CW / V;  // 16-byte pieces of a row
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (!src[i]) continue;
+#pragma unroll
+          for (int k = 0; k < (kStage * R + 31) / 32; ++k) {
+            const int e = lane + 32 * k, t = e / R, c = (e % R) * V;
+            if (e < kStage * R && t0 + t < nt && c < nq)
+              cp_async<16>(dst0 + i * kTensor + t * CW + c, src[i] + (t0 + t) * row[i] + c);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (!src[i]) continue;
+          for (int e = lane; e < kStage * CL; e += 32) {
+            const int t = e / CL, c = (e % CL) * 2;
+            if (t0 + t >= nt || c >= nq) continue;
+            Tin* dst = dst0 + i * kTensor + t * CW + c;
+            const Tin* from = src[i] + (t0 + t) * row[i] + c;
+            if (mode == 2) {  // an aligned pair
+              cp_async<2 * sizeof(Tin)>(dst, from);
+            } else if constexpr (sizeof(Tin) == 4) {
+              cp_async<4>(dst, from);
+              if (c + 1 < nq) cp_async<4>(dst + 1, from + 1);
+            } else {
+              dst[0] = from[0];
+              if (c + 1 < nq) dst[1] = from[1];
+            }
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // Makes stage s readable by the warp and starts the copy of stage s + kStages - 1
+  // into the slot that every lane has left.
+  __device__ __forceinline__ void next(int s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();
+    fill(s + kStages - 1);
+  }
+  __device__ __forceinline__ float2 get(int s, int t, int i, int cl) const {
+    const Two<Tin> v = *reinterpret_cast<const Two<Tin>*>(buf + (s % kStages) * kOne +
+                                                          i * kTensor + t * CW + 2 * cl);
+    return unpack2(v);
+  }
+};
+
+// K2 pairs of a channel's states from s0 on (rows of N floats), 0 past N; as
+// 16-byte accesses where rows allow (v4).
+template <int K2>
+__device__ __forceinline__ void ld_states(float2 (&v)[K2], const float* row, int s0, int N,
+                                          bool on, bool v4) {
+  if (v4) {
+#pragma unroll
+    for (int q = 0; q < K2 / 2; ++q) {
+      const float4 f = on && s0 + 4 * q < N
+                           ? *reinterpret_cast<const float4*>(row + s0 + 4 * q)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[2 * q] = lo2(f);
+      v[2 * q + 1] = hi2(f);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K2; ++k) {
+      const int s = s0 + 2 * k;
+      v[k].x = on && s < N ? row[s] : 0.f;
+      v[k].y = on && s + 1 < N ? row[s + 1] : 0.f;
+    }
+  }
+}
+template <int K2>
+__device__ __forceinline__ void st_states(const float2 (&v)[K2], float* row, int s0, int N,
+                                          bool v4) {
+  if (v4) {
+#pragma unroll
+    for (int q = 0; q < K2 / 2; ++q)
+      if (s0 + 4 * q < N)
+        *reinterpret_cast<float4*>(row + s0 + 4 * q) =
+            make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K2; ++k) {
+      const int s = s0 + 2 * k;
+      if (s < N) row[s] = v[k].x;
+      if (s + 1 < N) row[s + 1] = v[k].y;
+    }
+  }
+}
+
 constexpr int kFwdWarps = 4;
 constexpr int kFwdBlocksPerSm = 3;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 
+template <typename Tin, int SPT, int SL, int NI, bool C>
+struct PassSmem {
+  static constexpr int NP = SPT * SL, TT = NP > 16 ? 512 / NP : 32;
+  float B[2][TT * NP], Cm[2][C ? TT * NP : 4];
+  __align__(16) Tin ring[kFwdWarps][Ring<Tin, 32 / SL, NI>::kElems];
+};
+
 // Forward pass over one chunk.  OUT: with the outputs, from the state
 // hin (B, nc, D, N) (or init when there is one chunk); else the chunk's state
 // from zero into hin and its delta sum into sumd (B, nc, D).
-template <typename Tin, typename Tout, int SPT, int SL, bool WIDE, bool OUT>
+template <typename Tin, typename Tout, int SPT, int SL, bool OUT>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
     k_sel_scan(SelIn in, const float* __restrict__ init, float* __restrict__ hin,
                float* __restrict__ sumd, Tout* __restrict__ out, float* __restrict__ final_state,
                SelDims d) {
-  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, TT = NP > 16 ? 512 / NP : 32;
-  __shared__ __align__(16) float sB[2][TT * NP], sC[2][OUT ? TT * NP : 4];
+  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, NI = OUT ? 3 : 2;
+  using Smem = PassSmem<Tin, SPT, SL, NI, OUT>;
+  constexpr int TT = Smem::TT;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   griddep_launch_dependents();
   if (d.nc > 1 && OUT) griddep_wait();
   const int warp = threadIdx.x >> 5;
@@ -147,13 +284,26 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
   const int n = sel_len(in.lengths, p.b, d.T);
   const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), nt = max(min(t1, n) - t0, 0);
   const int64_t row0 = (int64_t)p.b * d.T + t0;
-  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D + ln.ch;
-  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D + ln.ch;
-  const Tin* z =
-      OUT && in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + ln.ch : nullptr;
+  const int qw = p.q0 + warp * CL * 2, cw = p.g * d.DG + qw;  // the warp's first channel
+  const bool gated = OUT && in.z;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
-  if (OUT) out += row0 * d.D + ln.ch;
+  Ring<Tin, CL, NI> ring;
+  ring.buf = sm.ring[warp];
+  ring.src[0] = static_cast<const Tin*>(in.x) + row0 * d.D + cw;
+  ring.src[1] = static_cast<const Tin*>(in.dt) + row0 * d.D + cw;
+  ring.row[0] = ring.row[1] = d.D;
+  if constexpr (OUT) {
+    ring.src[2] =
+        gated ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + cw : nullptr;
+    ring.row[2] = d.zs;
+  }
+  ring.nt = nt, ring.nq = d.DG - qw, ring.lane = threadIdx.x & 31, ring.mode = d.mode;
+  ring.fill(0);
+  ring.fill(1);
+  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  tB.fetch(Bm, d.bs, d.N, 0, nt);
+  if (OUT) tC.fetch(Cm, d.cs, d.N, 0, nt);
 
   float2 a2[2][K2], h[2][K2], bias = f2(0.f), skip = f2(0.f), sd = f2(0.f);
   if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
@@ -169,36 +319,16 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
       else if (init)
         h0 = init + ((int64_t)p.b * d.D + ch) * d.N;
     }
-    const float* A = on ? in.A + (int64_t)ch * d.N : nullptr;
+    ld_states<K2>(a2[j], in.A + (int64_t)ch * d.N, ln.sl * SPT, d.N, on, d.v4);
+    ld_states<K2>(h[j], h0, ln.sl * SPT, d.N, h0 != nullptr, d.v4);
 #pragma unroll
-    for (int k = 0; k < K2; ++k) {
-      const int s = ln.sl * SPT + 2 * k;
-      a2[j][k].x = A && s < d.N ? A[s] * kLog2e : 0.f;
-      a2[j][k].y = A && s + 1 < d.N ? A[s + 1] * kLog2e : 0.f;
-      h[j][k].x = h0 && s < d.N ? h0[s] : 0.f;
-      h[j][k].y = h0 && s + 1 < d.N ? h0[s + 1] : 0.f;
-    }
+    for (int k = 0; k < K2; ++k) a2[j][k] = mul2(a2[j][k], f2(kLog2e));
   }
-  Two<Tin> rx[kU], rd[kU], rz[kU];
-  auto fetch = [&](int t) {  // positions t .. t + kU - 1, the last one repeated past the end
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t at = min(t + u, nt - 1);
-      rx[u] = ld_two<Tin, WIDE>(x + at * d.D, ln.two);
-      rd[u] = ld_two<Tin, WIDE>(dt + at * d.D, ln.two);
-      if (OUT && z) rz[u] = ld_two<Tin, WIDE>(z + at * d.zs, ln.two);
-    }
-  };
-  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  tB.store(sm.B[0]);
+  if (OUT) tC.store(sm.Cm[0]);
+  __syncthreads();
+  Tout* o = OUT ? out + row0 * d.D + ln.ch : nullptr;
   int buf = 0;
-  if (nt > 0) {
-    fetch(0);
-    tB.fetch(Bm, d.bs, d.N, 0, nt);
-    if (OUT) tC.fetch(Cm, d.cs, d.N, 0, nt);
-    tB.store(sB[0]);
-    if (OUT) tC.store(sC[0]);
-    __syncthreads();
-  }
   for (int tb = 0; tb < nt; tb += TT) {
     const bool more = tb + TT < nt;
     if (more) {
@@ -206,67 +336,75 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
       if (OUT) tC.fetch(Cm, d.cs, d.N, tb + TT, nt);
     }
     const int te = min(TT, nt - tb);
-    for (int tu = 0; tu < te; tu += kU) {
-      float2 xv[kU], dl[kU], gate[kU];
+    for (int ts = 0; ts < te; ts += kStage) {
+      const int stage = (tb + ts) / kStage;
+      ring.next(stage);
+#pragma unroll 1
+      for (int tu = 0; tu < kStage; tu += kU) {
+        if (ts + tu >= te) break;
+        float2 xv[kU], dl[kU], gate[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        xv[u] = unpack2(rx[u]);
-        dl[u] = softplus2(add2(unpack2(rd[u]), bias));
-        if (OUT && z) {
-          const float2 zv = unpack2(rz[u]);
-          gate[u] = mul2(zv, sigmoid2(zv));
+        for (int u = 0; u < kU; ++u) {
+          xv[u] = ring.get(stage, tu + u, 0, ln.cl);
+          dl[u] = softplus2(add2(ring.get(stage, tu + u, 1, ln.cl), bias));
+          if constexpr (OUT)
+            if (gated) {
+              const float2 zv = ring.get(stage, tu + u, 2, ln.cl);
+              gate[u] = mul2(zv, sigmoid2(zv));
+            }
         }
-      }
-      if (tb + tu + kU < nt) fetch(tb + tu + kU);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (tu + u < te) {
-          const float4* Bv = reinterpret_cast<const float4*>(sB[buf] + (tu + u) * NP + ln.sl * SPT);
-          const float4* Cv = reinterpret_cast<const float4*>(sC[buf] + (tu + u) * NP + ln.sl * SPT);
-          const float2 dtx = mul2(dl[u], xv[u]);
-          if (!OUT) sd = add2(sd, dl[u]);
-          float2 y[2] = {f2(0.f), f2(0.f)};
+        for (int u = 0; u < kU; ++u) {
+          const int t = ts + tu + u;
+          if (t < te) {
+            const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
+            const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
+            const float2 dtx = mul2(dl[u], xv[u]);
+            if (!OUT) sd = add2(sd, dl[u]);
+            float2 y[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
-          for (int q = 0; q < SPT / 4; ++q) {
-            const float4 b4 = Bv[q];
-            float4 c4;
-            if (OUT) c4 = Cv[q];
+            for (int q = 0; q < SPT / 4; ++q) {
+              const float4 b4 = Bv[q];
+              float4 c4;
+              if (OUT) c4 = Cv[q];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int k = 2 * q + i;
-              const float2 bk = i ? hi2(b4) : lo2(b4);
+              for (int i = 0; i < 2; ++i) {
+                const int k = 2 * q + i;
+                const float2 bk = i ? hi2(b4) : lo2(b4);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
-                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
-                if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
+                for (int j = 0; j < 2; ++j) {
+                  const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                  h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                  if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
+                }
               }
             }
-          }
-          if (OUT) {
-            float2 yv = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+            if (OUT) {
+              float2 yv = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
 #pragma unroll
-            for (int o = CL; o < 32; o <<= 1) {
-              yv.x += __shfl_xor_sync(0xffffffffu, yv.x, o);
-              yv.y += __shfl_xor_sync(0xffffffffu, yv.y, o);
+              for (int w = CL; w < 32; w <<= 1) {
+                yv.x += __shfl_xor_sync(0xffffffffu, yv.x, w);
+                yv.y += __shfl_xor_sync(0xffffffffu, yv.y, w);
+              }
+              yv = fma2(skip, xv[u], yv);
+              if (gated) yv = mul2(yv, gate[u]);
+              if (ln.on && ln.sl == 0) st_two(o, yv, ln.two, d.wide);
+              o += d.D;
             }
-            yv = fma2(skip, xv[u], yv);
-            if (z) yv = mul2(yv, gate[u]);
-            if (ln.on && ln.sl == 0) st_two<WIDE>(out + (int64_t)(tb + tu + u) * d.D, yv, ln.two);
           }
         }
       }
     }
     if (more) {
       buf ^= 1;
-      tB.store(sB[buf]);
-      if (OUT) tC.store(sC[buf]);
+      tB.store(sm.B[buf]);
+      if (OUT) tC.store(sm.Cm[buf]);
       __syncthreads();
     }
   }
   if (!ln.on) return;
   if (OUT && ln.sl == 0)
-    for (int t = nt; t < t1 - t0; ++t) st_two<WIDE>(out + (int64_t)t * d.D, f2(0.f), ln.two);
+    for (int t = nt; t < t1 - t0; ++t, o += d.D) st_two(o, f2(0.f), ln.two, d.wide);
   if (!OUT && ln.sl == 0) {
     float* s = sumd + ((int64_t)p.b * d.nc + p.c) * d.D + ln.ch;
     s[0] = sd.x;
@@ -276,14 +414,9 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (j && !ln.two) break;
-    float* o = OUT ? final_state + ((int64_t)p.b * d.D + ln.ch + j) * d.N
+    float* v = OUT ? final_state + ((int64_t)p.b * d.D + ln.ch + j) * d.N
                    : hin + (((int64_t)p.b * d.nc + p.c) * d.D + ln.ch + j) * d.N;
-#pragma unroll
-    for (int k = 0; k < K2; ++k) {
-      const int s = ln.sl * SPT + 2 * k;
-      if (s < d.N) o[s] = h[j][k].x;
-      if (s + 1 < d.N) o[s + 1] = h[j][k].y;
-    }
+    st_states<K2>(h[j], v, ln.sl * SPT, d.N, d.v4);
   }
 }
 
@@ -293,13 +426,17 @@ constexpr int kBwdL = 32;  // positions of a backward chunk
 // (hin) and delta sum, and the group's adjoint at its start from zero after it
 // (gin).  Running products of the decays give the adjoint in the forward
 // direction, from the same exponentials.
-template <typename Tin, int SPT, int SL, bool WIDE>
+template <typename Tin, int SPT, int SL>
 __global__ void __launch_bounds__(kFwdThreads)
     k_sel_state(SelIn in, const Tin* __restrict__ dout, float* __restrict__ hin,
-                float* __restrict__ gin, float* __restrict__ sumd, SelDims d) {
-  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, TT = NP > 16 ? 512 / NP : 32;
+                float* __restrict__ gin, float* __restrict__ sumd, float* __restrict__ sumg,
+                SelDims d) {
+  constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2;
+  using Smem = PassSmem<Tin, SPT, SL, 4, true>;
+  constexpr int TT = Smem::TT;
   static_assert(kBwdL % TT == 0, "a chunk is whole tiles");
-  __shared__ __align__(16) float sB[2][TT * NP], sC[2][TT * NP];
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const Place p = place(d, CL * 2 * kFwdWarps);
@@ -307,23 +444,33 @@ __global__ void __launch_bounds__(kFwdThreads)
   const int n = sel_len(in.lengths, p.b, d.T);
   const int t0 = p.c * d.L, t1 = min(d.T, t0 + d.L), nt = max(min(t1, n) - t0, 0);
   const int64_t row0 = (int64_t)p.b * d.T + t0;
-  const Tin* x = static_cast<const Tin*>(in.x) + row0 * d.D + ln.ch;
-  const Tin* dt = static_cast<const Tin*>(in.dt) + row0 * d.D + ln.ch;
-  const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + ln.ch : nullptr;
+  const int qw = p.q0 + warp * CL * 2, cw = p.g * d.DG + qw;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
-  dout += row0 * d.D + ln.ch;
+  Ring<Tin, CL, 4> ring;
+  ring.buf = sm.ring[warp];
+  ring.src[0] = static_cast<const Tin*>(in.x) + row0 * d.D + cw;
+  ring.src[1] = static_cast<const Tin*>(in.dt) + row0 * d.D + cw;
+  ring.src[2] = dout + row0 * d.D + cw;
+  ring.src[3] = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + cw : nullptr;
+  ring.row[0] = ring.row[1] = ring.row[2] = d.D;
+  ring.row[3] = d.zs;
+  ring.nt = nt, ring.nq = d.DG - qw, ring.lane = threadIdx.x & 31, ring.mode = d.mode;
+  ring.fill(0);
+  ring.fill(1);
+  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  tB.fetch(Bm, d.bs, d.N, 0, nt);
+  tC.fetch(Cm, d.cs, d.N, 0, nt);
 
-  float2 a2[2][K2], h[2][K2], pr[2][K2], gl[2][K2], bias = f2(0.f), sd = f2(0.f);
+  float2 a2[2][K2], h[2][K2], pr[2][K2], gl[2][K2], bias = f2(0.f), sd = f2(0.f), sg = f2(0.f);
   if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const float* A = (j ? ln.two : ln.on) ? in.A + (int64_t)(ln.ch + j) * d.N : nullptr;
+    ld_states<K2>(a2[j], in.A + (int64_t)(ln.ch + j) * d.N, ln.sl * SPT, d.N, j ? ln.two : ln.on,
+                  d.v4);
 #pragma unroll
     for (int k = 0; k < K2; ++k) {
-      const int s = ln.sl * SPT + 2 * k;
-      a2[j][k].x = A && s < d.N ? A[s] * kLog2e : 0.f;
-      a2[j][k].y = A && s + 1 < d.N ? A[s + 1] * kLog2e : 0.f;
+      a2[j][k] = mul2(a2[j][k], f2(kLog2e));
       h[j][k] = gl[j][k] = f2(0.f);
       pr[j][k] = f2(1.f);
     }
@@ -333,37 +480,19 @@ __global__ void __launch_bounds__(kFwdThreads)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (j && !ln.two) break;
-      float* o = dst + (at * d.D + ln.ch + j) * d.N;
-#pragma unroll
-      for (int k = 0; k < K2; ++k) {
-        const int s = ln.sl * SPT + 2 * k;
-        if (s < d.N) o[s] = v[j][k].x;
-        if (s + 1 < d.N) o[s + 1] = v[j][k].y;
-      }
+      st_states<K2>(v[j], dst + (at * d.D + ln.ch + j) * d.N, ln.sl * SPT, d.N, d.v4);
     }
   };
-  Two<Tin> rx[kU], rd[kU], rz[kU], rg[kU];
-  auto fetch = [&](int t) {
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t at = min(t + u, nt - 1);
-      rx[u] = ld_two<Tin, WIDE>(x + at * d.D, ln.two);
-      rd[u] = ld_two<Tin, WIDE>(dt + at * d.D, ln.two);
-      rg[u] = ld_two<Tin, WIDE>(dout + at * d.D, ln.two);
-      if (z) rz[u] = ld_two<Tin, WIDE>(z + at * d.zs, ln.two);
-    }
+  auto write_sum = [&](float* dst, int64_t at, float2 v) {
+    if (!ln.on || ln.sl != 0) return;
+    dst[at * d.D + ln.ch] = v.x;
+    if (ln.two) dst[at * d.D + ln.ch + 1] = v.y;
   };
-  RowTile<Tin, NP, TT, kFwdThreads> tB, tC;
+  tB.store(sm.B[0]);
+  tC.store(sm.Cm[0]);
+  __syncthreads();
   int buf = 0;
-  if (nt > 0) {
-    fetch(0);
-    tB.fetch(Bm, d.bs, d.N, 0, nt);
-    tC.fetch(Cm, d.cs, d.N, 0, nt);
-    tB.store(sB[0]);
-    tC.store(sC[0]);
-    __syncthreads();
-  }
-  const int64_t c0 = (int64_t)p.b * d.nh + t0 / kBwdL;  // the group's first chunk
+  const int64_t c0 = (int64_t)p.b * d.nh + t0 / kBwdL;  // the range's first chunk
   for (int tb = 0; tb < t1 - t0; tb += TT) {
     const bool more = tb + TT < nt;
     if (more) {
@@ -371,39 +500,45 @@ __global__ void __launch_bounds__(kFwdThreads)
       tC.fetch(Cm, d.cs, d.N, tb + TT, nt);
     }
     const int te = min(TT, nt - tb);
-    for (int tu = 0; tu < te; tu += kU) {
-      float2 xv[kU], dl[kU], dy[kU];
+    for (int ts = 0; ts < te; ts += kStage) {
+      const int stage = (tb + ts) / kStage;
+      ring.next(stage);
+#pragma unroll 1
+      for (int tu = 0; tu < kStage; tu += kU) {
+        if (ts + tu >= te) break;
+        float2 xv[kU], dl[kU], dy[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        xv[u] = unpack2(rx[u]);
-        dl[u] = softplus2(add2(unpack2(rd[u]), bias));
-        dy[u] = unpack2(rg[u]);
-        if (z) {
-          const float2 zv = unpack2(rz[u]);
-          dy[u] = mul2(dy[u], mul2(zv, sigmoid2(zv)));
+        for (int u = 0; u < kU; ++u) {
+          xv[u] = ring.get(stage, tu + u, 0, ln.cl);
+          dl[u] = softplus2(add2(ring.get(stage, tu + u, 1, ln.cl), bias));
+          dy[u] = ring.get(stage, tu + u, 2, ln.cl);
+          if (in.z) {
+            const float2 zv = ring.get(stage, tu + u, 3, ln.cl);
+            dy[u] = mul2(dy[u], mul2(zv, sigmoid2(zv)));
+          }
         }
-      }
-      if (tb + tu + kU < nt) fetch(tb + tu + kU);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (tu + u < te) {
-          const float4* Bv = reinterpret_cast<const float4*>(sB[buf] + (tu + u) * NP + ln.sl * SPT);
-          const float4* Cv = reinterpret_cast<const float4*>(sC[buf] + (tu + u) * NP + ln.sl * SPT);
-          const float2 dtx = mul2(dl[u], xv[u]);
-          sd = add2(sd, dl[u]);
+        for (int u = 0; u < kU; ++u) {
+          const int t = ts + tu + u;
+          if (t < te) {
+            const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
+            const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
+            const float2 dtx = mul2(dl[u], xv[u]);
+            sd = add2(sd, dl[u]);
 #pragma unroll
-          for (int q = 0; q < SPT / 4; ++q) {
-            const float4 b4 = Bv[q], c4 = Cv[q];
+            for (int q = 0; q < SPT / 4; ++q) {
+              const float4 b4 = Bv[q], c4 = Cv[q];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int k = 2 * q + i;
-              const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
+              for (int i = 0; i < 2; ++i) {
+                const int k = 2 * q + i;
+                const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
-                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
-                pr[j][k] = mul2(pr[j][k], a);
-                gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
+                for (int j = 0; j < 2; ++j) {
+                  const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                  h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                  pr[j][k] = mul2(pr[j][k], a);
+                  gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
+                }
               }
             }
           }
@@ -413,10 +548,8 @@ __global__ void __launch_bounds__(kFwdThreads)
     if ((tb + TT) % kBwdL == 0 || tb + TT >= t1 - t0) {  // a chunk ends
       const int64_t at = c0 + tb / kBwdL;
       write(hin, at, h);
-      if (ln.on && ln.sl == 0) {
-        sumd[at * d.D + ln.ch] = sd.x;
-        if (ln.two) sumd[at * d.D + ln.ch + 1] = sd.y;
-      }
+      write_sum(sumd, at, sd);
+      sg = add2(sg, sd);
       sd = f2(0.f);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -425,61 +558,54 @@ __global__ void __launch_bounds__(kFwdThreads)
     }
     if (more) {
       buf ^= 1;
-      tB.store(sB[buf]);
-      tC.store(sC[buf]);
+      tB.store(sm.B[buf]);
+      tC.store(sm.Cm[buf]);
       __syncthreads();
     }
   }
   write(gin, (int64_t)p.b * d.nc + p.c, gl);
+  write_sum(sumg, (int64_t)p.b * d.nc + p.c, sg);
 }
 
 // hin (B, nh, D, N): each chunk's own state -> the state entering it, in place:
-// H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1; B, nc, D, N, groups
-// of `per` chunks): each group's own adjoint at its start -> the adjoint
-// entering it from the right: G_c = gin_c + exp(A sum of its sumd) G_{c+1}.  One
-// thread per (b, d, n), kC chunks' loads ahead of the chain.
+// H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1; B, nc, D, N): each
+// range's own adjoint at its start -> the adjoint entering it from the right:
+// G_c = gin_c + exp(A sumg_c) G_{c+1}.  One thread per (b, d, n), kC loads ahead of
+// the chain.  (The last own value of either walk is not needed.)
 __global__ void __launch_bounds__(256)
     k_sel_combine(const float* __restrict__ A, const float* __restrict__ init,
                   const float* __restrict__ dfinal, float* __restrict__ hin,
-                  float* __restrict__ gin, const float* __restrict__ sumd, SelDims d, int per) {
+                  float* __restrict__ gin, const float* __restrict__ sumd,
+                  const float* __restrict__ sumg, SelDims d) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t DN = (int64_t)d.D * d.N, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= d.B * DN) return;
   const int b = (int)(i / DN);
   const int64_t dn = i - b * DN;
-  const int ch = (int)(dn / d.N);
   const float a2 = A[dn] * kLog2e;
-  const float* sm = sumd + (int64_t)b * d.nh * d.D + ch;
-  constexpr int kC = 8;
-  if (blockIdx.y == 0) {
-    float* v = hin + (int64_t)b * d.nh * DN + dn;
-    float acc = init ? init[i] : 0.f;
-    for (int c0 = 0; c0 < d.nh; c0 += kC) {
-      float e[kC], s[kC];
+  const bool rev = blockIdx.y == 1;
+  const int nc = rev ? d.nc : d.nh;
+  const int64_t sv = rev ? -DN : DN, ss = rev ? -d.D : d.D;
+  float* v = (rev ? gin : hin) + ((int64_t)b * nc + (rev ? nc - 1 : 0)) * DN + dn;
+  const float* sm = (rev ? sumg : sumd) + ((int64_t)b * nc + (rev ? nc - 1 : 0)) * d.D + dn / d.N;
+  const float* start = rev ? dfinal : init;
+  float acc = start ? start[i] : 0.f;
+  constexpr int kC = 16;
+  for (int c0 = 0; c0 < nc; c0 += kC) {
+    float e[kC], s[kC];
 #pragma unroll
-      for (int u = 0; u < kC; ++u) {  // (the last chunk's own state is not needed)
-        const bool in = c0 + u < d.nh - 1;
-        s[u] = in ? v[(c0 + u) * DN] : 0.f;
-        e[u] = in ? sm[(int64_t)(c0 + u) * d.D] : 0.f;
+    for (int u = 0; u < kC; ++u) {
+      const bool in = c0 + u < nc - 1;
+      s[u] = in ? v[(c0 + u) * sv] : 0.f;
+      e[u] = in ? sm[(c0 + u) * ss] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kC; ++u)
+      if (c0 + u < nc) {
+        v[(c0 + u) * sv] = acc;
+        acc = fmaf(ex2(e[u] * a2), acc, s[u]);
       }
-#pragma unroll
-      for (int u = 0; u < kC; ++u)
-        if (c0 + u < d.nh) {
-          v[(c0 + u) * DN] = acc;
-          acc = fmaf(ex2(e[u] * a2), acc, s[u]);
-        }
-    }
-  } else {
-    float* v = gin + (int64_t)b * d.nc * DN + dn;
-    float acc = dfinal ? dfinal[i] : 0.f;
-    for (int c = d.nc - 1; c >= 0; --c) {
-      const float own = v[c * DN];
-      float e = 0.f;
-      for (int k = c * per; k < min(d.nh, (c + 1) * per); ++k) e += sm[(int64_t)k * d.D];
-      v[c * DN] = acc;
-      acc = fmaf(ex2(e * a2), acc, own);
-    }
   }
 }
 
@@ -509,6 +635,18 @@ __device__ __forceinline__ void reduce_lanes(float (&v)[NV], int cl) {
   }
 }
 
+// 1 - e^-v for v >= 0: by its series to v^7 below 1/4 (the next term is under
+// 2e-9 of it), where the difference would cancel.
+__device__ __forceinline__ float one_minus_exp(float v) {
+  float p = fmaf(v, 1.f / 5040.f, -1.f / 720.f);
+  p = fmaf(p, v, 1.f / 120.f);
+  p = fmaf(p, v, -1.f / 24.f);
+  p = fmaf(p, v, 1.f / 6.f);
+  p = fmaf(p, v, -0.5f);
+  p = fmaf(p, v, 1.f);
+  return v < 0.25f ? p * v : 1.f - ex2(-v * kLog2e);
+}
+
 constexpr int kBwdTS = 4, kBwdWarps = 4, kBwdThreads = 32 * kBwdWarps;
 constexpr int kBwdTiles = kBwdL / kBwdTS;
 
@@ -517,7 +655,7 @@ struct BwdSmem {
   static constexpr int NP = SPT * SL, CL = 32 / SL;
   float B[kBwdL * NP], C[kBwdL * NP];
   float red[2][kBwdWarps][kBwdTS][2 * NP];
-  float2 delta[kBwdWarps][kBwdL][CL], dtx[kBwdWarps][kBwdL][CL], dy[kBwdWarps][kBwdL][CL];
+  float2 delta[kBwdWarps][kBwdL][CL], x[kBwdWarps][kBwdL][CL], dy[kBwdWarps][kBwdL][CL];
   float4 start[kBwdWarps][kBwdTiles - 1][2][SPT / 4][32];
 };
 
@@ -534,7 +672,7 @@ struct BwdSmem {
 // keeps and what it sends sit in the same registers in every lane.  The
 // block's warps are then added in shared memory, and each block writes its
 // part (B, T, G, ctiles, 2 N).
-template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
+template <typename Tin, typename Tout, int SPT, int SL>
 __global__ void __launch_bounds__(kBwdThreads, 2)
     k_sel_bwd(SelIn in, const Tin* __restrict__ dout, const float* __restrict__ hin,
               const float* __restrict__ gin, Tout* __restrict__ dx, Tout* __restrict__ ddt,
@@ -563,8 +701,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   // the channel that this lane finishes: the pair's first or second
   const int fj = sl & 1, fch = ln.ch + fj;
   const bool fon = sl < 2 && (fj ? ln.two : ln.on);
-  const int fld = fj && !ln.two ? ln.ch : fch;  // where it loads from
-  const float fbias = in.dt_bias ? in.dt_bias[fld] : 0.f, fskip = in.D ? in.D[fld] : 0.f;
+  const float fskip = in.D && fon ? in.D[fch] : 0.f;
   float2 bias = f2(0.f);
   if (in.dt_bias) bias = make_float2(in.dt_bias[ln.ch], in.dt_bias[ln.ch + (ln.two ? 1 : 0)]);
 
@@ -572,20 +709,26 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   auto st = [&](int k) { return sl * SPT + ((k >> 1) ^ swap) * 4 + (k & 1) * 2; };
   float2 a2[2][K2], h[2][K2], gc[2][K2], dA[2][K2];
   const int64_t gat = ((int64_t)p.b * d.nc + p.c) * d.D + ln.ch;  // row of (B, nc, D)
+  auto load = [&](float2 (&v)[2][K2], const float* rows) {  // the pair's rows of states
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const bool on = j ? ln.two : ln.on;
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        float2 g[2];
+        ld_states<2>(g, rows + (int64_t)j * d.N, st(2 * q), d.N, j ? ln.two : ln.on, d.v4);
+        v[j][2 * q] = g[0];
+        v[j][2 * q + 1] = g[1];
+      }
+  };
+  load(a2, in.A + (int64_t)ln.ch * d.N);
+  load(gc, gin + gat * d.N);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int k = 0; k < K2; ++k) {
-      const int s = st(k);
-      const bool o0 = on && s < d.N, o1 = on && s + 1 < d.N;
-      const float* A = in.A + (int64_t)(ln.ch + j) * d.N + s;
-      const float* G = gin + (gat + j) * d.N + s;
-      a2[j][k] = make_float2(o0 ? A[0] * kLog2e : 0.f, o1 ? A[1] * kLog2e : 0.f);
-      gc[j][k] = make_float2(o0 ? G[0] : 0.f, o1 ? G[1] : 0.f);
+      a2[j][k] = mul2(a2[j][k], f2(kLog2e));
       dA[j][k] = f2(0.f);
     }
-  }
   float dD = 0.f, dbias = 0.f;
   int ph = 0;
   const int cfirst = p.c * (d.L / kBwdL), clast = min(d.nh, cfirst + d.L / kBwdL) - 1;
@@ -596,52 +739,49 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       RowTile<Tin, NP, kBwdL, kBwdThreads> tB, tC;
       tB.fetch(Bm + t0 * d.bs, d.bs, d.N, 0, nt);
       tC.fetch(Cm + t0 * d.cs, d.cs, d.N, 0, nt);
-      // lane -> (position sl + SL i, pair cl): delta, delta x and dy, once
-#pragma unroll 4
-      for (int t = sl; t < kBwdL; t += SL) {
-        float2 dl = f2(0.f), xd = f2(0.f), dy = f2(0.f);
-        if (ln.on && t < nt) {
-          const int64_t at = (int64_t)(t0 + t) * d.D + ln.ch;
-          const Two<Tin> rx = ld_two<Tin, WIDE>(x + at, ln.two);
-          const Two<Tin> rd = ld_two<Tin, WIDE>(dt + at, ln.two);
-          const Two<Tin> rg = ld_two<Tin, WIDE>(dout + at, ln.two);
-          dl = softplus2(add2(unpack2(rd), bias));
-          xd = mul2(dl, unpack2(rx));
-          dy = unpack2(rg);
+      // lane -> (position sl + SL i, pair cl): delta, x and dy, once; kE
+      // positions' loads together (past the end: the last one's, not used)
+      constexpr int kE = 8;
+      for (int i0 = 0; i0 < kBwdL / SL; i0 += kE) {
+        Two<Tin> rx[kE], rd[kE], rg[kE], rz[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int64_t t = t0 + max(min(sl + SL * (i0 + i), nt - 1), 0);
+          rx[i] = ld_two(x + t * d.D + ln.ch, ln.two, d.wide);
+          rd[i] = ld_two(dt + t * d.D + ln.ch, ln.two, d.wide);
+          rg[i] = ld_two(dout + t * d.D + ln.ch, ln.two, d.wide);
+          if (z) rz[i] = ld_two(z + t * d.zs + ln.ch, ln.two, d.wide);
+        }
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int t = sl + SL * (i0 + i);
+          float2 xv = unpack2(rx[i]), dl = softplus2(add2(unpack2(rd[i]), bias));
+          float2 dy = unpack2(rg[i]);
           if (z) {
-            const float2 zv =
-                unpack2(ld_two<Tin, WIDE>(z + (int64_t)(t0 + t) * d.zs + ln.ch, ln.two));
+            const float2 zv = unpack2(rz[i]);
             dy = mul2(dy, mul2(zv, sigmoid2(zv)));
           }
-          if (!ln.two) dl.y = xd.y = dy.y = 0.f;
+          if (!ln.on || t >= nt) dl = xv = dy = f2(0.f);
+          if (!ln.two) dl.y = xv.y = dy.y = 0.f;
+          if (i0 + i < kBwdL / SL) {
+            sm.delta[warp][t][cl] = dl;
+            sm.x[warp][t][cl] = xv;
+            sm.dy[warp][t][cl] = dy;
+          }
         }
-        sm.delta[warp][t][cl] = dl;
-        sm.dtx[warp][t][cl] = xd;
-        sm.dy[warp][t][cl] = dy;
       }
       tB.store(sm.B);
       tC.store(sm.C);
     }
     const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
-    auto enter = [&]() {  // h = the state entering the chunk
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool on = j ? ln.two : ln.on;
-#pragma unroll
-        for (int k = 0; k < K2; ++k) {
-          const int s = st(k);
-          const float* H = hin + (hat + j) * d.N + s;
-          h[j][k] = make_float2(on && s < d.N ? H[0] : 0.f, on && s + 1 < d.N ? H[1] : 0.f);
-        }
-      }
-    };
+    auto enter = [&]() { load(h, hin + hat * d.N); };  // the state entering the chunk
     enter();
     __syncthreads();
     const float4* const sBv = reinterpret_cast<const float4*>(sm.B);
     const float4* const sCv = reinterpret_cast<const float4*>(sm.C);
     auto at4 = [&](int t, int q) { return (t * NP + sl * SPT) / 4 + (q ^ swap); };
     auto step = [&](int t) {  // h at position t from h at t - 1
-      const float2 dl = sm.delta[warp][t][cl], xd = sm.dtx[warp][t][cl];
+      const float2 dl = sm.delta[warp][t][cl], xd = mul2(dl, sm.x[warp][t][cl]);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const float4 b4 = sBv[at4(t, q)];
@@ -681,19 +821,6 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
             h[j][2 * q + 1] = hi2(v);
           }
       };
-      // inputs of the positions that this lane finishes
-      float fx[kBwdTS], fdt[kBwdTS], fg[kBwdTS], fz[kBwdTS];
-#pragma unroll
-      for (int u = 0; u < kBwdTS; ++u) {
-        const bool in = fon && tb + u < nt;
-        const int64_t t = t0 + tb + u;
-        fx[u] = in ? to_f(x[t * d.D + fld]) : 0.f;
-        fdt[u] = in ? to_f(dt[t * d.D + fld]) : 0.f;
-        if (z) {
-          fg[u] = in ? to_f(dout[t * d.D + fld]) : 0.f;
-          fz[u] = in ? to_f(z[t * d.zs + fld]) : 0.f;
-        }
-      }
       // a lane's pair of sums -> the sum of the channel it finishes, over its SL lanes
       auto finish = [&](float2 v) {
         float r = (fj ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, fj ? v.x : v.y, CL);
@@ -702,6 +829,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         return r;
       };
       float2 hs[kBwdTS][2][K2];
+      float ys[kBwdTS];  // sum_n C h of the channel that this lane finishes
       begin();
 #pragma unroll
       for (int u = 0; u < kBwdTS; ++u) {
@@ -721,20 +849,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
               y[j] = fma2(h[j][2 * q + 1], hi2(c4), y[j]);
             }
           }
-          const float yv =
-              fmaf(fskip, fx[u], finish(make_float2(y[0].x + y[0].y, y[1].x + y[1].y)));
-          if (fon && tb + u < t1 - t0) {
-            const float sg = sigmoid(fz[u]);
-            dz[(rowb + t0 + tb + u) * d.D + fch] =
-                from_f<Tout>(fg[u] * yv * sg * (1.f + fz[u] * (1.f - sg)));
-          }
+          ys[u] = finish(make_float2(y[0].x + y[0].y, y[1].x + y[1].y));
         }
       }
       begin();
 #pragma unroll
       for (int u = kBwdTS - 1; u >= 0; --u) {
         const int t = tb + u;
-        const float2 dl = sm.delta[warp][t][cl], xd = sm.dtx[warp][t][cl], dy = sm.dy[warp][t][cl];
+        const float2 dl = sm.delta[warp][t][cl], xv = sm.x[warp][t][cl], dy = sm.dy[warp][t][cl];
+        const float2 xd = mul2(dl, xv);
         float2 gb[2] = {f2(0.f), f2(0.f)}, aw[2] = {f2(0.f), f2(0.f)}, vB[K2], vC[K2];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -786,16 +909,19 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         }
         const float fgb = finish(make_float2(gb[0].x + gb[0].y, gb[1].x + gb[1].y));
         const float faw = finish(make_float2(aw[0].x + aw[0].y, aw[1].x + aw[1].y)) * kLn2;
+        const float fdl = fj ? dl.y : dl.x, fdy = fj ? dy.y : dy.x, fx = fj ? xv.y : xv.x;
+        // sigmoid(v) = 1 - e^-softplus(v)
+        const float dv = t < nt ? fmaf(fx, fgb, faw) * one_minus_exp(fdl) : 0.f;
         if (fon && t < t1 - t0) {
           const int64_t at = (rowb + t0 + t) * d.D + fch;
-          const float fdl = fj ? dl.y : dl.x, fdy = fj ? dy.y : dy.x;
-          float dv = 0.f;
-          if (t < nt) dv = fmaf(fx[u], fgb, faw) * sigmoid(fdt[u] + fbias);
           dx[at] = from_f<Tout>(fmaf(fdl, fgb, fskip * fdy));
           ddt[at] = from_f<Tout>(dv);
-          dD = fmaf(fdy, fx[u], dD);
+          dD = fmaf(fdy, fx, dD);
           dbias += dv;
+          // dy's slot is free now: it takes y for dz
+          if (z) reinterpret_cast<float*>(&sm.dy[warp][t][cl])[fj] = fmaf(fskip, fx, ys[u]);
         }
+        __syncwarp();
       }
       __syncthreads();
       for (int i = threadIdx.x; i < kBwdTS * 2 * NP; i += kBwdThreads) {
@@ -810,6 +936,28 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       }
       ph ^= 1;
     }
+    if (z) {  // dz = dout y silu'(z), a pair a lane
+      constexpr int kE = 8;
+      for (int i0 = 0; i0 < kBwdL / SL; i0 += kE) {
+        Two<Tin> rg[kE], rz[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int64_t t = t0 + max(min(sl + SL * (i0 + i), nt - 1), 0);
+          rg[i] = ld_two(dout + t * d.D + ln.ch, ln.two, d.wide);
+          rz[i] = ld_two(z + t * d.zs + ln.ch, ln.two, d.wide);
+        }
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int t = sl + SL * (i0 + i);
+          if (i0 + i < kBwdL / SL && ln.on && t < t1 - t0) {
+            const float2 zv = unpack2(rz[i]), sg = sigmoid2(zv);
+            const float2 ds = fma2(mul2(sg, zv), fma2(sg, f2(-1.f), f2(1.f)), sg);
+            const float2 o = mul2(mul2(unpack2(rg[i]), sm.dy[warp][t][cl]), ds);
+            st_two(dz + (rowb + t0 + t) * d.D + ln.ch, t < nt ? o : f2(0.f), ln.two, d.wide);
+          }
+        }
+      }
+    }
   }
   if (fon) {
     const int64_t at = ((int64_t)p.b * d.nc + p.c) * d.D + fch;
@@ -819,15 +967,12 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (!(j ? ln.two : ln.on)) continue;
-    float* a = dApart + (gat + j) * d.N;
     float* gi = dinit && p.c == 0 ? dinit + ((int64_t)p.b * d.D + ln.ch + j) * d.N : nullptr;
 #pragma unroll
-    for (int k = 0; k < K2; ++k) {
-      const int s = st(k);
-      if (s < d.N) a[s] = dA[j][k].x;
-      if (s + 1 < d.N) a[s + 1] = dA[j][k].y;
-      if (gi && s < d.N) gi[s] = gc[j][k].x;
-      if (gi && s + 1 < d.N) gi[s + 1] = gc[j][k].y;
+    for (int q = 0; q < Q; ++q) {
+      const float2 a[2] = {dA[j][2 * q], dA[j][2 * q + 1]}, g[2] = {gc[j][2 * q], gc[j][2 * q + 1]};
+      st_states<2>(a, dApart + (gat + j) * d.N, st(2 * q), d.N, d.v4);
+      if (gi) st_states<2>(g, gi, st(2 * q), d.N, d.v4);
     }
   }
 }
@@ -929,8 +1074,10 @@ void fwd_chunks(SelDims* d) {
 }
 
 // Backward: the two passes have their own channel tiles (first: as the
-// forward; main: SPT 8 states a lane).  Ranges of whole chunks, as many as give
-// the main pass about four waves of its two blocks an SM.
+// forward; main: half the states a lane).  Ranges of whole chunks; their length
+// is the one with the shortest modelled time: each pass runs in waves of its
+// two blocks an SM, and a range costs the main pass about 24 issues an element,
+// the first 7.
 int bwd_main_tiles(const SelDims& d) {
   const int sl = d.N > 32 ? 8 : d.N > 16 ? 4 : 2;
   return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);
@@ -939,16 +1086,23 @@ void bwd_chunks(SelDims* d) {
   const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   d->nh = ceil_div(d->T, kBwdL);
-  const int64_t blocks = (int64_t)d->B * d->G * bwd_main_tiles(*d);
-  int64_t ranges = ceil_div(4 * 2 * 152, blocks);
-  if (ranges > d->nh) ranges = d->nh;
-  const int per = ceil_div(d->nh, ranges);
-  d->L = per * kBwdL;
-  d->nc = ceil_div(d->nh, per);
+  const int64_t bg = (int64_t)d->B * d->G, wave = 2 * 152;
+  int64_t best = -1;
+  int best_per = 1;
+  for (int per = 1; per <= d->nh && per <= 64; ++per) {
+    const int64_t nc = ceil_div(d->nh, per);
+    const int64_t main = (bg * bwd_main_tiles(*d) * nc + wave - 1) / wave;
+    const int64_t first = (bg * d->ctiles * nc + wave - 1) / wave;
+    // (half a chunk's time for what a range costs by itself)
+    const int64_t cost = (24 * main + 7 * first) * (2 * per + 1);
+    if (best < 0 || cost < best) best = cost, best_per = per;
+  }
+  d->L = best_per * kBwdL;
+  d->nc = ceil_div(d->nh, best_per);
 }
 
 struct SelBwdWs {
-  float *hin, *gin, *sumd, *bc, *dA, *pp;
+  float *hin, *gin, *sumd, *sumg, *bc, *dA, *pp;
   size_t total;
 };
 
@@ -964,6 +1118,7 @@ SelBwdWs bwd_ws(const SelDims& d, void* base) {
   w.hin = take(hd * d.N);
   w.gin = take(cd * d.N);
   w.sumd = take(hd);
+  w.sumg = take(cd);
   w.dA = take(cd * d.N);
   w.pp = take(cd * 2);
   w.bc = take((size_t)d.B * d.T * d.G * bwd_main_tiles(d) * 2 * d.N);
@@ -976,34 +1131,45 @@ dim3 sel_grid(const SelDims& d, int chunks) {
 }
 
 cudaError_t combine(const SelDims& d, const float* A, const float* init, const float* dfinal,
-                    float* hin, float* gin, const float* sumd, cudaStream_t s) {
+                    float* hin, float* gin, const float* sumd, const float* sumg, cudaStream_t s) {
   const int64_t n = (int64_t)d.B * d.D * d.N;
   const dim3 grid((unsigned)((n + 255) / 256), gin ? 2 : 1);
   cudaError_t e;
   SSD_LAUNCH("k_sel_combine", s, e = launch_pdl(k_sel_combine, grid, 256, 0, s, A, init, dfinal,
-                                                hin, gin, sumd, d, d.L / kBwdL));
+                                                hin, gin, sumd, sumg, d));
   return e;
 }
 
-template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  return bytes <= 48 * 1024
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename Tin, typename Tout, int SPT, int SL>
 int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out, float* fin,
                 float* hin, float* sumd, cudaStream_t s) {
   Tout* const o = static_cast<Tout*>(out);
+  auto kstate = k_sel_scan<Tin, Tout, SPT, SL, false>;
+  auto kout = k_sel_scan<Tin, Tout, SPT, SL, true>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 2, false>);
+  constexpr size_t mo = sizeof(PassSmem<Tin, SPT, SL, 3, true>);
+  if (allow_smem(kstate, ms) != cudaSuccess || allow_smem(kout, mo) != cudaSuccess)
+    return SSD_ERR_CUDA;
   if (d.nc > 1) {
     SSD_LAUNCH("k_sel_chunk_state", s,
-               k_sel_scan<Tin, Tout, SPT, SL, WIDE, false>
-               <<<sel_grid(d, d.nc - 1), kFwdThreads, 0, s>>>(in, nullptr, hin, sumd, nullptr,
-                                                              nullptr, d));
-    if (combine(d, in.A, init, nullptr, hin, nullptr, sumd, s) != cudaSuccess) return SSD_ERR_CUDA;
+               kstate<<<sel_grid(d, d.nc - 1), kFwdThreads, ms, s>>>(in, nullptr, hin, sumd,
+                                                                     nullptr, nullptr, d));
+    if (combine(d, in.A, init, nullptr, hin, nullptr, sumd, nullptr, s) != cudaSuccess)
+      return SSD_ERR_CUDA;
     cudaError_t e;
-    SSD_LAUNCH("k_sel_scan", s,
-               e = launch_pdl(k_sel_scan<Tin, Tout, SPT, SL, WIDE, true>, sel_grid(d, d.nc),
-                              kFwdThreads, 0, s, in, init, hin, sumd, o, fin, d));
+    SSD_LAUNCH("k_sel_scan", s, e = launch_pdl(kout, sel_grid(d, d.nc), kFwdThreads, mo, s, in,
+                                               init, hin, sumd, o, fin, d));
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
   }
   SSD_LAUNCH("k_sel_scan", s,
-             k_sel_scan<Tin, Tout, SPT, SL, WIDE, true>
-             <<<sel_grid(d, 1), kFwdThreads, 0, s>>>(in, init, hin, sumd, o, fin, d));
+             kout<<<sel_grid(d, 1), kFwdThreads, mo, s>>>(in, init, hin, sumd, o, fin, d));
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -1016,21 +1182,22 @@ struct SelGrads {
 
 // SPT, SL: the first pass's states and state lanes; the main pass has half the
 // states a lane (its live set is three times as large) on twice the lanes.
-template <typename Tin, typename Tout, int SPT, int SL, bool WIDE>
+template <typename Tin, typename Tout, int SPT, int SL>
 int sel_backward(const SelDims& d, const SelIn& in, const float* init, const void* dout,
                  const float* dfinal, const SelGrads& g, const SelBwdWs& w, cudaStream_t s) {
   const Tin* go = static_cast<const Tin*>(dout);
-  SSD_LAUNCH("k_sel_state", s,
-             k_sel_state<Tin, SPT, SL, WIDE><<<sel_grid(d, d.nc), kFwdThreads, 0, s>>>(
-                 in, go, w.hin, w.gin, w.sumd, d));
-  if (combine(d, in.A, init, dfinal, w.hin, w.gin, w.sumd, s) != cudaSuccess) return SSD_ERR_CUDA;
+  auto kstate = k_sel_state<Tin, SPT, SL>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 4, true>);
+  if (allow_smem(kstate, ms) != cudaSuccess) return SSD_ERR_CUDA;
+  SSD_LAUNCH("k_sel_state", s, kstate<<<sel_grid(d, d.nc), kFwdThreads, ms, s>>>(
+                                   in, go, w.hin, w.gin, w.sumd, w.sumg, d));
+  if (combine(d, in.A, init, dfinal, w.hin, w.gin, w.sumd, w.sumg, s) != cudaSuccess)
+    return SSD_ERR_CUDA;
   SelDims m = d;
   m.ctiles = bwd_main_tiles(d);
-  auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2, WIDE>;
+  auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2>;
   constexpr size_t smem = sizeof(BwdSmem<SPT / 2, SL * 2>);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return SSD_ERR_CUDA;
+  if (allow_smem(kern, smem) != cudaSuccess) return SSD_ERR_CUDA;
   cudaError_t e;
   SSD_LAUNCH("k_sel_bwd", s,
              e = launch_pdl(kern, sel_grid(m, m.nc), kBwdThreads, smem, s, in, go, w.hin, w.gin,
@@ -1053,19 +1220,27 @@ int sel_backward(const SelDims& d, const SelIn& in, const float* init, const voi
 template <int V>
 using Int = std::integral_constant<int, V>;
 template <typename F>
-int by_states(int N, bool wide, F&& f) {
-  auto go = [&](auto spt, auto sl) {
-    return wide ? f(spt, sl, std::true_type{}) : f(spt, sl, std::false_type{});
-  };
-  if (N <= 8) return go(Int<8>{}, Int<1>{});
-  if (N <= 16) return go(Int<16>{}, Int<1>{});
-  if (N <= 32) return go(Int<16>{}, Int<2>{});
-  return go(Int<16>{}, Int<4>{});
+int by_states(int N, F&& f) {
+  if (N <= 8) return f(Int<8>{}, Int<1>{});
+  if (N <= 16) return f(Int<16>{}, Int<1>{});
+  if (N <= 32) return f(Int<16>{}, Int<2>{});
+  return f(Int<16>{}, Int<4>{});
 }
 
-// Whether channel pairs can be accessed as one element of twice the size.
-bool pairs_ok(const void* p, int64_t row, int64_t batch, int esize) {
-  return vec_ok(p, row, esize, 2) && vec_ok(p, batch, esize, 2);
+// How the inputs (and outputs of oe bytes an element) can be accessed: the
+// rings' mode, the pairs' width, and the state rows.
+void access(SelDims* d, int ie, int oe, const void* const* ins, const void* const* outs,
+            const void* z, const void* const* states) {
+  d->v4 = 1;
+  for (int i = 0; i < 3; ++i) d->v4 = d->v4 && vec_ok(states[i], d->N, 4, 4);
+  auto rows_ok = [&](int v) {
+    bool ok = d->DG % v == 0;
+    for (int i = 0; i < 3; ++i) ok = ok && vec_ok(ins[i], d->D, ie, v);
+    return ok && (!z || (vec_ok(z, d->zs, ie, v) && vec_ok(z, d->zb, ie, v)));
+  };
+  d->mode = rows_ok(16 / ie) ? 16 : rows_ok(2) ? 2 : 1;
+  d->wide = d->mode != 1;
+  for (int i = 0; i < 3; ++i) d->wide = d->wide && vec_ok(outs[i], d->D, oe, 2);
 }
 
 bool off(const void* p, int esize) {
@@ -1120,11 +1295,13 @@ int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, cons
       align_up((size_t)d.B * d.nc * d.D * d.N * sizeof(float), 256));
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool wide = d.DG % 2 == 0 && pairs_ok(x, d.D, 0, ie) && pairs_ok(dt, d.D, 0, ie) &&
-                    pairs_ok(out, d.D, 0, oe) && (!z || pairs_ok(z, d.zs, d.zb, ie));
-  return by_states(d.N, wide, [&](auto spt, auto sl, auto w) {
+  const void* const ins[3] = {x, dt, nullptr};
+  const void* const outs[3] = {out, nullptr, nullptr};
+  const void* const states[3] = {A, init_states, final_states};
+  access(&d, ie, oe, ins, outs, z, states);
+  return by_states(d.N, [&](auto spt, auto sl) {
 #define SSD_GO(TI, TO)                                                                      \
-  sel_forward<TI, TO, spt(), sl(), w()>(d, in, init_states, out, final_states, hin, sumd, s)
+  sel_forward<TI, TO, spt(), sl()>(d, in, init_states, out, final_states, hin, sumd, s)
     if (ie == 4) return SSD_GO(float, float);
     return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
 #undef SSD_GO
@@ -1158,11 +1335,13 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const SelGrads g{dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit_states};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool wide = d.DG % 2 == 0 && pairs_ok(x, d.D, 0, ie) && pairs_ok(dt, d.D, 0, ie) &&
-                    pairs_ok(dout, d.D, 0, ie) && (!z || pairs_ok(z, d.zs, d.zb, ie));
-  return by_states(d.N, wide, [&](auto spt, auto sl, auto wd) {
+  const void* const ins[3] = {x, dt, dout};
+  const void* const outs[3] = {dz, nullptr, nullptr};
+  const void* const states[3] = {A, dinit_states, nullptr};
+  access(&d, ie, oe, ins, outs, z, states);
+  return by_states(d.N, [&](auto spt, auto sl) {
 #define SSD_GO(TI, TO)                                                                      \
-  sel_backward<TI, TO, spt(), sl(), wd()>(d, in, init_states, dout, dfinal_states, g, w, s)
+  sel_backward<TI, TO, spt(), sl()>(d, in, init_states, dout, dfinal_states, g, w, s)
     if (ie == 4) return SSD_GO(float, float);
     return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
 #undef SSD_GO
