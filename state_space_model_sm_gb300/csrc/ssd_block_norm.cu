@@ -7,16 +7,20 @@
 // next layer's opening norm are one pass over r and o.  The backward takes the
 // forward's inputs and forms r' again:
 //     gx = dh w_pre,  dR = dr' + rstd(r') (gx - xhat mean(gx xhat)),  xhat = r' rstd(r')
-//     dr = dR,  dw_pre = sum dh xhat,  dgate = s sum dR t
-//     dt = s gate dR,  dw_post = sum dt ohat,  do = rstd(o) (gy - ohat mean(gy ohat)),
-//     gy = dt w_post,  ohat = o rstd(o).
+//     dr = dR,  dw_pre = sum dh xhat,  do = rstd(o) (gy - ohat mean(gy ohat)),
+//     gy = s gate w_post dR,  ohat = o rstd(o)
+// and, with P_g = sum of dR ohat over the rows of gate row g,
+//     dgate_g = s w_post P_g,  dw_post = sum_g s gate_g P_g,
+// so two sums over rows give all three gradients.
 // The pages name no kernel for it.
 //
 // HBM-bound: 12 bytes an element forward and 18 backward (bf16 layer, fp32
-// residual) against ~12 and ~30 operations.  A block owns a contiguous range
-// of rows and walks it, a thread keeping its columns, so the weight gradients
-// stay in registers until the range ends; the row's sums are two (forward) or
-// three (backward) block-wide reductions.
+// residual), which leaves about 65 and 98 issue slots an element and lane; so
+// the arithmetic is in packed pairs, an absent weight or gate is a vector of
+// ones (no branches), and a thread owns 16 columns, over which the two (forward)
+// or three (backward) block-wide sums of a row are spread.  A block owns a
+// contiguous range of rows and walks it, a thread keeping its columns, so the
+// weight gradients stay in registers until the range ends.
 #include <cuda_bf16.h>
 
 #include "layer_math.cuh"
@@ -31,232 +35,407 @@ using bf16 = __nv_bfloat16;
 struct BnDims {
   int rows, F, ng, gs;  // gs: rows of a gate row
   int R, grid;          // rows of a block; blocks
+  int nt, S;            // threads of a block; ring stages
   float eps, scale;
 };
 
 constexpr int kMaxThreads = 512;
+constexpr int kMaxStages = 4;
 
-// Sums of a and b over the block, in warp order.  Buffers alternate (ph), so one
-// barrier a call is enough.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2 (*red)[16], int& ph) {
+// Sums over the block of v (both components), in warp order.  Buffers alternate
+// (ph), so one barrier a call is enough.
+__device__ __forceinline__ float2 block_sum(float2 v, float2 (*red)[16], int& ph) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) red[ph][threadIdx.x >> 5] = make_float2(a, b);
+  for (int o = 16; o > 0; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                            __shfl_xor_sync(0xffffffffu, v.y, o)));
+  const int nw = blockDim.x >> 5, pw = nw > 8 ? 16 : nw > 4 ? 8 : nw > 2 ? 4 : 2;
+  const int i = threadIdx.x & (pw - 1);  // every aligned group of pw lanes adds the warps' sums
+  if (nw == 1) return v;
+  if ((threadIdx.x & 31) == 0) red[ph][threadIdx.x >> 5] = v;
   __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-  for (int i = 0; i < nw; ++i) s.x += red[ph][i].x, s.y += red[ph][i].y;
+  v = i < nw ? red[ph][i] : f2(0.f);
+  for (int o = pw / 2; o > 0; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                            __shfl_xor_sync(0xffffffffu, v.y, o)));
   ph ^= 1;
-  return s;
+  return v;
+}
+__device__ __forceinline__ float block_sum(float a, float2 (*red)[16], int& ph) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int nw = blockDim.x >> 5, pw = nw > 8 ? 16 : nw > 4 ? 8 : nw > 2 ? 4 : 2;
+  const int i = threadIdx.x & (pw - 1);  // every aligned group of pw lanes adds the warps' sums
+  if (nw == 1) return a;
+  if ((threadIdx.x & 31) == 0) red[ph][threadIdx.x >> 5].x = a;
+  __syncthreads();
+  a = i < nw ? red[ph][i].x : 0.f;
+  for (int o = pw / 2; o > 0; o >>= 1)
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+  ph ^= 1;
+  return a;
 }
 
-template <typename Tio, typename Tres, int V, int NV>
-__global__ void __launch_bounds__(kMaxThreads)
+// A thread's EPT columns, as pairs.  VEC: EPT / 4 pieces of 4 consecutive columns
+// (16 bytes of fp32, 8 of bf16), the threads' pieces side by side, so every
+// access of a warp is one unbroken run (8 columns would be 32-byte pieces of
+// fp32, whose 16-byte halves touch each sector twice: 20 % slower); else single
+// columns, blockDim.x apart (widths or addresses that these do not fit).
+template <bool VEC, int EPT>
+struct Cols {
+  static constexpr int W = VEC ? 4 : 1, P2 = EPT / 2, NV = EPT / W;
+  __device__ __forceinline__ static int col(int v) {
+    return (v * (int)blockDim.x + (int)threadIdx.x) * W;
+  }
+  template <typename T>
+  __device__ __forceinline__ static void load(const T* p, int F, float2 (&x)[P2], float fill) {
+    float* f = reinterpret_cast<float*>(x);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = col(v);
+      float t[W];
+      if (c < F && p) {
+        unpack<T, W>(ld_raw<T, W>(p + c), t);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) t[i] = fill;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[v * W + i] = t[i];
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ static void store(T* p, int F, const float2 (&x)[P2]) {
+    const float* f = reinterpret_cast<const float*>(x);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = col(v);
+      if (c >= F) break;
+      float t[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) t[i] = f[v * W + i];
+      st_raw<T, W>(p + c, pack<T, W>(t));
+    }
+  }
+};
+
+// A block's rows of its inputs.  VEC: a ring in shared memory; a thread copies the
+// pieces that it will use itself, S - 1 rows ahead, so the bytes in flight are
+// set by the ring and no barrier is needed.  Else plain loads of the row.
+// Addresses advance by a row at a time.
+template <typename Tio, typename Tres, bool VEC, int EPT, int NIO, int NRES>
+struct Rows {
+  using C = Cols<VEC, EPT>;
+  static constexpr int NV = VEC ? C::NV : 0;
+  // bytes of a thread's piece of one tensor, of its row of one, of its slot
+  static constexpr int kIo = 4 * sizeof(Tio), kRes = 4 * sizeof(Tres);
+  static constexpr int kSlot = NV * (NIO * kIo + NRES * kRes);
+  const Tio* io[NIO];     // VEC: this thread's first column of the next row to copy;
+  const Tres* res[NRES];  // else the row in use
+  uint32_t put, use, end, slot;  // ring offsets: next copy's slot, the row in use; end; a slot
+  int F, S, left;                // left: rows still to copy
+
+  __device__ __forceinline__ static unsigned char* smem() {
+    extern __shared__ __align__(16) unsigned char ring[];
+    return ring;
+  }
+  __device__ __forceinline__ void start(int width, int stages, int r0, int r1) {
+    F = width, S = stages, left = r1 - r0;
+    const int64_t at = VEC ? (int64_t)r0 * F + C::col(0) : ((int64_t)r0 - 1) * F;
+#pragma unroll
+    for (int i = 0; i < NIO; ++i) io[i] += at;
+#pragma unroll
+    for (int i = 0; i < NRES; ++i)
+      if (res[i]) res[i] += at;
+    if constexpr (VEC) {
+      slot = kSlot * blockDim.x, end = S * slot, put = 0, use = end - slot;
+      for (int i = 0; i < S - 1; ++i) fill();
+    }
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int i = 0; i < NIO; ++i) io[i] += F;
+#pragma unroll
+    for (int i = 0; i < NRES; ++i)
+      if (res[i]) res[i] += F;
+  }
+  // offset in a slot of this thread's piece v of tensor i (io first, then res)
+  __device__ __forceinline__ static uint32_t io_at(int i, int v) {
+    return (i * NV + v) * kIo * blockDim.x + threadIdx.x * kIo;
+  }
+  __device__ __forceinline__ static uint32_t res_at(int i, int v) {
+    return (NIO * NV * kIo + (i * NV + v) * kRes) * blockDim.x + threadIdx.x * kRes;
+  }
+  __device__ __forceinline__ void fill() {  // the next row, into the next slot
+    if (left > 0) {
+      unsigned char* const q = smem() + put;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (C::col(v) >= F) break;
+        const int c = v * (int)blockDim.x * 4;
+#pragma unroll
+        for (int i = 0; i < NIO; ++i) cp_async<kIo>(q + io_at(i, v), io[i] + c);
+#pragma unroll
+        for (int i = 0; i < NRES; ++i)
+          if (res[i]) cp_async<kRes>(q + res_at(i, v), res[i] + c);
+      }
+      advance();
+      --left;
+      put = put + slot == end ? 0 : put + slot;
+    }
+    cp_commit();
+  }
+  // Makes the next row readable and starts the copy of the one S - 1 further,
+  // into the slot that this thread read last.
+  __device__ __forceinline__ void next() {
+    if constexpr (VEC) {
+      use = use + slot == end ? 0 : use + slot;
+      if (S == 1) {  // no room for a second row: copied when it is needed
+        fill();
+        cp_wait<0>();
+        return;
+      }
+      if (S == 4)
+        cp_wait<2>();
+      else if (S == 3)
+        cp_wait<1>();
+      else
+        cp_wait<0>();
+      fill();
+    } else {
+      advance();
+    }
+  }
+  __device__ __forceinline__ void get_io(int i, float2 (&x)[C::P2]) const {
+    if constexpr (VEC)
+      get<Tio>(io_at(i, 0), kIo, true, x);
+    else
+      C::load(io[i], F, x, 0.f);
+  }
+  __device__ __forceinline__ void get_res(int i, float2 (&x)[C::P2]) const {
+    if constexpr (VEC)
+      get<Tres>(res_at(i, 0), kRes, res[i] != nullptr, x);
+    else
+      C::load(res[i], F, x, 0.f);
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(uint32_t at, int piece, bool there, float2 (&x)[C::P2]) const {
+    float* f = reinterpret_cast<float*>(x);
+    const unsigned char* q = smem() + use + at;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      Raw<T, 4> r = zero_raw<T, 4>();
+      if (C::col(v) < F && there)
+        r = *reinterpret_cast<const Raw<T, 4>*>(q + v * piece * blockDim.x);
+      float t[4];
+      unpack<T, 4>(r, t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[v * 4 + k] = t[k];
+    }
+  }
+};
+
+// d r' / d ohat of a thread's columns: s gate_g w_post (absent vectors: ones).
+template <typename C>
+__device__ __forceinline__ void load_gw(float2 (&gw)[C::P2], const float* w_post, const float* gate,
+                                        int g, const BnDims& d) {
+  float2 t[C::P2];
+  C::load(w_post, d.F, gw, 1.f);
+  C::load(gate ? gate + (int64_t)g * d.F : gate, d.F, t, 1.f);
+#pragma unroll
+  for (int i = 0; i < C::P2; ++i) gw[i] = mul2(gw[i], mul2(t[i], f2(d.scale)));
+}
+
+template <typename Tio, typename Tres, bool VEC, int EPT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_fwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
                      const float* __restrict__ gate, Tres* __restrict__ rout, Tio* __restrict__ h,
                      BnDims d) {
+  using C = Cols<VEC, EPT>;
+  constexpr int P2 = C::P2;
   __shared__ float2 red[2][16];
   int ph = 0;
   const float inv = 1.f / (float)d.F;
   const int r0 = blockIdx.x * d.R, r1 = min(d.rows, r0 + d.R);
-  for (int row = r0; row < r1; ++row) {
-    const int64_t base = (int64_t)row * d.F;
-    const float* gp = gate ? gate + (int64_t)(row / d.gs) * d.F : nullptr;
-    float ov[NV][V], rv[NV][V], so = 0.f, sr = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      const bool in = c < d.F;
-      unpack<Tio, V>(in ? ld_raw<Tio, V>(o + base + c) : zero_raw<Tio, V>(), ov[v]);
-      unpack<Tres, V>(in ? ld_raw<Tres, V>(r + base + c) : zero_raw<Tres, V>(), rv[v]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) so = fmaf(ov[v][i], ov[v][i], so);
+  Rows<Tio, Tres, VEC, EPT, 1, 1> in;
+  in.io[0] = o, in.res[0] = r;
+  in.start(d.F, d.S, r0, r1);
+  float2 gw[P2], wp[P2];
+  C::load(w_pre, d.F, wp, 0.f);
+  int g = r0 / d.gs, gend = (g + 1) * d.gs;  // the gate row in use, and where it ends
+  load_gw<C>(gw, w_post, gate, g, d);
+  rout += (int64_t)r0 * d.F;
+  h += (int64_t)r0 * d.F;
+  for (int row = r0; row < r1; ++row, rout += d.F, h += d.F) {
+    if (row == gend) {
+      load_gw<C>(gw, w_post, gate, ++g, d);
+      gend += d.gs;
     }
+    in.next();
+    float2 ov[P2], rv[P2];
+    in.get_io(0, ov);
     float ro = 1.f;
-    if (w_post) ro = rsqrtf(block_sum2(so, 0.f, red, ph).x * inv + d.eps);
+    if (w_post) {
+      float2 so = f2(0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      if (c >= d.F) continue;
-      float wp[V], gt[V];
-      if (w_post) unpack<float, V>(ld_raw<float, V>(w_post + c), wp);
-      if (gp) unpack<float, V>(ld_raw<float, V>(gp + c), gt);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float t = ov[v][i];
-        if (w_post) t *= ro * wp[i];
-        if (gp) t *= gt[i];
-        rv[v][i] = fmaf(d.scale, t, rv[v][i]);
-        sr = fmaf(rv[v][i], rv[v][i], sr);
-      }
-      st_raw<Tres, V>(rout + base + c, pack<Tres, V>(rv[v]));
+      for (int i = 0; i < P2; ++i) so = fma2(ov[i], ov[i], so);
+      ro = rsqrtf(block_sum(so.x + so.y, red, ph) * inv + d.eps);
     }
-    const float rr = rsqrtf(block_sum2(sr, 0.f, red, ph).x * inv + d.eps);
+    in.get_res(0, rv);
+    float2 sr = f2(0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      if (c >= d.F) continue;
-      float wv[V];
-      unpack<float, V>(ld_raw<float, V>(w_pre + c), wv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) rv[v][i] *= rr * wv[i];
-      st_raw<Tio, V>(h + base + c, pack<Tio, V>(rv[v]));
+    for (int i = 0; i < P2; ++i) {
+      rv[i] = fma2(mul2(ov[i], f2(ro)), gw[i], rv[i]);
+      sr = fma2(rv[i], rv[i], sr);
     }
+    C::store(rout, d.F, rv);
+    const float rr = rsqrtf(block_sum(sr.x + sr.y, red, ph) * inv + d.eps);
+#pragma unroll
+    for (int i = 0; i < P2; ++i) rv[i] = mul2(mul2(rv[i], f2(rr)), wp[i]);
+    C::store(h, d.F, rv);
   }
 }
 
-// part: dw_pre (grid, F), dw_post (grid, F), dgate (grid + ng, F).  A block's
-// rows cover the gate rows g of a contiguous range; its part for g is slot
-// blockIdx.x + g, which no other (block, gate row) pair has, because from one
-// pair that shares rows to the next the block, the gate row or both grow.
-template <typename Tio, typename Tres, int V, int NV>
-__global__ void __launch_bounds__(kMaxThreads)
+// part: dw_pre (grid, F), P (grid + gate rows, F).  A block's rows cover the gate
+// rows g of a contiguous range (all rows are one without a gate); its part of
+// P_g is slot blockIdx.x + g, which no other (block, gate row) pair has, because
+// from one pair that shares rows to the next the block, the gate row or both
+// grow.
+template <typename Tio, typename Tres, bool VEC, int EPT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_bwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
                      const float* __restrict__ gate, const Tio* __restrict__ dh,
                      const Tres* __restrict__ drout, Tres* __restrict__ dr, Tio* __restrict__ dout,
                      float* __restrict__ part, BnDims d) {
+  using C = Cols<VEC, EPT>;
+  constexpr int P2 = C::P2;
   __shared__ float2 red[2][16];
+  griddep_launch_dependents();
   int ph = 0;
   const float inv = 1.f / (float)d.F;
   const int r0 = blockIdx.x * d.R, r1 = min(d.rows, r0 + d.R);
-  float apre[NV][V], apost[NV][V], agate[NV][V];
+  Rows<Tio, Tres, VEC, EPT, 2, 2> in;
+  in.io[0] = o, in.io[1] = dh, in.res[0] = r, in.res[1] = drout;
+  in.start(d.F, d.S, r0, r1);
+  float2 apre[P2], ap[P2], gw[P2], wp[P2];
+  C::load(w_pre, d.F, wp, 0.f);
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int i = 0; i < V; ++i) apre[v][i] = apost[v][i] = agate[v][i] = 0.f;
-  float* const pgate = part + 2 * (int64_t)d.grid * d.F;
-  for (int row = r0; row < r1; ++row) {
-    const int64_t base = (int64_t)row * d.F;
-    const float* gp = gate ? gate + (int64_t)(row / d.gs) * d.F : nullptr;
-    float ov[NV][V], rv[NV][V], hv[NV][V], so = 0.f, sr = 0.f, sx = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      const bool in = c < d.F;
-      unpack<Tio, V>(in ? ld_raw<Tio, V>(o + base + c) : zero_raw<Tio, V>(), ov[v]);
-      unpack<Tres, V>(in ? ld_raw<Tres, V>(r + base + c) : zero_raw<Tres, V>(), rv[v]);
-      unpack<Tio, V>(in ? ld_raw<Tio, V>(dh + base + c) : zero_raw<Tio, V>(), hv[v]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) so = fmaf(ov[v][i], ov[v][i], so);
-    }
+  for (int i = 0; i < P2; ++i) apre[i] = ap[i] = f2(0.f);
+  float* const pp = part + (int64_t)d.grid * d.F;
+  int g = r0 / d.gs, gend = (g + 1) * d.gs;  // the gate row in use, and where it ends
+  load_gw<C>(gw, w_post, gate, g, d);
+  dr += (int64_t)r0 * d.F;
+  dout += (int64_t)r0 * d.F;
+  for (int row = r0; row < r1; ++row, dr += d.F, dout += d.F) {
+    in.next();
+    float2 ov[P2], rv[P2], t[P2];
+    in.get_io(0, ov);
     float ro = 1.f;
-    if (w_post) ro = rsqrtf(block_sum2(so, 0.f, red, ph).x * inv + d.eps);
-    // ov: ohat; rv: r'
+    if (w_post) {
+      float2 so = f2(0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      if (c >= d.F) continue;
-      float wp[V], gt[V], wv[V];
-      if (w_post) unpack<float, V>(ld_raw<float, V>(w_post + c), wp);
-      if (gp) unpack<float, V>(ld_raw<float, V>(gp + c), gt);
-      unpack<float, V>(ld_raw<float, V>(w_pre + c), wv);
+      for (int i = 0; i < P2; ++i) so = fma2(ov[i], ov[i], so);
+      ro = rsqrtf(block_sum(so.x + so.y, red, ph) * inv + d.eps);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ov[v][i] *= ro;
-        float t = ov[v][i];
-        if (w_post) t *= wp[i];
-        if (gp) t *= gt[i];
-        rv[v][i] = fmaf(d.scale, t, rv[v][i]);
-        sr = fmaf(rv[v][i], rv[v][i], sr);
-        sx = fmaf(hv[v][i] * wv[i], rv[v][i], sx);
-      }
+      for (int i = 0; i < P2; ++i) ov[i] = mul2(ov[i], f2(ro));  // ohat
     }
-    const float2 s2 = block_sum2(sr, sx, red, ph);
+    in.get_res(0, rv);
+    in.get_io(1, t);  // dh
+    float2 sr = f2(0.f), sx = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < P2; ++i) {
+      rv[i] = fma2(gw[i], ov[i], rv[i]);  // r'
+      sr = fma2(rv[i], rv[i], sr);
+      sx = fma2(mul2(t[i], wp[i]), rv[i], sx);
+    }
+    const float2 s2 = block_sum(make_float2(sr.x + sr.y, sx.x + sx.y), red, ph);
     const float rr = rsqrtf(s2.x * inv + d.eps), cx = s2.y * inv * rr * rr;
-    float sy = 0.f;
-    // rv: dR; hv: dt
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      if (c >= d.F) continue;
-      float wp[V], gt[V], wv[V], dv[V];
-      if (w_post) unpack<float, V>(ld_raw<float, V>(w_post + c), wp);
-      if (gp) unpack<float, V>(ld_raw<float, V>(gp + c), gt);
-      unpack<float, V>(ld_raw<float, V>(w_pre + c), wv);
-      unpack<Tres, V>(drout ? ld_raw<Tres, V>(drout + base + c) : zero_raw<Tres, V>(), dv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        apre[v][i] = fmaf(hv[v][i], rv[v][i] * rr, apre[v][i]);
-        rv[v][i] = dv[i] + rr * (hv[v][i] * wv[i] - rv[v][i] * cx);
-        float dt = d.scale * rv[v][i];
-        if (gp) {
-          agate[v][i] = fmaf(dt, w_post ? ov[v][i] * wp[i] : ov[v][i], agate[v][i]);
-          dt *= gt[i];
-        }
-        if (w_post) {
-          apost[v][i] = fmaf(dt, ov[v][i], apost[v][i]);
-          dt *= wp[i];
-        }
-        hv[v][i] = dt;
-        sy = fmaf(dt, ov[v][i], sy);
-      }
-      st_raw<Tres, V>(dr + base + c, pack<Tres, V>(rv[v]));
+    for (int i = 0; i < P2; ++i) {
+      apre[i] = fma2(t[i], mul2(rv[i], f2(rr)), apre[i]);
+      rv[i] = fma2(t[i], wp[i], mul2(rv[i], f2(-cx)));
     }
-    float cy = 0.f;
-    if (w_post) cy = block_sum2(sy, 0.f, red, ph).x * inv;
-    const bool flush = gp && (row + 1 == r1 || (row + 1) % d.gs == 0);
-    float* pg = pgate + (int64_t)(blockIdx.x + row / d.gs) * d.F;
+    in.get_res(1, t);  // dr'
+    float2 sy = f2(0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * V;
-      if (c >= d.F) continue;
-      if (w_post) {
+    for (int i = 0; i < P2; ++i) {
+      rv[i] = fma2(rv[i], f2(rr), t[i]);  // dR
+      ap[i] = fma2(rv[i], ov[i], ap[i]);
+    }
+    C::store(dr, d.F, rv);
 #pragma unroll
-        for (int i = 0; i < V; ++i) hv[v][i] = ro * (hv[v][i] - ov[v][i] * cy);
-      }
-      st_raw<Tio, V>(dout + base + c, pack<Tio, V>(hv[v]));
-      if (flush) {
-        st_raw<float, V>(pg + c, pack<float, V>(agate[v]));
+    for (int i = 0; i < P2; ++i) {
+      rv[i] = mul2(rv[i], gw[i]);  // gy
+      sy = fma2(rv[i], ov[i], sy);
+    }
+    if (w_post) {
+      const float cy = block_sum(sy.x + sy.y, red, ph) * inv;
 #pragma unroll
-        for (int i = 0; i < V; ++i) agate[v][i] = 0.f;
+      for (int i = 0; i < P2; ++i) rv[i] = mul2(fma2(ov[i], f2(-cy), rv[i]), f2(ro));
+    }
+    C::store(dout, d.F, rv);
+    if (row + 1 == gend || row + 1 == r1) {  // the gate row's part ends
+      C::store(pp + (int64_t)(blockIdx.x + g) * d.F, d.F, ap);
+      if (row + 1 < r1) {
+#pragma unroll
+        for (int i = 0; i < P2; ++i) ap[i] = f2(0.f);
+        load_gw<C>(gw, w_post, gate, ++g, d);
+        gend += d.gs;
       }
     }
   }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * blockDim.x + threadIdx.x) * V;
-    if (c >= d.F) continue;
-    st_raw<float, V>(part + (int64_t)blockIdx.x * d.F + c, pack<float, V>(apre[v]));
-    if (w_post)
-      st_raw<float, V>(part + (int64_t)(d.grid + blockIdx.x) * d.F + c, pack<float, V>(apost[v]));
-  }
+  C::store(part + (int64_t)blockIdx.x * d.F, d.F, apre);
 }
 
-// dw_pre, dw_post and the gate rows' gradients: the blocks' parts in a fixed
-// order, 32 columns a block, its 8 warps taking every 8th part.
+// dw_pre, dw_post and the gate rows' gradients from the blocks' parts in a fixed
+// order, 32 columns a block, its 16 warps taking every 16th block's part.
 // blockIdx.y = 0: dw_pre, 1: dw_post, 2 + g: gate row g.
-__global__ void __launch_bounds__(256)
-    k_block_norm_dw(const float* __restrict__ part, float* __restrict__ dw_pre,
+__global__ void __launch_bounds__(512)
+    k_block_norm_dw(const float* __restrict__ part, const float* __restrict__ w_post,
+                    const float* __restrict__ gate, float* __restrict__ dw_pre,
                     float* __restrict__ dw_post, float* __restrict__ dgate, BnDims d) {
-  __shared__ float red[8][32];
+  __shared__ float red[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, which = blockIdx.y, g = which - 2;
-  int k0 = 0, k1 = d.grid;
-  const float* p = part + (which == 1 ? (int64_t)d.grid * d.F : 0);
-  float* dst = which == 0 ? dw_pre : dw_post;
-  if (which >= 2) {
-    k0 = (int)((int64_t)g * d.gs / d.R);
-    k1 = (int)((((int64_t)g + 1) * d.gs - 1) / d.R) + 1;
-    p = part + (2 * (int64_t)d.grid + g) * d.F;
-    dst = dgate + (int64_t)g * d.F;
-  }
-  if (!dst) return;
+  griddep_wait();
+  float* const dst = which == 0 ? dw_pre : which == 1 ? dw_post : dgate + (int64_t)g * d.F;
+  if (which < 2 && !dst) return;
+  const float* pp = part + (int64_t)d.grid * d.F;
   float a = 0.f;
-  if (c < d.F)
-    for (int k = k0 + warp; k < k1; k += 8) a += p[(int64_t)k * d.F + c];
+  if (c < d.F) {
+    if (which == 0) {
+#pragma unroll 8
+      for (int k = warp; k < d.grid; k += 16) a += part[(int64_t)k * d.F + c];
+    } else if (which == 1 && d.ng <= 16) {  // gate row by gate row
+      for (int i = 0; i < (d.ng ? d.ng : 1); ++i) {
+        const int k0 = i * d.gs / d.R, k1 = ((i + 1) * d.gs - 1) / d.R + 1;
+        float p = 0.f;
+#pragma unroll 8
+        for (int k = k0 + warp; k < k1; k += 16) p += pp[(int64_t)(k + i) * d.F + c];
+        a = fmaf(gate ? gate[(int64_t)i * d.F + c] : 1.f, p, a);
+      }
+    } else if (which == 1) {  // block by block
+      for (int k = warp; k < d.grid; k += 16) {
+        const int g0 = k * d.R / d.gs, g1 = (min((k + 1) * d.R, d.rows) - 1) / d.gs;
+        for (int i = g0; i <= g1; ++i)
+          a = fmaf(gate[(int64_t)i * d.F + c], pp[(int64_t)(k + i) * d.F + c], a);
+      }
+    } else {
+      const int k0 = (int)((int64_t)g * d.gs / d.R);
+      const int k1 = (int)((((int64_t)g + 1) * d.gs - 1) / d.R) + 1;
+#pragma unroll 8
+      for (int k = k0 + warp; k < k1; k += 16) a += pp[(int64_t)(k + g) * d.F + c];
+    }
+  }
   red[warp][lane] = a;
   __syncthreads();
   if (warp == 0 && c < d.F) {
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][lane];
-    dst[c] = s;
+    for (int k = 0; k < 16; ++k) s += red[k][lane];
+    dst[c] = which == 0 ? s : d.scale * (which == 1 || !w_post ? s : w_post[c] * s);
   }
 }
 
@@ -280,18 +459,38 @@ int bn_dims(const ssd_block_norm_shape* s, BnDims* d) {
   return SSD_OK;
 }
 
-// Row ranges: as many blocks as are resident at once (1024 threads an SM),
-// each with the same number of consecutive rows.
-void bn_grid(BnDims* d) {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;
-  const int nt = d->F >= 4096 ? 512 : d->F >= 2048 ? 256 : 128;  // threads, about
-  d->R = ceil_div(d->rows, (int64_t)sms * (1024 / nt));
-  d->grid = ceil_div(d->rows, d->R);
+// Columns of a thread: 16 where rows divide into vectors, else 4, or 16 above
+// 2048 columns.
+int bn_cols(int F, bool vec) { return vec || F > 4 * kMaxThreads ? 16 : 4; }
+
+// Blocks resident on an SM: 512 threads of them (100 to 128 registers each).
+int bn_ctas(int nt) {
+  const int n = 512 / nt;
+  return n < 1 ? 1 : n > 16 ? 16 : n;
 }
 
-size_t bn_part_floats(const BnDims& d) { return ((size_t)3 * d.grid + d.ng) * d.F; }
+// Row ranges: as many blocks as are resident at once, each with the same number
+// of consecutive rows; in the backward at least four while that still leaves
+// two blocks an SM (each block adds a part to the gradients' sums).
+void bn_grid(BnDims* d, bool vec, bool bwd) {
+  const int sms = sm_count();
+  d->nt = ceil_div(ceil_div(d->F, bn_cols(d->F, vec)), 32) * 32;
+  d->R = ceil_div(d->rows, (int64_t)sms * bn_ctas(d->nt));
+  if (bwd && d->R < 4) {
+    const int few = ceil_div(d->rows, 2 * sms);
+    d->R = few > 4 ? 4 : few > d->R ? few : d->R;
+  }
+  d->grid = ceil_div(d->rows, d->R);
+}
+// The backward's parts are counted for the scalar launch, which has the most
+// blocks, so the size does not depend on addresses.
+size_t bn_bwd_floats(BnDims d) {
+  bn_grid(&d, false, true);
+  const size_t a = ((size_t)2 * d.grid + (d.ng ? d.ng : 1)) * d.F;
+  bn_grid(&d, true, true);
+  const size_t b = ((size_t)2 * d.grid + (d.ng ? d.ng : 1)) * d.F;
+  return a > b ? a : b;
+}
 
 struct BnPtrs {
   const void *r, *o;
@@ -301,37 +500,52 @@ struct BnPtrs {
   float* part;
 };
 
-template <typename Tio, typename Tres, int V, int NV>
-int bn_launch(const BnDims& d, const BnPtrs& p, bool bwd, cudaStream_t s) {
-  const int nt = ceil_div(ceil_div(d.F, V * NV), 32) * 32;
+// Ring stages: what an SM's shared memory (200 KB of it) holds for its
+// resident blocks, kMaxStages at most (one at the widest fp32 rows).
+template <typename K>
+cudaError_t bn_ring(K kern, BnDims* d, size_t stage, size_t* bytes) {
+  *bytes = 0;
+  d->S = 2;
+  if (stage == 0) return cudaSuccess;
+  const size_t fit = (size_t)200 * 1024 / bn_ctas(d->nt) / stage;
+  d->S = fit < 1 ? 1 : fit > kMaxStages ? kMaxStages : (int)fit;
+  *bytes = d->S * stage;
+  return *bytes <= 48 * 1024
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
+}
+
+template <typename Tio, typename Tres, bool VEC, int EPT>
+int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
   const Tres* r = static_cast<const Tres*>(p.r);
   const Tio* o = static_cast<const Tio*>(p.o);
-  if (bwd)
+  size_t bytes;
+  if (bwd) {
+    auto kern = k_block_norm_bwd<Tio, Tres, VEC, EPT>;
+    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, 2, 2>::kSlot;
+    if (bn_ring(kern, &d, stage, &bytes) != cudaSuccess) return SSD_ERR_CUDA;
     SSD_LAUNCH("k_block_norm_bwd", s,
-               k_block_norm_bwd<Tio, Tres, V, NV><<<d.grid, nt, 0, s>>>(
+               kern<<<d.grid, d.nt, bytes, s>>>(
                    r, o, p.w_pre, p.w_post, p.gate, static_cast<const Tio*>(p.dh),
                    static_cast<const Tres*>(p.drout), static_cast<Tres*>(p.rout),
                    static_cast<Tio*>(p.h), p.part, d));
-  else
+  } else {
+    auto kern = k_block_norm_fwd<Tio, Tres, VEC, EPT>;
+    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, 1, 1>::kSlot;
+    if (bn_ring(kern, &d, stage, &bytes) != cudaSuccess) return SSD_ERR_CUDA;
     SSD_LAUNCH("k_block_norm_fwd", s,
-               k_block_norm_fwd<Tio, Tres, V, NV><<<d.grid, nt, 0, s>>>(
-                   r, o, p.w_pre, p.w_post, p.gate, static_cast<Tres*>(p.rout),
-                   static_cast<Tio*>(p.h), d));
+               kern<<<d.grid, d.nt, bytes, s>>>(r, o, p.w_pre, p.w_post, p.gate,
+                                                static_cast<Tres*>(p.rout),
+                                                static_cast<Tio*>(p.h), d));
+  }
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-// 8 columns a thread (one 16-byte access of bf16, two of fp32) where rows
-// divide into them, else single columns; then twice as many per thread until a
-// row fits 512 threads.
 template <typename Tio, typename Tres>
 int bn_pick(const BnDims& d, const BnPtrs& p, bool vec, bool bwd, cudaStream_t s) {
-  if (vec) {
-    if (d.F <= 8 * kMaxThreads) return bn_launch<Tio, Tres, 8, 1>(d, p, bwd, s);
-    return bn_launch<Tio, Tres, 8, 2>(d, p, bwd, s);
-  }
-  if (d.F <= kMaxThreads) return bn_launch<Tio, Tres, 1, 1>(d, p, bwd, s);
-  if (d.F <= 4 * kMaxThreads) return bn_launch<Tio, Tres, 1, 4>(d, p, bwd, s);
-  return bn_launch<Tio, Tres, 1, 16>(d, p, bwd, s);
+  if (vec) return bn_launch<Tio, Tres, true, 16>(d, p, bwd, s);
+  if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, false, 4>(d, p, bwd, s);
+  return bn_launch<Tio, Tres, false, 16>(d, p, bwd, s);
 }
 
 int bn_run(const BnDims& d, const ssd_block_norm_shape* sh, const BnPtrs& p, bool vec, bool bwd,
@@ -356,8 +570,7 @@ size_t ssd_block_norm_workspace_size(const ssd_block_norm_shape* shape) {
   BnDims d;
   if (bn_dims(shape, &d) != SSD_OK) return 0;
   if (d.rows == 0) return 256;
-  bn_grid(&d);
-  return bn_part_floats(d) * sizeof(float);
+  return bn_bwd_floats(d) * sizeof(float);
 }
 
 int ssd_block_norm_fwd(const ssd_block_norm_shape* shape, const void* residual, const void* o,
@@ -373,10 +586,10 @@ int ssd_block_norm_fwd(const ssd_block_norm_shape* shape, const void* residual, 
   if (off(residual, re) || off(residual_out, re) || off(o, ie) || off(h, ie) || off(w_pre, 4) ||
       off(w_post, 4) || off(gate, 4))
     return SSD_ERR_INVALID_ARG;
-  bn_grid(&d);
-  const bool vec = vec_ok(o, d.F, ie, 8) && vec_ok(h, d.F, ie, 8) && vec_ok(residual, d.F, re, 8) &&
-                   vec_ok(residual_out, d.F, re, 8) && vec_ok(w_pre, d.F, 4, 8) &&
-                   vec_ok(w_post, d.F, 4, 8) && vec_ok(gate, d.F, 4, 8) && d.F % 8 == 0;
+  const bool vec = vec_ok(o, d.F, ie, 4) && vec_ok(h, d.F, ie, 4) && vec_ok(residual, d.F, re, 4) &&
+                   vec_ok(residual_out, d.F, re, 4) && vec_ok(w_pre, d.F, 4, 4) &&
+                   vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4) && d.F % 4 == 0;
+  bn_grid(&d, vec, false);
   const BnPtrs p{residual, o, w_pre, w_post, gate, nullptr, nullptr, residual_out, h, nullptr};
   return bn_run(d, shape, p, vec, false, static_cast<cudaStream_t>(stream));
 }
@@ -406,22 +619,23 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
     if (dgate) ok = ok && cudaMemsetAsync(dgate, 0, n * d.ng, s) == cudaSuccess;
     return ok ? SSD_OK : SSD_ERR_CUDA;
   }
-  bn_grid(&d);
-  if (!workspace || off(workspace, 16) || workspace_bytes < bn_part_floats(d) * sizeof(float))
+  if (!workspace || off(workspace, 16) || workspace_bytes < bn_bwd_floats(d) * sizeof(float))
     return SSD_ERR_WORKSPACE;
   if (d.ng + 2 > 65535) return SSD_ERR_UNSUPPORTED;
-  const bool vec = d.F % 8 == 0 && vec_ok(o, d.F, ie, 8) && vec_ok(dh, d.F, ie, 8) &&
-                   vec_ok(d_o, d.F, ie, 8) && vec_ok(residual, d.F, re, 8) &&
-                   vec_ok(dresidual_out, d.F, re, 8) && vec_ok(dresidual, d.F, re, 8) &&
-                   vec_ok(w_pre, d.F, 4, 8) && vec_ok(w_post, d.F, 4, 8) && vec_ok(gate, d.F, 4, 8);
+  const bool vec = d.F % 4 == 0 && vec_ok(o, d.F, ie, 4) && vec_ok(dh, d.F, ie, 4) &&
+                   vec_ok(d_o, d.F, ie, 4) && vec_ok(residual, d.F, re, 4) &&
+                   vec_ok(dresidual_out, d.F, re, 4) && vec_ok(dresidual, d.F, re, 4) &&
+                   vec_ok(w_pre, d.F, 4, 4) && vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4);
+  bn_grid(&d, vec, true);
   const BnPtrs p{residual, o, w_pre, w_post, gate, dh, dresidual_out, dresidual, d_o,
                  static_cast<float*>(workspace)};
   const int e = bn_run(d, shape, p, vec, true, s);
   if (e != SSD_OK) return e;
   const dim3 grid(ceil_div(d.F, 32), 2 + d.ng);
-  SSD_LAUNCH("k_block_norm_dw", s,
-             k_block_norm_dw<<<grid, 256, 0, s>>>(p.part, dw_pre, dw_post, dgate, d));
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  cudaError_t le;
+  SSD_LAUNCH("k_block_norm_dw", s, le = launch_pdl(k_block_norm_dw, grid, 512, 0, s, p.part, w_post,
+                                                   gate, dw_pre, dw_post, dgate, d));
+  return le == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -24,6 +24,15 @@ struct Dims {
 // ssd_api.cu).  Kernels whose bounded waits expire store SSD_ERR_TIMEOUT there.
 int* device_status_ptr();
 
+// SM count of the current device (152, the GB300's, where the query fails).
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;
+  return sms;
+}
+
 // The opt-in NaN / Inf scan of outputs (ssd_set_check_finite): whether it is
 // on, and one scan launch over n values (f32, or bf16 when is_bf16).
 bool check_finite_enabled();

@@ -101,16 +101,6 @@ __device__ __forceinline__ Pair lane_pair(const SelDims& d, const Place& p, int 
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
-                 : "memory");
-}
-
 // B (and C) of one group in shared memory as fp32, NP states a position
 // (zeros past N and past position n), TT positions at a time: fetched into
 // registers while the tile before is used, then stored.
@@ -194,12 +184,12 @@ struct Ring {
         }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_commit();
   }
   // Makes stage s readable by the warp and starts the copy of stage s + kStages - 1
   // into the slot that every lane has left.
   __device__ __forceinline__ void next(int s) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    cp_wait<kStages - 2>();
     __syncwarp();
     fill(s + kStages - 1);
   }
@@ -253,7 +243,14 @@ __device__ __forceinline__ void st_states(const float2 (&v)[K2], float* row, int
 }
 
 constexpr int kFwdWarps = 4;
-constexpr int kFwdBlocksPerSm = 3;
+#ifndef SD
+#define SD 1
+#define SB 3
+#define TD 1
+#define TB 2
+#endif
+constexpr int kScanDiv = SD, kStateDiv = TD;
+constexpr int kFwdBlocksPerSm = SB, kStateBlocksPerSm = TB;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 
 template <typename Tin, int SPT, int SL, int NI, bool C>
@@ -345,6 +342,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
         float2 xv[kU], dl[kU], gate[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
+          gate[u] = f2(1.f);
           xv[u] = ring.get(stage, tu + u, 0, ln.cl);
           dl[u] = softplus2(add2(ring.get(stage, tu + u, 1, ln.cl), bias));
           if constexpr (OUT)
@@ -353,45 +351,50 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
               gate[u] = mul2(zv, sigmoid2(zv));
             }
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        auto step = [&](int u) {
           const int t = ts + tu + u;
-          if (t < te) {
-            const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
-            const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
-            const float2 dtx = mul2(dl[u], xv[u]);
-            if (!OUT) sd = add2(sd, dl[u]);
-            float2 y[2] = {f2(0.f), f2(0.f)};
+          const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
+          const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
+          const float2 dtx = mul2(dl[u], xv[u]);
+          if (!OUT) sd = add2(sd, dl[u]);
+          float2 y[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
-            for (int q = 0; q < SPT / 4; ++q) {
-              const float4 b4 = Bv[q];
-              float4 c4;
-              if (OUT) c4 = Cv[q];
+          for (int q = 0; q < SPT / 4; ++q) {
+            const float4 b4 = Bv[q];
+            float4 c4;
+            if (OUT) c4 = Cv[q];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int k = 2 * q + i;
-                const float2 bk = i ? hi2(b4) : lo2(b4);
+            for (int i = 0; i < 2; ++i) {
+              const int k = 2 * q + i;
+              const float2 bk = i ? hi2(b4) : lo2(b4);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
-                  h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
-                  if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
-                }
+              for (int j = 0; j < 2; ++j) {
+                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
               }
-            }
-            if (OUT) {
-              float2 yv = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
-#pragma unroll
-              for (int w = CL; w < 32; w <<= 1) {
-                yv.x += __shfl_xor_sync(0xffffffffu, yv.x, w);
-                yv.y += __shfl_xor_sync(0xffffffffu, yv.y, w);
-              }
-              yv = fma2(skip, xv[u], yv);
-              if (gated) yv = mul2(yv, gate[u]);
-              if (ln.on && ln.sl == 0) st_two(o, yv, ln.two, d.wide);
-              o += d.D;
             }
           }
+          if (OUT) {
+            float2 yv = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+#pragma unroll
+            for (int w = CL; w < 32; w <<= 1) {
+              yv.x += __shfl_xor_sync(0xffffffffu, yv.x, w);
+              yv.y += __shfl_xor_sync(0xffffffffu, yv.y, w);
+            }
+            yv = fma2(skip, xv[u], yv);
+            if (gated) yv = mul2(yv, gate[u]);
+            if (ln.on && ln.sl == 0) st_two(o, yv, ln.two, d.wide);
+            o += d.D;
+          }
+        };
+        if (ts + tu + kU <= te) {  // no branch between the steps: they overlap
+#pragma unroll
+          for (int u = 0; u < kU; ++u) step(u);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (ts + tu + u < te) step(u);
         }
       }
     }
@@ -427,7 +430,7 @@ constexpr int kBwdL = 32;  // positions of a backward chunk
 // (gin).  Running products of the decays give the adjoint in the forward
 // direction, from the same exponentials.
 template <typename Tin, int SPT, int SL>
-__global__ void __launch_bounds__(kFwdThreads)
+__global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
     k_sel_state(SelIn in, const Tin* __restrict__ dout, float* __restrict__ hin,
                 float* __restrict__ gin, float* __restrict__ sumd, float* __restrict__ sumg,
                 SelDims d) {
@@ -517,31 +520,36 @@ __global__ void __launch_bounds__(kFwdThreads)
             dy[u] = mul2(dy[u], mul2(zv, sigmoid2(zv)));
           }
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        auto step = [&](int u) {
           const int t = ts + tu + u;
-          if (t < te) {
-            const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
-            const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
-            const float2 dtx = mul2(dl[u], xv[u]);
-            sd = add2(sd, dl[u]);
+          const float4* Bv = reinterpret_cast<const float4*>(sm.B[buf] + t * NP + ln.sl * SPT);
+          const float4* Cv = reinterpret_cast<const float4*>(sm.Cm[buf] + t * NP + ln.sl * SPT);
+          const float2 dtx = mul2(dl[u], xv[u]);
+          sd = add2(sd, dl[u]);
 #pragma unroll
-            for (int q = 0; q < SPT / 4; ++q) {
-              const float4 b4 = Bv[q], c4 = Cv[q];
+          for (int q = 0; q < SPT / 4; ++q) {
+            const float4 b4 = Bv[q], c4 = Cv[q];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int k = 2 * q + i;
-                const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
+            for (int i = 0; i < 2; ++i) {
+              const int k = 2 * q + i;
+              const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
-                  h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
-                  pr[j][k] = mul2(pr[j][k], a);
-                  gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
-                }
+              for (int j = 0; j < 2; ++j) {
+                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
+                pr[j][k] = mul2(pr[j][k], a);
+                gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
               }
             }
           }
+        };
+        if (ts + tu + kU <= te) {  // no branch between the steps: they overlap
+#pragma unroll
+          for (int u = 0; u < kU; ++u) step(u);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (ts + tu + u < te) step(u);
         }
       }
     }
@@ -1062,7 +1070,7 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
 // SM), each at least 64 positions; one (no state pass) where the channels fill
 // half of it by themselves.
 void fwd_chunks(SelDims* d) {
-  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
+  const int sl = (d->N > 32 ? 4 : d->N > 16 ? 2 : 1) * kScanDiv;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   const int64_t blocks = (int64_t)d->B * d->G * d->ctiles;
   int64_t nc = kFwdBlocksPerSm * 152 / blocks;
@@ -1083,7 +1091,7 @@ int bwd_main_tiles(const SelDims& d) {
   return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);
 }
 void bwd_chunks(SelDims* d) {
-  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
+  const int sl = (d->N > 32 ? 4 : d->N > 16 ? 2 : 1) * kStateDiv;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   d->nh = ceil_div(d->T, kBwdL);
   const int64_t bg = (int64_t)d->B * d->G, wave = 2 * 152;
@@ -1092,7 +1100,8 @@ void bwd_chunks(SelDims* d) {
   for (int per = 1; per <= d->nh && per <= 64; ++per) {
     const int64_t nc = ceil_div(d->nh, per);
     const int64_t main = (bg * bwd_main_tiles(*d) * nc + wave - 1) / wave;
-    const int64_t first = (bg * d->ctiles * nc + wave - 1) / wave;
+    const int64_t wave1 = kStateBlocksPerSm * 152;
+    const int64_t first = (bg * d->ctiles * nc + wave1 - 1) / wave1;
     // (half a chunk's time for what a range costs by itself)
     const int64_t cost = (24 * main + 7 * first) * (2 * per + 1);
     if (best < 0 || cost < best) best = cost, best_per = per;
@@ -1151,10 +1160,11 @@ template <typename Tin, typename Tout, int SPT, int SL>
 int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out, float* fin,
                 float* hin, float* sumd, cudaStream_t s) {
   Tout* const o = static_cast<Tout*>(out);
-  auto kstate = k_sel_scan<Tin, Tout, SPT, SL, false>;
-  auto kout = k_sel_scan<Tin, Tout, SPT, SL, true>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 2, false>);
-  constexpr size_t mo = sizeof(PassSmem<Tin, SPT, SL, 3, true>);
+  constexpr int kS = SPT / kScanDiv, kL = SL * kScanDiv;
+  auto kstate = k_sel_scan<Tin, Tout, kS, kL, false>;
+  auto kout = k_sel_scan<Tin, Tout, kS, kL, true>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, kS, kL, 2, false>);
+  constexpr size_t mo = sizeof(PassSmem<Tin, kS, kL, 3, true>);
   if (allow_smem(kstate, ms) != cudaSuccess || allow_smem(kout, mo) != cudaSuccess)
     return SSD_ERR_CUDA;
   if (d.nc > 1) {
@@ -1186,8 +1196,9 @@ template <typename Tin, typename Tout, int SPT, int SL>
 int sel_backward(const SelDims& d, const SelIn& in, const float* init, const void* dout,
                  const float* dfinal, const SelGrads& g, const SelBwdWs& w, cudaStream_t s) {
   const Tin* go = static_cast<const Tin*>(dout);
-  auto kstate = k_sel_state<Tin, SPT, SL>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 4, true>);
+  constexpr int kS = SPT / kStateDiv, kL = SL * kStateDiv;
+  auto kstate = k_sel_state<Tin, kS, kL>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, kS, kL, 4, true>);
   if (allow_smem(kstate, ms) != cudaSuccess) return SSD_ERR_CUDA;
   SSD_LAUNCH("k_sel_state", s, kstate<<<sel_grid(d, d.nc), kFwdThreads, ms, s>>>(
                                    in, go, w.hin, w.gin, w.sumd, w.sumg, d));

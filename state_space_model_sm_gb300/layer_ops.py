@@ -17,7 +17,16 @@ import torch
 from . import _native
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}  # ssd_dtype
-_F32 = torch.float32
+_F32, _I32 = torch.float32, torch.int32
+_stream = torch._C._cuda_getCurrentRawStream  # of a device index; no Stream object
+_lib = None
+
+
+def _native_lib():
+    global _lib
+    if _lib is None:
+        _lib = _native.load()
+    return _lib
 
 
 def _fail(fn, status):
@@ -33,25 +42,31 @@ def _code(dtype):
 
 
 def _lead(t, name, ndim):
-    """The call's first tensor: its rank, device and type."""
+    """Index of the device of the call's first tensor, whose rank is checked."""
     if t.dim() != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    return t.device
+    return t.get_device()
+
+
+def _wrong(t, name, shape, dtype, device):
+    """Raises what is wrong with t (apart from its strides)."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected device cuda:{device}, got {t.device}")
 
 
 def _check(t, name, shape, dtype, device):
     """Shape, type, device and density of t; its address (None for None)."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if not t.is_contiguous():
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device
+            or not t.is_contiguous()):
+        _wrong(t, name, shape, dtype, device)
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
@@ -63,12 +78,8 @@ def _rows(t, name, shape, lead, dtype, device):
     batch rows); a row stride of 0 stands for a dense tensor."""
     if t is None:
         return None, 0, 0
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _wrong(t, name, shape, dtype, device)
     if t.is_contiguous():
         return t.data_ptr(), 0, 0
     dense, stride = 1, t.stride()
@@ -82,25 +93,22 @@ def _rows(t, name, shape, lead, dtype, device):
     return t.data_ptr(), row, stride[0]
 
 
-def _output(t, name, shape, dtype, device):
+def _output(t, name, shape, dtype, like):
+    """t after its check, or a new tensor, on the device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, shape, dtype, device)
+        return like.new_empty(shape, dtype=dtype)
+    _check(t, name, shape, dtype, like.get_device())
     return t
 
 
-def _scratch(nbytes, device, workspace):
+def _scratch(nbytes, like, workspace):
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return like.new_empty(nbytes, dtype=torch.uint8)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError("workspace too small")
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous on {device}")
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous on {like.device}")
     return workspace
-
-
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _at(t):
@@ -136,13 +144,13 @@ def causal_conv_fwd(x, w, bias=None, init_state=None, lengths=None, silu: bool =
     lengths (batch,) int32: positions from lengths[b] on are padding.
     final_state is the state after lengths[b] positions, which
     ``causal_conv_step`` goes on from.  y is in ``out_dtype`` (x's type)."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (B, T, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 3, silu, out_dtype)
     ip = _check(init_state, "init_state", (B, K - 1, C), x.dtype, dev)
-    lp = _check(lengths, "lengths", (B,), torch.int32, dev)
-    y = _output(y, "y", (B, T, C), odt, dev)
+    lp = _check(lengths, "lengths", (B,), _I32, dev)
+    y = _output(y, "y", (B, T, C), odt, x)
     if return_final_state:
-        final_state = _output(final_state, "final_state", (B, K - 1, C), x.dtype, dev)
+        final_state = _output(final_state, "final_state", (B, K - 1, C), x.dtype, x)
     else:
         final_state = None
     st = lib.ssd_causal_conv_fwd(shape, xp, wp, bp, ip, lp, y.data_ptr(), _at(final_state),
@@ -157,20 +165,20 @@ def causal_conv_bwd(x, w, bias, dy, init_state=None, lengths=None, silu: bool = 
     """Gradients of <dy, y> + <dfinal_state, final_state> of ``causal_conv_fwd``
     (``ssd_causal_conv_bwd``): a dict with dx (``out_dtype``, x's type by default),
     dw and dbias (float32) and, with init_state, dinit_state (``out_dtype``)."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (B, T, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 3, silu, out_dtype)
     ip = _check(init_state, "init_state", (B, K - 1, C), x.dtype, dev)
-    lp = _check(lengths, "lengths", (B,), torch.int32, dev)
+    lp = _check(lengths, "lengths", (B,), _I32, dev)
     gp = _check(dy, "dy", (B, T, C), x.dtype, dev)
     fp = _check(dfinal_state, "dfinal_state", (B, K - 1, C), x.dtype, dev)
     got = {} if out is None else out
-    out = dict(dx=_output(got.get("dx"), "dx", (B, T, C), odt, dev),
-               dw=_output(got.get("dw"), "dw", (C, K), _F32, dev),
-               dbias=_output(got.get("dbias"), "dbias", (C,), _F32, dev))
+    out = dict(dx=_output(got.get("dx"), "dx", (B, T, C), odt, x),
+               dw=_output(got.get("dw"), "dw", (C, K), _F32, x),
+               dbias=_output(got.get("dbias"), "dbias", (C,), _F32, x))
     if init_state is not None:
-        out["dinit_state"] = _output(got.get("dinit_state"), "dinit_state", (B, K - 1, C), odt, dev)
+        out["dinit_state"] = _output(got.get("dinit_state"), "dinit_state", (B, K - 1, C), odt, x)
     nbytes = lib.ssd_causal_conv_workspace_size(shape)
-    ws = _scratch(max(nbytes, 1), dev, workspace)
+    ws = _scratch(max(nbytes, 1), x, workspace)
     st = lib.ssd_causal_conv_bwd(shape, xp, wp, bp, ip, lp, gp, fp, out["dx"].data_ptr(),
                                  out["dw"].data_ptr(), out["dbias"].data_ptr(),
                                  _at(out.get("dinit_state")), ws.data_ptr(),
@@ -185,11 +193,11 @@ def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_
     channels); state (nslots, width - 1, channels) in x's type, updated in place.
     slots (batch,) int32 names each row's state; a negative one marks an empty
     row, whose output is 0."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (B, _, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 2, silu, out_dtype)
     sp = _check(state, "state", (state.shape[0], K - 1, C), x.dtype, dev)
-    lp = _check(slots, "slots", (B,), torch.int32, dev)
-    y = _output(y, "y", (B, C), odt, dev)
+    lp = _check(slots, "slots", (B,), _I32, dev)
+    y = _output(y, "y", (B, C), odt, x)
     st = lib.ssd_causal_conv_step(shape, xp, sp, wp, bp, lp, state.shape[0], y.data_ptr(),
                                   _stream(dev))
     if st:
@@ -232,17 +240,17 @@ def selective_scan_fwd(x, dt, dt_bias, A, B, C, D=None, z=None, init_states=None
     (channels,), init_states (batch, channels, dstate) float32; lengths (batch,)
     int32: positions from lengths[b] on are padding.  dstate <= 64.  final_states
     is what ``selective_step`` goes on from."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (Bt, T, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 3, out_dtype)
     ip = _check(init_states, "init_states", (Bt, ch, N), _F32, dev)
-    lp = _check(lengths, "lengths", (Bt,), torch.int32, dev)
-    out = _output(out, "out", (Bt, T, ch), odt, dev)
+    lp = _check(lengths, "lengths", (Bt,), _I32, dev)
+    out = _output(out, "out", (Bt, T, ch), odt, x)
     if return_final_states:
-        final_states = _output(final_states, "final_states", (Bt, ch, N), _F32, dev)
+        final_states = _output(final_states, "final_states", (Bt, ch, N), _F32, x)
     else:
         final_states = None
     nbytes = lib.ssd_selective_scan_fwd_workspace_size(shape)
-    ws = _scratch(max(nbytes, 1), dev, workspace)
+    ws = _scratch(max(nbytes, 1), x, workspace)
     st = lib.ssd_selective_scan_fwd(shape, *p, ip, lp, out.data_ptr(), _at(final_states),
                                     ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
     if st:
@@ -256,10 +264,10 @@ def selective_scan_bwd(x, dt, dt_bias, A, B, C, D, z, dout, init_states=None, le
     ``selective_scan_fwd`` (``ssd_selective_scan_bwd``): a dict with dx, ddt and,
     with z, dz in ``out_dtype`` (x's type), and dA, dB, dC, dD, ddt_bias and, with
     init_states, dinit_states in float32."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (Bt, T, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 3, out_dtype)
     ip = _check(init_states, "init_states", (Bt, ch, N), _F32, dev)
-    lp = _check(lengths, "lengths", (Bt,), torch.int32, dev)
+    lp = _check(lengths, "lengths", (Bt,), _I32, dev)
     gp = _check(dout, "dout", (Bt, T, ch), x.dtype, dev)
     fp = _check(dfinal_states, "dfinal_states", (Bt, ch, N), _F32, dev)
     want = [("dx", (Bt, T, ch), odt), ("ddt", (Bt, T, ch), odt), ("dA", (ch, N), _F32),
@@ -270,9 +278,9 @@ def selective_scan_bwd(x, dt, dt_bias, A, B, C, D, z, dout, init_states=None, le
     if init_states is not None:
         want.append(("dinit_states", (Bt, ch, N), _F32))
     got = {} if out is None else out
-    out = {k: _output(got.get(k), k, s, t, dev) for k, s, t in want}
+    out = {k: _output(got.get(k), k, s, t, x) for k, s, t in want}
     nbytes = lib.ssd_selective_scan_bwd_workspace_size(shape)
-    ws = _scratch(max(nbytes, 1), dev, workspace)
+    ws = _scratch(max(nbytes, 1), x, workspace)
     st = lib.ssd_selective_scan_bwd(
         shape, *p, ip, lp, gp, fp, *(_at(out.get(k)) for k in (
             "dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinit_states")),
@@ -286,11 +294,11 @@ def selective_step(x, dt, dt_bias, A, B, C, state, D=None, z=None, slots=None, o
     """One token of ``selective_scan_fwd`` (``ssd_selective_step``): x, dt, z, y
     (batch, channels); B, C (batch, ngroups, dstate); state (nslots, channels,
     dstate) float32, updated in place; slots as in ``causal_conv_step``."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, (Bt, _, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 2, out_dtype)
     sp = _check(state, "state", (state.shape[0], ch, N), _F32, dev)
-    lp = _check(slots, "slots", (Bt,), torch.int32, dev)
-    y = _output(y, "y", (Bt, ch), odt, dev)
+    lp = _check(slots, "slots", (Bt,), _I32, dev)
+    y = _output(y, "y", (Bt, ch), odt, x)
     st = lib.ssd_selective_step(shape, *p, sp, lp, state.shape[0], y.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_selective_step", st)
@@ -302,7 +310,7 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
     dt (batch, nheads), B, C (batch, ngroups, dstate); A, dt_bias, D (nheads,) and
     state (nslots, nheads, headdim, dstate) float32, the state updated in place;
     slots as in ``causal_conv_step``.  y is in ``out_dtype`` (x's type)."""
-    lib = _native.load()
+    lib = _native_lib()
     dev = _lead(x, "x", 3)
     if B.dim() != 3:
         raise ValueError("B and C must be (batch, ngroups, dstate)")
@@ -319,8 +327,8 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
     cp = _check(C, "C", (Bt, G, N), xd, dev)
     kp = _check(D, "D", (H,), _F32, dev)
     sp = _check(state, "state", (state.shape[0], H, P, N), _F32, dev)
-    lp = _check(slots, "slots", (Bt,), torch.int32, dev)
-    y = _output(y, "y", (Bt, H, P), odt, dev)
+    lp = _check(slots, "slots", (Bt,), _I32, dev)
+    y = _output(y, "y", (Bt, H, P), odt, x)
     st = lib.ssd_step(shape, xp, dp, tp, ap, bp, cp, kp, sp, lp, state.shape[0], y.data_ptr(),
                       _stream(dev))
     if st:
@@ -333,7 +341,7 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
 def _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps):
     if residual.dim() < 1 or not residual.is_cuda:
         raise ValueError("residual must be a CUDA tensor (..., features)")
-    dev, F = residual.device, residual.shape[-1]
+    dev, F = residual.get_device(), residual.shape[-1]
     rows = residual.numel() // F if F else 0
     ptrs = (_check(residual, "residual", residual.shape, residual.dtype, dev),
             _check(o, "o", residual.shape, o.dtype, dev),
@@ -359,10 +367,10 @@ def block_norm_fwd(residual, o, w_pre, w_post=None, gate=None, scale: float = 1.
     gate (ngates, features) float32: one row for all, one per sequence or one per
     row, each covering rows / ngates consecutive rows.  residual_out may be
     ``residual`` and h may be ``o`` (in place)."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
-    residual_out = _output(residual_out, "residual_out", residual.shape, residual.dtype, dev)
-    h = _output(h, "h", o.shape, o.dtype, dev)
+    residual_out = _output(residual_out, "residual_out", residual.shape, residual.dtype, residual)
+    h = _output(h, "h", o.shape, o.dtype, residual)
     st = lib.ssd_block_norm_fwd(shape, *p, residual_out.data_ptr(), h.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_block_norm_fwd", st)
@@ -374,7 +382,7 @@ def block_norm_bwd(residual, o, w_pre, w_post, gate, dh, dresidual_out=None, sca
     """Gradients of <dh, h> + <dresidual_out, residual_out> of ``block_norm_fwd``
     from its inputs (``ssd_block_norm_bwd``): a dict with dresidual (residual's type),
     do (o's type), dw_pre and, with w_post and gate, dw_post and dgate (float32)."""
-    lib = _native.load()
+    lib = _native_lib()
     dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
     hp = _check(dh, "dh", o.shape, o.dtype, dev)
     rp = _check(dresidual_out, "dresidual_out", residual.shape, residual.dtype, dev)
@@ -385,9 +393,9 @@ def block_norm_bwd(residual, o, w_pre, w_post, gate, dh, dresidual_out=None, sca
     if gate is not None:
         want.append(("dgate", gate.shape, _F32))
     got = {} if out is None else out
-    out = {k: _output(got.get(k), k, s, t, dev) for k, s, t in want}
+    out = {k: _output(got.get(k), k, s, t, residual) for k, s, t in want}
     nbytes = lib.ssd_block_norm_workspace_size(shape)
-    ws = _scratch(max(nbytes, 1), dev, workspace)
+    ws = _scratch(max(nbytes, 1), residual, workspace)
     st = lib.ssd_block_norm_bwd(shape, *p, hp, rp, *(_at(out.get(k)) for k in (
         "dresidual", "do", "dw_pre", "dw_post", "dgate")), ws.data_ptr(),
         ws.numel() * ws.element_size(), _stream(dev))
