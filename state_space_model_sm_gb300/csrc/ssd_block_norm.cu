@@ -81,7 +81,8 @@ __device__ __forceinline__ float block_sum(float a, float2 (*red)[16], int& ph) 
 // access of a warp is one unbroken run (8 columns would be 32-byte pieces of
 // fp32, whose 16-byte halves touch each sector twice: 20 % slower); else single
 // columns, blockDim.x apart (widths or addresses that these do not fit).
-template <bool VEC, int EPT>
+// FULL: the row is exactly the block's columns (no bounds to check).
+template <bool VEC, int EPT, bool FULL>
 struct Cols {
   static constexpr int W = VEC ? 4 : 1, P2 = EPT / 2, NV = EPT / W;
   __device__ __forceinline__ static int col(int v) {
@@ -94,7 +95,7 @@ struct Cols {
     for (int v = 0; v < NV; ++v) {
       const int c = col(v);
       float t[W];
-      if (c < F && p) {
+      if ((FULL || c < F) && p) {
         unpack<T, W>(ld_raw<T, W>(p + c), t);
       } else {
 #pragma unroll
@@ -110,7 +111,7 @@ struct Cols {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = col(v);
-      if (c >= F) break;
+      if (!FULL && c >= F) break;
       float t[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) t[i] = f[v * W + i];
@@ -123,9 +124,9 @@ struct Cols {
 // pieces that it will use itself, S - 1 rows ahead, so the bytes in flight are
 // set by the ring and no barrier is needed.  Else plain loads of the row.
 // Addresses advance by a row at a time.
-template <typename Tio, typename Tres, bool VEC, int EPT, int NIO, int NRES>
+template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL, int NIO, int NRES>
 struct Rows {
-  using C = Cols<VEC, EPT>;
+  using C = Cols<VEC, EPT, FULL>;
   static constexpr int NV = VEC ? C::NV : 0;
   // bytes of a thread's piece of one tensor, of its row of one, of its slot
   static constexpr int kIo = 4 * sizeof(Tio), kRes = 4 * sizeof(Tres);
@@ -133,7 +134,8 @@ struct Rows {
   const Tio* io[NIO];     // VEC: this thread's first column of the next row to copy;
   const Tres* res[NRES];  // else the row in use
   uint32_t put, use, end, slot;  // ring offsets: next copy's slot, the row in use; end; a slot
-  int F, S, left;                // left: rows still to copy
+  uint32_t iostep, resstep;      // bytes of the block's pieces v of one tensor
+  int F, S, left, pieces;        // left: rows still to copy; pieces: of this thread in a row
 
   __device__ __forceinline__ static unsigned char* smem() {
     extern __shared__ __align__(16) unsigned char ring[];
@@ -148,6 +150,10 @@ struct Rows {
     for (int i = 0; i < NRES; ++i)
       if (res[i]) res[i] += at;
     if constexpr (VEC) {
+      iostep = kIo * blockDim.x, resstep = kRes * blockDim.x;
+      pieces = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) pieces += C::col(v) < F;
       slot = kSlot * blockDim.x, end = S * slot, put = 0, use = end - slot;
       for (int i = 0; i < S - 1; ++i) fill();
     }
@@ -159,26 +165,29 @@ struct Rows {
     for (int i = 0; i < NRES; ++i)
       if (res[i]) res[i] += F;
   }
-  // offset in a slot of this thread's piece v of tensor i (io first, then res)
-  __device__ __forceinline__ static uint32_t io_at(int i, int v) {
-    return (i * NV + v) * kIo * blockDim.x + threadIdx.x * kIo;
+  // offset in a slot of this thread's first piece of tensor i (io first, then res)
+  __device__ __forceinline__ uint32_t io_at(int i) const {
+    return i * NV * iostep + threadIdx.x * kIo;
   }
-  __device__ __forceinline__ static uint32_t res_at(int i, int v) {
-    return (NIO * NV * kIo + (i * NV + v) * kRes) * blockDim.x + threadIdx.x * kRes;
+  __device__ __forceinline__ uint32_t res_at(int i) const {
+    return NIO * NV * iostep + i * NV * resstep + threadIdx.x * kRes;
   }
   __device__ __forceinline__ void fill() {  // the next row, into the next slot
     if (left > 0) {
       unsigned char* const q = smem() + put;
+      const int cols = 4 * blockDim.x;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (C::col(v) >= F) break;
-        const int c = v * (int)blockDim.x * 4;
+      for (int i = 0; i < NIO; ++i)
 #pragma unroll
-        for (int i = 0; i < NIO; ++i) cp_async<kIo>(q + io_at(i, v), io[i] + c);
+        for (int v = 0; v < NV; ++v)
+          if (FULL || v < pieces) cp_async<kIo>(q + io_at(i) + v * iostep, io[i] + v * cols);
 #pragma unroll
-        for (int i = 0; i < NRES; ++i)
-          if (res[i]) cp_async<kRes>(q + res_at(i, v), res[i] + c);
-      }
+      for (int i = 0; i < NRES; ++i)
+        if (res[i]) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+            if (FULL || v < pieces) cp_async<kRes>(q + res_at(i) + v * resstep, res[i] + v * cols);
+        }
       advance();
       --left;
       put = put + slot == end ? 0 : put + slot;
@@ -208,25 +217,30 @@ struct Rows {
   }
   __device__ __forceinline__ void get_io(int i, float2 (&x)[C::P2]) const {
     if constexpr (VEC)
-      get<Tio>(io_at(i, 0), kIo, true, x);
+      get<Tio>(io_at(i), iostep, pieces, x);
     else
       C::load(io[i], F, x, 0.f);
   }
   __device__ __forceinline__ void get_res(int i, float2 (&x)[C::P2]) const {
-    if constexpr (VEC)
-      get<Tres>(res_at(i, 0), kRes, res[i] != nullptr, x);
-    else
+    if constexpr (VEC) {
+      if (res[i]) {
+        get<Tres>(res_at(i), resstep, pieces, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < C::P2; ++k) x[k] = f2(0.f);
+      }
+    } else {
       C::load(res[i], F, x, 0.f);
+    }
   }
   template <typename T>
-  __device__ __forceinline__ void get(uint32_t at, int piece, bool there, float2 (&x)[C::P2]) const {
+  __device__ __forceinline__ void get(uint32_t at, uint32_t step, int n, float2 (&x)[C::P2]) const {
     float* f = reinterpret_cast<float*>(x);
     const unsigned char* q = smem() + use + at;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       Raw<T, 4> r = zero_raw<T, 4>();
-      if (C::col(v) < F && there)
-        r = *reinterpret_cast<const Raw<T, 4>*>(q + v * piece * blockDim.x);
+      if (FULL || v < n) r = *reinterpret_cast<const Raw<T, 4>*>(q + v * step);
       float t[4];
       unpack<T, 4>(r, t);
 #pragma unroll
@@ -246,19 +260,19 @@ __device__ __forceinline__ void load_gw(float2 (&gw)[C::P2], const float* w_post
   for (int i = 0; i < C::P2; ++i) gw[i] = mul2(gw[i], mul2(t[i], f2(d.scale)));
 }
 
-template <typename Tio, typename Tres, bool VEC, int EPT>
+template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_fwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
                      const float* __restrict__ gate, Tres* __restrict__ rout, Tio* __restrict__ h,
                      BnDims d) {
-  using C = Cols<VEC, EPT>;
+  using C = Cols<VEC, EPT, FULL>;
   constexpr int P2 = C::P2;
   __shared__ float2 red[2][16];
   int ph = 0;
   const float inv = 1.f / (float)d.F;
   const int r0 = blockIdx.x * d.R, r1 = min(d.rows, r0 + d.R);
-  Rows<Tio, Tres, VEC, EPT, 1, 1> in;
+  Rows<Tio, Tres, VEC, EPT, FULL, 1, 1> in;
   in.io[0] = o, in.res[0] = r;
   in.start(d.F, d.S, r0, r1);
   float2 gw[P2], wp[P2];
@@ -302,21 +316,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 // P_g is slot blockIdx.x + g, which no other (block, gate row) pair has, because
 // from one pair that shares rows to the next the block, the gate row or both
 // grow.
-template <typename Tio, typename Tres, bool VEC, int EPT>
+template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_bwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
                      const float* __restrict__ gate, const Tio* __restrict__ dh,
                      const Tres* __restrict__ drout, Tres* __restrict__ dr, Tio* __restrict__ dout,
                      float* __restrict__ part, BnDims d) {
-  using C = Cols<VEC, EPT>;
+  using C = Cols<VEC, EPT, FULL>;
   constexpr int P2 = C::P2;
   __shared__ float2 red[2][16];
   griddep_launch_dependents();
   int ph = 0;
   const float inv = 1.f / (float)d.F;
   const int r0 = blockIdx.x * d.R, r1 = min(d.rows, r0 + d.R);
-  Rows<Tio, Tres, VEC, EPT, 2, 2> in;
+  Rows<Tio, Tres, VEC, EPT, FULL, 2, 2> in;
   in.io[0] = o, in.io[1] = dh, in.res[0] = r, in.res[1] = drout;
   in.start(d.F, d.S, r0, r1);
   float2 apre[P2], ap[P2], gw[P2], wp[P2];
@@ -515,14 +529,14 @@ cudaError_t bn_ring(K kern, BnDims* d, size_t stage, size_t* bytes) {
              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
 }
 
-template <typename Tio, typename Tres, bool VEC, int EPT>
+template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
 int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
   const Tres* r = static_cast<const Tres*>(p.r);
   const Tio* o = static_cast<const Tio*>(p.o);
   size_t bytes;
   if (bwd) {
-    auto kern = k_block_norm_bwd<Tio, Tres, VEC, EPT>;
-    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, 2, 2>::kSlot;
+    auto kern = k_block_norm_bwd<Tio, Tres, VEC, EPT, FULL>;
+    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, FULL, 2, 2>::kSlot;
     if (bn_ring(kern, &d, stage, &bytes) != cudaSuccess) return SSD_ERR_CUDA;
     SSD_LAUNCH("k_block_norm_bwd", s,
                kern<<<d.grid, d.nt, bytes, s>>>(
@@ -530,8 +544,8 @@ int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
                    static_cast<const Tres*>(p.drout), static_cast<Tres*>(p.rout),
                    static_cast<Tio*>(p.h), p.part, d));
   } else {
-    auto kern = k_block_norm_fwd<Tio, Tres, VEC, EPT>;
-    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, 1, 1>::kSlot;
+    auto kern = k_block_norm_fwd<Tio, Tres, VEC, EPT, FULL>;
+    const size_t stage = (size_t)d.nt * Rows<Tio, Tres, VEC, EPT, FULL, 1, 1>::kSlot;
     if (bn_ring(kern, &d, stage, &bytes) != cudaSuccess) return SSD_ERR_CUDA;
     SSD_LAUNCH("k_block_norm_fwd", s,
                kern<<<d.grid, d.nt, bytes, s>>>(r, o, p.w_pre, p.w_post, p.gate,
@@ -543,9 +557,10 @@ int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
 
 template <typename Tio, typename Tres>
 int bn_pick(const BnDims& d, const BnPtrs& p, bool vec, bool bwd, cudaStream_t s) {
-  if (vec) return bn_launch<Tio, Tres, true, 16>(d, p, bwd, s);
-  if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, false, 4>(d, p, bwd, s);
-  return bn_launch<Tio, Tres, false, 16>(d, p, bwd, s);
+  if (vec && d.F == 16 * d.nt) return bn_launch<Tio, Tres, true, 16, true>(d, p, bwd, s);
+  if (vec) return bn_launch<Tio, Tres, true, 16, false>(d, p, bwd, s);
+  if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, false, 4, false>(d, p, bwd, s);
+  return bn_launch<Tio, Tres, false, 16, false>(d, p, bwd, s);
 }
 
 int bn_run(const BnDims& d, const ssd_block_norm_shape* sh, const BnPtrs& p, bool vec, bool bwd,
