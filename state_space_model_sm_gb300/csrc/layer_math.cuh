@@ -146,6 +146,12 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   return fma2(add2(s, s), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
+// The same for single values, for code over either.
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sigmoid2(float v) { return sigmoid(v); }
+
 // Two adjacent elements as one access where wide (their address is then
 // aligned to both), else as two; `two` says whether there is a second one.
 template <typename T>

@@ -119,17 +119,22 @@ def _at(t):
 
 def _conv_inputs(x, w, bias, ndim, silu, out_dtype):
     dev = _lead(x, "x", ndim)
-    C = x.shape[-1]
-    if w.dim() != 2:
+    xshape, xd = x.shape, x.dtype
+    batch, C = xshape[0], xshape[-1]
+    T = xshape[1] if ndim == 3 else 1
+    wshape = w.shape
+    if len(wshape) != 2:
         raise ValueError("w must be (channels, width)")
-    K = w.shape[1]
-    batch, T = x.shape[0], (x.shape[1] if ndim == 3 else 1)
-    xp, xs, xb = _rows(x, "x", x.shape, ndim - 1, x.dtype, dev)
+    K = wshape[1]
+    xp, xs, xb = _rows(x, "x", xshape, ndim - 1, xd, dev)
     wp = _check(w, "w", (C, K), _F32, dev)
-    bp = _check(bias, "bias", (C,), _F32, dev)
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    shape = _native.ConvShape(batch, T, C, K, xs, xb, 1 if silu else 0, _code(x.dtype),
-                              _code(out_dtype))
+    bp = None if bias is None else _check(bias, "bias", (C,), _F32, dev)
+    code = _code(xd)
+    if out_dtype is None:
+        out_dtype, ocode = xd, code
+    else:
+        ocode = _code(out_dtype)
+    shape = _native.ConvShape(batch, T, C, K, xs, xb, 1 if silu else 0, code, ocode)
     return dev, shape, (batch, T, C, K), out_dtype, xp, wp, bp
 
 
@@ -209,23 +214,27 @@ def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_
 
 def _sel_inputs(x, dt, dt_bias, A, B, C, D, z, ndim, out_dtype):
     dev = _lead(x, "x", ndim)
+    xshape, xd = x.shape, x.dtype
     if B.dim() != ndim + 1 or A.dim() != 2:
         raise ValueError("A must be (channels, dstate), B and C (..., ngroups, dstate)")
-    lead = x.shape[:-1]
-    ch, N, G = x.shape[-1], A.shape[1], B.shape[-2]
-    xd = x.dtype
-    gn = tuple(lead) + (G, N)
-    bp, bs, bb = _rows(B, "B", gn, ndim - 1, xd, dev)
-    cp, cs, cb = _rows(C, "C", gn, ndim - 1, xd, dev)
-    zp, zs, zb = _rows(z, "z", x.shape, ndim - 1, xd, dev)
-    ptrs = (_check(x, "x", x.shape, xd, dev), _check(dt, "dt", x.shape, xd, dev),
+    batch, ch = xshape[0], xshape[-1]
+    T = xshape[1] if ndim == 3 else 1
+    N, G = A.shape[1], B.shape[-2]
+    gn = (batch, T, G, N) if ndim == 3 else (batch, G, N)
+    lead = ndim - 1
+    bp, bs, bb = _rows(B, "B", gn, lead, xd, dev)
+    cp, cs, cb = _rows(C, "C", gn, lead, xd, dev)
+    zp, zs, zb = (None, 0, 0) if z is None else _rows(z, "z", xshape, lead, xd, dev)
+    ptrs = (_check(x, "x", xshape, xd, dev), _check(dt, "dt", xshape, xd, dev),
             _check(dt_bias, "dt_bias", (ch,), _F32, dev), _check(A, "A", (ch, N), _F32, dev),
             bp, cp, _check(D, "D", (ch,), _F32, dev), zp)
-    out_dtype = xd if out_dtype is None else out_dtype
-    T = lead[1] if ndim == 3 else 1
-    shape = _native.SelectiveShape(lead[0], T, ch, N, G, zs, bs, cs, zb, bb, cb, _code(xd),
-                                   _code(out_dtype))
-    return dev, shape, (lead[0], T, ch, N, G), out_dtype, ptrs
+    code = _code(xd)
+    if out_dtype is None:
+        out_dtype, ocode = xd, code
+    else:
+        ocode = _code(out_dtype)
+    shape = _native.SelectiveShape(batch, T, ch, N, G, zs, bs, cs, zb, bb, cb, code, ocode)
+    return dev, shape, (batch, T, ch, N, G), out_dtype, ptrs
 
 
 def selective_scan_fwd(x, dt, dt_bias, A, B, C, D=None, z=None, init_states=None, lengths=None,
