@@ -127,18 +127,18 @@ struct RowTile {
 __device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
 __device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
 
-// A warp's ring of its inputs: kStage positions of its channels for NI tensors a
-// stage, kStages stages, filled by cp.async ahead of the computation (no
+// A warp's ring of its inputs: L positions of its channels for NI tensors a
+// stage, S stages, filled by cp.async ahead of the computation (no
 // registers held, and nothing the compiler can sink to the loads' use).
 // Where rows are 16-byte aligned a copy moves 16 bytes; else pairs are copied by
 // 4 or 8 bytes, and odd bf16 rows by element through registers.
 constexpr int kStage = 8, kStages = 3;
 constexpr int kU = 4;  // positions whose steps and gates are formed together
 
-template <typename Tin, int CL, int NI>
+template <typename Tin, int CL, int NI, int L = kStage, int S = kStages>
 struct Ring {
-  static constexpr int CW = 2 * CL, kTensor = kStage * CW, kOne = NI * kTensor;
-  static constexpr int kElems = kStages * kOne;  // of one warp
+  static constexpr int CW = 2 * CL, kTensor = L * CW, kOne = NI * kTensor;
+  static constexpr int kElems = S * kOne;  // of one warp
   Tin* buf;
   const Tin* src[NI];  // position 0 of the range, the warp's first channel
   int64_t row[NI];     // elements between positions; NULL sources are skipped
@@ -147,8 +147,8 @@ struct Ring {
   // stage s of the range into its slot; positions past nt, and channels past nq
   // are left as zeros or as they are (their results are never written)
   __device__ __forceinline__ void fill(int s) {
-    Tin* const dst0 = buf + (s % kStages) * kOne;
-    const int t0 = s * kStage;
+    Tin* const dst0 = buf + (s % S) * kOne;
+    const int t0 = s * L;
     if (t0 < nt) {
       if (mode == 16) {
         constexpr int V = 16 / sizeof(Tin), R = CW / V;  // 16-byte pieces of a row
@@ -156,9 +156,9 @@ struct Ring {
         for (int i = 0; i < NI; ++i) {
           if (!src[i]) continue;
 #pragma unroll
-          for (int k = 0; k < (kStage * R + 31) / 32; ++k) {
+          for (int k = 0; k < (L * R + 31) / 32; ++k) {
             const int e = lane + 32 * k, t = e / R, c = (e % R) * V;
-            if (e < kStage * R && t0 + t < nt && c < nq)
+            if (e < L * R && t0 + t < nt && c < nq)
               cp_async<16>(dst0 + i * kTensor + t * CW + c, src[i] + (t0 + t) * row[i] + c);
           }
         }
@@ -166,7 +166,7 @@ struct Ring {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           if (!src[i]) continue;
-          for (int e = lane; e < kStage * CL; e += 32) {
+          for (int e = lane; e < L * CL; e += 32) {
             const int t = e / CL, c = (e % CL) * 2;
             if (t0 + t >= nt || c >= nq) continue;
             Tin* dst = dst0 + i * kTensor + t * CW + c;
@@ -186,15 +186,15 @@ struct Ring {
     }
     cp_commit();
   }
-  // Makes stage s readable by the warp and starts the copy of stage s + kStages - 1
+  // Makes stage s readable by the warp and starts the copy of stage s + S - 1
   // into the slot that every lane has left.
   __device__ __forceinline__ void next(int s) {
-    cp_wait<kStages - 2>();
+    cp_wait<S - 2>();
     __syncwarp();
-    fill(s + kStages - 1);
+    fill(s + S - 1);
   }
   __device__ __forceinline__ float2 get(int s, int t, int i, int cl) const {
-    const Two<Tin> v = *reinterpret_cast<const Two<Tin>*>(buf + (s % kStages) * kOne +
+    const Two<Tin> v = *reinterpret_cast<const Two<Tin>*>(buf + (s % S) * kOne +
                                                           i * kTensor + t * CW + 2 * cl);
     return unpack2(v);
   }
@@ -658,13 +658,19 @@ __device__ __forceinline__ float one_minus_exp(float v) {
 constexpr int kBwdTS = 4, kBwdWarps = 4, kBwdThreads = 32 * kBwdWarps;
 constexpr int kBwdTiles = kBwdL / kBwdTS;
 
-template <int SPT, int SL>
+// The next chunk's inputs are copied over the kept states once those are used
+// up: x, dt, dout and z where they fit (z is else read when it is needed).
+template <typename Tin, int SPT, int SL>
 struct BwdSmem {
-  static constexpr int NP = SPT * SL, CL = 32 / SL;
+  static constexpr int NP = SPT * SL, CL = 32 / SL, Q = SPT / 4;
+  static constexpr int NI = sizeof(Tin) == 2 || Q == 1 ? 4 : 3;
   float B[kBwdL * NP], C[kBwdL * NP];
   float red[2][kBwdWarps][kBwdTS][2 * NP];
   float2 delta[kBwdWarps][kBwdL][CL], x[kBwdWarps][kBwdL][CL], dy[kBwdWarps][kBwdL][CL];
-  float4 start[kBwdWarps][kBwdTiles - 1][2][SPT / 4][32];
+  union {
+    float4 start[kBwdTiles - 1][2][Q][32];
+    __align__(16) unsigned char raw[NI * kBwdL * 2 * CL * sizeof(Tin)];
+  } w[kBwdWarps];
 };
 
 // Gradients of a group of chunks, from its last chunk to its first.  With the
@@ -689,7 +695,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, Q = SPT / 4;
   static_assert(SL >= 2 && Q <= 2, "a lane finishes one of its two channels");
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  BwdSmem<SPT, SL>& sm = *reinterpret_cast<BwdSmem<SPT, SL>*>(raw_smem);
+  using Smem = BwdSmem<Tin, SPT, SL>;
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -737,53 +744,68 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       a2[j][k] = mul2(a2[j][k], f2(kLog2e));
       dA[j][k] = f2(0.f);
     }
+  // starts the copy of chunk c's inputs (positions and channels past the end are
+  // left as they are: they are masked when they are read)
+  const int qw = p.q0 + warp * CL * 2, nq = d.DG - qw;
+  auto copy_raw = [&](int c) {
+    Ring<Tin, CL, Smem::NI, kBwdL, 1> r;
+    const int64_t t0 = (int64_t)c * kBwdL;
+    const int cw = p.g * d.DG + qw;
+    r.buf = reinterpret_cast<Tin*>(sm.w[warp].raw);
+    r.src[0] = x + t0 * d.D + cw;
+    r.src[1] = dt + t0 * d.D + cw;
+    r.src[2] = dout + t0 * d.D + cw;
+    r.row[0] = r.row[1] = r.row[2] = d.D;
+    if constexpr (Smem::NI == 4) {
+      r.src[3] = z ? z + t0 * d.zs + cw : nullptr;
+      r.row[3] = d.zs;
+    }
+    r.nt = max(min(n, d.T) - (int)t0, 0), r.nq = nq, r.lane = lane, r.mode = d.mode;
+    r.fill(0);
+  };
   float dD = 0.f, dbias = 0.f;
   int ph = 0;
+  // this thread's element of a tile's dB / dC sums (position u, state e)
+  constexpr int kSum = kBwdTS * 2 * NP, kSums = (kSum + kBwdThreads - 1) / kBwdThreads;
   const int cfirst = p.c * (d.L / kBwdL), clast = min(d.nh, cfirst + d.L / kBwdL) - 1;
   for (int c = clast; c >= cfirst; --c) {
     const int t0 = c * kBwdL, t1 = min(d.T, t0 + kBwdL), nt = max(min(t1, n) - t0, 0);
-    __syncthreads();  // the chunk after this one is done with B, C and its own staging
+    if (c == clast) copy_raw(c);
+    const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
+    auto enter = [&]() { load(h, hin + hat * d.N); };  // the state entering the chunk
+    __syncthreads();  // the chunk after this one is done with B and C
     {
       RowTile<Tin, NP, kBwdL, kBwdThreads> tB, tC;
       tB.fetch(Bm + t0 * d.bs, d.bs, d.N, 0, nt);
       tC.fetch(Cm + t0 * d.cs, d.cs, d.N, 0, nt);
-      // lane -> (position sl + SL i, pair cl): delta, x and dy, once; kE
-      // positions' loads together (past the end: the last one's, not used)
-      constexpr int kE = 8;
-      for (int i0 = 0; i0 < kBwdL / SL; i0 += kE) {
-        Two<Tin> rx[kE], rd[kE], rg[kE], rz[kE];
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          const int64_t t = t0 + max(min(sl + SL * (i0 + i), nt - 1), 0);
-          rx[i] = ld_two(x + t * d.D + ln.ch, ln.two, d.wide);
-          rd[i] = ld_two(dt + t * d.D + ln.ch, ln.two, d.wide);
-          rg[i] = ld_two(dout + t * d.D + ln.ch, ln.two, d.wide);
-          if (z) rz[i] = ld_two(z + t * d.zs + ln.ch, ln.two, d.wide);
+      enter();
+      cp_wait<0>();
+      __syncwarp();
+      // lane -> (position sl + SL i, pair cl): delta, x and dy, once
+      const Two<Tin>* const rw = reinterpret_cast<const Two<Tin>*>(sm.w[warp].raw) + cl;
+#pragma unroll 4
+      for (int t = sl; t < kBwdL; t += SL) {
+        float2 xv = unpack2(rw[t * CL]);
+        float2 dl = softplus2(add2(unpack2(rw[(kBwdL + t) * CL]), bias));
+        float2 dy = unpack2(rw[(2 * kBwdL + t) * CL]);
+        if (z) {
+          float2 zv;
+          if constexpr (Smem::NI == 4)
+            zv = unpack2(rw[(3 * kBwdL + t) * CL]);
+          else
+            zv = unpack2(ld_two(z + (int64_t)(t0 + max(min(t, nt - 1), 0)) * d.zs + ln.ch, ln.two,
+                                d.wide));
+          dy = mul2(dy, mul2(zv, sigmoid2(zv)));
         }
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          const int t = sl + SL * (i0 + i);
-          float2 xv = unpack2(rx[i]), dl = softplus2(add2(unpack2(rd[i]), bias));
-          float2 dy = unpack2(rg[i]);
-          if (z) {
-            const float2 zv = unpack2(rz[i]);
-            dy = mul2(dy, mul2(zv, sigmoid2(zv)));
-          }
-          if (!ln.on || t >= nt) dl = xv = dy = f2(0.f);
-          if (!ln.two) dl.y = xv.y = dy.y = 0.f;
-          if (i0 + i < kBwdL / SL) {
-            sm.delta[warp][t][cl] = dl;
-            sm.x[warp][t][cl] = xv;
-            sm.dy[warp][t][cl] = dy;
-          }
-        }
+        if (!ln.on || t >= nt) dl = xv = dy = f2(0.f);
+        if (!ln.two) dl.y = xv.y = dy.y = 0.f;
+        sm.delta[warp][t][cl] = dl;
+        sm.x[warp][t][cl] = xv;
+        sm.dy[warp][t][cl] = dy;
       }
       tB.store(sm.B);
       tC.store(sm.C);
     }
-    const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
-    auto enter = [&]() { load(h, hin + hat * d.N); };  // the state entering the chunk
-    enter();
     __syncthreads();
     const float4* const sBv = reinterpret_cast<const float4*>(sm.B);
     const float4* const sCv = reinterpret_cast<const float4*>(sm.C);
@@ -810,11 +832,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-          sm.start[warp][tile - 1][j][q][lane] =
+          sm.w[warp].start[tile - 1][j][q][lane] =
               make_float4(h[j][2 * q].x, h[j][2 * q].y, h[j][2 * q + 1].x, h[j][2 * q + 1].y);
     }
     for (int tile = kBwdTiles - 1; tile >= 0; --tile) {
       const int tb = tile * kBwdTS;
+      if (tile == 0 && c > cfirst) {  // the kept states are used up
+        __syncwarp();
+        copy_raw(c - 1);
+      }
       auto begin = [&]() {  // h = the state entering the tile
         if (tile == 0) {
           enter();
@@ -824,7 +850,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            const float4 v = sm.start[warp][tile - 1][j][q][lane];
+            const float4 v = sm.w[warp].start[tile - 1][j][q][lane];
             h[j][2 * q] = lo2(v);
             h[j][2 * q + 1] = hi2(v);
           }
@@ -926,25 +952,31 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
           ddt[at] = from_f<Tout>(dv);
           dD = fmaf(fdy, fx, dD);
           dbias += dv;
-          // dy's slot is free now: it takes y for dz
-          if (z) reinterpret_cast<float*>(&sm.dy[warp][t][cl])[fj] = fmaf(fskip, fx, ys[u]);
+          if (z) ys[u] = fmaf(fskip, fx, ys[u]);
         }
-        __syncwarp();
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < kBwdTS * 2 * NP; i += kBwdThreads) {
-        const int u = i / (2 * NP), e = i % (2 * NP), s = e % NP;
-        if (s < d.N && tb + u < t1 - t0) {
+#pragma unroll
+      for (int k = 0; k < kSums; ++k) {
+        const int i = threadIdx.x + k * kBwdThreads;
+        const int u = i / (2 * NP), e = i % (2 * NP), st = e % NP;
+        if ((kSum % kBwdThreads == 0 || i < kSum) && st < d.N && tb + u < t1 - t0) {
           float a = 0.f;
 #pragma unroll
           for (int wv = 0; wv < kBwdWarps; ++wv) a += sm.red[ph][wv][u][e];
           bcpart[(((rowb + t0 + tb + u) * d.G + p.g) * d.ctiles + p.ct) * (2 * d.N) +
-                 (e / NP) * d.N + s] = a;
+                 (e / NP) * d.N + st] = a;
         }
+      }
+      if (z && fon) {  // the tile's dy is used up: its slots take y for dz
+#pragma unroll
+        for (int u = 0; u < kBwdTS; ++u)
+          reinterpret_cast<float*>(&sm.dy[warp][tb + u][cl])[fj] = ys[u];
       }
       ph ^= 1;
     }
     if (z) {  // dz = dout y silu'(z), a pair a lane
+      __syncwarp();
       constexpr int kE = 8;
       for (int i0 = 0; i0 < kBwdL / SL; i0 += kE) {
         Two<Tin> rg[kE], rz[kE];
@@ -1207,7 +1239,7 @@ int sel_backward(const SelDims& d, const SelIn& in, const float* init, const voi
   SelDims m = d;
   m.ctiles = bwd_main_tiles(d);
   auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2>;
-  constexpr size_t smem = sizeof(BwdSmem<SPT / 2, SL * 2>);
+  constexpr size_t smem = sizeof(BwdSmem<Tin, SPT / 2, SL * 2>);
   if (allow_smem(kern, smem) != cudaSuccess) return SSD_ERR_CUDA;
   cudaError_t e;
   SSD_LAUNCH("k_sel_bwd", s,
