@@ -138,7 +138,6 @@ constexpr int kU = 4;  // positions whose steps and gates are formed together
 template <typename Tin, int CL, int NI, int L = kStage, int S = kStages>
 struct Ring {
   static constexpr int CW = 2 * CL, kTensor = L * CW, kOne = NI * kTensor;
-  static constexpr int kElems = S * kOne;  // of one warp
   Tin* buf;
   const Tin* src[NI];  // position 0 of the range, the warp's first channel
   int64_t row[NI];     // elements between positions; NULL sources are skipped
@@ -243,21 +242,14 @@ __device__ __forceinline__ void st_states(const float2 (&v)[K2], float* row, int
 }
 
 constexpr int kFwdWarps = 4;
-#ifndef SD
-#define SD 1
-#define SB 3
-#define TD 1
-#define TB 2
-#endif
-constexpr int kScanDiv = SD, kStateDiv = TD;
-constexpr int kFwdBlocksPerSm = SB, kStateBlocksPerSm = TB;
+constexpr int kFwdBlocksPerSm = 3, kStateBlocksPerSm = 2;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 
 template <typename Tin, int SPT, int SL, int NI, bool C>
 struct PassSmem {
   static constexpr int NP = SPT * SL, TT = NP > 16 ? 512 / NP : 32;
   float B[2][TT * NP], Cm[2][C ? TT * NP : 4];
-  __align__(16) Tin ring[kFwdWarps][Ring<Tin, 32 / SL, NI>::kElems];
+  __align__(16) Tin ring[kFwdWarps][kStages * Ring<Tin, 32 / SL, NI>::kOne];
 };
 
 // Forward pass over one chunk.  OUT: with the outputs, from the state
@@ -578,8 +570,8 @@ __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
 // hin (B, nh, D, N): each chunk's own state -> the state entering it, in place:
 // H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1; B, nc, D, N): each
 // range's own adjoint at its start -> the adjoint entering it from the right:
-// G_c = gin_c + exp(A sumg_c) G_{c+1}.  One thread per (b, d, n), kC loads ahead of
-// the chain.  (The last own value of either walk is not needed.)
+// G_c = gin_c + exp(A sumg_c) G_{c+1}.  One thread per (b, d, n); the next kC
+// chunks are loaded while the chain runs over kC.  (The last own value of either walk is not needed.)
 __global__ void __launch_bounds__(256)
     k_sel_combine(const float* __restrict__ A, const float* __restrict__ init,
                   const float* __restrict__ dfinal, float* __restrict__ hin,
@@ -599,20 +591,26 @@ __global__ void __launch_bounds__(256)
   const float* sm = (rev ? sumg : sumd) + ((int64_t)b * nc + (rev ? nc - 1 : 0)) * d.D + dn / d.N;
   const float* start = rev ? dfinal : init;
   float acc = start ? start[i] : 0.f;
-  constexpr int kC = 16;
-  for (int c0 = 0; c0 < nc; c0 += kC) {
-    float e[kC], s[kC];
+  constexpr int kC = 8;
+  float e[kC], o[kC], ne[kC], no[kC];
+  auto fetch = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < kC; ++u) {
       const bool in = c0 + u < nc - 1;
-      s[u] = in ? v[(c0 + u) * sv] : 0.f;
-      e[u] = in ? sm[(c0 + u) * ss] : 0.f;
+      no[u] = in ? v[(c0 + u) * sv] : 0.f;
+      ne[u] = in ? sm[(c0 + u) * ss] : 0.f;
     }
+  };
+  fetch(0);
+  for (int c0 = 0; c0 < nc; c0 += kC) {
+#pragma unroll
+    for (int u = 0; u < kC; ++u) e[u] = ne[u], o[u] = no[u];
+    fetch(c0 + kC);
 #pragma unroll
     for (int u = 0; u < kC; ++u)
       if (c0 + u < nc) {
         v[(c0 + u) * sv] = acc;
-        acc = fmaf(ex2(e[u] * a2), acc, s[u]);
+        acc = fmaf(ex2(e[u] * a2), acc, o[u]);
       }
   }
 }
@@ -1099,14 +1097,14 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
 }
 
 // Forward ranges: as many as fill the machine once (kFwdBlocksPerSm blocks an
-// SM), each at least 64 positions; one (no state pass) where the channels fill
+// SM), each at least 32 positions; one (no state pass) where the channels fill
 // half of it by themselves.
 void fwd_chunks(SelDims* d) {
-  const int sl = (d->N > 32 ? 4 : d->N > 16 ? 2 : 1) * kScanDiv;
+  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   const int64_t blocks = (int64_t)d->B * d->G * d->ctiles;
   int64_t nc = kFwdBlocksPerSm * 152 / blocks;
-  const int64_t most = ceil_div(d->T, 64);
+  const int64_t most = ceil_div(d->T, 32);
   if (nc > most) nc = most;
   if (nc < 2) nc = 1;
   d->L = ceil_div(ceil_div(d->T, nc), 32) * 32;
@@ -1123,7 +1121,7 @@ int bwd_main_tiles(const SelDims& d) {
   return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);
 }
 void bwd_chunks(SelDims* d) {
-  const int sl = (d->N > 32 ? 4 : d->N > 16 ? 2 : 1) * kStateDiv;
+  const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   d->nh = ceil_div(d->T, kBwdL);
   const int64_t bg = (int64_t)d->B * d->G, wave = 2 * 152;
@@ -1192,11 +1190,10 @@ template <typename Tin, typename Tout, int SPT, int SL>
 int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out, float* fin,
                 float* hin, float* sumd, cudaStream_t s) {
   Tout* const o = static_cast<Tout*>(out);
-  constexpr int kS = SPT / kScanDiv, kL = SL * kScanDiv;
-  auto kstate = k_sel_scan<Tin, Tout, kS, kL, false>;
-  auto kout = k_sel_scan<Tin, Tout, kS, kL, true>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, kS, kL, 2, false>);
-  constexpr size_t mo = sizeof(PassSmem<Tin, kS, kL, 3, true>);
+  auto kstate = k_sel_scan<Tin, Tout, SPT, SL, false>;
+  auto kout = k_sel_scan<Tin, Tout, SPT, SL, true>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 2, false>);
+  constexpr size_t mo = sizeof(PassSmem<Tin, SPT, SL, 3, true>);
   if (allow_smem(kstate, ms) != cudaSuccess || allow_smem(kout, mo) != cudaSuccess)
     return SSD_ERR_CUDA;
   if (d.nc > 1) {
@@ -1228,9 +1225,8 @@ template <typename Tin, typename Tout, int SPT, int SL>
 int sel_backward(const SelDims& d, const SelIn& in, const float* init, const void* dout,
                  const float* dfinal, const SelGrads& g, const SelBwdWs& w, cudaStream_t s) {
   const Tin* go = static_cast<const Tin*>(dout);
-  constexpr int kS = SPT / kStateDiv, kL = SL * kStateDiv;
-  auto kstate = k_sel_state<Tin, kS, kL>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, kS, kL, 4, true>);
+  auto kstate = k_sel_state<Tin, SPT, SL>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 4, true>);
   if (allow_smem(kstate, ms) != cudaSuccess) return SSD_ERR_CUDA;
   SSD_LAUNCH("k_sel_state", s, kstate<<<sel_grid(d, d.nc), kFwdThreads, ms, s>>>(
                                    in, go, w.hin, w.gin, w.sumd, w.sumg, d));
