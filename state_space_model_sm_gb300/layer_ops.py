@@ -43,11 +43,12 @@ def _code(dtype):
 
 def _lead(t, name, ndim):
     """Index of the device of the call's first tensor, whose rank is checked."""
+    dev = t.get_device()
     if t.dim() != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got {tuple(t.shape)}")
-    if not t.is_cuda:
+    if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    return t.get_device()
+    return dev
 
 
 def _wrong(t, name, shape, dtype, device):
@@ -99,6 +100,14 @@ def _output(t, name, shape, dtype, like):
         return like.new_empty(shape, dtype=dtype)
     _check(t, name, shape, dtype, like.get_device())
     return t
+
+
+def _outputs(out, want, like):
+    """The named outputs (name, shape, dtype), new or from the caller's dict."""
+    if out is None:
+        new = like.new_empty
+        return {k: new(s, dtype=t) for k, s, t in want}
+    return {k: _output(out.get(k), k, s, t, like) for k, s, t in want}
 
 
 def _scratch(nbytes, like, workspace):
@@ -176,12 +185,10 @@ def causal_conv_bwd(x, w, bias, dy, init_state=None, lengths=None, silu: bool = 
     lp = _check(lengths, "lengths", (B,), _I32, dev)
     gp = _check(dy, "dy", (B, T, C), x.dtype, dev)
     fp = _check(dfinal_state, "dfinal_state", (B, K - 1, C), x.dtype, dev)
-    got = {} if out is None else out
-    out = dict(dx=_output(got.get("dx"), "dx", (B, T, C), odt, x),
-               dw=_output(got.get("dw"), "dw", (C, K), _F32, x),
-               dbias=_output(got.get("dbias"), "dbias", (C,), _F32, x))
+    want = [("dx", (B, T, C), odt), ("dw", (C, K), _F32), ("dbias", (C,), _F32)]
     if init_state is not None:
-        out["dinit_state"] = _output(got.get("dinit_state"), "dinit_state", (B, K - 1, C), odt, x)
+        want.append(("dinit_state", (B, K - 1, C), odt))
+    out = _outputs(out, want, x)
     nbytes = lib.ssd_causal_conv_workspace_size(shape)
     ws = _scratch(max(nbytes, 1), x, workspace)
     st = lib.ssd_causal_conv_bwd(shape, xp, wp, bp, ip, lp, gp, fp, out["dx"].data_ptr(),
@@ -286,8 +293,7 @@ def selective_scan_bwd(x, dt, dt_bias, A, B, C, D, z, dout, init_states=None, le
         want.append(("dz", (Bt, T, ch), odt))
     if init_states is not None:
         want.append(("dinit_states", (Bt, ch, N), _F32))
-    got = {} if out is None else out
-    out = {k: _output(got.get(k), k, s, t, x) for k, s, t in want}
+    out = _outputs(out, want, x)
     nbytes = lib.ssd_selective_scan_bwd_workspace_size(shape)
     ws = _scratch(max(nbytes, 1), x, workspace)
     st = lib.ssd_selective_scan_bwd(
@@ -348,20 +354,20 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
 # ------------------------------------------------------------------ block norm
 
 def _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps):
-    if residual.dim() < 1 or not residual.is_cuda:
+    dev, rshape = residual.get_device(), residual.shape
+    if dev < 0 or len(rshape) < 1:
         raise ValueError("residual must be a CUDA tensor (..., features)")
-    dev, F = residual.get_device(), residual.shape[-1]
+    F = rshape[-1]
     rows = residual.numel() // F if F else 0
-    ptrs = (_check(residual, "residual", residual.shape, residual.dtype, dev),
-            _check(o, "o", residual.shape, o.dtype, dev),
-            _check(w_pre, "w_pre", (F,), _F32, dev), _check(w_post, "w_post", (F,), _F32, dev),
-            None if gate is None else _check(gate, "gate", (gate.numel() // F if F else 0, F),
-                                             _F32, dev))
-    ng = 0 if gate is None else gate.shape[0]
-    if gate is not None and (ng < 1 or rows % ng != 0):
-        raise ValueError(f"gate: {ng} gate rows do not divide {rows} rows")
-    shape = _native.BlockNormShape(rows, F, ng, float(eps), float(scale), _code(o.dtype),
-                                   _code(residual.dtype))
+    rd, od, ng, gp = residual.dtype, o.dtype, 0, None
+    if gate is not None:
+        ng = gate.numel() // F if F else 0
+        gp = _check(gate, "gate", (ng, F), _F32, dev)
+        if ng < 1 or rows % ng != 0:
+            raise ValueError(f"gate: {ng} gate rows do not divide {rows} rows")
+    ptrs = (_check(residual, "residual", rshape, rd, dev), _check(o, "o", rshape, od, dev),
+            _check(w_pre, "w_pre", (F,), _F32, dev), _check(w_post, "w_post", (F,), _F32, dev), gp)
+    shape = _native.BlockNormShape(rows, F, ng, eps, scale, _code(od), _code(rd))
     return dev, shape, F, ptrs
 
 
@@ -401,8 +407,7 @@ def block_norm_bwd(residual, o, w_pre, w_post, gate, dh, dresidual_out=None, sca
         want.append(("dw_post", (F,), _F32))
     if gate is not None:
         want.append(("dgate", gate.shape, _F32))
-    got = {} if out is None else out
-    out = {k: _output(got.get(k), k, s, t, residual) for k, s, t in want}
+    out = _outputs(out, want, residual)
     nbytes = lib.ssd_block_norm_workspace_size(shape)
     ws = _scratch(max(nbytes, 1), residual, workspace)
     st = lib.ssd_block_norm_bwd(shape, *p, hp, rp, *(_at(out.get(k)) for k in (
