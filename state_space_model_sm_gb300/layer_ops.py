@@ -18,6 +18,7 @@ from . import _native
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}  # ssd_dtype
 _F32, _I32 = torch.float32, torch.int32
+_empty, _empty_like = torch.empty, torch.empty_like  # (Tensor.new_empty takes twice as long)
 _stream = torch._C._cuda_getCurrentRawStream  # of a device index; no Stream object
 _lib = None
 
@@ -72,6 +73,11 @@ def _check(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
+# The decoding calls (one token, and the block norm between layers) take a few
+# microseconds on the GPU, so their checks are written out in one condition for
+# the plain case (dense tensors, the default output); anything else goes through
+# the helpers above, which also say what is wrong.
+
 def _rows(t, name, shape, lead, dtype, device):
     """As _check for an input that may be a column range of a wider tensor: the
     ``lead`` leading dimensions (batch, or batch and position) may be strided, the
@@ -97,7 +103,7 @@ def _rows(t, name, shape, lead, dtype, device):
 def _output(t, name, shape, dtype, like):
     """t after its check, or a new tensor, on the device of ``like``."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _empty(shape, dtype=dtype, device=like.device)
     _check(t, name, shape, dtype, like.get_device())
     return t
 
@@ -105,14 +111,14 @@ def _output(t, name, shape, dtype, like):
 def _outputs(out, want, like):
     """The named outputs (name, shape, dtype), new or from the caller's dict."""
     if out is None:
-        new = like.new_empty
-        return {k: new(s, dtype=t) for k, s, t in want}
+        dev = like.device
+        return {k: _empty(s, dtype=t, device=dev) for k, s, t in want}
     return {k: _output(out.get(k), k, s, t, like) for k, s, t in want}
 
 
 def _scratch(nbytes, like, workspace):
     if workspace is None:
-        return like.new_empty(nbytes, dtype=torch.uint8)
+        return _empty(nbytes, dtype=torch.uint8, device=like.device)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError("workspace too small")
     if workspace.device != like.device or not workspace.is_contiguous():
@@ -205,13 +211,31 @@ def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_
     channels); state (nslots, width - 1, channels) in x's type, updated in place.
     slots (batch,) int32 names each row's state; a negative one marks an empty
     row, whose output is 0."""
-    lib = _native_lib()
-    dev, shape, (B, _, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 2, silu, out_dtype)
-    sp = _check(state, "state", (state.shape[0], K - 1, C), x.dtype, dev)
-    lp = _check(slots, "slots", (B,), _I32, dev)
-    y = _output(y, "y", (B, C), odt, x)
-    st = lib.ssd_causal_conv_step(shape, xp, sp, wp, bp, lp, state.shape[0], y.data_ptr(),
-                                  _stream(dev))
+    lib, xs, ws, ss, xd, dev = _lib, x.shape, w.shape, state.shape, x.dtype, x.get_device()
+    if (lib is not None and dev >= 0 and len(xs) == 2 and len(ws) == 2 and xd in _CODE
+            and out_dtype is None and y is None and x.is_contiguous()
+            and ws[0] == xs[1] and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
+            and ss == (ss[0], ws[1] - 1, xs[1]) and state.dtype is xd
+            and state.get_device() == dev and state.is_contiguous()
+            and (bias is None or (bias.shape == xs[1:] and bias.dtype is _F32
+                                  and bias.get_device() == dev and bias.is_contiguous()))
+            and (slots is None or (slots.shape == xs[:1] and slots.dtype is _I32
+                                   and slots.get_device() == dev and slots.is_contiguous()))):
+        code = _CODE[xd]
+        shape = _native.ConvShape(xs[0], 1, xs[1], ws[1], 0, 0, 1 if silu else 0, code, code)
+        y = _empty_like(x)
+        st = lib.ssd_causal_conv_step(
+            shape, x.data_ptr(), state.data_ptr(), w.data_ptr(),
+            None if bias is None else bias.data_ptr(), None if slots is None else slots.data_ptr(),
+            ss[0], y.data_ptr(), _stream(dev))
+    else:
+        lib = _native_lib()
+        dev, shape, (B, _, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 2, silu, out_dtype)
+        sp = _check(state, "state", (state.shape[0], K - 1, C), x.dtype, dev)
+        lp = _check(slots, "slots", (B,), _I32, dev)
+        y = _output(y, "y", (B, C), odt, x)
+        st = lib.ssd_causal_conv_step(shape, xp, sp, wp, bp, lp, state.shape[0], y.data_ptr(),
+                                      _stream(dev))
     if st:
         _fail("ssd_causal_conv_step", st)
     return y
@@ -309,12 +333,40 @@ def selective_step(x, dt, dt_bias, A, B, C, state, D=None, z=None, slots=None, o
     """One token of ``selective_scan_fwd`` (``ssd_selective_step``): x, dt, z, y
     (batch, channels); B, C (batch, ngroups, dstate); state (nslots, channels,
     dstate) float32, updated in place; slots as in ``causal_conv_step``."""
-    lib = _native_lib()
-    dev, shape, (Bt, _, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 2, out_dtype)
-    sp = _check(state, "state", (state.shape[0], ch, N), _F32, dev)
-    lp = _check(slots, "slots", (Bt,), _I32, dev)
-    y = _output(y, "y", (Bt, ch), odt, x)
-    st = lib.ssd_selective_step(shape, *p, sp, lp, state.shape[0], y.data_ptr(), _stream(dev))
+    lib, xs, bs, ss, xd, dev = _lib, x.shape, B.shape, state.shape, x.dtype, x.get_device()
+    if (lib is not None and dev >= 0 and len(xs) == 2 and len(bs) == 3 and xd in _CODE
+            and out_dtype is None and y is None and x.is_contiguous()
+            and dt.shape == xs and dt.dtype is xd and dt.get_device() == dev and dt.is_contiguous()
+            and bs[0] == xs[0] and B.dtype is xd and B.get_device() == dev and B.is_contiguous()
+            and C.shape == bs and C.dtype is xd and C.get_device() == dev and C.is_contiguous()
+            and ss == (ss[0], xs[1], bs[2]) and state.dtype is _F32
+            and state.get_device() == dev and state.is_contiguous()
+            and A.shape == ss[1:] and A.dtype is _F32 and A.get_device() == dev
+            and A.is_contiguous()
+            and (z is None or (z.shape == xs and z.dtype is xd and z.get_device() == dev
+                               and z.is_contiguous()))
+            and (dt_bias is None or (dt_bias.shape == xs[1:] and dt_bias.dtype is _F32
+                                     and dt_bias.get_device() == dev and dt_bias.is_contiguous()))
+            and (D is None or (D.shape == xs[1:] and D.dtype is _F32 and D.get_device() == dev
+                               and D.is_contiguous()))
+            and (slots is None or (slots.shape == xs[:1] and slots.dtype is _I32
+                                   and slots.get_device() == dev and slots.is_contiguous()))):
+        code = _CODE[xd]
+        shape = _native.SelectiveShape(xs[0], 1, xs[1], bs[2], bs[1], 0, 0, 0, 0, 0, 0, code, code)
+        y = _empty_like(x)
+        st = lib.ssd_selective_step(
+            shape, x.data_ptr(), dt.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(),
+            A.data_ptr(), B.data_ptr(), C.data_ptr(), None if D is None else D.data_ptr(),
+            None if z is None else z.data_ptr(), state.data_ptr(),
+            None if slots is None else slots.data_ptr(), ss[0], y.data_ptr(), _stream(dev))
+    else:
+        lib = _native_lib()
+        dev, shape, (Bt, _, ch, N, G), odt, p = _sel_inputs(x, dt, dt_bias, A, B, C, D, z, 2,
+                                                            out_dtype)
+        sp = _check(state, "state", (state.shape[0], ch, N), _F32, dev)
+        lp = _check(slots, "slots", (Bt,), _I32, dev)
+        y = _output(y, "y", (Bt, ch), odt, x)
+        st = lib.ssd_selective_step(shape, *p, sp, lp, state.shape[0], y.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_selective_step", st)
     return y
@@ -325,27 +377,48 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
     dt (batch, nheads), B, C (batch, ngroups, dstate); A, dt_bias, D (nheads,) and
     state (nslots, nheads, headdim, dstate) float32, the state updated in place;
     slots as in ``causal_conv_step``.  y is in ``out_dtype`` (x's type)."""
-    lib = _native_lib()
-    dev = _lead(x, "x", 3)
-    if B.dim() != 3:
-        raise ValueError("B and C must be (batch, ngroups, dstate)")
-    Bt, H, P = x.shape
-    G, N = B.shape[1:]
-    xd = x.dtype
-    odt = xd if out_dtype is None else out_dtype
-    shape = _native.Shape(Bt, 1, H, P, N, G, 1, _code(xd), _code(odt))
-    xp = _check(x, "x", x.shape, xd, dev)
-    dp = _check(dt, "dt", (Bt, H), xd, dev)
-    tp = _check(dt_bias, "dt_bias", (H,), _F32, dev)
-    ap = _check(A, "A", (H,), _F32, dev)
-    bp = _check(B, "B", (Bt, G, N), xd, dev)
-    cp = _check(C, "C", (Bt, G, N), xd, dev)
-    kp = _check(D, "D", (H,), _F32, dev)
-    sp = _check(state, "state", (state.shape[0], H, P, N), _F32, dev)
-    lp = _check(slots, "slots", (Bt,), _I32, dev)
-    y = _output(y, "y", (Bt, H, P), odt, x)
-    st = lib.ssd_step(shape, xp, dp, tp, ap, bp, cp, kp, sp, lp, state.shape[0], y.data_ptr(),
-                      _stream(dev))
+    lib, xs, bs, ss, xd, dev = _lib, x.shape, B.shape, state.shape, x.dtype, x.get_device()
+    if (lib is not None and dev >= 0 and len(xs) == 3 and len(bs) == 3 and xd in _CODE
+            and out_dtype is None and y is None and x.is_contiguous()
+            and dt.shape == xs[:2] and dt.dtype is xd and dt.get_device() == dev
+            and dt.is_contiguous()
+            and bs[0] == xs[0] and B.dtype is xd and B.get_device() == dev and B.is_contiguous()
+            and C.shape == bs and C.dtype is xd and C.get_device() == dev and C.is_contiguous()
+            and ss == (ss[0], xs[1], xs[2], bs[2]) and state.dtype is _F32
+            and state.get_device() == dev and state.is_contiguous()
+            and A.shape == xs[1:2] and A.dtype is _F32 and A.get_device() == dev
+            and A.is_contiguous()
+            and (dt_bias is None or (dt_bias.shape == xs[1:2] and dt_bias.dtype is _F32
+                                     and dt_bias.get_device() == dev and dt_bias.is_contiguous()))
+            and (D is None or (D.shape == xs[1:2] and D.dtype is _F32 and D.get_device() == dev
+                               and D.is_contiguous()))
+            and (slots is None or (slots.shape == xs[:1] and slots.dtype is _I32
+                                   and slots.get_device() == dev and slots.is_contiguous()))):
+        code = _CODE[xd]
+        shape = _native.Shape(xs[0], 1, xs[1], xs[2], bs[2], bs[1], 1, code, code)
+        y = _empty_like(x)
+        st = lib.ssd_step(
+            shape, x.data_ptr(), dt.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(),
+            A.data_ptr(), B.data_ptr(), C.data_ptr(), None if D is None else D.data_ptr(),
+            state.data_ptr(), None if slots is None else slots.data_ptr(), ss[0], y.data_ptr(),
+            _stream(dev))
+    else:
+        lib = _native_lib()
+        dev = _lead(x, "x", 3)
+        if B.dim() != 3:
+            raise ValueError("B and C must be (batch, ngroups, dstate)")
+        Bt, H, P = x.shape
+        G, N = B.shape[1:]
+        odt = xd if out_dtype is None else out_dtype
+        shape = _native.Shape(Bt, 1, H, P, N, G, 1, _code(xd), _code(odt))
+        p = (_check(x, "x", x.shape, xd, dev), _check(dt, "dt", (Bt, H), xd, dev),
+             _check(dt_bias, "dt_bias", (H,), _F32, dev), _check(A, "A", (H,), _F32, dev),
+             _check(B, "B", (Bt, G, N), xd, dev), _check(C, "C", (Bt, G, N), xd, dev),
+             _check(D, "D", (H,), _F32, dev),
+             _check(state, "state", (state.shape[0], H, P, N), _F32, dev),
+             _check(slots, "slots", (Bt,), _I32, dev))
+        y = _output(y, "y", (Bt, H, P), odt, x)
+        st = lib.ssd_step(shape, *p, state.shape[0], y.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_step", st)
     return y
@@ -382,11 +455,32 @@ def block_norm_fwd(residual, o, w_pre, w_post=None, gate=None, scale: float = 1.
     gate (ngates, features) float32: one row for all, one per sequence or one per
     row, each covering rows / ngates consecutive rows.  residual_out may be
     ``residual`` and h may be ``o`` (in place)."""
-    lib = _native_lib()
-    dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
-    residual_out = _output(residual_out, "residual_out", residual.shape, residual.dtype, residual)
-    h = _output(h, "h", o.shape, o.dtype, residual)
-    st = lib.ssd_block_norm_fwd(shape, *p, residual_out.data_ptr(), h.data_ptr(), _stream(dev))
+    lib, rs, rd, od, dev = _lib, residual.shape, residual.dtype, o.dtype, residual.get_device()
+    n = len(rs)
+    if (lib is not None and dev >= 0 and n > 0 and rs[-1] > 0 and rd in _CODE and od in _CODE
+            and residual.is_contiguous() and residual_out is None and h is None
+            and o.shape == rs and o.get_device() == dev and o.is_contiguous()
+            and w_pre.shape == rs[n - 1:] and w_pre.dtype is _F32 and w_pre.get_device() == dev
+            and w_pre.is_contiguous()
+            and (w_post is None or (w_post.shape == rs[n - 1:] and w_post.dtype is _F32
+                                    and w_post.get_device() == dev and w_post.is_contiguous()))
+            and (gate is None or (gate.shape == (1, rs[-1]) and gate.dtype is _F32
+                                  and gate.get_device() == dev and gate.is_contiguous()))):
+        F = rs[-1]
+        shape = _native.BlockNormShape(residual.numel() // F, F, 0 if gate is None else 1, eps,
+                                       scale, _CODE[od], _CODE[rd])
+        residual_out, h = _empty_like(residual), _empty_like(o)
+        st = lib.ssd_block_norm_fwd(
+            shape, residual.data_ptr(), o.data_ptr(), w_pre.data_ptr(),
+            None if w_post is None else w_post.data_ptr(),
+            None if gate is None else gate.data_ptr(), residual_out.data_ptr(), h.data_ptr(),
+            _stream(dev))
+    else:
+        lib = _native_lib()
+        dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
+        residual_out = _output(residual_out, "residual_out", rs, rd, residual)
+        h = _output(h, "h", o.shape, od, residual)
+        st = lib.ssd_block_norm_fwd(shape, *p, residual_out.data_ptr(), h.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_block_norm_fwd", st)
     return residual_out, h
