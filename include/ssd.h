@@ -383,8 +383,8 @@ int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
  * first, or 0.  x (batch, seqlen, channels) in_dtype, w (channels, width) f32,
  * bias (channels) f32 or NULL, y (batch, seqlen, channels) out_dtype;
  * final_state (batch, width - 1, channels) in_dtype or NULL: the last
- * width - 1 inputs.  2 <= width <= 4.  init_state and final_state must not
- * overlap. */
+ * width - 1 inputs.  2 <= width <= 4, batch * seqlen < 2^31, channels < 2^20.
+ * init_state and final_state must not overlap. */
 typedef struct {
   int64_t batch, seqlen, channels, width;
   int64_t x_row_stride, x_batch_stride;
@@ -422,7 +422,8 @@ int ssd_causal_conv_step(const ssd_conv_shape* shape, const void* x, void* state
  * in_dtype; dt_bias, D (channels) f32 or NULL; A (channels, dstate) f32;
  * init_states, final_states (batch, channels, dstate) f32 or NULL; out (batch,
  * seqlen, channels) out_dtype.  channels a multiple of ngroups, dstate <= 64
- * (<= 256 in ssd_selective_step), seqlen at most 2^21.  Workspace of the size
+ * (<= 256 in ssd_selective_step), seqlen at most 2^21, batch < 65536; the
+ * backward takes batch * seqlen * ngroups up to 2^31.  Workspace of the size
  * query's bytes (0 for a rejected shape), 16-byte aligned, caller-owned. */
 typedef struct {
   int64_t batch, seqlen, channels, dstate, ngroups;

@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
   __shared__ float red[kBwdWarps][K + 1][32 * V];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int v = blockIdx.x * 32 + lane, c0 = v * V;
-  const int b = blockIdx.y / nblk, s = (blockIdx.y - b * nblk) * kBwdWarps + warp;
+  const int v = blockIdx.y * 32 + lane, c0 = v * V;
+  const int b = blockIdx.x / nblk, s = (blockIdx.x - b * nblk) * kBwdWarps + warp;
   P dw[K + 1][N];
 #pragma unroll
   for (int k = 0; k <= K; ++k)
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
     for (int i = 0; i < V; ++i) red[warp][k][lane * V + i] = reinterpret_cast<float*>(dw[k])[i];
   __syncthreads();
   // part (blocks, K + 1, C)
-  const int nc = min(32 * V, d.C - blockIdx.x * 32 * V);
-  float* p = part + (int64_t)blockIdx.y * (K + 1) * d.C + (int64_t)blockIdx.x * 32 * V;
+  const int nc = min(32 * V, d.C - (int)blockIdx.y * 32 * V);
+  float* p = part + (int64_t)blockIdx.x * (K + 1) * d.C + (int64_t)blockIdx.y * 32 * V;
   for (int i = threadIdx.x; i < (K + 1) * 32 * V; i += blockDim.x) {
     const int k = i / (32 * V), c = i - k * (32 * V);
     if (c < nc) {
@@ -455,7 +455,8 @@ int conv_dims(const ssd_conv_shape* s, ConvDims* d) {
     return SSD_ERR_INVALID_ARG;
   if (s->width < 2 || s->width > 4) return SSD_ERR_UNSUPPORTED;
   if (s->in_dtype == SSD_F32 && s->out_dtype == SSD_BF16) return SSD_ERR_UNSUPPORTED;
-  if (s->batch >= 65536 || s->seqlen >= (1 << 30) || s->channels >= (1 << 24))
+  if (s->batch >= 65536 || s->seqlen >= (1 << 30) || s->batch * s->seqlen >= ((int64_t)1 << 31) ||
+      s->channels >= (1 << 20))
     return SSD_ERR_UNSUPPORTED;
   d->B = (int)s->batch, d->T = (int)s->seqlen, d->C = (int)s->channels;
   d->xs = s->x_row_stride ? s->x_row_stride : s->channels;
@@ -494,7 +495,7 @@ void bwd_segments(ConvDims* d) {  // blocks of 32 vectors x 8 segments
 
 // the backward's vector width and its blocks per sequence: shape-only, so
 // the workspace query and the call agree
-int bwd_parts(const ConvDims& d) { return d.B * ceil_div(d.nseg, kBwdWarps); }
+int bwd_parts(const ConvDims& d) { return d.B * ceil_div(d.nseg, kBwdWarps); }  // < 2^31: see conv_dims
 
 template <typename Tin, typename Tout, int V>
 int launch_fwd(ConvDims d, int K, const void* x, const float* w, const float* bias,
@@ -523,7 +524,7 @@ int launch_bwd(ConvDims d, int K, const void* x, const float* w, const float* bi
                float* dw, float* dbias, void* dinit, float* part, cudaStream_t s) {
   d.nvec = d.C / V;
   const int nblk = ceil_div(d.nseg, kBwdWarps), nparts = bwd_parts(d);
-  const dim3 grid(ceil_div(d.nvec, 32), nparts);
+  const dim3 grid(nparts, ceil_div(d.nvec, 32));
   constexpr int smem = 2 * 32 * kBwdWarps * Feed<Tin, V>::kBytes;
   auto go = [&](auto kern) {
     if (smem > 32 * 1024)  // beside the 20 KB of sums
@@ -625,7 +626,6 @@ int ssd_causal_conv_bwd(const ssd_conv_shape* shape, const void* x, const float*
     return SSD_ERR_WORKSPACE;
   d.nvec = ceil_div(d.C, 4);
   bwd_segments(&d);
-  if (bwd_parts(d) > 65535) return SSD_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* part = static_cast<float*>(workspace);
   const bool vec = d.C % 4 == 0 && vec_ok(x, d.xs, ie, 4) && vec_ok(x, d.xb, ie, 4) && vec_ok(init_state, d.C, ie, 4) &&

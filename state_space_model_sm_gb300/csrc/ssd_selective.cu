@@ -1369,7 +1369,9 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
       workspace_bytes < ssd_selective_scan_bwd_workspace_size(shape))
     return SSD_ERR_WORKSPACE;
   bwd_chunks(&d);
-  if ((int64_t)d.B * d.G * d.ctiles > 0x7fffffff || d.nc > 65535) return SSD_ERR_UNSUPPORTED;
+  if ((int64_t)d.B * d.G * d.ctiles > 0x7fffffff || d.nc > 65535 ||
+      (int64_t)d.B * d.T * d.G > ((int64_t)1 << 31))
+    return SSD_ERR_UNSUPPORTED;
   const SelBwdWs w = bwd_ws(d, workspace);
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const SelGrads g{dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit_states};
