@@ -146,13 +146,8 @@ struct Feed {
   __device__ __forceinline__ void start(unsigned char* smem, const T* src, int64_t step, int count) {
     ring = reinterpret_cast<Raw<T, V>*>(smem) + threadIdx.x;
     p = src, stride = step, left = count, put = 0, use = kStages - 1;
-    if constexpr (kAsync) {
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fill();
-    } else {
-      fill();
-    }
   }
+  static constexpr int kAhead = kAsync ? kStages - 1 : 1;  // groups copied ahead
   // Takes the next kU positions, copied by now (next_of), and starts a later copy.
   __device__ __forceinline__ void next() {
     if constexpr (kAsync) {
@@ -169,9 +164,23 @@ struct Feed {
   }
 };
 
-// The next kU positions of one or two feeds.  The feeds fill in turn, so each
-// has kStages - 1 groups in flight, the oldest of which is waited for (a thread
-// reads only what it copied itself).
+// The first copies, and then the next kU positions, of one or two feeds.  The feeds
+// fill in turn from the first group on: copies complete in the order they were
+// started, so leaving the last kStages - 2 of each in flight means that the group
+// to be read has arrived in both (a thread reads only what it copied itself).
+template <typename T, int V>
+__device__ __forceinline__ void start_of(Feed<T, V>& a) {
+#pragma unroll
+  for (int i = 0; i < Feed<T, V>::kAhead; ++i) a.fill();
+}
+template <typename T, int V>
+__device__ __forceinline__ void start_of(Feed<T, V>& a, Feed<T, V>& b) {
+#pragma unroll
+  for (int i = 0; i < Feed<T, V>::kAhead; ++i) {
+    a.fill();
+    b.fill();
+  }
+}
 template <typename T, int V>
 __device__ __forceinline__ void next_of(Feed<T, V>& a) {
   cp_wait<Feed<T, V>::kStages - 2>();
@@ -207,7 +216,10 @@ __global__ void __launch_bounds__(256)
   const int t0 = s * d.seg, t1 = min(d.T, t0 + d.seg), tv = min(t1, n);
   extern __shared__ __align__(16) unsigned char smem[];
   Feed<Tin, V> in;
-  if (t0 < tv) in.start(smem, x + (int64_t)t0 * d.xs, d.xs, tv - t0);
+  if (t0 < tv) {
+    in.start(smem, x + (int64_t)t0 * d.xs, d.xs, tv - t0);
+    start_of(in);
+  }
   if (s == 0 && final_state) {
     Tin* f = final_state + (int64_t)b * (K - 1) * d.C + c0;
     for (int j = 0; j < K - 1; ++j)
@@ -292,6 +304,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
     Feed<Tin, V> fx, fg;
     fx.start(smem, x + (int64_t)t0 * d.xs, d.xs, ti - t0);
     fg.start(smem + Feed<Tin, V>::kBytes * blockDim.x, dy + (int64_t)t0 * d.C, d.C, ti - t0);
+    start_of(fx, fg);
     const Taps<V, K> taps(w, bias, c0);
     P win[K][N], du[K][N];
 #pragma unroll

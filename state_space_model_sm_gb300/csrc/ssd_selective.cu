@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
               const float2 bk = i ? hi2(b4) : lo2(b4);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                const float2 a = decay2(j ? dl[u].y : dl[u].x, a2[j][k]);
                 h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
                 if (OUT) y[j] = fma2(h[j][k], i ? hi2(c4) : lo2(c4), y[j]);
               }
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
               const float2 bk = i ? hi2(b4) : lo2(b4), ck = i ? hi2(c4) : lo2(c4);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float2 a = ex2_2(mul2(f2(j ? dl[u].y : dl[u].x), a2[j][k]));
+                const float2 a = decay2(j ? dl[u].y : dl[u].x, a2[j][k]);
                 h[j][k] = fma2(a, h[j][k], mul2(f2(j ? dtx.y : dtx.x), bk));
                 pr[j][k] = mul2(pr[j][k], a);
                 gl[j][k] = fma2(pr[j][k], mul2(f2(j ? dy[u].y : dy[u].x), ck), gl[j][k]);
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < kC; ++u)
       if (c0 + u < nc) {
         v[(c0 + u) * sv] = acc;
-        acc = fmaf(ex2(e[u] * a2), acc, o[u]);
+        acc = fmaf(decay(e[u], a2), acc, o[u]);
       }
   }
 }
@@ -768,6 +768,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   const int cfirst = p.c * (d.L / kBwdL), clast = min(d.nh, cfirst + d.L / kBwdL) - 1;
   for (int c = clast; c >= cfirst; --c) {
     const int t0 = c * kBwdL, t1 = min(d.T, t0 + kBwdL), nt = max(min(t1, n) - t0, 0);
+    float cD = 0.f, cbias = 0.f;  // the chunk's parts: shorter sums round less
     if (c == clast) copy_raw(c);
     const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
     auto enter = [&]() { load(h, hin + hat * d.N); };  // the state entering the chunk
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int k = 2 * q + i;
-            const float2 a = ex2_2(mul2(f2(j ? dl.y : dl.x), a2[j][k]));
+            const float2 a = decay2(j ? dl.y : dl.x, a2[j][k]);
             h[j][k] = fma2(a, h[j][k], mul2(f2(j ? xd.y : xd.x), i ? hi2(b4) : lo2(b4)));
           }
       }
@@ -902,7 +903,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
             for (int j = 0; j < 2; ++j) {
               const float2 dlj = f2(j ? dl.y : dl.x);
               const float2 g = fma2(ck, f2(j ? dy.y : dy.x), gc[j][k]);
-              gc[j][k] = mul2(ex2_2(mul2(dlj, a2[j][k])), g);
+              gc[j][k] = mul2(decay2(dlj.x, a2[j][k]), g);
               const float2 w = mul2(gc[j][k], u > 0 ? hs[u > 0 ? u - 1 : 0][j][k] : h[j][k]);
               dA[j][k] = fma2(dlj, w, dA[j][k]);
               aw[j] = fma2(a2[j][k], w, aw[j]);
@@ -948,8 +949,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
           const int64_t at = (rowb + t0 + t) * d.D + fch;
           dx[at] = from_f<Tout>(fmaf(fdl, fgb, fskip * fdy));
           ddt[at] = from_f<Tout>(dv);
-          dD = fmaf(fdy, fx, dD);
-          dbias += dv;
+          cD = fmaf(fdy, fx, cD);
+          cbias += dv;
           if (z) ys[u] = fmaf(fskip, fx, ys[u]);
         }
       }
@@ -973,6 +974,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       }
       ph ^= 1;
     }
+    dD += cD;
+    dbias += cbias;
     if (z) {  // dz = dout y silu'(z), a pair a lane
       __syncwarp();
       constexpr int kE = 8;

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, RB > 2 ? 5 : 1)
     const int hd = SEL ? rm : rm / d.P;
     const float xv = to_f(x[b * d.xs + rm]);
     delta = softplus(to_f(dt[b * d.dts + hd]) + (dt_bias ? dt_bias[hd] : 0.f));
-    if constexpr (!SEL) dec = ex2(delta * A[hd] * kLog2e);
+    if constexpr (!SEL) dec = decay(delta, A[hd] * kLog2e);
     dtx = delta * xv;
     skip = D ? D[hd] * xv : 0.f;
   }
@@ -106,10 +106,10 @@ __global__ void __launch_bounds__(32 * kStepWarps, RB > 2 ? 5 : 1)
         float h[V], a[V];
         unpack<float, V>(raw[i], h);
         if constexpr (SEL) {
-          const float dl = __shfl_sync(0xffffffffu, delta, i, LPR) * kLog2e;
+          const float dl = __shfl_sync(0xffffffffu, delta, i, LPR);
           unpack<float, V>(ra[i], a);
 #pragma unroll
-          for (int j = 0; j < V; ++j) a[j] = ex2(dl * a[j]);
+          for (int j = 0; j < V; ++j) a[j] = decay(dl, a[j] * kLog2e);
         } else {
           const float dc = __shfl_sync(0xffffffffu, dec, i, LPR);
 #pragma unroll

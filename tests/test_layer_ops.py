@@ -89,6 +89,35 @@ def test_conv_matches_oracle(cuda_lib, case):
         close(k, v, r[k])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_conv_backward_under_load(cuda_lib, dtype):
+    """At a size that keeps the memory system busy, where a copy read before it has
+    arrived would show: the gradients against the formula in fp64, call after call
+    with the same bits."""
+    import torch
+    it, _ = types(dtype)
+    B, T, C, K = 4, 4096, 1792, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, dy = (torch.randn(B, T, C, generator=g, device="cuda").to(it) for _ in range(2))
+    w, bias = torch.randn(C, K, generator=g, device="cuda") * 0.5, torch.zeros(C, device="cuda")
+    first = {k: v.clone() for k, v in cuda_lib.causal_conv_bwd(x, w, bias, dy).items()}
+    xp = torch.nn.functional.pad(x.double(), (0, 0, K - 1, 0))
+    u = sum(xp[:, k:k + T] * w[:, k].double() for k in range(K))
+    sg = torch.sigmoid(u)
+    du = dy.double() * sg * (1 + u * (1 - sg))
+    dup = torch.nn.functional.pad(du, (0, 0, 0, K - 1))
+    dx = sum(dup[:, K - 1 - k:K - 1 - k + T] * w[:, k].double() for k in range(K))
+    close("dx", first["dx"], dx.cpu().numpy())
+    close("dw", first["dw"], torch.stack([(du * xp[:, k:k + T]).sum((0, 1)) for k in range(K)],
+                                         1).cpu().numpy())
+    close("dbias", first["dbias"], du.sum((0, 1)).cpu().numpy())
+    junk = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(50):
+        junk.add_(1)  # x and dy leave the L2 cache
+        again = cuda_lib.causal_conv_bwd(x, w, bias, dy)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
 def test_conv_of_a_column_range_and_in_place_step(cuda_lib):
     """x as columns of a wider tensor, at an offset that allows 8-byte accesses
     only; then tokens one by one from the prompt's state."""
@@ -245,6 +274,31 @@ def test_scan_of_column_ranges(cuda_lib):
     g1 = cuda_lib.selective_scan_bwd(x, dt, bias, A, B, C, D, z, dout)
     g2 = cuda_lib.selective_scan_bwd(*v, dout)
     assert all(torch.equal(g1[k], g2[k]) for k in g1)
+
+
+def test_repeats_under_load_are_bit_identical(cuda_lib):
+    """As test_conv_backward_under_load, for the rings of the scan and of the block
+    norm: their values are pinned at small sizes, a late copy would change bits."""
+    import torch
+    it, g = torch.bfloat16, torch.Generator(device="cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    B, T, D, N = 2, 2048, 1536, 16
+    A = -torch.arange(1.0, N + 1, device="cuda").repeat(D, 1)
+    x, z, dout = (r(B, T, D).to(it) for _ in range(3))
+    sc = (x, (r(B, T, D) - 4).to(it), r(D), A, r(B, T, 1, N).to(it), r(B, T, 1, N).to(it), r(D), z)
+    bn = (r(8192, 4096), r(8192, 4096).to(it), r(4096), r(4096), r(2, 4096))
+    dh, w = r(8192, 4096).to(it), r(D, 4)
+    calls = (lambda: dict(enumerate(cuda_lib.selective_scan_fwd(*sc))),
+             lambda: cuda_lib.selective_scan_bwd(*sc, dout),
+             lambda: dict(enumerate(cuda_lib.block_norm_fwd(*bn))),
+             lambda: cuda_lib.block_norm_bwd(*bn, dh, bn[0]),
+             lambda: dict(enumerate(cuda_lib.causal_conv_fwd(x, w))))
+    junk = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for call in calls:
+        first = {k: v.clone() for k, v in call().items()}
+        for _ in range(15):
+            junk.add_(1)  # the inputs leave the L2 cache
+            assert all(torch.equal(first[k], v) for k, v in call().items())
 
 
 def test_repeated_calls_are_bit_identical(cuda_lib):
