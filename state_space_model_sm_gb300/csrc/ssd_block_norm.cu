@@ -133,6 +133,11 @@ struct Rows {
   static constexpr int kSlot = NV * (NIO * kIo + NRES * kRes);
   const Tio* io[NIO];     // VEC: this thread's first column of the next row to copy;
   const Tres* res[NRES];  // else the row in use
+  // single columns, 8 a thread: the next row in registers (more would not fit)
+  static constexpr bool kReg = !VEC && EPT <= 8;
+  static constexpr int NR = kReg ? EPT : 1;
+  Tio cio[NIO][NR], nio[NIO][NR];
+  Tres cres[NRES][NR], nres[NRES][NR];
   uint32_t put, use, end, slot;  // ring offsets: next copy's slot, the row in use; end; a slot
   uint32_t iostep, resstep;      // bytes of the block's pieces v of one tensor
   int F, S, left, pieces;        // left: rows still to copy; pieces: of this thread in a row
@@ -143,7 +148,7 @@ struct Rows {
   }
   __device__ __forceinline__ void start(int width, int stages, int r0, int r1) {
     F = width, S = stages, left = r1 - r0;
-    const int64_t at = VEC ? (int64_t)r0 * F + C::col(0) : ((int64_t)r0 - 1) * F;
+    const int64_t at = VEC ? (int64_t)r0 * F + C::col(0) : ((int64_t)r0 - (kReg ? 0 : 1)) * F;
 #pragma unroll
     for (int i = 0; i < NIO; ++i) io[i] += at;
 #pragma unroll
@@ -156,6 +161,23 @@ struct Rows {
       for (int v = 0; v < NV; ++v) pieces += C::col(v) < F;
       slot = kSlot * blockDim.x, end = S * slot, put = 0, use = end - slot;
       for (int i = 0; i < S - 1; ++i) fill();
+    } else if constexpr (kReg) {
+      fetch();
+    }
+  }
+  __device__ __forceinline__ void fetch() {  // the next row into registers
+    if (left > 0) {
+#pragma unroll
+      for (int v = 0; v < NR; ++v) {
+        const int c = C::col(v);
+#pragma unroll
+        for (int i = 0; i < NIO; ++i) nio[i][v] = c < F ? io[i][c] : from_f<Tio>(0.f);
+#pragma unroll
+        for (int i = 0; i < NRES; ++i)
+          nres[i][v] = c < F && res[i] ? res[i][c] : from_f<Tres>(0.f);
+      }
+      advance();
+      --left;
     }
   }
   __device__ __forceinline__ void advance() {
@@ -211,6 +233,15 @@ struct Rows {
       else
         cp_wait<0>();
       fill();
+    } else if constexpr (kReg) {
+#pragma unroll
+      for (int v = 0; v < NR; ++v) {
+#pragma unroll
+        for (int i = 0; i < NIO; ++i) cio[i][v] = nio[i][v];
+#pragma unroll
+        for (int i = 0; i < NRES; ++i) cres[i][v] = nres[i][v];
+      }
+      fetch();
     } else {
       advance();
     }
@@ -218,6 +249,8 @@ struct Rows {
   __device__ __forceinline__ void get_io(int i, float2 (&x)[C::P2]) const {
     if constexpr (VEC)
       get<Tio>(io_at(i), iostep, pieces, x);
+    else if constexpr (kReg)
+      of_regs(cio[i], x);
     else
       C::load(io[i], F, x, 0.f);
   }
@@ -229,9 +262,16 @@ struct Rows {
 #pragma unroll
         for (int k = 0; k < C::P2; ++k) x[k] = f2(0.f);
       }
+    } else if constexpr (kReg) {
+      of_regs(cres[i], x);
     } else {
       C::load(res[i], F, x, 0.f);
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ static void of_regs(const T (&r)[NR], float2 (&x)[C::P2]) {
+#pragma unroll
+    for (int k = 0; k < C::P2; ++k) x[k] = make_float2(to_f(r[2 * k]), to_f(r[2 * k + 1]));
   }
   template <typename T>
   __device__ __forceinline__ void get(uint32_t at, uint32_t step, int n, float2 (&x)[C::P2]) const {
@@ -473,9 +513,11 @@ int bn_dims(const ssd_block_norm_shape* s, BnDims* d) {
   return SSD_OK;
 }
 
-// Columns of a thread: 16 where rows divide into vectors, else 4, or 16 above
-// 2048 columns.
-int bn_cols(int F, bool vec) { return vec || F > 4 * kMaxThreads ? 16 : 4; }
+// Columns of a thread: 16 where rows divide into vectors, else 4, 8 above 2048
+// columns and 16 above 4096 (512 threads at most).
+int bn_cols(int F, bool vec) {
+  return vec || F > 8 * kMaxThreads ? 16 : F > 4 * kMaxThreads ? 8 : 4;
+}
 
 // Blocks resident on an SM: 512 threads of them (100 to 128 registers each).
 int bn_ctas(int nt) {
@@ -560,6 +602,7 @@ int bn_pick(const BnDims& d, const BnPtrs& p, bool vec, bool bwd, cudaStream_t s
   if (vec && d.F == 16 * d.nt) return bn_launch<Tio, Tres, true, 16, true>(d, p, bwd, s);
   if (vec) return bn_launch<Tio, Tres, true, 16, false>(d, p, bwd, s);
   if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, false, 4, false>(d, p, bwd, s);
+  if (bn_cols(d.F, vec) == 8) return bn_launch<Tio, Tres, false, 8, false>(d, p, bwd, s);
   return bn_launch<Tio, Tres, false, 16, false>(d, p, bwd, s);
 }
 

@@ -62,6 +62,10 @@ __device__ __forceinline__ int sel_len(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+__device__ __forceinline__ int64_t z_end(const SelDims& d) {  // elements from z's first to its last
+  return (d.B - 1) * d.zb + (d.T - 1) * d.zs + d.D;
+}
+
 // A block's place: batch row, group of channels, chunk and first channel.
 struct Place {
   int b, g, c, q0, ct;
@@ -128,28 +132,63 @@ __device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x,
 __device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
 
 // A warp's ring of its inputs: L positions of its channels for NI tensors a
-// stage, S stages, filled by cp.async ahead of the computation (no
-// registers held, and nothing the compiler can sink to the loads' use).
-// Where rows are 16-byte aligned a copy moves 16 bytes; else pairs are copied by
-// 4 or 8 bytes, and odd bf16 rows by element through registers.
+// stage, S stages, filled by cp.async ahead of the computation (no registers
+// held, and nothing the compiler can sink to the loads' use).  Where rows are
+// 16-byte aligned a copy moves 16 bytes, else a pair of channels (4 or 8 bytes),
+// or 4-byte elements.  ODD: bf16 rows that start in the middle of a 4-byte word
+// at every other position are copied as the whole words that cover them, with
+// the row's first channel at element 0 or 1 (plain loads, through registers, took
+// three times as long over the whole scan).
 constexpr int kStage = 8, kStages = 3;
 constexpr int kU = 4;  // positions whose steps and gates are formed together
 
-template <typename Tin, int CL, int NI, int L = kStage, int S = kStages>
+template <typename Tin, int CL, int NI, bool ODD, int L = kStage, int S = kStages>
 struct Ring {
-  static constexpr int CW = 2 * CL, kTensor = L * CW, kOne = NI * kTensor;
+  static constexpr int CW = 2 * CL, W = CW + (ODD ? 8 : 0);  // channels; elements of a row
+  static constexpr int kTensor = L * W, kOne = NI * kTensor;
   Tin* buf;
   const Tin* src[NI];  // position 0 of the range, the warp's first channel
   int64_t row[NI];     // elements between positions; NULL sources are skipped
+  // ODD: the tensor's first element and its end, which no copy crosses
+  const Tin *lo[ODD ? NI : 1], *hi[ODD ? NI : 1];
   int nt, nq, lane, mode;
 
+  __device__ __forceinline__ void set(int i, const void* tensor, int64_t offset, int64_t stride,
+                                      int64_t last) {
+    const Tin* const t = static_cast<const Tin*>(tensor);
+    src[i] = t ? t + offset : t;
+    row[i] = stride;
+    if constexpr (ODD) lo[i] = t, hi[i] = t + last;
+  }
+  // element of a row at which its first channel lies (t: from the range's start)
+  __device__ __forceinline__ int shift(int i, int t) const {
+    if constexpr (!ODD) return 0;
+    return (int)((reinterpret_cast<uintptr_t>(src[i]) >> 1) + (uintptr_t)(t & (int)row[i])) & 1;
+  }
   // stage s of the range into its slot; positions past nt, and channels past nq
-  // are left as zeros or as they are (their results are never written)
+  // are left as they are (their results are never written)
   __device__ __forceinline__ void fill(int s) {
     Tin* const dst0 = buf + (s % S) * kOne;
     const int t0 = s * L;
     if (t0 < nt) {
-      if (mode == 16) {
+      if constexpr (ODD) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (!src[i]) continue;
+          for (int e = lane; e < L * (CL + 1); e += 32) {  // a word each
+            const int t = e / (CL + 1), c = (e % (CL + 1)) * 2, sh = shift(i, t0 + t);
+            if (t0 + t >= nt || c >= min(CW, nq) + sh) continue;
+            Tin* const dst = dst0 + i * kTensor + t * W + c;
+            const Tin* const from = src[i] + (t0 + t) * row[i] + c - sh;
+            if (from >= lo[i] && from + 2 <= hi[i]) {
+              cp_async<4>(dst, from);
+            } else {  // the tensor's first or last word
+              if (from >= lo[i]) dst[0] = from[0];
+              if (from + 1 >= lo[i] && from + 1 < hi[i]) dst[1] = from[1];
+            }
+          }
+        }
+      } else if (mode == 16) {
         constexpr int V = 16 / sizeof(Tin), R = CW / V;  // 16-byte pieces of a row
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -158,7 +197,7 @@ struct Ring {
           for (int k = 0; k < (L * R + 31) / 32; ++k) {
             const int e = lane + 32 * k, t = e / R, c = (e % R) * V;
             if (e < L * R && t0 + t < nt && c < nq)
-              cp_async<16>(dst0 + i * kTensor + t * CW + c, src[i] + (t0 + t) * row[i] + c);
+              cp_async<16>(dst0 + i * kTensor + t * W + c, src[i] + (t0 + t) * row[i] + c);
           }
         }
       } else {
@@ -168,16 +207,13 @@ struct Ring {
           for (int e = lane; e < L * CL; e += 32) {
             const int t = e / CL, c = (e % CL) * 2;
             if (t0 + t >= nt || c >= nq) continue;
-            Tin* dst = dst0 + i * kTensor + t * CW + c;
+            Tin* dst = dst0 + i * kTensor + t * W + c;
             const Tin* from = src[i] + (t0 + t) * row[i] + c;
             if (mode == 2) {  // an aligned pair
               cp_async<2 * sizeof(Tin)>(dst, from);
             } else if constexpr (sizeof(Tin) == 4) {
               cp_async<4>(dst, from);
               if (c + 1 < nq) cp_async<4>(dst + 1, from + 1);
-            } else {
-              dst[0] = from[0];
-              if (c + 1 < nq) dst[1] = from[1];
             }
           }
         }
@@ -193,9 +229,13 @@ struct Ring {
     fill(s + S - 1);
   }
   __device__ __forceinline__ float2 get(int s, int t, int i, int cl) const {
-    const Two<Tin> v = *reinterpret_cast<const Two<Tin>*>(buf + (s % S) * kOne +
-                                                          i * kTensor + t * CW + 2 * cl);
-    return unpack2(v);
+    const Tin* const q = buf + (s % S) * kOne + i * kTensor + t * W + 2 * cl;
+    if constexpr (ODD) {
+      const int sh = shift(i, t + (L % 2 ? s * L : 0));
+      return make_float2(to_f(q[sh]), to_f(q[sh + 1]));
+    } else {
+      return unpack2(*reinterpret_cast<const Two<Tin>*>(q));
+    }
   }
 };
 
@@ -245,23 +285,23 @@ constexpr int kFwdWarps = 4;
 constexpr int kFwdBlocksPerSm = 3, kStateBlocksPerSm = 2;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 
-template <typename Tin, int SPT, int SL, int NI, bool C>
+template <typename Tin, int SPT, int SL, int NI, bool C, bool ODD>
 struct PassSmem {
   static constexpr int NP = SPT * SL, TT = NP > 16 ? 512 / NP : 32;
   float B[2][TT * NP], Cm[2][C ? TT * NP : 4];
-  __align__(16) Tin ring[kFwdWarps][kStages * Ring<Tin, 32 / SL, NI>::kOne];
+  __align__(16) Tin ring[kFwdWarps][kStages * Ring<Tin, 32 / SL, NI, ODD>::kOne];
 };
 
 // Forward pass over one chunk.  OUT: with the outputs, from the state
 // hin (B, nc, D, N) (or init when there is one chunk); else the chunk's state
 // from zero into hin and its delta sum into sumd (B, nc, D).
-template <typename Tin, typename Tout, int SPT, int SL, bool OUT>
+template <typename Tin, typename Tout, int SPT, int SL, bool OUT, bool ODD>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
     k_sel_scan(SelIn in, const float* __restrict__ init, float* __restrict__ hin,
                float* __restrict__ sumd, Tout* __restrict__ out, float* __restrict__ final_state,
                SelDims d) {
   constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, NI = OUT ? 3 : 2;
-  using Smem = PassSmem<Tin, SPT, SL, NI, OUT>;
+  using Smem = PassSmem<Tin, SPT, SL, NI, OUT, ODD>;
   constexpr int TT = Smem::TT;
   extern __shared__ __align__(16) unsigned char raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
@@ -277,16 +317,12 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
   const bool gated = OUT && in.z;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
-  Ring<Tin, CL, NI> ring;
+  Ring<Tin, CL, NI, ODD> ring;
   ring.buf = sm.ring[warp];
-  ring.src[0] = static_cast<const Tin*>(in.x) + row0 * d.D + cw;
-  ring.src[1] = static_cast<const Tin*>(in.dt) + row0 * d.D + cw;
-  ring.row[0] = ring.row[1] = d.D;
-  if constexpr (OUT) {
-    ring.src[2] =
-        gated ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + cw : nullptr;
-    ring.row[2] = d.zs;
-  }
+  const int64_t all = (int64_t)d.B * d.T * d.D;
+  ring.set(0, in.x, row0 * d.D + cw, d.D, all);
+  ring.set(1, in.dt, row0 * d.D + cw, d.D, all);
+  if constexpr (OUT) ring.set(2, in.z, p.b * d.zb + t0 * d.zs + cw, d.zs, z_end(d));
   ring.nt = nt, ring.nq = d.DG - qw, ring.lane = threadIdx.x & 31, ring.mode = d.mode;
   ring.fill(0);
   ring.fill(1);
@@ -421,13 +457,13 @@ constexpr int kBwdL = 32;  // positions of a backward chunk
 // (hin) and delta sum, and the group's adjoint at its start from zero after it
 // (gin).  Running products of the decays give the adjoint in the forward
 // direction, from the same exponentials.
-template <typename Tin, int SPT, int SL>
+template <typename Tin, int SPT, int SL, bool ODD>
 __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
     k_sel_state(SelIn in, const Tin* __restrict__ dout, float* __restrict__ hin,
                 float* __restrict__ gin, float* __restrict__ sumd, float* __restrict__ sumg,
                 SelDims d) {
   constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2;
-  using Smem = PassSmem<Tin, SPT, SL, 4, true>;
+  using Smem = PassSmem<Tin, SPT, SL, 4, true, ODD>;
   constexpr int TT = Smem::TT;
   static_assert(kBwdL % TT == 0, "a chunk is whole tiles");
   extern __shared__ __align__(16) unsigned char raw_smem[];
@@ -442,14 +478,13 @@ __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
   const int qw = p.q0 + warp * CL * 2, cw = p.g * d.DG + qw;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + t0 * d.bs + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + t0 * d.cs + (int64_t)p.g * d.N;
-  Ring<Tin, CL, 4> ring;
+  Ring<Tin, CL, 4, ODD> ring;
   ring.buf = sm.ring[warp];
-  ring.src[0] = static_cast<const Tin*>(in.x) + row0 * d.D + cw;
-  ring.src[1] = static_cast<const Tin*>(in.dt) + row0 * d.D + cw;
-  ring.src[2] = dout + row0 * d.D + cw;
-  ring.src[3] = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb + t0 * d.zs + cw : nullptr;
-  ring.row[0] = ring.row[1] = ring.row[2] = d.D;
-  ring.row[3] = d.zs;
+  const int64_t all = (int64_t)d.B * d.T * d.D;
+  ring.set(0, in.x, row0 * d.D + cw, d.D, all);
+  ring.set(1, in.dt, row0 * d.D + cw, d.D, all);
+  ring.set(2, dout, row0 * d.D + cw, d.D, all);
+  ring.set(3, in.z, p.b * d.zb + t0 * d.zs + cw, d.zs, z_end(d));
   ring.nt = nt, ring.nq = d.DG - qw, ring.lane = threadIdx.x & 31, ring.mode = d.mode;
   ring.fill(0);
   ring.fill(1);
@@ -658,16 +693,17 @@ constexpr int kBwdTiles = kBwdL / kBwdTS;
 
 // The next chunk's inputs are copied over the kept states once those are used
 // up: x, dt, dout and z where they fit (z is else read when it is needed).
-template <typename Tin, int SPT, int SL>
+template <typename Tin, int SPT, int SL, bool ODD>
 struct BwdSmem {
   static constexpr int NP = SPT * SL, CL = 32 / SL, Q = SPT / 4;
   static constexpr int NI = sizeof(Tin) == 2 || Q == 1 ? 4 : 3;
   float B[kBwdL * NP], C[kBwdL * NP];
   float red[2][kBwdWarps][kBwdTS][2 * NP];
   float2 delta[kBwdWarps][kBwdL][CL], x[kBwdWarps][kBwdL][CL], dy[kBwdWarps][kBwdL][CL];
+  using R = Ring<Tin, CL, NI, ODD, kBwdL, 1>;
   union {
     float4 start[kBwdTiles - 1][2][Q][32];
-    __align__(16) unsigned char raw[NI * kBwdL * 2 * CL * sizeof(Tin)];
+    __align__(16) unsigned char raw[R::kOne * sizeof(Tin)];
   } w[kBwdWarps];
 };
 
@@ -684,7 +720,7 @@ struct BwdSmem {
 // keeps and what it sends sit in the same registers in every lane.  The
 // block's warps are then added in shared memory, and each block writes its
 // part (B, T, G, ctiles, 2 N).
-template <typename Tin, typename Tout, int SPT, int SL>
+template <typename Tin, typename Tout, int SPT, int SL, bool ODD>
 __global__ void __launch_bounds__(kBwdThreads, 2)
     k_sel_bwd(SelIn in, const Tin* __restrict__ dout, const float* __restrict__ hin,
               const float* __restrict__ gin, Tout* __restrict__ dx, Tout* __restrict__ ddt,
@@ -693,7 +729,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   constexpr int CL = 32 / SL, NP = SPT * SL, K2 = SPT / 2, Q = SPT / 4;
   static_assert(SL >= 2 && Q <= 2, "a lane finishes one of its two channels");
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  using Smem = BwdSmem<Tin, SPT, SL>;
+  using Smem = BwdSmem<Tin, SPT, SL, ODD>;
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   griddep_launch_dependents();
   griddep_wait();
@@ -709,6 +745,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   const Tin* z = in.z ? static_cast<const Tin*>(in.z) + p.b * d.zb : nullptr;
   const Tin* Bm = static_cast<const Tin*>(in.B) + p.b * d.bb + (int64_t)p.g * d.N;
   const Tin* Cm = static_cast<const Tin*>(in.C) + p.b * d.cb + (int64_t)p.g * d.N;
+  const Tin* const dout0 = dout;
   dout += rowb * d.D;
 
   // the channel that this lane finishes: the pair's first or second
@@ -744,22 +781,18 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
     }
   // starts the copy of chunk c's inputs (positions and channels past the end are
   // left as they are: they are masked when they are read)
-  const int qw = p.q0 + warp * CL * 2, nq = d.DG - qw;
-  auto copy_raw = [&](int c) {
-    Ring<Tin, CL, Smem::NI, kBwdL, 1> r;
-    const int64_t t0 = (int64_t)c * kBwdL;
-    const int cw = p.g * d.DG + qw;
+  const int qw = p.q0 + warp * CL * 2, cw = p.g * d.DG + qw;
+  auto ring_of = [&](int c) {
+    typename Smem::R r;
+    const int64_t t0 = (int64_t)c * kBwdL, at = (rowb + t0) * d.D + cw;
+    const int64_t all = (int64_t)d.B * d.T * d.D;
     r.buf = reinterpret_cast<Tin*>(sm.w[warp].raw);
-    r.src[0] = x + t0 * d.D + cw;
-    r.src[1] = dt + t0 * d.D + cw;
-    r.src[2] = dout + t0 * d.D + cw;
-    r.row[0] = r.row[1] = r.row[2] = d.D;
-    if constexpr (Smem::NI == 4) {
-      r.src[3] = z ? z + t0 * d.zs + cw : nullptr;
-      r.row[3] = d.zs;
-    }
-    r.nt = max(min(n, d.T) - (int)t0, 0), r.nq = nq, r.lane = lane, r.mode = d.mode;
-    r.fill(0);
+    r.set(0, in.x, at, d.D, all);
+    r.set(1, in.dt, at, d.D, all);
+    r.set(2, dout0, at, d.D, all);
+    if constexpr (Smem::NI == 4) r.set(3, in.z, p.b * d.zb + t0 * d.zs + cw, d.zs, z_end(d));
+    r.nt = max(n - (int)t0, 0), r.nq = d.DG - qw, r.lane = lane, r.mode = d.mode;
+    return r;
   };
   float dD = 0.f, dbias = 0.f;
   int ph = 0;
@@ -769,7 +802,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   for (int c = clast; c >= cfirst; --c) {
     const int t0 = c * kBwdL, t1 = min(d.T, t0 + kBwdL), nt = max(min(t1, n) - t0, 0);
     float cD = 0.f, cbias = 0.f;  // the chunk's parts: shorter sums round less
-    if (c == clast) copy_raw(c);
+    const auto raw = ring_of(c);
+    if (c == clast) ring_of(c).fill(0);
     const int64_t hat = ((int64_t)p.b * d.nh + c) * d.D + ln.ch;
     auto enter = [&]() { load(h, hin + hat * d.N); };  // the state entering the chunk
     __syncthreads();  // the chunk after this one is done with B and C
@@ -781,16 +815,15 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       cp_wait<0>();
       __syncwarp();
       // lane -> (position sl + SL i, pair cl): delta, x and dy, once
-      const Two<Tin>* const rw = reinterpret_cast<const Two<Tin>*>(sm.w[warp].raw) + cl;
 #pragma unroll 4
       for (int t = sl; t < kBwdL; t += SL) {
-        float2 xv = unpack2(rw[t * CL]);
-        float2 dl = softplus2(add2(unpack2(rw[(kBwdL + t) * CL]), bias));
-        float2 dy = unpack2(rw[(2 * kBwdL + t) * CL]);
+        float2 xv = raw.get(0, t, 0, cl);
+        float2 dl = softplus2(add2(raw.get(0, t, 1, cl), bias));
+        float2 dy = raw.get(0, t, 2, cl);
         if (z) {
           float2 zv;
           if constexpr (Smem::NI == 4)
-            zv = unpack2(rw[(3 * kBwdL + t) * CL]);
+            zv = raw.get(0, t, 3, cl);
           else
             zv = unpack2(ld_two(z + (int64_t)(t0 + max(min(t, nt - 1), 0)) * d.zs + ln.ch, ln.two,
                                 d.wide));
@@ -838,7 +871,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
       const int tb = tile * kBwdTS;
       if (tile == 0 && c > cfirst) {  // the kept states are used up
         __syncwarp();
-        copy_raw(c - 1);
+        ring_of(c - 1).fill(0);
       }
       auto begin = [&]() {  // h = the state entering the tile
         if (tile == 0) {
@@ -1189,14 +1222,14 @@ cudaError_t allow_smem(K kern, size_t bytes) {
              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename Tin, typename Tout, int SPT, int SL>
+template <typename Tin, typename Tout, int SPT, int SL, bool ODD>
 int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out, float* fin,
                 float* hin, float* sumd, cudaStream_t s) {
   Tout* const o = static_cast<Tout*>(out);
-  auto kstate = k_sel_scan<Tin, Tout, SPT, SL, false>;
-  auto kout = k_sel_scan<Tin, Tout, SPT, SL, true>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 2, false>);
-  constexpr size_t mo = sizeof(PassSmem<Tin, SPT, SL, 3, true>);
+  auto kstate = k_sel_scan<Tin, Tout, SPT, SL, false, ODD>;
+  auto kout = k_sel_scan<Tin, Tout, SPT, SL, true, ODD>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 2, false, ODD>);
+  constexpr size_t mo = sizeof(PassSmem<Tin, SPT, SL, 3, true, ODD>);
   if (allow_smem(kstate, ms) != cudaSuccess || allow_smem(kout, mo) != cudaSuccess)
     return SSD_ERR_CUDA;
   if (d.nc > 1) {
@@ -1224,12 +1257,12 @@ struct SelGrads {
 
 // SPT, SL: the first pass's states and state lanes; the main pass has half the
 // states a lane (its live set is three times as large) on twice the lanes.
-template <typename Tin, typename Tout, int SPT, int SL>
+template <typename Tin, typename Tout, int SPT, int SL, bool ODD>
 int sel_backward(const SelDims& d, const SelIn& in, const float* init, const void* dout,
                  const float* dfinal, const SelGrads& g, const SelBwdWs& w, cudaStream_t s) {
   const Tin* go = static_cast<const Tin*>(dout);
-  auto kstate = k_sel_state<Tin, SPT, SL>;
-  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 4, true>);
+  auto kstate = k_sel_state<Tin, SPT, SL, ODD>;
+  constexpr size_t ms = sizeof(PassSmem<Tin, SPT, SL, 4, true, ODD>);
   if (allow_smem(kstate, ms) != cudaSuccess) return SSD_ERR_CUDA;
   SSD_LAUNCH("k_sel_state", s, kstate<<<sel_grid(d, d.nc), kFwdThreads, ms, s>>>(
                                    in, go, w.hin, w.gin, w.sumd, w.sumg, d));
@@ -1237,8 +1270,8 @@ int sel_backward(const SelDims& d, const SelIn& in, const float* init, const voi
     return SSD_ERR_CUDA;
   SelDims m = d;
   m.ctiles = bwd_main_tiles(d);
-  auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2>;
-  constexpr size_t smem = sizeof(BwdSmem<Tin, SPT / 2, SL * 2>);
+  auto kern = k_sel_bwd<Tin, Tout, SPT / 2, SL * 2, ODD>;
+  constexpr size_t smem = sizeof(BwdSmem<Tin, SPT / 2, SL * 2, ODD>);
   if (allow_smem(kern, smem) != cudaSuccess) return SSD_ERR_CUDA;
   cudaError_t e;
   SSD_LAUNCH("k_sel_bwd", s,
@@ -1342,10 +1375,11 @@ int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, cons
   const void* const states[3] = {A, init_states, final_states};
   access(&d, ie, oe, ins, outs, z, states);
   return by_states(d.N, [&](auto spt, auto sl) {
-#define SSD_GO(TI, TO)                                                                      \
-  sel_forward<TI, TO, spt(), sl()>(d, in, init_states, out, final_states, hin, sumd, s)
-    if (ie == 4) return SSD_GO(float, float);
-    return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
+#define SSD_GO(TI, TO, ODD)                                                                   \
+  sel_forward<TI, TO, spt(), sl(), ODD>(d, in, init_states, out, final_states, hin, sumd, s)
+    if (ie == 4) return SSD_GO(float, float, false);
+    if (d.mode == 1) return oe == 4 ? SSD_GO(bf16, float, true) : SSD_GO(bf16, bf16, true);
+    return oe == 4 ? SSD_GO(bf16, float, false) : SSD_GO(bf16, bf16, false);
 #undef SSD_GO
   });
 }
@@ -1384,10 +1418,11 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
   const void* const states[3] = {A, dinit_states, nullptr};
   access(&d, ie, oe, ins, outs, z, states);
   return by_states(d.N, [&](auto spt, auto sl) {
-#define SSD_GO(TI, TO)                                                                      \
-  sel_backward<TI, TO, spt(), sl()>(d, in, init_states, dout, dfinal_states, g, w, s)
-    if (ie == 4) return SSD_GO(float, float);
-    return oe == 4 ? SSD_GO(bf16, float) : SSD_GO(bf16, bf16);
+#define SSD_GO(TI, TO, ODD)                                                                   \
+  sel_backward<TI, TO, spt(), sl(), ODD>(d, in, init_states, dout, dfinal_states, g, w, s)
+    if (ie == 4) return SSD_GO(float, float, false);
+    if (d.mode == 1) return oe == 4 ? SSD_GO(bf16, float, true) : SSD_GO(bf16, bf16, true);
+    return oe == 4 ? SSD_GO(bf16, float, false) : SSD_GO(bf16, bf16, false);
 #undef SSD_GO
   });
 }
