@@ -76,15 +76,17 @@ __device__ __forceinline__ float block_sum(float a, float2 (*red)[16], int& ph) 
   return a;
 }
 
-// A thread's EPT columns, as pairs.  VEC: EPT / 4 pieces of 4 consecutive columns
-// (16 bytes of fp32, 8 of bf16), the threads' pieces side by side, so every
-// access of a warp is one unbroken run (8 columns would be 32-byte pieces of
-// fp32, whose 16-byte halves touch each sector twice: 20 % slower); else single
-// columns, blockDim.x apart (widths or addresses that these do not fit).
+// A thread's EPT columns, as pairs, in pieces of VEC consecutive columns, the
+// threads' pieces side by side, so every access of a warp is one unbroken run.
+// VEC is 8 where layer and residual are bf16 (16-byte pieces: 88 us at 16384 x
+// 1000 forward and backward and 270 at 8192 x 8192, against 108 and 290 with 4);
+// 4 where one of them is fp32 (16 bytes; 8 would be 32-byte pieces, whose 16-byte
+// halves touch each sector twice: 20 % slower), or where the width or an address
+// fits only 4; 0 where none fits: single columns, blockDim.x apart.
 // FULL: the row is exactly the block's columns (no bounds to check).
-template <bool VEC, int EPT, bool FULL>
+template <int VEC, int EPT, bool FULL>
 struct Cols {
-  static constexpr int W = VEC ? 4 : 1, P2 = EPT / 2, NV = EPT / W;
+  static constexpr int W = VEC ? VEC : 1, P2 = EPT / 2, NV = EPT / W;
   __device__ __forceinline__ static int col(int v) {
     return (v * (int)blockDim.x + (int)threadIdx.x) * W;
   }
@@ -120,16 +122,16 @@ struct Cols {
   }
 };
 
-// A block's rows of its inputs.  VEC: a ring in shared memory; a thread copies the
+// A block's rows of its inputs.  VEC != 0: a ring in shared memory; a thread copies the
 // pieces that it will use itself, S - 1 rows ahead, so the bytes in flight are
 // set by the ring and no barrier is needed.  Else plain loads of the row.
 // Addresses advance by a row at a time.
-template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL, int NIO, int NRES>
+template <typename Tio, typename Tres, int VEC, int EPT, bool FULL, int NIO, int NRES>
 struct Rows {
   using C = Cols<VEC, EPT, FULL>;
   static constexpr int NV = VEC ? C::NV : 0;
   // bytes of a thread's piece of one tensor, of its row of one, of its slot
-  static constexpr int kIo = 4 * sizeof(Tio), kRes = 4 * sizeof(Tres);
+  static constexpr int kIo = VEC * sizeof(Tio), kRes = VEC * sizeof(Tres);
   static constexpr int kSlot = NV * (NIO * kIo + NRES * kRes);
   const Tio* io[NIO];     // VEC: this thread's first column of the next row to copy;
   const Tres* res[NRES];  // else the row in use
@@ -197,7 +199,7 @@ struct Rows {
   __device__ __forceinline__ void fill() {  // the next row, into the next slot
     if (left > 0) {
       unsigned char* const q = smem() + put;
-      const int cols = 4 * blockDim.x;
+      const int cols = VEC * blockDim.x;
 #pragma unroll
       for (int i = 0; i < NIO; ++i)
 #pragma unroll
@@ -279,12 +281,12 @@ struct Rows {
     const unsigned char* q = smem() + use + at;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      Raw<T, 4> r = zero_raw<T, 4>();
-      if (FULL || v < n) r = *reinterpret_cast<const Raw<T, 4>*>(q + v * step);
-      float t[4];
-      unpack<T, 4>(r, t);
+      Raw<T, C::W> r = zero_raw<T, C::W>();
+      if (FULL || v < n) r = *reinterpret_cast<const Raw<T, C::W>*>(q + v * step);
+      float t[C::W];
+      unpack<T, C::W>(r, t);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[v * 4 + k] = t[k];
+      for (int k = 0; k < C::W; ++k) f[v * C::W + k] = t[k];
     }
   }
 };
@@ -300,7 +302,7 @@ __device__ __forceinline__ void load_gw(float2 (&gw)[C::P2], const float* w_post
   for (int i = 0; i < C::P2; ++i) gw[i] = mul2(gw[i], mul2(t[i], f2(d.scale)));
 }
 
-template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
+template <typename Tio, typename Tres, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_fwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 // P_g is slot blockIdx.x + g, which no other (block, gate row) pair has, because
 // from one pair that shares rows to the next the block, the gate row or both
 // grow.
-template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
+template <typename Tio, typename Tres, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     k_block_norm_bwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
                      const float* __restrict__ w_pre, const float* __restrict__ w_post,
@@ -571,7 +573,7 @@ cudaError_t bn_ring(K kern, BnDims* d, size_t stage, size_t* bytes) {
              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
 }
 
-template <typename Tio, typename Tres, bool VEC, int EPT, bool FULL>
+template <typename Tio, typename Tres, int VEC, int EPT, bool FULL>
 int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
   const Tres* r = static_cast<const Tres*>(p.r);
   const Tio* o = static_cast<const Tio*>(p.o);
@@ -598,15 +600,19 @@ int bn_launch(BnDims d, const BnPtrs& p, bool bwd, cudaStream_t s) {
 }
 
 template <typename Tio, typename Tres>
-int bn_pick(const BnDims& d, const BnPtrs& p, bool vec, bool bwd, cudaStream_t s) {
-  if (vec && d.F == 16 * d.nt) return bn_launch<Tio, Tres, true, 16, true>(d, p, bwd, s);
-  if (vec) return bn_launch<Tio, Tres, true, 16, false>(d, p, bwd, s);
-  if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, false, 4, false>(d, p, bwd, s);
-  if (bn_cols(d.F, vec) == 8) return bn_launch<Tio, Tres, false, 8, false>(d, p, bwd, s);
-  return bn_launch<Tio, Tres, false, 16, false>(d, p, bwd, s);
+int bn_pick(const BnDims& d, const BnPtrs& p, int vec, bool bwd, cudaStream_t s) {
+  if constexpr (sizeof(Tres) == 2) {
+    if (vec == 8 && d.F == 16 * d.nt) return bn_launch<Tio, Tres, 8, 16, true>(d, p, bwd, s);
+    if (vec == 8) return bn_launch<Tio, Tres, 8, 16, false>(d, p, bwd, s);
+  }
+  if (vec && d.F == 16 * d.nt) return bn_launch<Tio, Tres, 4, 16, true>(d, p, bwd, s);
+  if (vec) return bn_launch<Tio, Tres, 4, 16, false>(d, p, bwd, s);
+  if (bn_cols(d.F, vec) == 4) return bn_launch<Tio, Tres, 0, 4, false>(d, p, bwd, s);
+  if (bn_cols(d.F, vec) == 8) return bn_launch<Tio, Tres, 0, 8, false>(d, p, bwd, s);
+  return bn_launch<Tio, Tres, 0, 16, false>(d, p, bwd, s);
 }
 
-int bn_run(const BnDims& d, const ssd_block_norm_shape* sh, const BnPtrs& p, bool vec, bool bwd,
+int bn_run(const BnDims& d, const ssd_block_norm_shape* sh, const BnPtrs& p, int vec, bool bwd,
            cudaStream_t s) {
   if (sh->in_dtype == SSD_F32) return bn_pick<float, float>(d, p, vec, bwd, s);
   if (sh->res_dtype == SSD_F32) return bn_pick<bf16, float>(d, p, vec, bwd, s);
@@ -644,9 +650,12 @@ int ssd_block_norm_fwd(const ssd_block_norm_shape* shape, const void* residual, 
   if (off(residual, re) || off(residual_out, re) || off(o, ie) || off(h, ie) || off(w_pre, 4) ||
       off(w_post, 4) || off(gate, 4))
     return SSD_ERR_INVALID_ARG;
-  const bool vec = vec_ok(o, d.F, ie, 4) && vec_ok(h, d.F, ie, 4) && vec_ok(residual, d.F, re, 4) &&
-                   vec_ok(residual_out, d.F, re, 4) && vec_ok(w_pre, d.F, 4, 4) &&
-                   vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4) && d.F % 4 == 0;
+  const auto fits = [&](int w) {
+    return d.F % w == 0 && vec_ok(o, d.F, ie, w) && vec_ok(h, d.F, ie, w) &&
+           vec_ok(residual, d.F, re, w) && vec_ok(residual_out, d.F, re, w) &&
+           vec_ok(w_pre, d.F, 4, 4) && vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4);
+  };
+  const int vec = re == 2 && fits(8) ? 8 : fits(4) ? 4 : 0;
   bn_grid(&d, vec, false);
   const BnPtrs p{residual, o, w_pre, w_post, gate, nullptr, nullptr, residual_out, h, nullptr};
   return bn_run(d, shape, p, vec, false, static_cast<cudaStream_t>(stream));
@@ -680,10 +689,13 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
   if (!workspace || off(workspace, 16) || workspace_bytes < bn_bwd_floats(d) * sizeof(float))
     return SSD_ERR_WORKSPACE;
   if (d.ng + 2 > 65535) return SSD_ERR_UNSUPPORTED;
-  const bool vec = d.F % 4 == 0 && vec_ok(o, d.F, ie, 4) && vec_ok(dh, d.F, ie, 4) &&
-                   vec_ok(d_o, d.F, ie, 4) && vec_ok(residual, d.F, re, 4) &&
-                   vec_ok(dresidual_out, d.F, re, 4) && vec_ok(dresidual, d.F, re, 4) &&
-                   vec_ok(w_pre, d.F, 4, 4) && vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4);
+  const auto fits = [&](int w) {
+    return d.F % w == 0 && vec_ok(o, d.F, ie, w) && vec_ok(dh, d.F, ie, w) &&
+           vec_ok(d_o, d.F, ie, w) && vec_ok(residual, d.F, re, w) &&
+           vec_ok(dresidual_out, d.F, re, w) && vec_ok(dresidual, d.F, re, w) &&
+           vec_ok(w_pre, d.F, 4, 4) && vec_ok(w_post, d.F, 4, 4) && vec_ok(gate, d.F, 4, 4);
+  };
+  const int vec = re == 2 && fits(8) ? 8 : fits(4) ? 4 : 0;
   bn_grid(&d, vec, true);
   const BnPtrs p{residual, o, w_pre, w_post, gate, dh, dresidual_out, dresidual, d_o,
                  static_cast<float*>(workspace)};

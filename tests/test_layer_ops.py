@@ -449,6 +449,28 @@ def test_block_norm_matches_oracle(cuda_lib, case):
             close(k, v, ref[k])
 
 
+@pytest.mark.parametrize("rows,F,shift", [(300, 1028, 0), (40, 512, 4), (40, 520, 4), (40, 512, 1)])
+def test_block_norm_bf16_rows_of_less_alignment(cuda_lib, rows, F, shift):
+    """bf16 layer and residual whose width or address admits only shorter accesses."""
+    import torch
+    it, g = torch.bfloat16, np.random.default_rng(rows + F + shift)
+    r, o, dh, dr = (stored(g.standard_normal((rows, F)), it) for _ in range(4))
+    wp, wq = (stored(1 + 0.1 * g.standard_normal(F), torch.float32) for _ in range(2))
+
+    def at(v):
+        buf = torch.empty(rows * F + shift, dtype=it, device="cuda")[shift:].view(rows, F)
+        return buf.copy_(dev(v, it))
+
+    rn, h = cuda_lib.block_norm_fwd(at(r), at(o), dev(wp), dev(wq))
+    rr, hr = lo.block_norm_fwd(r, o, wp, wq, None, 1.0)
+    close("residual", rn, rr)
+    close("h", h, hr)
+    ref = lo.block_norm_bwd(r, o, wp, wq, None, dh, dr, 1.0)
+    got = cuda_lib.block_norm_bwd(at(r), at(o), dev(wp), dev(wq), None, at(dh), at(dr))
+    for k, v in got.items():
+        close(k, v, ref[k])
+
+
 def test_block_norm_in_place_and_unaligned_rows(cuda_lib):
     import torch
     r = torch.randn(33, 64, device="cuda")
