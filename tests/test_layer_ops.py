@@ -471,6 +471,13 @@ def test_block_norm_bf16_rows_of_less_alignment(cuda_lib, rows, F, shift):
         close(k, v, ref[k])
 
 
+@pytest.mark.parametrize("io,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,F", [(700, 1030), (2, 2), (5, 8190)])
+def test_block_norm_even_widths(cuda_lib, io, res, rows, F):
+    gates = 2 if rows % 2 == 0 else 5
+    test_block_norm_matches_oracle(cuda_lib, (rows, F, io, res, True, gates, 0.5))
+
+
 def test_block_norm_in_place_and_unaligned_rows(cuda_lib):
     import torch
     r = torch.randn(33, 64, device="cuda")
