@@ -73,11 +73,6 @@ def _check(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
-# The decoding calls (one token, and the block norm between layers) take a few
-# microseconds on the GPU, so their checks are written out in one condition for
-# the plain case (dense tensors, the default output); anything else goes through
-# the helpers above, which also say what is wrong.
-
 def _rows(t, name, shape, lead, dtype, device):
     """As _check for an input that may be a column range of a wider tensor: the
     ``lead`` leading dimensions (batch, or batch and position) may be strided, the
@@ -205,6 +200,11 @@ def causal_conv_bwd(x, w, bias, dy, init_state=None, lengths=None, silu: bool = 
         _fail("ssd_causal_conv_bwd", st)
     return out
 
+
+# The decoding calls (one token, and the block norm between layers) take a few
+# microseconds on the GPU, so their checks are written out in one condition for
+# the plain case (dense tensors, the default output); anything else goes through
+# the checks of the helpers above, which also say what is wrong.
 
 def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_dtype=None, y=None):
     """One token of ``causal_conv_fwd`` (``ssd_causal_conv_step``): x, y (batch,
@@ -495,18 +495,26 @@ def block_norm_bwd(residual, o, w_pre, w_post, gate, dh, dresidual_out=None, sca
     dev, shape, F, p = _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps)
     hp = _check(dh, "dh", o.shape, o.dtype, dev)
     rp = _check(dresidual_out, "dresidual_out", residual.shape, residual.dtype, dev)
-    want = [("dresidual", residual.shape, residual.dtype), ("do", o.shape, o.dtype),
-            ("dw_pre", (F,), _F32)]
-    if w_post is not None:
-        want.append(("dw_post", (F,), _F32))
-    if gate is not None:
-        want.append(("dgate", gate.shape, _F32))
-    out = _outputs(out, want, residual)
+    given = out
+    if given is None:
+        out = {"dresidual": _empty_like(residual), "do": _empty_like(o), "dw_pre": _empty_like(w_pre)}
+        if w_post is not None:
+            out["dw_post"] = _empty_like(w_post)
+        if gate is not None:
+            out["dgate"] = _empty_like(gate)
+    else:
+        want = [("dresidual", residual.shape, residual.dtype), ("do", o.shape, o.dtype),
+                ("dw_pre", (F,), _F32), ("dw_post", (F,), _F32)]
+        out = _outputs(given, want if w_post is not None else want[:3], residual)
+        if gate is not None:
+            out["dgate"] = _output(given.get("dgate"), "dgate", gate.shape, _F32, residual)
     nbytes = lib.ssd_block_norm_workspace_size(shape)
-    ws = _scratch(max(nbytes, 1), residual, workspace)
-    st = lib.ssd_block_norm_bwd(shape, *p, hp, rp, *(_at(out.get(k)) for k in (
-        "dresidual", "do", "dw_pre", "dw_post", "dgate")), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(dev))
+    ws = _scratch(nbytes or 1, residual, workspace)
+    st = lib.ssd_block_norm_bwd(
+        shape, *p, hp, rp, out["dresidual"].data_ptr(), out["do"].data_ptr(),
+        out["dw_pre"].data_ptr(), None if w_post is None else out["dw_post"].data_ptr(),
+        None if gate is None else out["dgate"].data_ptr(), ws.data_ptr(),
+        nbytes if workspace is None else ws.numel() * ws.element_size(), _stream(dev))
     if st:
         _fail("ssd_block_norm_bwd", st)
     return out
