@@ -347,11 +347,10 @@ int ssd_scan_set_config(const ssd_shape* shape, const ssd_scan_config* config);
  * table entry exists, 0 if not, -SSD_ERR_INVALID_ARG for a bad shape. */
 int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
 
-/* Layer operators around the scan.  The pages name no kernels for them; they
- * are what a layer needs beside the scan and the gated norm: the short causal
- * convolution in front of it, the selective scan of layers with a decay per
- * channel and state, one token of each for decoding, and the residual / norm
- * step between layers.
+/* Layer operators around the scan: what a layer needs beside the scan and the
+ * gated norm, that is the short causal convolution in front of it, the selective
+ * scan of layers with a decay per channel and state, one token of each for
+ * decoding, and the residual / norm step between layers.
  *
  * Sequences of unequal lengths: `lengths` (batch) int32 device memory or NULL.
  * Positions from lengths[b] on (clamped to [0, seqlen]) are padding: their

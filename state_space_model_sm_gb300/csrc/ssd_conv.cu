@@ -3,7 +3,7 @@
 //     y = silu(u) or u,  silu(u) = u / (1 + e^-u)
 // with x before position 0 taken from the carried state (the K - 1 inputs
 // before the sequence, oldest first) or 0; its backward; and the single-token
-// form, which shifts the state by one.  The pages name no kernel for it.
+// form, which shifts the state by one.
 //
 // All three are HBM streams: an element costs 2 K + ~8 operations against 4
 // to 8 bytes, far below the machine's ratio.  Channels are contiguous, so a
@@ -11,6 +11,11 @@
 // accesses are unbroken) and walks positions with the last K - 1 inputs in
 // registers: every input is read once, plus K - 1 rows per segment.  The next
 // rows are loaded while the current ones are used.
+//
+// Measured at 4 x 4096 x 1792, K = 4, silu, bf16: forward 25 us (4.7 TB/s, 0.69 of
+// a plain copy's rate), backward 48 us (0.54) and 6 for the weights' sums; fp32:
+// 0.77 over both.  bf16 is bound by issue as much as by memory (60 % and 52 % of
+// the slots; 16 and 28 instructions an element, of which the taps are 2 and 6).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -111,7 +116,7 @@ struct Taps {
 // channels are at least 4 bytes they are copied asynchronously into a ring in
 // shared memory that only this thread reads (kStages - 1 groups ahead, no
 // barrier and no registers); single bf16 channels go through registers, one
-// group ahead.
+// group ahead (rows of 1791 bf16 channels take 1.5 times as long as 1792).
 constexpr int kU = 4;
 template <typename T, int V>
 struct Feed {
@@ -483,6 +488,8 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // Positions a thread walks, of 8 to 128, by the shortest modelled time: waves
 // of resident threads, each as long as a segment and what it costs by itself
 // (the K - 1 rows before it, the taps, one load's latency: about 12 positions).
+// Against fixed segments of 16, 32 and 128, forward and backward: 70 us at
+// 4 x 4096 x 1792 (92, 78, 84); forward at 1 x 512 x 1536: 6.3 us (8.3, 10.3, 22.6).
 template <typename F>
 void pick_segment(ConvDims* d, F&& waves) {
   int64_t best = -1;

@@ -3,10 +3,13 @@
 //     delta = softplus(dt + dt_bias)
 //     h[n]  = exp(delta A[d, n]) h[n] + delta x B[n]
 //     y     = sum_n C[n] h[n] + D[d] x,   out = y silu(z)  (or y without z)
-// and its backward.  The pages' scan has one scalar decay per head, which
-// turns a chunk into matrix products; with a decay per (d, n) there is no such
-// product, and every (position, channel, state) costs one exponential and four
-// operations of the FMA pipe: the arithmetic binds, not HBM.
+// and its backward.  With one decay per head a chunk turns into matrix products;
+// with a decay per (d, n) there is no such product, and every (position, channel,
+// state) costs one exponential and four operations of the FMA pipe: the
+// arithmetic binds, not HBM (figures at each kernel).  An SM forms 32
+// exponentials and issues 63 lanes of packed operations a clock, measured alone;
+// loops of this mix, measured without any loads, reach 50 to 60 % of the issue
+// slots, and so do these kernels.
 //
 // The sequence is cut into chunks that run in parallel, since B x channels
 // alone leaves most of the machine idle:
@@ -295,6 +298,10 @@ struct PassSmem {
 // Forward pass over one chunk.  OUT: with the outputs, from the state
 // hin (B, nc, D, N) (or init when there is one chunk); else the chunk's state
 // from zero into hin and its delta sum into sumd (B, nc, D).
+// Without OUT it is bound by the exponentials (61 to 65 % of their unit's slots,
+// 59 % of the issue slots): 82 us for 4 x 4096 x 1536 x 16 elements and 374 us for
+// 65536 x 2048 x 16, 5.0 and 5.7 elements a ps.  With OUT (the product with C, the
+// gate, the store) by issue: 58 %, 50 % of the exponentials' slots; 116 and 550 us.
 template <typename Tin, typename Tout, int SPT, int SL, bool OUT, bool ODD>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
     k_sel_scan(SelIn in, const float* __restrict__ init, float* __restrict__ hin,
@@ -456,7 +463,8 @@ constexpr int kBwdL = 32;  // positions of a backward chunk
 // The backward's first pass over a group of chunks: each chunk's state from zero
 // (hin) and delta sum, and the group's adjoint at its start from zero after it
 // (gin).  Running products of the decays give the adjoint in the forward
-// direction, from the same exponentials.
+// direction, from the same exponentials.  159 us for 4 x 4096 x 1536 x 16 (2.5
+// elements a ps) at 248 registers, two blocks an SM: issue, 48 % of the slots.
 template <typename Tin, int SPT, int SL, bool ODD>
 __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
     k_sel_state(SelIn in, const Tin* __restrict__ dout, float* __restrict__ hin,
@@ -606,7 +614,9 @@ __global__ void __launch_bounds__(kFwdThreads, kStateBlocksPerSm)
 // H_{c+1} = exp(A sumd_c) H_c + S_c.  With gin (blockIdx.y = 1; B, nc, D, N): each
 // range's own adjoint at its start -> the adjoint entering it from the right:
 // G_c = gin_c + exp(A sumg_c) G_{c+1}.  One thread per (b, d, n); the next kC
-// chunks are loaded while the chain runs over kC.  (The last own value of either walk is not needed.)
+// chunks are loaded while the chain runs over kC.  (The last own value of either
+// walk is not needed.)  Bound by the loads' latency: 8 us for the forward of
+// 4 x 4096 x 1536 x 16, 30 for the backward, which has a state every 32 positions.
 __global__ void __launch_bounds__(256)
     k_sel_combine(const float* __restrict__ A, const float* __restrict__ init,
                   const float* __restrict__ dfinal, float* __restrict__ hin,
@@ -720,6 +730,12 @@ struct BwdSmem {
 // keeps and what it sends sit in the same registers in every lane.  The
 // block's warps are then added in shared memory, and each block writes its
 // part (B, T, G, ctiles, 2 N).
+// 578 us for 4 x 4096 x 1536 x 16 (0.7 elements a ps): 27 instructions an element,
+// of which the two walks forward are 8 and the sums over lanes 4, at 50 % of the
+// issue slots with 236 registers a thread.  Measured and not kept: tiles of 2
+// positions, chunks of 16 (580 to 628, and combine 38 -> 97 us), half the states a
+// lane on twice the warps.  h_prev is formed again rather than taken from
+// a h_prev = h - delta x B, which cancels where the decay is strong.
 template <typename Tin, typename Tout, int SPT, int SL, bool ODD>
 __global__ void __launch_bounds__(kBwdThreads, 2)
     k_sel_bwd(SelIn in, const Tin* __restrict__ dout, const float* __restrict__ hin,
@@ -1134,7 +1150,8 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
 
 // Forward ranges: as many as fill the machine once (kFwdBlocksPerSm blocks an
 // SM), each at least 32 positions; one (no state pass) where the channels fill
-// half of it by themselves.
+// half of it by themselves (2048 positions of 30 x 2048 channels: 715 us, 943 in two
+// ranges; of 27 x 2048, which do not: 715 and 732).
 void fwd_chunks(SelDims* d) {
   const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
@@ -1151,7 +1168,8 @@ void fwd_chunks(SelDims* d) {
 // forward; main: half the states a lane).  Ranges of whole chunks; their length
 // is the one with the shortest modelled time: each pass runs in waves of its
 // two blocks an SM, and a range costs the main pass about 24 issues an element,
-// the first 7.
+// the first 7.  Ranges of twice and of half that length: forward and backward of
+// 4 x 4096 x 1536 x 16 take 960 us (1009, 968), of 8192 x 1024 x 16 378 (614, 399).
 int bwd_main_tiles(const SelDims& d) {
   const int sl = d.N > 32 ? 8 : d.N > 16 ? 4 : 2;
   return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);

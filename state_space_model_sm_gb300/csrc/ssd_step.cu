@@ -13,8 +13,10 @@
 // streams whole 512-byte lines; each lane holds RB rows' states at once, and
 // they are the first thing loaded, so that the latency of what a row needs once
 // (softplus, decay, skip term, gate: computed by one lane of its segment and
-// broadcast) lies under theirs: 203 -> 178 us for 256 rows of 64 x 64 x 128
-// states (6.0 TB/s), five blocks an SM.
+// broadcast) lies under theirs; five blocks an SM.  171 us for 256 batch rows of
+// 64 x 64 x 128 states: 6.3 TB/s, 0.93 of a plain copy's rate (203 us before the
+// states were loaded first).  A single row's call is its launch: 2.3 us in a
+// captured graph.
 #include <cuda_bf16.h>
 
 #include "layer_math.cuh"
@@ -170,28 +172,32 @@ int launch_step(StepDims d, const StepPtrs& p, cudaStream_t s) {
 }
 
 // Lanes per row: the power of two that covers the row's V-wide vectors, 32 at
-// most (then the row is walked).  Rows per lane: 8, to have 128 bytes a lane
-// in flight; 2 where 8 would leave fewer than two warps per SM quarter.
+// most (then the row is walked).  Rows per lane: 8, to have 128 bytes a lane in
+// flight (171 us at 256 rows of 64 x 64 x 128 states, 240 with 2); 2 where 8 would
+// leave fewer than two warps per SM quarter (one row of 24 x 64 x 128: 2.3 us, 2.6
+// with 8).  4 in rows of four lanes, whatever the size (16 rows of 4096 x 16: 3.6 us,
+// 3.8 with 2), and in the selective form in place of 8 where a lane's access is 4
+// states, since it holds as many of A (256 rows of 4096 x 64: 127 us, and 138 with 8,
+// which spill; 64 rows of 4096 x 32: 12.8 and 20.3).
 template <typename Tin, typename Tout, bool SEL, int V>
 int pick_step(const StepDims& d, const StepPtrs& p, cudaStream_t s) {
   const int nv = (d.N + V - 1) / V;
   const int lpr = nv > 16 ? 32 : nv > 8 ? 16 : nv > 4 ? 8 : nv > 2 ? 4 : nv > 1 ? 2 : 1;
+  constexpr int many = SEL && V == 4 ? 4 : 8;
   const bool few = (int64_t)d.B * d.R * lpr < (int64_t)152 * 8 * 32 * 8;
   switch (lpr) {
     case 1: return launch_step<Tin, Tout, SEL, 1, V, 1>(d, p, s);
     case 2: return launch_step<Tin, Tout, SEL, 2, V, 2>(d, p, s);
-    case 4:
-      return few ? launch_step<Tin, Tout, SEL, 4, V, 2>(d, p, s)
-                 : launch_step<Tin, Tout, SEL, 4, V, 4>(d, p, s);
+    case 4: return launch_step<Tin, Tout, SEL, 4, V, 4>(d, p, s);
     case 8:
       return few ? launch_step<Tin, Tout, SEL, 8, V, 2>(d, p, s)
-                 : launch_step<Tin, Tout, SEL, 8, V, 8>(d, p, s);
+                 : launch_step<Tin, Tout, SEL, 8, V, many>(d, p, s);
     case 16:
       return few ? launch_step<Tin, Tout, SEL, 16, V, 2>(d, p, s)
-                 : launch_step<Tin, Tout, SEL, 16, V, 8>(d, p, s);
+                 : launch_step<Tin, Tout, SEL, 16, V, many>(d, p, s);
     default:
       return few ? launch_step<Tin, Tout, SEL, 32, V, 2>(d, p, s)
-                 : launch_step<Tin, Tout, SEL, 32, V, 8>(d, p, s);
+                 : launch_step<Tin, Tout, SEL, 32, V, many>(d, p, s);
   }
 }
 
