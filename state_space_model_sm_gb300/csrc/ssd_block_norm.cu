@@ -572,7 +572,8 @@ cudaError_t bn_ring(K kern, BnDims* d, size_t stage, size_t* bytes) {
   const size_t fit = (size_t)200 * 1024 / bn_ctas(d->nt) / stage;
   d->S = fit < 1 ? 1 : fit > kMaxStages ? kMaxStages : (int)fit;
   *bytes = d->S * stage;
-  return *bytes <= 48 * 1024
+  // (a launch may have 48 KB without being allowed more, the blocks' sums included)
+  return *bytes + sizeof(float2[2][16]) <= 48 * 1024
              ? cudaSuccess
              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
 }

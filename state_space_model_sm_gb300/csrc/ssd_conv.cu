@@ -547,7 +547,7 @@ int launch_bwd(ConvDims d, int K, const void* x, const float* w, const float* bi
   const dim3 grid(nparts, ceil_div(d.nvec, 32));
   constexpr int smem = 2 * 32 * kBwdWarps * Feed<Tin, V>::kBytes;
   auto go = [&](auto kern) {
-    if (smem > 32 * 1024)  // beside the 20 KB of sums
+    if (smem + 20 * 1024 > 48 * 1024)  // with the sums, 20 KB at most
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     SSD_LAUNCH("k_conv_bwd", s,
                kern<<<grid, 32 * kBwdWarps, smem, s>>>(

@@ -478,6 +478,15 @@ def test_block_norm_even_widths(cuda_lib, io, res, rows, F):
     test_block_norm_matches_oracle(cuda_lib, (rows, F, io, res, True, gates, 0.5))
 
 
+@pytest.mark.parametrize("io,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_block_norm_every_block_size(cuda_lib, io, res):
+    """Widths that fill blocks of 32 to 512 threads, one column fewer, and narrower rows:
+    every size of the rows' ring in shared memory."""
+    for nt in range(32, 513, 32):
+        for F in (16 * nt, 16 * nt - 1, 16 * nt - 248):
+            test_block_norm_matches_oracle(cuda_lib, (3, F, io, res, True, 3, 0.5))
+
+
 def test_block_norm_in_place_and_unaligned_rows(cuda_lib):
     import torch
     r = torch.randn(33, 64, device="cuda")
