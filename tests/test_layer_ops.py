@@ -89,6 +89,63 @@ def test_conv_matches_oracle(cuda_lib, case):
         close(k, v, r[k])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), "lowest"])
+@pytest.mark.parametrize("C,dtype", [(33, "bf16"), (64, "bf16"), (48, "f32"), (7, "f32")])
+def test_conv_padding_reaches_nothing(cuda_lib, C, dtype, value):
+    import torch
+    it, _ = types(dtype)
+    value = torch.finfo(it).min if value == "lowest" else value
+    g, T, lengths = np.random.default_rng(C), 150, [150, 0, 77, 1]
+    x, dy = (dev(g.standard_normal((4, T, C)), it) for _ in range(2))
+    w, init = dev(g.standard_normal((C, 4))), dev(g.standard_normal((4, 3, C)), it)
+    ln = dev(np.array(lengths), torch.int32)
+
+    def run(fill):
+        xp, dp = padded(x, lengths, fill), padded(dy, lengths, fill)
+        got = cuda_lib.causal_conv_bwd(xp, w, None, dp, init_state=init, lengths=ln)
+        got["y"], got["final"] = cuda_lib.causal_conv_fwd(xp, w, None, init_state=init, lengths=ln)
+        return got
+
+    zero, other = run(0.0), run(value)
+    assert all(torch.equal(zero[k], other[k]) for k in zero)
+    assert all(bool(torch.isfinite(v).all()) for v in other.values())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_empty_rows_of_a_decoding_step_reach_nothing(cuda_lib, dtype):
+    """Rows without a slot may hold anything: outputs 0, and no state is touched."""
+    import torch
+    it, _ = types(dtype)
+    g, nan = np.random.default_rng(3), float("nan")
+    slots = dev(np.array([2, -1, 0, 9, -7]), torch.int32)  # 9 is past the 4 states
+    live = [0, 2]
+
+    def rows(*shape):
+        t = dev(g.standard_normal((5,) + shape), it)
+        t[[1, 3, 4]] = nan
+        return t
+
+    def check(y, state, before):
+        assert bool((y[[1, 3, 4]] == 0).all()) and bool(torch.isfinite(y[live]).all())
+        assert torch.equal(state[[1, 3]], before[[1, 3]]) and bool(torch.isfinite(state).all())
+
+    A = dev(-np.exp(g.standard_normal((24, 16))))
+    state = dev(g.standard_normal((4, 24, 16)))
+    before = state.clone()
+    y = cuda_lib.selective_step(rows(24), rows(24), None, A, rows(1, 16), rows(1, 16), state,
+                                z=rows(24), slots=slots)
+    check(y, state, before)
+    state = dev(g.standard_normal((4, 3, 8, 16)))
+    before = state.clone()
+    y = cuda_lib.ssd_step(rows(3, 8), rows(3), None, A[0, :3].contiguous(), rows(1, 16),
+                          rows(1, 16), state, slots=slots)
+    check(y, state, before)
+    state = dev(g.standard_normal((4, 3, 24)), it)
+    before = state.clone()
+    y = cuda_lib.causal_conv_step(rows(24), state, dev(g.standard_normal((24, 4))), slots=slots)
+    check(y, state, before)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_conv_backward_under_load(cuda_lib, dtype):
     """At a size that keeps the memory system busy, where a copy read before it has
@@ -204,6 +261,40 @@ def test_scan_matches_oracle(cuda_lib, case):
     assert ("dz" in got) == gated and ("dinit_states" in got) == has_init
     for k, v in got.items():
         close(k, v, r[k])
+
+
+def padded(t, lengths, value):
+    """A copy of t (batch, seqlen, ..) with value from each row's length on."""
+    t = t.clone()
+    for b, n in enumerate(lengths):
+        t[b, n:] = value
+    return t
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), "lowest"])
+@pytest.mark.parametrize("T,D,N,dtype", [(70, 37, 16, "bf16"), (700, 64, 16, "bf16"),
+                                         (333, 30, 24, "f32")])
+def test_scan_padding_reaches_nothing(cuda_lib, T, D, N, dtype, value):
+    """Padded positions may hold anything: every output has the bits of zero padding."""
+    import torch
+    it, _ = types(dtype)
+    value = torch.finfo(it).min if value == "lowest" else value
+    lengths = [T, 0, T // 2 + 1, 1]
+    a, init, g = scan_inputs(T + D, 4, T, D, N, 1, it, True, True)
+    dout = dev(g.standard_normal((4, T, D)), it)
+    ln = dev(np.array(lengths), torch.int32)
+
+    def run(fill):
+        args = [padded(t, lengths, fill) if k in ("x", "dt", "B", "C", "z") else t
+                for k, t in zip(("x", "dt", "dt_bias", "A", "B", "C", "D", "z"), scan_dev(a, it))]
+        got = cuda_lib.selective_scan_bwd(*args, padded(dout, lengths, fill), init_states=dev(init),
+                                          lengths=ln)
+        got["out"], got["final"] = cuda_lib.selective_scan_fwd(*args, init_states=dev(init), lengths=ln)
+        return got
+
+    zero, other = run(0.0), run(value)
+    assert all(torch.equal(zero[k], other[k]) for k in zero)
+    assert all(bool(torch.isfinite(v).all()) for v in other.values())
 
 
 def test_scan_without_bias_skip_or_final_gradient(cuda_lib):
