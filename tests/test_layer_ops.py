@@ -649,3 +649,91 @@ def test_refusals(cuda_lib):
     with pytest.raises(cuda_lib.SSDError) as e:                       # bf16 residual, f32 layer
         cuda_lib.block_norm_fwd(r.bfloat16(), r, f)
     assert e.value.status == 2
+
+
+# ------------------------------------------------- tensors of more than 2^31 elements
+
+def test_step_of_a_cache_past_32_bits(cuda_lib):
+    """70000 slots of 4 x 64 x 128 states: the last slot's offset is past 2^31."""
+    import torch
+    g = np.random.default_rng(1)
+    state = torch.empty(70000, 4, 64, 128, device="cuda")
+    slots = dev(np.array([3, 69999]), torch.int32)
+    state[3] = state[69999] = dev(g.standard_normal((4, 64, 128)))
+    before = state[3].clone()
+
+    def twice(*shape):
+        t = dev(g.standard_normal((1,) + shape), torch.bfloat16)
+        return t.expand(2, *shape).contiguous()
+
+    y = cuda_lib.ssd_step(twice(4, 64), twice(4), None, dev(-np.ones(4)), twice(1, 128),
+                          twice(1, 128), state, slots=slots)
+    assert torch.equal(y[0], y[1]) and torch.equal(state[3], state[69999])
+    assert not torch.equal(state[3], before)
+
+
+def test_conv_past_32_bits(cuda_lib):
+    """The last positions of 1.2 M x 1792 inputs, against a call on them alone."""
+    import torch
+    T, C, tail = 1200000, 1792, 67
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.randn(1, T, C, generator=gen, device="cuda", dtype=torch.bfloat16)
+             for _ in range(2))
+    w = torch.randn(C, 4, generator=gen, device="cuda")
+    xt, dt = x[:, -tail:], dy[:, -tail:]
+    y, _ = cuda_lib.causal_conv_fwd(x, w)
+    yt, _ = cuda_lib.causal_conv_fwd(xt, w)
+    assert torch.equal(y[:, 3 - tail:], yt[:, 3:])
+    del y
+    dx = cuda_lib.causal_conv_bwd(x, w, None, dy)["dx"]
+    dxt = cuda_lib.causal_conv_bwd(xt, w, None, dt)["dx"]
+    assert torch.equal(dx[:, 3 - tail:], dxt[:, 3:])
+
+
+def test_scan_past_32_bits(cuda_lib):
+    """The last positions of 1.15 M x 1920 inputs, against a call that goes on from the
+    state before them.  Both round to bf16, from ranges cut at other places."""
+    import torch
+    T, D, N, tail = 1150000, 1920, 4, 96
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=gen, device="cuda", dtype=dtype)
+
+    x, dt, dout = rand(1, T, D), rand(1, T, D), rand(1, T, D)
+    B, C = rand(1, T, 1, N), rand(1, T, 1, N)
+    A, bias = -torch.rand(D, N, generator=gen, device="cuda") - 0.1, torch.full((D,), -3.0, device="cuda")
+    head, rest = T - tail, slice(T - tail, None)
+    _, state = cuda_lib.selective_scan_fwd(x[:, :head], dt[:, :head], bias, A, B[:, :head], C[:, :head])
+    part = (x[:, rest], dt[:, rest], bias, A, B[:, rest], C[:, rest])
+
+    def same(a, b):
+        a, b = a.double(), b.double()
+        assert bool(torch.isfinite(a).all()) and (a - b).norm() <= 2.0 ** -8 * b.norm()
+
+    out, fin = cuda_lib.selective_scan_fwd(x, dt, bias, A, B, C)
+    want, wfin = cuda_lib.selective_scan_fwd(*part, init_states=state)
+    same(out[:, rest], want)
+    same(fin, wfin)
+    del out
+    got = cuda_lib.selective_scan_bwd(x, dt, bias, A, B, C, None, None, dout)
+    want = cuda_lib.selective_scan_bwd(*part, None, None, dout[:, rest], init_states=state)
+    for k in ("dx", "ddt", "dB", "dC"):
+        same(got[k][:, rest], want[k])
+
+
+def test_block_norm_past_32_bits(cuda_lib):
+    """The last rows of 540000 x 4096, against a call on them alone (rows are independent)."""
+    import torch
+    rows, F, tail = 540000, 4096, 5
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    r, o, dh = (torch.randn(rows, F, generator=gen, device="cuda", dtype=torch.bfloat16)
+                for _ in range(3))
+    w, v = (torch.rand(F, generator=gen, device="cuda") + 0.5 for _ in range(2))
+    rn, h = cuda_lib.block_norm_fwd(r, o, w, v)
+    rt, ht = cuda_lib.block_norm_fwd(r[-tail:], o[-tail:], w, v)
+    assert torch.equal(rn[-tail:], rt) and torch.equal(h[-tail:], ht)
+    del rn, h
+    got = cuda_lib.block_norm_bwd(r, o, w, v, None, dh)
+    want = cuda_lib.block_norm_bwd(r[-tail:], o[-tail:], w, v, None, dh[-tail:])
+    assert all(torch.equal(got[k][-tail:], want[k]) for k in ("dresidual", "do"))
