@@ -302,6 +302,8 @@ struct PassSmem {
 // 59 % of the issue slots): 82 us for 4 x 4096 x 1536 x 16 elements and 374 us for
 // 65536 x 2048 x 16, 5.0 and 5.7 elements a ps.  With OUT (the product with C, the
 // gate, the store) by issue: 58 %, 50 % of the exponentials' slots; 116 and 550 us.
+// Where few warps are resident (short inputs) each waits for its own chain, about 4
+// clocks an instruction, so ranges are cut short there.
 template <typename Tin, typename Tout, int SPT, int SL, bool OUT, bool ODD>
 __global__ void __launch_bounds__(kFwdThreads, kFwdBlocksPerSm)
     k_sel_scan(SelIn in, const float* __restrict__ init, float* __restrict__ hin,
@@ -1148,19 +1150,21 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
   return SSD_OK;
 }
 
-// Forward ranges: as many as fill the machine once (kFwdBlocksPerSm blocks an
-// SM), each at least 32 positions; one (no state pass) where the channels fill
-// half of it by themselves (2048 positions of 30 x 2048 channels: 715 us, 943 in two
-// ranges; of 27 x 2048, which do not: 715 and 732).
+// Forward ranges of whole stages: as many as fill the machine once
+// (kFwdBlocksPerSm blocks an SM); one (no state pass) where the channels fill half
+// of it by themselves (2048 positions of 30 x 2048 channels: 715 us, 943 in two
+// ranges; of 27 x 2048, which do not: 715 and 732), or up to kOneRange positions
+// (1536 channels: 16 positions in one range take 10.3 us, in ranges of a stage 12.6;
+// 24 12.4 and 12.4; 32 14.4 and 12.4).  Short ranges pay where the machine is not
+// full: 4 x 333 x 300 takes 22.6 us, 26.7 with ranges of 16 positions, 36.9 with 32.
+constexpr int kOneRange = 24;
 void fwd_chunks(SelDims* d) {
   const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   const int64_t blocks = (int64_t)d->B * d->G * d->ctiles;
   int64_t nc = kFwdBlocksPerSm * 152 / blocks;
-  const int64_t most = ceil_div(d->T, 32);
-  if (nc > most) nc = most;
-  if (nc < 2) nc = 1;
-  d->L = ceil_div(ceil_div(d->T, nc), 32) * 32;
+  if (nc < 2 || d->T <= kOneRange) nc = 1;
+  d->L = ceil_div(ceil_div(d->T, nc), kStage) * kStage;
   d->nc = d->nh = ceil_div(d->T, d->L);
 }
 
