@@ -5,8 +5,9 @@ decoding, and the residual / norm step between layers.
 Bindings of the same names as ``include/ssd.h`` declares (without the prefix):
 they check the tensors, allocate outputs and workspace, and pass pointers and
 the current stream.  Inputs are float32 or bfloat16 CUDA tensors; parameters
-(weights, biases, A, D) and scan states are float32.  Every call is
-asynchronous and its results are ordered on the current stream.
+(weights, biases, A, D) and scan states are float32.  Tensors live on the current
+device (those of another one are refused).  Every call is asynchronous and its
+results are ordered on the current stream.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ _CODE = {torch.float32: 0, torch.bfloat16: 1}  # ssd_dtype
 _F32, _I32 = torch.float32, torch.int32
 _empty, _empty_like = torch.empty, torch.empty_like  # (Tensor.new_empty takes twice as long)
 _stream = torch._C._cuda_getCurrentRawStream  # of a device index; no Stream object
+_current_device = torch._C._cuda_getDevice
 _lib = None
 
 
@@ -42,14 +44,23 @@ def _code(dtype):
     return c
 
 
-def _lead(t, name, ndim):
-    """Index of the device of the call's first tensor, whose rank is checked."""
+def _device(t):
+    """Index of t's device, which has to be the current one: the library launches
+    there, whatever device the stream and the addresses are of."""
     dev = t.get_device()
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got {tuple(t.shape)}")
     if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
+    if dev != _current_device():
+        raise ValueError(f"tensors live on cuda:{dev}, but the current device is "
+                         f"cuda:{_current_device()}")
     return dev
+
+
+def _lead(t, name, ndim):
+    """Index of the device of the call's first tensor, whose rank is checked."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got {tuple(t.shape)}")
+    return _device(t)
 
 
 def _wrong(t, name, shape, dtype, device):
@@ -212,7 +223,8 @@ def causal_conv_step(x, state, w, bias=None, slots=None, silu: bool = True, out_
     slots (batch,) int32 names each row's state; a negative one marks an empty
     row, whose output is 0."""
     lib, xs, ws, ss, xd, dev = _lib, x.shape, w.shape, state.shape, x.dtype, x.get_device()
-    if (lib is not None and dev >= 0 and len(xs) == 2 and len(ws) == 2 and xd in _CODE
+    if (lib is not None and dev >= 0 and dev == _current_device()
+            and len(xs) == 2 and len(ws) == 2 and xd in _CODE
             and out_dtype is None and y is None and x.is_contiguous()
             and ws[0] == xs[1] and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
             and ss == (ss[0], ws[1] - 1, xs[1]) and state.dtype is xd
@@ -334,7 +346,8 @@ def selective_step(x, dt, dt_bias, A, B, C, state, D=None, z=None, slots=None, o
     (batch, channels); B, C (batch, ngroups, dstate); state (nslots, channels,
     dstate) float32, updated in place; slots as in ``causal_conv_step``."""
     lib, xs, bs, ss, xd, dev = _lib, x.shape, B.shape, state.shape, x.dtype, x.get_device()
-    if (lib is not None and dev >= 0 and len(xs) == 2 and len(bs) == 3 and xd in _CODE
+    if (lib is not None and dev >= 0 and dev == _current_device()
+            and len(xs) == 2 and len(bs) == 3 and xd in _CODE
             and out_dtype is None and y is None and x.is_contiguous()
             and dt.shape == xs and dt.dtype is xd and dt.get_device() == dev and dt.is_contiguous()
             and bs[0] == xs[0] and B.dtype is xd and B.get_device() == dev and B.is_contiguous()
@@ -378,7 +391,8 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
     state (nslots, nheads, headdim, dstate) float32, the state updated in place;
     slots as in ``causal_conv_step``.  y is in ``out_dtype`` (x's type)."""
     lib, xs, bs, ss, xd, dev = _lib, x.shape, B.shape, state.shape, x.dtype, x.get_device()
-    if (lib is not None and dev >= 0 and len(xs) == 3 and len(bs) == 3 and xd in _CODE
+    if (lib is not None and dev >= 0 and dev == _current_device()
+            and len(xs) == 3 and len(bs) == 3 and xd in _CODE
             and out_dtype is None and y is None and x.is_contiguous()
             and dt.shape == xs[:2] and dt.dtype is xd and dt.get_device() == dev
             and dt.is_contiguous()
@@ -427,9 +441,10 @@ def ssd_step(x, dt, dt_bias, A, B, C, state, D=None, slots=None, out_dtype=None,
 # ------------------------------------------------------------------ block norm
 
 def _bn_inputs(residual, o, w_pre, w_post, gate, scale, eps):
-    dev, rshape = residual.get_device(), residual.shape
-    if dev < 0 or len(rshape) < 1:
+    rshape = residual.shape
+    if len(rshape) < 1:
         raise ValueError("residual must be a CUDA tensor (..., features)")
+    dev = _device(residual)
     F = rshape[-1]
     rows = residual.numel() // F if F else 0
     rd, od, ng, gp = residual.dtype, o.dtype, 0, None
@@ -457,7 +472,8 @@ def block_norm_fwd(residual, o, w_pre, w_post=None, gate=None, scale: float = 1.
     ``residual`` and h may be ``o`` (in place)."""
     lib, rs, rd, od, dev = _lib, residual.shape, residual.dtype, o.dtype, residual.get_device()
     n = len(rs)
-    if (lib is not None and dev >= 0 and n > 0 and rs[-1] > 0 and rd in _CODE and od in _CODE
+    if (lib is not None and dev >= 0 and dev == _current_device() and n > 0 and rs[-1] > 0
+            and rd in _CODE and od in _CODE
             and residual.is_contiguous() and residual_out is None and h is None
             and o.shape == rs and o.get_device() == dev and o.is_contiguous()
             and w_pre.shape == rs[n - 1:] and w_pre.dtype is _F32 and w_pre.get_device() == dev
