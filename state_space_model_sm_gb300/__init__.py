@@ -47,6 +47,18 @@ def make_shape(batch, seqlen, nheads, headdim, dstate, ngroups, chunk_size, in_d
                          out_dtype)
 
 
+def _stream(device) -> int:
+    """Handle of the current stream of the tensors' device, which has to be the current
+    one: the library launches there, whatever device stream and addresses are of."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"tensors live on {device}, but the current device is cuda:{current}")
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -153,7 +165,7 @@ def ssd_fwd(x, dt, dt_bias, A, B, C, D=None, chunk_size: int = 256, init_states=
     if ws_bytes == 0:
         raise ValueError("invalid SSD shape")
     ws = _workspace(ws_bytes, x.device, workspace)
-    stream = torch.cuda.current_stream(x.device).cuda_stream
+    stream = _stream(x.device)
     st = lib.ssd_fwd(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B),
                      _ptr(C), _ptr(D), _ptr(init_states), _ptr(y),
                      _ptr(final_states) if return_final_states else None, _ptr(ws),
@@ -192,7 +204,7 @@ def ssd_bwd(x, dt, dt_bias, A, B, C, D, chunk_size: int, init_states, dy, dfinal
     if ws_bytes == 0:
         raise ValueError("invalid SSD shape")
     ws = _workspace(ws_bytes, x.device, workspace)
-    stream = torch.cuda.current_stream(x.device).cuda_stream
+    stream = _stream(x.device)
     st = lib.ssd_bwd(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B),
                      _ptr(C), _ptr(D), _ptr(init_states), _ptr(dy), _ptr(dfinal_states),
                      _ptr(out["dx"]), _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]),
@@ -219,7 +231,7 @@ def ssd_final_state(x, dt, dt_bias, A, B, chunk_size: int = 256, init_states=Non
         final_states = torch.empty((Bt, H, P, N), dtype=torch.float32, device=x.device)
     _check(final_states, "final_states", (Bt, H, P, N), torch.float32, x.device)
     ws = _workspace(lib.ssd_fwd_workspace_size(ctypes.byref(shape)), x.device, workspace)
-    stream = torch.cuda.current_stream(x.device).cuda_stream
+    stream = _stream(x.device)
     st = lib.ssd_fwd_final_state(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A),
                                  _ptr(B), _ptr(init_states), _ptr(final_states), _ptr(ws),
                                  ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream))
@@ -242,7 +254,7 @@ def ssd_dinit(x, dt, dt_bias, A, C, dy, chunk_size: int = 256, dfinal_states=Non
         dinit_states = torch.empty((Bt, H, P, N), dtype=torch.float32, device=x.device)
     _check(dinit_states, "dinit_states", (Bt, H, P, N), torch.float32, x.device)
     ws = _workspace(lib.ssd_fwd_workspace_size(ctypes.byref(shape)), x.device, workspace)
-    stream = torch.cuda.current_stream(x.device).cuda_stream
+    stream = _stream(x.device)
     st = lib.ssd_bwd_dinit(ctypes.byref(shape), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(C),
                            _ptr(dy), _ptr(dfinal_states), _ptr(dinit_states), _ptr(ws),
                            ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream))
@@ -284,7 +296,7 @@ def gated_norm_fwd(y, z, w, group_size: int, eps: float = 1e-5, out_dtype=None,
     if return_rstd and rstd is None:
         rstd = torch.empty((shape.rows, max(D // max(group_size, 1), 1)), dtype=torch.float32,
                            device=y.device)
-    stream = torch.cuda.current_stream(y.device).cuda_stream
+    stream = _stream(y.device)
     st = lib.ssd_gated_norm_fwd(ctypes.byref(shape), _ptr(y), _ptr(z), _ptr(w), _ptr(out),
                                 _ptr(rstd) if return_rstd else None, ctypes.c_void_p(stream))
     if st != 0:
@@ -318,7 +330,7 @@ def gated_norm_bwd(y, z, w, dout, group_size: int, eps: float = 1e-5, rstd=None,
     if nbytes == 0:
         raise SSDError("ssd_gated_norm_workspace_size", 2)
     ws = _workspace(nbytes, y.device, workspace)
-    stream = torch.cuda.current_stream(y.device).cuda_stream
+    stream = _stream(y.device)
     st = lib.ssd_gated_norm_bwd(ctypes.byref(shape), _ptr(y), _ptr(z), _ptr(w), _ptr(rstd),
                                 _ptr(dout), _ptr(out["dy"]), _ptr(out["dz"]), _ptr(out["dw"]),
                                 _ptr(ws), ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream))
@@ -342,7 +354,7 @@ def segment_decay(dt, dt_bias, A):
     out = torch.empty((Bt, H), dtype=torch.float32, device=dt.device)
     shape = make_shape(Bt, T, H, 1, 1, 1, 1, _dtype_code(dt.dtype), SSD_F32)
     ws = _workspace(lib.ssd_segment_decay_workspace_size(ctypes.byref(shape)), dt.device, None)
-    stream = torch.cuda.current_stream(dt.device).cuda_stream
+    stream = _stream(dt.device)
     st = lib.ssd_segment_decay(ctypes.byref(shape), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(out),
                                _ptr(ws), ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream))
     if st != 0:
@@ -366,7 +378,7 @@ def state_scan(decays, states, rank: int, direction: int):
     bh = states.shape[1] * states.shape[2]
     pn = states.shape[3] * states.shape[4]
     out = torch.empty(states.shape[1:], dtype=torch.float32, device=states.device)
-    stream = torch.cuda.current_stream(states.device).cuda_stream
+    stream = _stream(states.device)
     st = lib.ssd_state_scan(int(R), int(rank), int(direction), int(bh), int(pn), _ptr(decays),
                             _ptr(states), _ptr(out), ctypes.c_void_p(stream))
     if st != 0:

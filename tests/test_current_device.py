@@ -72,3 +72,37 @@ def test_layer_operators(monkeypatch, name, current):
         with pytest.raises(ValueError, match="cuda:1.*current device.*cuda:0"):
             call()
         assert lib.calls == []
+
+
+def test_stream_of_a_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1.*current device.*cuda:0"):
+        ssd._stream(torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="CUDA device"):
+        ssd._stream(torch.device("cpu"))
+
+
+@pytest.mark.gpu
+def test_scan_and_norm(cuda_lib, monkeypatch):
+    """Tensors of cuda:0 while the current device says that it is another (here it is
+    not, so the launches that are to be refused would be sound)."""
+    z = lambda *s: torch.zeros(*s, device="cuda:0")  # noqa: E731
+    x, dt, h, B, s = z(1, 64, 2, 16), z(1, 64, 2), z(2), z(1, 64, 1, 16), z(1, 2, 16, 16)
+    y, w = z(8, 64), z(64)
+    calls = (lambda: ssd.ssd_fwd(x, dt, h, h, B, B, h, 64),
+             lambda: ssd.ssd_bwd(x, dt, h, h, B, B, h, 64, None, x),
+             lambda: ssd.ssd_final_state(x, dt, h, h, B, 64),
+             lambda: ssd.ssd_dinit(x, dt, h, h, B, x, 64),
+             lambda: ssd.gated_norm_fwd(y, y, w, 64),
+             lambda: ssd.gated_norm_bwd(y, y, w, y, 64),
+             lambda: ssd.segment_decay(dt, h, h),
+             lambda: ssd.state_scan(z(2, 1, 2), torch.stack([s, s]), 0, 0))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    before = ssd.launch_count()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 7)
+    for call in calls:
+        with pytest.raises(ValueError, match="cuda:0.*current device.*cuda:7"):
+            call()
+    assert ssd.launch_count() == before
