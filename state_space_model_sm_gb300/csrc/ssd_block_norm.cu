@@ -450,51 +450,58 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
 // dw_pre, dw_post and the gate rows' gradients from the blocks' parts in a fixed
 // order, 32 columns a block, its 16 warps taking every 16th block's part.
-// blockIdx.y = 0: dw_pre, 1: dw_post, 2 + g: gate row g.
+// Results: 0 is dw_pre, 1 dw_post, 2 + g gate row g.  blockIdx.y is a block's first;
+// where there are more than a grid has rows of blocks, it goes on a grid further.
+constexpr int kMaxGridY = 65535;
+
 __global__ void __launch_bounds__(512)
     k_block_norm_dw(const float* __restrict__ part, const float* __restrict__ w_post,
                     const float* __restrict__ gate, float* __restrict__ dw_pre,
                     float* __restrict__ dw_post, float* __restrict__ dgate, BnDims d) {
   __shared__ float red[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane, which = blockIdx.y, g = which - 2;
+  const int c = blockIdx.x * 32 + lane;
   griddep_wait();
-  float* const dst = which == 0 ? dw_pre : which == 1 ? dw_post : dgate + (int64_t)g * d.F;
-  if (which < 2 && !dst) return;
   const float* pp = part + (int64_t)d.grid * d.F;
-  float a = 0.f;
-  if (c < d.F) {
-    if (which == 0) {
+  for (int which = blockIdx.y; which < 2 + d.ng; which += gridDim.y) {
+    const int g = which - 2;
+    float* const dst = which == 0 ? dw_pre : which == 1 ? dw_post : dgate + (int64_t)g * d.F;
+    if (!dst) continue;  // no dw_post
+    float a = 0.f;
+    if (c < d.F) {
+      if (which == 0) {
 #pragma unroll 8
-      for (int k = warp; k < d.grid; k += 16) a += part[(int64_t)k * d.F + c];
-    } else if (which == 1 && d.ng <= 16) {  // gate row by gate row
-      for (int i = 0; i < (d.ng ? d.ng : 1); ++i) {
-        const int k0 = i * d.gs / d.R, k1 = ((i + 1) * d.gs - 1) / d.R + 1;
-        float p = 0.f;
+        for (int k = warp; k < d.grid; k += 16) a += part[(int64_t)k * d.F + c];
+      } else if (which == 1 && d.ng <= 16) {  // gate row by gate row
+        for (int i = 0; i < (d.ng ? d.ng : 1); ++i) {
+          const int k0 = i * d.gs / d.R, k1 = ((i + 1) * d.gs - 1) / d.R + 1;
+          float p = 0.f;
 #pragma unroll 8
-        for (int k = k0 + warp; k < k1; k += 16) p += pp[(int64_t)(k + i) * d.F + c];
-        a = fmaf(gate ? gate[(int64_t)i * d.F + c] : 1.f, p, a);
+          for (int k = k0 + warp; k < k1; k += 16) p += pp[(int64_t)(k + i) * d.F + c];
+          a = fmaf(gate ? gate[(int64_t)i * d.F + c] : 1.f, p, a);
+        }
+      } else if (which == 1) {  // block by block
+        for (int k = warp; k < d.grid; k += 16) {
+          const int g0 = k * d.R / d.gs, g1 = (min((k + 1) * d.R, d.rows) - 1) / d.gs;
+          for (int i = g0; i <= g1; ++i)
+            a = fmaf(gate[(int64_t)i * d.F + c], pp[(int64_t)(k + i) * d.F + c], a);
+        }
+      } else {
+        const int k0 = (int)((int64_t)g * d.gs / d.R);
+        const int k1 = (int)((((int64_t)g + 1) * d.gs - 1) / d.R) + 1;
+#pragma unroll 8
+        for (int k = k0 + warp; k < k1; k += 16) a += pp[(int64_t)(k + g) * d.F + c];
       }
-    } else if (which == 1) {  // block by block
-      for (int k = warp; k < d.grid; k += 16) {
-        const int g0 = k * d.R / d.gs, g1 = (min((k + 1) * d.R, d.rows) - 1) / d.gs;
-        for (int i = g0; i <= g1; ++i)
-          a = fmaf(gate[(int64_t)i * d.F + c], pp[(int64_t)(k + i) * d.F + c], a);
-      }
-    } else {
-      const int k0 = (int)((int64_t)g * d.gs / d.R);
-      const int k1 = (int)((((int64_t)g + 1) * d.gs - 1) / d.R) + 1;
-#pragma unroll 8
-      for (int k = k0 + warp; k < k1; k += 16) a += pp[(int64_t)(k + g) * d.F + c];
     }
-  }
-  red[warp][lane] = a;
-  __syncthreads();
-  if (warp == 0 && c < d.F) {
-    float s = 0.f;
+    red[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && c < d.F) {
+      float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += red[k][lane];
-    dst[c] = which == 0 ? s : d.scale * (which == 1 || !w_post ? s : w_post[c] * s);
+      for (int k = 0; k < 16; ++k) s += red[k][lane];
+      dst[c] = which == 0 ? s : d.scale * (which == 1 || !w_post ? s : w_post[c] * s);
+    }
+    if (which + (int64_t)gridDim.y < 2 + d.ng) __syncthreads();  // before the sums' next use
   }
 }
 
@@ -693,7 +700,6 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
   }
   if (!workspace || off(workspace, 16) || workspace_bytes < bn_bwd_floats(d) * sizeof(float))
     return SSD_ERR_WORKSPACE;
-  if (d.ng + 2 > 65535) return SSD_ERR_UNSUPPORTED;
   const auto fits = [&](int w) {
     return d.F % w == 0 && vec_ok(o, d.F, ie, w) && vec_ok(dh, d.F, ie, w) &&
            vec_ok(d_o, d.F, ie, w) && vec_ok(residual, d.F, re, w) &&
@@ -706,7 +712,7 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
                  static_cast<float*>(workspace)};
   const int e = bn_run(d, shape, p, vec, true, s);
   if (e != SSD_OK) return e;
-  const dim3 grid(ceil_div(d.F, 32), 2 + d.ng);
+  const dim3 grid(ceil_div(d.F, 32), 2 + d.ng < kMaxGridY ? 2 + d.ng : kMaxGridY);
   cudaError_t le;
   SSD_LAUNCH("k_block_norm_dw", s, le = launch_pdl(k_block_norm_dw, grid, 512, 0, s, p.part, w_post,
                                                    gate, dw_pre, dw_post, dgate, d));

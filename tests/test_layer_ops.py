@@ -577,6 +577,14 @@ def test_block_norm_every_block_size(cuda_lib, io, res):
         for F in (16 * nt, 16 * nt - 1, 16 * nt - 248):
             test_block_norm_matches_oracle(cuda_lib, (3, F, io, res, True, 3, 0.5))
 
+@pytest.mark.parametrize("rows,F,gates,io,post", [
+    (70000, 5, 70000, "bf16", True),     # a gate row per row, more than a grid has block rows
+    (140000, 8, 70000, "f32", False),    # two rows a gate row
+    (65534, 4, 65534, "bf16", True),     # the first count past what one grid covers
+    (65533, 4, 65533, "bf16", True)])
+def test_block_norm_many_gate_rows(cuda_lib, rows, F, gates, io, post):
+    test_block_norm_matches_oracle(cuda_lib, (rows, F, io, "f32", post, gates, 0.5))
+
 
 def test_block_norm_in_place_and_unaligned_rows(cuda_lib):
     import torch
