@@ -476,7 +476,8 @@ int ssd_step(const ssd_shape* shape, const void* x, const void* dt, const float*
  * w_post (features) f32; gate (ngates, features) f32, row i using gate row
  * i / (rows / ngates) (one row: shared by all; one per sequence; one per row),
  * or NULL with ngates 0.  h is formed from r' before r' is rounded.
- * features <= 8192; rows a multiple of ngates; res_dtype f32 when in_dtype is.
+ * rows < 2^30, features <= 8192; rows a multiple of ngates; res_dtype f32 when
+ * in_dtype is.
  * r' may be written over r and h over o. */
 typedef struct {
   int64_t rows, features, ngates;

@@ -516,8 +516,8 @@ int bn_dims(const ssd_block_norm_shape* s, BnDims* d) {
   if ((s->in_dtype != SSD_F32 && s->in_dtype != SSD_BF16) ||
       (s->res_dtype != SSD_F32 && s->res_dtype != SSD_BF16))
     return SSD_ERR_INVALID_ARG;
-  if (s->rows >= (1 << 30) || (s->ngates && s->rows % s->ngates != 0)) return SSD_ERR_INVALID_ARG;
-  if (s->features > 8192) return SSD_ERR_UNSUPPORTED;
+  if (s->ngates && s->rows % s->ngates != 0) return SSD_ERR_INVALID_ARG;
+  if (s->rows >= (1 << 30) || s->features > 8192) return SSD_ERR_UNSUPPORTED;
   if (s->in_dtype == SSD_F32 && s->res_dtype == SSD_BF16) return SSD_ERR_UNSUPPORTED;
   d->rows = (int)s->rows, d->F = (int)s->features, d->ng = (int)s->ngates;
   d->gs = d->ng && d->rows ? d->rows / d->ng : (d->rows ? d->rows : 1);

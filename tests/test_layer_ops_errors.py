@@ -151,3 +151,14 @@ def test_block_norm_pointers(lib):
     assert lib.ssd_block_norm_bwd(s, *bwd, None, BIG, None) == WORKSPACE
     assert lib.ssd_block_norm_bwd(s, *bwd[:10], D, None, D, BIG, None) == INVALID  # dw_post alone
     assert lib.ssd_block_norm_fwd(norm(rows=0), *[None] * 7, None) == OK
+
+
+def test_block_norm_row_limit(lib):
+    """Too many rows is a limit, a gate that does not divide them a wrong argument."""
+    for s, g, code in ((norm(rows=1 << 30), None, UNSUPPORTED),
+                       (norm(rows=1 << 30, ngates=3), D, INVALID)):
+        assert lib.ssd_block_norm_fwd(s, D, D, D, None, g, D, D, None) == code
+        assert lib.ssd_block_norm_bwd(s, D, D, D, None, g, D, None, D, D, D, None, g, D, BIG,
+                                      None) == code
+        assert lib.ssd_block_norm_workspace_size(s) == 0
+    assert lib.ssd_block_norm_workspace_size(norm(rows=(1 << 30) - 1)) > 0
