@@ -1258,6 +1258,7 @@ int sel_forward(const SelDims& d, const SelIn& in, const float* init, void* out,
     SSD_LAUNCH("k_sel_chunk_state", s,
                kstate<<<sel_grid(d, d.nc - 1), kFwdThreads, ms, s>>>(in, nullptr, hin, sumd,
                                                                      nullptr, nullptr, d));
+    if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;  // no states to go on from
     if (combine(d, in.A, init, nullptr, hin, nullptr, sumd, nullptr, s) != cudaSuccess)
       return SSD_ERR_CUDA;
     cudaError_t e;
@@ -1288,6 +1289,7 @@ int sel_backward(const SelDims& d, const SelIn& in, const float* init, const voi
   if (allow_smem(kstate, ms) != cudaSuccess) return SSD_ERR_CUDA;
   SSD_LAUNCH("k_sel_state", s, kstate<<<sel_grid(d, d.nc), kFwdThreads, ms, s>>>(
                                    in, go, w.hin, w.gin, w.sumd, w.sumg, d));
+  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;  // no states to go on from
   if (combine(d, in.A, init, dfinal, w.hin, w.gin, w.sumd, w.sumg, s) != cudaSuccess)
     return SSD_ERR_CUDA;
   SelDims m = d;

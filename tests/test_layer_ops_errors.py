@@ -162,3 +162,21 @@ def test_block_norm_row_limit(lib):
                                       None) == code
         assert lib.ssd_block_norm_workspace_size(s) == 0
     assert lib.ssd_block_norm_workspace_size(norm(rows=(1 << 30) - 1)) > 0
+
+
+@pytest.mark.parametrize("call", ["forward", "backward"])
+def test_scan_stops_at_a_refused_launch(lib, call):
+    """Without a GPU every launch is refused: the scan's first pass is the only one
+    tried, since the others would read what it has not written."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the stand-in addresses must never reach a GPU")
+    s = sel(seqlen=4096, dstate=64)  # several ranges; no pass needs more than 48 KB of shared memory
+    before = lib.ssd_launch_count()
+    if call == "forward":
+        st = lib.ssd_selective_scan_fwd(s, D, D, None, D, D, D, None, None, None, None, D, None, D,
+                                        BIG, None)
+    else:
+        st = lib.ssd_selective_scan_bwd(s, D, D, None, D, D, D, None, None, None, None, D, None, D,
+                                        D, D, D, D, None, None, None, None, D, BIG, None)
+    assert st == 4 and lib.ssd_launch_count() == before + 1  # SSD_ERR_CUDA
