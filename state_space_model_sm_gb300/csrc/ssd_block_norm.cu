@@ -305,12 +305,13 @@ __device__ __forceinline__ void load_gw(float2 (&gw)[C::P2], const float* w_post
   for (int i = 0; i < C::P2; ++i) gw[i] = mul2(gw[i], mul2(t[i], f2(d.scale)));
 }
 
+// rout may be r and h may be o: a thread reads its columns of a row before it writes
+// them, and nothing else does either, so these four are not __restrict__.
 template <typename Tio, typename Tres, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
-    k_block_norm_fwd(const Tres* __restrict__ r, const Tio* __restrict__ o,
-                     const float* __restrict__ w_pre, const float* __restrict__ w_post,
-                     const float* __restrict__ gate, Tres* __restrict__ rout, Tio* __restrict__ h,
-                     BnDims d) {
+    k_block_norm_fwd(const Tres* r, const Tio* o, const float* __restrict__ w_pre,
+                     const float* __restrict__ w_post, const float* __restrict__ gate, Tres* rout,
+                     Tio* h, BnDims d) {
   using C = Cols<VEC, EPT, FULL>;
   constexpr int P2 = C::P2;
   __shared__ float2 red[2][16];

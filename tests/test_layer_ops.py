@@ -602,6 +602,23 @@ def test_block_norm_in_place_and_unaligned_rows(cuda_lib):
     assert a is r and b is o and torch.equal(r, rn) and torch.equal(o, h)
 
 
+@pytest.mark.parametrize("io,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,F", [(1000, 1001), (500, 3001), (500, 8191), (700, 2048), (500, 4100)])
+def test_block_norm_in_place(cuda_lib, rows, F, io, res):
+    """Several rows a block, in every way that rows are read: 4, 8 and 16 single columns
+    a thread, whole pieces, and pieces with a remainder.  The bits of the call with
+    outputs of its own."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(rows + F)
+    r, o = (torch.randn(rows, F, generator=g, device="cuda").to(types(t)[0]) for t in (res, io))
+    w, v = (torch.rand(F, generator=g, device="cuda") + 0.5 for _ in range(2))
+    gate = torch.randn(5, F, generator=g, device="cuda")
+    want = cuda_lib.block_norm_fwd(r, o, w, v, gate, scale=0.5)
+    got = cuda_lib.block_norm_fwd(r, o, w, v, gate, scale=0.5, residual_out=r, h=o)
+    assert got[0] is r and got[1] is o
+    assert torch.equal(r, want[0]) and torch.equal(o, want[1])
+
+
 def test_block_norm_zero_rows(cuda_lib):
     import torch
     r, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
