@@ -421,9 +421,10 @@ int ssd_causal_conv_step(const ssd_conv_shape* shape, const void* x, void* state
  * in_dtype; dt_bias, D (channels) f32 or NULL; A (channels, dstate) f32;
  * init_states, final_states (batch, channels, dstate) f32 or NULL; out (batch,
  * seqlen, channels) out_dtype.  channels a multiple of ngroups, dstate <= 64
- * (<= 256 in ssd_selective_step), seqlen at most 2^21, batch < 65536; the
- * backward takes batch * seqlen * ngroups up to 2^31.  Workspace of the size
- * query's bytes (0 for a rejected shape), 16-byte aligned, caller-owned. */
+ * (<= 256 in ssd_selective_step), seqlen < 2^30, batch < 65536; the backward
+ * takes seqlen up to 134215680 (65535 ranges of 64 chunks of 32 positions) and
+ * batch * seqlen * ngroups up to 2^31.  Workspace of the size query's bytes (0 for
+ * a rejected shape), 16-byte aligned, caller-owned. */
 typedef struct {
   int64_t batch, seqlen, channels, dstate, ngroups;
   int64_t z_row_stride, b_row_stride, c_row_stride;

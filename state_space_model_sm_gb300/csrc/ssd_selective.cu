@@ -1158,7 +1158,7 @@ int sel_dims(const ssd_selective_shape* s, SelDims* d) {
 // 24 12.4 and 12.4; 32 14.4 and 12.4).  Short ranges pay where the machine is not
 // full: 4 x 333 x 300 takes 22.6 us, 26.7 with ranges of 16 positions, 36.9 with 32.
 constexpr int kOneRange = 24;
-void fwd_chunks(SelDims* d) {
+int fwd_chunks(SelDims* d) {
   const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   const int64_t blocks = (int64_t)d->B * d->G * d->ctiles;
@@ -1166,6 +1166,7 @@ void fwd_chunks(SelDims* d) {
   if (nc < 2 || d->T <= kOneRange) nc = 1;
   d->L = ceil_div(ceil_div(d->T, nc), kStage) * kStage;
   d->nc = d->nh = ceil_div(d->T, d->L);
+  return blocks <= 0x7fffffff ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
 // Backward: the two passes have their own channel tiles (first: as the
@@ -1174,19 +1175,23 @@ void fwd_chunks(SelDims* d) {
 // two blocks an SM, and a range costs the main pass about 24 issues an element,
 // the first 7.  Ranges of twice and of half that length: forward and backward of
 // 4 x 4096 x 1536 x 16 take 960 us (1009, 968), of 8192 x 1024 x 16 378 (614, 399).
+// A range has at most kMaxPer chunks and a grid kMaxGridY rows of blocks, a range each,
+// so a sequence has at most kMaxPer * kMaxGridY chunks.
+constexpr int kMaxPer = 64, kMaxGridY = 65535;
 int bwd_main_tiles(const SelDims& d) {
   const int sl = d.N > 32 ? 8 : d.N > 16 ? 4 : 2;
   return ceil_div(d.DG, 32 / sl * 2 * kBwdWarps);
 }
-void bwd_chunks(SelDims* d) {
+int bwd_chunks(SelDims* d) {
   const int sl = d->N > 32 ? 4 : d->N > 16 ? 2 : 1;
   d->ctiles = ceil_div(d->DG, 32 / sl * 2 * kFwdWarps);
   d->nh = ceil_div(d->T, kBwdL);
   const int64_t bg = (int64_t)d->B * d->G, wave = 2 * 152;
   int64_t best = -1;
   int best_per = 1;
-  for (int per = 1; per <= d->nh && per <= 64; ++per) {
+  for (int per = 1; per <= d->nh && per <= kMaxPer; ++per) {
     const int64_t nc = ceil_div(d->nh, per);
+    if (nc > kMaxGridY) continue;
     const int64_t main = (bg * bwd_main_tiles(*d) * nc + wave - 1) / wave;
     const int64_t wave1 = kStateBlocksPerSm * 152;
     const int64_t first = (bg * d->ctiles * nc + wave1 - 1) / wave1;
@@ -1194,8 +1199,12 @@ void bwd_chunks(SelDims* d) {
     const int64_t cost = (24 * main + 7 * first) * (2 * per + 1);
     if (best < 0 || cost < best) best = cost, best_per = per;
   }
+  if (best < 0 || bg * d->ctiles > 0x7fffffff || bg * bwd_main_tiles(*d) > 0x7fffffff ||
+      (int64_t)d->B * d->T * d->G > ((int64_t)1 << 31))
+    return SSD_ERR_UNSUPPORTED;
   d->L = best_per * kBwdL;
   d->nc = ceil_div(d->nh, best_per);
+  return SSD_OK;
 }
 
 struct SelBwdWs {
@@ -1355,8 +1364,7 @@ extern "C" {
 
 size_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_shape* shape) {
   SelDims d;
-  if (sel_dims(shape, &d) != SSD_OK) return 0;
-  fwd_chunks(&d);
+  if (sel_dims(shape, &d) != SSD_OK || fwd_chunks(&d) != SSD_OK) return 0;
   if (d.nc == 1) return 256;
   const size_t cd = (size_t)d.B * d.nc * d.D;
   return align_up(cd * d.N * sizeof(float), 256) + align_up(cd * sizeof(float), 256);
@@ -1364,8 +1372,7 @@ size_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_shape* shape) {
 
 size_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_shape* shape) {
   SelDims d;
-  if (sel_dims(shape, &d) != SSD_OK) return 0;
-  bwd_chunks(&d);
+  if (sel_dims(shape, &d) != SSD_OK || bwd_chunks(&d) != SSD_OK) return 0;
   return bwd_ws(d, nullptr).total;
 }
 
@@ -1375,7 +1382,8 @@ int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, cons
                            const int32_t* lengths, void* out, float* final_states,
                            void* workspace, size_t workspace_bytes, void* stream) {
   SelDims d;
-  const int st = sel_dims(shape, &d);
+  int st = sel_dims(shape, &d);
+  if (st == SSD_OK) st = fwd_chunks(&d);
   if (st != SSD_OK) return st;
   const int ie = shape->in_dtype == SSD_BF16 ? 2 : 4, oe = shape->out_dtype == SSD_BF16 ? 2 : 4;
   if (!x || !dt || !A || !B || !C || !out) return SSD_ERR_INVALID_ARG;
@@ -1386,8 +1394,6 @@ int ssd_selective_scan_fwd(const ssd_selective_shape* shape, const void* x, cons
   if (!workspace || off(workspace, 16) ||
       workspace_bytes < ssd_selective_scan_fwd_workspace_size(shape))
     return SSD_ERR_WORKSPACE;
-  fwd_chunks(&d);
-  if ((int64_t)d.B * d.G * d.ctiles > 0x7fffffff || d.nc > 65535) return SSD_ERR_UNSUPPORTED;
   float* hin = static_cast<float*>(workspace);
   float* sumd = reinterpret_cast<float*>(
       static_cast<char*>(workspace) +
@@ -1416,7 +1422,8 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
                            void* dz, float* ddt_bias, float* dinit_states, void* workspace,
                            size_t workspace_bytes, void* stream) {
   SelDims d;
-  const int st = sel_dims(shape, &d);
+  int st = sel_dims(shape, &d);
+  if (st == SSD_OK) st = bwd_chunks(&d);
   if (st != SSD_OK) return st;
   const int ie = shape->in_dtype == SSD_BF16 ? 2 : 4, oe = shape->out_dtype == SSD_BF16 ? 2 : 4;
   if (!x || !dt || !A || !B || !C || !dout || !dx || !ddt || !dA || !dB || !dC || (z && !dz))
@@ -1429,10 +1436,6 @@ int ssd_selective_scan_bwd(const ssd_selective_shape* shape, const void* x, cons
   if (!workspace || off(workspace, 16) ||
       workspace_bytes < ssd_selective_scan_bwd_workspace_size(shape))
     return SSD_ERR_WORKSPACE;
-  bwd_chunks(&d);
-  if ((int64_t)d.B * d.G * d.ctiles > 0x7fffffff || d.nc > 65535 ||
-      (int64_t)d.B * d.T * d.G > ((int64_t)1 << 31))
-    return SSD_ERR_UNSUPPORTED;
   const SelBwdWs w = bwd_ws(d, workspace);
   const SelIn in{x, dt, dt_bias, A, B, C, D, z, lengths};
   const SelGrads g{dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit_states};

@@ -762,3 +762,34 @@ def test_block_norm_past_32_bits(cuda_lib):
     got = cuda_lib.block_norm_bwd(r, o, w, v, None, dh)
     want = cuda_lib.block_norm_bwd(r[-tail:], o[-tail:], w, v, None, dh[-tail:])
     assert all(torch.equal(got[k][-tail:], want[k]) for k in ("dresidual", "do"))
+
+
+@pytest.mark.parametrize("T,D,dtype", [(3000000, 17, "bf16"), (64 * 65535 * 32, 1, "f32")])
+def test_scan_of_the_longest_sequences(cuda_lib, T, D, dtype):
+    """As test_scan_past_32_bits, at lengths up to the backward's limit."""
+    import torch
+    it, N, tail = types(dtype)[0], 2, 96
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda", dtype=it)
+
+    x, dt, dout = rand(1, T, D), rand(1, T, D), rand(1, T, D)
+    B, C = rand(1, T, 1, N), rand(1, T, 1, N)
+    A, bias = -torch.rand(D, N, generator=gen, device="cuda") - 0.1, torch.full((D,), -3.0, device="cuda")
+    cut = lambda s: (x[:, s], dt[:, s], bias, A, B[:, s], C[:, s])  # noqa: E731
+    _, state = cuda_lib.selective_scan_fwd(*cut(slice(0, T - tail)))
+    rest = slice(T - tail, T)
+
+    def same(a, b):
+        a, b = a.double(), b.double()
+        assert bool(torch.isfinite(a).all()) and (a - b).norm() <= 2.0 ** -8 * b.norm()
+
+    out, fin = cuda_lib.selective_scan_fwd(x, dt, bias, A, B, C)
+    want, wfin = cuda_lib.selective_scan_fwd(*cut(rest), init_states=state)
+    same(out[:, rest], want)
+    same(fin, wfin)
+    got = cuda_lib.selective_scan_bwd(x, dt, bias, A, B, C, None, None, dout)
+    want = cuda_lib.selective_scan_bwd(*cut(rest), None, None, dout[:, rest], init_states=state)
+    for k in ("dx", "ddt", "dB", "dC"):
+        same(got[k][:, rest], want[k])

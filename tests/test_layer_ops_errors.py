@@ -180,3 +180,26 @@ def test_scan_stops_at_a_refused_launch(lib, call):
         st = lib.ssd_selective_scan_bwd(s, D, D, None, D, D, D, None, None, None, None, D, None, D,
                                         D, D, D, D, None, None, None, None, D, BIG, None)
     assert st == 4 and lib.ssd_launch_count() == before + 1  # SSD_ERR_CUDA
+
+
+def test_scan_length_limits(lib):
+    """The limits of the header, in the calls and in the size queries alike."""
+    fwd = [D, D, None, D, D, D, None, None, None, None, D, None, None, BIG, None]
+    bwd = [D, D, None, D, D, D, None, None, None, None, D, None, D, D, D, D, D, None, None, None,
+           None, None, BIG, None]  # no workspace: nothing past the shape's check is launched
+    top = 64 * 65535 * 32
+    for kw, forward, backward in (
+            (dict(batch=1, seqlen=top), WORKSPACE, WORKSPACE),
+            (dict(batch=1, seqlen=top + 1), WORKSPACE, UNSUPPORTED),
+            (dict(batch=1, seqlen=(1 << 30) - 1), WORKSPACE, UNSUPPORTED),
+            (dict(batch=1, seqlen=1 << 30), UNSUPPORTED, UNSUPPORTED),
+            (dict(batch=128, seqlen=1 << 24), WORKSPACE, WORKSPACE),      # batch * seqlen = 2^31
+            (dict(batch=129, seqlen=1 << 24), WORKSPACE, UNSUPPORTED),
+            (dict(batch=65, seqlen=1 << 24, ngroups=2), WORKSPACE, UNSUPPORTED),
+            (dict(batch=65535, seqlen=1, channels=1 << 23, ngroups=1 << 23), UNSUPPORTED,
+             UNSUPPORTED)):
+        s = sel(**kw)
+        assert lib.ssd_selective_scan_fwd(s, *fwd) == forward, kw
+        assert lib.ssd_selective_scan_bwd(s, *bwd) == backward, kw
+        assert (lib.ssd_selective_scan_fwd_workspace_size(s) == 0) == (forward == UNSUPPORTED), kw
+        assert (lib.ssd_selective_scan_bwd_workspace_size(s) == 0) == (backward == UNSUPPORTED), kw
