@@ -110,8 +110,9 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kL
 // log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3.  atanh(s) / s as a polynomial in
 // q = s^2 on [0, 1/9], interpolated at the Chebyshev nodes: degree 4 is within
 // 8e-9.  Steps are typically 1e-3 to 1e-1, where 1 + e in fp32 would round away
-// what the logarithm needs; this form keeps ~5e-7 relative everywhere (above 20
-// it is v, as e vanishes against v).
+// what the logarithm needs; this form is within 5e-7 + 1e-7 max(-v, 0) of the value
+// (the second part from the rounding of v log2(e), which e^-|v| passes on); above 20
+// it is v, as e vanishes against v, and below -87 0, as e is not a normal number.
 constexpr float kAtanh1 = 0.3333316147327423f, kAtanh2 = 0.20012298226356506f,
                 kAtanh3 = 0.13982579112052917f, kAtanh4 = 0.14078889787197113f;
 __device__ __forceinline__ float softplus(float v) {

@@ -428,6 +428,27 @@ def test_selective_step_matches_oracle(cuda_lib, B, D, N, G, dtype, gated):
     assert np.array_equal(sd.cpu().numpy()[rest], state[rest].astype(np.float32))
 
 
+def test_softplus_within_its_bound(cuda_lib):
+    """With x = B = C = 1 and a state of 0 the output is delta itself.  v log2(e) has two
+    roundings, 1e-7 of v together, which e^v makes errors of its value; 2^v, the
+    quotient and the logarithm's series add 5e-7."""
+    import torch
+    v = stored(np.linspace(-86.0, 40.0, 20001), torch.float32)
+    want = np.logaddexp(0.0, v)
+    n = len(v)
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    A, dt = -one(n, 1), dev(v)
+    got = [cuda_lib.selective_scan_fwd(one(1, 1, n), dt.view(1, 1, n), None, A, one(1, 1, 1, 1),
+                                       one(1, 1, 1, 1))[0],
+           cuda_lib.selective_step(one(1, n), dt.view(1, n), None, A, one(1, 1, 1), one(1, 1, 1),
+                                   0 * one(1, n, 1)),
+           cuda_lib.ssd_step(one(n, 1, 1), dt.view(n, 1), None, -one(1), one(n, 1, 1), one(n, 1, 1),
+                             0 * one(n, 1, 1, 1))]
+    for y in got:
+        err = np.abs(y.double().cpu().numpy().ravel() / want - 1.0)
+        assert np.all(err <= 5e-7 + 1e-7 * np.maximum(-v, 0.0)), float(err.max())
+
+
 @pytest.mark.parametrize("B,H,P,N,G,dtype", [
     (1, 1, 1, 1, 1, "f32"), (1, 24, 64, 128, 1, "bf16"), (3, 6, 40, 33, 2, "mixed"),
     (2, 5, 16, 16, 1, "f32"), (7, 4, 128, 64, 2, "bf16"), (2, 2, 64, 200, 1, "f32"),
