@@ -367,6 +367,34 @@ def test_scan_of_column_ranges(cuda_lib):
     assert all(torch.equal(g1[k], g2[k]) for k in g1)
 
 
+@pytest.mark.parametrize("T,D,G", [(50, 37, 1), (333, 48, 1), (41, 66, 2), (1, 5, 1)])
+@pytest.mark.parametrize("at", [0, 1, 4, "end"])
+def test_scan_of_odd_column_ranges(cuda_lib, T, D, G, at):
+    """z at odd and even columns of a wider tensor of odd rows, and as its very last
+    columns (the whole words that cover a row must not pass the tensor's ends), B and C at
+    odd columns; everything beside them is NaN."""
+    import torch
+    it = torch.bfloat16
+    a, init, g = scan_inputs(T + D, 3, T, D, 16, G, it, True, True)
+    x, dt, bias, A, B, C, Dv, z = scan_dev(a, it)
+    W = 2 * D + (2 * D + 1) % 2  # odd
+    off = W - D if at == "end" else at
+    zw = torch.full((3, T, W), float("nan"), dtype=it, device="cuda")
+    zw[..., off:off + D] = z
+    bc = torch.full((3, T, 2 * G * 16 + 1), float("nan"), dtype=it, device="cuda")
+    bc[..., 1:] = torch.cat([B.flatten(2), C.flatten(2)], 2)
+    Bw, Cw = (t.unflatten(2, (G, 16)) for t in bc[..., 1:].split(G * 16, 2))
+    v = (x, dt, bias, A, Bw, Cw, Dv, zw[..., off:off + D])
+    out, fin = cuda_lib.selective_scan_fwd(*v, init_states=dev(init))
+    orf, fr = lo.scan_fwd(init=init, **a)
+    close("out", out, orf)
+    close("final", fin, fr)
+    dout = stored(g.standard_normal((3, T, D)), it)
+    r = lo.scan_bwd(*(a[k] for k in ("x", "dt", "dt_bias", "A", "B", "C", "D", "z")), dout, init)
+    for k, t in cuda_lib.selective_scan_bwd(*v, dev(dout, it), init_states=dev(init)).items():
+        close(k, t, r[k])
+
+
 def test_repeats_under_load_are_bit_identical(cuda_lib):
     """As test_conv_backward_under_load, for the rings of the scan and of the block
     norm: their values are pinned at small sizes, a late copy would change bits."""
@@ -426,6 +454,54 @@ def test_selective_step_matches_oracle(cuda_lib, B, D, N, G, dtype, gated):
     close("state", sd, want)
     rest = np.setdiff1d(np.arange(n), slots)
     assert np.array_equal(sd.cpu().numpy()[rest], state[rest].astype(np.float32))
+
+
+@pytest.mark.parametrize("B,C,K,dtype,has_bias,silu", [
+    (1, 1, 2, "f32", False, True), (3, 24, 2, "bf16", True, True), (5, 33, 3, "mixed", True, True),
+    (2, 777, 3, "f32", True, False), (7, 41, 4, "mixed", False, True), (3, 40, 3, "bf16", True, False),
+    (4, 36, 2, "mixed", True, True), (2, 1023, 4, "bf16", True, True), (64, 1792, 4, "bf16", True, True)])
+def test_conv_step_matches_oracle(cuda_lib, B, C, K, dtype, has_bias, silu):
+    import torch
+    it, ot = types(dtype)
+    g = np.random.default_rng(B + C + K)
+    x, n = stored(g.standard_normal((B, C)), it), B + 2
+    w = stored(g.uniform(-0.5, 0.5, (C, K)), torch.float32)
+    bias = stored(g.standard_normal(C), torch.float32) if has_bias else None
+    slots = g.permutation(n)[:B]
+    state = stored(g.standard_normal((n, K - 1, C)), it)
+    yr, fr = lo.conv_fwd(x[:, None], w, bias, state[slots], None, silu)
+    want = state.copy()
+    want[slots] = fr
+    wide = torch.zeros(B, C + 5, dtype=it, device="cuda")
+    wide[:, 3:3 + C] = dev(x, it)
+    for xd in (dev(x, it), wide[:, 3:3 + C]):  # dense, and columns at an odd offset
+        sd = dev(state, it)
+        y = cuda_lib.causal_conv_step(xd, sd, dev(w), dev(bias), slots=dev(slots, torch.int32),
+                                      silu=silu, out_dtype=ot)
+        close("y", y, yr[:, 0])
+        assert np.array_equal(sd.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("D,N,G,dtype", [(48, 16, 1, "bf16"), (37, 7, 1, "bf16"), (66, 16, 2, "mixed"),
+                                         (33, 16, 3, "f32")])
+def test_selective_step_of_column_ranges(cuda_lib, D, N, G, dtype):
+    """z, B and C as columns of wider rows, at odd and even offsets: the bits of dense ones."""
+    import torch
+    it, ot = types(dtype)
+    g = np.random.default_rng(D)
+    r = lambda *s: dev(g.standard_normal(s), it)  # noqa: E731
+    x, dt, z, B, C = r(5, D), r(5, D), r(5, D), r(5, G, N), r(5, G, N)
+    A, state = dev(-np.exp(g.standard_normal((D, N)))), dev(g.standard_normal((5, D, N)))
+    for at in (0, 1, 2, 5):
+        wide = r(5, at + D + 2 * G * N + 1)
+        zw, Bw, Cw = (wide[:, a:a + n] for a, n in ((at, D), (at + D, G * N), (at + D + G * N, G * N)))
+        for t, v in ((zw, z), (Bw, B), (Cw, C)):
+            t.copy_(v.reshape(t.shape))
+        s1, s2 = state.clone(), state.clone()
+        y1 = cuda_lib.selective_step(x, dt, None, A, B, C, s1, None, z, out_dtype=ot)
+        y2 = cuda_lib.selective_step(x, dt, None, A, Bw.unflatten(1, (G, N)), Cw.unflatten(1, (G, N)),
+                                     s2, None, zw, out_dtype=ot)
+        assert torch.equal(y1, y2) and torch.equal(s1, s2)
 
 
 def test_softplus_within_its_bound(cuda_lib):
