@@ -365,10 +365,11 @@ int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
  * Row strides are the elements between consecutive positions (batch rows in
  * the single-token calls) of an input that is a column range of a wider
  * tensor, batch strides those between its batch rows; a row stride of 0 means
- * dense (the batch stride is then ignored).  Everything else is dense and row-major.  Pointers
- * must be aligned to their element size; 16-byte alignment of pointers and
- * rows lets the kernels use wide accesses.  bf16 inputs give bf16 or f32
- * outputs, f32 inputs f32 ones (else SSD_ERR_UNSUPPORTED).  Every call is
+ * dense (the batch stride is then ignored).  Everything else is dense and
+ * row-major.  Outputs overlap no input, except where a call is said to work in
+ * place.  Pointers must be aligned to their element size; 16-byte alignment of
+ * pointers and rows lets the kernels use wide accesses.  bf16 inputs give bf16
+ * or f32 outputs, f32 inputs f32 ones (else SSD_ERR_UNSUPPORTED).  Every call is
  * asynchronous on `stream`, waits for nothing on the device, and returns
  * SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE (workspace NULL,
  * misaligned or too small) or SSD_ERR_CUDA.  All sums over rows, positions or
@@ -383,7 +384,7 @@ int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
  * bias (channels) f32 or NULL, y (batch, seqlen, channels) out_dtype;
  * final_state (batch, width - 1, channels) in_dtype or NULL: the last
  * width - 1 inputs.  2 <= width <= 4, batch * seqlen < 2^31, channels < 2^20.
- * init_state and final_state must not overlap. */
+ * init_state and final_state must not overlap (SSD_ERR_INVALID_ARG). */
 typedef struct {
   int64_t batch, seqlen, channels, width;
   int64_t x_row_stride, x_batch_stride;

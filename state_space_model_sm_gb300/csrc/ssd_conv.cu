@@ -605,6 +605,11 @@ int ssd_causal_conv_fwd(const ssd_conv_shape* shape, const void* x, const float*
   if (misaligned(x, ie) || misaligned(init_state, ie) || misaligned(final_state, ie) ||
       misaligned(y, oe) || misaligned(w, 4) || misaligned(bias, 4) || misaligned(lengths, 4))
     return SSD_ERR_INVALID_ARG;
+  if (init_state && final_state) {  // the final state is written before the initial one is used up
+    const uintptr_t a = reinterpret_cast<uintptr_t>(init_state);
+    const uintptr_t b = reinterpret_cast<uintptr_t>(final_state);
+    if ((a > b ? a - b : b - a) < (uintptr_t)d.B * (K - 1) * d.C * ie) return SSD_ERR_INVALID_ARG;
+  }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = d.C % 4 == 0 && vec_ok(x, d.xs, ie, 4) && vec_ok(x, d.xb, ie, 4) &&
                    vec_ok(init_state, d.C, ie, 4) && vec_ok(final_state, d.C, ie, 4) &&

@@ -169,7 +169,7 @@ def causal_conv_fwd(x, w, bias=None, init_state=None, lengths=None, silu: bool =
     (batch, width - 1, channels) in x's type: the inputs before position 0;
     lengths (batch,) int32: positions from lengths[b] on are padding.
     final_state is the state after lengths[b] positions, which
-    ``causal_conv_step`` goes on from.  y is in ``out_dtype`` (x's type)."""
+    ``causal_conv_step`` goes on from (a given one must not overlap init_state).  y is in ``out_dtype`` (x's type)."""
     lib = _native_lib()
     dev, shape, (B, T, C, K), odt, xp, wp, bp = _conv_inputs(x, w, bias, 3, silu, out_dtype)
     ip = _check(init_state, "init_state", (B, K - 1, C), x.dtype, dev)

@@ -202,6 +202,25 @@ def test_conv_of_a_column_range_and_in_place_step(cuda_lib):
     assert bool((state[[1, 3]] == 7.0).all())
 
 
+def test_conv_states_side_by_side(cuda_lib):
+    """The initial and the final state next to each other in one buffer are fine; one for
+    both, or shifted into each other, is refused."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, w = torch.randn(2, 9, 8, generator=g, device="cuda"), torch.randn(8, 4, generator=g, device="cuda")
+    buf = torch.randn(3, 2, 3, 8, generator=g, device="cuda")
+    init = buf[1].clone()
+    y, fin = cuda_lib.causal_conv_fwd(x, w, init_state=init)
+    for k in (0, 2):
+        y2, fin2 = cuda_lib.causal_conv_fwd(x, w, init_state=buf[1], final_state=buf[k])
+        assert torch.equal(y2, y) and torch.equal(buf[k], fin) and torch.equal(buf[1], init)
+    flat = buf.view(-1)
+    for at in (48, 49, 95, 1):
+        with pytest.raises(cuda_lib.SSDError) as e:
+            cuda_lib.causal_conv_fwd(x, w, init_state=buf[1], final_state=flat[at:at + 48].view(2, 3, 8))
+        assert e.value.status == 1
+
+
 # ------------------------------------------------------------- selective scan
 
 def scan_inputs(seed, B, T, D, N, G, it, gated, has_init):

@@ -203,3 +203,12 @@ def test_scan_length_limits(lib):
         assert lib.ssd_selective_scan_bwd(s, *bwd) == backward, kw
         assert (lib.ssd_selective_scan_fwd_workspace_size(s) == 0) == (forward == UNSUPPORTED), kw
         assert (lib.ssd_selective_scan_bwd_workspace_size(s) == 0) == (backward == UNSUPPORTED), kw
+
+
+def test_conv_states_must_not_overlap(lib):
+    """The final state is written before the initial one is used up, so going on in
+    place would give wrong outputs: refused, at any overlap of the two."""
+    s = conv(batch=2, width=4, channels=8)  # states of 2 x 3 x 8 bf16: 96 bytes
+    at = ctypes.c_void_p
+    for init, final in ((256, 256), (256, 350), (350, 256)):
+        assert lib.ssd_causal_conv_fwd(s, D, D, None, at(init), None, D, at(final), None) == INVALID
