@@ -505,6 +505,91 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
                        float* dw_post, float* dgate, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* Gated delta rule: the scan whose state is corrected towards each value.  For
+ * head h of group g(h) = h / (nheads / ngroups), with delta = softplus(dt +
+ * dt_bias), a = exp(delta A[h]) and b = sigmoid(beta),
+ *   S <- a S,   S <- S + b (v - S k) (outer) k,   y = scale S q
+ * q, k (batch, seqlen, ngroups, dstate), v, y (batch, seqlen, nheads, headdim),
+ * dt, beta (batch, seqlen, nheads); q, k, v, dt, beta in_dtype, y out_dtype;
+ * dt_bias (nheads) f32 or NULL, A (nheads) f32 (negative: decay); init_states,
+ * final_states (batch, nheads, headdim, dstate) f32 or NULL.  Keys of a length up
+ * to 1 keep the state bounded (ssd_qk_norm_fwd with l2); the call does not
+ * normalise them.  dstate <= 128, headdim <= 256, batch and nheads < 65536,
+ * seqlen < 2^30, batch * nheads * ceil(seqlen / 64) < 2^31.  A step's decay below
+ * 2^-150 counts as 2^-150, 0 in f32.  Workspace of the size query's bytes (0 for a
+ * rejected shape), 16-byte aligned, caller-owned. */
+typedef struct {
+  int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+  int64_t q_row_stride, k_row_stride, v_row_stride;
+  int64_t q_batch_stride, k_batch_stride, v_batch_stride;
+  float scale;
+  int32_t in_dtype;  /* q, k, v, dt, beta, dy              */
+  int32_t out_dtype; /* y; dq, dk, dv, ddt and dbeta       */
+} ssd_delta_shape;
+
+size_t ssd_gated_delta_fwd_workspace_size(const ssd_delta_shape* shape);
+int ssd_gated_delta_fwd(const ssd_delta_shape* shape, const void* q, const void* k, const void* v,
+                        const void* dt, const float* dt_bias, const float* A, const void* beta,
+                        const float* init_states, const int32_t* lengths, void* y,
+                        float* final_states, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Gradients of <dy, y> + <dfinal_states, final_states>, from the forward's inputs
+ * (the states are formed again): dq, dk, dv, ddt, dbeta (dense, out_dtype; dq and
+ * dk summed over the heads of each group), dA, ddt_bias (nheads), dinit_states
+ * f32.  dfinal_states, dA, ddt_bias and dinit_states may be NULL. */
+size_t ssd_gated_delta_bwd_workspace_size(const ssd_delta_shape* shape);
+int ssd_gated_delta_bwd(const ssd_delta_shape* shape, const void* q, const void* k, const void* v,
+                        const void* dt, const float* dt_bias, const float* A, const void* beta,
+                        const float* init_states, const int32_t* lengths, const void* dy,
+                        const float* dfinal_states, void* dq, void* dk, void* dv, void* ddt,
+                        void* dbeta, float* dA, float* ddt_bias, float* dinit_states,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of the gated delta rule (shape->seqlen 1): q, k (batch, ngroups,
+ * dstate), v, y (batch, nheads, headdim), dt, beta (batch, nheads); state (nslots,
+ * nheads, headdim, dstate) f32, updated in place.  dstate <= 256, headdim < 2^14,
+ * batch < 2^24, nheads * headdim < 2^26. */
+int ssd_gated_delta_step(const ssd_delta_shape* shape, const void* q, const void* k, const void* v,
+                         const void* dt, const float* dt_bias, const float* A, const void* beta,
+                         float* state, const int32_t* slots, int64_t nslots, void* y,
+                         void* stream);
+
+/* Norm of queries and keys, per head, with the rotation of positions.  Of each row
+ * x of headdim values of q (rows, q_heads, headdim) and k (rows, k_heads, headdim),
+ *   n = x / sqrt(mean(x^2) + eps) w   (l2: x / sqrt(sum(x^2) + eps) w)
+ * with w = w_q or w_k (headdim) f32, or NULL (1), and the first `rotary` columns of
+ * n turned in pairs (a, b) by the angle f = position * freq[i]:
+ *   a' = a cos f - b sin f,   b' = b cos f + a sin f
+ * where pair i is columns (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved.
+ * rows = batch * seqlen; positions (rows) int32 device memory, or NULL: row r is at
+ * position r % seqlen.  freq (rotary / 2) f32 device memory (NULL with rotary 0).
+ * Angles are reduced exactly for every int32 position.  q_out, k_out dense.
+ * headdim <= 1024, q_heads, k_heads < 65536, rows * (q_heads + k_heads) < 2^31;
+ * rotary even, <= headdim; eps > 0; |freq| < 2^20. */
+typedef struct {
+  int64_t batch, seqlen, q_heads, k_heads, headdim, rotary;
+  int64_t q_row_stride, k_row_stride, q_batch_stride, k_batch_stride;
+  float eps;
+  int32_t l2, interleaved;
+  int32_t in_dtype;  /* q, k, dq_out, dk_out  */
+  int32_t out_dtype; /* q_out, k_out, dq, dk  */
+} ssd_qk_norm_shape;
+
+int ssd_qk_norm_fwd(const ssd_qk_norm_shape* shape, const void* q, const void* k, const float* w_q,
+                    const float* w_k, const float* freq, const int32_t* positions, void* q_out,
+                    void* k_out, void* stream);
+
+/* Gradients of <dq_out, q_out> + <dk_out, k_out> from the forward's inputs: dq, dk
+ * (dense, out_dtype), dw_q, dw_k (headdim) f32, required exactly when w_q and w_k
+ * are given.  Workspace of the size query's bytes, 16-byte aligned, caller-owned;
+ * its size depends on the current device's SM count. */
+size_t ssd_qk_norm_workspace_size(const ssd_qk_norm_shape* shape);
+int ssd_qk_norm_bwd(const ssd_qk_norm_shape* shape, const void* q, const void* k, const float* w_q,
+                    const float* w_k, const float* freq, const int32_t* positions,
+                    const void* dq_out, const void* dk_out, void* dq, void* dk, float* dw_q,
+                    float* dw_k, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Diagnostic: one tcgen05 tile product on the current device,
  * D[128][nn] = A[128][k] * B[nn][k]^T (A, B bf16 row-major, D f32 row-major,
  * all device memory), with A and B staged in shared memory K-major (0) or

@@ -431,15 +431,21 @@ def launch_count() -> int:
     return int(_native.load().ssd_launch_count())
 
 
-_LAYER_OPS = ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
-              "selective_scan_bwd", "selective_step", "ssd_step", "block_norm_fwd",
-              "block_norm_bwd")
+_LAYER_OPS = {
+    "layer_ops": ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
+                  "selective_scan_bwd", "selective_step", "ssd_step", "block_norm_fwd",
+                  "block_norm_bwd"),
+    "delta_ops": ("gated_delta_fwd", "gated_delta_bwd", "gated_delta_step", "qk_norm_fwd",
+                  "qk_norm_bwd"),
+}
 
 
 def __getattr__(name):
-    """The layer operators (``layer_ops``), loaded with torch on first use."""
-    if name in _LAYER_OPS:
-        from . import layer_ops
-        globals().update({k: getattr(layer_ops, k) for k in _LAYER_OPS})
-        return globals()[name]
+    """The layer operators (``layer_ops``, ``delta_ops``), loaded with torch on first use."""
+    for module, names in _LAYER_OPS.items():
+        if name in names:
+            from importlib import import_module
+            loaded = import_module(f".{module}", __name__)
+            globals().update({k: getattr(loaded, k) for k in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

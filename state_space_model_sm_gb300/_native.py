@@ -133,12 +133,35 @@ class BlockNormShape(ctypes.Structure):
                 ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)]
 
 
+class DeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("q_batch_stride", ctypes.c_int64),
+                ("k_batch_stride", ctypes.c_int64), ("v_batch_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class QkNormShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("rotary", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("q_batch_stride", ctypes.c_int64), ("k_batch_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("l2", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _SP = ctypes.POINTER(Shape)
 _NP = ctypes.POINTER(NormShape)
 _CP = ctypes.POINTER(ConvShape)
 _EP = ctypes.POINTER(SelectiveShape)
 _BP = ctypes.POINTER(BlockNormShape)
+_DP = ctypes.POINTER(DeltaShape)
+_QP = ctypes.POINTER(QkNormShape)
 SIGNATURES = {
     "ssd_fwd_workspace_size": ([_SP], ctypes.c_size_t),
     "ssd_bwd_workspace_size": ([_SP], ctypes.c_size_t),
@@ -184,6 +207,14 @@ SIGNATURES = {
     "ssd_block_norm_workspace_size": ([_BP], ctypes.c_size_t),
     "ssd_block_norm_fwd": ([_BP] + [_VP] * 8, ctypes.c_int),
     "ssd_block_norm_bwd": ([_BP] + [_VP] * 13 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_gated_delta_fwd_workspace_size": ([_DP], ctypes.c_size_t),
+    "ssd_gated_delta_fwd": ([_DP] + [_VP] * 12 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_gated_delta_bwd_workspace_size": ([_DP], ctypes.c_size_t),
+    "ssd_gated_delta_bwd": ([_DP] + [_VP] * 20 + [ctypes.c_size_t, _VP], ctypes.c_int),
+    "ssd_gated_delta_step": ([_DP] + [_VP] * 9 + [ctypes.c_int64, _VP, _VP], ctypes.c_int),
+    "ssd_qk_norm_fwd": ([_QP] + [_VP] * 9, ctypes.c_int),
+    "ssd_qk_norm_workspace_size": ([_QP], ctypes.c_size_t),
+    "ssd_qk_norm_bwd": ([_QP] + [_VP] * 13 + [ctypes.c_size_t, _VP], ctypes.c_int),
 }
 
 _lock = threading.Lock()

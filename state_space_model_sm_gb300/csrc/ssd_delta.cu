@@ -1,0 +1,1655 @@
+// The gated delta rule: the scan whose state is corrected towards each value.
+//     delta_t = softplus(dt + dt_bias),  a_t = exp(delta_t A),  b_t = sigmoid(beta)
+//     h <- a_t h,   h <- h + b_t (v_t - h k_t) k_t^T,   y_t = scale h q_t
+// for a state h (headdim x dstate) of each head.
+//
+// By chunks of 64 tokens.  With G the running sum of log a inside a chunk, S the state
+// in front of it and rows for tokens, the corrections U (64 x headdim) solve
+//     (I + M) U = b (V - e^G K S^T),   M[i, j] = b_i e^(G_i - G_j) k_i . k_j   (j < i)
+// and then  Y = scale (e^G Q S^T + ((Q K^T) e^(G_i - G_j))_{j <= i} U),
+//           S' = e^(G_63) S + (e^(G_63 - G) U)^T K.
+// X = (I + M)^-1 does not depend on the state, so the work splits into what every
+// chunk does by itself (k_delta_prep: X; k_delta_out: Y) and the chain over the chunks
+// (k_delta_chain: U and the states), whose rows p of the state are independent.
+//
+// Numerics: all matrix products run on the tensor cores with bf16 planes of fp32
+// values (warp_mma.cuh), three planes wherever the result reaches a state, a state's
+// gradient or a parameter's gradient; two where it only reaches a bf16 output.  Log
+// decays are summed in 64 bits and kept as two floats, so that a strong decay early in
+// a chunk takes nothing from the differences behind it.
+#include <cuda_bf16.h>
+
+#include "layer_math.cuh"
+#include "ssd_internal.h"
+#include "warp_mma.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace wm;
+using lm::cp_async;
+using lm::cp_commit;
+using lm::cp_wait;
+using lm::ex2;
+using lm::from_f;
+using lm::sigmoid;
+using lm::softplus;
+using lm::to_f;
+
+constexpr int kC = 64;       // tokens of a chunk
+constexpr int kTP = kC + 8;  // pitch of tiles with a chunk's tokens or 64 value rows across
+constexpr int kF = 68;       // pitch of fp32 tiles of 64 columns
+
+struct DeltaDims {
+  int B, T, H, G, P, N, nc;
+  int rep;  // heads of a group
+  int Ps;   // value rows in the workspace: P up to a multiple of 16
+  int NP;   // key columns in the workspace: 64 or 128
+  int nb;   // head blocks of a group in the gradient
+  float scale;
+  int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
+  int vq, vk, vv, vdy;             // whether rows can be read 16 bytes at a time
+};
+
+// Gates of a chunk: the log2 decays' running sum in two floats, and b.
+struct Gates {
+  float gh[kC], gl[kC], b[kC];
+};
+
+struct DeltaWs {
+  Gates* gates;  // (B, H, nc)
+  bf16* X;       // (B, H, nc, 3, 64, 64) planes of (I + M)^-1
+  float* U;      // (B, H, nc, Ps, 64)  transposed: [p][token]
+  float* S0;     // (B, H, nc, Ps, NP)  the state in front of each chunk
+  // backward
+  float* Zb;   // (B, H, nc, Ps, 64)  b e^G S k
+  float* E;    // (B, H, nc, Ps, 64)  the part of dU from dY
+  float* Zd;   // (B, H, nc, Ps, 64)  the part of dU from the state behind the chunk
+  float* dR;   // (B, H, nc, Ps, 64)
+  float* dS;   // (B, H, nc, Ps, NP)  gradient of the state behind each chunk
+  float* part; // (B, H, nc, 2) sums for dA and ddt_bias
+  float* dqp;  // (nb, B, T, G, N) head-block parts of dq, dk where nb > 1
+  float* dkp;
+  size_t total;
+};
+
+template <typename T>
+constexpr int planes_of() { return sizeof(T) == 2 ? 1 : 3; }
+
+__device__ __forceinline__ int tokens_of(const DeltaDims& d, const int* lengths, int b) {
+  if (!lengths) return d.T;
+  const int n = lengths[b];
+  return n < 0 ? 0 : n > d.T ? d.T : n;
+}
+
+__device__ __forceinline__ float decay_between(const Gates& g, int i, int j) {
+  return ex2((g.gh[i] - g.gh[j]) + (g.gl[i] - g.gl[j]));
+}
+
+// 64 rows of W columns of src as planes of pitch LD; rows from rv and columns from cv
+// on are zeros.  vec: rows are 16-byte aligned and cv is a multiple of 16 bytes.
+template <typename T, int W, int LD, int THREADS>
+__device__ __forceinline__ void load_tile(bf16* dst, const T* src, int64_t ld, int rv, int cv,
+                                          bool vec) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec) {
+      for (int i = threadIdx.x; i < kC * (W / 8); i += THREADS) {
+        const int r = i / (W / 8), c = i % (W / 8) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rv && c < cv) v = *reinterpret_cast<const uint4*>(src + r * ld + c);
+        *reinterpret_cast<uint4*>(dst + r * LD + c) = v;
+      }
+    } else {
+      for (int i = threadIdx.x; i < kC * W; i += THREADS) {
+        const int r = i / W, c = i % W;
+        dst[r * LD + c] = r < rv && c < cv ? src[r * ld + c] : from_f<bf16>(0.f);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < kC * (W / 4); i += THREADS) {
+      const int r = i / (W / 4), c = i % (W / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rv) {
+        const T* p = src + r * ld + c;
+        if (vec) {
+          if (c < cv) v = *reinterpret_cast<const float4*>(p);
+        } else {
+          if (c < cv) v.x = p[0];
+          if (c + 1 < cv) v.y = p[1];
+          if (c + 2 < cv) v.z = p[2];
+          if (c + 3 < cv) v.w = p[3];
+        }
+      }
+      uint32_t a[3], b[3];
+      split2<3>(v.x, v.y, a);
+      split2<3>(v.z, v.w, b);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint2*>(dst + k * kC * LD + r * LD + c) = make_uint2(a[k], b[k]);
+    }
+  }
+}
+
+// 64 rows of W fp32 values of the workspace (rows from rv on: zeros) as NPL planes.
+template <int NPL, int W, int LD, int THREADS>
+__device__ __forceinline__ void load_split(bf16* dst, const float* src, int rv) {
+  for (int i = threadIdx.x; i < kC * (W / 4); i += THREADS) {
+    const int r = i / (W / 4), c = i % (W / 4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rv) v = *reinterpret_cast<const float4*>(src + (size_t)r * W + c);
+    uint32_t a[NPL], b[NPL];
+    split2<NPL>(v.x, v.y, a);
+    split2<NPL>(v.z, v.w, b);
+#pragma unroll
+    for (int k = 0; k < NPL; ++k)
+      *reinterpret_cast<uint2*>(dst + k * kC * LD + r * LD + c) = make_uint2(a[k], b[k]);
+  }
+}
+
+// As load_tile, started asynchronously: bf16 rows with vec.
+template <int W, int LD, int THREADS>
+__device__ __forceinline__ void copy_tile(bf16* dst, const bf16* src, int64_t ld, int rv, int cv) {
+  for (int i = threadIdx.x; i < kC * (W / 8); i += THREADS) {
+    const int r = i / (W / 8), c = i % (W / 8) * 8;
+    bf16* to = dst + r * LD + c;
+    if (r < rv && c < cv)
+      cp_async<16>(to, src + r * ld + c);
+    else
+      *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+  }
+}
+// The planes of X, started asynchronously.
+template <int THREADS>
+__device__ __forceinline__ void copy_x(bf16* dst, const bf16* src) {
+  for (int i = threadIdx.x; i < 3 * kC * 8; i += THREADS)
+    cp_async<16>(dst + i / 8 * kTP + i % 8 * 8, src + i * 8);
+}
+
+// A raw tile of tokens x 64 value columns, as it is, for reads element by element.
+template <typename T>
+constexpr int raw_pitch() { return sizeof(T) == 2 ? kTP : kF; }
+template <typename T, int THREADS>
+__device__ __forceinline__ void load_raw(T* dst, const T* src, int64_t ld, int rv, int cv, bool vec) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {
+    for (int i = threadIdx.x; i < kC * (kC / V); i += THREADS) {
+      const int r = i / (kC / V), c = i % (kC / V) * V;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rv && c < cv) v = *reinterpret_cast<const uint4*>(src + r * ld + c);
+      *reinterpret_cast<uint4*>(dst + r * raw_pitch<T>() + c) = v;
+    }
+  } else {
+    for (int i = threadIdx.x; i < kC * kC; i += THREADS) {
+      const int r = i / kC, c = i % kC;
+      dst[r * raw_pitch<T>() + c] = r < rv && c < cv ? src[r * ld + c] : from_f<T>(0.f);
+    }
+  }
+}
+
+struct Place {  // the (batch, head, chunk) of a block
+  int b, h, c;
+  int64_t i;  // (b * H + h) * nc + c
+};
+__device__ __forceinline__ Place place(const DeltaDims& d, int64_t block) {
+  Place p;
+  p.i = block;
+  p.c = (int)(block % d.nc);
+  const int64_t bh = block / d.nc;
+  p.h = (int)(bh % d.H);
+  p.b = (int)(bh / d.H);
+  return p;
+}
+
+// ---------------------------------------------------------------------- prep
+
+// Lower part (tiles 0 .. 2 strip + 1) of the 16 rows of strip of A B^T over NP columns;
+// A and B tiles of NI planes.
+template <int NI, int NP>
+__device__ __forceinline__ void lower_product(float (&acc)[8][4], const bf16* A, const bf16* Bt,
+                                              int strip, int lane) {
+  constexpr int LD = NP + 8;
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+  for (int kk = 0; kk < NP / 16; ++kk) {
+    uint32_t a[NI][4];
+#pragma unroll
+    for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], A + p * kC * LD, strip * 16, kk * 16, lane);
+#pragma unroll
+    for (int np = 0; np < 4; ++np)
+      if (np <= strip)
+        mma_planes<NI, NI, NI>(acc[2 * np], acc[2 * np + 1], a, [&](int j, uint32_t(&r)[4]) {
+          b_rows<LD>(r, Bt + j * kC * LD, np * 16, kk * 16, lane);
+        });
+  }
+}
+
+constexpr int kPrepThreads = 128;
+
+template <typename T, int NP, bool BWD>
+constexpr size_t prep_smem() {
+  constexpr size_t tile = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+  return sizeof(Gates) + 2 * kC * kF * 4 + tile * (BWD ? 2 : 1);
+}
+
+// Gates and X of one chunk of one head; in the backward also E^T = dY^T (Q K^T e^(..)).
+//
+// X by halves: the four 16 x 16 blocks on the diagonal by substitution, a column a
+// thread; then twice  [A 0; C B]^-1 = [A' 0; -B' C A', B'].  Substitution is stable
+// whatever the keys (a run of equal keys makes I + M ill suited to a power series).
+template <typename T, int NP, bool BWD>
+__global__ void __launch_bounds__(kPrepThreads)
+    k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
+                 const T* __restrict__ dt, const float* __restrict__ dt_bias,
+                 const float* __restrict__ A, const T* __restrict__ beta,
+                 const T* __restrict__ dy, const int* __restrict__ lengths, DeltaWs w) {
+  constexpr int NI = planes_of<T>(), LD = NP + 8;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Gates& g = *reinterpret_cast<Gates*>(smem);
+  float* const M = reinterpret_cast<float*>(smem + sizeof(Gates));
+  float* const X = M + kC * kF;
+  bf16* const Kt = reinterpret_cast<bf16*>(X + kC * kF);
+  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  const Place pl = place(d, blockIdx.x);
+  const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
+  if (t0 >= n) return;
+  const int rv = min(kC, n - t0), grp = pl.h / d.rep;
+
+  load_tile<T, NP, LD, kPrepThreads>(Kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
+                                     d.N, d.vk);
+  if (BWD)
+    load_tile<T, NP, LD, kPrepThreads>(Kt + NI * kC * LD,
+                                       q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
+                                       d.N, d.vq);
+  if (strip == 0) {  // two tokens a lane
+    double s[2];
+    float bb[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = 2 * lane + j;
+      float g2 = 0.f;
+      bb[j] = 0.f;
+      if (i < rv) {
+        const int64_t at = ((int64_t)pl.b * d.T + t0 + i) * d.H + pl.h;
+        const float delta = softplus(to_f(dt[at]) + (dt_bias ? dt_bias[pl.h] : 0.f));
+        // 2^-150 is 0 in fp32: a bound that changes no decay keeps the sums finite
+        g2 = fmaxf(delta * (A[pl.h] * lm::kLog2e), -150.f);
+        bb[j] = sigmoid(to_f(beta[at]));
+      }
+      s[j] = g2;
+    }
+    s[1] += s[0];
+    double run = s[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    const double before = run - s[1];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const double v = before + s[j];
+      const float hi = (float)v;
+      g.gh[2 * lane + j] = hi;
+      g.gl[2 * lane + j] = (float)(v - hi);
+      g.b[2 * lane + j] = bb[j];
+    }
+  }
+  __syncthreads();
+  if (tid < sizeof(Gates) / 16)
+    reinterpret_cast<uint4*>(w.gates + pl.i)[tid] = reinterpret_cast<const uint4*>(&g)[tid];
+
+  const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
+  float acc[8][4];
+  lower_product<NI, NP>(acc, Kt, Kt, strip, lane);
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+    if (t < 2 * strip + 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r0 + (e >> 1) * 8, j = 8 * t + c0 + (e & 1);
+        M[i * kF + j] = j < i ? g.b[i] * decay_between(g, i, j) * acc[t][e] : 0.f;
+      }
+  __syncthreads();
+  if (tid < kC) {  // column j of the inverse of the diagonal block from row o on
+    const int o = tid & 48, j = tid & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == j ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 0; l < i; ++l) s = fmaf(-M[(o + i) * kF + o + l], x[l], s);
+      x[i] = s;
+      X[(o + i) * kF + o + j] = s;
+    }
+  }
+  __syncthreads();
+  {  // blocks (1, 0) and (3, 2): 64 threads each, four columns of a row a thread
+    const int o = (tid >> 6) * 32, r = (tid & 63) >> 2, c = (tid & 3) * 4;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int l = 0; l < 16; ++l) {
+      const float m = M[(o + 16 + r) * kF + o + l];
+      const float4 x = *reinterpret_cast<const float4*>(X + (o + l) * kF + o + c);
+      s[0] = fmaf(m, x.x, s[0]), s[1] = fmaf(m, x.y, s[1]);
+      s[2] = fmaf(m, x.z, s[2]), s[3] = fmaf(m, x.w, s[3]);
+    }
+    // M's upper part is free: the product waits there
+    *reinterpret_cast<float4*>(M + (o + r) * kF + o + 16 + c) = make_float4(s[0], s[1], s[2], s[3]);
+    __syncthreads();
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+    for (int l = 0; l < 16; ++l) {
+      const float m = -X[(o + 16 + r) * kF + o + 16 + l];
+      const float4 x = *reinterpret_cast<const float4*>(M + (o + l) * kF + o + 16 + c);
+      s[0] = fmaf(m, x.x, s[0]), s[1] = fmaf(m, x.y, s[1]);
+      s[2] = fmaf(m, x.z, s[2]), s[3] = fmaf(m, x.w, s[3]);
+    }
+    *reinterpret_cast<float4*>(X + (o + 16 + r) * kF + o + c) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(X + (o + r) * kF + o + 16 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  {  // the block of rows 32.., columns ..31: eight columns of a row a thread
+    const int r = tid >> 2, c = (tid & 3) * 8;
+    float s[8];
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      const float* L = pass == 0 ? M + (32 + r) * kF : X + (32 + r) * kF + 32;
+      const float* R = pass == 0 ? X + c : M + 32 + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = 0.f;
+#pragma unroll 8
+      for (int l = 0; l < 32; ++l) {
+        const float m = L[l];
+        const float4 u = *reinterpret_cast<const float4*>(R + l * kF);
+        const float4 v = *reinterpret_cast<const float4*>(R + l * kF + 4);
+        s[0] = fmaf(m, u.x, s[0]), s[1] = fmaf(m, u.y, s[1]);
+        s[2] = fmaf(m, u.z, s[2]), s[3] = fmaf(m, u.w, s[3]);
+        s[4] = fmaf(m, v.x, s[4]), s[5] = fmaf(m, v.y, s[5]);
+        s[6] = fmaf(m, v.z, s[6]), s[7] = fmaf(m, v.w, s[7]);
+      }
+      float* to = pass == 0 ? M + r * kF + 32 + c : X + (32 + r) * kF + c;
+      const float sg = pass == 0 ? 1.f : -1.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to[e] = sg * s[e];
+      if (pass == 0) __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) X[r * kF + 32 + c + e] = 0.f;
+  }
+  __syncthreads();
+  bf16* const xp = w.X + pl.i * (3 * kC * kC);
+  for (int i = tid; i < kC * 8; i += kPrepThreads) {
+    const float* s = X + (i >> 3) * kF + (i & 7) * 8;
+    uint32_t p[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2<3>(s[2 * e], s[2 * e + 1], p[e]);
+#pragma unroll
+    for (int l = 0; l < 3; ++l)
+      *reinterpret_cast<uint4*>(xp + l * kC * kC + i * 8) =
+          make_uint4(p[0][l], p[1][l], p[2][l], p[3][l]);
+  }
+  if constexpr (BWD) {
+    // E^T[p][j] = sum_{i >= j} dy[i][p] scale e^(G_i - G_j) q_i . k_j
+    lower_product<NI, NP>(acc, Kt + NI * kC * LD, Kt, strip, lane);
+    __syncthreads();  // X and M are read: their place takes the planes; K's takes dy
+    bf16* const at = reinterpret_cast<bf16*>(M);
+    static_assert(3 * kC * kTP * 2 <= 2 * kC * kF * 4, "the planes fit");
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = r0 + e * 8, j = 8 * t + c0;
+        float v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          if (t < 2 * strip + 2 && j + f <= i)
+            v[f] = d.scale * decay_between(g, i, j + f) * acc[t][2 * e + f];
+        uint32_t p[3];
+        split2<3>(v[0], v[1], p);
+#pragma unroll
+        for (int l = 0; l < 3; ++l)
+          *reinterpret_cast<uint32_t*>(at + l * kC * kTP + i * kTP + j) = p[l];
+      }
+    bf16* const yt = Kt;
+    for (int p0 = 0; p0 < d.Ps; p0 += kC) {
+      load_tile<T, kC, kTP, kPrepThreads>(
+          yt, dy + (((int64_t)pl.b * d.T + t0) * d.H + pl.h) * d.P + p0, (int64_t)d.H * d.P, rv,
+          d.P - p0, d.vdy);
+      __syncthreads();
+      if (p0 + strip * 16 < d.Ps) {
+        float e[8][4];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) e[t][x] = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          uint32_t a[NI][4];
+#pragma unroll
+          for (int p = 0; p < NI; ++p) a_cols<kTP>(a[p], yt + p * kC * kTP, strip * 16, kb * 16, lane);
+#pragma unroll
+          for (int np = 0; np <= kb; ++np)
+            mma_planes<NI, 3, 3>(e[2 * np], e[2 * np + 1], a, [&](int j, uint32_t(&r)[4]) {
+              b_cols<kTP>(r, at + j * kC * kTP, np * 16, kb * 16, lane);
+            });
+        }
+        float* to = w.E + (pl.i * d.Ps + p0 + r0) * kC + c0;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          *reinterpret_cast<float2*>(to + 8 * t) = make_float2(e[t][0], e[t][1]);
+          *reinterpret_cast<float2*>(to + 8 * kC + 8 * t) = make_float2(e[t][2], e[t][3]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// --------------------------------------------------------------------- chain
+
+constexpr int kChainThreads = 128;
+
+template <typename T, int NP>
+constexpr size_t chain_stage() {
+  return sizeof(Gates) + (size_t)planes_of<T>() * kC * (NP + 8) * 2 +
+         (size_t)kC * raw_pitch<T>() * sizeof(T) + (size_t)3 * kC * kTP * 2;
+}
+template <typename T, int NP, bool ASYNC>
+constexpr size_t chain_smem() { return chain_stage<T, NP>() * (ASYNC ? 2 : 1); }
+
+// A state strip (16 rows of a warp, NP columns) from or to rows of N floats.
+template <int NP>
+__device__ __forceinline__ void load_state(float (&S)[NP / 8][4], const float* src, int rows, int N,
+                                           int lane) {
+  const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+  for (int t = 0; t < NP / 8; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
+      S[t][e] = src && i < rows && j < N ? src[(int64_t)i * N + j] : 0.f;
+    }
+}
+template <int NP>
+__device__ __forceinline__ void store_state(float* dst, const float (&S)[NP / 8][4], int rows, int N,
+                                            int lane) {
+  const int r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+  for (int t = 0; t < NP / 8; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
+      if (i < rows && j < N) dst[(int64_t)i * N + j] = S[t][e];
+    }
+}
+// A strip of NT tiles to rows of 8 NT floats of the workspace.
+template <int NT>
+__device__ __forceinline__ void store_strip(float* dst, const float (&S)[NT][4], int lane) {
+  float* p = dst + (lane >> 2) * (8 * NT) + (lane & 3) * 2;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    *reinterpret_cast<float2*>(p + 8 * t) = make_float2(S[t][0], S[t][1]);
+    *reinterpret_cast<float2*>(p + 64 * NT + 8 * t) = make_float2(S[t][2], S[t][3]);
+  }
+}
+
+// The chain over a head's chunks: 64 value rows a block, a strip of 16 rows a warp with
+// its state in registers (16 x NP fp32, an accumulator).  A chunk is three products,
+//     Z^T = S K^T,   U^T = (b (V - e^G Z))^T X^T,   S <- e^G63 S + (e^(G63 - G) U)^T K,
+// each left operand formed from the last accumulator, so the only traffic between them
+// is the shared tiles of K, V and X, copied while the chunk before is at work (ASYNC).
+// KEEP: also writes b e^G Z, for the backward.
+template <typename T, int NP, bool ASYNC, bool KEEP>
+__global__ void __launch_bounds__(kChainThreads)
+    k_delta_chain(DeltaDims d, const T* __restrict__ k, const T* __restrict__ v,
+                  const float* __restrict__ init, const int* __restrict__ lengths, DeltaWs w,
+                  float* __restrict__ final_states) {
+  constexpr int NI = planes_of<T>(), LD = NP + 8, RP = raw_pitch<T>(), M = max2(NI, 3);
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
+  const int ptiles = (d.Ps + kC - 1) / kC;
+  const int p0 = (int)(blockIdx.x % ptiles) * kC;
+  const int64_t bh = blockIdx.x / ptiles;
+  const int h = (int)(bh % d.H), b = (int)(bh / d.H);
+  const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
+  const int row = p0 + strip * 16;  // this warp's first value row
+  const bool active = row < d.Ps;
+  const T* const kg = k + b * d.kb + (int64_t)(h / d.rep) * d.N;
+  const T* const vg = v + b * d.vb + (int64_t)h * d.P + p0;
+
+  auto stage = [&](int s) { return smem + s * chain_stage<T, NP>(); };
+  auto fetch = [&](int c, int s) {
+    unsigned char* at = stage(s);
+    const Gates* src = w.gates + bh * d.nc + c;
+    if (threadIdx.x < sizeof(Gates) / 16)
+      cp_async<16>(at + threadIdx.x * 16, reinterpret_cast<const char*>(src) + threadIdx.x * 16);
+    bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
+    T* vt = reinterpret_cast<T*>(kt + NI * kC * LD);
+    bf16* xt = reinterpret_cast<bf16*>(vt + kC * RP);
+    const int t0 = c * kC, rv = min(kC, n - t0);
+    if constexpr (ASYNC) {
+      copy_tile<NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N);
+      copy_tile<kC, kTP, kChainThreads>(vt, vg + t0 * d.vs, d.vs, rv, d.P - p0);
+    } else {
+      load_tile<T, NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N, d.vk);
+      load_raw<T, kChainThreads>(vt, vg + t0 * d.vs, d.vs, rv, d.P - p0, d.vv);
+    }
+    copy_x<kChainThreads>(xt, w.X + (bh * d.nc + c) * (3 * kC * kC));
+    cp_commit();
+  };
+
+  float S[NP / 8][4];
+  load_state<NP>(S, init && active ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  if (ASYNC && nc > 0) fetch(0, 0);
+  for (int c = 0; c < nc; ++c) {
+    const int s = ASYNC ? c & 1 : 0;
+    if constexpr (ASYNC) {
+      if (c + 1 < nc) {
+        fetch(c + 1, s ^ 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
+    } else {
+      fetch(c, 0);
+      cp_wait<0>();
+    }
+    __syncthreads();
+    if (active) {
+      const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
+      const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
+      const T* vt = reinterpret_cast<const T*>(kt + NI * kC * LD);
+      const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
+      const int64_t at = bh * d.nc + c;
+      store_strip<NP / 8>(w.S0 + (at * d.Ps + row) * NP, S, lane);
+      float r[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < NP / 16; ++kk) {
+        uint32_t a[3][4];
+        a_from_acc<3>(a, S, kk);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          mma_planes<3, NI, M>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
+          });
+      }
+      // r = b (v - e^G z), of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
+      float z[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 8 * t + t2 + (e & 1), p = strip * 16 + g8 + (e >> 1) * 8;
+          const float bi = g.b[i];
+          z[t][e] = bi * ex2(g.gh[i]) * r[t][e];
+          r[t][e] = fmaf(bi, to_f(vt[i * RP + p]), -z[t][e]);
+        }
+      if constexpr (KEEP) store_strip<8>(w.Zb + (at * d.Ps + row) * kC, z, lane);
+      float u[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t a[3][4];
+        a_from_acc<3>(a, r, kb);
+#pragma unroll
+        for (int np = kb; np < 4; ++np)
+          mma_planes<3, 3, 3>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+          });
+      }
+      store_strip<8>(w.U + (at * d.Ps + row) * kC, u, lane);
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = decay_between(g, kC - 1, 8 * t + t2 + e);
+          u[t][e] *= f;
+          u[t][2 + e] *= f;
+        }
+      const float end = ex2(g.gh[kC - 1]);
+#pragma unroll
+      for (int t = 0; t < NP / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][e] *= end;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t a[3][4];
+        a_from_acc<3>(a, u, kb);
+#pragma unroll
+        for (int np = 0; np < NP / 16; ++np)
+          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
+          });
+      }
+    }
+    __syncthreads();
+  }
+  if (final_states && active)
+    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+}
+
+// ----------------------------------------------------------------------- out
+
+constexpr int kOutThreads = 128;
+
+// Planes of values that only reach an output of type TO.
+template <typename TO>
+constexpr int out_planes() { return sizeof(TO) == 2 ? 2 : 3; }
+
+template <typename T, typename TO, int NP>
+constexpr size_t out_smem() {
+  constexpr size_t raw = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+  constexpr size_t st = (size_t)out_planes<TO>() * kC * (NP + 8) * 2;
+  return sizeof(Gates) + raw + (raw > st ? raw : st) + (size_t)out_planes<TO>() * kC * kTP * 2;
+}
+
+// Y of one chunk of one head, 16 tokens a warp.
+template <typename T, typename TO, int NP>
+__global__ void __launch_bounds__(kOutThreads)
+    k_delta_out(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
+                const int* __restrict__ lengths, DeltaWs w, TO* __restrict__ y) {
+  constexpr int NI = planes_of<T>(), NL = out_planes<TO>(), LD = NP + 8;
+  constexpr size_t raw = (size_t)NI * kC * LD, st = (size_t)NL * kC * LD;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Gates& g = *reinterpret_cast<Gates*>(smem);
+  bf16* const qt = reinterpret_cast<bf16*>(smem + sizeof(Gates));
+  bf16* const kt = qt + raw;  // and the state's planes after the keys'
+  bf16* const ut = kt + (raw > st ? raw : st);
+  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  const Place pl = place(d, blockIdx.x);
+  const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
+  const int rows = min(kC, d.T - t0);  // of the output; tokens from n on are padding
+  TO* const yo = y + (((int64_t)pl.b * d.T + t0) * d.H + pl.h) * d.P;
+  const int64_t ys = (int64_t)d.H * d.P;
+  if (t0 >= n) {
+    for (int i = tid; i < rows * d.P; i += kOutThreads) yo[i / d.P * ys + i % d.P] = from_f<TO>(0.f);
+    return;
+  }
+  const int rv = min(kC, n - t0), grp = pl.h / d.rep;
+  load_tile<T, NP, LD, kOutThreads>(qt, q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
+                                    d.N, d.vq);
+  load_tile<T, NP, LD, kOutThreads>(kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
+                                    d.N, d.vk);
+  if (tid < sizeof(Gates) / 16)
+    reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + pl.i)[tid];
+  __syncthreads();
+  const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
+  float s[8][4];
+  lower_product<NI, NP>(s, qt, kt, strip, lane);
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = r0 + (e >> 1) * 8, j = 8 * t + c0 + (e & 1);
+      s[t][e] = j <= i ? d.scale * decay_between(g, i, j) * s[t][e] : 0.f;
+    }
+  const float f0 = d.scale * ex2(g.gh[r0]), f1 = d.scale * ex2(g.gh[r0 + 8]);
+  for (int p0 = 0; p0 < d.Ps; p0 += kC) {
+    __syncthreads();
+    const int pr = min(kC, d.Ps - p0);
+    load_split<NL, NP, LD, kOutThreads>(kt, w.S0 + (pl.i * d.Ps + p0) * NP, pr);
+    load_split<NL, kC, kTP, kOutThreads>(ut, w.U + (pl.i * d.Ps + p0) * kC, pr);
+    __syncthreads();
+    float o[8][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < NP / 16; ++kk) {
+      uint32_t a[NI][4];
+#pragma unroll
+      for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
+        mma_planes<NI, NL, max2(NI, NL)>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
+        });
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+      if (kb <= strip) {
+        uint32_t a[NL][4];
+        a_from_acc<NL>(a, s, kb);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          mma_planes<NL, NL, NL>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<kTP>(x, ut + j * kC * kTP, np * 16, kb * 16, lane);
+          });
+      }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r0 + (e >> 1) * 8, p = p0 + 8 * t + c0 + (e & 1);
+        if (i < rows && p < d.P) yo[i * ys + p] = from_f<TO>(i < rv ? o[t][e] : 0.f);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------- back
+
+template <typename T, int NP>
+constexpr size_t back_stage() {
+  return chain_stage<T, NP>() + (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+}
+template <typename T, int NP, bool ASYNC>
+constexpr size_t back_smem() { return back_stage<T, NP>() * (ASYNC ? 2 : 1); }
+
+// The chain of the backward, from the last chunk to the first, with the gradient of the
+// state behind the chunk in registers:
+//     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
+//     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K.
+template <typename T, int NP, bool ASYNC>
+__global__ void __launch_bounds__(kChainThreads)
+    k_delta_back(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
+                 const T* __restrict__ dy, const float* __restrict__ dfinal,
+                 const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit) {
+  constexpr int NI = planes_of<T>(), LD = NP + 8, RP = raw_pitch<T>(), M = max2(NI, 3);
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
+  const int ptiles = (d.Ps + kC - 1) / kC;
+  const int p0 = (int)(blockIdx.x % ptiles) * kC;
+  const int64_t bh = blockIdx.x / ptiles;
+  const int h = (int)(bh % d.H), b = (int)(bh / d.H);
+  const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
+  const int row = p0 + strip * 16;
+  const bool active = row < d.Ps;
+  const T* const qg = q + b * d.qb + (int64_t)(h / d.rep) * d.N;
+  const T* const kg = k + b * d.kb + (int64_t)(h / d.rep) * d.N;
+  const int64_t ys = (int64_t)d.H * d.P;
+  const T* const yg = dy + b * (int64_t)d.T * ys + (int64_t)h * d.P + p0;
+
+  auto stage = [&](int s) { return smem + s * back_stage<T, NP>(); };
+  auto fetch = [&](int c, int s) {
+    unsigned char* at = stage(s);
+    const Gates* src = w.gates + bh * d.nc + c;
+    if (threadIdx.x < sizeof(Gates) / 16)
+      cp_async<16>(at + threadIdx.x * 16, reinterpret_cast<const char*>(src) + threadIdx.x * 16);
+    bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
+    bf16* qt = kt + NI * kC * LD;
+    T* yt = reinterpret_cast<T*>(qt + NI * kC * LD);
+    bf16* xt = reinterpret_cast<bf16*>(yt + kC * RP);
+    const int t0 = c * kC, rv = min(kC, n - t0);
+    if constexpr (ASYNC) {
+      copy_tile<NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N);
+      copy_tile<NP, LD, kChainThreads>(qt, qg + t0 * d.qs, d.qs, rv, d.N);
+      copy_tile<kC, kTP, kChainThreads>(yt, yg + t0 * ys, ys, rv, d.P - p0);
+    } else {
+      load_tile<T, NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N, d.vk);
+      load_tile<T, NP, LD, kChainThreads>(qt, qg + t0 * d.qs, d.qs, rv, d.N, d.vq);
+      load_raw<T, kChainThreads>(yt, yg + t0 * ys, ys, rv, d.P - p0, d.vdy);
+    }
+    copy_x<kChainThreads>(xt, w.X + (bh * d.nc + c) * (3 * kC * kC));
+    cp_commit();
+  };
+
+  float S[NP / 8][4];
+  load_state<NP>(S, dfinal && active ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N,
+                 lane);
+  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  if (ASYNC && nc > 0) fetch(nc - 1, 0);
+  for (int c = nc - 1; c >= 0; --c) {
+    const int s = ASYNC ? (nc - 1 - c) & 1 : 0;
+    if constexpr (ASYNC) {
+      if (c > 0) {
+        fetch(c - 1, s ^ 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
+    } else {
+      fetch(c, 0);
+      cp_wait<0>();
+    }
+    __syncthreads();
+    if (active) {
+      const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
+      const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
+      const bf16* qt = kt + NI * kC * LD;
+      const T* yt = reinterpret_cast<const T*>(qt + NI * kC * LD);
+      const bf16* xt = reinterpret_cast<const bf16*>(yt + kC * RP);
+      const int64_t at = bh * d.nc + c;
+      store_strip<NP / 8>(w.dS + (at * d.Ps + row) * NP, S, lane);
+      const float* ep = w.E + (at * d.Ps + row + g8) * kC + t2;
+      float r[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < NP / 16; ++kk) {
+        uint32_t a[3][4];
+        a_from_acc<3>(a, S, kk);
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          mma_planes<3, NI, M>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
+          });
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = decay_between(g, kC - 1, 8 * t + t2 + e);
+          r[t][e] *= f;
+          r[t][2 + e] *= f;
+        }
+      store_strip<8>(w.Zd + (at * d.Ps + row) * kC, r, lane);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float2 e0 = *reinterpret_cast<const float2*>(ep + 8 * t);
+        const float2 e1 = *reinterpret_cast<const float2*>(ep + 8 * kC + 8 * t);
+        r[t][0] += e0.x, r[t][1] += e0.y, r[t][2] += e1.x, r[t][3] += e1.y;
+      }
+      float u[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
+        uint32_t a[3][4];
+        a_from_acc<3>(a, r, kb);
+#pragma unroll
+        for (int np = 0; np <= kb; ++np)
+          mma_planes<3, 3, 3>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+          });
+      }
+      store_strip<8>(w.dR + (at * d.Ps + row) * kC, u, lane);
+      // r = scale e^G dY^T, u = -b e^G dR^T
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 8 * t + t2 + (e & 1), p = strip * 16 + g8 + (e >> 1) * 8;
+          const float f = ex2(g.gh[i]);
+          r[t][e] = d.scale * f * to_f(yt[i * RP + p]);
+          u[t][e] *= -g.b[i] * f;
+        }
+      const float end = ex2(g.gh[kC - 1]);
+#pragma unroll
+      for (int t = 0; t < NP / 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][e] *= end;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t a[3][4];
+        a_from_acc<3>(a, u, kb);
+#pragma unroll
+        for (int np = 0; np < NP / 16; ++np)
+          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
+          });
+        a_from_acc<3>(a, r, kb);
+#pragma unroll
+        for (int np = 0; np < NP / 16; ++np)
+          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, qt + j * kC * LD, np * 16, kb * 16, lane);
+          });
+      }
+    }
+    __syncthreads();
+  }
+  if (dinit && active) store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+}
+
+// ---------------------------------------------------------------------- grad
+
+constexpr int kGradThreads = 256;
+
+// Sums of the tokens of a chunk that the gate's gradient is made of.
+struct GradSums {
+  float row[2][kC];   // rows of dAqk Aqk - W M, a column half each
+  float col[4][kC];   // columns of the same, a row strip each
+  float qd[2][kC];    // scale e^G q . (dY S0), a half of the key columns each
+  float part[4][3][kC];  // U . Zd, dR . Zb, dR . U, of a quarter of the value rows each
+  float dot[8];       // <dS, S0>, a warp each
+};
+
+template <typename T, typename TO, int NP>
+constexpr size_t grad_smem() {
+  constexpr size_t row = kC * (NP + 8) * 2, tok = kC * kTP * 2, ni = planes_of<T>();
+  constexpr size_t a = ni * tok + 6 * tok + 3 * row;                     // while value tiles pass
+  constexpr size_t b = 2 * ni * row + 2 * out_planes<TO>() * tok;        // at the head's end
+  return sizeof(Gates) + sizeof(GradSums) + (a > b ? a : b);
+}
+
+// dq, dk, dv, ddt and dbeta of one chunk of the heads of one head block.  Eight warps:
+// 16 tokens by half the key columns (or half the chunk's tokens) each.  With
+// dAqk = dY U^T (j <= i) and W = dR U^T (j < i),
+//     dq = scale e^G dY S0 + P1 K,                       P1 = scale e^(G_i - G_j) dAqk
+//     dk = e^(G63 - G) U dS - b e^G dR S0 + P1^T Q + (P2 + P2^T) K,
+//                                                        P2 = -b_i e^(G_i - G_j) W
+//     dv = b dR,   dbeta = (1 - b) dR . U   (as b_i dL/db_i = W_ii)
+// and the gradient of G_i is the row sum less the column sum of dAqk Aqk - W M, plus
+// scale e^G q . (dY S0) - dR . (b e^G S0 k) - U . (e^(G63 - G) dS k), where what the
+// last token's G takes from the state behind the chunk is added.  Row and column sums
+// are of the same products, so that what cancels in their difference cancels exactly.
+template <typename T, typename TO, int NP>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    k_delta_grad(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
+                 const T* __restrict__ dt, const float* __restrict__ dt_bias,
+                 const float* __restrict__ A, const T* __restrict__ dy,
+                 const int* __restrict__ lengths, DeltaWs w, TO* __restrict__ dq,
+                 TO* __restrict__ dk, TO* __restrict__ dv, TO* __restrict__ ddt,
+                 TO* __restrict__ dbeta) {
+  constexpr int NI = planes_of<T>(), NL = out_planes<TO>(), LD = NP + 8, HT = NP / 16;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Gates& g = *reinterpret_cast<Gates*>(smem);
+  GradSums& sm = *reinterpret_cast<GradSums*>(smem + sizeof(Gates));
+  bf16* const base = reinterpret_cast<bf16*>(smem + sizeof(Gates) + sizeof(GradSums));
+  bf16* const yt = base;                 // dY [token][p]
+  bf16* const rt = yt + NI * kC * kTP;   // dR [p][token]
+  bf16* const ut = rt + 3 * kC * kTP;    // U [p][token]
+  bf16* const st = ut + 3 * kC * kTP;    // S0, then dS [p][n]
+  bf16* const qt = base;                 // at the head's end
+  bf16* const kt = qt + NI * kC * LD;
+  bf16* const p1 = kt + NI * kC * LD;
+  bf16* const p2 = p1 + NL * kC * kTP;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, strip = warp & 3, half = warp >> 2;
+  int64_t blk = blockIdx.x;
+  const int c = (int)(blk % d.nc);
+  blk /= d.nc;
+  const int hb = (int)(blk % d.nb);
+  blk /= d.nb;
+  const int grp = (int)(blk % d.G), b = (int)(blk / d.G);
+  const int n = tokens_of(d, lengths, b), t0 = c * kC, rows = min(kC, d.T - t0);
+  const int rv = max(0, min(kC, n - t0));
+  const int h0 = grp * d.rep + (int)((int64_t)d.rep * hb / d.nb);
+  const int h1 = grp * d.rep + (int)((int64_t)d.rep * (hb + 1) / d.nb);
+  const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
+  const int64_t ys = (int64_t)d.H * d.P;
+
+  float tq[HT][4], tk[HT][4];  // dq, dk over the heads: columns half * NP / 2 + 8 t + c0
+#pragma unroll
+  for (int t = 0; t < HT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) tq[t][e] = tk[t][e] = 0.f;
+
+  for (int h = h0; h < h1; ++h) {
+    const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
+    const int64_t tok = (int64_t)b * d.T + t0;
+    if (rv == 0) {  // padding only
+      for (int i = tid; i < rows * d.P; i += kGradThreads)
+        dv[(tok + i / d.P) * ys + (int64_t)h * d.P + i % d.P] = from_f<TO>(0.f);
+      if (tid < rows) {
+        ddt[(tok + tid) * d.H + h] = from_f<TO>(0.f);
+        dbeta[(tok + tid) * d.H + h] = from_f<TO>(0.f);
+      }
+      if (tid < 2) w.part[at * 2 + tid] = 0.f;
+      continue;
+    }
+    __syncthreads();
+    if (tid < sizeof(Gates) / 16)
+      reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + at)[tid];
+    float da[4][4], wm[4][4], dqh[HT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) da[t][e] = wm[t][e] = 0.f;
+#pragma unroll
+    for (int t = 0; t < HT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dqh[t][e] = 0.f;
+    float su = 0.f, sr = 0.f, sw = 0.f, dot = 0.f;
+    for (int p0 = 0; p0 < d.Ps; p0 += kC) {
+      const int pr = min(kC, d.Ps - p0);
+      __syncthreads();
+      load_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
+                                          d.vdy);
+      load_split<3, NP, LD, kGradThreads>(st, w.S0 + (at * d.Ps + p0) * NP, pr);
+      {  // token tid & 63, every fourth value row
+        const int i = tid & 63;
+#pragma unroll 4
+        for (int p = tid >> 6; p < kC; p += 4) {
+          float r = 0.f, u = 0.f;
+          if (p < pr) {
+            const size_t o = (size_t)(at * d.Ps + p0 + p) * kC + i;
+            r = w.dR[o], u = w.U[o];
+            su = fmaf(u, w.Zd[o], su);
+            sr = fmaf(r, w.Zb[o], sr);
+            sw = fmaf(r, u, sw);
+          }
+          uint32_t x[3];
+          split2<3>(r, u, x);
+#pragma unroll
+          for (int l = 0; l < 3; ++l) {
+            reinterpret_cast<uint16_t*>(rt)[l * kC * kTP + p * kTP + i] = (uint16_t)(x[l] & 0xffffu);
+            reinterpret_cast<uint16_t*>(ut)[l * kC * kTP + p * kTP + i] = (uint16_t)(x[l] >> 16);
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * kC; i += kGradThreads) {  // dv = b dR
+        const int t = i / kC, p = i % kC;
+        if (p0 + p < d.P) {
+          float v = 0.f;
+          if (t < rv)
+#pragma unroll
+            for (int l = 2; l >= 0; --l) v += to_f(rt[l * kC * kTP + p * kTP + t]);
+          dv[(tok + t) * ys + (int64_t)h * d.P + p0 + p] = from_f<TO>(v * g.b[t]);
+        }
+      }
+      const float sx0 = -g.b[r0] * ex2(g.gh[r0]), sx1 = -g.b[r0 + 8] * ex2(g.gh[r0 + 8]);
+      const float sk0 = decay_between(g, kC - 1, r0), sk1 = decay_between(g, kC - 1, r0 + 8);
+      // a left operand of two or three planes with its rows scaled
+      auto scaled = [&](uint32_t(&a)[NL][4], const bf16* t, int kb, float f0, float f1) {
+        uint32_t x[3][4];
+#pragma unroll
+        for (int l = 0; l < 3; ++l) a_cols<kTP>(x[l], t + l * kC * kTP, strip * 16, kb * 16, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo = 0.f, hi = 0.f;
+#pragma unroll
+          for (int l = 2; l >= 0; --l) {
+            lo += __uint_as_float(x[l][e] << 16);
+            hi += __uint_as_float(x[l][e] & 0xffff0000u);
+          }
+          const float f = e & 1 ? f1 : f0;
+          uint32_t pp[NL];
+          split2<NL>(lo * f, hi * f, pp);
+#pragma unroll
+          for (int l = 0; l < NL; ++l) a[l][e] = pp[l];
+        }
+      };
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t ya[NI][4], ra[3][4], xa[NL][4];
+#pragma unroll
+        for (int l = 0; l < NI; ++l) a_rows<kTP>(ya[l], yt + l * kC * kTP, strip * 16, kb * 16, lane);
+#pragma unroll
+        for (int l = 0; l < 3; ++l) a_cols<kTP>(ra[l], rt + l * kC * kTP, strip * 16, kb * 16, lane);
+        scaled(xa, rt, kb, sx0, sx1);
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+          if (half * 2 + np <= strip) {
+            auto ub = [&](int j, uint32_t(&x)[4]) {
+              b_cols<kTP>(x, ut + j * kC * kTP, half * 32 + np * 16, kb * 16, lane);
+            };
+            mma_planes<NI, 3, 3>(da[2 * np], da[2 * np + 1], ya, ub);
+            mma_planes<3, 3, 3>(wm[2 * np], wm[2 * np + 1], ra, ub);
+          }
+#pragma unroll
+        for (int np = 0; np < HT / 2; ++np) {
+          auto sb = [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, st + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+          };
+          mma_planes<NI, 3, 3>(dqh[2 * np], dqh[2 * np + 1], ya, sb);
+          mma_planes<NL, NL, NL>(tk[2 * np], tk[2 * np + 1], xa, sb);
+        }
+      }
+      __syncthreads();
+      {  // dS over S0's place, and <dS, S0>
+        const float* s0 = w.S0 + (at * d.Ps + p0) * NP;
+        const float* ds = w.dS + (at * d.Ps + p0) * NP;
+        for (int i = tid; i < kC * (NP / 4); i += kGradThreads) {
+          const int r = i / (NP / 4), cc = i % (NP / 4) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < pr) {
+            v = *reinterpret_cast<const float4*>(ds + (size_t)r * NP + cc);
+            const float4 s = *reinterpret_cast<const float4*>(s0 + (size_t)r * NP + cc);
+            dot = fmaf(v.x, s.x, fmaf(v.y, s.y, fmaf(v.z, s.z, fmaf(v.w, s.w, dot))));
+          }
+          uint32_t x[NL], z[NL];
+          split2<NL>(v.x, v.y, x);
+          split2<NL>(v.z, v.w, z);
+#pragma unroll
+          for (int l = 0; l < NL; ++l)
+            *reinterpret_cast<uint2*>(st + l * kC * LD + r * LD + cc) = make_uint2(x[l], z[l]);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t xa[NL][4];
+        scaled(xa, ut, kb, sk0, sk1);
+#pragma unroll
+        for (int np = 0; np < HT / 2; ++np)
+          mma_planes<NL, NL, NL>(tk[2 * np], tk[2 * np + 1], xa, [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, st + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+          });
+      }
+    }
+    __syncthreads();
+    load_tile<T, NP, LD, kGradThreads>(qt, q + b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
+                                       d.N, d.vq);
+    load_tile<T, NP, LD, kGradThreads>(kt, k + b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
+                                       d.N, d.vk);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) sm.dot[warp] = dot;
+    sm.part[tid >> 6][0][tid & 63] = su;
+    sm.part[tid >> 6][1][tid & 63] = sr;
+    sm.part[tid >> 6][2][tid & 63] = sw;
+    __syncthreads();
+    {  // the pairs of this warp: rows of its strip, 32 columns from half * 32 on
+      float qk[4][4], kk[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qk[t][e] = kk[t][e] = 0.f;
+      for (int x = 0; x < NP / 16; ++x) {
+        uint32_t qa[NI][4], ka[NI][4];
+#pragma unroll
+        for (int l = 0; l < NI; ++l) {
+          a_rows<LD>(qa[l], qt + l * kC * LD, strip * 16, x * 16, lane);
+          a_rows<LD>(ka[l], kt + l * kC * LD, strip * 16, x * 16, lane);
+        }
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+          if (half * 2 + np <= strip) {
+            auto kb = [&](int j, uint32_t(&r)[4]) {
+              b_rows<LD>(r, kt + j * kC * LD, half * 32 + np * 16, x * 16, lane);
+            };
+            mma_planes<NI, NI, NI>(qk[2 * np], qk[2 * np + 1], qa, kb);
+            mma_planes<NI, NI, NI>(kk[2 * np], kk[2 * np + 1], ka, kb);
+          }
+      }
+      float rs[2] = {0.f, 0.f}, cs[4][2];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        cs[t][0] = cs[t][1] = 0.f;
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int i = r0 + e2 * 8, j = half * 32 + 8 * t + c0;
+          float v1[2], v2[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int e = 2 * e2 + f;
+            const float dec = j + f <= i ? decay_between(g, i, j + f) : 0.f;
+            const float bd = j + f < i ? g.b[i] * dec : 0.f;
+            const float a1 = d.scale * dec;
+            v1[f] = a1 * da[t][e];
+            v2[f] = -bd * wm[t][e];
+            const float pair = v1[f] * qk[t][e] + v2[f] * kk[t][e];
+            rs[e2] += pair;
+            cs[t][f] += pair;
+          }
+          uint32_t x1[NL], x2[NL];
+          split2<NL>(v1[0], v1[1], x1);
+          split2<NL>(v2[0], v2[1], x2);
+#pragma unroll
+          for (int l = 0; l < NL; ++l) {
+            *reinterpret_cast<uint32_t*>(p1 + l * kC * kTP + i * kTP + j) = x1[l];
+            *reinterpret_cast<uint32_t*>(p2 + l * kC * kTP + i * kTP + j) = x2[l];
+          }
+        }
+      }
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        rs[e2] += __shfl_xor_sync(0xffffffffu, rs[e2], 1);
+        rs[e2] += __shfl_xor_sync(0xffffffffu, rs[e2], 2);
+        if ((lane & 3) == 0) sm.row[half][r0 + e2 * 8] = rs[e2];
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float v = cs[t][f];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane < 4) sm.col[strip][half * 32 + 8 * t + c0 + f] = v;
+        }
+    }
+    {  // scale e^G q . (dY S0), and its part of dq
+      const float f0 = d.scale * ex2(g.gh[r0]), f1 = d.scale * ex2(g.gh[r0 + 8]);
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = r0 + (e >> 1) * 8, j = half * (NP / 2) + 8 * t + c0 + (e & 1);
+          float qv = 0.f;
+#pragma unroll
+          for (int l = NI - 1; l >= 0; --l) qv += to_f(qt[l * kC * LD + i * LD + j]);
+          const float v = dqh[t][e] * (e >> 1 ? f1 : f0);
+          tq[t][e] += v;
+          (e >> 1 ? s1 : s0) += v * qv;
+        }
+      s0 += __shfl_xor_sync(0xffffffffu, s0, 1), s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+      s0 += __shfl_xor_sync(0xffffffffu, s0, 2), s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+      if ((lane & 3) == 0) sm.qd[half][r0] = s0, sm.qd[half][r0 + 8] = s1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t a[NL][4], a2[NL][4];
+      if (kb <= strip) {
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          a_rows<kTP>(a[l], p1 + l * kC * kTP, strip * 16, kb * 16, lane);
+          a_rows<kTP>(a2[l], p2 + l * kC * kTP, strip * 16, kb * 16, lane);
+        }
+#pragma unroll
+        for (int np = 0; np < HT / 2; ++np) {
+          auto kbl = [&](int j, uint32_t(&x)[4]) {
+            b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+          };
+          mma_planes<NL, NI, max2(NL, NI)>(tq[2 * np], tq[2 * np + 1], a, kbl);
+          mma_planes<NL, NI, max2(NL, NI)>(tk[2 * np], tk[2 * np + 1], a2, kbl);
+        }
+      }
+      if (kb >= strip) {
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          a_cols<kTP>(a[l], p1 + l * kC * kTP, strip * 16, kb * 16, lane);
+          a_cols<kTP>(a2[l], p2 + l * kC * kTP, strip * 16, kb * 16, lane);
+        }
+#pragma unroll
+        for (int np = 0; np < HT / 2; ++np) {
+          mma_planes<NL, NI, max2(NL, NI)>(
+              tk[2 * np], tk[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+                b_cols<LD>(x, qt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+              });
+          mma_planes<NL, NI, max2(NL, NI)>(
+              tk[2 * np], tk[2 * np + 1], a2, [&](int j, uint32_t(&x)[4]) {
+                b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+              });
+        }
+      }
+    }
+    if (warp == 0) {  // the gates' gradients, two tokens a lane
+      float dg[2], wii[2], last = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int i = 2 * lane + x;
+        float u = 0.f, r = 0.f, ww = 0.f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
+        const float cols = ((sm.col[0][i] + sm.col[1][i]) + sm.col[2][i]) + sm.col[3][i];
+        dg[x] = ((sm.row[0][i] + sm.row[1][i]) - cols) + ((sm.qd[0][i] + sm.qd[1][i]) - r) - u;
+        wii[x] = ww;
+        last += u;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
+      float ss = 0.f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) ss += sm.dot[p];
+      last += ex2(g.gh[kC - 1]) * ss;
+      if (lane == 31) dg[1] += last;
+      // sums from each token on
+      dg[0] += dg[1];
+      float run = dg[0];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float dn = __shfl_down_sync(0xffffffffu, run, o);
+        if (lane + o < 32) run += dn;
+      }
+      const float after = run - dg[0];
+      float sa = 0.f, sb = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int i = 2 * lane + x;
+        const float v = dg[x] + after;
+        const int64_t o = (tok + i) * d.H + h;
+        if (i < rv) {
+          const float z = to_f(dt[o]) + (dt_bias ? dt_bias[h] : 0.f);
+          const float dz = v * A[h] * sigmoid(z);
+          sa = fmaf(v, softplus(z), sa);
+          sb += dz;
+          ddt[o] = from_f<TO>(dz);
+          dbeta[o] = from_f<TO>((1.f - g.b[i]) * wii[x]);
+        } else if (i < rows) {
+          ddt[o] = from_f<TO>(0.f);
+          dbeta[o] = from_f<TO>(0.f);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sb += __shfl_xor_sync(0xffffffffu, sb, o);
+      }
+      if (lane == 0) w.part[at * 2] = sa, w.part[at * 2 + 1] = sb;
+    }
+  }
+  // padding rows are zeros: their keys, queries, corrections and gradients are
+#pragma unroll
+  for (int t = 0; t < HT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = r0 + (e >> 1) * 8, j = half * (NP / 2) + 8 * t + c0 + (e & 1);
+      if (i < rows && j < d.N) {
+        const int64_t o = (((int64_t)b * d.T + t0 + i) * d.G + grp) * d.N + j;
+        if (d.nb == 1) {
+          dq[o] = from_f<TO>(tq[t][e]);
+          dk[o] = from_f<TO>(tk[t][e]);
+        } else {
+          const int64_t whole = (int64_t)d.B * d.T * d.G * d.N;
+          w.dqp[hb * whole + o] = tq[t][e];
+          w.dkp[hb * whole + o] = tk[t][e];
+        }
+      }
+    }
+}
+
+// dq and dk as the sums of the head blocks' parts.
+template <typename TO>
+__global__ void __launch_bounds__(256)
+    k_delta_sum(const float* __restrict__ qp, const float* __restrict__ kp, int nb, int64_t n,
+                TO* __restrict__ dq, TO* __restrict__ dk) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float a = 0.f, b = 0.f;
+    for (int l = 0; l < nb; ++l) a += qp[l * n + i], b += kp[l * n + i];
+    dq[i] = from_f<TO>(a);
+    dk[i] = from_f<TO>(b);
+  }
+}
+
+// dA and ddt_bias of a head from the sums of its chunks, in a fixed order.
+__global__ void __launch_bounds__(256)
+    k_delta_params(const float* __restrict__ part, int B, int H, int nc, float* __restrict__ dA,
+                   float* __restrict__ dbias) {
+  __shared__ float s[2][8];
+  const int h = blockIdx.x;
+  float a = 0.f, b = 0.f;
+  for (int64_t i = threadIdx.x; i < (int64_t)B * nc; i += 256) {
+    const float* p = part + ((i / nc * H + h) * nc + i % nc) * 2;
+    a += p[0], b += p[1];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if ((threadIdx.x & 31) == 0) s[0][threadIdx.x >> 5] = a, s[1][threadIdx.x >> 5] = b;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a = b = 0.f;
+    for (int i = 0; i < 8; ++i) a += s[0][i], b += s[1][i];
+    if (dA) dA[h] = a;
+    if (dbias) dbias[h] = b;
+  }
+}
+
+// ---------------------------------------------------------------------- host
+
+// One part for each block of the heads of a group, so that the gradient's blocks fill
+// the machine; each block sums its heads in registers.
+constexpr int kGradBlocks = 2 * 152;
+
+int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
+  if (!s || s->batch < 1 || s->seqlen < 1 || s->nheads < 1 || s->headdim < 1 || s->dstate < 1 ||
+      s->ngroups < 1 || s->nheads % s->ngroups != 0)
+    return SSD_ERR_INVALID_ARG;
+  if ((s->in_dtype != SSD_F32 && s->in_dtype != SSD_BF16) ||
+      (s->out_dtype != SSD_F32 && s->out_dtype != SSD_BF16))
+    return SSD_ERR_INVALID_ARG;
+  if (s->in_dtype == SSD_F32 && s->out_dtype == SSD_BF16) return SSD_ERR_UNSUPPORTED;
+  if (s->dstate > 128 || s->headdim > 256 || s->batch >= 65536 || s->nheads >= 65536 ||
+      s->seqlen >= (1 << 30))
+    return SSD_ERR_UNSUPPORTED;
+  const int64_t gn = s->ngroups * s->dstate, hp = s->nheads * s->headdim;
+  if ((s->q_row_stride && s->q_row_stride < gn) || (s->k_row_stride && s->k_row_stride < gn) ||
+      (s->v_row_stride && s->v_row_stride < hp) || s->q_batch_stride < 0 ||
+      s->k_batch_stride < 0 || s->v_batch_stride < 0)
+    return SSD_ERR_INVALID_ARG;
+  d->B = (int)s->batch, d->T = (int)s->seqlen, d->H = (int)s->nheads, d->G = (int)s->ngroups;
+  d->P = (int)s->headdim, d->N = (int)s->dstate;
+  d->rep = d->H / d->G;
+  d->nc = (d->T + kC - 1) / kC;
+  d->Ps = (d->P + 15) / 16 * 16;
+  d->NP = d->N <= 64 ? 64 : 128;
+  d->scale = s->scale;
+  // a block for each (batch, head, chunk), or 64 value rows of a (batch, head)
+  const int64_t bh = (int64_t)d->B * d->H;
+  if (bh * d->nc >= 0x7fffffff || bh * 4 >= 0x7fffffff) return SSD_ERR_UNSUPPORTED;
+  const int64_t blocks = (int64_t)d->B * d->G * d->nc;
+  const int64_t nb = (kGradBlocks + blocks - 1) / blocks;
+  d->nb = (int)(nb < d->rep ? nb : d->rep);
+  d->qs = s->q_row_stride ? s->q_row_stride : gn;
+  d->ks = s->k_row_stride ? s->k_row_stride : gn;
+  d->vs = s->v_row_stride ? s->v_row_stride : hp;
+  d->qb = s->q_row_stride ? s->q_batch_stride : d->qs * d->T;
+  d->kb = s->k_row_stride ? s->k_batch_stride : d->ks * d->T;
+  d->vb = s->v_row_stride ? s->v_batch_stride : d->vs * d->T;
+  return SSD_OK;
+}
+
+DeltaWs delta_ws(const DeltaDims& d, void* base, bool bwd) {
+  DeltaWs w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    void* p = base ? static_cast<char*>(base) + at : nullptr;
+    at += align_up(bytes, 256);
+    return p;
+  };
+  const size_t n = (size_t)d.B * d.H * d.nc, tok = n * d.Ps * kC * 4, st = n * d.Ps * d.NP * 4;
+  w.gates = static_cast<Gates*>(take(n * sizeof(Gates)));
+  w.X = static_cast<bf16*>(take(n * 3 * kC * kC * 2));
+  w.U = static_cast<float*>(take(tok));
+  w.S0 = static_cast<float*>(take(st));
+  if (bwd) {
+    w.Zb = static_cast<float*>(take(tok));
+    w.E = static_cast<float*>(take(tok));
+    w.Zd = static_cast<float*>(take(tok));
+    w.dR = static_cast<float*>(take(tok));
+    w.dS = static_cast<float*>(take(st));
+    w.part = static_cast<float*>(take(n * 8));
+    if (d.nb > 1) {
+      const size_t whole = (size_t)d.nb * d.B * d.T * d.G * d.N * 4;
+      w.dqp = static_cast<float*>(take(whole));
+      w.dkp = static_cast<float*>(take(whole));
+    }
+  }
+  w.total = at;
+  return w;
+}
+
+struct DeltaIn {
+  const void *q, *k, *v, *dt;
+  const float *dt_bias, *A;
+  const void* beta;
+  const float* init;
+  const int32_t* lengths;
+};
+struct DeltaGrads {
+  const void* dy;
+  const float* dfinal;
+  void *dq, *dk, *dv, *ddt, *dbeta;
+  float *dA, *ddt_bias, *dinit;
+};
+
+template <typename K>
+bool allow_smem(K kern, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+             cudaSuccess;
+}
+
+// Launches kern and returns from the caller on an error.
+#define DELTA_LAUNCH(name, kern, grid, threads, smem, ...)                       \
+  do {                                                                           \
+    if (!allow_smem(kern, smem)) return SSD_ERR_CUDA;                            \
+    SSD_LAUNCH(name, s, kern<<<(unsigned)(grid), threads, smem, s>>>(__VA_ARGS__)); \
+    if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;                  \
+  } while (0)
+
+// Whether the chains can copy a raw tile asynchronously.
+template <typename T>
+bool async_ok(const DeltaDims& d, bool bwd) {
+  return sizeof(T) == 2 && d.vk && (bwd ? d.vq && d.vdy : d.vv);
+}
+
+template <typename T, int NP, bool BWD>
+int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const DeltaWs& w,
+                 float* final_states, cudaStream_t s) {
+  const T *q = static_cast<const T*>(in.q), *k = static_cast<const T*>(in.k),
+          *v = static_cast<const T*>(in.v);
+  const int64_t n = (int64_t)d.B * d.H * d.nc, chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
+  const auto prep = k_delta_prep<T, NP, BWD>;
+  DELTA_LAUNCH("k_delta_prep", prep, n, kPrepThreads, (prep_smem<T, NP, BWD>()), d, q, k,
+               static_cast<const T*>(in.dt), in.dt_bias, in.A, static_cast<const T*>(in.beta),
+               static_cast<const T*>(dy), in.lengths, w);
+  if constexpr (sizeof(T) == 2) {
+    if (async_ok<T>(d, false)) {
+      const auto chain = k_delta_chain<T, NP, true, BWD>;
+      DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP, true>()), d, k, v,
+                   in.init, in.lengths, w, final_states);
+      return SSD_OK;
+    }
+  }
+  const auto chain = k_delta_chain<T, NP, false, BWD>;
+  DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP, false>()), d, k, v,
+               in.init, in.lengths, w, final_states);
+  return SSD_OK;
+}
+
+template <typename T, typename TO, int NP>
+int delta_forward(const DeltaDims& d, const DeltaIn& in, const DeltaWs& w, void* y,
+                  float* final_states, cudaStream_t s) {
+  const int st = delta_states<T, NP, false>(d, in, nullptr, w, final_states, s);
+  if (st != SSD_OK) return st;
+  const auto out = k_delta_out<T, TO, NP>;
+  DELTA_LAUNCH("k_delta_out", out, (int64_t)d.B * d.H * d.nc, kOutThreads, (out_smem<T, TO, NP>()), d,
+               static_cast<const T*>(in.q), static_cast<const T*>(in.k), in.lengths, w,
+               static_cast<TO*>(y));
+  return SSD_OK;
+}
+
+template <typename T, typename TO, int NP>
+int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, const DeltaWs& w,
+                   cudaStream_t s) {
+  const int st = delta_states<T, NP, true>(d, in, g.dy, w, nullptr, s);
+  if (st != SSD_OK) return st;
+  const T *q = static_cast<const T*>(in.q), *k = static_cast<const T*>(in.k),
+          *dy = static_cast<const T*>(g.dy);
+  const int64_t chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
+  bool done = false;
+  if constexpr (sizeof(T) == 2) {
+    if (async_ok<T>(d, true)) {
+      const auto back = k_delta_back<T, NP, true>;
+      DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP, true>()), d, q, k, dy,
+                   g.dfinal, in.lengths, w, g.dinit);
+      done = true;
+    }
+  }
+  if (!done) {
+    const auto back = k_delta_back<T, NP, false>;
+    DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP, false>()), d, q, k, dy,
+                 g.dfinal, in.lengths, w, g.dinit);
+  }
+  const auto grad = k_delta_grad<T, TO, NP>;
+  TO *dq = static_cast<TO*>(g.dq), *dk = static_cast<TO*>(g.dk);
+  DELTA_LAUNCH("k_delta_grad", grad, (int64_t)d.B * d.G * d.nb * d.nc, kGradThreads,
+               (grad_smem<T, TO, NP>()), d, q, k, static_cast<const T*>(in.dt), in.dt_bias, in.A, dy,
+               in.lengths, w, dq, dk, static_cast<TO*>(g.dv), static_cast<TO*>(g.ddt),
+               static_cast<TO*>(g.dbeta));
+  if (d.nb > 1) {
+    const int64_t m = (int64_t)d.B * d.T * d.G * d.N, blocks = (m + 255) / 256;
+    DELTA_LAUNCH("k_delta_sum", k_delta_sum<TO>, blocks < 152 * 8 ? blocks : 152 * 8, 256, 0, w.dqp,
+                 w.dkp, d.nb, m, dq, dk);
+  }
+  DELTA_LAUNCH("k_delta_params", k_delta_params, d.H, 256, 0, w.part, d.B, d.H, d.nc, g.dA,
+               g.ddt_bias);
+  return SSD_OK;
+}
+
+bool off(const void* p, int esize) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(esize - 1)) != 0;
+}
+
+// Whether rows of `cols` elements that start `step` elements apart at p, tokens row and
+// batch rows batch elements apart, can be read 16 bytes at a time.
+bool rows16(const void* p, int e, int64_t step, int64_t row, int64_t batch) {
+  return !off(p, 16) && step * e % 16 == 0 && row * e % 16 == 0 && batch * e % 16 == 0;
+}
+
+int check_in(const ssd_delta_shape* shape, DeltaDims* d, const DeltaIn& in) {
+  const int st = delta_dims(shape, d);
+  if (st != SSD_OK) return st;
+  const int e = shape->in_dtype == SSD_BF16 ? 2 : 4;
+  if (!in.q || !in.k || !in.v || !in.dt || !in.A || !in.beta) return SSD_ERR_INVALID_ARG;
+  if (off(in.q, e) || off(in.k, e) || off(in.v, e) || off(in.dt, e) || off(in.beta, e) ||
+      off(in.dt_bias, 4) || off(in.A, 4) || off(in.init, 4) || off(in.lengths, 4))
+    return SSD_ERR_INVALID_ARG;
+  d->vq = rows16(in.q, e, d->N, d->qs, d->qb);
+  d->vk = rows16(in.k, e, d->N, d->ks, d->kb);
+  d->vv = rows16(in.v, e, d->P, d->vs, d->vb);
+  return SSD_OK;
+}
+
+int check_ws(const DeltaWs& w, const void* workspace, size_t bytes) {
+  return !workspace || off(workspace, 16) || bytes < w.total ? SSD_ERR_WORKSPACE : SSD_OK;
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+// The instance for the types and the key columns.
+#define DELTA_PICK(call, ...)                                                             \
+  (shape->in_dtype == SSD_F32                                                             \
+       ? (d.NP == 64 ? call<float, float, 64>(__VA_ARGS__) : call<float, float, 128>(__VA_ARGS__)) \
+   : shape->out_dtype == SSD_F32                                                          \
+       ? (d.NP == 64 ? call<bf16, float, 64>(__VA_ARGS__) : call<bf16, float, 128>(__VA_ARGS__))   \
+       : (d.NP == 64 ? call<bf16, bf16, 64>(__VA_ARGS__) : call<bf16, bf16, 128>(__VA_ARGS__)))
+
+extern "C" {
+
+size_t ssd_gated_delta_fwd_workspace_size(const ssd_delta_shape* shape) {
+  DeltaDims d{};
+  return delta_dims(shape, &d) == SSD_OK ? delta_ws(d, nullptr, false).total : 0;
+}
+
+size_t ssd_gated_delta_bwd_workspace_size(const ssd_delta_shape* shape) {
+  DeltaDims d{};
+  return delta_dims(shape, &d) == SSD_OK ? delta_ws(d, nullptr, true).total : 0;
+}
+
+int ssd_gated_delta_fwd(const ssd_delta_shape* shape, const void* q, const void* k, const void* v,
+                        const void* dt, const float* dt_bias, const float* A, const void* beta,
+                        const float* init_states, const int32_t* lengths, void* y,
+                        float* final_states, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  DeltaDims d{};
+  const DeltaIn in{q, k, v, dt, dt_bias, A, beta, init_states, lengths};
+  int st = check_in(shape, &d, in);
+  if (st != SSD_OK) return st;
+  if (!y || off(y, shape->out_dtype == SSD_BF16 ? 2 : 4) || off(final_states, 4))
+    return SSD_ERR_INVALID_ARG;
+  const DeltaWs w = delta_ws(d, workspace, false);
+  if ((st = check_ws(w, workspace, workspace_bytes)) != SSD_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return DELTA_PICK(delta_forward, d, in, w, y, final_states, s);
+}
+
+int ssd_gated_delta_bwd(const ssd_delta_shape* shape, const void* q, const void* k, const void* v,
+                        const void* dt, const float* dt_bias, const float* A, const void* beta,
+                        const float* init_states, const int32_t* lengths, const void* dy,
+                        const float* dfinal_states, void* dq, void* dk, void* dv, void* ddt,
+                        void* dbeta, float* dA, float* ddt_bias, float* dinit_states,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  DeltaDims d{};
+  const DeltaIn in{q, k, v, dt, dt_bias, A, beta, init_states, lengths};
+  int st = check_in(shape, &d, in);
+  if (st != SSD_OK) return st;
+  const int e = shape->in_dtype == SSD_BF16 ? 2 : 4, o = shape->out_dtype == SSD_BF16 ? 2 : 4;
+  if (!dy || !dq || !dk || !dv || !ddt || !dbeta || off(dy, e) || off(dq, o) || off(dk, o) ||
+      off(dv, o) || off(ddt, o) || off(dbeta, o) || off(dA, 4) || off(ddt_bias, 4) ||
+      off(dfinal_states, 4) || off(dinit_states, 4))
+    return SSD_ERR_INVALID_ARG;
+  d.vdy = rows16(dy, e, d.P, (int64_t)d.H * d.P, (int64_t)d.T * d.H * d.P);
+  const DeltaWs w = delta_ws(d, workspace, true);
+  if ((st = check_ws(w, workspace, workspace_bytes)) != SSD_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const DeltaGrads g{dy, dfinal_states, dq, dk, dv, ddt, dbeta, dA, ddt_bias, dinit_states};
+  return DELTA_PICK(delta_backward, d, in, g, w, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,118 @@
+// Warp-level matrix pieces of the gated delta rule's chunk kernels: bf16 products
+// with fp32 accumulators (m16n8k16) whose operands are sums of bf16 planes.
+//
+// An fp32 value v is the sum of the planes rn(v), rn(v - p0), rn(v - p0 - p1): 8
+// significant bits each, so three planes hold v exactly up to 2^-25 of it.  A
+// product of values with NA and NB planes takes the plane products i + j < max(NA,
+// NB): a bf16 input (one plane, exact) times an fp32 value is three instructions and
+// as good as an fp32 product, two fp32 values take six.  Chains of products stay in
+// registers: an accumulator tile of 16 rows is, column block by column block, the
+// left operand of the next product.
+//
+// Operand tiles in shared memory are rows of bf16 with a pitch of an odd number of 16
+// bytes, which ldmatrix reads without bank conflicts.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace ssd {
+namespace wm {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ uint32_t saddr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const bf16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const bf16* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr(p))
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Lane addresses.  A (16 x 16) and B (16 x 16: two tiles of 8 columns) of a tile
+// stored either way round; `ld` is the pitch in elements.
+//   a_rows: stored [row][k]      a_cols: stored [k][row]
+//   b_rows: stored [n][k]        b_cols: stored [k][n]
+template <int LD>
+__device__ __forceinline__ void a_rows(uint32_t (&r)[4], const bf16* t, int row, int k, int lane) {
+  ldsm4(r, t + (row + (lane & 15)) * LD + k + (lane >> 4) * 8);
+}
+template <int LD>
+__device__ __forceinline__ void a_cols(uint32_t (&r)[4], const bf16* t, int row, int k, int lane) {
+  ldsm4t(r, t + (k + (lane & 7) + (lane >> 4) * 8) * LD + row + ((lane >> 3) & 1) * 8);
+}
+template <int LD>
+__device__ __forceinline__ void b_rows(uint32_t (&r)[4], const bf16* t, int n, int k, int lane) {
+  ldsm4(r, t + (n + (lane & 7) + (lane >> 4) * 8) * LD + k + ((lane >> 3) & 1) * 8);
+}
+template <int LD>
+__device__ __forceinline__ void b_cols(uint32_t (&r)[4], const bf16* t, int n, int k, int lane) {
+  ldsm4t(r, t + (k + (lane & 7) + ((lane >> 3) & 1) * 8) * LD + n + (lane >> 4) * 8);
+}
+
+// The planes of a pair of values, packed (first value in the low half).
+template <int NPL>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[NPL]) {
+  float2 v = make_float2(a, b);
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    if (i + 1 < NPL) {  // what the plane leaves, exact in fp32
+      const float2 f =
+          make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u));
+      v = __ffma2_rn(f, make_float2(-1.f, -1.f), v);
+    }
+  }
+}
+// Left operand of column block kb of an accumulator strip c[tile][4], as planes.
+template <int NPL, int NT>
+__device__ __forceinline__ void a_from_acc(uint32_t (&a)[NPL][4], const float (&c)[NT][4], int kb) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t p[NPL];
+    const float(&t)[4] = c[2 * kb + (q >> 1)];
+    split2<NPL>(t[(q & 1) * 2], t[(q & 1) * 2 + 1], p);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) a[i][q] = p[i];
+  }
+}
+
+// c0, c1 (two tiles of 8 columns) += A B over plane products i + j < M; B of plane j
+// comes from load(j, regs).
+template <int NA, int NB, int M, typename Load>
+__device__ __forceinline__ void mma_planes(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
+                                           Load&& load) {
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    uint32_t b[4];
+    load(j, b);
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (i + j < M) {
+        mma16816(c0, a[i], b[0], b[1]);
+        mma16816(c1, a[i], b[2], b[3]);
+      }
+  }
+}
+
+constexpr int max2(int a, int b) { return a > b ? a : b; }
+
+}  // namespace wm
+}  // namespace ssd
