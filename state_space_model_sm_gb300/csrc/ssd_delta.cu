@@ -49,6 +49,7 @@ struct DeltaDims {
   float scale;
   int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
   int vq, vk, vv, vdy;             // whether rows can be read 16 bytes at a time
+  int wide;                        // whether pairs of output columns can be written at once
 };
 
 // Gates of a chunk: the log2 decays' running sum in two floats, and b.
@@ -130,21 +131,40 @@ __device__ __forceinline__ void load_tile(bf16* dst, const T* src, int64_t ld, i
   }
 }
 
-// 64 rows of W fp32 values of the workspace (rows from rv on: zeros) as NPL planes.
-template <int NPL, int W, int LD, int THREADS>
-__device__ __forceinline__ void load_split(bf16* dst, const float* src, int rv) {
-  for (int i = threadIdx.x; i < kC * (W / 4); i += THREADS) {
-    const int r = i / (W / 4), c = i % (W / 4) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rv) v = *reinterpret_cast<const float4*>(src + (size_t)r * W + c);
-    uint32_t a[NPL], b[NPL];
-    split2<NPL>(v.x, v.y, a);
-    split2<NPL>(v.z, v.w, b);
-#pragma unroll
-    for (int k = 0; k < NPL; ++k)
-      *reinterpret_cast<uint2*>(dst + k * kC * LD + r * LD + c) = make_uint2(a[k], b[k]);
+// 64 rows of W fp32 values of the workspace (rows from rv on: zeros), first into
+// registers, all loads in flight, then as NPL planes into a tile.
+template <int W, int LD, int THREADS>
+struct WsTile {
+  static constexpr int kN = kC * (W / 4) / THREADS;
+  float4 v[kN];
+  __device__ __forceinline__ static void at(int n, int* r, int* c) {
+    const int i = threadIdx.x + n * THREADS;
+    *r = i / (W / 4), *c = i % (W / 4) * 4;
   }
-}
+  __device__ __forceinline__ void load(const float* src, int rv) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      int r, c;
+      at(n, &r, &c);
+      v[n] = r < rv ? *reinterpret_cast<const float4*>(src + r * W + c)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  template <int NPL>
+  __device__ __forceinline__ void store(bf16* dst) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      int r, c;
+      at(n, &r, &c);
+      uint32_t a[NPL], b[NPL];
+      split2<NPL>(v[n].x, v[n].y, a);
+      split2<NPL>(v[n].z, v[n].w, b);
+#pragma unroll
+      for (int k = 0; k < NPL; ++k)
+        *reinterpret_cast<uint2*>(dst + k * kC * LD + r * LD + c) = make_uint2(a[k], b[k]);
+    }
+  }
+};
 
 // As load_tile, started asynchronously: bf16 rows with vec.
 template <int W, int LD, int THREADS>
@@ -157,6 +177,18 @@ __device__ __forceinline__ void copy_tile(bf16* dst, const bf16* src, int64_t ld
     else
       *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
   }
+}
+// A raw tile, asynchronously where it can be (cp_wait and a barrier complete it).
+template <typename T, int W, int LD, int THREADS>
+__device__ __forceinline__ void fetch_tile(bf16* dst, const T* src, int64_t ld, int rv, int cv,
+                                           bool vec) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec) {
+      copy_tile<W, LD, THREADS>(dst, src, ld, rv, cv);
+      return;
+    }
+  }
+  load_tile<T, W, LD, THREADS>(dst, src, ld, rv, cv, vec);
 }
 // The planes of X, started asynchronously.
 template <int THREADS>
@@ -227,11 +259,16 @@ __device__ __forceinline__ void lower_product(float (&acc)[8][4], const bf16* A,
 
 constexpr int kPrepThreads = 128;
 
+// Shared memory: the keys' tile, whose place M takes; the queries' (backward), whose
+// place X takes; the planes of the scaled Q K^T over both; and dY's tile.
 template <typename T, int NP, bool BWD>
-constexpr size_t prep_smem() {
-  constexpr size_t tile = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
-  return sizeof(Gates) + 2 * kC * kF * 4 + tile * (BWD ? 2 : 1);
-}
+struct PrepSmem {
+  static constexpr size_t tile = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+  static constexpr size_t f32 = (size_t)kC * kF * 4;
+  static constexpr size_t one = tile > f32 ? tile : f32;
+  static constexpr size_t dy = BWD ? (size_t)planes_of<T>() * kC * kTP * 2 : 0;
+  static constexpr size_t total = sizeof(Gates) + one + (BWD ? one : f32) + dy;
+};
 
 // Gates and X of one chunk of one head; in the backward also E^T = dY^T (Q K^T e^(..)).
 //
@@ -239,29 +276,38 @@ constexpr size_t prep_smem() {
 // thread; then twice  [A 0; C B]^-1 = [A' 0; -B' C A', B'].  Substitution is stable
 // whatever the keys (a run of equal keys makes I + M ill suited to a power series).
 template <typename T, int NP, bool BWD>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 5 : 1)
     k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
                  const T* __restrict__ dt, const float* __restrict__ dt_bias,
                  const float* __restrict__ A, const T* __restrict__ beta,
                  const T* __restrict__ dy, const int* __restrict__ lengths, DeltaWs w) {
   constexpr int NI = planes_of<T>(), LD = NP + 8;
+  using SM = PrepSmem<T, NP, BWD>;
   extern __shared__ __align__(16) unsigned char smem[];
   Gates& g = *reinterpret_cast<Gates*>(smem);
-  float* const M = reinterpret_cast<float*>(smem + sizeof(Gates));
-  float* const X = M + kC * kF;
-  bf16* const Kt = reinterpret_cast<bf16*>(X + kC * kF);
+  bf16* const Kt = reinterpret_cast<bf16*>(smem + sizeof(Gates));
+  bf16* const Qt = reinterpret_cast<bf16*>(smem + sizeof(Gates) + SM::one);
+  bf16* const yt = Qt + SM::one / 2;
+  float* const M = reinterpret_cast<float*>(Kt);
+  float* const X = reinterpret_cast<float*>(Qt);
   const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
   const Place pl = place(d, blockIdx.x);
   const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
   if (t0 >= n) return;
   const int rv = min(kC, n - t0), grp = pl.h / d.rep;
+  const int64_t ys = (int64_t)d.H * d.P;
+  const T* const yg = BWD ? dy + ((int64_t)pl.b * d.T + t0) * ys + (int64_t)pl.h * d.P : nullptr;
 
-  load_tile<T, NP, LD, kPrepThreads>(Kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
-                                     d.N, d.vk);
-  if (BWD)
-    load_tile<T, NP, LD, kPrepThreads>(Kt + NI * kC * LD,
-                                       q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
-                                       d.N, d.vq);
+  fetch_tile<T, NP, LD, kPrepThreads>(Kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
+                                      d.N, d.vk);
+  if constexpr (BWD)
+    fetch_tile<T, NP, LD, kPrepThreads>(Qt, q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
+                                        d.N, d.vq);
+  cp_commit();
+  if constexpr (BWD) {
+    fetch_tile<T, kC, kTP, kPrepThreads>(yt, yg, ys, rv, d.P, d.vdy);
+    cp_commit();
+  }
   if (strip == 0) {  // two tokens a lane
     double s[2];
     float bb[2];
@@ -296,13 +342,16 @@ __global__ void __launch_bounds__(kPrepThreads)
       g.b[2 * lane + j] = bb[j];
     }
   }
+  cp_wait<BWD ? 1 : 0>();
   __syncthreads();
   if (tid < sizeof(Gates) / 16)
     reinterpret_cast<uint4*>(w.gates + pl.i)[tid] = reinterpret_cast<const uint4*>(&g)[tid];
 
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
-  float acc[8][4];
+  float acc[8][4], qk[BWD ? 8 : 1][4];
   lower_product<NI, NP>(acc, Kt, Kt, strip, lane);
+  if constexpr (BWD) lower_product<NI, NP>(qk, Qt, Kt, strip, lane);
+  __syncthreads();  // the tiles are read
 #pragma unroll
   for (int t = 0; t < 8; ++t)
     if (t < 2 * strip + 2)
@@ -392,10 +441,9 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
   if constexpr (BWD) {
     // E^T[p][j] = sum_{i >= j} dy[i][p] scale e^(G_i - G_j) q_i . k_j
-    lower_product<NI, NP>(acc, Kt + NI * kC * LD, Kt, strip, lane);
-    __syncthreads();  // X and M are read: their place takes the planes; K's takes dy
+    __syncthreads();  // X is written out: its and M's place takes the planes
     bf16* const at = reinterpret_cast<bf16*>(M);
-    static_assert(3 * kC * kTP * 2 <= 2 * kC * kF * 4, "the planes fit");
+    static_assert(3 * kC * kTP * 2 <= 2 * SM::one, "the planes fit");
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -405,18 +453,19 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
         for (int f = 0; f < 2; ++f)
           if (t < 2 * strip + 2 && j + f <= i)
-            v[f] = d.scale * decay_between(g, i, j + f) * acc[t][2 * e + f];
+            v[f] = d.scale * decay_between(g, i, j + f) * qk[t][2 * e + f];
         uint32_t p[3];
         split2<3>(v[0], v[1], p);
 #pragma unroll
         for (int l = 0; l < 3; ++l)
           *reinterpret_cast<uint32_t*>(at + l * kC * kTP + i * kTP + j) = p[l];
       }
-    bf16* const yt = Kt;
     for (int p0 = 0; p0 < d.Ps; p0 += kC) {
-      load_tile<T, kC, kTP, kPrepThreads>(
-          yt, dy + (((int64_t)pl.b * d.T + t0) * d.H + pl.h) * d.P + p0, (int64_t)d.H * d.P, rv,
-          d.P - p0, d.vdy);
+      if (p0 > 0) {
+        load_tile<T, kC, kTP, kPrepThreads>(yt, yg + p0, ys, rv, d.P - p0, d.vdy);
+      } else {
+        cp_wait<0>();
+      }
       __syncthreads();
       if (p0 + strip * 16 < d.Ps) {
         float e[8][4];
@@ -640,32 +689,37 @@ __global__ void __launch_bounds__(kChainThreads)
 
 // ----------------------------------------------------------------------- out
 
-constexpr int kOutThreads = 128;
+constexpr int kOutThreads = 256;
 
 // Planes of values that only reach an output of type TO.
 template <typename TO>
 constexpr int out_planes() { return sizeof(TO) == 2 ? 2 : 3; }
 
+// Shared memory: queries; keys, whose place the state's planes take; U; the pairs.
 template <typename T, typename TO, int NP>
-constexpr size_t out_smem() {
-  constexpr size_t raw = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
-  constexpr size_t st = (size_t)out_planes<TO>() * kC * (NP + 8) * 2;
-  return sizeof(Gates) + raw + (raw > st ? raw : st) + (size_t)out_planes<TO>() * kC * kTP * 2;
-}
+struct OutSmem {
+  static constexpr size_t raw = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+  static constexpr size_t st = (size_t)out_planes<TO>() * kC * (NP + 8) * 2;
+  static constexpr size_t one = raw > st ? raw : st;
+  static constexpr size_t tok = (size_t)out_planes<TO>() * kC * kTP * 2;
+  static constexpr size_t total = sizeof(Gates) + raw + one + 2 * tok;
+};
 
-// Y of one chunk of one head, 16 tokens a warp.
+// Y of one chunk of one head: 16 tokens by half of 64 value columns a warp, in passes of
+// 64 value columns; the pairs Q K^T e^(..) are formed once, by halves of the tokens.
 template <typename T, typename TO, int NP>
-__global__ void __launch_bounds__(kOutThreads)
+__global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2 ? 2 : 1)
     k_delta_out(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
                 const int* __restrict__ lengths, DeltaWs w, TO* __restrict__ y) {
   constexpr int NI = planes_of<T>(), NL = out_planes<TO>(), LD = NP + 8;
-  constexpr size_t raw = (size_t)NI * kC * LD, st = (size_t)NL * kC * LD;
+  using SM = OutSmem<T, TO, NP>;
   extern __shared__ __align__(16) unsigned char smem[];
   Gates& g = *reinterpret_cast<Gates*>(smem);
   bf16* const qt = reinterpret_cast<bf16*>(smem + sizeof(Gates));
-  bf16* const kt = qt + raw;  // and the state's planes after the keys'
-  bf16* const ut = kt + (raw > st ? raw : st);
-  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  bf16* const kt = qt + SM::raw / 2;  // and the state's planes after the keys'
+  bf16* const ut = kt + SM::one / 2;
+  bf16* const pt = ut + SM::tok / 2;
+  const int tid = threadIdx.x, lane = tid & 31, strip = (tid >> 5) & 3, half = tid >> 7;
   const Place pl = place(d, blockIdx.x);
   const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
   const int rows = min(kC, d.T - t0);  // of the output; tokens from n on are padding
@@ -676,33 +730,69 @@ __global__ void __launch_bounds__(kOutThreads)
     return;
   }
   const int rv = min(kC, n - t0), grp = pl.h / d.rep;
-  load_tile<T, NP, LD, kOutThreads>(qt, q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
-                                    d.N, d.vq);
-  load_tile<T, NP, LD, kOutThreads>(kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
-                                    d.N, d.vk);
+  fetch_tile<T, NP, LD, kOutThreads>(qt, q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
+                                     d.N, d.vq);
+  fetch_tile<T, NP, LD, kOutThreads>(kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
+                                     d.N, d.vk);
+  cp_commit();
   if (tid < sizeof(Gates) / 16)
     reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + pl.i)[tid];
+  WsTile<NP, LD, kOutThreads> ws;
+  WsTile<kC, kTP, kOutThreads> wu;
+  ws.load(w.S0 + pl.i * d.Ps * NP, min(kC, d.Ps));
+  wu.load(w.U + pl.i * d.Ps * kC, min(kC, d.Ps));
+  cp_wait<0>();
   __syncthreads();
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
-  float s[8][4];
-  lower_product<NI, NP>(s, qt, kt, strip, lane);
+  {
+    float s[4][4];
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = r0 + (e >> 1) * 8, j = 8 * t + c0 + (e & 1);
-      s[t][e] = j <= i ? d.scale * decay_between(g, i, j) * s[t][e] : 0.f;
-    }
+      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+    if (2 * half <= strip)
+#pragma unroll
+      for (int kk = 0; kk < NP / 16; ++kk) {
+        uint32_t a[NI][4];
+#pragma unroll
+        for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+          mma_planes<NI, NI, NI>(s[2 * np], s[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<LD>(x, kt + j * kC * LD, half * 32 + np * 16, kk * 16, lane);
+          });
+      }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = r0 + e * 8, j = half * 32 + 8 * t + c0;
+        float v[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          v[f] = j + f <= i ? d.scale * decay_between(g, i, j + f) * s[t][2 * e + f] : 0.f;
+        uint32_t x[NL];
+        split2<NL>(v[0], v[1], x);
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+          *reinterpret_cast<uint32_t*>(pt + l * kC * kTP + i * kTP + j) = x[l];
+      }
+  }
   const float f0 = d.scale * ex2(g.gh[r0]), f1 = d.scale * ex2(g.gh[r0 + 8]);
   for (int p0 = 0; p0 < d.Ps; p0 += kC) {
     __syncthreads();
-    const int pr = min(kC, d.Ps - p0);
-    load_split<NL, NP, LD, kOutThreads>(kt, w.S0 + (pl.i * d.Ps + p0) * NP, pr);
-    load_split<NL, kC, kTP, kOutThreads>(ut, w.U + (pl.i * d.Ps + p0) * kC, pr);
+    ws.template store<NL>(kt);
+    wu.template store<NL>(ut);
     __syncthreads();
-    float o[8][4];
+    if (p0 + kC < d.Ps) {  // the next value rows, on their way under this tile's products
+      const int pr = min(kC, d.Ps - p0 - kC);
+      ws.load(w.S0 + (pl.i * d.Ps + p0 + kC) * NP, pr);
+      wu.load(w.U + (pl.i * d.Ps + p0 + kC) * kC, pr);
+    }
+    if (p0 + half * 32 >= d.Ps) continue;
+    float o[4][4];
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
 #pragma unroll
@@ -711,30 +801,35 @@ __global__ void __launch_bounds__(kOutThreads)
 #pragma unroll
       for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
 #pragma unroll
-      for (int np = 0; np < 4; ++np)
+      for (int np = 0; np < 2; ++np)
         mma_planes<NI, NL, max2(NI, NL)>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-          b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
+          b_rows<LD>(x, kt + j * kC * LD, half * 32 + np * 16, kk * 16, lane);
         });
     }
 #pragma unroll
-    for (int t = 0; t < 8; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
+    for (int t = 0; t < 4; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
       if (kb <= strip) {
         uint32_t a[NL][4];
-        a_from_acc<NL>(a, s, kb);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
+        for (int l = 0; l < NL; ++l) a_rows<kTP>(a[l], pt + l * kC * kTP, strip * 16, kb * 16, lane);
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
           mma_planes<NL, NL, NL>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<kTP>(x, ut + j * kC * kTP, np * 16, kb * 16, lane);
+            b_rows<kTP>(x, ut + j * kC * kTP, half * 32 + np * 16, kb * 16, lane);
           });
       }
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = r0 + (e >> 1) * 8, p = p0 + 8 * t + c0 + (e & 1);
-        if (i < rows && p < d.P) yo[i * ys + p] = from_f<TO>(i < rv ? o[t][e] : 0.f);
+      for (int e = 0; e < 2; ++e) {
+        const int i = r0 + e * 8, p = p0 + half * 32 + 8 * t + c0;
+        if (i < rows && p < d.P) {
+          const bool in = i < rv;
+          lm::st_two(yo + i * ys + p, make_float2(in ? o[t][2 * e] : 0.f, in ? o[t][2 * e + 1] : 0.f),
+                     p + 1 < d.P, d.wide);
+        }
       }
   }
 }
@@ -909,27 +1004,32 @@ __global__ void __launch_bounds__(kChainThreads)
 
 // ---------------------------------------------------------------------- grad
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 
-// Sums of the tokens of a chunk that the gate's gradient is made of.
+// Sums over the tokens of a chunk that the gates' gradients are made of.
 struct GradSums {
-  float row[2][kC];   // rows of dAqk Aqk - W M, a column half each
-  float col[4][kC];   // columns of the same, a row strip each
-  float qd[2][kC];    // scale e^G q . (dY S0), a half of the key columns each
-  float part[4][3][kC];  // U . Zd, dR . Zb, dR . U, of a quarter of the value rows each
-  float dot[8];       // <dS, S0>, a warp each
+  float row[4][kC];       // rows of dAqk Aqk - W M, a column block each
+  float col[4][kC];       // columns of the same, a row strip each
+  float qd[4][kC];        // scale e^G q . (dY S0), a quarter of the key columns each
+  float part[16][3][kC];  // U . Zd, dR . Zb, dR . U, a warp's value rows each
+  float dot[16];          // <dS, S0>, a warp each
 };
 
+// Shared memory: dY, dR, U and S0 (then dS) of a tile of value rows; P1 and P2 over
+// dR and U; Q and K beside them, or over dY, where they are three planes wide.
 template <typename T, typename TO, int NP>
-constexpr size_t grad_smem() {
-  constexpr size_t row = kC * (NP + 8) * 2, tok = kC * kTP * 2, ni = planes_of<T>();
-  constexpr size_t a = ni * tok + 6 * tok + 3 * row;                     // while value tiles pass
-  constexpr size_t b = 2 * ni * row + 2 * out_planes<TO>() * tok;        // at the head's end
-  return sizeof(Gates) + sizeof(GradSums) + (a > b ? a : b);
-}
+struct GradSmem {
+  static constexpr size_t row = kC * (NP + 8) * 2, tok = kC * kTP * 2, ni = planes_of<T>();
+  static constexpr bool beside = ni == 1;
+  static constexpr size_t values = ni * tok + 6 * tok + 3 * row, qk = 2 * ni * row;
+  static constexpr size_t pairs = 2 * out_planes<TO>() * tok;
+  static constexpr size_t over = qk + pairs > values ? qk + pairs : values;
+  static constexpr size_t head = sizeof(Gates) + sizeof(GradSums);
+  static constexpr size_t total = head + (beside ? values + qk : over);
+};
 
-// dq, dk, dv, ddt and dbeta of one chunk of the heads of one head block.  Eight warps:
-// 16 tokens by half the key columns (or half the chunk's tokens) each.  With
+// dq, dk, dv, ddt and dbeta of one chunk of the heads of one head block.  Sixteen warps:
+// 16 tokens by a quarter of the key columns (or 16 of the chunk's tokens) each.  With
 // dAqk = dY U^T (j <= i) and W = dR U^T (j < i),
 //     dq = scale e^G dY S0 + P1 K,                       P1 = scale e^(G_i - G_j) dAqk
 //     dk = e^(G63 - G) U dS - b e^G dR S0 + P1^T Q + (P2 + P2^T) K,
@@ -947,20 +1047,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                  const int* __restrict__ lengths, DeltaWs w, TO* __restrict__ dq,
                  TO* __restrict__ dk, TO* __restrict__ dv, TO* __restrict__ ddt,
                  TO* __restrict__ dbeta) {
-  constexpr int NI = planes_of<T>(), NL = out_planes<TO>(), LD = NP + 8, HT = NP / 16;
+  constexpr int NI = planes_of<T>(), NL = out_planes<TO>(), LD = NP + 8;
+  constexpr int WC = NP / 4, HT = WC / 8;  // key columns and tiles of a warp
+  using SM = GradSmem<T, TO, NP>;
   extern __shared__ __align__(16) unsigned char smem[];
   Gates& g = *reinterpret_cast<Gates*>(smem);
   GradSums& sm = *reinterpret_cast<GradSums*>(smem + sizeof(Gates));
-  bf16* const base = reinterpret_cast<bf16*>(smem + sizeof(Gates) + sizeof(GradSums));
-  bf16* const yt = base;                 // dY [token][p]
-  bf16* const rt = yt + NI * kC * kTP;   // dR [p][token]
-  bf16* const ut = rt + 3 * kC * kTP;    // U [p][token]
-  bf16* const st = ut + 3 * kC * kTP;    // S0, then dS [p][n]
-  bf16* const qt = base;                 // at the head's end
+  bf16* const base = reinterpret_cast<bf16*>(smem + SM::head);
+  bf16* const yt = base;                // dY [token][p]
+  bf16* const rt = yt + NI * kC * kTP;  // dR [p][token]
+  bf16* const ut = rt + 3 * kC * kTP;   // U [p][token]
+  bf16* const st = ut + 3 * kC * kTP;   // S0, then dS [p][n]
+  bf16* const qt = SM::beside ? st + 3 * kC * LD : base;
   bf16* const kt = qt + NI * kC * LD;
-  bf16* const p1 = kt + NI * kC * LD;
+  bf16* const p1 = SM::beside ? rt : kt + NI * kC * LD;
   bf16* const p2 = p1 + NL * kC * kTP;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, strip = warp & 3, half = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, strip = warp & 3, part = warp >> 2;
   int64_t blk = blockIdx.x;
   const int c = (int)(blk % d.nc);
   blk /= d.nc;
@@ -972,17 +1074,23 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const int h0 = grp * d.rep + (int)((int64_t)d.rep * hb / d.nb);
   const int h1 = grp * d.rep + (int)((int64_t)d.rep * (hb + 1) / d.nb);
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
-  const int64_t ys = (int64_t)d.H * d.P;
+  const int64_t ys = (int64_t)d.H * d.P, tok = (int64_t)b * d.T + t0;
+  const T* const qg = q + b * d.qb + t0 * d.qs + (int64_t)grp * d.N;
+  const T* const kg = k + b * d.kb + t0 * d.ks + (int64_t)grp * d.N;
 
-  float tq[HT][4], tk[HT][4];  // dq, dk over the heads: columns half * NP / 2 + 8 t + c0
+  float tq[HT][4], tk[HT][4];  // dq, dk over the heads: columns part * WC + 8 t + c0
 #pragma unroll
   for (int t = 0; t < HT; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) tq[t][e] = tk[t][e] = 0.f;
+  if (SM::beside && rv > 0) {
+    fetch_tile<T, NP, LD, kGradThreads>(qt, qg, d.qs, rv, d.N, d.vq);
+    fetch_tile<T, NP, LD, kGradThreads>(kt, kg, d.ks, rv, d.N, d.vk);
+    cp_commit();
+  }
 
   for (int h = h0; h < h1; ++h) {
     const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
-    const int64_t tok = (int64_t)b * d.T + t0;
     if (rv == 0) {  // padding only
       for (int i = tid; i < rows * d.P; i += kGradThreads)
         dv[(tok + i / d.P) * ys + (int64_t)h * d.P + i % d.P] = from_f<TO>(0.f);
@@ -993,47 +1101,49 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (tid < 2) w.part[at * 2 + tid] = 0.f;
       continue;
     }
-    __syncthreads();
-    if (tid < sizeof(Gates) / 16)
-      reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + at)[tid];
-    float da[4][4], wm[4][4], dqh[HT][4];
+    float da[2][4], wm[2][4], dqh[HT][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) da[t][e] = wm[t][e] = 0.f;
 #pragma unroll
     for (int t = 0; t < HT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dqh[t][e] = 0.f;
-    float su = 0.f, sr = 0.f, sw = 0.f, dot = 0.f;
+    float4 su = make_float4(0.f, 0.f, 0.f, 0.f), sr = su, sw = su;  // of tokens 4 (tid & 15) ..
+    float dot = 0.f;
     for (int p0 = 0; p0 < d.Ps; p0 += kC) {
       const int pr = min(kC, d.Ps - p0);
-      __syncthreads();
-      load_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
-                                          d.vdy);
-      load_split<3, NP, LD, kGradThreads>(st, w.S0 + (at * d.Ps + p0) * NP, pr);
-      {  // token tid & 63, every fourth value row
-        const int i = tid & 63;
-#pragma unroll 4
-        for (int p = tid >> 6; p < kC; p += 4) {
-          float r = 0.f, u = 0.f;
-          if (p < pr) {
-            const size_t o = (size_t)(at * d.Ps + p0 + p) * kC + i;
-            r = w.dR[o], u = w.U[o];
-            su = fmaf(u, w.Zd[o], su);
-            sr = fmaf(r, w.Zb[o], sr);
-            sw = fmaf(r, u, sw);
-          }
-          uint32_t x[3];
-          split2<3>(r, u, x);
+      WsTile<NP, LD, kGradThreads> ws;
+      WsTile<kC, kTP, kGradThreads> wr, wu, wz, wb;
+      const size_t pt = (size_t)(at * d.Ps + p0);
+      ws.load(w.S0 + pt * NP, pr);
+      wr.load(w.dR + pt * kC, pr);
+      wu.load(w.U + pt * kC, pr);
+      wz.load(w.Zd + pt * kC, pr);
+      wb.load(w.Zb + pt * kC, pr);
+      __syncthreads();  // the tiles (and, at a head's start, the gates and sums) are read
+      fetch_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
+                                           d.vdy);
+      cp_commit();
+      if (p0 == 0 && tid < sizeof(Gates) / 16)
+        reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + at)[tid];
+      ws.template store<3>(st);
+      wr.template store<3>(rt);
+      wu.template store<3>(ut);
 #pragma unroll
-          for (int l = 0; l < 3; ++l) {
-            reinterpret_cast<uint16_t*>(rt)[l * kC * kTP + p * kTP + i] = (uint16_t)(x[l] & 0xffffu);
-            reinterpret_cast<uint16_t*>(ut)[l * kC * kTP + p * kTP + i] = (uint16_t)(x[l] >> 16);
-          }
-        }
+      for (int i = 0; i < wr.kN; ++i) {
+        const float4 r = wr.v[i], u = wu.v[i], z = wz.v[i], x = wb.v[i];
+        su.x = fmaf(u.x, z.x, su.x), su.y = fmaf(u.y, z.y, su.y);
+        su.z = fmaf(u.z, z.z, su.z), su.w = fmaf(u.w, z.w, su.w);
+        sr.x = fmaf(r.x, x.x, sr.x), sr.y = fmaf(r.y, x.y, sr.y);
+        sr.z = fmaf(r.z, x.z, sr.z), sr.w = fmaf(r.w, x.w, sr.w);
+        sw.x = fmaf(r.x, u.x, sw.x), sw.y = fmaf(r.y, u.y, sw.y);
+        sw.z = fmaf(r.z, u.z, sw.z), sw.w = fmaf(r.w, u.w, sw.w);
       }
+      cp_wait<0>();
       __syncthreads();
+      ws.load(w.dS + pt * NP, pr);  // on its way under the products
       for (int i = tid; i < rows * kC; i += kGradThreads) {  // dv = b dR
         const int t = i / kC, p = i % kC;
         if (p0 + p < d.P) {
@@ -1046,11 +1156,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       const float sx0 = -g.b[r0] * ex2(g.gh[r0]), sx1 = -g.b[r0 + 8] * ex2(g.gh[r0 + 8]);
       const float sk0 = decay_between(g, kC - 1, r0), sk1 = decay_between(g, kC - 1, r0 + 8);
-      // a left operand of two or three planes with its rows scaled
-      auto scaled = [&](uint32_t(&a)[NL][4], const bf16* t, int kb, float f0, float f1) {
-        uint32_t x[3][4];
-#pragma unroll
-        for (int l = 0; l < 3; ++l) a_cols<kTP>(x[l], t + l * kC * kTP, strip * 16, kb * 16, lane);
+      // a left operand of three planes with its rows scaled, as NL planes
+      auto scaled = [&](uint32_t(&a)[NL][4], const uint32_t(&x)[3][4], float f0, float f1) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float lo = 0.f, hi = 0.f;
@@ -1073,107 +1180,106 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int l = 0; l < NI; ++l) a_rows<kTP>(ya[l], yt + l * kC * kTP, strip * 16, kb * 16, lane);
 #pragma unroll
         for (int l = 0; l < 3; ++l) a_cols<kTP>(ra[l], rt + l * kC * kTP, strip * 16, kb * 16, lane);
-        scaled(xa, rt, kb, sx0, sx1);
-#pragma unroll
-        for (int np = 0; np < 2; ++np)
-          if (half * 2 + np <= strip) {
-            auto ub = [&](int j, uint32_t(&x)[4]) {
-              b_cols<kTP>(x, ut + j * kC * kTP, half * 32 + np * 16, kb * 16, lane);
-            };
-            mma_planes<NI, 3, 3>(da[2 * np], da[2 * np + 1], ya, ub);
-            mma_planes<3, 3, 3>(wm[2 * np], wm[2 * np + 1], ra, ub);
-          }
+        scaled(xa, ra, sx0, sx1);
+        if (part <= strip) {
+          auto ub = [&](int j, uint32_t(&x)[4]) {
+            b_cols<kTP>(x, ut + j * kC * kTP, part * 16, kb * 16, lane);
+          };
+          mma_planes<NI, 3, 3>(da[0], da[1], ya, ub);
+          mma_planes<3, 3, 3>(wm[0], wm[1], ra, ub);
+        }
 #pragma unroll
         for (int np = 0; np < HT / 2; ++np) {
           auto sb = [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, st + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+            b_cols<LD>(x, st + j * kC * LD, part * WC + np * 16, kb * 16, lane);
           };
           mma_planes<NI, 3, 3>(dqh[2 * np], dqh[2 * np + 1], ya, sb);
           mma_planes<NL, NL, NL>(tk[2 * np], tk[2 * np + 1], xa, sb);
         }
       }
       __syncthreads();
-      {  // dS over S0's place, and <dS, S0>
-        const float* s0 = w.S0 + (at * d.Ps + p0) * NP;
-        const float* ds = w.dS + (at * d.Ps + p0) * NP;
-        for (int i = tid; i < kC * (NP / 4); i += kGradThreads) {
-          const int r = i / (NP / 4), cc = i % (NP / 4) * 4;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < pr) {
-            v = *reinterpret_cast<const float4*>(ds + (size_t)r * NP + cc);
-            const float4 s = *reinterpret_cast<const float4*>(s0 + (size_t)r * NP + cc);
-            dot = fmaf(v.x, s.x, fmaf(v.y, s.y, fmaf(v.z, s.z, fmaf(v.w, s.w, dot))));
-          }
-          uint32_t x[NL], z[NL];
-          split2<NL>(v.x, v.y, x);
-          split2<NL>(v.z, v.w, z);
+      // dS over S0's place, and <dS, S0> of what is replaced
 #pragma unroll
-          for (int l = 0; l < NL; ++l)
-            *reinterpret_cast<uint2*>(st + l * kC * LD + r * LD + cc) = make_uint2(x[l], z[l]);
+      for (int i = 0; i < ws.kN; ++i) {
+        int r, cc;
+        ws.at(i, &r, &cc);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int l = 2; l >= 0; --l) {
+          const uint2 x = *reinterpret_cast<const uint2*>(st + l * kC * LD + r * LD + cc);
+          s.x += __uint_as_float(x.x << 16), s.y += __uint_as_float(x.x & 0xffff0000u);
+          s.z += __uint_as_float(x.y << 16), s.w += __uint_as_float(x.y & 0xffff0000u);
         }
+        const float4 v = ws.v[i];
+        dot = fmaf(v.x, s.x, fmaf(v.y, s.y, fmaf(v.z, s.z, fmaf(v.w, s.w, dot))));
       }
+      ws.template store<NL>(st);
       __syncthreads();
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        uint32_t xa[NL][4];
-        scaled(xa, ut, kb, sk0, sk1);
+        uint32_t ua[3][4], xa[NL][4];
+#pragma unroll
+        for (int l = 0; l < 3; ++l) a_cols<kTP>(ua[l], ut + l * kC * kTP, strip * 16, kb * 16, lane);
+        scaled(xa, ua, sk0, sk1);
 #pragma unroll
         for (int np = 0; np < HT / 2; ++np)
           mma_planes<NL, NL, NL>(tk[2 * np], tk[2 * np + 1], xa, [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, st + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+            b_cols<LD>(x, st + j * kC * LD, part * WC + np * 16, kb * 16, lane);
           });
       }
     }
-    __syncthreads();
-    load_tile<T, NP, LD, kGradThreads>(qt, q + b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
-                                       d.N, d.vq);
-    load_tile<T, NP, LD, kGradThreads>(kt, k + b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
-                                       d.N, d.vk);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) sm.dot[warp] = dot;
-    sm.part[tid >> 6][0][tid & 63] = su;
-    sm.part[tid >> 6][1][tid & 63] = sr;
-    sm.part[tid >> 6][2][tid & 63] = sw;
-    __syncthreads();
-    {  // the pairs of this warp: rows of its strip, 32 columns from half * 32 on
-      float qk[4][4], kk[4][4];
+    auto halves = [&](float4 v, int which) {  // two value rows a warp at a time
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+      v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+      if (lane < 16) *reinterpret_cast<float4*>(&sm.part[warp][which][4 * lane]) = v;
+    };
+    halves(su, 0);
+    halves(sr, 1);
+    halves(sw, 2);
+    __syncthreads();  // the value tiles are read
+    if constexpr (!SM::beside) {
+      load_tile<T, NP, LD, kGradThreads>(qt, qg, d.qs, rv, d.N, d.vq);
+      load_tile<T, NP, LD, kGradThreads>(kt, kg, d.ks, rv, d.N, d.vk);
+      __syncthreads();
+    }
+    {  // the pairs of this warp: rows of its strip, 16 columns from part * 16 on
+      float qk[2][4], kk[2][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) qk[t][e] = kk[t][e] = 0.f;
-      for (int x = 0; x < NP / 16; ++x) {
-        uint32_t qa[NI][4], ka[NI][4];
+      if (part <= strip)
 #pragma unroll
-        for (int l = 0; l < NI; ++l) {
-          a_rows<LD>(qa[l], qt + l * kC * LD, strip * 16, x * 16, lane);
-          a_rows<LD>(ka[l], kt + l * kC * LD, strip * 16, x * 16, lane);
-        }
+        for (int x = 0; x < NP / 16; ++x) {
+          uint32_t qa[NI][4], ka[NI][4];
 #pragma unroll
-        for (int np = 0; np < 2; ++np)
-          if (half * 2 + np <= strip) {
-            auto kb = [&](int j, uint32_t(&r)[4]) {
-              b_rows<LD>(r, kt + j * kC * LD, half * 32 + np * 16, x * 16, lane);
-            };
-            mma_planes<NI, NI, NI>(qk[2 * np], qk[2 * np + 1], qa, kb);
-            mma_planes<NI, NI, NI>(kk[2 * np], kk[2 * np + 1], ka, kb);
+          for (int l = 0; l < NI; ++l) {
+            a_rows<LD>(qa[l], qt + l * kC * LD, strip * 16, x * 16, lane);
+            a_rows<LD>(ka[l], kt + l * kC * LD, strip * 16, x * 16, lane);
           }
-      }
-      float rs[2] = {0.f, 0.f}, cs[4][2];
+          auto kb = [&](int j, uint32_t(&r)[4]) {
+            b_rows<LD>(r, kt + j * kC * LD, part * 16, x * 16, lane);
+          };
+          mma_planes<NI, NI, NI>(qk[0], qk[1], qa, kb);
+          mma_planes<NI, NI, NI>(kk[0], kk[1], ka, kb);
+        }
+      float rs[2] = {0.f, 0.f}, cs[2][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         cs[t][0] = cs[t][1] = 0.f;
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          const int i = r0 + e2 * 8, j = half * 32 + 8 * t + c0;
+          const int i = r0 + e2 * 8, j = part * 16 + 8 * t + c0;
           float v1[2], v2[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int e = 2 * e2 + f;
             const float dec = j + f <= i ? decay_between(g, i, j + f) : 0.f;
             const float bd = j + f < i ? g.b[i] * dec : 0.f;
-            const float a1 = d.scale * dec;
-            v1[f] = a1 * da[t][e];
+            v1[f] = d.scale * dec * da[t][e];
             v2[f] = -bd * wm[t][e];
             const float pair = v1[f] * qk[t][e] + v2[f] * kk[t][e];
             rs[e2] += pair;
@@ -1193,16 +1299,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int e2 = 0; e2 < 2; ++e2) {
         rs[e2] += __shfl_xor_sync(0xffffffffu, rs[e2], 1);
         rs[e2] += __shfl_xor_sync(0xffffffffu, rs[e2], 2);
-        if ((lane & 3) == 0) sm.row[half][r0 + e2 * 8] = rs[e2];
+        if ((lane & 3) == 0) sm.row[part][r0 + e2 * 8] = rs[e2];
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           float v = cs[t][f];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane < 4) sm.col[strip][half * 32 + 8 * t + c0 + f] = v;
+          if (lane < 4) sm.col[strip][part * 16 + 8 * t + c0 + f] = v;
         }
     }
     {  // scale e^G q . (dY S0), and its part of dq
@@ -1211,18 +1317,21 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
       for (int t = 0; t < HT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = r0 + (e >> 1) * 8, j = half * (NP / 2) + 8 * t + c0 + (e & 1);
-          float qv = 0.f;
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int i = r0 + e2 * 8, j = part * WC + 8 * t + c0;
+          float qx = 0.f, qy = 0.f;
 #pragma unroll
-          for (int l = NI - 1; l >= 0; --l) qv += to_f(qt[l * kC * LD + i * LD + j]);
-          const float v = dqh[t][e] * (e >> 1 ? f1 : f0);
-          tq[t][e] += v;
-          (e >> 1 ? s1 : s0) += v * qv;
+          for (int l = NI - 1; l >= 0; --l) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(qt + l * kC * LD + i * LD + j);
+            qx += __uint_as_float(x << 16), qy += __uint_as_float(x & 0xffff0000u);
+          }
+          const float f = e2 ? f1 : f0, v0 = dqh[t][2 * e2] * f, v1 = dqh[t][2 * e2 + 1] * f;
+          tq[t][2 * e2] += v0, tq[t][2 * e2 + 1] += v1;
+          (e2 ? s1 : s0) += fmaf(v0, qx, v1 * qy);
         }
       s0 += __shfl_xor_sync(0xffffffffu, s0, 1), s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
       s0 += __shfl_xor_sync(0xffffffffu, s0, 2), s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
-      if ((lane & 3) == 0) sm.qd[half][r0] = s0, sm.qd[half][r0 + 8] = s1;
+      if ((lane & 3) == 0) sm.qd[part][r0] = s0, sm.qd[part][r0 + 8] = s1;
     }
     __syncthreads();
 #pragma unroll
@@ -1237,7 +1346,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int np = 0; np < HT / 2; ++np) {
           auto kbl = [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+            b_cols<LD>(x, kt + j * kC * LD, part * WC + np * 16, kb * 16, lane);
           };
           mma_planes<NL, NI, max2(NL, NI)>(tq[2 * np], tq[2 * np + 1], a, kbl);
           mma_planes<NL, NI, max2(NL, NI)>(tk[2 * np], tk[2 * np + 1], a2, kbl);
@@ -1253,11 +1362,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int np = 0; np < HT / 2; ++np) {
           mma_planes<NL, NI, max2(NL, NI)>(
               tk[2 * np], tk[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-                b_cols<LD>(x, qt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+                b_cols<LD>(x, qt + j * kC * LD, part * WC + np * 16, kb * 16, lane);
               });
           mma_planes<NL, NI, max2(NL, NI)>(
               tk[2 * np], tk[2 * np + 1], a2, [&](int j, uint32_t(&x)[4]) {
-                b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, kb * 16, lane);
+                b_cols<LD>(x, kt + j * kC * LD, part * WC + np * 16, kb * 16, lane);
               });
         }
       }
@@ -1267,11 +1376,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int i = 2 * lane + x;
-        float u = 0.f, r = 0.f, ww = 0.f;
+        float u = 0.f, r = 0.f, ww = 0.f, rs = 0.f, cs = 0.f, qs = 0.f;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
-        const float cols = ((sm.col[0][i] + sm.col[1][i]) + sm.col[2][i]) + sm.col[3][i];
-        dg[x] = ((sm.row[0][i] + sm.row[1][i]) - cols) + ((sm.qd[0][i] + sm.qd[1][i]) - r) - u;
+        for (int p = 0; p < 16; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) rs += sm.row[p][i], cs += sm.col[p][i], qs += sm.qd[p][i];
+        dg[x] = (rs - cs) + (qs - r) - u;
         wii[x] = ww;
         last += u;
       }
@@ -1279,7 +1389,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
       float ss = 0.f;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) ss += sm.dot[p];
+      for (int p = 0; p < 16; ++p) ss += sm.dot[p];
       last += ex2(g.gh[kC - 1]) * ss;
       if (lane == 31) dg[1] += last;
       // sums from each token on
@@ -1322,7 +1432,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   for (int t = 0; t < HT; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = r0 + (e >> 1) * 8, j = half * (NP / 2) + 8 * t + c0 + (e & 1);
+      const int i = r0 + (e >> 1) * 8, j = part * WC + 8 * t + c0 + (e & 1);
       if (i < rows && j < d.N) {
         const int64_t o = (((int64_t)b * d.T + t0 + i) * d.G + grp) * d.N + j;
         if (d.nb == 1) {
@@ -1492,7 +1602,7 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
           *v = static_cast<const T*>(in.v);
   const int64_t n = (int64_t)d.B * d.H * d.nc, chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
   const auto prep = k_delta_prep<T, NP, BWD>;
-  DELTA_LAUNCH("k_delta_prep", prep, n, kPrepThreads, (prep_smem<T, NP, BWD>()), d, q, k,
+  DELTA_LAUNCH("k_delta_prep", prep, n, kPrepThreads, (PrepSmem<T, NP, BWD>::total), d, q, k,
                static_cast<const T*>(in.dt), in.dt_bias, in.A, static_cast<const T*>(in.beta),
                static_cast<const T*>(dy), in.lengths, w);
   if constexpr (sizeof(T) == 2) {
@@ -1515,7 +1625,7 @@ int delta_forward(const DeltaDims& d, const DeltaIn& in, const DeltaWs& w, void*
   const int st = delta_states<T, NP, false>(d, in, nullptr, w, final_states, s);
   if (st != SSD_OK) return st;
   const auto out = k_delta_out<T, TO, NP>;
-  DELTA_LAUNCH("k_delta_out", out, (int64_t)d.B * d.H * d.nc, kOutThreads, (out_smem<T, TO, NP>()), d,
+  DELTA_LAUNCH("k_delta_out", out, (int64_t)d.B * d.H * d.nc, kOutThreads, (OutSmem<T, TO, NP>::total), d,
                static_cast<const T*>(in.q), static_cast<const T*>(in.k), in.lengths, w,
                static_cast<TO*>(y));
   return SSD_OK;
@@ -1546,7 +1656,7 @@ int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, c
   const auto grad = k_delta_grad<T, TO, NP>;
   TO *dq = static_cast<TO*>(g.dq), *dk = static_cast<TO*>(g.dk);
   DELTA_LAUNCH("k_delta_grad", grad, (int64_t)d.B * d.G * d.nb * d.nc, kGradThreads,
-               (grad_smem<T, TO, NP>()), d, q, k, static_cast<const T*>(in.dt), in.dt_bias, in.A, dy,
+               (GradSmem<T, TO, NP>::total), d, q, k, static_cast<const T*>(in.dt), in.dt_bias, in.A, dy,
                in.lengths, w, dq, dk, static_cast<TO*>(g.dv), static_cast<TO*>(g.ddt),
                static_cast<TO*>(g.dbeta));
   if (d.nb > 1) {
@@ -1623,6 +1733,7 @@ int ssd_gated_delta_fwd(const ssd_delta_shape* shape, const void* q, const void*
   if (st != SSD_OK) return st;
   if (!y || off(y, shape->out_dtype == SSD_BF16 ? 2 : 4) || off(final_states, 4))
     return SSD_ERR_INVALID_ARG;
+  d.wide = d.P % 2 == 0 && !off(y, shape->out_dtype == SSD_BF16 ? 4 : 8);
   const DeltaWs w = delta_ws(d, workspace, false);
   if ((st = check_ws(w, workspace, workspace_bytes)) != SSD_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
