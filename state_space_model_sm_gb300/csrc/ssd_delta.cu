@@ -45,6 +45,7 @@ struct DeltaDims {
   int rep;  // heads of a group
   int Ps;   // value rows in the workspace: P up to a multiple of 16
   int NP;   // key columns in the workspace: 64 or 128
+  int ip;   // planes of the images of keys and queries
   int nb;   // head blocks of a group in the gradient
   float scale;
   int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
@@ -52,14 +53,23 @@ struct DeltaDims {
   int wide;                        // whether pairs of output columns can be written at once
 };
 
-// Gates of a chunk: the log2 decays' running sum in two floats, and b.
+// Gates of a chunk's tokens: the log2 decays' running sum G in two floats, b, and what
+// the chains multiply rows and columns by, with the powers of two that undo the row
+// scales of the images of K, Q and X^T (2^k, 2^q, 2^x of each token).
 struct Gates {
   float gh[kC], gl[kC], b[kC];
+  float fz[kC];  // b e^G 2^k
+  float fu[kC];  // e^(G63 - G) 2^k
+  float fx[kC];  // 2^x
+  float fq[kC];  // scale e^G 2^q (backward)
 };
+constexpr int kGateCopies = sizeof(Gates) / 16;
 
 struct DeltaWs {
   Gates* gates;  // (B, H, nc)
-  bf16* X;       // (B, H, nc, 3, 64, 64) planes of (I + M)^-1
+  bf16* X;       // (B, H, nc, 2, 64, 64) fp16 planes of the transpose of (I + M)^-1
+  bf16* K;       // (B, G, nc, planes, 64, NP) fp16 planes of the keys, rows scaled
+  bf16* Q;       // the same of the queries (backward)
   float* U;      // (B, H, nc, Ps, 64)  transposed: [p][token]
   float* S0;     // (B, H, nc, Ps, NP)  the state in front of each chunk
   // backward
@@ -190,25 +200,31 @@ __device__ __forceinline__ void fetch_tile(bf16* dst, const T* src, int64_t ld, 
   }
   load_tile<T, W, LD, THREADS>(dst, src, ld, rv, cv, vec);
 }
-// The planes of X, started asynchronously.
-template <int THREADS>
-__device__ __forceinline__ void copy_x(bf16* dst, const bf16* src) {
-  for (int i = threadIdx.x; i < 3 * kC * 8; i += THREADS)
-    cp_async<16>(dst + i / 8 * kTP + i % 8 * 8, src + i * 8);
+// ROWS dense rows of W 16-bit values of the workspace, started asynchronously.
+template <int ROWS, int W, int LD, int THREADS>
+__device__ __forceinline__ void copy_image(bf16* dst, const bf16* src) {
+#pragma unroll
+  for (int i = threadIdx.x; i < ROWS * (W / 8); i += THREADS)
+    cp_async<16>(dst + i / (W / 8) * LD + i % (W / 8) * 8, src + i * 8);
 }
+// Planes of an input's fp16 image.
+template <typename T>
+constexpr int image_planes() { return sizeof(T) == 2 ? 1 : 2; }
 
 // A raw tile of tokens x 64 value columns, as it is, for reads element by element.
 template <typename T>
 constexpr int raw_pitch() { return sizeof(T) == 2 ? kTP : kF; }
 template <typename T, int THREADS>
-__device__ __forceinline__ void load_raw(T* dst, const T* src, int64_t ld, int rv, int cv, bool vec) {
+__device__ __forceinline__ void fetch_raw(T* dst, const T* src, int64_t ld, int rv, int cv, bool vec) {
   constexpr int V = 16 / sizeof(T);
   if (vec) {
     for (int i = threadIdx.x; i < kC * (kC / V); i += THREADS) {
       const int r = i / (kC / V), c = i % (kC / V) * V;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rv && c < cv) v = *reinterpret_cast<const uint4*>(src + r * ld + c);
-      *reinterpret_cast<uint4*>(dst + r * raw_pitch<T>() + c) = v;
+      T* to = dst + r * raw_pitch<T>() + c;
+      if (r < rv && c < cv)
+        cp_async<16>(to, src + r * ld + c);
+      else
+        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
     }
   } else {
     for (int i = threadIdx.x; i < kC * kC; i += THREADS) {
@@ -259,38 +275,87 @@ __device__ __forceinline__ void lower_product(float (&acc)[8][4], const bf16* A,
 
 constexpr int kPrepThreads = 128;
 
-// Shared memory: the keys' tile, whose place M takes; the queries' (backward), whose
-// place X takes; the planes of the scaled Q K^T over both; and dY's tile.
+// Shared memory: the tiles of keys and (backward) queries, whose place the planes of M
+// take, and the diagonal blocks in fp32; dY's tile.
 template <typename T, int NP, bool BWD>
 struct PrepSmem {
-  static constexpr size_t tile = (size_t)planes_of<T>() * kC * (NP + 8) * 2;
-  static constexpr size_t f32 = (size_t)kC * kF * 4;
-  static constexpr size_t one = tile > f32 ? tile : f32;
+  static constexpr size_t tiles = (size_t)planes_of<T>() * kC * (NP + 8) * 2 * (BWD ? 2 : 1);
+  static constexpr size_t m = (size_t)3 * kC * kTP * 2, diag = (size_t)4 * 16 * 20 * 4;
+  static constexpr size_t one = tiles > m + diag ? tiles : m + diag;
   static constexpr size_t dy = BWD ? (size_t)planes_of<T>() * kC * kTP * 2 : 0;
-  static constexpr size_t total = sizeof(Gates) + one + (BWD ? one : f32) + dy;
+  static constexpr size_t total = sizeof(Gates) + one + dy;
 };
 
-// Gates and X of one chunk of one head; in the backward also E^T = dY^T (Q K^T e^(..)).
+// The scale that brings row tid / 2 of a tile (two threads a row) to at most 2, and, with
+// `to`, the scaled row as fp16 planes.  Returns the inverse.
+template <int NI, int NIMG, int NP>
+__device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
+  constexpr int LD = NP + 8, W = NP / 2;
+  const int r = threadIdx.x >> 1, c0 = (threadIdx.x & 1) * W;
+  auto piece = [&](int c, float(&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.f;
+#pragma unroll
+    for (int l = NI - 1; l >= 0; --l) {
+      float x[8];
+      lm::unpack<bf16, 8>(lm::ld_raw<bf16, 8>(tile + l * kC * LD + r * LD + c0 + c), x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += x[j];
+    }
+  };
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < W; c += 8) {
+    float f[8];
+    piece(c, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const Scale s = scale_of(m);
+  if (to) {
+#pragma unroll
+    for (int c = 0; c < W; c += 8) {
+      float f[8];
+      piece(c, f);
+      uint32_t p[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2h(f[2 * j], f[2 * j + 1], s.s, p[j]);
+#pragma unroll
+      for (int l = 0; l < NIMG; ++l)
+        *reinterpret_cast<uint4*>(to + l * kC * NP + r * NP + c0 + c) =
+            make_uint4(p[0][l], p[1][l], p[2][l], p[3][l]);
+    }
+  }
+  return s.inv;
+}
+
+// Gates, images and X of one chunk of one head; in the backward also
+// E^T = dY^T (Q K^T e^(..)).
 //
-// X by halves: the four 16 x 16 blocks on the diagonal by substitution, a column a
-// thread; then twice  [A 0; C B]^-1 = [A' 0; -B' C A', B'].  Substitution is stable
-// whatever the keys (a run of equal keys makes I + M ill suited to a power series).
+// X^T by strips of 16 columns of X, a warp each: with D_i the inverse of the diagonal
+// block i of I + M (by substitution, a column a lane; stable whatever the keys, where a
+// run of equal keys makes I + M ill suited to a power series),
+//     X_jj = D_j,   X_ij^T = -(sum_{j <= l < i} X_lj^T M_il^T) D_i^T,
+// a chain of 16 x 16 products whose left operands are the last accumulators.  (With both
+// halves of X merged by fp32 products from shared memory the kernel was bound by shared
+// memory, 62 us for 3072 chunks at 88 % of its rate.)
 template <typename T, int NP, bool BWD>
-__global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 5 : 1)
+__global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
     k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
                  const T* __restrict__ dt, const float* __restrict__ dt_bias,
                  const float* __restrict__ A, const T* __restrict__ beta,
                  const T* __restrict__ dy, const int* __restrict__ lengths, DeltaWs w) {
-  constexpr int NI = planes_of<T>(), LD = NP + 8;
+  constexpr int NI = planes_of<T>(), NIMG = image_planes<T>(), LD = NP + 8;
   using SM = PrepSmem<T, NP, BWD>;
   extern __shared__ __align__(16) unsigned char smem[];
   Gates& g = *reinterpret_cast<Gates*>(smem);
   bf16* const Kt = reinterpret_cast<bf16*>(smem + sizeof(Gates));
-  bf16* const Qt = reinterpret_cast<bf16*>(smem + sizeof(Gates) + SM::one);
-  bf16* const yt = Qt + SM::one / 2;
-  float* const M = reinterpret_cast<float*>(Kt);
-  float* const X = reinterpret_cast<float*>(Qt);
+  bf16* const Qt = Kt + NI * kC * LD;
+  bf16* const yt = reinterpret_cast<bf16*>(smem + sizeof(Gates) + SM::one);
+  bf16* const Mp = Kt;
   const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  float* const diag = reinterpret_cast<float*>(smem + sizeof(Gates) + SM::m) + strip * 16 * 20;
   const Place pl = place(d, blockIdx.x);
   const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
   if (t0 >= n) return;
@@ -344,10 +409,20 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 5 : 1)
   }
   cp_wait<BWD ? 1 : 0>();
   __syncthreads();
-  if (tid < sizeof(Gates) / 16)
-    reinterpret_cast<uint4*>(w.gates + pl.i)[tid] = reinterpret_cast<const uint4*>(&g)[tid];
 
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
+  const bool first = pl.h % d.rep == 0;  // writes the images of its group
+  const int64_t img = (((int64_t)pl.b * d.G + grp) * d.nc + pl.c) * NIMG * kC * NP;
+  const float ki = row_image<NI, NIMG, NP>(Kt, first ? w.K + img : nullptr);
+  float qi = 0.f;
+  if constexpr (BWD) qi = row_image<NI, NIMG, NP>(Qt, first ? w.Q + img : nullptr);
+  if ((tid & 1) == 0) {
+    const int i = tid >> 1;
+    const float eg = ex2(g.gh[i]);
+    g.fz[i] = g.b[i] * eg * ki;
+    g.fu[i] = decay_between(g, kC - 1, i) * ki;
+    g.fq[i] = d.scale * eg * qi;
+  }
   float acc[8][4], qk[BWD ? 8 : 1][4];
   lower_product<NI, NP>(acc, Kt, Kt, strip, lane);
   if constexpr (BWD) lower_product<NI, NP>(qk, Qt, Kt, strip, lane);
@@ -356,94 +431,104 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 5 : 1)
   for (int t = 0; t < 8; ++t)
     if (t < 2 * strip + 2)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = r0 + (e >> 1) * 8, j = 8 * t + c0 + (e & 1);
-        M[i * kF + j] = j < i ? g.b[i] * decay_between(g, i, j) * acc[t][e] : 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const int i = r0 + e * 8, j = 8 * t + c0;
+        float v[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          v[f] = j + f < i ? g.b[i] * decay_between(g, i, j + f) * acc[t][2 * e + f] : 0.f;
+        if (t < 2 * strip) {
+          uint32_t p[3];
+          split2<3>(v[0], v[1], p);
+#pragma unroll
+          for (int l = 0; l < 3; ++l)
+            *reinterpret_cast<uint32_t*>(Mp + l * kC * kTP + i * kTP + j) = p[l];
+        } else {
+          *reinterpret_cast<float2*>(diag + (i & 15) * 20 + (j & 15)) = make_float2(v[0], v[1]);
+        }
       }
-  __syncthreads();
-  if (tid < kC) {  // column j of the inverse of the diagonal block from row o on
-    const int o = tid & 48, j = tid & 15;
+  __syncwarp();
+  {  // column j of D: the diagonal block is this warp's own
+    const int j = lane & 15;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == j ? 1.f : 0.f;
 #pragma unroll
-      for (int l = 0; l < i; ++l) s = fmaf(-M[(o + i) * kF + o + l], x[l], s);
+      for (int l = 0; l < i; ++l) s = fmaf(-diag[i * 20 + l], x[l], s);
       x[i] = s;
-      X[(o + i) * kF + o + j] = s;
     }
-  }
-  __syncthreads();
-  {  // blocks (1, 0) and (3, 2): 64 threads each, four columns of a row a thread
-    const int o = (tid >> 6) * 32, r = (tid & 63) >> 2, c = (tid & 3) * 4;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    __syncwarp();
+    if (lane < 16)
 #pragma unroll
-    for (int l = 0; l < 16; ++l) {
-      const float m = M[(o + 16 + r) * kF + o + l];
-      const float4 x = *reinterpret_cast<const float4*>(X + (o + l) * kF + o + c);
-      s[0] = fmaf(m, x.x, s[0]), s[1] = fmaf(m, x.y, s[1]);
-      s[2] = fmaf(m, x.z, s[2]), s[3] = fmaf(m, x.w, s[3]);
-    }
-    // M's upper part is free: the product waits there
-    *reinterpret_cast<float4*>(M + (o + r) * kF + o + 16 + c) = make_float4(s[0], s[1], s[2], s[3]);
-    __syncthreads();
-    s[0] = s[1] = s[2] = s[3] = 0.f;
+      for (int i = 0; i < 16; ++i) {
+        diag[i * 20 + j] = x[i];
+        uint32_t p[3];
+        split2<3>(x[i], 0.f, p);
 #pragma unroll
-    for (int l = 0; l < 16; ++l) {
-      const float m = -X[(o + 16 + r) * kF + o + 16 + l];
-      const float4 x = *reinterpret_cast<const float4*>(M + (o + l) * kF + o + 16 + c);
-      s[0] = fmaf(m, x.x, s[0]), s[1] = fmaf(m, x.y, s[1]);
-      s[2] = fmaf(m, x.z, s[2]), s[3] = fmaf(m, x.w, s[3]);
-    }
-    *reinterpret_cast<float4*>(X + (o + 16 + r) * kF + o + c) = make_float4(s[0], s[1], s[2], s[3]);
-    *reinterpret_cast<float4*>(X + (o + r) * kF + o + 16 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __syncthreads();
-  {  // the block of rows 32.., columns ..31: eight columns of a row a thread
-    const int r = tid >> 2, c = (tid & 3) * 8;
-    float s[8];
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      const float* L = pass == 0 ? M + (32 + r) * kF : X + (32 + r) * kF + 32;
-      const float* R = pass == 0 ? X + c : M + 32 + c;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = 0.f;
-#pragma unroll 8
-      for (int l = 0; l < 32; ++l) {
-        const float m = L[l];
-        const float4 u = *reinterpret_cast<const float4*>(R + l * kF);
-        const float4 v = *reinterpret_cast<const float4*>(R + l * kF + 4);
-        s[0] = fmaf(m, u.x, s[0]), s[1] = fmaf(m, u.y, s[1]);
-        s[2] = fmaf(m, u.z, s[2]), s[3] = fmaf(m, u.w, s[3]);
-        s[4] = fmaf(m, v.x, s[4]), s[5] = fmaf(m, v.y, s[5]);
-        s[6] = fmaf(m, v.z, s[6]), s[7] = fmaf(m, v.w, s[7]);
+        for (int l = 0; l < 3; ++l)
+          reinterpret_cast<uint16_t*>(Mp)[l * kC * kTP + (strip * 16 + i) * kTP + strip * 16 + j] =
+              (uint16_t)(p[l] & 0xffffu);
       }
-      float* to = pass == 0 ? M + r * kF + 32 + c : X + (32 + r) * kF + c;
-      const float sg = pass == 0 ? 1.f : -1.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) to[e] = sg * s[e];
-      if (pass == 0) __syncthreads();
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) X[r * kF + 32 + c + e] = 0.f;
   }
   __syncthreads();
-  bf16* const xp = w.X + pl.i * (3 * kC * kC);
-  for (int i = tid; i < kC * 8; i += kPrepThreads) {
-    const float* s = X + (i >> 3) * kF + (i & 7) * 8;
-    uint32_t p[4][3];
+  {
+    float x[4][2][4];  // X^T, columns of block row i: rows strip * 16 + lane / 4, + 8
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2<3>(s[2 * e], s[2 * e + 1], p[e]);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int l = 0; l < 3; ++l)
-      *reinterpret_cast<uint4*>(xp + l * kC * kC + i * 8) =
-          make_uint4(p[0][l], p[1][l], p[2][l], p[3][l]);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[i][t][e] = i == strip ? diag[(8 * t + c0 + (e & 1)) * 20 + (lane >> 2) + (e >> 1) * 8] : 0.f;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (i > strip) {
+        float s[2][4] = {};
+#pragma unroll
+        for (int l = 0; l < i; ++l)
+          if (l >= strip) {
+            uint32_t a[3][4];
+            a_from_acc<3>(a, x[l], 0);
+            mma_planes<3, 3, 3>(s[0], s[1], a, [&](int j, uint32_t(&r)[4]) {
+              b_rows<kTP>(r, Mp + j * kC * kTP, i * 16, l * 16, lane);
+            });
+          }
+        uint32_t a[3][4];
+        a_from_acc<3>(a, s, 0);
+        mma_planes<3, 3, 3>(x[i][0], x[i][1], a, [&](int j, uint32_t(&r)[4]) {
+          b_rows<kTP>(r, Mp + j * kC * kTP, i * 16, i * 16, lane);
+        });
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][t][e] = -x[i][t][e];
+      }
+    float m0, m1;
+    row_max<8>(reinterpret_cast<const float(&)[8][4]>(x), m0, m1);
+    const Scale s0 = scale_of(m0), s1 = scale_of(m1);
+    if ((lane & 3) == 0) g.fx[r0] = s0.inv, g.fx[r0 + 8] = s1.inv;
+    bf16* const xp = w.X + pl.i * (2 * kC * kC);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t p[2];
+          split2h(x[i][t][2 * e], x[i][t][2 * e + 1], e ? s1.s : s0.s, p);
+#pragma unroll
+          for (int l = 0; l < 2; ++l)
+            *reinterpret_cast<uint32_t*>(xp + l * kC * kC + (r0 + 8 * e) * kC + i * 16 + 8 * t + c0) =
+                p[l];
+        }
   }
+  __syncthreads();
+  if (tid < kGateCopies)
+    reinterpret_cast<uint4*>(w.gates + pl.i)[tid] = reinterpret_cast<const uint4*>(&g)[tid];
   if constexpr (BWD) {
     // E^T[p][j] = sum_{i >= j} dy[i][p] scale e^(G_i - G_j) q_i . k_j
-    __syncthreads();  // X is written out: its and M's place takes the planes
-    bf16* const at = reinterpret_cast<bf16*>(M);
-    static_assert(3 * kC * kTP * 2 <= 2 * SM::one, "the planes fit");
+    bf16* const at = Mp;  // M's planes are read
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -502,11 +587,11 @@ constexpr int kChainThreads = 128;
 
 template <typename T, int NP>
 constexpr size_t chain_stage() {
-  return sizeof(Gates) + (size_t)planes_of<T>() * kC * (NP + 8) * 2 +
-         (size_t)kC * raw_pitch<T>() * sizeof(T) + (size_t)3 * kC * kTP * 2;
+  return sizeof(Gates) + (size_t)image_planes<T>() * kC * (NP + 8) * 2 +
+         (size_t)kC * raw_pitch<T>() * sizeof(T) + (size_t)2 * kC * kTP * 2;
 }
-template <typename T, int NP, bool ASYNC>
-constexpr size_t chain_smem() { return chain_stage<T, NP>() * (ASYNC ? 2 : 1); }
+template <typename T, int NP>
+constexpr size_t chain_smem() { return 2 * chain_stage<T, NP>(); }
 
 // A state strip (16 rows of a warp, NP columns) from or to rows of N floats.
 template <int NP>
@@ -548,14 +633,16 @@ __device__ __forceinline__ void store_strip(float* dst, const float (&S)[NT][4],
 // its state in registers (16 x NP fp32, an accumulator).  A chunk is three products,
 //     Z^T = S K^T,   U^T = (b (V - e^G Z))^T X^T,   S <- e^G63 S + (e^(G63 - G) U)^T K,
 // each left operand formed from the last accumulator, so the only traffic between them
-// is the shared tiles of K, V and X, copied while the chunk before is at work (ASYNC).
-// KEEP: also writes b e^G Z, for the backward.
-template <typename T, int NP, bool ASYNC, bool KEEP>
+// is the shared tiles of K, V and X, copied while the chunk before is at work.
+// Left operands are two fp16 planes of rows scaled by their largest value, K is one
+// (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
+// bf16 take 504.  The products are issued by one warp per SM quarter at 8 clocks each,
+// which bounds a chunk by 1.3 us.  KEEP: also writes b e^G Z, for the backward.
+template <typename T, int NP, bool KEEP>
 __global__ void __launch_bounds__(kChainThreads)
-    k_delta_chain(DeltaDims d, const T* __restrict__ k, const T* __restrict__ v,
-                  const float* __restrict__ init, const int* __restrict__ lengths, DeltaWs w,
-                  float* __restrict__ final_states) {
-  constexpr int NI = planes_of<T>(), LD = NP + 8, RP = raw_pitch<T>(), M = max2(NI, 3);
+    k_delta_chain(DeltaDims d, const T* __restrict__ v, const float* __restrict__ init,
+                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states) {
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
   const int ptiles = (d.Ps + kC - 1) / kC;
@@ -565,45 +652,35 @@ __global__ void __launch_bounds__(kChainThreads)
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
   const int row = p0 + strip * 16;  // this warp's first value row
   const bool active = row < d.Ps;
-  const T* const kg = k + b * d.kb + (int64_t)(h / d.rep) * d.N;
   const T* const vg = v + b * d.vb + (int64_t)h * d.P + p0;
+  const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * NP;
 
   auto stage = [&](int s) { return smem + s * chain_stage<T, NP>(); };
   auto fetch = [&](int c, int s) {
     unsigned char* at = stage(s);
-    const Gates* src = w.gates + bh * d.nc + c;
-    if (threadIdx.x < sizeof(Gates) / 16)
-      cp_async<16>(at + threadIdx.x * 16, reinterpret_cast<const char*>(src) + threadIdx.x * 16);
+    if (threadIdx.x < kGateCopies)
+      cp_async<16>(at + threadIdx.x * 16,
+                   reinterpret_cast<const char*>(w.gates + bh * d.nc + c) + threadIdx.x * 16);
     bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
     T* vt = reinterpret_cast<T*>(kt + NI * kC * LD);
     bf16* xt = reinterpret_cast<bf16*>(vt + kC * RP);
-    const int t0 = c * kC, rv = min(kC, n - t0);
-    if constexpr (ASYNC) {
-      copy_tile<NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N);
-      copy_tile<kC, kTP, kChainThreads>(vt, vg + t0 * d.vs, d.vs, rv, d.P - p0);
-    } else {
-      load_tile<T, NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N, d.vk);
-      load_raw<T, kChainThreads>(vt, vg + t0 * d.vs, d.vs, rv, d.P - p0, d.vv);
-    }
-    copy_x<kChainThreads>(xt, w.X + (bh * d.nc + c) * (3 * kC * kC));
+    copy_image<NI * kC, NP, LD, kChainThreads>(kt, kg + (int64_t)c * NI * kC * NP);
+    fetch_raw<T, kChainThreads>(vt, vg + (int64_t)c * kC * d.vs, d.vs, min(kC, n - c * kC), d.P - p0,
+                                d.vv);
+    copy_image<2 * kC, kC, kTP, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kC));
     cp_commit();
   };
 
   float S[NP / 8][4];
   load_state<NP>(S, init && active ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-  if (ASYNC && nc > 0) fetch(0, 0);
+  if (nc > 0) fetch(0, 0);
   for (int c = 0; c < nc; ++c) {
-    const int s = ASYNC ? c & 1 : 0;
-    if constexpr (ASYNC) {
-      if (c + 1 < nc) {
-        fetch(c + 1, s ^ 1);
-        cp_wait<1>();
-      } else {
-        cp_wait<0>();
-      }
+    const int s = c & 1;
+    if (c + 1 < nc) {
+      fetch(c + 1, s ^ 1);
+      cp_wait<1>();
     } else {
-      fetch(c, 0);
       cp_wait<0>();
     }
     __syncthreads();
@@ -613,7 +690,10 @@ __global__ void __launch_bounds__(kChainThreads)
       const T* vt = reinterpret_cast<const T*>(kt + NI * kC * LD);
       const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
       const int64_t at = bh * d.nc + c;
-      store_strip<NP / 8>(w.S0 + (at * d.Ps + row) * NP, S, lane);
+      float m0, m1;
+      row_max<NP / 8>(S, m0, m1);
+      const Scale s0 = scale_of(m0), s1 = scale_of(m1);
+      const float least0 = m0 * 5.9604644775390625e-8f, least1 = m1 * 5.9604644775390625e-8f;  // 2^-24
       float r[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -621,26 +701,34 @@ __global__ void __launch_bounds__(kChainThreads)
         for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < NP / 16; ++kk) {
-        uint32_t a[3][4];
-        a_from_acc<3>(a, S, kk);
+        uint32_t a[2][4];
+        a_from_acc_h(a, S, kk, s0.s, s1.s);
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          mma_planes<3, NI, M>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          mma_planes_h<NI>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
             b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
           });
       }
-      // r = b (v - e^G z), of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
-      float z[8][4];
+      store_strip<NP / 8>(w.S0 + (at * d.Ps + row) * NP, S, lane);
+      // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
+      float z[KEEP ? 8 : 1][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 8 * t + t2 + (e & 1), p = strip * 16 + g8 + (e >> 1) * 8;
-          const float bi = g.b[i];
-          z[t][e] = bi * ex2(g.gh[i]) * r[t][e];
-          r[t][e] = fmaf(bi, to_f(vt[i * RP + p]), -z[t][e]);
+        for (int f = 0; f < 2; ++f) {
+          const int i = 8 * t + t2 + f;
+          const float bi = g.b[i], fz = g.fz[i], fx = g.fx[i];
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const int e = 2 * o + f, p = strip * 16 + g8 + o * 8;
+            const float ze = fz * (o ? s1.inv : s0.inv) * r[t][e];
+            r[t][e] = fx * fmaf(bi, to_f(vt[i * RP + p]), -ze);
+            if constexpr (KEEP) z[t][e] = ze;
+          }
         }
       if constexpr (KEEP) store_strip<8>(w.Zb + (at * d.Ps + row) * kC, z, lane);
+      row_max<8>(r, m0, m1);
+      const Scale q0 = scale_of(m0), q1 = scale_of(m1);
       float u[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -648,38 +736,47 @@ __global__ void __launch_bounds__(kChainThreads)
         for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[3][4];
-        a_from_acc<3>(a, r, kb);
+        uint32_t a[2][4];
+        a_from_acc_h(a, r, kb, q0.s, q1.s);
 #pragma unroll
         for (int np = kb; np < 4; ++np)
-          mma_planes<3, 3, 3>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+          mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
           });
       }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        u[t][0] *= q0.inv, u[t][1] *= q0.inv, u[t][2] *= q1.inv, u[t][3] *= q1.inv;
       store_strip<8>(w.U + (at * d.Ps + row) * kC, u, lane);
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = decay_between(g, kC - 1, 8 * t + t2 + e);
-          u[t][e] *= f;
-          u[t][2 + e] *= f;
+        for (int f = 0; f < 2; ++f) {
+          const float fu = g.fu[8 * t + t2 + f];
+          u[t][f] *= fu;
+          u[t][2 + f] *= fu;
         }
-      const float end = ex2(g.gh[kC - 1]);
+      // the state takes the products in the scale of U, or of its own where that is
+      // 2^24 larger (what U would lose there is below the state's own rounding)
+      row_max<8>(u, m0, m1);
+      const Scale u0 = scale_of(fmaxf(m0, least0)),
+                  u1 = scale_of(fmaxf(m1, least1));
+      const float end = ex2(g.gh[kC - 1]), d0 = end * u0.s, d1 = end * u1.s;
 #pragma unroll
-      for (int t = 0; t < NP / 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[t][e] *= end;
+      for (int t = 0; t < NP / 8; ++t) S[t][0] *= d0, S[t][1] *= d0, S[t][2] *= d1, S[t][3] *= d1;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[3][4];
-        a_from_acc<3>(a, u, kb);
+        uint32_t a[2][4];
+        a_from_acc_h(a, u, kb, u0.s, u1.s);
 #pragma unroll
         for (int np = 0; np < NP / 16; ++np)
-          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
             b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
           });
       }
+#pragma unroll
+      for (int t = 0; t < NP / 8; ++t)
+        S[t][0] *= u0.inv, S[t][1] *= u0.inv, S[t][2] *= u1.inv, S[t][3] *= u1.inv;
     }
     __syncthreads();
   }
@@ -735,7 +832,7 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
   fetch_tile<T, NP, LD, kOutThreads>(kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
                                      d.N, d.vk);
   cp_commit();
-  if (tid < sizeof(Gates) / 16)
+  if (tid < kGateCopies)
     reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + pl.i)[tid];
   WsTile<NP, LD, kOutThreads> ws;
   WsTile<kC, kTP, kOutThreads> wu;
@@ -838,21 +935,25 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
 
 template <typename T, int NP>
 constexpr size_t back_stage() {
-  return chain_stage<T, NP>() + (size_t)planes_of<T>() * kC * (NP + 8) * 2;
+  return chain_stage<T, NP>() + (size_t)image_planes<T>() * kC * (NP + 8) * 2;
 }
-template <typename T, int NP, bool ASYNC>
-constexpr size_t back_smem() { return back_stage<T, NP>() * (ASYNC ? 2 : 1); }
+// (three stages of fp32 inputs' size would not fit; one holds the chunk at work)
+template <typename T, int NP>
+constexpr int back_stages() { return 2 * back_stage<T, NP>() <= 220 * 1024 ? 2 : 1; }
+template <typename T, int NP>
+constexpr size_t back_smem() { return back_stages<T, NP>() * back_stage<T, NP>(); }
 
 // The chain of the backward, from the last chunk to the first, with the gradient of the
 // state behind the chunk in registers:
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
-//     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K.
-template <typename T, int NP, bool ASYNC>
+//     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
+// in the manner of k_delta_chain: 444 products a chunk.
+template <typename T, int NP>
 __global__ void __launch_bounds__(kChainThreads)
-    k_delta_back(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
-                 const T* __restrict__ dy, const float* __restrict__ dfinal,
+    k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit) {
-  constexpr int NI = planes_of<T>(), LD = NP + 8, RP = raw_pitch<T>(), M = max2(NI, 3);
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
+  constexpr int STAGES = back_stages<T, NP>();
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
   const int ptiles = (d.Ps + kC - 1) / kC;
@@ -862,32 +963,25 @@ __global__ void __launch_bounds__(kChainThreads)
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
   const int row = p0 + strip * 16;
   const bool active = row < d.Ps;
-  const T* const qg = q + b * d.qb + (int64_t)(h / d.rep) * d.N;
-  const T* const kg = k + b * d.kb + (int64_t)(h / d.rep) * d.N;
   const int64_t ys = (int64_t)d.H * d.P;
   const T* const yg = dy + b * (int64_t)d.T * ys + (int64_t)h * d.P + p0;
+  const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * NP;
 
   auto stage = [&](int s) { return smem + s * back_stage<T, NP>(); };
   auto fetch = [&](int c, int s) {
     unsigned char* at = stage(s);
-    const Gates* src = w.gates + bh * d.nc + c;
-    if (threadIdx.x < sizeof(Gates) / 16)
-      cp_async<16>(at + threadIdx.x * 16, reinterpret_cast<const char*>(src) + threadIdx.x * 16);
+    if (threadIdx.x < kGateCopies)
+      cp_async<16>(at + threadIdx.x * 16,
+                   reinterpret_cast<const char*>(w.gates + bh * d.nc + c) + threadIdx.x * 16);
     bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
     bf16* qt = kt + NI * kC * LD;
     T* yt = reinterpret_cast<T*>(qt + NI * kC * LD);
     bf16* xt = reinterpret_cast<bf16*>(yt + kC * RP);
-    const int t0 = c * kC, rv = min(kC, n - t0);
-    if constexpr (ASYNC) {
-      copy_tile<NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N);
-      copy_tile<NP, LD, kChainThreads>(qt, qg + t0 * d.qs, d.qs, rv, d.N);
-      copy_tile<kC, kTP, kChainThreads>(yt, yg + t0 * ys, ys, rv, d.P - p0);
-    } else {
-      load_tile<T, NP, LD, kChainThreads>(kt, kg + t0 * d.ks, d.ks, rv, d.N, d.vk);
-      load_tile<T, NP, LD, kChainThreads>(qt, qg + t0 * d.qs, d.qs, rv, d.N, d.vq);
-      load_raw<T, kChainThreads>(yt, yg + t0 * ys, ys, rv, d.P - p0, d.vdy);
-    }
-    copy_x<kChainThreads>(xt, w.X + (bh * d.nc + c) * (3 * kC * kC));
+    copy_image<NI * kC, NP, LD, kChainThreads>(kt, w.K + img + (int64_t)c * NI * kC * NP);
+    copy_image<NI * kC, NP, LD, kChainThreads>(qt, w.Q + img + (int64_t)c * NI * kC * NP);
+    fetch_raw<T, kChainThreads>(yt, yg + (int64_t)c * kC * ys, ys, min(kC, n - c * kC), d.P - p0,
+                                d.vdy);
+    copy_image<2 * kC, kC, kTP, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kC));
     cp_commit();
   };
 
@@ -895,18 +989,13 @@ __global__ void __launch_bounds__(kChainThreads)
   load_state<NP>(S, dfinal && active ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N,
                  lane);
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-  if (ASYNC && nc > 0) fetch(nc - 1, 0);
+  if (nc > 0) fetch(nc - 1, 0);
   for (int c = nc - 1; c >= 0; --c) {
-    const int s = ASYNC ? (nc - 1 - c) & 1 : 0;
-    if constexpr (ASYNC) {
-      if (c > 0) {
-        fetch(c - 1, s ^ 1);
-        cp_wait<1>();
-      } else {
-        cp_wait<0>();
-      }
+    const int s = STAGES == 2 ? (nc - 1 - c) & 1 : 0;
+    if (STAGES == 2 && c > 0) {
+      fetch(c - 1, s ^ 1);
+      cp_wait<1>();
     } else {
-      fetch(c, 0);
       cp_wait<0>();
     }
     __syncthreads();
@@ -917,8 +1006,11 @@ __global__ void __launch_bounds__(kChainThreads)
       const T* yt = reinterpret_cast<const T*>(qt + NI * kC * LD);
       const bf16* xt = reinterpret_cast<const bf16*>(yt + kC * RP);
       const int64_t at = bh * d.nc + c;
-      store_strip<NP / 8>(w.dS + (at * d.Ps + row) * NP, S, lane);
       const float* ep = w.E + (at * d.Ps + row + g8) * kC + t2;
+      float m0, m1;
+      row_max<NP / 8>(S, m0, m1);
+      const Scale s0 = scale_of(m0), s1 = scale_of(m1);
+      const float least0 = m0 * 5.9604644775390625e-8f, least1 = m1 * 5.9604644775390625e-8f;  // 2^-24
       float r[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -926,21 +1018,22 @@ __global__ void __launch_bounds__(kChainThreads)
         for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < NP / 16; ++kk) {
-        uint32_t a[3][4];
-        a_from_acc<3>(a, S, kk);
+        uint32_t a[2][4];
+        a_from_acc_h(a, S, kk, s0.s, s1.s);
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          mma_planes<3, NI, M>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          mma_planes_h<NI>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
             b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
           });
       }
+      store_strip<NP / 8>(w.dS + (at * d.Ps + row) * NP, S, lane);
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = decay_between(g, kC - 1, 8 * t + t2 + e);
-          r[t][e] *= f;
-          r[t][2 + e] *= f;
+        for (int f = 0; f < 2; ++f) {
+          const float fu = g.fu[8 * t + t2 + f];
+          r[t][f] *= fu * s0.inv;
+          r[t][2 + f] *= fu * s1.inv;
         }
       store_strip<8>(w.Zd + (at * d.Ps + row) * kC, r, lane);
 #pragma unroll
@@ -949,6 +1042,8 @@ __global__ void __launch_bounds__(kChainThreads)
         const float2 e1 = *reinterpret_cast<const float2*>(ep + 8 * kC + 8 * t);
         r[t][0] += e0.x, r[t][1] += e0.y, r[t][2] += e1.x, r[t][3] += e1.y;
       }
+      row_max<8>(r, m0, m1);
+      const Scale q0 = scale_of(m0), q1 = scale_of(m1);
       float u[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -956,48 +1051,66 @@ __global__ void __launch_bounds__(kChainThreads)
         for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
-        uint32_t a[3][4];
-        a_from_acc<3>(a, r, kb);
+        uint32_t a[2][4];
+        a_from_acc_h(a, r, kb, q0.s, q1.s);
 #pragma unroll
         for (int np = 0; np <= kb; ++np)
-          mma_planes<3, 3, 3>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+          mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
           });
       }
-      store_strip<8>(w.dR + (at * d.Ps + row) * kC, u, lane);
-      // r = scale e^G dY^T, u = -b e^G dR^T
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 8 * t + t2 + (e & 1), p = strip * 16 + g8 + (e >> 1) * 8;
-          const float f = ex2(g.gh[i]);
-          r[t][e] = d.scale * f * to_f(yt[i * RP + p]);
-          u[t][e] *= -g.b[i] * f;
+        for (int f = 0; f < 2; ++f) {
+          const float fx = g.fx[8 * t + t2 + f];
+          u[t][f] *= fx * q0.inv;
+          u[t][2 + f] *= fx * q1.inv;
         }
-      const float end = ex2(g.gh[kC - 1]);
+      store_strip<8>(w.dR + (at * d.Ps + row) * kC, u, lane);
+      // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
 #pragma unroll
-      for (int t = 0; t < NP / 8; ++t)
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[t][e] *= end;
+        for (int f = 0; f < 2; ++f) {
+          const int i = 8 * t + t2 + f;
+          const float fq = g.fq[i], fz = -g.fz[i];
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            r[t][2 * o + f] = fq * to_f(yt[i * RP + strip * 16 + g8 + o * 8]);
+            u[t][2 * o + f] *= fz;
+          }
+        }
+      float n0, n1;
+      row_max<8>(r, m0, m1);
+      row_max<8>(u, n0, n1);
+      const Scale u0 = scale_of(fmaxf(fmaxf(m0, n0), least0)),
+                  u1 = scale_of(fmaxf(fmaxf(m1, n1), least1));
+      const float end = ex2(g.gh[kC - 1]), d0 = end * u0.s, d1 = end * u1.s;
+#pragma unroll
+      for (int t = 0; t < NP / 8; ++t) S[t][0] *= d0, S[t][1] *= d0, S[t][2] *= d1, S[t][3] *= d1;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[3][4];
-        a_from_acc<3>(a, u, kb);
+        uint32_t a[2][4];
+        a_from_acc_h(a, u, kb, u0.s, u1.s);
 #pragma unroll
         for (int np = 0; np < NP / 16; ++np)
-          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
             b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
           });
-        a_from_acc<3>(a, r, kb);
+        a_from_acc_h(a, r, kb, u0.s, u1.s);
 #pragma unroll
         for (int np = 0; np < NP / 16; ++np)
-          mma_planes<3, NI, M>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
             b_cols<LD>(x, qt + j * kC * LD, np * 16, kb * 16, lane);
           });
       }
+#pragma unroll
+      for (int t = 0; t < NP / 8; ++t)
+        S[t][0] *= u0.inv, S[t][1] *= u0.inv, S[t][2] *= u1.inv, S[t][3] *= u1.inv;
     }
     __syncthreads();
+    if (STAGES == 1 && c > 0) fetch(c - 1, 0);
   }
   if (dinit && active) store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
 }
@@ -1126,7 +1239,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       fetch_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
                                            d.vdy);
       cp_commit();
-      if (p0 == 0 && tid < sizeof(Gates) / 16)
+      if (p0 == 0 && tid < kGateCopies)
         reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + at)[tid];
       ws.template store<3>(st);
       wr.template store<3>(rt);
@@ -1514,6 +1627,7 @@ int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   d->nc = (d->T + kC - 1) / kC;
   d->Ps = (d->P + 15) / 16 * 16;
   d->NP = d->N <= 64 ? 64 : 128;
+  d->ip = s->in_dtype == SSD_BF16 ? 1 : 2;
   d->scale = s->scale;
   // a block for each (batch, head, chunk), or 64 value rows of a (batch, head)
   const int64_t bh = (int64_t)d->B * d->H;
@@ -1540,10 +1654,13 @@ DeltaWs delta_ws(const DeltaDims& d, void* base, bool bwd) {
   };
   const size_t n = (size_t)d.B * d.H * d.nc, tok = n * d.Ps * kC * 4, st = n * d.Ps * d.NP * 4;
   w.gates = static_cast<Gates*>(take(n * sizeof(Gates)));
-  w.X = static_cast<bf16*>(take(n * 3 * kC * kC * 2));
+  w.X = static_cast<bf16*>(take(n * 2 * kC * kC * 2));
+  const size_t image = (size_t)d.B * d.G * d.nc * d.ip * kC * d.NP * 2;
+  w.K = static_cast<bf16*>(take(image));
   w.U = static_cast<float*>(take(tok));
   w.S0 = static_cast<float*>(take(st));
   if (bwd) {
+    w.Q = static_cast<bf16*>(take(image));
     w.Zb = static_cast<float*>(take(tok));
     w.E = static_cast<float*>(take(tok));
     w.Zd = static_cast<float*>(take(tok));
@@ -1589,12 +1706,6 @@ bool allow_smem(K kern, size_t bytes) {
     if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;                  \
   } while (0)
 
-// Whether the chains can copy a raw tile asynchronously.
-template <typename T>
-bool async_ok(const DeltaDims& d, bool bwd) {
-  return sizeof(T) == 2 && d.vk && (bwd ? d.vq && d.vdy : d.vv);
-}
-
 template <typename T, int NP, bool BWD>
 int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const DeltaWs& w,
                  float* final_states, cudaStream_t s) {
@@ -1605,17 +1716,9 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
   DELTA_LAUNCH("k_delta_prep", prep, n, kPrepThreads, (PrepSmem<T, NP, BWD>::total), d, q, k,
                static_cast<const T*>(in.dt), in.dt_bias, in.A, static_cast<const T*>(in.beta),
                static_cast<const T*>(dy), in.lengths, w);
-  if constexpr (sizeof(T) == 2) {
-    if (async_ok<T>(d, false)) {
-      const auto chain = k_delta_chain<T, NP, true, BWD>;
-      DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP, true>()), d, k, v,
-                   in.init, in.lengths, w, final_states);
-      return SSD_OK;
-    }
-  }
-  const auto chain = k_delta_chain<T, NP, false, BWD>;
-  DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP, false>()), d, k, v,
-               in.init, in.lengths, w, final_states);
+  const auto chain = k_delta_chain<T, NP, BWD>;
+  DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,
+               in.lengths, w, final_states);
   return SSD_OK;
 }
 
@@ -1639,20 +1742,9 @@ int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, c
   const T *q = static_cast<const T*>(in.q), *k = static_cast<const T*>(in.k),
           *dy = static_cast<const T*>(g.dy);
   const int64_t chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
-  bool done = false;
-  if constexpr (sizeof(T) == 2) {
-    if (async_ok<T>(d, true)) {
-      const auto back = k_delta_back<T, NP, true>;
-      DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP, true>()), d, q, k, dy,
-                   g.dfinal, in.lengths, w, g.dinit);
-      done = true;
-    }
-  }
-  if (!done) {
-    const auto back = k_delta_back<T, NP, false>;
-    DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP, false>()), d, q, k, dy,
-                 g.dfinal, in.lengths, w, g.dinit);
-  }
+  const auto back = k_delta_back<T, NP>;
+  DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP>()), d, dy, g.dfinal,
+               in.lengths, w, g.dinit);
   const auto grad = k_delta_grad<T, TO, NP>;
   TO *dq = static_cast<TO*>(g.dq), *dk = static_cast<TO*>(g.dk);
   DELTA_LAUNCH("k_delta_grad", grad, (int64_t)d.B * d.G * d.nb * d.nc, kGradThreads,

@@ -1,5 +1,5 @@
-// Warp-level matrix pieces of the gated delta rule's chunk kernels: bf16 products
-// with fp32 accumulators (m16n8k16) whose operands are sums of bf16 planes.
+// Warp-level matrix pieces of the gated delta rule's chunk kernels: 16-bit products
+// with fp32 accumulators (m16n8k16) whose operands are sums of 16-bit planes.
 //
 // An fp32 value v is the sum of the planes rn(v), rn(v - p0), rn(v - p0 - p1): 8
 // significant bits each, so three planes hold v exactly up to 2^-25 of it.  A
@@ -9,11 +9,16 @@
 // registers: an accumulator tile of 16 rows is, column block by column block, the
 // left operand of the next product.
 //
-// Operand tiles in shared memory are rows of bf16 with a pitch of an odd number of 16
+// Where rows can be scaled by a power of two first, two planes of fp16 do what three of
+// bf16 do: rn(v) and rn(v - p0) leave 2^-23 of the row's largest value, and a product
+// of two such values takes three instructions (the lower planes' product is below).
+//
+// Operand tiles in shared memory are rows of 16-bit values with a pitch of an odd number of 16
 // bytes, which ldmatrix reads without bank conflicts.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace ssd {
@@ -40,6 +45,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -108,6 +122,74 @@ __device__ __forceinline__ void mma_planes(float (&c0)[4], float (&c1)[4], const
       if (i + j < M) {
         mma16816(c0, a[i], b[0], b[1]);
         mma16816(c1, a[i], b[2], b[3]);
+      }
+  }
+}
+
+// ----------------------------------------------------------- fp16, rows scaled
+
+// Power of two that brings the largest value m of a row to [1, 2), and its inverse; 1
+// for a row of zeros.
+struct Scale {
+  float s, inv;
+};
+__device__ __forceinline__ Scale scale_of(float m) {
+  const int e = min((int)(__float_as_uint(m) >> 23), 253);
+  Scale r;
+  r.s = __uint_as_float((uint32_t)(e > 0 ? 254 - e : 127) << 23);
+  r.inv = __uint_as_float((uint32_t)(e > 0 ? e : 127) << 23);
+  return r;
+}
+// The planes of a pair of values times f.
+__device__ __forceinline__ void split2h(float a, float b, float f, uint32_t (&p)[2]) {
+  const float2 v = __fmul2_rn(make_float2(a, b), make_float2(f, f));
+  const __half2 h = __float22half2_rn(v);
+  const __half2 l = __float22half2_rn(__ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), v));
+  p[0] = *reinterpret_cast<const uint32_t*>(&h);
+  p[1] = *reinterpret_cast<const uint32_t*>(&l);
+}
+// Left operand of column block kb of an accumulator strip whose rows (lane / 4, + 8)
+// are scaled by f0 and f1.
+template <int NT>
+__device__ __forceinline__ void a_from_acc_h(uint32_t (&a)[2][4], const float (&c)[NT][4], int kb,
+                                             float f0, float f1) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t p[2];
+    const float(&t)[4] = c[2 * kb + (q >> 1)];
+    split2h(t[(q & 1) * 2], t[(q & 1) * 2 + 1], q & 1 ? f1 : f0, p);
+    a[0][q] = p[0], a[1][q] = p[1];
+  }
+}
+// Largest magnitudes of the strip's rows lane / 4 and lane / 4 + 8.
+template <int NT>
+__device__ __forceinline__ void row_max(const float (&c)[NT][4], float& m0, float& m1) {
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    a[t & 1] = fmaxf(a[t & 1], fmaxf(fabsf(c[t][0]), fabsf(c[t][1])));
+    a[2 + (t & 1)] = fmaxf(a[2 + (t & 1)], fmaxf(fabsf(c[t][2]), fabsf(c[t][3])));
+  }
+  m0 = fmaxf(a[0], a[1]), m1 = fmaxf(a[2], a[3]);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+}
+// c0, c1 += A B over planes: A of two, B of NB.
+template <int NB, typename Load>
+__device__ __forceinline__ void mma_planes_h(float (&c0)[4], float (&c1)[4],
+                                             const uint32_t (&a)[2][4], Load&& load) {
+#pragma unroll
+  for (int j = NB - 1; j >= 0; --j) {
+    uint32_t b[4];
+    load(j, b);
+#pragma unroll
+    for (int i = 1; i >= 0; --i)
+      if (i + j < 2) {
+        mma16816h(c0, a[i], b[0], b[1]);
+        mma16816h(c1, a[i], b[2], b[3]);
       }
   }
 }
