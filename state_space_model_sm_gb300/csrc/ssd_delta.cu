@@ -19,6 +19,8 @@
 // a chunk takes nothing from the differences behind it.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "layer_math.cuh"
 #include "ssd_internal.h"
 #include "warp_mma.cuh"
@@ -67,8 +69,8 @@ constexpr int kGateCopies = sizeof(Gates) / 16;
 
 struct DeltaWs {
   Gates* gates;  // (B, H, nc)
-  bf16* X;       // (B, H, nc, 2, 64, 64) fp16 planes of the transpose of (I + M)^-1
-  bf16* K;       // (B, G, nc, planes, 64, NP) fp16 planes of the keys, rows scaled
+  bf16* X;       // (B, H, nc, 2, 64, 72) fp16 planes of the transpose of (I + M)^-1
+  bf16* K;       // (B, G, nc, planes, 64, NP + 8) fp16 planes of the keys, rows scaled
   bf16* Q;       // the same of the queries (backward)
   float* U;      // (B, H, nc, Ps, 64)  transposed: [p][token]
   float* S0;     // (B, H, nc, Ps, NP)  the state in front of each chunk
@@ -141,23 +143,34 @@ __device__ __forceinline__ void load_tile(bf16* dst, const T* src, int64_t ld, i
   }
 }
 
-// 64 rows of W fp32 values of the workspace (rows from rv on: zeros), first into
-// registers, all loads in flight, then as NPL planes into a tile.
+// fp32 matrices of the workspace (S0, dS: value rows x key columns; U, Zb, E, Zd, dR:
+// value rows x tokens) are held as the accumulators that write them: 16 rows by 8 columns
+// after one another, a float4 for each lane, with the lane's two columns of row lane / 4
+// and of the row 8 below.  A warp's store or load is then 512 bytes in a row.
+__device__ __forceinline__ float4* frag(float* m, int64_t strip, int tiles, int lane) {
+  return reinterpret_cast<float4*>(m) + strip * tiles * 32 + lane;
+}
+__device__ __forceinline__ float4 as4(const float (&c)[4]) {
+  return make_float4(c[0], c[1], c[2], c[3]);
+}
+
+// 64 value rows (4 strips; zeros from rv rows on) of W columns of the workspace, first
+// into registers, all loads in flight, then as NPL planes into a tile of rows.
 template <int W, int LD, int THREADS>
 struct WsTile {
-  static constexpr int kN = kC * (W / 4) / THREADS;
+  static constexpr int kN = kC * (W / 4) / THREADS, kT = W / 8;
   float4 v[kN];
+  // the first row and column of this thread's n-th float4
   __device__ __forceinline__ static void at(int n, int* r, int* c) {
-    const int i = threadIdx.x + n * THREADS;
-    *r = i / (W / 4), *c = i % (W / 4) * 4;
+    const int i = threadIdx.x + n * THREADS, lane = i & 31;
+    *r = i / (32 * kT) * 16 + (lane >> 2), *c = (i >> 5) % kT * 8 + (lane & 3) * 2;
   }
   __device__ __forceinline__ void load(const float* src, int rv) {
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      int r, c;
-      at(n, &r, &c);
-      v[n] = r < rv ? *reinterpret_cast<const float4*>(src + r * W + c)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int i = threadIdx.x + n * THREADS;
+      v[n] = i / (32 * kT) * 16 < rv ? reinterpret_cast<const float4*>(src)[i]
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   template <int NPL>
@@ -170,8 +183,10 @@ struct WsTile {
       split2<NPL>(v[n].x, v[n].y, a);
       split2<NPL>(v[n].z, v[n].w, b);
 #pragma unroll
-      for (int k = 0; k < NPL; ++k)
-        *reinterpret_cast<uint2*>(dst + k * kC * LD + r * LD + c) = make_uint2(a[k], b[k]);
+      for (int k = 0; k < NPL; ++k) {
+        *reinterpret_cast<uint32_t*>(dst + k * kC * LD + r * LD + c) = a[k];
+        *reinterpret_cast<uint32_t*>(dst + k * kC * LD + (r + 8) * LD + c) = b[k];
+      }
     }
   }
 };
@@ -200,12 +215,15 @@ __device__ __forceinline__ void fetch_tile(bf16* dst, const T* src, int64_t ld, 
   }
   load_tile<T, W, LD, THREADS>(dst, src, ld, rv, cv, vec);
 }
-// ROWS dense rows of W 16-bit values of the workspace, started asynchronously.
-template <int ROWS, int W, int LD, int THREADS>
-__device__ __forceinline__ void copy_image(bf16* dst, const bf16* src) {
+// BYTES of the workspace to shared memory, started asynchronously; images lie there with
+// the pitch of the tiles.
+template <int BYTES, int THREADS>
+__device__ __forceinline__ void copy_image(void* dst, const void* src) {
+  const int o = threadIdx.x * 16;
 #pragma unroll
-  for (int i = threadIdx.x; i < ROWS * (W / 8); i += THREADS)
-    cp_async<16>(dst + i / (W / 8) * LD + i % (W / 8) * 8, src + i * 8);
+  for (int i = 0; i < BYTES; i += THREADS * 16)
+    if (i + THREADS * 16 <= BYTES || i + o < BYTES)
+      cp_async<16>(static_cast<char*>(dst) + o + i, static_cast<const char*>(src) + o + i);
 }
 // Planes of an input's fp16 image.
 template <typename T>
@@ -323,7 +341,7 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
       for (int j = 0; j < 4; ++j) split2h(f[2 * j], f[2 * j + 1], s.s, p[j]);
 #pragma unroll
       for (int l = 0; l < NIMG; ++l)
-        *reinterpret_cast<uint4*>(to + l * kC * NP + r * NP + c0 + c) =
+        *reinterpret_cast<uint4*>(to + l * kC * LD + r * LD + c0 + c) =
             make_uint4(p[0][l], p[1][l], p[2][l], p[3][l]);
     }
   }
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
 
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
   const bool first = pl.h % d.rep == 0;  // writes the images of its group
-  const int64_t img = (((int64_t)pl.b * d.G + grp) * d.nc + pl.c) * NIMG * kC * NP;
+  const int64_t img = (((int64_t)pl.b * d.G + grp) * d.nc + pl.c) * NIMG * kC * LD;
   const float ki = row_image<NI, NIMG, NP>(Kt, first ? w.K + img : nullptr);
   float qi = 0.f;
   if constexpr (BWD) qi = row_image<NI, NIMG, NP>(Qt, first ? w.Q + img : nullptr);
@@ -508,7 +526,7 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
     row_max<8>(reinterpret_cast<const float(&)[8][4]>(x), m0, m1);
     const Scale s0 = scale_of(m0), s1 = scale_of(m1);
     if ((lane & 3) == 0) g.fx[r0] = s0.inv, g.fx[r0 + 8] = s1.inv;
-    bf16* const xp = w.X + pl.i * (2 * kC * kC);
+    bf16* const xp = w.X + pl.i * (2 * kC * kTP);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -519,7 +537,7 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
           split2h(x[i][t][2 * e], x[i][t][2 * e + 1], e ? s1.s : s0.s, p);
 #pragma unroll
           for (int l = 0; l < 2; ++l)
-            *reinterpret_cast<uint32_t*>(xp + l * kC * kC + (r0 + 8 * e) * kC + i * 16 + 8 * t + c0) =
+            *reinterpret_cast<uint32_t*>(xp + l * kC * kTP + (r0 + 8 * e) * kTP + i * 16 + 8 * t + c0) =
                 p[l];
         }
   }
@@ -569,12 +587,9 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
               b_cols<kTP>(r, at + j * kC * kTP, np * 16, kb * 16, lane);
             });
         }
-        float* to = w.E + (pl.i * d.Ps + p0 + r0) * kC + c0;
+        float4* to = frag(w.E, (pl.i * d.Ps + p0) / 16 + strip, 8, lane);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          *reinterpret_cast<float2*>(to + 8 * t) = make_float2(e[t][0], e[t][1]);
-          *reinterpret_cast<float2*>(to + 8 * kC + 8 * t) = make_float2(e[t][2], e[t][3]);
-        }
+        for (int t = 0; t < 8; ++t) to[t * 32] = as4(e[t]);
       }
       __syncthreads();
     }
@@ -583,23 +598,21 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
 
 // --------------------------------------------------------------------- chain
 
-constexpr int kChainThreads = 128;
+constexpr int kChainThreads = 256;
 
 template <typename T, int NP>
 constexpr size_t chain_stage() {
   return sizeof(Gates) + (size_t)image_planes<T>() * kC * (NP + 8) * 2 +
          (size_t)kC * raw_pitch<T>() * sizeof(T) + (size_t)2 * kC * kTP * 2;
 }
-template <typename T, int NP>
-constexpr size_t chain_smem() { return 2 * chain_stage<T, NP>(); }
-
-// A state strip (16 rows of a warp, NP columns) from or to rows of N floats.
+// Half of a state strip (16 rows, NP / 2 columns from half * NP / 2 on) from or to rows of
+// N floats.
 template <int NP>
-__device__ __forceinline__ void load_state(float (&S)[NP / 8][4], const float* src, int rows, int N,
-                                           int lane) {
-  const int r = lane >> 2, c = (lane & 3) * 2;
+__device__ __forceinline__ void load_state(float (&S)[NP / 16][4], const float* src, int rows, int N,
+                                           int half, int lane) {
+  const int r = lane >> 2, c = half * (NP / 2) + (lane & 3) * 2;
 #pragma unroll
-  for (int t = 0; t < NP / 8; ++t)
+  for (int t = 0; t < NP / 16; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
@@ -607,44 +620,158 @@ __device__ __forceinline__ void load_state(float (&S)[NP / 8][4], const float* s
     }
 }
 template <int NP>
-__device__ __forceinline__ void store_state(float* dst, const float (&S)[NP / 8][4], int rows, int N,
-                                            int lane) {
-  const int r = lane >> 2, c = (lane & 3) * 2;
+__device__ __forceinline__ void store_state(float* dst, const float (&S)[NP / 16][4], int rows, int N,
+                                            int half, int lane) {
+  const int r = lane >> 2, c = half * (NP / 2) + (lane & 3) * 2;
 #pragma unroll
-  for (int t = 0; t < NP / 8; ++t)
+  for (int t = 0; t < NP / 16; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
       if (i < rows && j < N) dst[(int64_t)i * N + j] = S[t][e];
     }
 }
-// A strip of NT tiles to rows of 8 NT floats of the workspace.
-template <int NT>
-__device__ __forceinline__ void store_strip(float* dst, const float (&S)[NT][4], int lane) {
-  float* p = dst + (lane >> 2) * (8 * NT) + (lane & 3) * 2;
+// The same to the workspace.
+template <int NP>
+__device__ __forceinline__ void store_state_ws(float* m, int64_t strip, const float (&S)[NP / 16][4],
+                                               int half, int lane) {
+  float4* p = frag(m, strip, NP / 8, lane) + half * (NP / 16) * 32;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    *reinterpret_cast<float2*>(p + 8 * t) = make_float2(S[t][0], S[t][1]);
-    *reinterpret_cast<float2*>(p + 64 * NT + 8 * t) = make_float2(S[t][2], S[t][3]);
-  }
+  for (int t = 0; t < NP / 16; ++t) p[t * 32] = as4(S[t]);
 }
 
-// The chain over a head's chunks: 64 value rows a block, a strip of 16 rows a warp with
-// its state in registers (16 x NP fp32, an accumulator).  A chunk is three products,
+// Barrier of the two warps of a strip.
+__device__ __forceinline__ void pair_sync(int strip) {
+  asm volatile("bar.sync %0, 64;" ::"r"(strip + 1) : "memory");
+}
+// A box read by one warp of the pair (emptied) before the other fills it again (refill).
+__device__ __forceinline__ void emptied(int strip) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(strip + 5) : "memory");
+}
+__device__ __forceinline__ void refill(int strip) {
+  asm volatile("bar.sync %0, 64;" ::"r"(strip + 5) : "memory");
+}
+// Four tiles of a strip to and from the other warp of the pair, lane by lane.
+__device__ __forceinline__ void give(float4* box, const float (&c)[8][4], int t0, int lane) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    box[t * 32 + lane] = make_float4(c[t0 + t][0], c[t0 + t][1], c[t0 + t][2], c[t0 + t][3]);
+}
+__device__ __forceinline__ void take_add(const float4* box, float (&c)[8][4], int t0, int lane) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float4 v = box[t * 32 + lane];
+    c[t0 + t][0] += v.x, c[t0 + t][1] += v.y, c[t0 + t][2] += v.z, c[t0 + t][3] += v.w;
+  }
+}
+__device__ __forceinline__ void take(const float4* box, float (&c)[8][4], int t0, int lane) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float4 v = box[t * 32 + lane];
+    c[t0 + t][0] = v.x, c[t0 + t][1] = v.y, c[t0 + t][2] = v.z, c[t0 + t][3] = v.w;
+  }
+}
+constexpr int kBox = 4 * 32;                  // float4s of one exchange
+constexpr size_t kBoxes = 4 * 2 * kBox * 16;  // two for each strip
+// Largest magnitudes of four tiles' rows.
+__device__ __forceinline__ void half_max(const float (&c)[8][4], int t0, float& m0, float& m1) {
+  m0 = m1 = 0.f;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    m0 = fmaxf(fmaxf(m0, fabsf(c[t0 + t][0])), fabsf(c[t0 + t][1]));
+    m1 = fmaxf(fmaxf(m1, fabsf(c[t0 + t][2])), fabsf(c[t0 + t][3]));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+}
+// A strip's rows times f0 and f1.
+template <int NT>
+__device__ __forceinline__ void scale_rows(float (&c)[NT][4], float f0, float f1) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float2 a = __fmul2_rn(make_float2(c[t][0], c[t][1]), make_float2(f0, f0));
+    const float2 b = __fmul2_rn(make_float2(c[t][2], c[t][3]), make_float2(f1, f1));
+    c[t][0] = a.x, c[t][1] = a.y, c[t][2] = b.x, c[t][3] = b.y;
+  }
+}
+// Four tiles (32 tokens, from tile t0 on) of a strip to the workspace.
+__device__ __forceinline__ void store_half(float* m, int64_t strip, const float (&c)[8][4], int t0,
+                                           int lane) {
+  float4* p = frag(m, strip, 8, lane);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) p[(t0 + t) * 32] = as4(c[t0 + t]);
+}
+template <int NT>
+__device__ __forceinline__ void clear(float (&c)[NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[t][e] = 0.f;
+}
+// Z^T += S K^T over the warp's key columns; rows of S scaled.
+template <int NI, int NP>
+__device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (&S)[NP / 16][4],
+                                                 const bf16* kt, int half, Scale s0, Scale s1,
+                                                 int lane) {
+  constexpr int LD = NP + 8;
+  clear(z);
+#pragma unroll
+  for (int kk = 0; kk < NP / 32; ++kk) {
+    uint32_t a[2][4];
+    a_from_acc_h(a, S, kk, s0.s, s1.s);
+#pragma unroll
+    for (int np = 0; np < 4; ++np)
+      mma_planes_h<NI>(z[2 * np], z[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+        b_rows<LD>(x, kt + j * kC * LD, np * 16, half * (NP / 2) + kk * 16, lane);
+      });
+  }
+  scale_rows(z, s0.inv, s1.inv);
+}
+// S += the product of tokens 16 kb0 .. of c (rows scaled) with their rows of the tile.
+template <int NI, int NP, int NB>
+__device__ __forceinline__ void add_outer(float (&S)[NP / 16][4], const float (&c)[8][4], int kb0,
+                                          const bf16* kt, int half, float f0, float f1, int lane) {
+  constexpr int LD = NP + 8;
+#pragma unroll
+  for (int kb = 0; kb < NB; ++kb) {
+    uint32_t a[2][4];
+    a_from_acc_h(a, c, kb0 + kb, f0, f1);
+#pragma unroll
+    for (int np = 0; np < NP / 32; ++np)
+      mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+        b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, (kb0 + kb) * 16, lane);
+      });
+  }
+}
+constexpr float kBelow = 5.9604644775390625e-8f;  // 2^-24
+
+// The chain over a head's chunks: 64 value rows a block, a strip of 16 rows for each pair
+// of warps, whose state is in registers: half the key columns a warp (16 x NP / 2 fp32,
+// an accumulator).  A chunk is three products,
 //     Z^T = S K^T,   U^T = (b (V - e^G Z))^T X^T,   S <- e^G63 S + (e^(G63 - G) U)^T K,
-// each left operand formed from the last accumulator, so the only traffic between them
-// is the shared tiles of K, V and X, copied while the chunk before is at work.
+// each left operand formed from the last accumulator; K, V and X are shared tiles, copied
+// while the chunk before is at work.
 // Left operands are two fp16 planes of rows scaled by their largest value, K is one
-// (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
-// bf16 take 504.  The products are issued by one warp per SM quarter at 8 clocks each,
-// which bounds a chunk by 1.3 us.  KEEP: also writes b e^G Z, for the backward.
+// (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a strip and chunk, where three
+// planes of bf16 take 504.  At 8 clocks each they bound a chunk by 1.3 us.
+// Two warps a strip, on the same SM quarter, so that one's products run under the other's
+// conversions (one warp a strip: 3.4 us a chunk).  Each forms Z over its key columns; they
+// swap halves, so that each has 32 tokens; the first warp's tokens need no others, and
+// what they give to the later ones goes to the second warp with them; the second's go back
+// while the first adds its own to its state.
+// KEEP: also writes b e^G Z, for the backward.
 template <typename T, int NP, bool KEEP>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_chain(DeltaDims d, const T* __restrict__ v, const float* __restrict__ init,
                   const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states) {
-  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>(), NT = NP / 16;
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, strip = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+  float4* const to = reinterpret_cast<float4*>(smem) + (strip * 2 + half) * kBox;
+  float4* const from = reinterpret_cast<float4*>(smem) + (strip * 2 + (half ^ 1)) * kBox;
   const int ptiles = (d.Ps + kC - 1) / kC;
   const int p0 = (int)(blockIdx.x % ptiles) * kC;
   const int64_t bh = blockIdx.x / ptiles;
@@ -653,136 +780,140 @@ __global__ void __launch_bounds__(kChainThreads)
   const int row = p0 + strip * 16;  // this warp's first value row
   const bool active = row < d.Ps;
   const T* const vg = v + b * d.vb + (int64_t)h * d.P + p0;
-  const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * NP;
+  const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
 
-  auto stage = [&](int s) { return smem + s * chain_stage<T, NP>(); };
+  auto stage = [&](int s) { return smem + kBoxes + s * chain_stage<T, NP>(); };
   auto fetch = [&](int c, int s) {
     unsigned char* at = stage(s);
-    if (threadIdx.x < kGateCopies)
-      cp_async<16>(at + threadIdx.x * 16,
-                   reinterpret_cast<const char*>(w.gates + bh * d.nc + c) + threadIdx.x * 16);
+    copy_image<sizeof(Gates), kChainThreads>(at, w.gates + bh * d.nc + c);
     bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
     T* vt = reinterpret_cast<T*>(kt + NI * kC * LD);
     bf16* xt = reinterpret_cast<bf16*>(vt + kC * RP);
-    copy_image<NI * kC, NP, LD, kChainThreads>(kt, kg + (int64_t)c * NI * kC * NP);
+    copy_image<NI * kC * LD * 2, kChainThreads>(kt, kg + (int64_t)c * NI * kC * LD);
     fetch_raw<T, kChainThreads>(vt, vg + (int64_t)c * kC * d.vs, d.vs, min(kC, n - c * kC), d.P - p0,
                                 d.vv);
-    copy_image<2 * kC, kC, kTP, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kC));
+    copy_image<2 * kC * kTP * 2, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kTP));
     cp_commit();
   };
 
-  float S[NP / 8][4];
-  load_state<NP>(S, init && active ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  float S[NT][4];
+  load_state<NP>(S, init && active ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, half,
+                 lane);
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
   if (nc > 0) fetch(0, 0);
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
-    if (c + 1 < nc) {
-      fetch(c + 1, s ^ 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
-    __syncthreads();
+    cp_wait<0>();
+    __syncthreads();  // this chunk's tiles are there, the last one's are read
+    if (c + 1 < nc) fetch(c + 1, s ^ 1);
     if (active) {
       const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
       const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
       const T* vt = reinterpret_cast<const T*>(kt + NI * kC * LD);
       const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
-      const int64_t at = bh * d.nc + c;
-      float m0, m1;
-      row_max<NP / 8>(S, m0, m1);
-      const Scale s0 = scale_of(m0), s1 = scale_of(m1);
-      const float least0 = m0 * 5.9604644775390625e-8f, least1 = m1 * 5.9604644775390625e-8f;  // 2^-24
+      const int64_t at = bh * d.nc + c, srow = (at * d.Ps + row) / 16;
+      float m0, m1, a0, a1;
+      row_max<NT>(S, m0, m1);
       float r[8][4];
+      state_times_keys<NI, NP>(r, S, kt, half, scale_of(m0), scale_of(m1), lane);
+      if (half) give(to, r, 0, lane);
+      else give(to, r, 4, lane);
+      store_state_ws<NP>(w.S0, srow, S, half, lane);
+      pair_sync(strip);
+      // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and the warp's 32 tokens
+      auto correct = [&](auto first) {
+        constexpr int t0 = first();
+        take_add(from, r, t0, lane);
+        if (t0 == 4) emptied(strip);
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < NP / 16; ++kk) {
-        uint32_t a[2][4];
-        a_from_acc_h(a, S, kk, s0.s, s1.s);
-#pragma unroll
-        for (int np = 0; np < 4; ++np)
-          mma_planes_h<NI>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
-          });
-      }
-      store_strip<NP / 8>(w.S0 + (at * d.Ps + row) * NP, S, lane);
-      // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
-      float z[KEEP ? 8 : 1][4];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int i = 8 * t + t2 + f;
-          const float bi = g.b[i], fz = g.fz[i], fx = g.fx[i];
+        for (int t = t0; t < t0 + 4; ++t) {
+          const int i = 8 * t + t2;
+          const float2 bi = *reinterpret_cast<const float2*>(g.b + i);
+          const float2 fz = *reinterpret_cast<const float2*>(g.fz + i);
+          float z0 = 0.f, z1 = 0.f;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
-            const int e = 2 * o + f, p = strip * 16 + g8 + o * 8;
-            const float ze = fz * (o ? s1.inv : s0.inv) * r[t][e];
-            r[t][e] = fx * fmaf(bi, to_f(vt[i * RP + p]), -ze);
-            if constexpr (KEEP) z[t][e] = ze;
+            const int p = strip * 16 + g8 + o * 8;
+            r[t][2 * o] *= fz.x, r[t][2 * o + 1] *= fz.y;
+            if constexpr (KEEP)
+              if (o == 1) frag(w.Zb, srow, 8, lane)[t * 32] = make_float4(z0, z1, r[t][2], r[t][3]);
+            if (o == 0) z0 = r[t][0], z1 = r[t][1];
+            r[t][2 * o] = fmaf(bi.x, to_f(vt[i * RP + p]), -r[t][2 * o]);
+            r[t][2 * o + 1] = fmaf(bi.y, to_f(vt[(i + 1) * RP + p]), -r[t][2 * o + 1]);
           }
+          const float2 fx = *reinterpret_cast<const float2*>(g.fx + i);
+          r[t][0] *= fx.x, r[t][1] *= fx.y, r[t][2] *= fx.x, r[t][3] *= fx.y;
         }
-      if constexpr (KEEP) store_strip<8>(w.Zb + (at * d.Ps + row) * kC, z, lane);
-      row_max<8>(r, m0, m1);
-      const Scale q0 = scale_of(m0), q1 = scale_of(m1);
-      float u[8][4];
+        float x0, x1;
+        half_max(r, t0, x0, x1);
+        const Scale q0 = scale_of(x0), q1 = scale_of(x1);
+        float u[8][4];
+        clear(u);
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+        for (int kb = t0 / 2; kb < t0 / 2 + 2; ++kb) {
+          uint32_t a[2][4];
+          a_from_acc_h(a, r, kb, q0.s, q1.s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[2][4];
-        a_from_acc_h(a, r, kb, q0.s, q1.s);
-#pragma unroll
-        for (int np = kb; np < 4; ++np)
-          mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
-          });
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        u[t][0] *= q0.inv, u[t][1] *= q0.inv, u[t][2] *= q1.inv, u[t][3] *= q1.inv;
-      store_strip<8>(w.U + (at * d.Ps + row) * kC, u, lane);
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const float fu = g.fu[8 * t + t2 + f];
-          u[t][f] *= fu;
-          u[t][2 + f] *= fu;
+          for (int np = kb; np < 4; ++np)
+            mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+              b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+            });
         }
-      // the state takes the products in the scale of U, or of its own where that is
-      // 2^24 larger (what U would lose there is below the state's own rounding)
-      row_max<8>(u, m0, m1);
-      const Scale u0 = scale_of(fmaxf(m0, least0)),
-                  u1 = scale_of(fmaxf(m1, least1));
-      const float end = ex2(g.gh[kC - 1]), d0 = end * u0.s, d1 = end * u1.s;
+        scale_rows(u, q0.inv, q1.inv);
 #pragma unroll
-      for (int t = 0; t < NP / 8; ++t) S[t][0] *= d0, S[t][1] *= d0, S[t][2] *= d1, S[t][3] *= d1;
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[2][4];
-        a_from_acc_h(a, u, kb, u0.s, u1.s);
+          for (int e = 0; e < 4; ++e) r[t][e] = u[t][e];
+      };
+      auto weigh = [&](auto first) {  // tokens' U to the workspace, then times e^(G63 - G) 2^k
+        constexpr int t0 = first();
+        store_half(w.U, srow, r, t0, lane);
 #pragma unroll
-        for (int np = 0; np < NP / 16; ++np)
-          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
-          });
+        for (int t = t0; t < t0 + 4; ++t) {
+          const float2 fu = *reinterpret_cast<const float2*>(g.fu + 8 * t + t2);
+          r[t][0] *= fu.x, r[t][1] *= fu.y, r[t][2] *= fu.x, r[t][3] *= fu.y;
+        }
+      };
+      const std::integral_constant<int, 0> lo;
+      const std::integral_constant<int, 4> hi;
+      if (half == 0) {
+        correct(lo);
+        give(from, r, 4, lane);  // (the box that this warp has emptied)
+        weigh(lo);
+        refill(strip);
+        give(to, r, 0, lane);
+        pair_sync(strip);
+      } else {
+        correct(hi);
+        pair_sync(strip);
+        take_add(to, r, 4, lane);
+        take(from, r, 0, lane);
+        weigh(hi);
       }
-#pragma unroll
-      for (int t = 0; t < NP / 8; ++t)
-        S[t][0] *= u0.inv, S[t][1] *= u0.inv, S[t][2] *= u1.inv, S[t][3] *= u1.inv;
+      // the state takes tokens 0 .. 31, then 32 .. 63, each in the scale of its rows, or in
+      // the state's own where that is 2^24 larger (what is lost there is below its rounding)
+      half_max(r, 0, a0, a1);
+      const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
+      const float end = ex2(g.gh[kC - 1]);
+      scale_rows(S, end * u0.s, end * u1.s);
+      add_outer<NI, NP, 2>(S, r, 0, kt, half, u0.s, u1.s, lane);
+      m0 = fmaxf(m0, a0 * kC), m1 = fmaxf(m1, a1 * kC);  // bounds of the rows by now
+      if (half == 1) give(to, r, 4, lane);
+      pair_sync(strip);
+      if (half == 0) take(from, r, 4, lane);
+      half_max(r, 4, a0, a1);
+      const Scale v0 = scale_of(fmaxf(a0, m0 * kBelow)), v1 = scale_of(fmaxf(a1, m1 * kBelow));
+      scale_rows(S, v0.s * u0.inv, v1.s * u1.inv);
+      add_outer<NI, NP, 2>(S, r, 2, kt, half, v0.s, v1.s, lane);
+      scale_rows(S, v0.inv, v1.inv);
     }
-    __syncthreads();
   }
   if (final_states && active)
-    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, half, lane);
 }
+
+template <typename T, int NP>
+constexpr size_t chain_smem() { return kBoxes + 2 * chain_stage<T, NP>(); }
 
 // ----------------------------------------------------------------------- out
 
@@ -937,25 +1068,28 @@ template <typename T, int NP>
 constexpr size_t back_stage() {
   return chain_stage<T, NP>() + (size_t)image_planes<T>() * kC * (NP + 8) * 2;
 }
-// (three stages of fp32 inputs' size would not fit; one holds the chunk at work)
+// (two stages of fp32 inputs' size do not fit)
 template <typename T, int NP>
-constexpr int back_stages() { return 2 * back_stage<T, NP>() <= 220 * 1024 ? 2 : 1; }
+constexpr int back_stages() { return kBoxes + 2 * back_stage<T, NP>() <= 220 * 1024 ? 2 : 1; }
 template <typename T, int NP>
-constexpr size_t back_smem() { return back_stages<T, NP>() * back_stage<T, NP>(); }
+constexpr size_t back_smem() { return kBoxes + back_stages<T, NP>() * back_stage<T, NP>(); }
 
 // The chain of the backward, from the last chunk to the first, with the gradient of the
 // state behind the chunk in registers:
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
 //     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
-// in the manner of k_delta_chain: 444 products a chunk.
+// in the manner of k_delta_chain, 444 products a chunk.  Here the later 32 tokens need no
+// others: they are first.
 template <typename T, int NP>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit) {
-  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>(), NT = NP / 16;
   constexpr int STAGES = back_stages<T, NP>();
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, strip = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+  float4* const to = reinterpret_cast<float4*>(smem) + (strip * 2 + half) * kBox;
+  float4* const from = reinterpret_cast<float4*>(smem) + (strip * 2 + (half ^ 1)) * kBox;
   const int ptiles = (d.Ps + kC - 1) / kC;
   const int p0 = (int)(blockIdx.x % ptiles) * kC;
   const int64_t bh = blockIdx.x / ptiles;
@@ -965,154 +1099,149 @@ __global__ void __launch_bounds__(kChainThreads)
   const bool active = row < d.Ps;
   const int64_t ys = (int64_t)d.H * d.P;
   const T* const yg = dy + b * (int64_t)d.T * ys + (int64_t)h * d.P + p0;
-  const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * NP;
+  const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
 
-  auto stage = [&](int s) { return smem + s * back_stage<T, NP>(); };
+  auto stage = [&](int s) { return smem + kBoxes + s * back_stage<T, NP>(); };
   auto fetch = [&](int c, int s) {
     unsigned char* at = stage(s);
-    if (threadIdx.x < kGateCopies)
-      cp_async<16>(at + threadIdx.x * 16,
-                   reinterpret_cast<const char*>(w.gates + bh * d.nc + c) + threadIdx.x * 16);
+    copy_image<sizeof(Gates), kChainThreads>(at, w.gates + bh * d.nc + c);
     bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
     bf16* qt = kt + NI * kC * LD;
     T* yt = reinterpret_cast<T*>(qt + NI * kC * LD);
     bf16* xt = reinterpret_cast<bf16*>(yt + kC * RP);
-    copy_image<NI * kC, NP, LD, kChainThreads>(kt, w.K + img + (int64_t)c * NI * kC * NP);
-    copy_image<NI * kC, NP, LD, kChainThreads>(qt, w.Q + img + (int64_t)c * NI * kC * NP);
+    copy_image<NI * kC * LD * 2, kChainThreads>(kt, w.K + img + (int64_t)c * NI * kC * LD);
+    copy_image<NI * kC * LD * 2, kChainThreads>(qt, w.Q + img + (int64_t)c * NI * kC * LD);
     fetch_raw<T, kChainThreads>(yt, yg + (int64_t)c * kC * ys, ys, min(kC, n - c * kC), d.P - p0,
                                 d.vdy);
-    copy_image<2 * kC, kC, kTP, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kC));
+    copy_image<2 * kC * kTP * 2, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kTP));
     cp_commit();
   };
 
-  float S[NP / 8][4];
+  float S[NT][4];
   load_state<NP>(S, dfinal && active ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N,
-                 lane);
+                 half, lane);
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
   if (nc > 0) fetch(nc - 1, 0);
   for (int c = nc - 1; c >= 0; --c) {
     const int s = STAGES == 2 ? (nc - 1 - c) & 1 : 0;
-    if (STAGES == 2 && c > 0) {
-      fetch(c - 1, s ^ 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
-    __syncthreads();
+    cp_wait<0>();
+    __syncthreads();  // this chunk's tiles are there, the last one's are read
+    if (STAGES == 2 && c > 0) fetch(c - 1, s ^ 1);
     if (active) {
       const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
       const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
       const bf16* qt = kt + NI * kC * LD;
       const T* yt = reinterpret_cast<const T*>(qt + NI * kC * LD);
       const bf16* xt = reinterpret_cast<const bf16*>(yt + kC * RP);
-      const int64_t at = bh * d.nc + c;
-      const float* ep = w.E + (at * d.Ps + row + g8) * kC + t2;
-      float m0, m1;
-      row_max<NP / 8>(S, m0, m1);
-      const Scale s0 = scale_of(m0), s1 = scale_of(m1);
-      const float least0 = m0 * 5.9604644775390625e-8f, least1 = m1 * 5.9604644775390625e-8f;  // 2^-24
+      const int64_t at = bh * d.nc + c, srow = (at * d.Ps + row) / 16;
+      float m0, m1, a0, a1;
+      row_max<NT>(S, m0, m1);
+      // the warp's tokens of E, on their way under the products
+      float4 ev[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ev[t] = frag(w.E, srow, 8, lane)[(half * 4 + t) * 32];
       float r[8][4];
+      state_times_keys<NI, NP>(r, S, kt, half, scale_of(m0), scale_of(m1), lane);
+      if (half) give(to, r, 0, lane);
+      else give(to, r, 4, lane);
+      store_state_ws<NP>(w.dS, srow, S, half, lane);
+      pair_sync(strip);
+      auto correct = [&](auto first) {
+        constexpr int t0 = first();
+        take_add(from, r, t0, lane);
+        if (t0 == 0) emptied(strip);
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[t][e] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < NP / 16; ++kk) {
-        uint32_t a[2][4];
-        a_from_acc_h(a, S, kk, s0.s, s1.s);
-#pragma unroll
-        for (int np = 0; np < 4; ++np)
-          mma_planes_h<NI>(r[2 * np], r[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
-          });
-      }
-      store_strip<NP / 8>(w.dS + (at * d.Ps + row) * NP, S, lane);
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const float fu = g.fu[8 * t + t2 + f];
-          r[t][f] *= fu * s0.inv;
-          r[t][2 + f] *= fu * s1.inv;
+        for (int t = t0; t < t0 + 4; ++t) {
+          const float2 fu = *reinterpret_cast<const float2*>(g.fu + 8 * t + t2);
+          r[t][0] *= fu.x, r[t][1] *= fu.y, r[t][2] *= fu.x, r[t][3] *= fu.y;
         }
-      store_strip<8>(w.Zd + (at * d.Ps + row) * kC, r, lane);
+        store_half(w.Zd, srow, r, t0, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          r[t0 + t][0] += ev[t].x, r[t0 + t][1] += ev[t].y;
+          r[t0 + t][2] += ev[t].z, r[t0 + t][3] += ev[t].w;
+        }
+        float x0, x1;
+        half_max(r, t0, x0, x1);
+        const Scale q0 = scale_of(x0), q1 = scale_of(x1);
+        float u[8][4];
+        clear(u);
+#pragma unroll
+        for (int kb = t0 / 2; kb < t0 / 2 + 2; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
+          uint32_t a[2][4];
+          a_from_acc_h(a, r, kb, q0.s, q1.s);
+#pragma unroll
+          for (int np = 0; np <= kb; ++np)
+            mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+              b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+            });
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float2 fx = *reinterpret_cast<const float2*>(g.fx + 8 * t + t2);
+          r[t][0] = u[t][0] * (fx.x * q0.inv), r[t][1] = u[t][1] * (fx.y * q0.inv);
+          r[t][2] = u[t][2] * (fx.x * q1.inv), r[t][3] = u[t][3] * (fx.y * q1.inv);
+        }
+      };
+      auto weigh = [&](auto first) {  // tokens' dR to the workspace, then times -b e^G 2^k
+        constexpr int t0 = first();
+        store_half(w.dR, srow, r, t0, lane);
+#pragma unroll
+        for (int t = t0; t < t0 + 4; ++t) {
+          const float2 fz = *reinterpret_cast<const float2*>(g.fz + 8 * t + t2);
+          r[t][0] *= -fz.x, r[t][1] *= -fz.y, r[t][2] *= -fz.x, r[t][3] *= -fz.y;
+        }
+      };
+      const std::integral_constant<int, 0> lo;
+      const std::integral_constant<int, 4> hi;
+      if (half == 1) {
+        correct(hi);
+        give(from, r, 0, lane);
+        weigh(hi);
+        refill(strip);
+        give(to, r, 4, lane);
+        pair_sync(strip);
+      } else {
+        correct(lo);
+        pair_sync(strip);
+        take_add(to, r, 0, lane);
+        take(from, r, 4, lane);
+        weigh(lo);
+      }
+      // tokens 32 .. 63 of dR and every token of scale e^G dY 2^q, then tokens 0 .. 31
+      float y[8][4], b0, b1;
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const float2 e0 = *reinterpret_cast<const float2*>(ep + 8 * t);
-        const float2 e1 = *reinterpret_cast<const float2*>(ep + 8 * kC + 8 * t);
-        r[t][0] += e0.x, r[t][1] += e0.y, r[t][2] += e1.x, r[t][3] += e1.y;
+        const int i = 8 * t + t2, p = strip * 16 + g8;
+        const float2 fq = *reinterpret_cast<const float2*>(g.fq + i);
+        y[t][0] = fq.x * to_f(yt[i * RP + p]), y[t][1] = fq.y * to_f(yt[(i + 1) * RP + p]);
+        y[t][2] = fq.x * to_f(yt[i * RP + p + 8]), y[t][3] = fq.y * to_f(yt[(i + 1) * RP + p + 8]);
       }
-      row_max<8>(r, m0, m1);
-      const Scale q0 = scale_of(m0), q1 = scale_of(m1);
-      float u[8][4];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
-        uint32_t a[2][4];
-        a_from_acc_h(a, r, kb, q0.s, q1.s);
-#pragma unroll
-        for (int np = 0; np <= kb; ++np)
-          mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
-          });
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const float fx = g.fx[8 * t + t2 + f];
-          u[t][f] *= fx * q0.inv;
-          u[t][2 + f] *= fx * q1.inv;
-        }
-      store_strip<8>(w.dR + (at * d.Ps + row) * kC, u, lane);
-      // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int i = 8 * t + t2 + f;
-          const float fq = g.fq[i], fz = -g.fz[i];
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            r[t][2 * o + f] = fq * to_f(yt[i * RP + strip * 16 + g8 + o * 8]);
-            u[t][2 * o + f] *= fz;
-          }
-        }
-      float n0, n1;
-      row_max<8>(r, m0, m1);
-      row_max<8>(u, n0, n1);
-      const Scale u0 = scale_of(fmaxf(fmaxf(m0, n0), least0)),
-                  u1 = scale_of(fmaxf(fmaxf(m1, n1), least1));
-      const float end = ex2(g.gh[kC - 1]), d0 = end * u0.s, d1 = end * u1.s;
-#pragma unroll
-      for (int t = 0; t < NP / 8; ++t) S[t][0] *= d0, S[t][1] *= d0, S[t][2] *= d1, S[t][3] *= d1;
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[2][4];
-        a_from_acc_h(a, u, kb, u0.s, u1.s);
-#pragma unroll
-        for (int np = 0; np < NP / 16; ++np)
-          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
-          });
-        a_from_acc_h(a, r, kb, u0.s, u1.s);
-#pragma unroll
-        for (int np = 0; np < NP / 16; ++np)
-          mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_cols<LD>(x, qt + j * kC * LD, np * 16, kb * 16, lane);
-          });
-      }
-#pragma unroll
-      for (int t = 0; t < NP / 8; ++t)
-        S[t][0] *= u0.inv, S[t][1] *= u0.inv, S[t][2] *= u1.inv, S[t][3] *= u1.inv;
+      row_max<8>(y, b0, b1);
+      half_max(r, 4, a0, a1);
+      a0 = fmaxf(a0, b0), a1 = fmaxf(a1, b1);
+      const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
+      const float end = ex2(g.gh[kC - 1]);
+      scale_rows(S, end * u0.s, end * u1.s);
+      add_outer<NI, NP, 4>(S, y, 0, qt, half, u0.s, u1.s, lane);
+      add_outer<NI, NP, 2>(S, r, 2, kt, half, u0.s, u1.s, lane);
+      m0 = fmaxf(m0, a0 * 2 * kC), m1 = fmaxf(m1, a1 * 2 * kC);
+      if (half == 0) give(to, r, 0, lane);
+      pair_sync(strip);
+      if (half == 1) take(from, r, 0, lane);
+      half_max(r, 0, a0, a1);
+      const Scale v0 = scale_of(fmaxf(a0, m0 * kBelow)), v1 = scale_of(fmaxf(a1, m1 * kBelow));
+      scale_rows(S, v0.s * u0.inv, v1.s * u1.inv);
+      add_outer<NI, NP, 2>(S, r, 0, kt, half, v0.s, v1.s, lane);
+      scale_rows(S, v0.inv, v1.inv);
     }
-    __syncthreads();
-    if (STAGES == 1 && c > 0) fetch(c - 1, 0);
+    if (STAGES == 1 && c > 0) {
+      __syncthreads();
+      fetch(c - 1, 0);
+    }
   }
-  if (dinit && active) store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+  if (dinit && active)
+    store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, half, lane);
 }
 
 // ---------------------------------------------------------------------- grad
@@ -1124,7 +1253,7 @@ struct GradSums {
   float row[4][kC];       // rows of dAqk Aqk - W M, a column block each
   float col[4][kC];       // columns of the same, a row strip each
   float qd[4][kC];        // scale e^G q . (dY S0), a quarter of the key columns each
-  float part[16][3][kC];  // U . Zd, dR . Zb, dR . U, a warp's value rows each
+  float part[2][3][kC];   // U . Zd, dR . Zb, dR . U, half of the value rows each
   float dot[16];          // <dS, S0>, a warp each
 };
 
@@ -1223,7 +1352,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     for (int t = 0; t < HT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dqh[t][e] = 0.f;
-    float4 su = make_float4(0.f, 0.f, 0.f, 0.f), sr = su, sw = su;  // of tokens 4 (tid & 15) ..
+    float2 su = make_float2(0.f, 0.f), sr = su, sw = su;  // of two tokens, the same in every load
     float dot = 0.f;
     for (int p0 = 0; p0 < d.Ps; p0 += kC) {
       const int pr = min(kC, d.Ps - p0);
@@ -1247,12 +1376,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
       for (int i = 0; i < wr.kN; ++i) {
         const float4 r = wr.v[i], u = wu.v[i], z = wz.v[i], x = wb.v[i];
-        su.x = fmaf(u.x, z.x, su.x), su.y = fmaf(u.y, z.y, su.y);
-        su.z = fmaf(u.z, z.z, su.z), su.w = fmaf(u.w, z.w, su.w);
-        sr.x = fmaf(r.x, x.x, sr.x), sr.y = fmaf(r.y, x.y, sr.y);
-        sr.z = fmaf(r.z, x.z, sr.z), sr.w = fmaf(r.w, x.w, sr.w);
-        sw.x = fmaf(r.x, u.x, sw.x), sw.y = fmaf(r.y, u.y, sw.y);
-        sw.z = fmaf(r.z, u.z, sw.z), sw.w = fmaf(r.w, u.w, sw.w);
+        su.x = fmaf(u.x, z.x, fmaf(u.z, z.z, su.x)), su.y = fmaf(u.y, z.y, fmaf(u.w, z.w, su.y));
+        sr.x = fmaf(r.x, x.x, fmaf(r.z, x.z, sr.x)), sr.y = fmaf(r.y, x.y, fmaf(r.w, x.w, sr.y));
+        sw.x = fmaf(r.x, u.x, fmaf(r.z, u.z, sw.x)), sw.y = fmaf(r.y, u.y, fmaf(r.w, u.w, sw.y));
       }
       cp_wait<0>();
       __syncthreads();
@@ -1319,9 +1445,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int l = 2; l >= 0; --l) {
-          const uint2 x = *reinterpret_cast<const uint2*>(st + l * kC * LD + r * LD + cc);
-          s.x += __uint_as_float(x.x << 16), s.y += __uint_as_float(x.x & 0xffff0000u);
-          s.z += __uint_as_float(x.y << 16), s.w += __uint_as_float(x.y & 0xffff0000u);
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(st + l * kC * LD + r * LD + cc);
+          const uint32_t z = *reinterpret_cast<const uint32_t*>(st + l * kC * LD + (r + 8) * LD + cc);
+          s.x += __uint_as_float(x << 16), s.y += __uint_as_float(x & 0xffff0000u);
+          s.z += __uint_as_float(z << 16), s.w += __uint_as_float(z & 0xffff0000u);
         }
         const float4 v = ws.v[i];
         dot = fmaf(v.x, s.x, fmaf(v.y, s.y, fmaf(v.z, s.z, fmaf(v.w, s.w, dot))));
@@ -1344,10 +1471,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) sm.dot[warp] = dot;
-    auto halves = [&](float4 v, int which) {  // two value rows a warp at a time
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
-      v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
-      if (lane < 16) *reinterpret_cast<float4*>(&sm.part[warp][which][4 * lane]) = v;
+    auto halves = [&](float2 v, int which) {  // over the rows of a warp's loads
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      }
+      static_assert(kGradThreads / 32 % 8 == 0, "every load of a thread has the same tokens");
+      if (lane < 4)
+        *reinterpret_cast<float2*>(&sm.part[warp >> 3][which][(warp & 7) * 8 + 2 * lane]) = v;
     };
     halves(su, 0);
     halves(sr, 1);
@@ -1491,7 +1623,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const int i = 2 * lane + x;
         float u = 0.f, r = 0.f, ww = 0.f, rs = 0.f, cs = 0.f, qs = 0.f;
 #pragma unroll
-        for (int p = 0; p < 16; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
+        for (int p = 0; p < 2; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
 #pragma unroll
         for (int p = 0; p < 4; ++p) rs += sm.row[p][i], cs += sm.col[p][i], qs += sm.qd[p][i];
         dg[x] = (rs - cs) + (qs - r) - u;
@@ -1654,8 +1786,8 @@ DeltaWs delta_ws(const DeltaDims& d, void* base, bool bwd) {
   };
   const size_t n = (size_t)d.B * d.H * d.nc, tok = n * d.Ps * kC * 4, st = n * d.Ps * d.NP * 4;
   w.gates = static_cast<Gates*>(take(n * sizeof(Gates)));
-  w.X = static_cast<bf16*>(take(n * 2 * kC * kC * 2));
-  const size_t image = (size_t)d.B * d.G * d.nc * d.ip * kC * d.NP * 2;
+  w.X = static_cast<bf16*>(take(n * 2 * kC * kTP * 2));
+  const size_t image = (size_t)d.B * d.G * d.nc * d.ip * kC * (d.NP + 8) * 2;
   w.K = static_cast<bf16*>(take(image));
   w.U = static_cast<float*>(take(tok));
   w.S0 = static_cast<float*>(take(st));

@@ -167,8 +167,8 @@ __device__ __forceinline__ void row_max(const float (&c)[NT][4], float& m0, floa
   float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    a[t & 1] = fmaxf(a[t & 1], fmaxf(fabsf(c[t][0]), fabsf(c[t][1])));
-    a[2 + (t & 1)] = fmaxf(a[2 + (t & 1)], fmaxf(fabsf(c[t][2]), fabsf(c[t][3])));
+    a[t & 1] = fmaxf(fmaxf(a[t & 1], fabsf(c[t][0])), fabsf(c[t][1]));
+    a[2 + (t & 1)] = fmaxf(fmaxf(a[2 + (t & 1)], fabsf(c[t][2])), fabsf(c[t][3]));
   }
   m0 = fmaxf(a[0], a[1]), m1 = fmaxf(a[2], a[3]);
 #pragma unroll
