@@ -19,10 +19,9 @@
 // a chunk takes nothing from the differences behind it.
 #include <cuda_bf16.h>
 
-#include <type_traits>
-
 #include "layer_math.cuh"
 #include "ssd_internal.h"
+#include "tc_ptx.cuh"
 #include "warp_mma.cuh"
 
 namespace ssd {
@@ -215,16 +214,6 @@ __device__ __forceinline__ void fetch_tile(bf16* dst, const T* src, int64_t ld, 
   }
   load_tile<T, W, LD, THREADS>(dst, src, ld, rv, cv, vec);
 }
-// BYTES of the workspace to shared memory, started asynchronously; images lie there with
-// the pitch of the tiles.
-template <int BYTES, int THREADS>
-__device__ __forceinline__ void copy_image(void* dst, const void* src) {
-  const int o = threadIdx.x * 16;
-#pragma unroll
-  for (int i = 0; i < BYTES; i += THREADS * 16)
-    if (i + THREADS * 16 <= BYTES || i + o < BYTES)
-      cp_async<16>(static_cast<char*>(dst) + o + i, static_cast<const char*>(src) + o + i);
-}
 // Planes of an input's fp16 image.
 template <typename T>
 constexpr int image_planes() { return sizeof(T) == 2 ? 1 : 2; }
@@ -232,26 +221,6 @@ constexpr int image_planes() { return sizeof(T) == 2 ? 1 : 2; }
 // A raw tile of tokens x 64 value columns, as it is, for reads element by element.
 template <typename T>
 constexpr int raw_pitch() { return sizeof(T) == 2 ? kTP : kF; }
-template <typename T, int THREADS>
-__device__ __forceinline__ void fetch_raw(T* dst, const T* src, int64_t ld, int rv, int cv, bool vec) {
-  constexpr int V = 16 / sizeof(T);
-  if (vec) {
-    for (int i = threadIdx.x; i < kC * (kC / V); i += THREADS) {
-      const int r = i / (kC / V), c = i % (kC / V) * V;
-      T* to = dst + r * raw_pitch<T>() + c;
-      if (r < rv && c < cv)
-        cp_async<16>(to, src + r * ld + c);
-      else
-        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-    }
-  } else {
-    for (int i = threadIdx.x; i < kC * kC; i += THREADS) {
-      const int r = i / kC, c = i % kC;
-      dst[r * raw_pitch<T>() + c] = r < rv && c < cv ? src[r * ld + c] : from_f<T>(0.f);
-    }
-  }
-}
-
 struct Place {  // the (batch, head, chunk) of a block
   int b, h, c;
   int64_t i;  // (b * H + h) * nc + c
@@ -598,21 +567,21 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
 
 // --------------------------------------------------------------------- chain
 
-constexpr int kChainThreads = 256;
+constexpr int kChainThreads = 160;
 
 template <typename T, int NP>
 constexpr size_t chain_stage() {
   return sizeof(Gates) + (size_t)image_planes<T>() * kC * (NP + 8) * 2 +
          (size_t)kC * raw_pitch<T>() * sizeof(T) + (size_t)2 * kC * kTP * 2;
 }
-// Half of a state strip (16 rows, NP / 2 columns from half * NP / 2 on) from or to rows of
-// N floats.
+
+// A state strip (16 rows of a warp, NP columns) from or to rows of N floats.
 template <int NP>
-__device__ __forceinline__ void load_state(float (&S)[NP / 16][4], const float* src, int rows, int N,
-                                           int half, int lane) {
-  const int r = lane >> 2, c = half * (NP / 2) + (lane & 3) * 2;
+__device__ __forceinline__ void load_state(float (&S)[NP / 8][4], const float* src, int rows, int N,
+                                           int lane) {
+  const int r = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
-  for (int t = 0; t < NP / 16; ++t)
+  for (int t = 0; t < NP / 8; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
@@ -620,71 +589,80 @@ __device__ __forceinline__ void load_state(float (&S)[NP / 16][4], const float* 
     }
 }
 template <int NP>
-__device__ __forceinline__ void store_state(float* dst, const float (&S)[NP / 16][4], int rows, int N,
-                                            int half, int lane) {
-  const int r = lane >> 2, c = half * (NP / 2) + (lane & 3) * 2;
+__device__ __forceinline__ void store_state(float* dst, const float (&S)[NP / 8][4], int rows, int N,
+                                            int lane) {
+  const int r = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
-  for (int t = 0; t < NP / 16; ++t)
+  for (int t = 0; t < NP / 8; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = r + (e >> 1) * 8, j = 8 * t + c + (e & 1);
       if (i < rows && j < N) dst[(int64_t)i * N + j] = S[t][e];
     }
 }
-// The same to the workspace.
-template <int NP>
-__device__ __forceinline__ void store_state_ws(float* m, int64_t strip, const float (&S)[NP / 16][4],
-                                               int half, int lane) {
-  float4* p = frag(m, strip, NP / 8, lane) + half * (NP / 16) * 32;
-#pragma unroll
-  for (int t = 0; t < NP / 16; ++t) p[t * 32] = as4(S[t]);
+
+// The value rows (tokens for dY) of a chunk as they are, 64 columns from p0 on, by the
+// lanes of one warp: rows of 16 bytes by bulk copies, others element by element; rows
+// from rv on are zeros, columns from cv on stay as they were.  Returns the bytes that
+// will complete on bar.
+template <typename T>
+__device__ __forceinline__ uint32_t raw_rows(T* dst, const T* src, int64_t ld, int rv, int cv, bool vec,
+                                             uint64_t* bar, int lane) {
+  constexpr int RP = raw_pitch<T>();
+  cv = min(cv, kC);
+  for (int r = max(rv, 0) + lane; r < kC; r += 32)
+    for (int c = 0; c < kC; ++c) dst[r * RP + c] = from_f<T>(0.f);
+  if (vec) {
+    for (int r = lane; r < rv; r += 32) tc::bulk_g2s(dst + r * RP, src + r * ld, cv * sizeof(T), bar);
+    return (uint32_t)(rv * cv * sizeof(T));
+  }
+  for (int r = 0; r < rv; ++r)
+    for (int c = lane; c < cv; c += 32) dst[r * RP + c] = src[r * ld + c];
+  return 0;
 }
 
-// Barrier of the two warps of a strip.
-__device__ __forceinline__ void pair_sync(int strip) {
-  asm volatile("bar.sync %0, 64;" ::"r"(strip + 1) : "memory");
-}
-// A box read by one warp of the pair (emptied) before the other fills it again (refill).
-__device__ __forceinline__ void emptied(int strip) {
-  asm volatile("bar.arrive %0, 64;" ::"r"(strip + 5) : "memory");
-}
-__device__ __forceinline__ void refill(int strip) {
-  asm volatile("bar.sync %0, 64;" ::"r"(strip + 5) : "memory");
-}
-// Four tiles of a strip to and from the other warp of the pair, lane by lane.
-__device__ __forceinline__ void give(float4* box, const float (&c)[8][4], int t0, int lane) {
+// Stages of a chain: filled by a warp of their own (the fifth), used by a warp for each
+// strip, which wait for nothing but their stage.
+struct ChainBars {
+  uint64_t full[2], empty[2];
+  int abort, pad[3];
+};
+constexpr int kChainWarps = 4, kFillWarp = 4;
+
+// Z^T = S K^T, rows of S scaled.
+template <int NI, int NP>
+__device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (&S)[NP / 8][4],
+                                                 const bf16* kt, Scale s0, Scale s1, int lane) {
+  constexpr int LD = NP + 8;
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    box[t * 32 + lane] = make_float4(c[t0 + t][0], c[t0 + t][1], c[t0 + t][2], c[t0 + t][3]);
-}
-__device__ __forceinline__ void take_add(const float4* box, float (&c)[8][4], int t0, int lane) {
+  for (int t = 0; t < 8; ++t)
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const float4 v = box[t * 32 + lane];
-    c[t0 + t][0] += v.x, c[t0 + t][1] += v.y, c[t0 + t][2] += v.z, c[t0 + t][3] += v.w;
+    for (int e = 0; e < 4; ++e) z[t][e] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < NP / 16; ++kk) {
+    uint32_t a[2][4];
+    a_from_acc_h(a, S, kk, s0.s, s1.s);
+#pragma unroll
+    for (int np = 0; np < 4; ++np)
+      mma_planes_h<NI>(z[2 * np], z[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+        b_rows<LD>(x, kt + j * kC * LD, np * 16, kk * 16, lane);
+      });
   }
 }
-__device__ __forceinline__ void take(const float4* box, float (&c)[8][4], int t0, int lane) {
+// S += the product of the tokens of c (rows scaled) with their rows of the tile.
+template <int NI, int NP>
+__device__ __forceinline__ void add_outer(float (&S)[NP / 8][4], const float (&c)[8][4],
+                                          const bf16* kt, float f0, float f1, int lane) {
+  constexpr int LD = NP + 8;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const float4 v = box[t * 32 + lane];
-    c[t0 + t][0] = v.x, c[t0 + t][1] = v.y, c[t0 + t][2] = v.z, c[t0 + t][3] = v.w;
-  }
-}
-constexpr int kBox = 4 * 32;                  // float4s of one exchange
-constexpr size_t kBoxes = 4 * 2 * kBox * 16;  // two for each strip
-// Largest magnitudes of four tiles' rows.
-__device__ __forceinline__ void half_max(const float (&c)[8][4], int t0, float& m0, float& m1) {
-  m0 = m1 = 0.f;
+  for (int kb = 0; kb < 4; ++kb) {
+    uint32_t a[2][4];
+    a_from_acc_h(a, c, kb, f0, f1);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    m0 = fmaxf(fmaxf(m0, fabsf(c[t0 + t][0])), fabsf(c[t0 + t][1]));
-    m1 = fmaxf(fmaxf(m1, fabsf(c[t0 + t][2])), fabsf(c[t0 + t][3]));
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    for (int np = 0; np < NP / 16; ++np)
+      mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+        b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
+      });
   }
 }
 // A strip's rows times f0 and f1.
@@ -697,223 +675,160 @@ __device__ __forceinline__ void scale_rows(float (&c)[NT][4], float f0, float f1
     c[t][0] = a.x, c[t][1] = a.y, c[t][2] = b.x, c[t][3] = b.y;
   }
 }
-// Four tiles (32 tokens, from tile t0 on) of a strip to the workspace.
-__device__ __forceinline__ void store_half(float* m, int64_t strip, const float (&c)[8][4], int t0,
-                                           int lane) {
-  float4* p = frag(m, strip, 8, lane);
+// Its columns (tokens 8 t + t2, + 1) times the tokens' factors.
+__device__ __forceinline__ void scale_tokens(float (&c)[8][4], const float* f, int t2, float g0, float g1) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) p[(t0 + t) * 32] = as4(c[t0 + t]);
+  for (int t = 0; t < 8; ++t) {
+    const float2 x = *reinterpret_cast<const float2*>(f + 8 * t + t2);
+    const float2 a = __fmul2_rn(make_float2(c[t][0], c[t][1]), __fmul2_rn(x, make_float2(g0, g0)));
+    const float2 b = __fmul2_rn(make_float2(c[t][2], c[t][3]), __fmul2_rn(x, make_float2(g1, g1)));
+    c[t][0] = a.x, c[t][1] = a.y, c[t][2] = b.x, c[t][3] = b.y;
+  }
 }
 template <int NT>
-__device__ __forceinline__ void clear(float (&c)[NT][4]) {
+__device__ __forceinline__ void store_strip(float* m, int64_t strip, const float (&c)[NT][4], int lane) {
+  float4* p = frag(m, strip, NT, lane);
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[t][e] = 0.f;
-}
-// Z^T += S K^T over the warp's key columns; rows of S scaled.
-template <int NI, int NP>
-__device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (&S)[NP / 16][4],
-                                                 const bf16* kt, int half, Scale s0, Scale s1,
-                                                 int lane) {
-  constexpr int LD = NP + 8;
-  clear(z);
-#pragma unroll
-  for (int kk = 0; kk < NP / 32; ++kk) {
-    uint32_t a[2][4];
-    a_from_acc_h(a, S, kk, s0.s, s1.s);
-#pragma unroll
-    for (int np = 0; np < 4; ++np)
-      mma_planes_h<NI>(z[2 * np], z[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-        b_rows<LD>(x, kt + j * kC * LD, np * 16, half * (NP / 2) + kk * 16, lane);
-      });
-  }
-  scale_rows(z, s0.inv, s1.inv);
-}
-// S += the product of tokens 16 kb0 .. of c (rows scaled) with their rows of the tile.
-template <int NI, int NP, int NB>
-__device__ __forceinline__ void add_outer(float (&S)[NP / 16][4], const float (&c)[8][4], int kb0,
-                                          const bf16* kt, int half, float f0, float f1, int lane) {
-  constexpr int LD = NP + 8;
-#pragma unroll
-  for (int kb = 0; kb < NB; ++kb) {
-    uint32_t a[2][4];
-    a_from_acc_h(a, c, kb0 + kb, f0, f1);
-#pragma unroll
-    for (int np = 0; np < NP / 32; ++np)
-      mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-        b_cols<LD>(x, kt + j * kC * LD, half * (NP / 2) + np * 16, (kb0 + kb) * 16, lane);
-      });
-  }
+  for (int t = 0; t < NT; ++t) p[t * 32] = as4(c[t]);
 }
 constexpr float kBelow = 5.9604644775390625e-8f;  // 2^-24
 
-// The chain over a head's chunks: 64 value rows a block, a strip of 16 rows for each pair
-// of warps, whose state is in registers: half the key columns a warp (16 x NP / 2 fp32,
-// an accumulator).  A chunk is three products,
+// The chain over a head's chunks: 64 value rows a block, a strip of 16 rows a warp with
+// its state in registers (16 x NP fp32, an accumulator).  A chunk is three products,
 //     Z^T = S K^T,   U^T = (b (V - e^G Z))^T X^T,   S <- e^G63 S + (e^(G63 - G) U)^T K,
-// each left operand formed from the last accumulator; K, V and X are shared tiles, copied
-// while the chunk before is at work.
+// each left operand formed from the last accumulator.
 // Left operands are two fp16 planes of rows scaled by their largest value, K is one
-// (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a strip and chunk, where three
-// planes of bf16 take 504.  At 8 clocks each they bound a chunk by 1.3 us.
-// Two warps a strip, on the same SM quarter, so that one's products run under the other's
-// conversions (one warp a strip: 3.4 us a chunk).  Each forms Z over its key columns; they
-// swap halves, so that each has 32 tokens; the first warp's tokens need no others, and
-// what they give to the later ones goes to the second warp with them; the second's go back
-// while the first adds its own to its state.
-// KEEP: also writes b e^G Z, for the backward.
+// (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
+// bf16 take 504.  The products are issued by one warp per SM quarter at 8 clocks each,
+// which bounds a chunk by 1.3 us.  KEEP: also writes b e^G Z, for the backward.
 template <typename T, int NP, bool KEEP>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_chain(DeltaDims d, const T* __restrict__ v, const float* __restrict__ init,
-                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states) {
-  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>(), NT = NP / 16;
+                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states,
+                  int* status) {
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 31, strip = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
-  float4* const to = reinterpret_cast<float4*>(smem) + (strip * 2 + half) * kBox;
-  float4* const from = reinterpret_cast<float4*>(smem) + (strip * 2 + (half ^ 1)) * kBox;
+  ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
   const int ptiles = (d.Ps + kC - 1) / kC;
   const int p0 = (int)(blockIdx.x % ptiles) * kC;
   const int64_t bh = blockIdx.x / ptiles;
   const int h = (int)(bh % d.H), b = (int)(bh / d.H);
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
+  const int strips = min(kChainWarps, (d.Ps - p0) / 16);
+  unsigned char* const stages = smem + sizeof(ChainBars);
+  constexpr size_t STAGE = chain_stage<T, NP>(), VT = sizeof(Gates) + NI * kC * LD * 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.full[i], 32);
+      tc::mbar_init(&sm.empty[i], strips);
+    }
+    tc::fence_mbar_init();
+    sm.abort = 0;
+  }
+  for (int i = threadIdx.x; i < 2 * kC * RP; i += kChainThreads)  // columns that no copy fills
+    reinterpret_cast<T*>(stages + (i >= kC * RP ? STAGE : 0) + VT)[i % (kC * RP)] = from_f<T>(0.f);
+  tc::fence_async_smem();
+  __syncthreads();
+
+  if (strip == kFillWarp) {
+    const T* const vg = v + b * d.vb + (int64_t)h * d.P + p0;
+    const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
+    int c = 0;
+    for (; c < nc; ++c) {
+      const int s = c & 1;
+      if (!tc::mbar_wait(&sm.empty[s], ((c >> 1) & 1) ^ 1, status, &sm.abort)) break;
+      unsigned char* at = stages + s * STAGE;
+      uint64_t* bar = &sm.full[s];
+      if (lane == 0) {
+        tc::bulk_g2s(at, w.gates + bh * d.nc + c, sizeof(Gates), bar);
+        tc::bulk_g2s(at + sizeof(Gates), kg + (int64_t)c * NI * kC * LD, NI * kC * LD * 2, bar);
+        tc::bulk_g2s(at + VT + kC * RP * sizeof(T), w.X + (bh * d.nc + c) * (2 * kC * kTP),
+                     2 * kC * kTP * 2, bar);
+      }
+      const uint32_t raw = raw_rows<T>(reinterpret_cast<T*>(at + VT), vg + (int64_t)c * kC * d.vs, d.vs,
+                                       min(kC, n - c * kC), d.P - p0, d.vv, bar, lane);
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(bar, raw + sizeof(Gates) + NI * kC * LD * 2 + 2 * kC * kTP * 2);
+      else
+        tc::mbar_arrive(bar);
+    }
+    // what is on its way lands before the block ends (where its strips gave up)
+    for (int i = max(0, c - 2); i < c; ++i) tc::mbar_drain(&sm.full[i & 1], (i >> 1) & 1);
+    return;
+  }
+  if (strip >= strips) return;
   const int row = p0 + strip * 16;  // this warp's first value row
-  const bool active = row < d.Ps;
-  const T* const vg = v + b * d.vb + (int64_t)h * d.P + p0;
-  const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
-
-  auto stage = [&](int s) { return smem + kBoxes + s * chain_stage<T, NP>(); };
-  auto fetch = [&](int c, int s) {
-    unsigned char* at = stage(s);
-    copy_image<sizeof(Gates), kChainThreads>(at, w.gates + bh * d.nc + c);
-    bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
-    T* vt = reinterpret_cast<T*>(kt + NI * kC * LD);
-    bf16* xt = reinterpret_cast<bf16*>(vt + kC * RP);
-    copy_image<NI * kC * LD * 2, kChainThreads>(kt, kg + (int64_t)c * NI * kC * LD);
-    fetch_raw<T, kChainThreads>(vt, vg + (int64_t)c * kC * d.vs, d.vs, min(kC, n - c * kC), d.P - p0,
-                                d.vv);
-    copy_image<2 * kC * kTP * 2, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kTP));
-    cp_commit();
-  };
-
-  float S[NT][4];
-  load_state<NP>(S, init && active ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, half,
-                 lane);
+  float S[NP / 8][4];
+  load_state<NP>(S, init ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-  if (nc > 0) fetch(0, 0);
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
-    cp_wait<0>();
-    __syncthreads();  // this chunk's tiles are there, the last one's are read
-    if (c + 1 < nc) fetch(c + 1, s ^ 1);
-    if (active) {
-      const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
-      const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
-      const T* vt = reinterpret_cast<const T*>(kt + NI * kC * LD);
-      const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
-      const int64_t at = bh * d.nc + c, srow = (at * d.Ps + row) / 16;
-      float m0, m1, a0, a1;
-      row_max<NT>(S, m0, m1);
-      float r[8][4];
-      state_times_keys<NI, NP>(r, S, kt, half, scale_of(m0), scale_of(m1), lane);
-      if (half) give(to, r, 0, lane);
-      else give(to, r, 4, lane);
-      store_state_ws<NP>(w.S0, srow, S, half, lane);
-      pair_sync(strip);
-      // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and the warp's 32 tokens
-      auto correct = [&](auto first) {
-        constexpr int t0 = first();
-        take_add(from, r, t0, lane);
-        if (t0 == 4) emptied(strip);
+    if (!tc::mbar_wait(&sm.full[s], (c >> 1) & 1, status, &sm.abort)) return;
+    const unsigned char* at = stages + s * STAGE;
+    const Gates& g = *reinterpret_cast<const Gates*>(at);
+    const bf16* kt = reinterpret_cast<const bf16*>(at + sizeof(Gates));
+    const T* vt = reinterpret_cast<const T*>(at + VT);
+    const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
+    const int64_t srow = ((bh * d.nc + c) * d.Ps + row) / 16;
+    float m0, m1, a0, a1;
+    row_max<NP / 8>(S, m0, m1);
+    const Scale s0 = scale_of(m0), s1 = scale_of(m1);
+    float r[8][4];
+    state_times_keys<NI, NP>(r, S, kt, s0, s1, lane);
+    store_strip<NP / 8>(w.S0, srow, S, lane);
+    // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
+    scale_tokens(r, g.fz, t2, s0.inv, s1.inv);
+    if constexpr (KEEP) store_strip<8>(w.Zb, srow, r, lane);
 #pragma unroll
-        for (int t = t0; t < t0 + 4; ++t) {
-          const int i = 8 * t + t2;
-          const float2 bi = *reinterpret_cast<const float2*>(g.b + i);
-          const float2 fz = *reinterpret_cast<const float2*>(g.fz + i);
-          float z0 = 0.f, z1 = 0.f;
+    for (int t = 0; t < 8; ++t) {
+      const int i = 8 * t + t2;
+      const float2 bi = *reinterpret_cast<const float2*>(g.b + i);
+      const float2 fx = *reinterpret_cast<const float2*>(g.fx + i);
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int p = strip * 16 + g8 + o * 8;
-            r[t][2 * o] *= fz.x, r[t][2 * o + 1] *= fz.y;
-            if constexpr (KEEP)
-              if (o == 1) frag(w.Zb, srow, 8, lane)[t * 32] = make_float4(z0, z1, r[t][2], r[t][3]);
-            if (o == 0) z0 = r[t][0], z1 = r[t][1];
-            r[t][2 * o] = fmaf(bi.x, to_f(vt[i * RP + p]), -r[t][2 * o]);
-            r[t][2 * o + 1] = fmaf(bi.y, to_f(vt[(i + 1) * RP + p]), -r[t][2 * o + 1]);
-          }
-          const float2 fx = *reinterpret_cast<const float2*>(g.fx + i);
-          r[t][0] *= fx.x, r[t][1] *= fx.y, r[t][2] *= fx.x, r[t][3] *= fx.y;
-        }
-        float x0, x1;
-        half_max(r, t0, x0, x1);
-        const Scale q0 = scale_of(x0), q1 = scale_of(x1);
-        float u[8][4];
-        clear(u);
-#pragma unroll
-        for (int kb = t0 / 2; kb < t0 / 2 + 2; ++kb) {
-          uint32_t a[2][4];
-          a_from_acc_h(a, r, kb, q0.s, q1.s);
-#pragma unroll
-          for (int np = kb; np < 4; ++np)
-            mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-              b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
-            });
-        }
-        scale_rows(u, q0.inv, q1.inv);
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[t][e] = u[t][e];
-      };
-      auto weigh = [&](auto first) {  // tokens' U to the workspace, then times e^(G63 - G) 2^k
-        constexpr int t0 = first();
-        store_half(w.U, srow, r, t0, lane);
-#pragma unroll
-        for (int t = t0; t < t0 + 4; ++t) {
-          const float2 fu = *reinterpret_cast<const float2*>(g.fu + 8 * t + t2);
-          r[t][0] *= fu.x, r[t][1] *= fu.y, r[t][2] *= fu.x, r[t][3] *= fu.y;
-        }
-      };
-      const std::integral_constant<int, 0> lo;
-      const std::integral_constant<int, 4> hi;
-      if (half == 0) {
-        correct(lo);
-        give(from, r, 4, lane);  // (the box that this warp has emptied)
-        weigh(lo);
-        refill(strip);
-        give(to, r, 0, lane);
-        pair_sync(strip);
-      } else {
-        correct(hi);
-        pair_sync(strip);
-        take_add(to, r, 4, lane);
-        take(from, r, 0, lane);
-        weigh(hi);
+      for (int o = 0; o < 2; ++o) {
+        const int p = strip * 16 + g8 + o * 8;
+        r[t][2 * o] = fx.x * fmaf(bi.x, to_f(vt[i * RP + p]), -r[t][2 * o]);
+        r[t][2 * o + 1] = fx.y * fmaf(bi.y, to_f(vt[(i + 1) * RP + p]), -r[t][2 * o + 1]);
       }
-      // the state takes tokens 0 .. 31, then 32 .. 63, each in the scale of its rows, or in
-      // the state's own where that is 2^24 larger (what is lost there is below its rounding)
-      half_max(r, 0, a0, a1);
-      const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
-      const float end = ex2(g.gh[kC - 1]);
-      scale_rows(S, end * u0.s, end * u1.s);
-      add_outer<NI, NP, 2>(S, r, 0, kt, half, u0.s, u1.s, lane);
-      m0 = fmaxf(m0, a0 * kC), m1 = fmaxf(m1, a1 * kC);  // bounds of the rows by now
-      if (half == 1) give(to, r, 4, lane);
-      pair_sync(strip);
-      if (half == 0) take(from, r, 4, lane);
-      half_max(r, 4, a0, a1);
-      const Scale v0 = scale_of(fmaxf(a0, m0 * kBelow)), v1 = scale_of(fmaxf(a1, m1 * kBelow));
-      scale_rows(S, v0.s * u0.inv, v1.s * u1.inv);
-      add_outer<NI, NP, 2>(S, r, 2, kt, half, v0.s, v1.s, lane);
-      scale_rows(S, v0.inv, v1.inv);
     }
+    row_max<8>(r, a0, a1);
+    const Scale q0 = scale_of(a0), q1 = scale_of(a1);
+    float u[8][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t a[2][4];
+      a_from_acc_h(a, r, kb, q0.s, q1.s);
+#pragma unroll
+      for (int np = kb; np < 4; ++np)
+        mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          b_cols<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+        });
+    }
+    scale_rows(u, q0.inv, q1.inv);
+    store_strip<8>(w.U, srow, u, lane);
+    scale_tokens(u, g.fu, t2, 1.f, 1.f);
+    // the state takes the products in the scale of U's rows, or of its own where that is
+    // 2^24 larger (what U would lose there is below the state's own rounding)
+    row_max<8>(u, a0, a1);
+    const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
+    const float end = ex2(g.gh[kC - 1]);
+    scale_rows(S, end * u0.s, end * u1.s);
+    add_outer<NI, NP>(S, u, kt, u0.s, u1.s, lane);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+    scale_rows(S, u0.inv, u1.inv);
   }
-  if (final_states && active)
-    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, half, lane);
+  if (final_states)
+    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
 }
 
 template <typename T, int NP>
-constexpr size_t chain_smem() { return kBoxes + 2 * chain_stage<T, NP>(); }
+constexpr size_t chain_smem() { return sizeof(ChainBars) + 2 * chain_stage<T, NP>(); }
 
 // ----------------------------------------------------------------------- out
 
@@ -1068,180 +983,141 @@ template <typename T, int NP>
 constexpr size_t back_stage() {
   return chain_stage<T, NP>() + (size_t)image_planes<T>() * kC * (NP + 8) * 2;
 }
-// (two stages of fp32 inputs' size do not fit)
 template <typename T, int NP>
-constexpr int back_stages() { return kBoxes + 2 * back_stage<T, NP>() <= 220 * 1024 ? 2 : 1; }
-template <typename T, int NP>
-constexpr size_t back_smem() { return kBoxes + back_stages<T, NP>() * back_stage<T, NP>(); }
+constexpr size_t back_smem() { return sizeof(ChainBars) + 2 * back_stage<T, NP>(); }
 
 // The chain of the backward, from the last chunk to the first, with the gradient of the
 // state behind the chunk in registers:
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
 //     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
-// in the manner of k_delta_chain, 444 products a chunk.  Here the later 32 tokens need no
-// others: they are first.
+// in the manner of k_delta_chain: 444 products a chunk.
 template <typename T, int NP>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
-                 const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit) {
-  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>(), NT = NP / 16;
-  constexpr int STAGES = back_stages<T, NP>();
+                 const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit, int* status) {
+  constexpr int NI = image_planes<T>(), LD = NP + 8, RP = raw_pitch<T>();
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 31, strip = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
-  float4* const to = reinterpret_cast<float4*>(smem) + (strip * 2 + half) * kBox;
-  float4* const from = reinterpret_cast<float4*>(smem) + (strip * 2 + (half ^ 1)) * kBox;
+  ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
   const int ptiles = (d.Ps + kC - 1) / kC;
   const int p0 = (int)(blockIdx.x % ptiles) * kC;
   const int64_t bh = blockIdx.x / ptiles;
   const int h = (int)(bh % d.H), b = (int)(bh / d.H);
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
-  const int row = p0 + strip * 16;
-  const bool active = row < d.Ps;
-  const int64_t ys = (int64_t)d.H * d.P;
-  const T* const yg = dy + b * (int64_t)d.T * ys + (int64_t)h * d.P + p0;
-  const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
-
-  auto stage = [&](int s) { return smem + kBoxes + s * back_stage<T, NP>(); };
-  auto fetch = [&](int c, int s) {
-    unsigned char* at = stage(s);
-    copy_image<sizeof(Gates), kChainThreads>(at, w.gates + bh * d.nc + c);
-    bf16* kt = reinterpret_cast<bf16*>(at + sizeof(Gates));
-    bf16* qt = kt + NI * kC * LD;
-    T* yt = reinterpret_cast<T*>(qt + NI * kC * LD);
-    bf16* xt = reinterpret_cast<bf16*>(yt + kC * RP);
-    copy_image<NI * kC * LD * 2, kChainThreads>(kt, w.K + img + (int64_t)c * NI * kC * LD);
-    copy_image<NI * kC * LD * 2, kChainThreads>(qt, w.Q + img + (int64_t)c * NI * kC * LD);
-    fetch_raw<T, kChainThreads>(yt, yg + (int64_t)c * kC * ys, ys, min(kC, n - c * kC), d.P - p0,
-                                d.vdy);
-    copy_image<2 * kC * kTP * 2, kChainThreads>(xt, w.X + (bh * d.nc + c) * (2 * kC * kTP));
-    cp_commit();
-  };
-
-  float S[NT][4];
-  load_state<NP>(S, dfinal && active ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N,
-                 half, lane);
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-  if (nc > 0) fetch(nc - 1, 0);
-  for (int c = nc - 1; c >= 0; --c) {
-    const int s = STAGES == 2 ? (nc - 1 - c) & 1 : 0;
-    cp_wait<0>();
-    __syncthreads();  // this chunk's tiles are there, the last one's are read
-    if (STAGES == 2 && c > 0) fetch(c - 1, s ^ 1);
-    if (active) {
-      const Gates& g = *reinterpret_cast<const Gates*>(stage(s));
-      const bf16* kt = reinterpret_cast<const bf16*>(stage(s) + sizeof(Gates));
-      const bf16* qt = kt + NI * kC * LD;
-      const T* yt = reinterpret_cast<const T*>(qt + NI * kC * LD);
-      const bf16* xt = reinterpret_cast<const bf16*>(yt + kC * RP);
-      const int64_t at = bh * d.nc + c, srow = (at * d.Ps + row) / 16;
-      float m0, m1, a0, a1;
-      row_max<NT>(S, m0, m1);
-      // the warp's tokens of E, on their way under the products
-      float4 ev[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) ev[t] = frag(w.E, srow, 8, lane)[(half * 4 + t) * 32];
-      float r[8][4];
-      state_times_keys<NI, NP>(r, S, kt, half, scale_of(m0), scale_of(m1), lane);
-      if (half) give(to, r, 0, lane);
-      else give(to, r, 4, lane);
-      store_state_ws<NP>(w.dS, srow, S, half, lane);
-      pair_sync(strip);
-      auto correct = [&](auto first) {
-        constexpr int t0 = first();
-        take_add(from, r, t0, lane);
-        if (t0 == 0) emptied(strip);
-#pragma unroll
-        for (int t = t0; t < t0 + 4; ++t) {
-          const float2 fu = *reinterpret_cast<const float2*>(g.fu + 8 * t + t2);
-          r[t][0] *= fu.x, r[t][1] *= fu.y, r[t][2] *= fu.x, r[t][3] *= fu.y;
-        }
-        store_half(w.Zd, srow, r, t0, lane);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          r[t0 + t][0] += ev[t].x, r[t0 + t][1] += ev[t].y;
-          r[t0 + t][2] += ev[t].z, r[t0 + t][3] += ev[t].w;
-        }
-        float x0, x1;
-        half_max(r, t0, x0, x1);
-        const Scale q0 = scale_of(x0), q1 = scale_of(x1);
-        float u[8][4];
-        clear(u);
-#pragma unroll
-        for (int kb = t0 / 2; kb < t0 / 2 + 2; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
-          uint32_t a[2][4];
-          a_from_acc_h(a, r, kb, q0.s, q1.s);
-#pragma unroll
-          for (int np = 0; np <= kb; ++np)
-            mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-              b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
-            });
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const float2 fx = *reinterpret_cast<const float2*>(g.fx + 8 * t + t2);
-          r[t][0] = u[t][0] * (fx.x * q0.inv), r[t][1] = u[t][1] * (fx.y * q0.inv);
-          r[t][2] = u[t][2] * (fx.x * q1.inv), r[t][3] = u[t][3] * (fx.y * q1.inv);
-        }
-      };
-      auto weigh = [&](auto first) {  // tokens' dR to the workspace, then times -b e^G 2^k
-        constexpr int t0 = first();
-        store_half(w.dR, srow, r, t0, lane);
-#pragma unroll
-        for (int t = t0; t < t0 + 4; ++t) {
-          const float2 fz = *reinterpret_cast<const float2*>(g.fz + 8 * t + t2);
-          r[t][0] *= -fz.x, r[t][1] *= -fz.y, r[t][2] *= -fz.x, r[t][3] *= -fz.y;
-        }
-      };
-      const std::integral_constant<int, 0> lo;
-      const std::integral_constant<int, 4> hi;
-      if (half == 1) {
-        correct(hi);
-        give(from, r, 0, lane);
-        weigh(hi);
-        refill(strip);
-        give(to, r, 4, lane);
-        pair_sync(strip);
-      } else {
-        correct(lo);
-        pair_sync(strip);
-        take_add(to, r, 0, lane);
-        take(from, r, 4, lane);
-        weigh(lo);
-      }
-      // tokens 32 .. 63 of dR and every token of scale e^G dY 2^q, then tokens 0 .. 31
-      float y[8][4], b0, b1;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const int i = 8 * t + t2, p = strip * 16 + g8;
-        const float2 fq = *reinterpret_cast<const float2*>(g.fq + i);
-        y[t][0] = fq.x * to_f(yt[i * RP + p]), y[t][1] = fq.y * to_f(yt[(i + 1) * RP + p]);
-        y[t][2] = fq.x * to_f(yt[i * RP + p + 8]), y[t][3] = fq.y * to_f(yt[(i + 1) * RP + p + 8]);
-      }
-      row_max<8>(y, b0, b1);
-      half_max(r, 4, a0, a1);
-      a0 = fmaxf(a0, b0), a1 = fmaxf(a1, b1);
-      const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
-      const float end = ex2(g.gh[kC - 1]);
-      scale_rows(S, end * u0.s, end * u1.s);
-      add_outer<NI, NP, 4>(S, y, 0, qt, half, u0.s, u1.s, lane);
-      add_outer<NI, NP, 2>(S, r, 2, kt, half, u0.s, u1.s, lane);
-      m0 = fmaxf(m0, a0 * 2 * kC), m1 = fmaxf(m1, a1 * 2 * kC);
-      if (half == 0) give(to, r, 0, lane);
-      pair_sync(strip);
-      if (half == 1) take(from, r, 0, lane);
-      half_max(r, 0, a0, a1);
-      const Scale v0 = scale_of(fmaxf(a0, m0 * kBelow)), v1 = scale_of(fmaxf(a1, m1 * kBelow));
-      scale_rows(S, v0.s * u0.inv, v1.s * u1.inv);
-      add_outer<NI, NP, 2>(S, r, 0, kt, half, v0.s, v1.s, lane);
-      scale_rows(S, v0.inv, v1.inv);
+  const int strips = min(kChainWarps, (d.Ps - p0) / 16);
+  unsigned char* const stages = smem + sizeof(ChainBars);
+  constexpr size_t STAGE = back_stage<T, NP>(), IMG = NI * kC * LD * 2;
+  constexpr size_t YT = sizeof(Gates) + 2 * IMG;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.full[i], 32);
+      tc::mbar_init(&sm.empty[i], strips);
     }
-    if (STAGES == 1 && c > 0) {
-      __syncthreads();
-      fetch(c - 1, 0);
-    }
+    tc::fence_mbar_init();
+    sm.abort = 0;
   }
-  if (dinit && active)
-    store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, half, lane);
+  for (int i = threadIdx.x; i < 2 * kC * RP; i += kChainThreads)
+    reinterpret_cast<T*>(stages + (i >= kC * RP ? STAGE : 0) + YT)[i % (kC * RP)] = from_f<T>(0.f);
+  tc::fence_async_smem();
+  __syncthreads();
+
+  if (strip == kFillWarp) {
+    const int64_t ys = (int64_t)d.H * d.P;
+    const T* const yg = dy + b * (int64_t)d.T * ys + (int64_t)h * d.P + p0;
+    const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
+    int i = 0;  // chunks filled, the last one first
+    for (; i < nc; ++i) {
+      const int s = i & 1, c = nc - 1 - i;
+      if (!tc::mbar_wait(&sm.empty[s], ((i >> 1) & 1) ^ 1, status, &sm.abort)) break;
+      unsigned char* at = stages + s * STAGE;
+      uint64_t* bar = &sm.full[s];
+      if (lane == 0) {
+        tc::bulk_g2s(at, w.gates + bh * d.nc + c, sizeof(Gates), bar);
+        tc::bulk_g2s(at + sizeof(Gates), w.K + img + (int64_t)c * NI * kC * LD, IMG, bar);
+        tc::bulk_g2s(at + sizeof(Gates) + IMG, w.Q + img + (int64_t)c * NI * kC * LD, IMG, bar);
+        tc::bulk_g2s(at + YT + kC * RP * sizeof(T), w.X + (bh * d.nc + c) * (2 * kC * kTP),
+                     2 * kC * kTP * 2, bar);
+      }
+      const uint32_t raw = raw_rows<T>(reinterpret_cast<T*>(at + YT), yg + (int64_t)c * kC * ys, ys,
+                                       min(kC, n - c * kC), d.P - p0, d.vdy, bar, lane);
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(bar, raw + sizeof(Gates) + 2 * IMG + 2 * kC * kTP * 2);
+      else
+        tc::mbar_arrive(bar);
+    }
+    for (int j = max(0, i - 2); j < i; ++j) tc::mbar_drain(&sm.full[j & 1], (j >> 1) & 1);
+    return;
+  }
+  if (strip >= strips) return;
+  const int row = p0 + strip * 16;
+  float S[NP / 8][4];
+  load_state<NP>(S, dfinal ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  for (int i = 0; i < nc; ++i) {
+    const int s = i & 1, c = nc - 1 - i;
+    if (!tc::mbar_wait(&sm.full[s], (i >> 1) & 1, status, &sm.abort)) return;
+    const unsigned char* at = stages + s * STAGE;
+    const Gates& g = *reinterpret_cast<const Gates*>(at);
+    const bf16* kt = reinterpret_cast<const bf16*>(at + sizeof(Gates));
+    const bf16* qt = reinterpret_cast<const bf16*>(at + sizeof(Gates) + IMG);
+    const T* yt = reinterpret_cast<const T*>(at + YT);
+    const bf16* xt = reinterpret_cast<const bf16*>(yt + kC * RP);
+    const int64_t srow = ((bh * d.nc + c) * d.Ps + row) / 16;
+    float m0, m1, a0, a1;
+    row_max<NP / 8>(S, m0, m1);
+    const Scale s0 = scale_of(m0), s1 = scale_of(m1);
+    float r[8][4];
+    state_times_keys<NI, NP>(r, S, kt, s0, s1, lane);
+    store_strip<NP / 8>(w.dS, srow, S, lane);
+    scale_tokens(r, g.fu, t2, s0.inv, s1.inv);
+    store_strip<8>(w.Zd, srow, r, lane);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float4 e = frag(w.E, srow, 8, lane)[t * 32];
+      r[t][0] += e.x, r[t][1] += e.y, r[t][2] += e.z, r[t][3] += e.w;
+    }
+    row_max<8>(r, a0, a1);
+    const Scale q0 = scale_of(a0), q1 = scale_of(a1);
+    float u[8][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[t][e] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {  // dR^T[p][j] = sum_{i >= j} dU^T[p][i] X[i][j]
+      uint32_t a[2][4];
+      a_from_acc_h(a, r, kb, q0.s, q1.s);
+#pragma unroll
+      for (int np = 0; np <= kb; ++np)
+        mma_planes_h<2>(u[2 * np], u[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+          b_rows<kTP>(x, xt + j * kC * kTP, np * 16, kb * 16, lane);
+        });
+    }
+    scale_tokens(u, g.fx, t2, q0.inv, q1.inv);
+    store_strip<8>(w.dR, srow, u, lane);
+    // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
+    scale_tokens(u, g.fz, t2, -1.f, -1.f);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int j = 8 * t + t2, p = strip * 16 + g8;
+      r[t][0] = to_f(yt[j * RP + p]), r[t][1] = to_f(yt[(j + 1) * RP + p]);
+      r[t][2] = to_f(yt[j * RP + p + 8]), r[t][3] = to_f(yt[(j + 1) * RP + p + 8]);
+    }
+    scale_tokens(r, g.fq, t2, 1.f, 1.f);
+    float b0, b1;
+    row_max<8>(r, a0, a1);
+    row_max<8>(u, b0, b1);
+    const Scale u0 = scale_of(fmaxf(fmaxf(a0, b0), m0 * kBelow)),
+                u1 = scale_of(fmaxf(fmaxf(a1, b1), m1 * kBelow));
+    const float end = ex2(g.gh[kC - 1]);
+    scale_rows(S, end * u0.s, end * u1.s);
+    add_outer<NI, NP>(S, r, qt, u0.s, u1.s, lane);
+    add_outer<NI, NP>(S, u, kt, u0.s, u1.s, lane);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+    scale_rows(S, u0.inv, u1.inv);
+  }
+  if (dinit) store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
 }
 
 // ---------------------------------------------------------------------- grad
@@ -1850,7 +1726,7 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
                static_cast<const T*>(dy), in.lengths, w);
   const auto chain = k_delta_chain<T, NP, BWD>;
   DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,
-               in.lengths, w, final_states);
+               in.lengths, w, final_states, device_status_ptr());
   return SSD_OK;
 }
 
@@ -1876,7 +1752,7 @@ int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, c
   const int64_t chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
   const auto back = k_delta_back<T, NP>;
   DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP>()), d, dy, g.dfinal,
-               in.lengths, w, g.dinit);
+               in.lengths, w, g.dinit, device_status_ptr());
   const auto grad = k_delta_grad<T, TO, NP>;
   TO *dq = static_cast<TO*>(g.dq), *dk = static_cast<TO*>(g.dk);
   DELTA_LAUNCH("k_delta_grad", grad, (int64_t)d.B * d.G * d.nb * d.nc, kGradThreads,
