@@ -138,15 +138,6 @@ __device__ __forceinline__ void set_lane(const QkDims& d, const float* freq, int
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_piece(const T* p, int c, float (&f)[V]) {
-  if (c >= 0) {
-    unpack<T, V>(ld_raw<T, V>(p + c), f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = 0.f;
-  }
-}
-template <typename T, int V>
 __device__ __forceinline__ void store_piece(T* p, int c, const float (&f)[V]) {
   if (c >= 0) st_raw<T, V>(p + c, pack<T, V>(f));
 }
@@ -177,33 +168,62 @@ __device__ __forceinline__ void turn(bool inter, const float (&sn)[V], const flo
   }
 }
 
-// A unit's token, and the heads (queries, then keys) of its part.
+// A unit's token and position, its rows of q and k, and the heads (queries, then keys) of
+// its part.
 struct Unit {
-  int64_t row;
-  int h0, h1, pos;
+  int row, pos, h0, h1;
+  int64_t q, k;  // elements from the inputs' start to the token's first head
 };
-__device__ __forceinline__ Unit unit(const QkDims& d, int64_t u, const int* positions) {
+__device__ __forceinline__ Unit unit(const QkDims& d, int u, const int* positions) {
   Unit x;
-  x.row = u / d.parts;
-  const int part = (int)(u - x.row * d.parts), n = d.HQ + d.HK;
-  x.h0 = (int)((int64_t)n * part / d.parts);
-  x.h1 = (int)((int64_t)n * (part + 1) / d.parts);
-  x.pos = d.R == 0 ? 0 : positions ? positions[x.row] : (int)(x.row % d.T);
+  x.row = d.parts == 1 ? u : u / d.parts;
+  const int part = u - x.row * d.parts, n = d.HQ + d.HK;
+  x.h0 = d.parts == 1 ? 0 : (int)((int64_t)n * part / d.parts);
+  x.h1 = d.parts == 1 ? n : (int)((int64_t)n * (part + 1) / d.parts);
+  const int b = x.row / d.T, t = x.row - b * d.T;
+  x.q = b * d.qb + t * d.qs;
+  x.k = b * d.kb + t * d.ks;
+  x.pos = d.R == 0 ? 0 : positions ? positions[x.row] : t;
   return x;
 }
 
-// Start of head h's row in a strided input (queries before HQ, keys from it on) and in
-// a dense tensor of the same heads.
-template <typename T>
-__device__ __forceinline__ const T* in_row(const QkDims& d, const T* q, const T* k, int64_t row,
-                                           int h) {
-  const int64_t b = row / d.T, t = row - b * d.T;
-  return h < d.HQ ? q + b * d.qb + t * d.qs + (int64_t)h * d.D
-                  : k + b * d.kb + t * d.ks + (int64_t)(h - d.HQ) * d.D;
-}
-template <typename T>
-__device__ __forceinline__ T* dense_row(const QkDims& d, T* q, T* k, int64_t row, int h) {
-  return h < d.HQ ? q + (row * d.HQ + h) * d.D : k + (row * d.HK + (h - d.HQ)) * d.D;
+// The raw pieces of a head's row.
+template <typename T, int V, int NS>
+struct Row {
+  Raw<T, V> a[NS], b[NS];
+  __device__ __forceinline__ void load(const T* p, const Lane<V, NS>& L) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      a[n] = L.a[n] >= 0 ? ld_raw<T, V>(p + L.a[n]) : zero_raw<T, V>();
+      b[n] = L.b[n] >= 0 ? ld_raw<T, V>(p + L.b[n]) : zero_raw<T, V>();
+    }
+  }
+};
+
+// The weights of queries and keys in a lane's columns.
+template <int V, int NS>
+struct Weights {
+  float a[2][NS][V], b[2][NS][V];
+  __device__ __forceinline__ void load(const float* w_q, const float* w_k, const Lane<V, NS>& L) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      load_weight<V>(w_q, L.a[n], a[0][n]);
+      load_weight<V>(w_q, L.b[n], b[0][n]);
+      load_weight<V>(w_k, L.a[n], a[1][n]);
+      load_weight<V>(w_k, L.b[n], b[1][n]);
+    }
+  }
+};
+
+// The sines and cosines of a token in a lane's columns.
+template <int V, int NS>
+__device__ __forceinline__ void rotations(const QkDims& d, const Lane<V, NS>& L, int pos,
+                                          float (&sn)[NS][V], float (&cs)[NS][V]) {
+  if (d.R > 0)
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int j = 0; j < V; ++j) rotation(L.turn[n][j], pos, &sn[n][j], &cs[n][j]);
 }
 
 template <typename T, typename TO, int V, int LPH, int NS>
@@ -212,52 +232,53 @@ __global__ void __launch_bounds__(kQkThreads)
                   const float* __restrict__ w_q, const float* __restrict__ w_k,
                   const float* __restrict__ freq, const int* __restrict__ positions,
                   TO* __restrict__ q_out, TO* __restrict__ k_out) {
+  constexpr int HP = 32 / LPH;  // heads of a warp at a time
   const int lane = threadIdx.x & 31, seg = lane / LPH, sl = lane % LPH;
-  const int64_t first = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5);
+  const int step = gridDim.x * kQkWarps;
   const bool inter = d.interleaved != 0;
   Lane<V, NS> L;
   set_lane<V, NS>(d, freq, sl, LPH, &L);
-  for (int64_t u = first; u < d.units; u += (int64_t)gridDim.x * kQkWarps) {
-    const Unit x = unit(d, u, positions);
+  Weights<V, NS> W;
+  W.load(w_q, w_k, L);
+  for (int64_t u = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5); u < d.units; u += step) {
+    const Unit x = unit(d, (int)u, positions);
     float sn[NS][V], cs[NS][V];
-    if (d.R > 0)
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int j = 0; j < V; ++j) rotation(L.turn[n][j], x.pos, &sn[n][j], &cs[n][j]);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {  // queries, keys
-      const int lo = kind ? max(x.h0, d.HQ) : x.h0, hi = kind ? x.h1 : min(x.h1, d.HQ);
+      const int base = kind ? d.HQ : 0;
+      const int lo = max(x.h0, base) - base, hi = (kind ? x.h1 : min(x.h1, d.HQ)) - base;
       if (lo >= hi) continue;
-      float wa[NS][V], wb[NS][V];
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        load_weight<V>(kind ? w_k : w_q, L.a[n], wa[n]);
-        load_weight<V>(kind ? w_k : w_q, L.b[n], wb[n]);
-      }
-      for (int h = lo + seg; h - seg < hi; h += 32 / LPH) {
-        const bool live = h < hi;
-        const T* in = in_row(d, q, k, x.row, live ? h : lo);
+      const T* in = (kind ? k + x.k : q + x.q);
+      TO* out = kind ? k_out + (int64_t)x.row * d.HK * d.D : q_out + (int64_t)x.row * d.HQ * d.D;
+      Row<T, V, NS> next;
+      next.load(in + (int64_t)min(lo + seg, hi - 1) * d.D, L);
+      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, L, x.pos, sn, cs);
+      for (int h = lo + seg; h - seg < hi; h += HP) {
+        const Row<T, V, NS> now = next;  // the next head's row is on its way
+        if (h + HP - seg < hi) next.load(in + (int64_t)min(h + HP, hi - 1) * d.D, L);
         float a[NS][V], b[NS][V], ss = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          load_piece<T, V>(in, L.a[n], a[n]);
-          load_piece<T, V>(in, L.b[n], b[n]);
+          unpack<T, V>(now.a[n], a[n]);
+          unpack<T, V>(now.b[n], b[n]);
 #pragma unroll
           for (int j = 0; j < V; ++j) ss = fmaf(a[n][j], a[n][j], fmaf(b[n][j], b[n][j], ss));
         }
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rs = 1.f / sqrtf(fmaf(ss, d.inv, d.eps));
-        TO* out = dense_row(d, q_out, k_out, x.row, live ? h : lo);
+        const float rs = rsqrtf(fmaf(ss, d.inv, d.eps));
+        TO* to = out + (int64_t)h * d.D;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) a[n][j] *= rs * wa[n][j], b[n][j] *= rs * wb[n][j];
+          for (int j = 0; j < V; ++j) {
+            a[n][j] *= rs * W.a[kind][n][j];
+            b[n][j] *= rs * W.b[kind][n][j];
+          }
           if (L.on[n]) turn<1, V>(inter, sn[n], cs[n], a[n], b[n]);
-          if (live) {
-            store_piece<TO, V>(out, L.a[n], a[n]);
-            store_piece<TO, V>(out, L.b[n], b[n]);
+          if (h < hi) {
+            store_piece<TO, V>(to, L.a[n], a[n]);
+            store_piece<TO, V>(to, L.b[n], b[n]);
           }
         }
       }
@@ -275,7 +296,8 @@ __global__ void __launch_bounds__(kQkThreads)
                   TO* __restrict__ dk, float* __restrict__ part) {
   extern __shared__ float sums[];  // (warps, 2, D)
   const int lane = threadIdx.x & 31, seg = lane / LPH, sl = lane % LPH, warp = threadIdx.x >> 5;
-  const int64_t first = (int64_t)blockIdx.x * kQkWarps + warp;
+  constexpr int HP = 32 / LPH;
+  const int step = gridDim.x * kQkWarps;
   const bool inter = d.interleaved != 0;
   Lane<V, NS> L;
   set_lane<V, NS>(d, freq, sl, LPH, &L);
@@ -286,43 +308,42 @@ __global__ void __launch_bounds__(kQkThreads)
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int j = 0; j < V; ++j) ga[kind][n][j] = gb[kind][n][j] = 0.f;
-  for (int64_t u = first; u < d.units; u += (int64_t)gridDim.x * kQkWarps) {
-    const Unit x = unit(d, u, positions);
+  Weights<V, NS> W;
+  W.load(w_q, w_k, L);
+  for (int64_t u = (int64_t)blockIdx.x * kQkWarps + warp; u < d.units; u += step) {
+    const Unit x = unit(d, (int)u, positions);
     float sn[NS][V], cs[NS][V];
-    if (d.R > 0)
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int j = 0; j < V; ++j) rotation(L.turn[n][j], x.pos, &sn[n][j], &cs[n][j]);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      const int lo = kind ? max(x.h0, d.HQ) : x.h0, hi = kind ? x.h1 : min(x.h1, d.HQ);
+      const int base = kind ? d.HQ : 0;
+      const int lo = max(x.h0, base) - base, hi = (kind ? x.h1 : min(x.h1, d.HQ)) - base;
       if (lo >= hi) continue;
-      float wa[NS][V], wb[NS][V];
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        load_weight<V>(kind ? w_k : w_q, L.a[n], wa[n]);
-        load_weight<V>(kind ? w_k : w_q, L.b[n], wb[n]);
-      }
-      for (int h = lo + seg; h - seg < hi; h += 32 / LPH) {
-        const bool live = h < hi;
-        const T* in = in_row(d, q, k, x.row, live ? h : lo);
-        const T* up = dense_row(d, dqo, dko, x.row, live ? h : lo);
+      const T* in = (kind ? k + x.k : q + x.q);
+      const int64_t dense = (int64_t)x.row * (kind ? d.HK : d.HQ) * d.D;
+      const T* up = (kind ? dko : dqo) + dense;
+      TO* out = (kind ? dk : dq) + dense;
+      Row<T, V, NS> nx, ng;
+      nx.load(in + (int64_t)min(lo + seg, hi - 1) * d.D, L);
+      ng.load(up + (int64_t)min(lo + seg, hi - 1) * d.D, L);
+      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, L, x.pos, sn, cs);
+      for (int h = lo + seg; h - seg < hi; h += HP) {
+        const Row<T, V, NS> cx = nx, cg = ng;  // the next head's rows are on their way
+        if (h + HP - seg < hi) {
+          nx.load(in + (int64_t)min(h + HP, hi - 1) * d.D, L);
+          ng.load(up + (int64_t)min(h + HP, hi - 1) * d.D, L);
+        }
         float a[NS][V], b[NS][V], g[NS][V], f[NS][V], ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          load_piece<T, V>(in, L.a[n], a[n]);
-          load_piece<T, V>(in, L.b[n], b[n]);
-          load_piece<T, V>(up, L.a[n], g[n]);
-          load_piece<T, V>(up, L.b[n], f[n]);
-        }
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
+          unpack<T, V>(cx.a[n], a[n]);
+          unpack<T, V>(cx.b[n], b[n]);
+          unpack<T, V>(cg.a[n], g[n]);
+          unpack<T, V>(cg.b[n], f[n]);
           if (L.on[n]) turn<-1, V>(inter, sn[n], cs[n], g[n], f[n]);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             ss = fmaf(a[n][j], a[n][j], fmaf(b[n][j], b[n][j], ss));
-            dot = fmaf(a[n][j] * wa[n][j], g[n][j], fmaf(b[n][j] * wb[n][j], f[n][j], dot));
+            dot = fmaf(a[n][j] * W.a[kind][n][j], g[n][j], fmaf(b[n][j] * W.b[kind][n][j], f[n][j], dot));
           }
         }
 #pragma unroll
@@ -330,23 +351,22 @@ __global__ void __launch_bounds__(kQkThreads)
           ss += __shfl_xor_sync(0xffffffffu, ss, o);
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        const float rs = 1.f / sqrtf(fmaf(ss, d.inv, d.eps));
+        const float rs = rsqrtf(fmaf(ss, d.inv, d.eps));
         const float m = dot * rs * d.inv * rs;  // rstd mean(g w xhat)
-        const float keep = live ? 1.f : 0.f;
-        TO* out = dense_row(d, dq, dk, x.row, live ? h : lo);
+        const float keep = h < hi ? rs : 0.f;
+        TO* to = out + (int64_t)h * d.D;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float xa = a[n][j] * rs, xb = b[n][j] * rs;
-            ga[kind][n][j] = fmaf(g[n][j], xa * keep, ga[kind][n][j]);
-            gb[kind][n][j] = fmaf(f[n][j], xb * keep, gb[kind][n][j]);
-            a[n][j] = fmaf(g[n][j] * wa[n][j], rs, -xa * m);
-            b[n][j] = fmaf(f[n][j] * wb[n][j], rs, -xb * m);
+            ga[kind][n][j] = fmaf(g[n][j], a[n][j] * keep, ga[kind][n][j]);
+            gb[kind][n][j] = fmaf(f[n][j], b[n][j] * keep, gb[kind][n][j]);
+            a[n][j] = rs * fmaf(-a[n][j], m, g[n][j] * W.a[kind][n][j]);
+            b[n][j] = rs * fmaf(-b[n][j], m, f[n][j] * W.b[kind][n][j]);
           }
-          if (live) {
-            store_piece<TO, V>(out, L.a[n], a[n]);
-            store_piece<TO, V>(out, L.b[n], b[n]);
+          if (h < hi) {
+            store_piece<TO, V>(to, L.a[n], a[n]);
+            store_piece<TO, V>(to, L.b[n], b[n]);
           }
         }
       }
