@@ -103,17 +103,17 @@ __device__ __forceinline__ void columns(const QkDims& d, int s, int* a, int* b, 
   }
 }
 
-// What a lane keeps for its pieces.
+// Where a lane's pieces lie: first columns (a < 0: no piece), whether they are turned, and
+// the first of their pairs (interleaved pieces of two pairs a column: of a's; b's first is
+// D / 4 further).
 template <int V, int NS>
 struct Lane {
-  int a[NS], b[NS];  // first columns; a < 0: no piece
+  int a[NS], b[NS], pair[NS];
   bool on[NS];
-  uint64_t turn[NS][V];
 };
 
 template <int V, int NS>
-__device__ __forceinline__ void set_lane(const QkDims& d, const float* freq, int sl, int lph,
-                                         Lane<V, NS>* L) {
+__device__ __forceinline__ void set_lane(const QkDims& d, int sl, int lph, Lane<V, NS>* L) {
   const int pieces = V > 1 ? d.D / (2 * V) : (d.R >> 1) + ((d.D - d.R + 1) >> 1);
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
@@ -122,17 +122,49 @@ __device__ __forceinline__ void set_lane(const QkDims& d, const float* freq, int
     L->on[n] = false;
     if (s < pieces) columns<V>(d, s, &L->a[n], &L->b[n], &L->on[n]);
     if (d.R == 0) L->on[n] = false;
+    L->pair[n] = V > 1 && d.interleaved ? s * V / 2 : s * V;
+  }
+}
+
+// Shared memory: what a frequency turns a step by, the weights (1 where there are none),
+// and for each warp its token's sines and cosines.  Pairs that do not turn (columns from
+// R on of interleaved pieces) have sine 0 and cosine 1.
+struct QkSmem {
+  uint64_t* turn;
+  float *w, *rot;
+  int pairs;  // a multiple of 4
+};
+__host__ __device__ inline int qk_pairs(int D) { return (D / 2 + 3) / 4 * 4; }
+__host__ __device__ inline size_t qk_smem(int D, int R) {
+  return (R ? (size_t)qk_pairs(D) * (8 + kQkWarps * 8) : 0) + (size_t)2 * ((D + 3) / 4 * 4) * 4;
+}
+__device__ __forceinline__ QkSmem qk_tables(const QkDims& d, unsigned char* smem, const float* freq,
+                                            const float* w_q, const float* w_k) {
+  QkSmem m;
+  m.pairs = qk_pairs(d.D);
+  m.w = reinterpret_cast<float*>(smem);
+  const int dw = (d.D + 3) / 4 * 4;
+  m.turn = reinterpret_cast<uint64_t*>(m.w + 2 * dw);
+  m.rot = reinterpret_cast<float*>(m.turn + m.pairs) + (threadIdx.x >> 5) * 2 * m.pairs;
+  for (int i = threadIdx.x; i < d.D; i += kQkThreads) {
+    m.w[i] = w_q ? w_q[i] : 1.f;
+    m.w[dw + i] = w_k ? w_k[i] : 1.f;
+  }
+  if (d.R)
+    for (int i = threadIdx.x; i < m.pairs; i += kQkThreads)
+      m.turn[i] = 2 * i < d.R ? turns(freq[i]) : 0;
+  return m;
+}
+// V values from p on, in pieces of up to 4 (p is then 16-byte aligned).
+template <int V>
+__device__ __forceinline__ void from_table(const float* p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = p[0];
+  } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      L->turn[n][j] = 0;
-      if (L->on[n]) {
-        if (V > 1 && d.interleaved) {  // pairs (a + 2 j, + 1), then (b + 2 j, + 1)
-          const int c = j < V / 2 ? L->a[n] + 2 * j : L->b[n] + 2 * (j - V / 2);
-          if (c < d.R) L->turn[n][j] = turns(freq[c >> 1]);
-        } else {
-          L->turn[n][j] = turns(freq[s * V + j]);
-        }
-      }
+    for (int j = 0; j < V; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + j);
+      f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
     }
   }
 }
@@ -141,12 +173,6 @@ template <typename T, int V>
 __device__ __forceinline__ void store_piece(T* p, int c, const float (&f)[V]) {
   if (c >= 0) st_raw<T, V>(p + c, pack<T, V>(f));
 }
-template <int V>
-__device__ __forceinline__ void load_weight(const float* w, int c, float (&f)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) f[j] = w && c >= 0 ? w[c + j] : 1.f;
-}
-
 // (a, b) turned: by the angle (DIR 1) or back (DIR -1).
 template <int DIR, int V>
 __device__ __forceinline__ void turn(bool inter, const float (&sn)[V], const float (&cs)[V],
@@ -200,34 +226,53 @@ struct Row {
   }
 };
 
-// The weights of queries and keys in a lane's columns.
+// The weights of queries (kind 0) or keys in a lane's columns.
 template <int V, int NS>
-struct Weights {
-  float a[2][NS][V], b[2][NS][V];
-  __device__ __forceinline__ void load(const float* w_q, const float* w_k, const Lane<V, NS>& L) {
+__device__ __forceinline__ void weights(const QkDims& d, const QkSmem& m, const Lane<V, NS>& L, int kind,
+                                        float (&wa)[NS][V], float (&wb)[NS][V]) {
+  const float* w = m.w + kind * ((d.D + 3) / 4 * 4);
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      load_weight<V>(w_q, L.a[n], a[0][n]);
-      load_weight<V>(w_q, L.b[n], b[0][n]);
-      load_weight<V>(w_k, L.a[n], a[1][n]);
-      load_weight<V>(w_k, L.b[n], b[1][n]);
-    }
+  for (int n = 0; n < NS; ++n) {
+    from_table<V>(w + max(L.a[n], 0), wa[n]);
+    from_table<V>(w + max(L.b[n], 0), wb[n]);
   }
-};
+}
 
-// The sines and cosines of a token in a lane's columns.
+// The sines and cosines of a token in a lane's columns: each formed by one lane of the
+// warp, handed on through shared memory.
 template <int V, int NS>
-__device__ __forceinline__ void rotations(const QkDims& d, const Lane<V, NS>& L, int pos,
+__device__ __forceinline__ void rotations(const QkDims& d, const QkSmem& m, const Lane<V, NS>& L, int pos,
                                           float (&sn)[NS][V], float (&cs)[NS][V]) {
-  if (d.R > 0)
+  if (d.R == 0) return;
+  __syncwarp();  // the last token's are read
+  for (int i = threadIdx.x & 31; i < m.pairs; i += 32) {
+    float a = 0.f, b = 1.f;
+    if (2 * i < d.R) rotation(m.turn[i], pos, &a, &b);
+    m.rot[i] = a;
+    m.rot[m.pairs + i] = b;
+  }
+  __syncwarp();
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+  for (int n = 0; n < NS; ++n)
+    if (L.on[n]) {
+      if constexpr (V > 1) {
+        if (d.interleaved) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) rotation(L.turn[n][j], pos, &sn[n][j], &cs[n][j]);
+          for (int j = 0; j < V / 2; ++j) {
+            const int i = L.pair[n] + j, k = i + (d.D >> 2);
+            sn[n][j] = m.rot[i], cs[n][j] = m.rot[m.pairs + i];
+            sn[n][V / 2 + j] = m.rot[k], cs[n][V / 2 + j] = m.rot[m.pairs + k];
+          }
+          continue;
+        }
+      }
+      from_table<V>(m.rot + L.pair[n], sn[n]);
+      from_table<V>(m.rot + m.pairs + L.pair[n], cs[n]);
+    }
 }
 
 template <typename T, typename TO, int V, int LPH, int NS>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, NS == 1 ? 6 : 1)
     k_qk_norm_fwd(QkDims d, const T* __restrict__ q, const T* __restrict__ k,
                   const float* __restrict__ w_q, const float* __restrict__ w_k,
                   const float* __restrict__ freq, const int* __restrict__ positions,
@@ -236,10 +281,11 @@ __global__ void __launch_bounds__(kQkThreads)
   const int lane = threadIdx.x & 31, seg = lane / LPH, sl = lane % LPH;
   const int step = gridDim.x * kQkWarps;
   const bool inter = d.interleaved != 0;
+  extern __shared__ __align__(16) unsigned char tables[];
   Lane<V, NS> L;
-  set_lane<V, NS>(d, freq, sl, LPH, &L);
-  Weights<V, NS> W;
-  W.load(w_q, w_k, L);
+  set_lane<V, NS>(d, sl, LPH, &L);
+  const QkSmem m = qk_tables(d, tables, freq, w_q, w_k);
+  __syncthreads();
   for (int64_t u = (int64_t)blockIdx.x * kQkWarps + (threadIdx.x >> 5); u < d.units; u += step) {
     const Unit x = unit(d, (int)u, positions);
     float sn[NS][V], cs[NS][V];
@@ -252,7 +298,9 @@ __global__ void __launch_bounds__(kQkThreads)
       TO* out = kind ? k_out + (int64_t)x.row * d.HK * d.D : q_out + (int64_t)x.row * d.HQ * d.D;
       Row<T, V, NS> next;
       next.load(in + (int64_t)min(lo + seg, hi - 1) * d.D, L);
-      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, L, x.pos, sn, cs);
+      float wa[NS][V], wb[NS][V];
+      weights<V, NS>(d, m, L, kind, wa, wb);
+      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, m, L, x.pos, sn, cs);
       for (int h = lo + seg; h - seg < hi; h += HP) {
         const Row<T, V, NS> now = next;  // the next head's row is on its way
         if (h + HP - seg < hi) next.load(in + (int64_t)min(h + HP, hi - 1) * d.D, L);
@@ -272,8 +320,8 @@ __global__ void __launch_bounds__(kQkThreads)
         for (int n = 0; n < NS; ++n) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            a[n][j] *= rs * W.a[kind][n][j];
-            b[n][j] *= rs * W.b[kind][n][j];
+            a[n][j] *= rs * wa[n][j];
+            b[n][j] *= rs * wb[n][j];
           }
           if (L.on[n]) turn<1, V>(inter, sn[n], cs[n], a[n], b[n]);
           if (h < hi) {
@@ -288,19 +336,22 @@ __global__ void __launch_bounds__(kQkThreads)
 
 // part (gridDim.x, 2, D): each block's sums of dw_q and dw_k.
 template <typename T, typename TO, int V, int LPH, int NS>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, NS == 1 ? 4 : 1)
     k_qk_norm_bwd(QkDims d, const T* __restrict__ q, const T* __restrict__ k,
                   const float* __restrict__ w_q, const float* __restrict__ w_k,
                   const float* __restrict__ freq, const int* __restrict__ positions,
                   const T* __restrict__ dqo, const T* __restrict__ dko, TO* __restrict__ dq,
                   TO* __restrict__ dk, float* __restrict__ part) {
-  extern __shared__ float sums[];  // (warps, 2, D)
+  extern __shared__ __align__(16) unsigned char tables[];
+  float* const sums = reinterpret_cast<float*>(tables + qk_smem(d.D, d.R));  // (warps, 2, D)
   const int lane = threadIdx.x & 31, seg = lane / LPH, sl = lane % LPH, warp = threadIdx.x >> 5;
   constexpr int HP = 32 / LPH;
   const int step = gridDim.x * kQkWarps;
   const bool inter = d.interleaved != 0;
   Lane<V, NS> L;
-  set_lane<V, NS>(d, freq, sl, LPH, &L);
+  set_lane<V, NS>(d, sl, LPH, &L);
+  const QkSmem tb = qk_tables(d, tables, freq, w_q, w_k);
+  __syncthreads();
   float ga[2][NS][V], gb[2][NS][V];  // sums of dw
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind)
@@ -308,8 +359,6 @@ __global__ void __launch_bounds__(kQkThreads)
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int j = 0; j < V; ++j) ga[kind][n][j] = gb[kind][n][j] = 0.f;
-  Weights<V, NS> W;
-  W.load(w_q, w_k, L);
   for (int64_t u = (int64_t)blockIdx.x * kQkWarps + warp; u < d.units; u += step) {
     const Unit x = unit(d, (int)u, positions);
     float sn[NS][V], cs[NS][V];
@@ -325,7 +374,9 @@ __global__ void __launch_bounds__(kQkThreads)
       Row<T, V, NS> nx, ng;
       nx.load(in + (int64_t)min(lo + seg, hi - 1) * d.D, L);
       ng.load(up + (int64_t)min(lo + seg, hi - 1) * d.D, L);
-      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, L, x.pos, sn, cs);
+      float wa[NS][V], wb[NS][V];
+      weights<V, NS>(d, tb, L, kind, wa, wb);
+      if (kind == 0 || x.h0 >= d.HQ) rotations<V, NS>(d, tb, L, x.pos, sn, cs);
       for (int h = lo + seg; h - seg < hi; h += HP) {
         const Row<T, V, NS> cx = nx, cg = ng;  // the next head's rows are on their way
         if (h + HP - seg < hi) {
@@ -343,7 +394,7 @@ __global__ void __launch_bounds__(kQkThreads)
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             ss = fmaf(a[n][j], a[n][j], fmaf(b[n][j], b[n][j], ss));
-            dot = fmaf(a[n][j] * W.a[kind][n][j], g[n][j], fmaf(b[n][j] * W.b[kind][n][j], f[n][j], dot));
+            dot = fmaf(a[n][j] * wa[n][j], g[n][j], fmaf(b[n][j] * wb[n][j], f[n][j], dot));
           }
         }
 #pragma unroll
@@ -361,8 +412,8 @@ __global__ void __launch_bounds__(kQkThreads)
           for (int j = 0; j < V; ++j) {
             ga[kind][n][j] = fmaf(g[n][j], a[n][j] * keep, ga[kind][n][j]);
             gb[kind][n][j] = fmaf(f[n][j], b[n][j] * keep, gb[kind][n][j]);
-            a[n][j] = rs * fmaf(-a[n][j], m, g[n][j] * W.a[kind][n][j]);
-            b[n][j] = rs * fmaf(-b[n][j], m, f[n][j] * W.b[kind][n][j]);
+            a[n][j] = rs * fmaf(-a[n][j], m, g[n][j] * wa[n][j]);
+            b[n][j] = rs * fmaf(-b[n][j], m, f[n][j] * wb[n][j]);
           }
           if (h < hi) {
             store_piece<TO, V>(to, L.a[n], a[n]);
@@ -400,21 +451,23 @@ __global__ void __launch_bounds__(kQkThreads)
   }
 }
 
-// dw_q and dw_k: 32 columns a block, 8 ranges of the blocks' sums, in a fixed order.
-__global__ void __launch_bounds__(256)
+// dw_q and dw_k: 32 columns a block, 32 ranges of the blocks' sums, in a fixed order.
+__global__ void __launch_bounds__(1024)
     k_qk_norm_dw(const float* __restrict__ part, int blocks, int D, float* __restrict__ dw_q,
                  float* __restrict__ dw_k) {
-  __shared__ float s[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  __shared__ float s[32][32];
+  const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
   float a = 0.f;
-  if (c < 2 * D)
-    for (int i = r; i < blocks; i += 8) a += part[(int64_t)i * 2 * D + c];
-  s[r][threadIdx.x & 31] = a;
+  if (c < 2 * D) {
+#pragma unroll 8
+    for (int i = r; i < blocks; i += 32) a += part[(int64_t)i * 2 * D + c];
+  }
+  s[r][lane] = a;
   __syncthreads();
   if (r == 0 && c < 2 * D) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += s[i][threadIdx.x & 31];
+    for (int i = 0; i < 32; ++i) a += s[i][lane];
     float* to = c < D ? dw_q : dw_k;
     if (to) to[c < D ? c : c - D] = a;
   }
@@ -493,7 +546,7 @@ int qk_launch(QkDims d, const QkPtrs& p, bool bwd, cudaStream_t s) {
     const int64_t most = (int64_t)sm_count() * kFwdBlocksPerSm;
     blocks = blocks < most ? blocks : most;
     SSD_LAUNCH("k_qk_norm_fwd", s,
-               k_qk_norm_fwd<T, TO, V, LPH, NS><<<(unsigned)blocks, kQkThreads, 0, s>>>(
+               k_qk_norm_fwd<T, TO, V, LPH, NS><<<(unsigned)blocks, kQkThreads, qk_smem(d.D, d.R), s>>>(
                    d, q, k, p.w_q, p.w_k, p.freq, p.positions, static_cast<TO*>(p.q_out),
                    static_cast<TO*>(p.k_out)));
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
@@ -501,15 +554,20 @@ int qk_launch(QkDims d, const QkPtrs& p, bool bwd, cudaStream_t s) {
   const int64_t most = bwd_blocks(d);
   blocks = blocks < most ? blocks : most;
   float* part = p.w_q || p.w_k ? p.part : nullptr;
+  const size_t smem = qk_smem(d.D, d.R) + (part ? kQkWarps * 2 * d.D * sizeof(float) : 0);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(k_qk_norm_bwd<T, TO, V, LPH, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return SSD_ERR_CUDA;
   SSD_LAUNCH("k_qk_norm_bwd", s,
              k_qk_norm_bwd<T, TO, V, LPH, NS>
-             <<<(unsigned)blocks, kQkThreads, part ? kQkWarps * 2 * d.D * sizeof(float) : 0, s>>>(
+             <<<(unsigned)blocks, kQkThreads, smem, s>>>(
                  d, q, k, p.w_q, p.w_k, p.freq, p.positions, static_cast<const T*>(p.dqo),
                  static_cast<const T*>(p.dko), static_cast<TO*>(p.dq), static_cast<TO*>(p.dk), part));
   if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
   if (!part) return SSD_OK;
   SSD_LAUNCH("k_qk_norm_dw", s,
-             k_qk_norm_dw<<<(unsigned)((2 * d.D + 31) / 32), 256, 0, s>>>(part, (int)blocks, d.D,
+             k_qk_norm_dw<<<(unsigned)((2 * d.D + 31) / 32), 1024, 0, s>>>(part, (int)blocks, d.D,
                                                                           p.dw_q, p.dw_k));
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
