@@ -48,10 +48,11 @@ struct DeltaDims {
   int NP;   // key columns in the workspace: 64 or 128
   int ip;   // planes of the images of keys and queries
   int nb;   // head blocks of a group in the gradient
+  int sms;  // SMs of the device
   float scale;
   int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
   int vq, vk, vv, vdy;             // whether rows can be read 16 bytes at a time
-  int wide;                        // whether pairs of output columns can be written at once
+  int wide, wide_k;                // whether pairs of y's or dv's, of dq's and dk's columns can be written at once
 };
 
 // Gates of a chunk's tokens: the log2 decays' running sum G in two floats, b, and what
@@ -221,6 +222,10 @@ constexpr int image_planes() { return sizeof(T) == 2 ? 1 : 2; }
 // A raw tile of tokens x 64 value columns, as it is, for reads element by element.
 template <typename T>
 constexpr int raw_pitch() { return sizeof(T) == 2 ? kTP : kF; }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 struct Place {  // the (batch, head, chunk) of a block
   int b, h, c;
   int64_t i;  // (b * H + h) * nc + c
@@ -1207,18 +1212,54 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     cp_commit();
   }
 
-  for (int h = h0; h < h1; ++h) {
-    const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
-    if (rv == 0) {  // padding only
+  if (rv == 0) {  // padding only
+    for (int h = h0; h < h1; ++h) {
       for (int i = tid; i < rows * d.P; i += kGradThreads)
         dv[(tok + i / d.P) * ys + (int64_t)h * d.P + i % d.P] = from_f<TO>(0.f);
       if (tid < rows) {
         ddt[(tok + tid) * d.H + h] = from_f<TO>(0.f);
         dbeta[(tok + tid) * d.H + h] = from_f<TO>(0.f);
       }
-      if (tid < 2) w.part[at * 2 + tid] = 0.f;
-      continue;
+      if (tid < 2) w.part[(((int64_t)b * d.H + h) * d.nc + c) * 2 + tid] = 0.f;
     }
+  }
+  // the next tile's values are fetched into L2 while this one's products run: of this
+  // head, of the block's next head, or of the first head of the block that is likely next
+  auto ahead = [&](int64_t at, int p0) {
+    const size_t pt = (size_t)(at * d.Ps + p0);
+    const int pr = min(kC, d.Ps - p0), sl = pr * NP / 32, tl = pr * kC / 32;  // lines of 128 bytes
+    for (int i = tid; i < 2 * sl + 4 * tl; i += kGradThreads) {
+      const int m = i < 2 * sl ? i / sl : 2 + (i - 2 * sl) / tl, l = i < 2 * sl ? i % sl : (i - 2 * sl) % tl;
+      const float* from = m == 0 ? w.S0 : m == 1 ? w.dS : m == 2 ? w.dR : m == 3 ? w.U : m == 4 ? w.Zd : w.Zb;
+      prefetch_l2(from + pt * (m < 2 ? NP : kC) + l * 32);
+    }
+  };
+  auto ahead_of = [&](int h, int p0) {
+    if (p0 + kC < d.Ps) {
+      ahead(((int64_t)b * d.H + h) * d.nc + c, p0 + kC);
+    } else if (h + 1 < h1) {
+      ahead(((int64_t)b * d.H + h + 1) * d.nc + c, 0);
+    } else if (blockIdx.x + d.sms < gridDim.x) {
+      int64_t nb = blockIdx.x + d.sms;
+      const int c2 = (int)(nb % d.nc);
+      nb /= d.nc;
+      const int hb2 = (int)(nb % d.nb);
+      nb /= d.nb;  // batch * groups + group
+      const int h2 = (int)(nb % d.G) * d.rep + (int)((int64_t)d.rep * hb2 / d.nb);
+      ahead(((nb / d.G) * d.H + h2) * d.nc + c2, 0);
+    }
+  };
+
+  for (int h = h0; h < h1 && rv > 0; ++h) {
+    const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
+    // the gates' inputs of the two tokens of a lane of the first warp, for the head's end
+    float zt[2] = {0.f, 0.f};
+    if (warp == 0)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (2 * lane + x < rv)
+          zt[x] = to_f(dt[(tok + 2 * lane + x) * d.H + h]) + (dt_bias ? dt_bias[h] : 0.f);
+    const float Ah = A[h];
     float da[2][4], wm[2][4], dqh[HT][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -1259,16 +1300,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       cp_wait<0>();
       __syncthreads();
       ws.load(w.dS + pt * NP, pr);  // on its way under the products
-      for (int i = tid; i < rows * kC; i += kGradThreads) {  // dv = b dR
-        const int t = i / kC, p = i % kC;
-        if (p0 + p < d.P) {
-          float v = 0.f;
-          if (t < rv)
-#pragma unroll
-            for (int l = 2; l >= 0; --l) v += to_f(rt[l * kC * kTP + p * kTP + t]);
-          dv[(tok + t) * ys + (int64_t)h * d.P + p0 + p] = from_f<TO>(v * g.b[t]);
-        }
-      }
+      ahead_of(h, p0);
       const float sx0 = -g.b[r0] * ex2(g.gh[r0]), sx1 = -g.b[r0 + 8] * ex2(g.gh[r0 + 8]);
       const float sk0 = decay_between(g, kC - 1, r0), sk1 = decay_between(g, kC - 1, r0 + 8);
       // a left operand of three planes with its rows scaled, as NL planes
@@ -1296,6 +1328,21 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int l = 0; l < 3; ++l) a_cols<kTP>(ra[l], rt + l * kC * kTP, strip * 16, kb * 16, lane);
         scaled(xa, ra, sx0, sx1);
+        if (kb == part) {  // dv = b dR: 16 of the value columns a warp
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = r0 + (e & 1) * 8, p = p0 + kb * 16 + (e >> 1) * 8 + c0;
+            float lo = 0.f, hi = 0.f;
+#pragma unroll
+            for (int l = 2; l >= 0; --l) {
+              lo += __uint_as_float(ra[l][e] << 16);
+              hi += __uint_as_float(ra[l][e] & 0xffff0000u);
+            }
+            if (i < rows && p < d.P)  // (rows from rv on are zeros)
+              lm::st_two(dv + (tok + i) * ys + (int64_t)h * d.P + p,
+                         make_float2(lo * g.b[i], hi * g.b[i]), p + 1 < d.P, d.wide);
+          }
+        }
         if (part <= strip) {
           auto ub = [&](int j, uint32_t(&x)[4]) {
             b_cols<kTP>(x, ut + j * kC * kTP, part * 16, kb * 16, lane);
@@ -1529,9 +1576,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const float v = dg[x] + after;
         const int64_t o = (tok + i) * d.H + h;
         if (i < rv) {
-          const float z = to_f(dt[o]) + (dt_bias ? dt_bias[h] : 0.f);
-          const float dz = v * A[h] * sigmoid(z);
-          sa = fmaf(v, softplus(z), sa);
+          const float dz = v * Ah * sigmoid(zt[x]);
+          sa = fmaf(v, softplus(zt[x]), sa);
           sb += dz;
           ddt[o] = from_f<TO>(dz);
           dbeta[o] = from_f<TO>((1.f - g.b[i]) * wii[x]);
@@ -1549,20 +1595,24 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
   }
   // padding rows are zeros: their keys, queries, corrections and gradients are
+  const int64_t row = ((int64_t)b * d.T + t0 + r0) * d.G + grp, whole = (int64_t)d.B * d.T * d.G * d.N;
 #pragma unroll
-  for (int t = 0; t < HT; ++t)
+  for (int e2 = 0; e2 < 2; ++e2)
+    if (r0 + 8 * e2 < rows) {
+      const int64_t o = (row + (int64_t)8 * e2 * d.G) * d.N;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = r0 + (e >> 1) * 8, j = part * WC + 8 * t + c0 + (e & 1);
-      if (i < rows && j < d.N) {
-        const int64_t o = (((int64_t)b * d.T + t0 + i) * d.G + grp) * d.N + j;
-        if (d.nb == 1) {
-          dq[o] = from_f<TO>(tq[t][e]);
-          dk[o] = from_f<TO>(tk[t][e]);
-        } else {
-          const int64_t whole = (int64_t)d.B * d.T * d.G * d.N;
-          w.dqp[hb * whole + o] = tq[t][e];
-          w.dkp[hb * whole + o] = tk[t][e];
+      for (int t = 0; t < HT; ++t) {
+        const int j = part * WC + 8 * t + c0;
+        const float2 vq = make_float2(tq[t][2 * e2], tq[t][2 * e2 + 1]);
+        const float2 vk = make_float2(tk[t][2 * e2], tk[t][2 * e2 + 1]);
+        if (j < d.N) {
+          if (d.nb == 1) {
+            lm::st_two(dq + o + j, vq, j + 1 < d.N, d.wide_k);
+            lm::st_two(dk + o + j, vk, j + 1 < d.N, d.wide_k);
+          } else {
+            lm::st_two(w.dqp + hb * whole + o + j, vq, j + 1 < d.N, d.N % 2 == 0);
+            lm::st_two(w.dkp + hb * whole + o + j, vk, j + 1 < d.N, d.N % 2 == 0);
+          }
         }
       }
     }
@@ -1855,7 +1905,10 @@ int ssd_gated_delta_bwd(const ssd_delta_shape* shape, const void* q, const void*
       off(dv, o) || off(ddt, o) || off(dbeta, o) || off(dA, 4) || off(ddt_bias, 4) ||
       off(dfinal_states, 4) || off(dinit_states, 4))
     return SSD_ERR_INVALID_ARG;
+  d.wide = d.P % 2 == 0 && !off(dv, 2 * o);
+  d.wide_k = d.N % 2 == 0 && !off(dq, 2 * o) && !off(dk, 2 * o);
   d.vdy = rows16(dy, e, d.P, (int64_t)d.H * d.P, (int64_t)d.T * d.H * d.P);
+  d.sms = sm_count();
   const DeltaWs w = delta_ws(d, workspace, true);
   if ((st = check_ws(w, workspace, workspace_bytes)) != SSD_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
