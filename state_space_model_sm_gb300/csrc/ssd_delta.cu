@@ -1225,14 +1225,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   // the next tile's values are fetched into L2 while this one's products run: of this
   // head, of the block's next head, or of the first head of the block that is likely next
+  // (a warp four rows of lines of the states, eight of the others)
   auto ahead = [&](int64_t at, int p0) {
     const size_t pt = (size_t)(at * d.Ps + p0);
-    const int pr = min(kC, d.Ps - p0), sl = pr * NP / 32, tl = pr * kC / 32;  // lines of 128 bytes
-    for (int i = tid; i < 2 * sl + 4 * tl; i += kGradThreads) {
-      const int m = i < 2 * sl ? i / sl : 2 + (i - 2 * sl) / tl, l = i < 2 * sl ? i % sl : (i - 2 * sl) % tl;
-      const float* from = m == 0 ? w.S0 : m == 1 ? w.dS : m == 2 ? w.dR : m == 3 ? w.U : m == 4 ? w.Zd : w.Zb;
-      prefetch_l2(from + pt * (m < 2 ? NP : kC) + l * 32);
-    }
+    const int pr = min(kC, d.Ps - p0), m = warp < 8 ? warp >> 2 : 2 + ((warp - 8) >> 1);
+    const float* from = m == 0 ? w.S0 : m == 1 ? w.dS : m == 2 ? w.dR : m == 3 ? w.U : m == 4 ? w.Zd : w.Zb;
+    const int cols = m < 2 ? NP : kC, lines = pr * cols / 32;
+    const int l0 = (m < 2 ? warp & 3 : warp & 1) * 64 + lane;
+    from += pt * cols;
+#pragma unroll
+    for (int l = l0; l < l0 + 64; l += 32)
+      if (l < lines) prefetch_l2(from + l * 32);
   };
   auto ahead_of = [&](int h, int p0) {
     if (p0 + kC < d.Ps) {
@@ -1240,13 +1243,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     } else if (h + 1 < h1) {
       ahead(((int64_t)b * d.H + h + 1) * d.nc + c, 0);
     } else if (blockIdx.x + d.sms < gridDim.x) {
-      int64_t nb = blockIdx.x + d.sms;
-      const int c2 = (int)(nb % d.nc);
-      nb /= d.nc;
-      const int hb2 = (int)(nb % d.nb);
-      nb /= d.nb;  // batch * groups + group
-      const int h2 = (int)(nb % d.G) * d.rep + (int)((int64_t)d.rep * hb2 / d.nb);
-      ahead(((nb / d.G) * d.H + h2) * d.nc + c2, 0);
+      const unsigned i = blockIdx.x + d.sms, j = i / d.nc, k = j / d.nb, l = k / d.G;
+      const int h2 = (int)(k - l * d.G) * d.rep + (int)((int64_t)d.rep * (j - k * d.nb) / d.nb);
+      ahead(((int64_t)l * d.H + h2) * d.nc + (i - j * d.nc), 0);
     }
   };
 
@@ -1284,9 +1283,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       __syncthreads();  // the tiles (and, at a head's start, the gates and sums) are read
       fetch_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
                                            d.vdy);
-      cp_commit();
       if (p0 == 0 && tid < kGateCopies)
-        reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + at)[tid];
+        cp_async<16>(reinterpret_cast<uint4*>(&g) + tid, reinterpret_cast<const uint4*>(w.gates + at) + tid);
+      cp_commit();
       ws.template store<3>(st);
       wr.template store<3>(rt);
       wu.template store<3>(ut);
@@ -1320,7 +1319,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           for (int l = 0; l < NL; ++l) a[l][e] = pp[l];
         }
       };
-#pragma unroll
+#pragma unroll 1  // (the code of one pass; four would miss the instruction cache)
       for (int kb = 0; kb < 4; ++kb) {
         uint32_t ya[NI][4], ra[3][4], xa[NL][4];
 #pragma unroll
@@ -1378,7 +1377,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       ws.template store<NL>(st);
       __syncthreads();
-#pragma unroll
+#pragma unroll 1  // (the code of one pass; four would miss the instruction cache)
       for (int kb = 0; kb < 4; ++kb) {
         uint32_t ua[3][4], xa[NL][4];
 #pragma unroll
@@ -1420,7 +1419,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) qk[t][e] = kk[t][e] = 0.f;
       if (part <= strip)
-#pragma unroll
+#pragma unroll 2
         for (int x = 0; x < NP / 16; ++x) {
           uint32_t qa[NI][4], ka[NI][4];
 #pragma unroll
@@ -1502,7 +1501,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if ((lane & 3) == 0) sm.qd[part][r0] = s0, sm.qd[part][r0 + 8] = s1;
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t a[NL][4], a2[NL][4];
       if (kb <= strip) {
