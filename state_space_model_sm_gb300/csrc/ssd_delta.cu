@@ -106,6 +106,7 @@ __device__ __forceinline__ void load_tile(bf16* dst, const T* src, int64_t ld, i
                                           bool vec) {
   if constexpr (sizeof(T) == 2) {
     if (vec) {
+#pragma unroll 1
       for (int i = threadIdx.x; i < kC * (W / 8); i += THREADS) {
         const int r = i / (W / 8), c = i % (W / 8) * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -113,12 +114,14 @@ __device__ __forceinline__ void load_tile(bf16* dst, const T* src, int64_t ld, i
         *reinterpret_cast<uint4*>(dst + r * LD + c) = v;
       }
     } else {
+#pragma unroll 1
       for (int i = threadIdx.x; i < kC * W; i += THREADS) {
         const int r = i / W, c = i % W;
         dst[r * LD + c] = r < rv && c < cv ? src[r * ld + c] : from_f<bf16>(0.f);
       }
     }
   } else {
+#pragma unroll 2
     for (int i = threadIdx.x; i < kC * (W / 4); i += THREADS) {
       const int r = i / (W / 4), c = i % (W / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -194,11 +197,14 @@ struct WsTile {
 // As load_tile, started asynchronously: bf16 rows with vec.
 template <int W, int LD, int THREADS>
 __device__ __forceinline__ void copy_tile(bf16* dst, const bf16* src, int64_t ld, int rv, int cv) {
-  for (int i = threadIdx.x; i < kC * (W / 8); i += THREADS) {
-    const int r = i / (W / 8), c = i % (W / 8) * 8;
-    bf16* to = dst + r * LD + c;
-    if (r < rv && c < cv)
-      cp_async<16>(to, src + r * ld + c);
+  constexpr int STEP = THREADS / (W / 8);  // rows between a thread's pieces
+  const int r0 = threadIdx.x / (W / 8), c = threadIdx.x % (W / 8) * 8;
+  const bf16* from = src + r0 * ld + c;
+  bf16* to = dst + r0 * LD + c;
+#pragma unroll
+  for (int r = 0; r < kC; r += STEP, from += STEP * ld, to += STEP * LD) {
+    if (r + r0 < rv && c < cv)
+      cp_async<16>(to, from);
     else
       *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
   }
@@ -222,21 +228,22 @@ constexpr int image_planes() { return sizeof(T) == 2 ? 1 : 2; }
 // A raw tile of tokens x 64 value columns, as it is, for reads element by element.
 template <typename T>
 constexpr int raw_pitch() { return sizeof(T) == 2 ? kTP : kF; }
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+// Bytes (a multiple of 16) from p on into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 struct Place {  // the (batch, head, chunk) of a block
   int b, h, c;
   int64_t i;  // (b * H + h) * nc + c
 };
-__device__ __forceinline__ Place place(const DeltaDims& d, int64_t block) {
+__device__ __forceinline__ Place place(const DeltaDims& d, unsigned block) {
   Place p;
+  const unsigned bh = block / (unsigned)d.nc;
   p.i = block;
-  p.c = (int)(block % d.nc);
-  const int64_t bh = block / d.nc;
-  p.h = (int)(bh % d.H);
-  p.b = (int)(bh / d.H);
+  p.c = (int)(block - bh * d.nc);
+  p.b = (int)(bh / (unsigned)d.H);
+  p.h = (int)(bh - (unsigned)p.b * d.H);
   return p;
 }
 
@@ -252,6 +259,7 @@ __device__ __forceinline__ void lower_product(float (&acc)[8][4], const bf16* A,
   for (int t = 0; t < 8; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+#pragma unroll 2
   for (int kk = 0; kk < NP / 16; ++kk) {
     uint32_t a[NI][4];
 #pragma unroll
@@ -296,7 +304,7 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
     }
   };
   float m = 0.f;
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < W; c += 8) {
     float f[8];
     piece(c, f);
@@ -306,7 +314,7 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const Scale s = scale_of(m);
   if (to) {
-#pragma unroll
+#pragma unroll 2
     for (int c = 0; c < W; c += 8) {
       float f[8];
       piece(c, f);
@@ -550,14 +558,14 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
         for (int t = 0; t < 8; ++t)
 #pragma unroll
           for (int x = 0; x < 4; ++x) e[t][x] = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int kb = 0; kb < 4; ++kb) {
           uint32_t a[NI][4];
 #pragma unroll
           for (int p = 0; p < NI; ++p) a_cols<kTP>(a[p], yt + p * kC * kTP, strip * 16, kb * 16, lane);
 #pragma unroll
-          for (int np = 0; np <= kb; ++np)
-            mma_planes<NI, 3, 3>(e[2 * np], e[2 * np + 1], a, [&](int j, uint32_t(&r)[4]) {
+          for (int np = 0; np < 4; ++np)
+            if (np <= kb) mma_planes<NI, 3, 3>(e[2 * np], e[2 * np + 1], a, [&](int j, uint32_t(&r)[4]) {
               b_cols<kTP>(r, at + j * kC * kTP, np * 16, kb * 16, lane);
             });
         }
@@ -715,10 +723,10 @@ __global__ void __launch_bounds__(kChainThreads)
   extern __shared__ __align__(16) unsigned char smem[];
   ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const int ptiles = (d.Ps + kC - 1) / kC;
-  const int p0 = (int)(blockIdx.x % ptiles) * kC;
-  const int64_t bh = blockIdx.x / ptiles;
-  const int h = (int)(bh % d.H), b = (int)(bh / d.H);
+  const unsigned ptiles = (d.Ps + kC - 1) / kC, bhu = blockIdx.x / ptiles;
+  const int p0 = (int)(blockIdx.x - bhu * ptiles) * kC, b = (int)(bhu / (unsigned)d.H);
+  const int h = (int)(bhu - (unsigned)b * d.H);
+  const int64_t bh = bhu;
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
   const int strips = min(kChainWarps, (d.Ps - p0) / 16);
   unsigned char* const stages = smem + sizeof(ChainBars);
@@ -874,6 +882,7 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
   TO* const yo = y + (((int64_t)pl.b * d.T + t0) * d.H + pl.h) * d.P;
   const int64_t ys = (int64_t)d.H * d.P;
   if (t0 >= n) {
+#pragma unroll 1
     for (int i = tid; i < rows * d.P; i += kOutThreads) yo[i / d.P * ys + i % d.P] = from_f<TO>(0.f);
     return;
   }
@@ -899,7 +908,7 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
     if (2 * half <= strip)
-#pragma unroll
+#pragma unroll 2
       for (int kk = 0; kk < NP / 16; ++kk) {
         uint32_t a[NI][4];
 #pragma unroll
@@ -943,7 +952,7 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
-#pragma unroll
+#pragma unroll 2
     for (int kk = 0; kk < NP / 16; ++kk) {
       uint32_t a[NI][4];
 #pragma unroll
@@ -956,7 +965,7 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
-#pragma unroll
+#pragma unroll 1
     for (int kb = 0; kb < 4; ++kb)
       if (kb <= strip) {
         uint32_t a[NL][4];
@@ -1004,10 +1013,10 @@ __global__ void __launch_bounds__(kChainThreads)
   extern __shared__ __align__(16) unsigned char smem[];
   ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const int ptiles = (d.Ps + kC - 1) / kC;
-  const int p0 = (int)(blockIdx.x % ptiles) * kC;
-  const int64_t bh = blockIdx.x / ptiles;
-  const int h = (int)(bh % d.H), b = (int)(bh / d.H);
+  const unsigned ptiles = (d.Ps + kC - 1) / kC, bhu = blockIdx.x / ptiles;
+  const int p0 = (int)(blockIdx.x - bhu * ptiles) * kC, b = (int)(bhu / (unsigned)d.H);
+  const int h = (int)(bhu - (unsigned)b * d.H);
+  const int64_t bh = bhu;
   const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
   const int strips = min(kChainWarps, (d.Ps - p0) / 16);
   unsigned char* const stages = smem + sizeof(ChainBars);
@@ -1186,16 +1195,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   bf16* const p1 = SM::beside ? rt : kt + NI * kC * LD;
   bf16* const p2 = p1 + NL * kC * kTP;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, strip = warp & 3, part = warp >> 2;
-  int64_t blk = blockIdx.x;
-  const int c = (int)(blk % d.nc);
-  blk /= d.nc;
-  const int hb = (int)(blk % d.nb);
-  blk /= d.nb;
-  const int grp = (int)(blk % d.G), b = (int)(blk / d.G);
+  const unsigned b1 = blockIdx.x / d.nc, b2 = b1 / d.nb;
+  const int c = (int)(blockIdx.x - b1 * d.nc), hb = (int)(b1 - b2 * d.nb);
+  const int b = (int)(b2 / d.G), grp = (int)(b2 - (unsigned)b * d.G);
   const int n = tokens_of(d, lengths, b), t0 = c * kC, rows = min(kC, d.T - t0);
   const int rv = max(0, min(kC, n - t0));
-  const int h0 = grp * d.rep + (int)((int64_t)d.rep * hb / d.nb);
-  const int h1 = grp * d.rep + (int)((int64_t)d.rep * (hb + 1) / d.nb);
+  const int h0 = grp * d.rep + (int)((unsigned)d.rep * hb / d.nb);
+  const int h1 = grp * d.rep + (int)((unsigned)d.rep * (hb + 1) / d.nb);
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
   const int64_t ys = (int64_t)d.H * d.P, tok = (int64_t)b * d.T + t0;
   const T* const qg = q + b * d.qb + t0 * d.qs + (int64_t)grp * d.N;
@@ -1214,6 +1220,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
   if (rv == 0) {  // padding only
     for (int h = h0; h < h1; ++h) {
+#pragma unroll 1
       for (int i = tid; i < rows * d.P; i += kGradThreads)
         dv[(tok + i / d.P) * ys + (int64_t)h * d.P + i % d.P] = from_f<TO>(0.f);
       if (tid < rows) {
@@ -1225,17 +1232,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   // the next tile's values are fetched into L2 while this one's products run: of this
   // head, of the block's next head, or of the first head of the block that is likely next
-  // (a warp four rows of lines of the states, eight of the others)
   auto ahead = [&](int64_t at, int p0) {
+    if (tid >= 6) return;
     const size_t pt = (size_t)(at * d.Ps + p0);
-    const int pr = min(kC, d.Ps - p0), m = warp < 8 ? warp >> 2 : 2 + ((warp - 8) >> 1);
-    const float* from = m == 0 ? w.S0 : m == 1 ? w.dS : m == 2 ? w.dR : m == 3 ? w.U : m == 4 ? w.Zd : w.Zb;
-    const int cols = m < 2 ? NP : kC, lines = pr * cols / 32;
-    const int l0 = (m < 2 ? warp & 3 : warp & 1) * 64 + lane;
-    from += pt * cols;
-#pragma unroll
-    for (int l = l0; l < l0 + 64; l += 32)
-      if (l < lines) prefetch_l2(from + l * 32);
+    const int cols = tid < 2 ? NP : kC;
+    const float* from = tid == 0 ? w.S0 : tid == 1 ? w.dS : tid == 2 ? w.dR : tid == 3 ? w.U : tid == 4 ? w.Zd : w.Zb;
+    prefetch_l2(from + pt * cols, min(kC, d.Ps - p0) * cols * 4);
   };
   auto ahead_of = [&](int h, int p0) {
     if (p0 + kC < d.Ps) {
@@ -1244,7 +1246,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       ahead(((int64_t)b * d.H + h + 1) * d.nc + c, 0);
     } else if (blockIdx.x + d.sms < gridDim.x) {
       const unsigned i = blockIdx.x + d.sms, j = i / d.nc, k = j / d.nb, l = k / d.G;
-      const int h2 = (int)(k - l * d.G) * d.rep + (int)((int64_t)d.rep * (j - k * d.nb) / d.nb);
+      const int h2 = (int)(k - l * d.G) * d.rep + (int)(d.rep * (j - k * d.nb) / d.nb);
       ahead(((int64_t)l * d.H + h2) * d.nc + (i - j * d.nc), 0);
     }
   };
@@ -1622,6 +1624,7 @@ template <typename TO>
 __global__ void __launch_bounds__(256)
     k_delta_sum(const float* __restrict__ qp, const float* __restrict__ kp, int nb, int64_t n,
                 TO* __restrict__ dq, TO* __restrict__ dk) {
+#pragma unroll 1
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     float a = 0.f, b = 0.f;
     for (int l = 0; l < nb; ++l) a += qp[l * n + i], b += kp[l * n + i];
@@ -1637,9 +1640,13 @@ __global__ void __launch_bounds__(256)
   __shared__ float s[2][8];
   const int h = blockIdx.x;
   float a = 0.f, b = 0.f;
-  for (int64_t i = threadIdx.x; i < (int64_t)B * nc; i += 256) {
-    const float* p = part + ((i / nc * H + h) * nc + i % nc) * 2;
-    a += p[0], b += p[1];
+  for (int n = 0; n < B; ++n) {
+    const float2* p = reinterpret_cast<const float2*>(part) + ((int64_t)n * H + h) * nc;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nc; i += 256) {
+      const float2 v = p[i];
+      a += v.x, b += v.y;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
