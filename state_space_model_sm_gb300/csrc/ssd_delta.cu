@@ -15,7 +15,7 @@
 // Numerics: all matrix products run on the tensor cores with bf16 planes of fp32
 // values (warp_mma.cuh), three planes wherever the result reaches a state, a state's
 // gradient or a parameter's gradient; two where it only reaches a bf16 output.  Log
-// decays are summed in 64 bits and kept as two floats, so that a strong decay early in
+// decays are summed and kept as two floats, so that a strong decay early in
 // a chunk takes nothing from the differences behind it.
 #include <cuda_bf16.h>
 
@@ -341,7 +341,7 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
 // halves of X merged by fp32 products from shared memory the kernel was bound by shared
 // memory, 62 us for 3072 chunks at 88 % of its rate.)
 template <typename T, int NP, bool BWD>
-__global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
+__global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) : 1)
     k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
                  const T* __restrict__ dt, const float* __restrict__ dt_bias,
                  const float* __restrict__ A, const T* __restrict__ beta,
@@ -363,6 +363,15 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
   const int64_t ys = (int64_t)d.H * d.P;
   const T* const yg = BWD ? dy + ((int64_t)pl.b * d.T + t0) * ys + (int64_t)pl.h * d.P : nullptr;
 
+  float zt[2] = {0.f, 0.f}, zb[2] = {0.f, 0.f};  // of two tokens a lane of the first warp
+  if (strip == 0)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (2 * lane + j < rv) {
+        const int64_t at = ((int64_t)pl.b * d.T + t0 + 2 * lane + j) * d.H + pl.h;
+        zt[j] = to_f(dt[at]) + (dt_bias ? dt_bias[pl.h] : 0.f);
+        zb[j] = to_f(beta[at]);
+      }
   fetch_tile<T, NP, LD, kPrepThreads>(Kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
                                       d.N, d.vk);
   if constexpr (BWD)
@@ -373,39 +382,30 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? 4 : 1)
     fetch_tile<T, kC, kTP, kPrepThreads>(yt, yg, ys, rv, d.P, d.vdy);
     cp_commit();
   }
-  if (strip == 0) {  // two tokens a lane
-    double s[2];
-    float bb[2];
+  if (strip == 0) {  // two tokens a lane; sums in two floats, each with its exact rest
+    float bb[2], hi[2], lo[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int i = 2 * lane + j;
-      float g2 = 0.f;
-      bb[j] = 0.f;
-      if (i < rv) {
-        const int64_t at = ((int64_t)pl.b * d.T + t0 + i) * d.H + pl.h;
-        const float delta = softplus(to_f(dt[at]) + (dt_bias ? dt_bias[pl.h] : 0.f));
-        // 2^-150 is 0 in fp32: a bound that changes no decay keeps the sums finite
-        g2 = fmaxf(delta * (A[pl.h] * lm::kLog2e), -150.f);
-        bb[j] = sigmoid(to_f(beta[at]));
-      }
-      s[j] = g2;
+      // 2^-150 is 0 in fp32: a bound that changes no decay keeps the sums finite
+      hi[j] = 2 * lane + j < rv ? fmaxf(softplus(zt[j]) * (A[pl.h] * lm::kLog2e), -150.f) : 0.f;
+      bb[j] = 2 * lane + j < rv ? sigmoid(zb[j]) : 0.f;
     }
-    s[1] += s[0];
-    double run = s[1];
+    auto plus = [](float& h, float& l, float h2, float l2) {
+      const float t = h + h2, z = t - h, e = (h - (t - z)) + (h2 - z) + (l + l2);
+      h = t + e;
+      l = e - (h - t);
+    };
+    plus(hi[1], lo[1], hi[0], lo[0]);
+    float rh = hi[1], rl = lo[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += up;
+      const float h2 = __shfl_up_sync(0xffffffffu, rh, o), l2 = __shfl_up_sync(0xffffffffu, rl, o);
+      if (lane >= o) plus(rh, rl, h2, l2);
     }
-    const double before = run - s[1];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const double v = before + s[j];
-      const float hi = (float)v;
-      g.gh[2 * lane + j] = hi;
-      g.gl[2 * lane + j] = (float)(v - hi);
-      g.b[2 * lane + j] = bb[j];
-    }
+    const float bh = __shfl_up_sync(0xffffffffu, rh, 1), bl = __shfl_up_sync(0xffffffffu, rl, 1);
+    if (lane > 0) plus(hi[0], lo[0], bh, bl);
+    g.gh[2 * lane] = hi[0], g.gl[2 * lane] = lo[0], g.b[2 * lane] = bb[0];
+    g.gh[2 * lane + 1] = rh, g.gl[2 * lane + 1] = rl, g.b[2 * lane + 1] = bb[1];
   }
   cp_wait<BWD ? 1 : 0>();
   __syncthreads();
