@@ -1,10 +1,11 @@
 """A small sequence model of two layers -- one with the selective scan, one with
-the SSD scan -- trained for a few steps and then used to generate.
+the SSD scan, and with --delta a third with the gated delta rule -- trained for a few
+steps and then used to generate.
 
-    python examples/layer_stack.py [--steps 30] [--dtype f32|bf16]
+    python examples/layer_stack.py [--steps 30] [--dtype f32|bf16] [--delta]
 
-Training runs the convolution, both scans, the gated norm and the block norm
-forward and backward (each wrapped as an autograd function below; the
+Training runs the convolution, the scans, the norm of queries and keys, the gated norm
+and the block norm forward and backward (each wrapped as an autograd function below; the
 projections are plain matrix products).  Generation takes a batch of prompts of
 unequal lengths (one of them empty) through the prompt forms, which leave every
 layer's convolution and scan states, and goes on token by token with the
@@ -63,6 +64,33 @@ class SSDScan(torch.autograd.Function):
         t = dy.dtype
         return (g["dx"].to(t), g["ddt"].to(t), g["ddt_bias"], g["dA"], g["dB"].to(t),
                 g["dC"].to(t), g["dD"])
+
+
+class QkNorm(torch.autograd.Function):
+    """Unit queries and keys, turned by their positions."""
+
+    @staticmethod
+    def forward(ctx, q, k, w_q, w_k, freq):
+        ctx.save_for_backward(q, k, w_q, w_k, freq)
+        return ssd.qk_norm_fwd(q, k, w_q, w_k, freq, l2=True)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        q, k, w_q, w_k, freq = ctx.saved_tensors
+        g = ssd.qk_norm_bwd(q, k, w_q, w_k, freq, None, dq.contiguous(), dk.contiguous(), l2=True)
+        return g["dq"], g["dk"], g["dw_q"], g["dw_k"], None
+
+
+class GatedDelta(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, dt, dt_bias, A, beta):
+        ctx.save_for_backward(q, k, v, dt, dt_bias, A, beta)
+        return ssd.gated_delta_fwd(q, k, v, dt, dt_bias, A, beta, return_final_states=False)[0]
+
+    @staticmethod
+    def backward(ctx, dy):
+        g = ssd.gated_delta_bwd(*ctx.saved_tensors, dy.contiguous())
+        return g["dq"], g["dk"], g["dv"], g["ddt"], g["ddt_bias"], g["dA"], g["dbeta"]
 
 
 class GatedNorm(torch.autograd.Function):
@@ -206,17 +234,85 @@ class SSDLayer:
                                   return_rstd=False)[0] @ p["w_out"]
 
 
+class DeltaLayer:
+    """in-projection -> convolution of q, k, v -> unit, turned queries and keys -> gated
+    delta rule -> gated norm -> out-projection."""
+
+    def __init__(self, width, heads, headdim, groups, state, gen, dtype):
+        n = lambda *s: torch.randn(*s, generator=gen) * s[0] ** -0.5  # noqa: E731
+        self.H, self.P, self.G, self.N, self.K = heads, headdim, groups, state, 4
+        self.inner, self.gn = heads * headdim, groups * state
+        self.ch = 2 * self.gn + self.inner
+        self.freq = (100.0 ** (-torch.arange(state // 4) / (state // 4))).cuda()  # half of each key
+        self.p = dict(w_in=n(width, self.inner + self.ch + 2 * heads).to(dtype),
+                      conv=torch.rand(self.ch, 4, generator=gen) - 0.5, conv_bias=torch.zeros(self.ch),
+                      w_q=torch.ones(state), w_k=torch.ones(state), dt_bias=_dt_bias(heads, gen),
+                      A_log=torch.log(1 + 15 * torch.rand(heads, generator=gen)),
+                      norm=torch.ones(self.inner), w_out=n(self.inner, width).to(dtype))
+
+    def _split(self, h):
+        return (h @ self.p["w_in"]).split([self.inner, self.ch, self.H, self.H], -1)
+
+    def _qkv(self, u):
+        q, k, v = u.split([self.gn, self.gn, self.inner], -1)
+        return (q.unflatten(-1, (self.G, self.N)), k.unflatten(-1, (self.G, self.N)),
+                v.unflatten(-1, (self.H, self.P)))
+
+    def train(self, h):
+        p = self.p
+        z, u, dt, beta = self._split(h)
+        q, k, v = self._qkv(Conv.apply(u, p["conv"], p["conv_bias"]))
+        q, k = QkNorm.apply(q, k, p["w_q"], p["w_k"], self.freq)
+        y = GatedDelta.apply(q, k, v, dt.contiguous(), p["dt_bias"], -torch.exp(p["A_log"]),
+                             beta.contiguous())
+        return GatedNorm.apply(y.flatten(-2), z.contiguous(), p["norm"]) @ p["w_out"]
+
+    def cache(self, slots, dtype):
+        """Convolution inputs, states, and the position of the next token of each slot."""
+        return [torch.zeros(slots, self.K - 1, self.ch, dtype=dtype, device="cuda"),
+                torch.zeros(slots, self.H, self.P, self.N, device="cuda"),
+                torch.zeros(slots, dtype=torch.int32, device="cuda")]
+
+    def prompt(self, h, lengths, cache, slots):
+        p = self.p
+        z, u, dt, beta = self._split(h)
+        u, conv = ssd.causal_conv_fwd(u, p["conv"], p["conv_bias"], lengths=lengths)
+        q, k, v = self._qkv(u)
+        q, k = ssd.qk_norm_fwd(q, k, p["w_q"], p["w_k"], self.freq, l2=True)
+        y, state = ssd.gated_delta_fwd(q, k, v, dt.contiguous(), p["dt_bias"], -torch.exp(p["A_log"]),
+                                       beta.contiguous(), lengths=lengths)
+        for c, new in zip(cache, (conv, state, lengths)):
+            c[slots.long()] = new
+        return ssd.gated_norm_fwd(y.flatten(-2), z.contiguous(), p["norm"], self.inner,
+                                  return_rstd=False)[0] @ p["w_out"]
+
+    def token(self, h, cache, slots):
+        p = self.p
+        z, u, dt, beta = self._split(h)
+        u = ssd.causal_conv_step(u, cache[0], p["conv"], p["conv_bias"], slots=slots)
+        q, k, v = self._qkv(u)
+        at = cache[2][slots.long()]
+        q, k = ssd.qk_norm_fwd(q, k, p["w_q"], p["w_k"], self.freq, at, l2=True)
+        y = ssd.gated_delta_step(q, k, v, dt.contiguous(), p["dt_bias"], -torch.exp(p["A_log"]),
+                                 beta.contiguous(), cache[1], slots=slots)
+        cache[2][slots.long()] = at + 1
+        return ssd.gated_norm_fwd(y.flatten(-2), z.contiguous(), p["norm"], self.inner,
+                                  return_rstd=False)[0] @ p["w_out"]
+
+
 class Stack:
     """Embedding, the layers with a block norm after each, and a head.  The residual
     stream is fp32; h is in the layers' type."""
 
-    def __init__(self, vocab=64, width=64, dtype=torch.float32, seed=0):
+    def __init__(self, vocab=64, width=64, dtype=torch.float32, seed=0, delta=False):
         gen = torch.Generator().manual_seed(seed)
         self.dtype, self.scale = dtype, 0.5
         self.layers = [SelectiveLayer(width, 2 * width, 16, 8, gen, dtype),
                        SSDLayer(width, 8, 16, 16, gen, dtype)]
         self.p = dict(embed=torch.randn(vocab, width, generator=gen),
                       head=(torch.randn(width, vocab, generator=gen) * width ** -0.5).to(dtype))
+        if delta:
+            self.layers.append(DeltaLayer(width, 8, 16, 4, 32, gen, dtype))
         for i in range(len(self.layers)):
             self.p.update({f"pre{i}": torch.ones(width), f"post{i}": torch.ones(width),
                            f"gate{i}": torch.ones(1, width)})
@@ -299,8 +395,9 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--dtype", choices=["f32", "bf16"], default="f32")
+    ap.add_argument("--delta", action="store_true", help="a third layer with the gated delta rule")
     a = ap.parse_args()
-    model = Stack(dtype=torch.float32 if a.dtype == "f32" else torch.bfloat16)
+    model = Stack(dtype=torch.float32 if a.dtype == "f32" else torch.bfloat16, delta=a.delta)
     losses = train(model, a.steps)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} in {a.steps} steps")
     d, top = generate(model)
