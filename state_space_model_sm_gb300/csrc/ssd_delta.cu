@@ -48,6 +48,7 @@ struct DeltaDims {
   int NP;   // key columns in the workspace: 64 or 128
   int ip;   // planes of the images of keys and queries
   int nb;   // head blocks of a group in the gradient
+  int no;   // and in the outputs' kernel
   int sms;  // SMs of the device
   float scale;
   int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
@@ -861,8 +862,11 @@ struct OutSmem {
   static constexpr size_t total = sizeof(Gates) + raw + one + 2 * tok;
 };
 
-// Y of one chunk of one head: 16 tokens by half of 64 value columns a warp, in passes of
-// 64 value columns; the pairs Q K^T e^(..) are formed once, by halves of the tokens.
+// Y of one chunk of the heads of one head block: 16 tokens by half of 64 value columns a
+// warp, in passes of 64 value columns of a head.  Q K^T is formed once for the heads, by
+// halves of the tokens; a head's decays make its planes of it.  The next pass's states and
+// corrections are on their way under a pass's products.  Bound by shared memory (the
+// states' planes are read by four warps).
 template <typename T, typename TO, int NP>
 __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2 ? 2 : 1)
     k_delta_out(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
@@ -876,82 +880,47 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
   bf16* const ut = kt + SM::one / 2;
   bf16* const pt = ut + SM::tok / 2;
   const int tid = threadIdx.x, lane = tid & 31, strip = (tid >> 5) & 3, half = tid >> 7;
-  const Place pl = place(d, blockIdx.x);
-  const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
+  const unsigned b1 = blockIdx.x / d.nc, b2 = b1 / d.no;
+  const int c = (int)(blockIdx.x - b1 * d.nc), hb = (int)(b1 - b2 * d.no);
+  const int b = (int)(b2 / d.G), grp = (int)(b2 - (unsigned)b * d.G);
+  const int h0 = grp * d.rep + (int)((unsigned)d.rep * hb / d.no);
+  const int h1 = grp * d.rep + (int)((unsigned)d.rep * (hb + 1) / d.no);
+  const int n = tokens_of(d, lengths, b), t0 = c * kC;
   const int rows = min(kC, d.T - t0);  // of the output; tokens from n on are padding
-  TO* const yo = y + (((int64_t)pl.b * d.T + t0) * d.H + pl.h) * d.P;
   const int64_t ys = (int64_t)d.H * d.P;
+  TO* const yb = y + ((int64_t)b * d.T + t0) * ys;
   if (t0 >= n) {
+    const int cols = (h1 - h0) * d.P;
 #pragma unroll 1
-    for (int i = tid; i < rows * d.P; i += kOutThreads) yo[i / d.P * ys + i % d.P] = from_f<TO>(0.f);
+    for (int i = tid; i < rows * cols; i += kOutThreads)
+      yb[i / cols * ys + (int64_t)h0 * d.P + i % cols] = from_f<TO>(0.f);
     return;
   }
-  const int rv = min(kC, n - t0), grp = pl.h / d.rep;
-  fetch_tile<T, NP, LD, kOutThreads>(qt, q + pl.b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv,
-                                     d.N, d.vq);
-  fetch_tile<T, NP, LD, kOutThreads>(kt, k + pl.b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv,
-                                     d.N, d.vk);
+  const int rv = min(kC, n - t0);
+  fetch_tile<T, NP, LD, kOutThreads>(qt, q + b * d.qb + t0 * d.qs + (int64_t)grp * d.N, d.qs, rv, d.N,
+                                     d.vq);
+  fetch_tile<T, NP, LD, kOutThreads>(kt, k + b * d.kb + t0 * d.ks + (int64_t)grp * d.N, d.ks, rv, d.N,
+                                     d.vk);
   cp_commit();
-  if (tid < kGateCopies)
-    reinterpret_cast<uint4*>(&g)[tid] = reinterpret_cast<const uint4*>(w.gates + pl.i)[tid];
   WsTile<NP, LD, kOutThreads> ws;
   WsTile<kC, kTP, kOutThreads> wu;
-  ws.load(w.S0 + pl.i * d.Ps * NP, min(kC, d.Ps));
-  wu.load(w.U + pl.i * d.Ps * kC, min(kC, d.Ps));
+  uint4 gates = make_uint4(0, 0, 0, 0);
+  auto ahead = [&](int h, int p0) {
+    const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
+    ws.load(w.S0 + (at * d.Ps + p0) * NP, min(kC, d.Ps - p0));
+    wu.load(w.U + (at * d.Ps + p0) * kC, min(kC, d.Ps - p0));
+    if (p0 == 0 && tid < kGateCopies) gates = reinterpret_cast<const uint4*>(w.gates + at)[tid];
+  };
+  ahead(h0, 0);
   cp_wait<0>();
   __syncthreads();
   const int r0 = strip * 16 + (lane >> 2), c0 = (lane & 3) * 2;
-  {
-    float s[4][4];
+  float s[4][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-    if (2 * half <= strip)
-#pragma unroll 2
-      for (int kk = 0; kk < NP / 16; ++kk) {
-        uint32_t a[NI][4];
-#pragma unroll
-        for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
-#pragma unroll
-        for (int np = 0; np < 2; ++np)
-          mma_planes<NI, NI, NI>(s[2 * np], s[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-            b_rows<LD>(x, kt + j * kC * LD, half * 32 + np * 16, kk * 16, lane);
-          });
-      }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = r0 + e * 8, j = half * 32 + 8 * t + c0;
-        float v[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          v[f] = j + f <= i ? d.scale * decay_between(g, i, j + f) * s[t][2 * e + f] : 0.f;
-        uint32_t x[NL];
-        split2<NL>(v[0], v[1], x);
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-          *reinterpret_cast<uint32_t*>(pt + l * kC * kTP + i * kTP + j) = x[l];
-      }
-  }
-  const float f0 = d.scale * ex2(g.gh[r0]), f1 = d.scale * ex2(g.gh[r0 + 8]);
-  for (int p0 = 0; p0 < d.Ps; p0 += kC) {
-    __syncthreads();
-    ws.template store<NL>(kt);
-    wu.template store<NL>(ut);
-    __syncthreads();
-    if (p0 + kC < d.Ps) {  // the next value rows, on their way under this tile's products
-      const int pr = min(kC, d.Ps - p0 - kC);
-      ws.load(w.S0 + (pl.i * d.Ps + p0 + kC) * NP, pr);
-      wu.load(w.U + (pl.i * d.Ps + p0 + kC) * kC, pr);
-    }
-    if (p0 + half * 32 >= d.Ps) continue;
-    float o[4][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+  if (2 * half <= strip)
 #pragma unroll 2
     for (int kk = 0; kk < NP / 16; ++kk) {
       uint32_t a[NI][4];
@@ -959,15 +928,60 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
       for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
 #pragma unroll
       for (int np = 0; np < 2; ++np)
-        mma_planes<NI, NL, max2(NI, NL)>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+        mma_planes<NI, NI, NI>(s[2 * np], s[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
           b_rows<LD>(x, kt + j * kC * LD, half * 32 + np * 16, kk * 16, lane);
         });
     }
+  for (int h = h0; h < h1; ++h) {
+    float f0 = 0.f, f1 = 0.f;
+    for (int p0 = 0; p0 < d.Ps; p0 += kC) {
+      __syncthreads();  // the last pass's tiles (at first: the keys) are read
+      ws.template store<NL>(kt);
+      wu.template store<NL>(ut);
+      if (p0 == 0 && tid < kGateCopies) reinterpret_cast<uint4*>(&g)[tid] = gates;
+      __syncthreads();
+      if (p0 + kC < d.Ps) ahead(h, p0 + kC);
+      else if (h + 1 < h1) ahead(h + 1, 0);
+      if (p0 == 0) {  // the head's pairs
+        f0 = d.scale * ex2(g.gh[r0]), f1 = d.scale * ex2(g.gh[r0 + 8]);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = r0 + e * 8, j = half * 32 + 8 * t + c0;
+            float v[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              v[f] = j + f <= i ? d.scale * decay_between(g, i, j + f) * s[t][2 * e + f] : 0.f;
+            uint32_t x[NL];
+            split2<NL>(v[0], v[1], x);
+#pragma unroll
+            for (int l = 0; l < NL; ++l)
+              *reinterpret_cast<uint32_t*>(pt + l * kC * kTP + i * kTP + j) = x[l];
+          }
+        __syncthreads();
+      }
+      if (p0 + half * 32 >= d.Ps) continue;
+      float o[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+#pragma unroll 2
+      for (int kk = 0; kk < NP / 16; ++kk) {
+        uint32_t a[NI][4];
+#pragma unroll
+        for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], qt + p * kC * LD, strip * 16, kk * 16, lane);
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+          mma_planes<NI, NL, max2(NI, NL)>(o[2 * np], o[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
+            b_rows<LD>(x, kt + j * kC * LD, half * 32 + np * 16, kk * 16, lane);
+          });
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t][0] *= f0, o[t][1] *= f0, o[t][2] *= f1, o[t][3] *= f1;
 #pragma unroll 1
-    for (int kb = 0; kb < 4; ++kb)
-      if (kb <= strip) {
+      for (int kb = 0; kb <= strip; ++kb) {
         uint32_t a[NL][4];
 #pragma unroll
         for (int l = 0; l < NL; ++l) a_rows<kTP>(a[l], pt + l * kC * kTP, strip * 16, kb * 16, lane);
@@ -977,17 +991,20 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
             b_rows<kTP>(x, ut + j * kC * kTP, half * 32 + np * 16, kb * 16, lane);
           });
       }
+      TO* const yo = yb + (int64_t)h * d.P;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = r0 + e * 8, p = p0 + half * 32 + 8 * t + c0;
-        if (i < rows && p < d.P) {
-          const bool in = i < rv;
-          lm::st_two(yo + i * ys + p, make_float2(in ? o[t][2 * e] : 0.f, in ? o[t][2 * e + 1] : 0.f),
-                     p + 1 < d.P, d.wide);
+        for (int e = 0; e < 2; ++e) {
+          const int i = r0 + e * 8, p = p0 + half * 32 + 8 * t + c0;
+          if (i < rows && p < d.P) {
+            const bool in = i < rv;
+            lm::st_two(yo + i * ys + p,
+                       make_float2(in ? o[t][2 * e] : 0.f, in ? o[t][2 * e + 1] : 0.f), p + 1 < d.P,
+                       d.wide);
+          }
         }
-      }
+    }
   }
 }
 
@@ -1667,7 +1684,7 @@ __global__ void __launch_bounds__(256)
 
 // One part for each block of the heads of a group, so that the gradient's blocks fill
 // the machine; each block sums its heads in registers.
-constexpr int kGradBlocks = 2 * 152;
+constexpr int kGradBlocks = 2 * 152, kOutBlocks = 8 * 152;
 
 int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   if (!s || s->batch < 1 || s->seqlen < 1 || s->nheads < 1 || s->headdim < 1 || s->dstate < 1 ||
@@ -1699,6 +1716,8 @@ int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   const int64_t blocks = (int64_t)d->B * d->G * d->nc;
   const int64_t nb = (kGradBlocks + blocks - 1) / blocks;
   d->nb = (int)(nb < d->rep ? nb : d->rep);
+  const int64_t no = (kOutBlocks + blocks - 1) / blocks;
+  d->no = (int)(no < d->rep ? no : d->rep);
   d->qs = s->q_row_stride ? s->q_row_stride : gn;
   d->ks = s->k_row_stride ? s->k_row_stride : gn;
   d->vs = s->v_row_stride ? s->v_row_stride : hp;
@@ -1792,7 +1811,7 @@ int delta_forward(const DeltaDims& d, const DeltaIn& in, const DeltaWs& w, void*
   const int st = delta_states<T, NP, false>(d, in, nullptr, w, final_states, s);
   if (st != SSD_OK) return st;
   const auto out = k_delta_out<T, TO, NP>;
-  DELTA_LAUNCH("k_delta_out", out, (int64_t)d.B * d.H * d.nc, kOutThreads, (OutSmem<T, TO, NP>::total), d,
+  DELTA_LAUNCH("k_delta_out", out, (int64_t)d.B * d.G * d.no * d.nc, kOutThreads, (OutSmem<T, TO, NP>::total), d,
                static_cast<const T*>(in.q), static_cast<const T*>(in.k), in.lengths, w,
                static_cast<TO*>(y));
   return SSD_OK;
