@@ -250,27 +250,38 @@ __device__ __forceinline__ Place place(const DeltaDims& d, unsigned block) {
 
 // ---------------------------------------------------------------------- prep
 
-// Lower part (tiles 0 .. 2 strip + 1) of the 16 rows of strip of A B^T over NP columns;
-// A and B tiles of NI planes.
-template <int NI, int NP>
-__device__ __forceinline__ void lower_product(float (&acc)[8][4], const bf16* A, const bf16* Bt,
-                                              int strip, int lane) {
+// Lower part (tiles 0 .. 2 strip + 1) of the 16 rows of strip of K K^T and, with queries,
+// of Q K^T over NP columns; tiles of NI planes.
+template <int NI, int NP, bool QS>
+__device__ __forceinline__ void lower_products(float (&kk)[8][4], float (&qk)[QS ? 8 : 1][4],
+                                               const bf16* K, const bf16* Q, int strip, int lane) {
   constexpr int LD = NP + 8;
 #pragma unroll
   for (int t = 0; t < 8; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+    for (int e = 0; e < 4; ++e) {
+      kk[t][e] = 0.f;
+      if constexpr (QS) qk[t][e] = 0.f;
+    }
 #pragma unroll 2
-  for (int kk = 0; kk < NP / 16; ++kk) {
-    uint32_t a[NI][4];
+  for (int x = 0; x < NP / 16; ++x) {
+    uint32_t a[NI][4], f[NI][4];
 #pragma unroll
-    for (int p = 0; p < NI; ++p) a_rows<LD>(a[p], A + p * kC * LD, strip * 16, kk * 16, lane);
+    for (int p = 0; p < NI; ++p) {
+      a_rows<LD>(a[p], K + p * kC * LD, strip * 16, x * 16, lane);
+      if constexpr (QS) a_rows<LD>(f[p], Q + p * kC * LD, strip * 16, x * 16, lane);
+    }
 #pragma unroll
     for (int np = 0; np < 4; ++np)
-      if (np <= strip)
-        mma_planes<NI, NI, NI>(acc[2 * np], acc[2 * np + 1], a, [&](int j, uint32_t(&r)[4]) {
-          b_rows<LD>(r, Bt + j * kC * LD, np * 16, kk * 16, lane);
-        });
+      if (np <= strip) {
+        auto b = [&](int j, uint32_t(&r)[4]) {
+          b_rows<LD>(r, K + j * kC * LD, np * 16, x * 16, lane);
+        };
+        if constexpr (QS)
+          mma_planes2<NI, NI, NI, NI, NI>(kk[2 * np], kk[2 * np + 1], a, qk[2 * np], qk[2 * np + 1], f, b);
+        else
+          mma_planes<NI, NI, NI>(kk[2 * np], kk[2 * np + 1], a, b);
+      }
   }
 }
 
@@ -425,8 +436,7 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) :
     g.fq[i] = d.scale * eg * qi;
   }
   float acc[8][4], qk[BWD ? 8 : 1][4];
-  lower_product<NI, NP>(acc, Kt, Kt, strip, lane);
-  if constexpr (BWD) lower_product<NI, NP>(qk, Qt, Kt, strip, lane);
+  lower_products<NI, NP, BWD>(acc, qk, Kt, Qt, strip, lane);
   __syncthreads();  // the tiles are read
 #pragma unroll
   for (int t = 0; t < 8; ++t)
@@ -1268,6 +1278,66 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
   };
 
+  // the gates' gradients of a head, by the first warp, two tokens a lane: from the sums that
+  // the head left, while the next head's first values are on their way
+  bool due = false;
+  float zd[2], bd[2], ed = 0.f;
+  auto gates_of = [&](int h) {
+    const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
+    float dg[2], wii[2], last = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = 2 * lane + x;
+      float u = 0.f, r = 0.f, ww = 0.f, rs = 0.f, cs = 0.f, qs = 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) rs += sm.row[p][i], cs += sm.col[p][i], qs += sm.qd[p][i];
+      dg[x] = (rs - cs) + (qs - r) - u;
+      wii[x] = ww;
+      last += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
+    float ss = 0.f;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) ss += sm.dot[p];
+    last += ed * ss;
+    if (lane == 31) dg[1] += last;
+    // sums from each token on
+    dg[0] += dg[1];
+    float run = dg[0];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float dn = __shfl_down_sync(0xffffffffu, run, o);
+      if (lane + o < 32) run += dn;
+    }
+    const float after = run - dg[0];
+    float sa = 0.f, sb = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = 2 * lane + x;
+      const float v = dg[x] + after;
+      const int64_t o = (tok + i) * d.H + h;
+      if (i < rv) {
+        const float dz = v * A[h] * sigmoid(zd[x]);
+        sa = fmaf(v, softplus(zd[x]), sa);
+        sb += dz;
+        ddt[o] = from_f<TO>(dz);
+        dbeta[o] = from_f<TO>((1.f - bd[x]) * wii[x]);
+      } else if (i < rows) {
+        ddt[o] = from_f<TO>(0.f);
+        dbeta[o] = from_f<TO>(0.f);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sa += __shfl_xor_sync(0xffffffffu, sa, o);
+      sb += __shfl_xor_sync(0xffffffffu, sb, o);
+    }
+    if (lane == 0) w.part[at * 2] = sa, w.part[at * 2 + 1] = sb;
+  };
+
   for (int h = h0; h < h1 && rv > 0; ++h) {
     const int64_t at = ((int64_t)b * d.H + h) * d.nc + c;
     // the gates' inputs of the two tokens of a lane of the first warp, for the head's end
@@ -1277,7 +1347,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int x = 0; x < 2; ++x)
         if (2 * lane + x < rv)
           zt[x] = to_f(dt[(tok + 2 * lane + x) * d.H + h]) + (dt_bias ? dt_bias[h] : 0.f);
-    const float Ah = A[h];
     float da[2][4], wm[2][4], dqh[HT][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -1299,6 +1368,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       wu.load(w.U + pt * kC, pr);
       wz.load(w.Zd + pt * kC, pr);
       wb.load(w.Zb + pt * kC, pr);
+      if (due) {
+        gates_of(h - 1);
+        due = false;
+      }
       __syncthreads();  // the tiles (and, at a head's start, the gates and sums) are read
       fetch_tile<T, kC, kTP, kGradThreads>(yt, dy + tok * ys + (int64_t)h * d.P + p0, ys, rv, d.P - p0,
                                            d.vdy);
@@ -1365,16 +1438,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           auto ub = [&](int j, uint32_t(&x)[4]) {
             b_cols<kTP>(x, ut + j * kC * kTP, part * 16, kb * 16, lane);
           };
-          mma_planes<NI, 3, 3>(da[0], da[1], ya, ub);
-          mma_planes<3, 3, 3>(wm[0], wm[1], ra, ub);
+          mma_planes2<NI, 3, 3, 3, 3>(da[0], da[1], ya, wm[0], wm[1], ra, ub);
         }
 #pragma unroll
         for (int np = 0; np < HT / 2; ++np) {
           auto sb = [&](int j, uint32_t(&x)[4]) {
             b_cols<LD>(x, st + j * kC * LD, part * WC + np * 16, kb * 16, lane);
           };
-          mma_planes<NI, 3, 3>(dqh[2 * np], dqh[2 * np + 1], ya, sb);
-          mma_planes<NL, NL, NL>(tk[2 * np], tk[2 * np + 1], xa, sb);
+          mma_planes2<NI, 3, NL, NL, 3>(dqh[2 * np], dqh[2 * np + 1], ya, tk[2 * np], tk[2 * np + 1], xa,
+                                        sb);
         }
       }
       __syncthreads();
@@ -1449,8 +1521,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           auto kb = [&](int j, uint32_t(&r)[4]) {
             b_rows<LD>(r, kt + j * kC * LD, part * 16, x * 16, lane);
           };
-          mma_planes<NI, NI, NI>(qk[0], qk[1], qa, kb);
-          mma_planes<NI, NI, NI>(kk[0], kk[1], ka, kb);
+          mma_planes2<NI, NI, NI, NI, NI>(qk[0], qk[1], qa, kk[0], kk[1], ka, kb);
         }
       float rs[2] = {0.f, 0.f}, cs[2][2];
 #pragma unroll
@@ -1534,8 +1605,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           auto kbl = [&](int j, uint32_t(&x)[4]) {
             b_cols<LD>(x, kt + j * kC * LD, part * WC + np * 16, kb * 16, lane);
           };
-          mma_planes<NL, NI, max2(NL, NI)>(tq[2 * np], tq[2 * np + 1], a, kbl);
-          mma_planes<NL, NI, max2(NL, NI)>(tk[2 * np], tk[2 * np + 1], a2, kbl);
+          mma_planes2<NL, max2(NL, NI), NL, max2(NL, NI), NI>(tq[2 * np], tq[2 * np + 1], a, tk[2 * np],
+                                                              tk[2 * np + 1], a2, kbl);
         }
       }
       if (kb >= strip) {
@@ -1557,61 +1628,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
       }
     }
-    if (warp == 0) {  // the gates' gradients, two tokens a lane
-      float dg[2], wii[2], last = 0.f;
+    if (warp == 0) {
+      due = true;
+      zd[0] = zt[0], zd[1] = zt[1];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * lane + x;
-        float u = 0.f, r = 0.f, ww = 0.f, rs = 0.f, cs = 0.f, qs = 0.f;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) u += sm.part[p][0][i], r += sm.part[p][1][i], ww += sm.part[p][2][i];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) rs += sm.row[p][i], cs += sm.col[p][i], qs += sm.qd[p][i];
-        dg[x] = (rs - cs) + (qs - r) - u;
-        wii[x] = ww;
-        last += u;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
-      float ss = 0.f;
-#pragma unroll
-      for (int p = 0; p < 16; ++p) ss += sm.dot[p];
-      last += ex2(g.gh[kC - 1]) * ss;
-      if (lane == 31) dg[1] += last;
-      // sums from each token on
-      dg[0] += dg[1];
-      float run = dg[0];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float dn = __shfl_down_sync(0xffffffffu, run, o);
-        if (lane + o < 32) run += dn;
-      }
-      const float after = run - dg[0];
-      float sa = 0.f, sb = 0.f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * lane + x;
-        const float v = dg[x] + after;
-        const int64_t o = (tok + i) * d.H + h;
-        if (i < rv) {
-          const float dz = v * Ah * sigmoid(zt[x]);
-          sa = fmaf(v, softplus(zt[x]), sa);
-          sb += dz;
-          ddt[o] = from_f<TO>(dz);
-          dbeta[o] = from_f<TO>((1.f - g.b[i]) * wii[x]);
-        } else if (i < rows) {
-          ddt[o] = from_f<TO>(0.f);
-          dbeta[o] = from_f<TO>(0.f);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sa += __shfl_xor_sync(0xffffffffu, sa, o);
-        sb += __shfl_xor_sync(0xffffffffu, sb, o);
-      }
-      if (lane == 0) w.part[at * 2] = sa, w.part[at * 2 + 1] = sb;
+      for (int x = 0; x < 2; ++x) bd[x] = g.b[2 * lane + x];
+      ed = ex2(g.gh[kC - 1]);
     }
   }
+  if (due) gates_of(h1 - 1);
   // padding rows are zeros: their keys, queries, corrections and gradients are
   const int64_t row = ((int64_t)b * d.T + t0 + r0) * d.G + grp, whole = (int64_t)d.B * d.T * d.G * d.N;
 #pragma unroll

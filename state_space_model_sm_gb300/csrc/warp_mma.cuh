@@ -194,6 +194,31 @@ __device__ __forceinline__ void mma_planes_h(float (&c0)[4], float (&c1)[4],
   }
 }
 
+// The same right operand in two products: c0, c1 += A B over plane products i + j < M,
+// e0, e1 += F B over i + j < ME.
+template <int NA, int M, int NF, int ME, int NB, typename Load>
+__device__ __forceinline__ void mma_planes2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
+                                            float (&e0)[4], float (&e1)[4], const uint32_t (&f)[NF][4],
+                                            Load&& load) {
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    uint32_t b[4];
+    load(j, b);
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (i + j < M) {
+        mma16816(c0, a[i], b[0], b[1]);
+        mma16816(c1, a[i], b[2], b[3]);
+      }
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      if (i + j < ME) {
+        mma16816(e0, f[i], b[0], b[1]);
+        mma16816(e1, f[i], b[2], b[3]);
+      }
+  }
+}
+
 constexpr int max2(int a, int b) { return a > b ? a : b; }
 
 }  // namespace wm
