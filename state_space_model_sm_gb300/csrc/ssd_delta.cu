@@ -653,6 +653,30 @@ struct ChainBars {
 };
 constexpr int kChainWarps = 4, kFillWarp = 4;
 
+// A strip's 16 value columns of a raw tile as its rows: the accumulator of the transpose.
+template <typename T>
+__device__ __forceinline__ void raw_strip(float (&c)[8][4], const T* tile, int strip, int lane) {
+  constexpr int RP = raw_pitch<T>();
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t x[4];
+      a_cols<RP>(x, tile, strip * 16, kb * 16, lane);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        c[2 * kb + (q >> 1)][(q & 1) * 2] = __uint_as_float(x[q] << 16);
+        c[2 * kb + (q >> 1)][(q & 1) * 2 + 1] = __uint_as_float(x[q] & 0xffff0000u);
+      }
+    }
+  } else {
+    const T* p = tile + (lane & 3) * 2 * RP + strip * 16 + (lane >> 2);
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[t][e] = p[(8 * t + (e & 1)) * RP + (e >> 1) * 8];
+  }
+}
+
 // Z^T = S K^T, rows of S scaled.
 template <int NI, int NP>
 __device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (&S)[NP / 8][4],
@@ -785,7 +809,7 @@ __global__ void __launch_bounds__(kChainThreads)
   const int row = p0 + strip * 16;  // this warp's first value row
   float S[NP / 8][4];
   load_state<NP>(S, init ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  const int t2 = (lane & 3) * 2;
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
     if (!tc::mbar_wait(&sm.full[s], (c >> 1) & 1, status, &sm.abort)) return;
@@ -804,21 +828,22 @@ __global__ void __launch_bounds__(kChainThreads)
     // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
     scale_tokens(r, g.fz, t2, s0.inv, s1.inv);
     if constexpr (KEEP) store_strip<8>(w.Zb, srow, r, lane);
+    float u[8][4];
+    raw_strip<T>(u, vt, strip, lane);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      const int i = 8 * t + t2;
-      const float2 bi = *reinterpret_cast<const float2*>(g.b + i);
-      const float2 fx = *reinterpret_cast<const float2*>(g.fx + i);
+      const float2 bi = *reinterpret_cast<const float2*>(g.b + 8 * t + t2);
+      const float2 fx = *reinterpret_cast<const float2*>(g.fx + 8 * t + t2);
+      const float2 m1 = make_float2(-1.f, -1.f);
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        const int p = strip * 16 + g8 + o * 8;
-        r[t][2 * o] = fx.x * fmaf(bi.x, to_f(vt[i * RP + p]), -r[t][2 * o]);
-        r[t][2 * o + 1] = fx.y * fmaf(bi.y, to_f(vt[(i + 1) * RP + p]), -r[t][2 * o + 1]);
+        const float2 v = __fmul2_rn(bi, make_float2(u[t][2 * o], u[t][2 * o + 1]));
+        const float2 x = __fmul2_rn(fx, __ffma2_rn(make_float2(r[t][2 * o], r[t][2 * o + 1]), m1, v));
+        r[t][2 * o] = x.x, r[t][2 * o + 1] = x.y;
       }
     }
     row_max<8>(r, a0, a1);
     const Scale q0 = scale_of(a0), q1 = scale_of(a1);
-    float u[8][4];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -1093,7 +1118,7 @@ __global__ void __launch_bounds__(kChainThreads)
   const int row = p0 + strip * 16;
   float S[NP / 8][4];
   load_state<NP>(S, dfinal ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  const int t2 = (lane & 3) * 2;
   for (int i = 0; i < nc; ++i) {
     const int s = i & 1, c = nc - 1 - i;
     if (!tc::mbar_wait(&sm.full[s], (i >> 1) & 1, status, &sm.abort)) return;
@@ -1138,12 +1163,7 @@ __global__ void __launch_bounds__(kChainThreads)
     store_strip<8>(w.dR, srow, u, lane);
     // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
     scale_tokens(u, g.fz, t2, -1.f, -1.f);
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int j = 8 * t + t2, p = strip * 16 + g8;
-      r[t][0] = to_f(yt[j * RP + p]), r[t][1] = to_f(yt[(j + 1) * RP + p]);
-      r[t][2] = to_f(yt[j * RP + p + 8]), r[t][3] = to_f(yt[(j + 1) * RP + p + 8]);
-    }
+    raw_strip<T>(r, yt, strip, lane);
     scale_tokens(r, g.fq, t2, 1.f, 1.f);
     float b0, b1;
     row_max<8>(r, a0, a1);
