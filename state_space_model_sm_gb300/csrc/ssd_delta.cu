@@ -50,6 +50,7 @@ struct DeltaDims {
   int nb;   // head blocks of a group in the gradient
   int no;   // and in the outputs' kernel
   int sms;  // SMs of the device
+  int W, cs;  // segments of a sequence in the chains, and chunks of one
   float scale;
   int64_t qs, qb, ks, kb, vs, vb;  // elements between tokens, and between batch rows
   int vq, vk, vv, vdy;             // whether rows can be read 16 bytes at a time
@@ -75,6 +76,9 @@ struct DeltaWs {
   bf16* Q;       // the same of the queries (backward)
   float* U;      // (B, H, nc, Ps, 64)  transposed: [p][token]
   float* S0;     // (B, H, nc, Ps, NP)  the state in front of each chunk
+  float* ends;  // (B, H, W, Ps, NP)  the state behind each segment from a zero state (W > 1)
+  float* move;  // (B, H, W, NP, NP)  and what it makes of the state in front of it
+  float* front; // (B, H, W, Ps, NP)  the state in front of each segment
   // backward
   float* Zb;   // (B, H, nc, Ps, 64)  b e^G S k
   float* E;    // (B, H, nc, Ps, 64)  the part of dU from dY
@@ -741,6 +745,94 @@ __device__ __forceinline__ void store_strip(float* m, int64_t strip, const float
 }
 constexpr float kBelow = 5.9604644775390625e-8f;  // 2^-24
 
+// A block of a chain: 64 rows (value rows, or rows of a segment's move) of one segment.
+struct Piece {
+  int b, h, p0, n;        // first row; tokens of the sequence
+  int seg, c0, count;     // first chunk, chunks
+  int strips;
+  bool moving, last, idle;  // rows of the move; holds the sequence's last chunk
+  int64_t bh;
+};
+template <int NP, bool SEG>
+__device__ __forceinline__ Piece piece(const DeltaDims& d, const int* lengths) {
+  Piece p;
+  const unsigned vt = (d.Ps + kC - 1) / kC, tiles = SEG ? vt + NP / kC : vt, segs = SEG ? d.W - 1 : d.W;
+  const unsigned x = blockIdx.x / tiles, tile = blockIdx.x - x * tiles, bh = x / segs;
+  p.seg = (int)(x - bh * segs);
+  p.bh = bh;
+  p.b = (int)(bh / (unsigned)d.H), p.h = (int)(bh - (unsigned)p.b * d.H);
+  p.n = tokens_of(d, lengths, p.b);
+  const int nc = (p.n + kC - 1) / kC;
+  p.c0 = p.seg * d.cs;
+  p.count = max(0, min(nc, p.c0 + d.cs) - p.c0);
+  p.moving = tile >= vt;
+  p.p0 = (int)(p.moving ? tile - vt : tile) * kC;
+  p.strips = min(4, ((p.moving ? NP : d.Ps) - p.p0) / 16);
+  p.last = p.count > 0 ? p.c0 + p.count == nc : p.seg == 0;
+  p.idle = SEG ? p.moving && p.seg == 0 : p.count == 0 && !p.last;
+  return p;
+}
+template <int NP, bool SEG>
+__device__ __forceinline__ void start_state(float (&S)[NP / 8][4], const DeltaDims& d, const Piece& p,
+                                            int row, const float* first, const float* front, int lane) {
+  if (!SEG && p.seg > 0) {
+    load_state<NP>(S, front + ((p.bh * d.W + p.seg) * d.Ps + row) * NP, 16, NP, lane);
+  } else if (SEG && (p.moving || p.seg > 0)) {
+    const int r = row + (lane >> 2), c = (lane & 3) * 2;
+#pragma unroll
+    for (int t = 0; t < NP / 8; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        S[t][e] = p.moving && 8 * t + c + (e & 1) == r + (e >> 1) * 8 ? 1.f : 0.f;
+  } else {
+    load_state<NP>(S, first ? first + (p.bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  }
+}
+template <int NP, bool SEG>
+__device__ __forceinline__ void end_state(const float (&S)[NP / 8][4], const DeltaDims& d, const Piece& p,
+                                          int row, float* last, const DeltaWs& w, int lane) {
+  if constexpr (SEG) {
+    float* to = p.moving ? w.move + ((p.bh * d.W + p.seg) * NP + row) * NP
+                         : w.ends + ((p.bh * d.W + p.seg) * d.Ps + row) * NP;
+    store_state<NP>(to, S, 16, NP, lane);
+  } else if (last) {
+    store_state<NP>(last + (p.bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+  }
+}
+
+// The state in front of each segment: front_0 is the sequence's first state, front_1 =
+// ends_0 (which starts from it), front_j+1 = ends_j + front_j move_j.  16 rows a block.
+template <int NP>
+__global__ void __launch_bounds__(NP) k_delta_join(DeltaDims d, DeltaWs w) {
+  __shared__ float s[16][NP];
+  const int col = threadIdx.x, strips = d.Ps / 16;
+  const int64_t bh = blockIdx.x / strips;
+  const int row = (int)(blockIdx.x % strips) * 16;
+  float a[16];
+  for (int j = 1; j < d.W; ++j) {
+    const float* e = w.ends + ((bh * d.W + j - 1) * d.Ps + row) * NP + col;
+    float b[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) b[r] = e[r * NP];
+    if (j > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r][col] = a[r];
+      __syncthreads();
+      const float* m = w.move + (bh * d.W + j - 1) * NP * NP + col;
+#pragma unroll 8
+      for (int k = 0; k < NP; ++k) {
+        const float x = m[k * NP];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = fmaf(s[r][k], x, b[r]);
+      }
+    }
+    float* f = w.front + ((bh * d.W + j) * d.Ps + row) * NP + col;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) a[r] = b[r], f[r * NP] = b[r];
+  }
+}
+
 // The chain over a head's chunks: 64 value rows a block, a strip of 16 rows a warp with
 // its state in registers (16 x NP fp32, an accumulator).  A chunk is three products,
 //     Z^T = S K^T,   U^T = (b (V - e^G Z))^T X^T,   S <- e^G63 S + (e^(G63 - G) U)^T K,
@@ -749,7 +841,14 @@ constexpr float kBelow = 5.9604644775390625e-8f;  // 2^-24
 // (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
 // bf16 take 504.  The products are issued by one warp per SM quarter at 8 clocks each,
 // which bounds a chunk by 1.3 us.  KEEP: also writes b e^G Z, for the backward.
-template <typename T, int NP, bool KEEP>
+//
+// Few heads leave most of the machine idle, so a long sequence is cut into W segments of cs
+// chunks.  A chunk's step is linear in the state and the values, row by row: the state
+// behind a segment is  ends + front move,  with `ends` from a zero state and `move` the
+// rows of the identity taken through the segment without values.  SEG is the pass that
+// forms both (no other output); k_delta_join adds them up to each segment's front; the
+// pass that writes the states and U then runs all segments at once.
+template <typename T, int NP, bool KEEP, bool SEG>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_chain(DeltaDims d, const T* __restrict__ v, const float* __restrict__ init,
                   const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states,
@@ -758,12 +857,11 @@ __global__ void __launch_bounds__(kChainThreads)
   extern __shared__ __align__(16) unsigned char smem[];
   ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const unsigned ptiles = (d.Ps + kC - 1) / kC, bhu = blockIdx.x / ptiles;
-  const int p0 = (int)(blockIdx.x - bhu * ptiles) * kC, b = (int)(bhu / (unsigned)d.H);
-  const int h = (int)(bhu - (unsigned)b * d.H);
-  const int64_t bh = bhu;
-  const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
-  const int strips = min(kChainWarps, (d.Ps - p0) / 16);
+  const Piece pc = piece<NP, SEG>(d, lengths);
+  const int p0 = pc.p0, b = pc.b, h = pc.h, n = pc.n, c0 = pc.c0, nc = pc.count;
+  const int64_t bh = pc.bh;
+  if (pc.idle) return;
+  const int strips = pc.strips;
   unsigned char* const stages = smem + sizeof(ChainBars);
   constexpr size_t STAGE = chain_stage<T, NP>(), VT = sizeof(Gates) + NI * kC * LD * 2;
   if (threadIdx.x == 0) {
@@ -784,18 +882,20 @@ __global__ void __launch_bounds__(kChainThreads)
     const bf16* const kg = w.K + ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
     int c = 0;
     for (; c < nc; ++c) {
-      const int s = c & 1;
+      const int s = c & 1, cc = c0 + c;
       if (!tc::mbar_wait(&sm.empty[s], ((c >> 1) & 1) ^ 1, status, &sm.abort)) break;
       unsigned char* at = stages + s * STAGE;
       uint64_t* bar = &sm.full[s];
       if (lane == 0) {
-        tc::bulk_g2s(at, w.gates + bh * d.nc + c, sizeof(Gates), bar);
-        tc::bulk_g2s(at + sizeof(Gates), kg + (int64_t)c * NI * kC * LD, NI * kC * LD * 2, bar);
-        tc::bulk_g2s(at + VT + kC * RP * sizeof(T), w.X + (bh * d.nc + c) * (2 * kC * kTP),
+        tc::bulk_g2s(at, w.gates + bh * d.nc + cc, sizeof(Gates), bar);
+        tc::bulk_g2s(at + sizeof(Gates), kg + (int64_t)cc * NI * kC * LD, NI * kC * LD * 2, bar);
+        tc::bulk_g2s(at + VT + kC * RP * sizeof(T), w.X + (bh * d.nc + cc) * (2 * kC * kTP),
                      2 * kC * kTP * 2, bar);
       }
-      const uint32_t raw = raw_rows<T>(reinterpret_cast<T*>(at + VT), vg + (int64_t)c * kC * d.vs, d.vs,
-                                       min(kC, n - c * kC), d.P - p0, d.vv, bar, lane);
+      uint32_t raw = 0;
+      if (!SEG || !pc.moving)
+        raw = raw_rows<T>(reinterpret_cast<T*>(at + VT), vg + (int64_t)cc * kC * d.vs, d.vs,
+                          min(kC, n - cc * kC), d.P - p0, d.vv, bar, lane);
       if (lane == 0)
         tc::mbar_arrive_expect_tx(bar, raw + sizeof(Gates) + NI * kC * LD * 2 + 2 * kC * kTP * 2);
       else
@@ -808,7 +908,7 @@ __global__ void __launch_bounds__(kChainThreads)
   if (strip >= strips) return;
   const int row = p0 + strip * 16;  // this warp's first value row
   float S[NP / 8][4];
-  load_state<NP>(S, init ? init + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  start_state<NP, SEG>(S, d, pc, row, init, w.front, lane);
   const int t2 = (lane & 3) * 2;
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
@@ -818,16 +918,16 @@ __global__ void __launch_bounds__(kChainThreads)
     const bf16* kt = reinterpret_cast<const bf16*>(at + sizeof(Gates));
     const T* vt = reinterpret_cast<const T*>(at + VT);
     const bf16* xt = reinterpret_cast<const bf16*>(vt + kC * RP);
-    const int64_t srow = ((bh * d.nc + c) * d.Ps + row) / 16;
+    const int64_t srow = ((bh * d.nc + c0 + c) * d.Ps + row) / 16;
     float m0, m1, a0, a1;
     row_max<NP / 8>(S, m0, m1);
     const Scale s0 = scale_of(m0), s1 = scale_of(m1);
     float r[8][4];
     state_times_keys<NI, NP>(r, S, kt, s0, s1, lane);
-    store_strip<NP / 8>(w.S0, srow, S, lane);
+    if constexpr (!SEG) store_strip<NP / 8>(w.S0, srow, S, lane);
     // r = b (v - e^G z) 2^x, of the value rows g8 and g8 + 8 and tokens 8 t + t2, + 1
     scale_tokens(r, g.fz, t2, s0.inv, s1.inv);
-    if constexpr (KEEP) store_strip<8>(w.Zb, srow, r, lane);
+    if constexpr (KEEP && !SEG) store_strip<8>(w.Zb, srow, r, lane);
     float u[8][4];
     raw_strip<T>(u, vt, strip, lane);
 #pragma unroll
@@ -859,7 +959,7 @@ __global__ void __launch_bounds__(kChainThreads)
         });
     }
     scale_rows(u, q0.inv, q1.inv);
-    store_strip<8>(w.U, srow, u, lane);
+    if constexpr (!SEG) store_strip<8>(w.U, srow, u, lane);
     scale_tokens(u, g.fu, t2, 1.f, 1.f);
     // the state takes the products in the scale of U's rows, or of its own where that is
     // 2^24 larger (what U would lose there is below the state's own rounding)
@@ -872,8 +972,7 @@ __global__ void __launch_bounds__(kChainThreads)
     if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
     scale_rows(S, u0.inv, u1.inv);
   }
-  if (final_states)
-    store_state<NP>(final_states + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+  end_state<NP, SEG>(S, d, pc, row, pc.last ? final_states : nullptr, w, lane);
 }
 
 template <typename T, int NP>
@@ -1731,6 +1830,25 @@ __global__ void __launch_bounds__(256)
 // the machine; each block sums its heads in registers.
 constexpr int kGradBlocks = 2 * 152, kOutBlocks = 8 * 152;
 
+// Segments of the chains: as many, up to 32 of at least 8 chunks, as make the modelled time
+// shortest.  A strip's chunk takes 2.8 us with up to one strip an SM quarter and 1.6 us for
+// each of them from two on; the extra pass has NP / 16 strips of a head more, and a
+// segment's join takes 6 us.
+void segments(DeltaDims* d) {
+  const double own = (double)d->B * d->H * d->Ps / 16, more = own + (double)d->B * d->H * d->NP / 16;
+  auto chunk = [](double strips) {
+    const double x = strips / (4 * 152);
+    return x <= 1.0 ? 2.8 : 1.6 * (x < 2.0 ? 2.0 : x);
+  };
+  d->W = 1, d->cs = d->nc;
+  double best = d->nc * chunk(own);
+  for (int w = 2; w <= 32 && d->nc / w >= 8; w *= 2) {
+    const int cs = (d->nc + w - 1) / w;
+    const double t = cs * (chunk(more * (w - 1)) + chunk(own * w)) + 6.0 * (w - 1);
+    if (t < 0.9 * best) best = t, d->W = w, d->cs = cs;
+  }
+}
+
 int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   if (!s || s->batch < 1 || s->seqlen < 1 || s->nheads < 1 || s->headdim < 1 || s->dstate < 1 ||
       s->ngroups < 1 || s->nheads % s->ngroups != 0)
@@ -1758,6 +1876,7 @@ int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   // a block for each (batch, head, chunk), or 64 value rows of a (batch, head)
   const int64_t bh = (int64_t)d->B * d->H;
   if (bh * d->nc >= 0x7fffffff || bh * 4 >= 0x7fffffff) return SSD_ERR_UNSUPPORTED;
+  segments(d);
   const int64_t blocks = (int64_t)d->B * d->G * d->nc;
   const int64_t nb = (kGradBlocks + blocks - 1) / blocks;
   d->nb = (int)(nb < d->rep ? nb : d->rep);
@@ -1787,6 +1906,12 @@ DeltaWs delta_ws(const DeltaDims& d, void* base, bool bwd) {
   w.K = static_cast<bf16*>(take(image));
   w.U = static_cast<float*>(take(tok));
   w.S0 = static_cast<float*>(take(st));
+  if (d.W > 1) {
+    const size_t segs = (size_t)d.B * d.H * d.W * d.NP * 4;
+    w.ends = static_cast<float*>(take(segs * d.Ps));
+    w.front = static_cast<float*>(take(segs * d.Ps));
+    w.move = static_cast<float*>(take(segs * d.NP));
+  }
   if (bwd) {
     w.Q = static_cast<bf16*>(take(image));
     w.Zb = static_cast<float*>(take(tok));
@@ -1844,8 +1969,15 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
   DELTA_LAUNCH("k_delta_prep", prep, n, kPrepThreads, (PrepSmem<T, NP, BWD>::total), d, q, k,
                static_cast<const T*>(in.dt), in.dt_bias, in.A, static_cast<const T*>(in.beta),
                static_cast<const T*>(dy), in.lengths, w);
-  const auto chain = k_delta_chain<T, NP, BWD>;
-  DELTA_LAUNCH("k_delta_chain", chain, chains, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,
+  if (d.W > 1) {
+    const auto ends = k_delta_chain<T, NP, false, true>;
+    DELTA_LAUNCH("k_delta_ends", ends, (int64_t)d.B * d.H * (d.W - 1) * ((d.Ps + kC - 1) / kC + NP / kC),
+                 kChainThreads, (chain_smem<T, NP>()), d, v, in.init, in.lengths, w, nullptr,
+                 device_status_ptr());
+    DELTA_LAUNCH("k_delta_join", k_delta_join<NP>, (int64_t)d.B * d.H * (d.Ps / 16), NP, 0, d, w);
+  }
+  const auto chain = k_delta_chain<T, NP, BWD, false>;
+  DELTA_LAUNCH("k_delta_chain", chain, chains * d.W, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,
                in.lengths, w, final_states, device_status_ptr());
   return SSD_OK;
 }
