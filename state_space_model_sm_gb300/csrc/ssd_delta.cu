@@ -18,6 +18,7 @@
 // decays are summed and kept as two floats, so that a strong decay early in
 // a chunk takes nothing from the differences behind it.
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include "layer_math.cuh"
 #include "ssd_internal.h"
@@ -801,35 +802,43 @@ __device__ __forceinline__ void end_state(const float (&S)[NP / 8][4], const Del
 }
 
 // The state in front of each segment: front_0 is the sequence's first state, front_1 =
-// ends_0 (which starts from it), front_j+1 = ends_j + front_j move_j.  16 rows a block.
+// ends_0 (which starts from it), front_j+1 = ends_j + front_j move_j.  16 rows a block;
+// four groups of threads take a quarter of the products' sums each.
 template <int NP>
-__global__ void __launch_bounds__(NP) k_delta_join(DeltaDims d, DeltaWs w) {
-  __shared__ float s[16][NP];
-  const int col = threadIdx.x, strips = d.Ps / 16;
+__global__ void __launch_bounds__(4 * NP) k_delta_join(DeltaDims d, DeltaWs w) {
+  __shared__ float s[16][NP], part[4][16][NP];
+  const int col = threadIdx.x % NP, g = threadIdx.x / NP, strips = d.Ps / 16;
   const int64_t bh = blockIdx.x / strips;
   const int row = (int)(blockIdx.x % strips) * 16;
-  float a[16];
   for (int j = 1; j < d.W; ++j) {
-    const float* e = w.ends + ((bh * d.W + j - 1) * d.Ps + row) * NP + col;
-    float b[16];
+    const int64_t at = bh * d.W + j - 1;
+    const float* e = w.ends + (at * d.Ps + row) * NP + col;
+    float* f = w.front + ((at + 1) * d.Ps + row) * NP + col;
+    float own[4];  // rows 4 g .. of this column
 #pragma unroll
-    for (int r = 0; r < 16; ++r) b[r] = e[r * NP];
+    for (int r = 0; r < 4; ++r) own[r] = e[(4 * g + r) * NP];
     if (j > 1) {
-      __syncthreads();
+      const float* m = w.move + (at * NP + g * (NP / 4)) * NP + col;
+      float b[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[r][col] = a[r];
-      __syncthreads();
-      const float* m = w.move + (bh * d.W + j - 1) * NP * NP + col;
-#pragma unroll 8
-      for (int k = 0; k < NP; ++k) {
+      for (int r = 0; r < 16; ++r) b[r] = 0.f;
+#pragma unroll 16
+      for (int k = 0; k < NP / 4; ++k) {
         const float x = m[k * NP];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) b[r] = fmaf(s[r][k], x, b[r]);
+        for (int r = 0; r < 16; ++r) b[r] = fmaf(s[r][g * (NP / 4) + k], x, b[r]);
       }
-    }
-    float* f = w.front + ((bh * d.W + j) * d.Ps + row) * NP + col;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) a[r] = b[r], f[r * NP] = b[r];
+      for (int r = 0; r < 16; ++r) part[g][r][col] = b[r];
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) own[r] += part[p][4 * g + r][col];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[4 * g + r][col] = f[(4 * g + r) * NP] = own[r];
+    __syncthreads();
   }
 }
 
@@ -849,7 +858,7 @@ __global__ void __launch_bounds__(NP) k_delta_join(DeltaDims d, DeltaWs w) {
 // forms both (no other output); k_delta_join adds them up to each segment's front; the
 // pass that writes the states and U then runs all segments at once.
 template <typename T, int NP, bool KEEP, bool SEG>
-__global__ void __launch_bounds__(kChainThreads)
+__global__ void __launch_bounds__(192, 2)
     k_delta_chain(DeltaDims d, const T* __restrict__ v, const float* __restrict__ init,
                   const int* __restrict__ lengths, DeltaWs w, float* __restrict__ final_states,
                   int* status) {
@@ -1831,21 +1840,27 @@ __global__ void __launch_bounds__(256)
 constexpr int kGradBlocks = 2 * 152, kOutBlocks = 8 * 152;
 
 // Segments of the chains: as many, up to 32 of at least 8 chunks, as make the modelled time
-// shortest.  A strip's chunk takes 2.8 us with up to one strip an SM quarter and 1.6 us for
-// each of them from two on; the extra pass has NP / 16 strips of a head more, and a
-// segment's join takes 6 us.
+// shortest.  Measured with 128 key columns: a chunk of the chain takes 2.9 us with a block
+// an SM and 5.1 with two (which fit); of the extra pass, which has the blocks of the moves
+// as well and writes nothing on its way, 3.2 with few blocks, 4.5 with up to two an SM and
+// 3.8 for every two from there; a segment's join 3.8 us, more where the machine is full.
+// 8192 tokens, the three together against one segment: 1 head of 64 x 128 116 and 357 us,
+// 16 heads 162 and 373, 24 heads 225 and 373, 48 heads (not cut) 395 in four.
 void segments(DeltaDims* d) {
-  const double own = (double)d->B * d->H * d->Ps / 16, more = own + (double)d->B * d->H * d->NP / 16;
-  auto chunk = [](double strips) {
-    const double x = strips / (4 * 152);
-    return x <= 1.0 ? 2.8 : 1.6 * (x < 2.0 ? 2.0 : x);
+  const double heads = (double)d->B * d->H, vt = (d->Ps + kC - 1) / kC, mt = d->NP / kC;
+  auto waves = [](double blocks) { return ceil(blocks / (2 * 152)); };
+  auto chain = [&](double blocks) { return blocks <= 152 ? 2.9 : 5.1 * waves(blocks); };
+  auto ends = [&](double blocks) {
+    return blocks <= 100 ? 3.2 : blocks <= 2 * 152 ? 4.5 : 3.8 * waves(blocks);
   };
   d->W = 1, d->cs = d->nc;
-  double best = d->nc * chunk(own);
+  double best = d->nc * chain(heads * vt);
   for (int w = 2; w <= 32 && d->nc / w >= 8; w *= 2) {
     const int cs = (d->nc + w - 1) / w;
-    const double t = cs * (chunk(more * (w - 1)) + chunk(own * w)) + 6.0 * (w - 1);
-    if (t < 0.9 * best) best = t, d->W = w, d->cs = cs;
+    const double join = heads * d->Ps / 16 / 100;
+    const double t = cs * (ends(heads * (vt * (w - 1) + mt * (w - 2))) + chain(heads * vt * w)) +
+                     3.8 * (w - 1) * (join < 1.0 ? 1.0 : join) + 8.0;
+    if (t < 0.85 * best || (d->W > 1 && t < best)) best = t, d->W = w, d->cs = cs;
   }
 }
 
@@ -1974,7 +1989,7 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
     DELTA_LAUNCH("k_delta_ends", ends, (int64_t)d.B * d.H * (d.W - 1) * ((d.Ps + kC - 1) / kC + NP / kC),
                  kChainThreads, (chain_smem<T, NP>()), d, v, in.init, in.lengths, w, nullptr,
                  device_status_ptr());
-    DELTA_LAUNCH("k_delta_join", k_delta_join<NP>, (int64_t)d.B * d.H * (d.Ps / 16), NP, 0, d, w);
+    DELTA_LAUNCH("k_delta_join", k_delta_join<NP>, (int64_t)d.B * d.H * (d.Ps / 16), 4 * NP, 0, d, w);
   }
   const auto chain = k_delta_chain<T, NP, BWD, false>;
   DELTA_LAUNCH("k_delta_chain", chain, chains * d.W, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,

@@ -8,7 +8,7 @@ and the current stream passed on.
 from __future__ import annotations
 
 from . import _native
-from .layer_ops import (_CODE, _F32, _I32, _at, _check, _code, _current_device, _device,
+from .layer_ops import (_CODE, _F32, _I32, _at, _check, _code, _current_device, _device, _empty,
                         _empty_like, _fail, _native_lib, _output, _outputs, _rows, _scratch, _stream)
 
 
@@ -190,11 +190,40 @@ def qk_norm_fwd(q, k, w_q=None, w_k=None, freq=None, positions=None, l2: bool = 
     seqlen for one token a row; both may be column ranges of wider tensors.  w_q, w_k
     (headdim,) float32 or None; freq float32, None: no rotation; positions (batch, seqlen), or
     (batch,), int32; None: 0, 1, ... along seqlen.  headdim <= 1024."""
-    lib = _native_lib()
-    dev, shape, odt, p = _qk_inputs(q, k, w_q, w_k, freq, positions, l2, interleaved, eps, out_dtype)
-    q_out = _output(q_out, "q_out", q.shape, odt, q)
-    k_out = _output(k_out, "k_out", k.shape, odt, q)
-    st = lib.ssd_qk_norm_fwd(shape, *p, q_out.data_ptr(), k_out.data_ptr(), _stream(dev))
+    lib, qs, ks, xd, dev = _native_lib(), q.shape, k.shape, q.dtype, q.get_device()
+    n, st, sk = len(qs), q.stride(), k.stride()
+    # (a decoding step's call, as in layer_ops: its checks in one condition)
+    if (n > 2 and dev >= 0 and dev == _current_device() and xd in _CODE and out_dtype is None
+            and q_out is None and k_out is None and n < 5 and len(ks) == n
+            and ks[:n - 2] == qs[:n - 2] and ks[n - 1] == qs[n - 1] and k.dtype is xd
+            and k.get_device() == dev
+            and st[n - 1] == 1 and sk[n - 1] == 1 and st[n - 2] == qs[n - 1] and sk[n - 2] == qs[n - 1]
+            and st[n - 3] >= qs[n - 2] * qs[n - 1] and sk[n - 3] >= ks[n - 2] * qs[n - 1]
+            and (w_q is None or (w_q.shape == qs[n - 1:] and w_q.dtype is _F32
+                                 and w_q.get_device() == dev and w_q.is_contiguous()))
+            and (w_k is None or (w_k.shape == qs[n - 1:] and w_k.dtype is _F32
+                                 and w_k.get_device() == dev and w_k.is_contiguous()))
+            and (positions is None or (positions.shape == qs[:n - 2] and positions.dtype is _I32
+                                       and positions.get_device() == dev and positions.is_contiguous()))
+            and (freq is None or (freq.dim() == 1 and freq.dtype is _F32 and freq.get_device() == dev
+                                  and freq.is_contiguous() and 2 * freq.shape[0] <= qs[n - 1]
+                                  and (n == 4 or positions is not None)))):
+        code = _CODE[xd]
+        shape = _native.QkNormShape(qs[0], qs[1] if n == 4 else 1, qs[n - 2], ks[n - 2], qs[n - 1],
+                                    0 if freq is None else 2 * freq.shape[0], st[n - 3], sk[n - 3],
+                                    st[0], sk[0], eps, 1 if l2 else 0, 1 if interleaved else 0, code, code)
+        q_out = _empty(qs, dtype=xd, device=q.device)
+        k_out = _empty(ks, dtype=xd, device=q.device)
+        st = lib.ssd_qk_norm_fwd(
+            shape, q.data_ptr(), k.data_ptr(), None if w_q is None else w_q.data_ptr(),
+            None if w_k is None else w_k.data_ptr(), None if freq is None else freq.data_ptr(),
+            None if positions is None else positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+            _stream(dev))
+    else:
+        dev, shape, odt, p = _qk_inputs(q, k, w_q, w_k, freq, positions, l2, interleaved, eps, out_dtype)
+        q_out = _output(q_out, "q_out", q.shape, odt, q)
+        k_out = _output(k_out, "k_out", k.shape, odt, q)
+        st = lib.ssd_qk_norm_fwd(shape, *p, q_out.data_ptr(), k_out.data_ptr(), _stream(dev))
     if st:
         _fail("ssd_qk_norm_fwd", st)
     return q_out, k_out

@@ -89,6 +89,16 @@ def test_delta_matches_oracle(cuda_lib, case):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("case", [
+    # few heads over many chunks: sequences long enough to be cut into segments, one that
+    # ends inside one, one of them empty
+    (3, 2100, 2, 1, 24, 40, "f32", True, [2100, 700, 0]),
+    (2, 1500, 1, 1, 72, 128, "bf16", False, [1025, 1500]),
+    (1, 4200, 2, 2, 16, 64, "mixed", True, None)])
+def test_delta_of_long_sequences_of_few_heads(cuda_lib, case):
+    test_delta_matches_oracle(cuda_lib, case)
+
+
 def test_delta_without_bias_or_final_gradient(cuda_lib):
     a, _, dy, _, _ = delta_case(2, 77, 2, 1, 16, 16, "f32", False, None)
     x = [None if n == "dt_bias" else dev(m) for n, m in a.items()]
