@@ -656,7 +656,7 @@ struct ChainBars {
   uint64_t full[2], empty[2];
   int abort, pad[3];
 };
-constexpr int kChainWarps = 4, kFillWarp = 4;
+constexpr int kFillWarp = 4;
 
 // A strip's 16 value columns of a raw tile as its rows: the accumulator of the transpose.
 template <typename T>
@@ -754,12 +754,13 @@ struct Piece {
   bool moving, last, idle;  // rows of the move; holds the sequence's last chunk
   int64_t bh;
 };
-template <int NP, bool SEG>
+// (REV: of the backward's chain, whose pass over segments leaves out the first one.)
+template <int NP, bool SEG, bool REV>
 __device__ __forceinline__ Piece piece(const DeltaDims& d, const int* lengths) {
   Piece p;
   const unsigned vt = (d.Ps + kC - 1) / kC, tiles = SEG ? vt + NP / kC : vt, segs = SEG ? d.W - 1 : d.W;
   const unsigned x = blockIdx.x / tiles, tile = blockIdx.x - x * tiles, bh = x / segs;
-  p.seg = (int)(x - bh * segs);
+  p.seg = (int)(x - bh * segs) + (SEG && REV ? 1 : 0);
   p.bh = bh;
   p.b = (int)(bh / (unsigned)d.H), p.h = (int)(bh - (unsigned)p.b * d.H);
   p.n = tokens_of(d, lengths, p.b);
@@ -770,15 +771,18 @@ __device__ __forceinline__ Piece piece(const DeltaDims& d, const int* lengths) {
   p.p0 = (int)(p.moving ? tile - vt : tile) * kC;
   p.strips = min(4, ((p.moving ? NP : d.Ps) - p.p0) / 16);
   p.last = p.count > 0 ? p.c0 + p.count == nc : p.seg == 0;
-  p.idle = SEG ? p.moving && p.seg == 0 : p.count == 0 && !p.last;
+  p.idle = SEG ? p.moving && p.seg == (REV ? d.W - 1 : 0) : p.count == 0 && !p.last;
   return p;
 }
-template <int NP, bool SEG>
+// The state that a block starts from: the sequence's first (for the backward: last) one,
+// what the join left, or in the pass over segments zeros or the identity's rows.
+template <int NP, bool SEG, bool REV>
 __device__ __forceinline__ void start_state(float (&S)[NP / 8][4], const DeltaDims& d, const Piece& p,
                                             int row, const float* first, const float* front, int lane) {
-  if (!SEG && p.seg > 0) {
+  const bool whole = REV ? p.last : p.seg == 0;
+  if (!SEG && !whole) {
     load_state<NP>(S, front + ((p.bh * d.W + p.seg) * d.Ps + row) * NP, 16, NP, lane);
-  } else if (SEG && (p.moving || p.seg > 0)) {
+  } else if (SEG && (p.moving || !whole)) {
     const int r = row + (lane >> 2), c = (lane & 3) * 2;
 #pragma unroll
     for (int t = 0; t < NP / 8; ++t)
@@ -803,17 +807,18 @@ __device__ __forceinline__ void end_state(const float (&S)[NP / 8][4], const Del
 
 // The state in front of each segment: front_0 is the sequence's first state, front_1 =
 // ends_0 (which starts from it), front_j+1 = ends_j + front_j move_j.  16 rows a block;
-// four groups of threads take a quarter of the products' sums each.
-template <int NP>
+// four groups of threads take a quarter of the products' sums each.  REV: the gradient
+// behind each segment, from the last one's (0: it starts from the sequence's) to the first.
+template <int NP, bool REV>
 __global__ void __launch_bounds__(4 * NP) k_delta_join(DeltaDims d, DeltaWs w) {
   __shared__ float s[16][NP], part[4][16][NP];
   const int col = threadIdx.x % NP, g = threadIdx.x / NP, strips = d.Ps / 16;
   const int64_t bh = blockIdx.x / strips;
   const int row = (int)(blockIdx.x % strips) * 16;
   for (int j = 1; j < d.W; ++j) {
-    const int64_t at = bh * d.W + j - 1;
+    const int64_t at = bh * d.W + (REV ? d.W - j : j - 1);
     const float* e = w.ends + (at * d.Ps + row) * NP + col;
-    float* f = w.front + ((at + 1) * d.Ps + row) * NP + col;
+    float* f = w.front + ((REV ? at - 1 : at + 1) * d.Ps + row) * NP + col;
     float own[4];  // rows 4 g .. of this column
 #pragma unroll
     for (int r = 0; r < 4; ++r) own[r] = e[(4 * g + r) * NP];
@@ -866,7 +871,7 @@ __global__ void __launch_bounds__(192, 2)
   extern __shared__ __align__(16) unsigned char smem[];
   ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const Piece pc = piece<NP, SEG>(d, lengths);
+  const Piece pc = piece<NP, SEG, false>(d, lengths);
   const int p0 = pc.p0, b = pc.b, h = pc.h, n = pc.n, c0 = pc.c0, nc = pc.count;
   const int64_t bh = pc.bh;
   if (pc.idle) return;
@@ -917,7 +922,7 @@ __global__ void __launch_bounds__(192, 2)
   if (strip >= strips) return;
   const int row = p0 + strip * 16;  // this warp's first value row
   float S[NP / 8][4];
-  start_state<NP, SEG>(S, d, pc, row, init, w.front, lane);
+  start_state<NP, SEG, false>(S, d, pc, row, init, w.front, lane);
   const int t2 = (lane & 3) * 2;
   for (int c = 0; c < nc; ++c) {
     const int s = c & 1;
@@ -1165,7 +1170,7 @@ constexpr size_t back_smem() { return sizeof(ChainBars) + 2 * back_stage<T, NP>(
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
 //     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
 // in the manner of k_delta_chain: 444 products a chunk.
-template <typename T, int NP>
+template <typename T, int NP, bool SEG>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
                  const int* __restrict__ lengths, DeltaWs w, float* __restrict__ dinit, int* status) {
@@ -1173,12 +1178,11 @@ __global__ void __launch_bounds__(kChainThreads)
   extern __shared__ __align__(16) unsigned char smem[];
   ChainBars& sm = *reinterpret_cast<ChainBars*>(smem);
   const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const unsigned ptiles = (d.Ps + kC - 1) / kC, bhu = blockIdx.x / ptiles;
-  const int p0 = (int)(blockIdx.x - bhu * ptiles) * kC, b = (int)(bhu / (unsigned)d.H);
-  const int h = (int)(bhu - (unsigned)b * d.H);
-  const int64_t bh = bhu;
-  const int n = tokens_of(d, lengths, b), nc = (n + kC - 1) / kC;
-  const int strips = min(kChainWarps, (d.Ps - p0) / 16);
+  const Piece pc = piece<NP, SEG, true>(d, lengths);
+  const int p0 = pc.p0, b = pc.b, h = pc.h, n = pc.n, nc = pc.count, end = pc.c0 + pc.count - 1;
+  const int64_t bh = pc.bh;
+  if (pc.idle) return;
+  const int strips = pc.strips;
   unsigned char* const stages = smem + sizeof(ChainBars);
   constexpr size_t STAGE = back_stage<T, NP>(), IMG = NI * kC * LD * 2;
   constexpr size_t YT = sizeof(Gates) + 2 * IMG;
@@ -1201,7 +1205,7 @@ __global__ void __launch_bounds__(kChainThreads)
     const int64_t img = ((int64_t)b * d.G + h / d.rep) * d.nc * NI * kC * LD;
     int i = 0;  // chunks filled, the last one first
     for (; i < nc; ++i) {
-      const int s = i & 1, c = nc - 1 - i;
+      const int s = i & 1, c = end - i;
       if (!tc::mbar_wait(&sm.empty[s], ((i >> 1) & 1) ^ 1, status, &sm.abort)) break;
       unsigned char* at = stages + s * STAGE;
       uint64_t* bar = &sm.full[s];
@@ -1212,8 +1216,10 @@ __global__ void __launch_bounds__(kChainThreads)
         tc::bulk_g2s(at + YT + kC * RP * sizeof(T), w.X + (bh * d.nc + c) * (2 * kC * kTP),
                      2 * kC * kTP * 2, bar);
       }
-      const uint32_t raw = raw_rows<T>(reinterpret_cast<T*>(at + YT), yg + (int64_t)c * kC * ys, ys,
-                                       min(kC, n - c * kC), d.P - p0, d.vdy, bar, lane);
+      uint32_t raw = 0;
+      if (!SEG || !pc.moving)
+        raw = raw_rows<T>(reinterpret_cast<T*>(at + YT), yg + (int64_t)c * kC * ys, ys,
+                          min(kC, n - c * kC), d.P - p0, d.vdy, bar, lane);
       if (lane == 0)
         tc::mbar_arrive_expect_tx(bar, raw + sizeof(Gates) + 2 * IMG + 2 * kC * kTP * 2);
       else
@@ -1225,10 +1231,10 @@ __global__ void __launch_bounds__(kChainThreads)
   if (strip >= strips) return;
   const int row = p0 + strip * 16;
   float S[NP / 8][4];
-  load_state<NP>(S, dfinal ? dfinal + (bh * d.P + row) * d.N : nullptr, d.P - row, d.N, lane);
+  start_state<NP, SEG, true>(S, d, pc, row, dfinal, w.front, lane);
   const int t2 = (lane & 3) * 2;
   for (int i = 0; i < nc; ++i) {
-    const int s = i & 1, c = nc - 1 - i;
+    const int s = i & 1, c = end - i;
     if (!tc::mbar_wait(&sm.full[s], (i >> 1) & 1, status, &sm.abort)) return;
     const unsigned char* at = stages + s * STAGE;
     const Gates& g = *reinterpret_cast<const Gates*>(at);
@@ -1242,9 +1248,10 @@ __global__ void __launch_bounds__(kChainThreads)
     const Scale s0 = scale_of(m0), s1 = scale_of(m1);
     float r[8][4];
     state_times_keys<NI, NP>(r, S, kt, s0, s1, lane);
-    store_strip<NP / 8>(w.dS, srow, S, lane);
+    if constexpr (!SEG) store_strip<NP / 8>(w.dS, srow, S, lane);
     scale_tokens(r, g.fu, t2, s0.inv, s1.inv);
-    store_strip<8>(w.Zd, srow, r, lane);
+    if constexpr (!SEG) store_strip<8>(w.Zd, srow, r, lane);
+    if (!SEG || !pc.moving)
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       const float4 e = frag(w.E, srow, 8, lane)[t * 32];
@@ -1268,7 +1275,7 @@ __global__ void __launch_bounds__(kChainThreads)
         });
     }
     scale_tokens(u, g.fx, t2, q0.inv, q1.inv);
-    store_strip<8>(w.dR, srow, u, lane);
+    if constexpr (!SEG) store_strip<8>(w.dR, srow, u, lane);
     // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
     scale_tokens(u, g.fz, t2, -1.f, -1.f);
     raw_strip<T>(r, yt, strip, lane);
@@ -1278,15 +1285,15 @@ __global__ void __launch_bounds__(kChainThreads)
     row_max<8>(u, b0, b1);
     const Scale u0 = scale_of(fmaxf(fmaxf(a0, b0), m0 * kBelow)),
                 u1 = scale_of(fmaxf(fmaxf(a1, b1), m1 * kBelow));
-    const float end = ex2(g.gh[kC - 1]);
-    scale_rows(S, end * u0.s, end * u1.s);
+    const float keep = ex2(g.gh[kC - 1]);
+    scale_rows(S, keep * u0.s, keep * u1.s);
     add_outer<NI, NP>(S, r, qt, u0.s, u1.s, lane);
     add_outer<NI, NP>(S, u, kt, u0.s, u1.s, lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
     scale_rows(S, u0.inv, u1.inv);
   }
-  if (dinit) store_state<NP>(dinit + (bh * d.P + row) * d.N, S, d.P - row, d.N, lane);
+  end_state<NP, SEG>(S, d, pc, row, pc.seg == 0 ? dinit : nullptr, w, lane);
 }
 
 // ---------------------------------------------------------------------- grad
@@ -1989,7 +1996,7 @@ int delta_states(const DeltaDims& d, const DeltaIn& in, const void* dy, const De
     DELTA_LAUNCH("k_delta_ends", ends, (int64_t)d.B * d.H * (d.W - 1) * ((d.Ps + kC - 1) / kC + NP / kC),
                  kChainThreads, (chain_smem<T, NP>()), d, v, in.init, in.lengths, w, nullptr,
                  device_status_ptr());
-    DELTA_LAUNCH("k_delta_join", k_delta_join<NP>, (int64_t)d.B * d.H * (d.Ps / 16), 4 * NP, 0, d, w);
+    DELTA_LAUNCH("k_delta_join", (k_delta_join<NP, false>), (int64_t)d.B * d.H * (d.Ps / 16), 4 * NP, 0, d, w);
   }
   const auto chain = k_delta_chain<T, NP, BWD, false>;
   DELTA_LAUNCH("k_delta_chain", chain, chains * d.W, kChainThreads, (chain_smem<T, NP>()), d, v, in.init,
@@ -2017,8 +2024,16 @@ int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, c
   const T *q = static_cast<const T*>(in.q), *k = static_cast<const T*>(in.k),
           *dy = static_cast<const T*>(g.dy);
   const int64_t chains = (int64_t)d.B * d.H * ((d.Ps + kC - 1) / kC);
-  const auto back = k_delta_back<T, NP>;
-  DELTA_LAUNCH("k_delta_back", back, chains, kChainThreads, (back_smem<T, NP>()), d, dy, g.dfinal,
+  if (d.W > 1) {
+    const auto ends = k_delta_back<T, NP, true>;
+    DELTA_LAUNCH("k_delta_back_ends", ends,
+                 (int64_t)d.B * d.H * (d.W - 1) * ((d.Ps + kC - 1) / kC + NP / kC), kChainThreads,
+                 (back_smem<T, NP>()), d, dy, g.dfinal, in.lengths, w, nullptr, device_status_ptr());
+    DELTA_LAUNCH("k_delta_join", (k_delta_join<NP, true>), (int64_t)d.B * d.H * (d.Ps / 16), 4 * NP, 0, d,
+                 w);
+  }
+  const auto back = k_delta_back<T, NP, false>;
+  DELTA_LAUNCH("k_delta_back", back, chains * d.W, kChainThreads, (back_smem<T, NP>()), d, dy, g.dfinal,
                in.lengths, w, g.dinit, device_status_ptr());
   const auto grad = k_delta_grad<T, TO, NP>;
   TO *dq = static_cast<TO*>(g.dq), *dk = static_cast<TO*>(g.dk);
