@@ -110,19 +110,49 @@ __device__ __forceinline__ void a_from_acc(uint32_t (&a)[NPL][4], const float (&
 
 // c0, c1 (two tiles of 8 columns) += A B over plane products i + j < M; B of plane j
 // comes from load(j, regs).
+// An accumulation truncates, which adds up where one accumulator takes many: of two fp32
+// operands the lower products are summed apart (from zero, added by a rounded fp32 add),
+// and the accumulator takes one product of the upper planes.  (Six into one: 3e-6 of an
+// fp32 result; so: 6e-7.)
+template <int NA, int NB, int M>
+constexpr bool kApart = NA == 3 && NB == 3 && M == 3;
+__device__ __forceinline__ void add4(float (&c)[4], const float (&t)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] += t[e];
+}
+// The products with plane j of B, into the accumulator or what is summed apart.
+template <int NA, int M, bool APART>
+__device__ __forceinline__ void plane_products(float (&c0)[4], float (&c1)[4], float (&t0)[4],
+                                               float (&t1)[4], const uint32_t (&a)[NA][4],
+                                               const uint32_t (&b)[4], int j) {
+#pragma unroll
+  for (int n = 0; n < NA; ++n) {
+    const int i = APART ? NA - 1 - n : n;  // apart: the upper planes' product last
+    if (i + j < M) {
+      if constexpr (APART) {
+        if (i + j > 0) {
+          mma16816(t0, a[i], b[0], b[1]);
+          mma16816(t1, a[i], b[2], b[3]);
+          continue;
+        }
+        add4(c0, t0);
+        add4(c1, t1);
+      }
+      mma16816(c0, a[i], b[0], b[1]);
+      mma16816(c1, a[i], b[2], b[3]);
+    }
+  }
+}
 template <int NA, int NB, int M, typename Load>
 __device__ __forceinline__ void mma_planes(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
                                            Load&& load) {
+  float t0[4] = {}, t1[4] = {};
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
+  for (int n = 0; n < NB; ++n) {
+    const int j = kApart<NA, NB, M> ? NB - 1 - n : n;
     uint32_t b[4];
     load(j, b);
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (i + j < M) {
-        mma16816(c0, a[i], b[0], b[1]);
-        mma16816(c1, a[i], b[2], b[3]);
-      }
+    plane_products<NA, M, kApart<NA, NB, M>>(c0, c1, t0, t1, a, b, j);
   }
 }
 
@@ -200,22 +230,15 @@ template <int NA, int M, int NF, int ME, int NB, typename Load>
 __device__ __forceinline__ void mma_planes2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4],
                                             float (&e0)[4], float (&e1)[4], const uint32_t (&f)[NF][4],
                                             Load&& load) {
+  constexpr bool APART = kApart<NA, NB, M> && kApart<NF, NB, ME>;  // both of fp32 operands
+  float t0[4] = {}, t1[4] = {}, u0[4] = {}, u1[4] = {};
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
+  for (int n = 0; n < NB; ++n) {
+    const int j = APART ? NB - 1 - n : n;
     uint32_t b[4];
     load(j, b);
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (i + j < M) {
-        mma16816(c0, a[i], b[0], b[1]);
-        mma16816(c1, a[i], b[2], b[3]);
-      }
-#pragma unroll
-    for (int i = 0; i < NF; ++i)
-      if (i + j < ME) {
-        mma16816(e0, f[i], b[0], b[1]);
-        mma16816(e1, f[i], b[2], b[3]);
-      }
+    plane_products<NA, M, APART>(c0, c1, t0, t1, a, b, j);
+    plane_products<NF, ME, APART>(e0, e1, u0, u1, f, b, j);
   }
 }
 
