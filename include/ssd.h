@@ -370,7 +370,8 @@ int ssd_scan_get_config(const ssd_shape* shape, ssd_scan_config* out);
  * place.  Pointers must be aligned to their element size; 16-byte alignment of
  * pointers and rows lets the kernels use wide accesses.  bf16 inputs give bf16
  * or f32 outputs, f32 inputs f32 ones (else SSD_ERR_UNSUPPORTED).  Every call is
- * asynchronous on `stream`, waits for nothing on the device, and returns
+ * asynchronous on `stream` and waits for nothing but its own copies on the device
+ * (bounded: 1 s, then SSD_ERR_TIMEOUT in the device status word), and returns
  * SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE (workspace NULL,
  * misaligned or too small) or SSD_ERR_CUDA.  All sums over rows, positions or
  * channels are taken in a fixed order in f32: repeated calls give bit-identical
@@ -515,7 +516,11 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
  * final_states (batch, nheads, headdim, dstate) f32 or NULL.  Keys of a length up
  * to 1 keep the state bounded (ssd_qk_norm_fwd with l2); the call does not
  * normalise them.  dstate <= 128, headdim <= 256, batch and nheads < 65536,
- * seqlen < 2^30, batch * nheads * ceil(seqlen / 64) < 2^31.  A step's decay below
+ * seqlen < 2^30, batch * nheads < 2^29, batch * nheads * ceil(seqlen / 64) < 2^31.
+ * The backward forms the states again: dy and the forward's inputs are all that it
+ * needs.  Long sequences of few heads are cut into segments that run at once and are
+ * joined by products of their transitions: keys that let a state grow past f32's range
+ * between two joins give infinities or NaN there.  A step's decay below
  * 2^-150 counts as 2^-150, 0 in f32.  Workspace of the size query's bytes (0 for a
  * rejected shape), 16-byte aligned, caller-owned. */
 typedef struct {

@@ -12,11 +12,22 @@
 // chunk does by itself (k_delta_prep: X; k_delta_out: Y) and the chain over the chunks
 // (k_delta_chain: U and the states), whose rows p of the state are independent.
 //
-// Numerics: all matrix products run on the tensor cores with bf16 planes of fp32
-// values (warp_mma.cuh), three planes wherever the result reaches a state, a state's
-// gradient or a parameter's gradient; two where it only reaches a bf16 output.  Log
-// decays are summed and kept as two floats, so that a strong decay early in
-// a chunk takes nothing from the differences behind it.
+// Numerics: all matrix products run on the tensor cores with planes of fp32 values
+// (warp_mma.cuh).  What reaches a state, a state's gradient or a parameter's gradient is
+// three planes of bf16 (X and the pairs' gradients) or two of fp16 with rows scaled (the
+// chains), 2^-23 of a row's largest value; what only reaches a bf16 output is two planes
+// of bf16, 2^-16.  Sums and states are fp32.  Log decays are summed and kept as two floats,
+// so that a strong decay early in a chunk takes nothing from the differences behind it.
+//
+// 64 tokens a chunk: X takes 64^2 / 2 products a token, and the chain's length is the
+// number of chunks.  tcgen05 was left aside: tiles of 64 rows run at half its rate, every
+// operand is an fp32 value split into planes first, and the chain's three dependent
+// products a chunk would each go through tensor memory and back, where mma.sync takes the
+// accumulators as its next left operand where they are.  Its rate, measured as 8 clocks an
+// instruction and SM quarter, is what the products' bounds below are of.
+//
+// Times below are, unless said, of a training step's sequences: 4 x 4096 tokens of 24 heads
+// in 12 groups, 64 value rows, 128 key columns, bf16, that is 6144 chunks of a head.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -354,9 +365,12 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
 // block i of I + M (by substitution, a column a lane; stable whatever the keys, where a
 // run of equal keys makes I + M ill suited to a power series),
 //     X_jj = D_j,   X_ij^T = -(sum_{j <= l < i} X_lj^T M_il^T) D_i^T,
-// a chain of 16 x 16 products whose left operands are the last accumulators.  (With both
-// halves of X merged by fp32 products from shared memory the kernel was bound by shared
-// memory, 62 us for 3072 chunks at 88 % of its rate.)
+// a chain of 16 x 16 products whose left operands are the last accumulators.  Merging
+// halves of X by fp32 products from shared memory ran at 88 % of shared memory's rate and
+// was slower; what bounds this form is the latency of its dependent steps (substitution,
+// then four products deep, then the gates' sums), with four blocks an SM to cover it:
+// 110 us forward and 200 us backward, which also has Q K^T and E^T.  (Several heads a block
+// keep K K^T but spill: 261 -> 272 us and more at 16384 chunks.)
 template <typename T, int NP, bool BWD>
 __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) : 1)
     k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
@@ -641,6 +655,7 @@ __device__ __forceinline__ uint32_t raw_rows(T* dst, const T* src, int64_t ld, i
   cv = min(cv, kC);
   for (int r = max(rv, 0) + lane; r < kC; r += 32)
     for (int c = 0; c < kC; ++c) dst[r * RP + c] = from_f<T>(0.f);
+  if (rv < kC) tc::fence_async_smem();  // the zeros, before a later chunk's copies
   if (vec) {
     for (int r = lane; r < rv; r += 32) tc::bulk_g2s(dst + r * RP, src + r * ld, cv * sizeof(T), bar);
     return (uint32_t)(rv * cv * sizeof(T));
@@ -853,8 +868,11 @@ __global__ void __launch_bounds__(4 * NP) k_delta_join(DeltaDims d, DeltaWs w) {
 // each left operand formed from the last accumulator.
 // Left operands are two fp16 planes of rows scaled by their largest value, K is one
 // (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
-// bf16 take 504.  The products are issued by one warp per SM quarter at 8 clocks each,
-// which bounds a chunk by 1.3 us.  KEEP: also writes b e^G Z, for the backward.
+// bf16 take 504.  A warp issues its strip's at 8 clocks each, which bounds a chunk by 1.3 us;
+// it takes 2.9 with a block an SM and 5.1 with two (168 registers a thread, so that two
+// fit), the rest of which is the accumulators' way into operands: maxima, scales, planes.
+// 200 us a pass (96 chains of 64 chunks); two warps a strip, which exchange halves, were
+// slower (3.3).  KEEP: also writes b e^G Z, for the backward.
 //
 // Few heads leave most of the machine idle, so a long sequence is cut into W segments of cs
 // chunks.  A chunk's step is linear in the state and the values, row by row: the state
@@ -1014,7 +1032,10 @@ struct OutSmem {
 // warp, in passes of 64 value columns of a head.  Q K^T is formed once for the heads, by
 // halves of the tokens; a head's decays make its planes of it.  The next pass's states and
 // corrections are on their way under a pass's products.  Bound by shared memory (the
-// states' planes are read by four warps).
+// states' planes are read by four warps) and the work around the products: 135 us, of
+// which reading states and corrections and writing y would take 48 at the copy rate.
+// Outputs formed in the chain, with operands of 11 bits, saved an eighth of a prompt but
+// were off by 2^-12 of the largest y.
 template <typename T, typename TO, int NP>
 __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2 ? 2 : 1)
     k_delta_out(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
@@ -1169,7 +1190,8 @@ constexpr size_t back_smem() { return sizeof(ChainBars) + 2 * back_stage<T, NP>(
 // state behind the chunk in registers:
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
 //     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
-// in the manner of k_delta_chain: 444 products a chunk.
+// in the manner of k_delta_chain: 444 products a chunk, 284 us (96 chains of 64 chunks,
+// 4.4 us each).
 template <typename T, int NP, bool SEG>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
@@ -1333,6 +1355,11 @@ struct GradSmem {
 // scale e^G q . (dY S0) - dR . (b e^G S0 k) - U . (e^(G63 - G) dS k), where what the
 // last token's G takes from the state behind the chunk is added.  Row and column sums
 // are of the same products, so that what cancels in their difference cancels exactly.
+// Twelve products of 64 x 64 x 64 to 128 a tile of value rows, whose operands each become
+// planes in shared memory first: 700 us, 32 thousand clocks a head and chunk of an SM where
+// the products alone take 11.  Issue slots are 44 % used, the tensor cores 26 %; a second
+// block does not fit (shared memory), and fetching the next head's tiles into registers
+// spills.
 template <typename T, typename TO, int NP>
 __global__ void __launch_bounds__(kGradThreads, 1)
     k_delta_grad(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
@@ -1843,7 +1870,9 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------- host
 
 // One part for each block of the heads of a group, so that the gradient's blocks fill
-// the machine; each block sums its heads in registers.
+// the machine; each block sums its heads in registers.  Blocks, and forward and backward
+// of 1 x 1024 and 1 x 256 tokens of 64 heads in 8 groups: gradient 152, outputs 608: 403 and
+// 150 us; 304 and 1216: 409 and 135; 608 and 2432: 412 and 136.
 constexpr int kGradBlocks = 2 * 152, kOutBlocks = 8 * 152;
 
 // Segments of the chains: as many, up to 32 of at least 8 chunks, as make the modelled time
