@@ -566,3 +566,45 @@ def test_a_layer_of_them_trains_and_decodes(cuda_lib):
         out = cuda_lib.gated_norm_fwd(y.flatten(-2), z[:, i].contiguous(), norm, H * P)[0]
         assert float((out - full[:, i]).abs().max()) <= 1e-4 * float(full.abs().max())
     assert float((S - S_all).abs().max()) <= 1e-4 * float(S_all.abs().max())
+
+
+def test_calls_of_two_threads(cuda_lib):
+    """Two host threads at the same time, each with shapes and a stream of its own: the bits
+    of the same calls one after another (sizes whose shared memory differs)."""
+    import threading
+
+    import torch
+    jobs = []
+    for i, (case, D) in enumerate([((2, 190, 6, 3, 128, 128, "bf16", True, None), 1024),
+                                   ((1, 1100, 2, 1, 24, 40, "f32", True, [1001]), 700)]):
+        it, _ = types(case[6])
+        a, init, dy, _, ln = delta_case(*case)
+        x, more = on_gpu(a, it), dict(init_states=dev(init), lengths=dev(ln, torch.int32))
+        g = np.random.default_rng(i)
+        q, k, dq, dk = (dev(g.standard_normal((3, 20, 2, D)), it) for _ in range(4))
+        w, f = dev(g.standard_normal(D), torch.float32), dev(g.random(D // 4), torch.float32)
+
+        def run(x=x, more=more, dy=dev(dy, it), q=q, k=k, w=w, f=f, dq=dq, dk=dk):
+            b = cuda_lib.gated_delta_bwd(*x, dy, **more)
+            n = cuda_lib.qk_norm_bwd(q, k, w, w, f, None, dq, dk)
+            return [*cuda_lib.gated_delta_fwd(*x, **more), *b.values(), *n.values()]
+        jobs.append(run)
+    want = [[t.clone() for t in run()] for run in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(run, ref):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = run()
+                    torch.cuda.current_stream().synchronize()
+                    wrong.extend(not torch.equal(a, b) for a, b in zip(got, ref))
+        except Exception as e:  # noqa: BLE001 - handed to the test's own thread
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=z) for z in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(wrong) == 20 * sum(len(w) for w in want) and not any(wrong), [w for w in wrong if w][:3]
