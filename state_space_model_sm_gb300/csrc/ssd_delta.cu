@@ -368,9 +368,11 @@ __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
 // a chain of 16 x 16 products whose left operands are the last accumulators.  Merging
 // halves of X by fp32 products from shared memory ran at 88 % of shared memory's rate and
 // was slower; what bounds this form is the latency of its dependent steps (substitution,
-// then four products deep, then the gates' sums), with four blocks an SM to cover it:
-// 110 us forward and 200 us backward, which also has Q K^T and E^T.  (Several heads a block
-// keep K K^T but spill: 261 -> 272 us and more at 16384 chunks.)
+// then four products deep, then the gates' sums), with four to six blocks an SM to cover it:
+// 287 us for a training step's two passes, of which the backward's also has Q K^T and E^T.
+// A strip's work differs from the next's, and a warp's place in its block decides its
+// scheduler, so strips are turned from block to block (313 us without).  (Several heads a
+// block keep K K^T but spill: 261 -> 272 us and more at 16384 chunks.)
 template <typename T, int NP, bool BWD>
 __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) : 1)
     k_delta_prep(DeltaDims d, const T* __restrict__ q, const T* __restrict__ k,
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) :
   bf16* const Qt = Kt + NI * kC * LD;
   bf16* const yt = reinterpret_cast<bf16*>(smem + sizeof(Gates) + SM::one);
   bf16* const Mp = Kt;
-  const int tid = threadIdx.x, lane = tid & 31, strip = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, strip = ((tid >> 5) + blockIdx.x) & 3;
   float* const diag = reinterpret_cast<float*>(smem + sizeof(Gates) + SM::m) + strip * 16 * 20;
   const Place pl = place(d, blockIdx.x);
   const int n = tokens_of(d, lengths, pl.b), t0 = pl.c * kC;
@@ -1032,7 +1034,8 @@ struct OutSmem {
 // warp, in passes of 64 value columns of a head.  Q K^T is formed once for the heads, by
 // halves of the tokens; a head's decays make its planes of it.  The next pass's states and
 // corrections are on their way under a pass's products.  Bound by shared memory (the
-// states' planes are read by four warps) and the work around the products: 135 us, of
+// states' planes are read by four warps; by two, with 32 tokens by 16 columns a warp, it
+// spills: 295 -> 346 us for 16384 chunks) and the work around the products: 134 us, of
 // which reading states and corrections and writing y would take 48 at the copy rate.
 // Outputs formed in the chain, with operands of 11 bits, saved an eighth of a prompt but
 // were off by 2^-12 of the largest y.
@@ -1048,7 +1051,10 @@ __global__ void __launch_bounds__(kOutThreads, sizeof(T) == 2 && sizeof(TO) == 2
   bf16* const kt = qt + SM::raw / 2;  // and the state's planes after the keys'
   bf16* const ut = kt + SM::one / 2;
   bf16* const pt = ut + SM::tok / 2;
-  const int tid = threadIdx.x, lane = tid & 31, strip = (tid >> 5) & 3, half = tid >> 7;
+  // (strips have products with up to their own block of tokens: each scheduler gets a long
+  // and a short one)
+  const int tid = threadIdx.x, lane = tid & 31, half = tid >> 7;
+  const int strip = half ? 3 - ((tid >> 5) & 3) : tid >> 5;
   const unsigned b1 = blockIdx.x / d.nc, b2 = b1 / d.no;
   const int c = (int)(blockIdx.x - b1 * d.nc), hb = (int)(b1 - b2 * d.no);
   const int b = (int)(b2 / d.G), grp = (int)(b2 - (unsigned)b * d.G);
