@@ -168,6 +168,7 @@ int launch_step(DeltaStepDims d, const DeltaStepPtrs& p, cudaStream_t s) {
 // with 128 key columns, us a call in a row of them, 4 and 8 rows a lane: 2048 state rows
 // 2.42 and 2.57, 16384 3.92 and 4.16, 32768 4.63 and 4.60, 65536 9.52 and 9.15, 131072
 // 16.6 and 15.6; with 64: 65536 5.65 and 6.00, 131072 9.13 and 8.88.
+// Fewer where a row takes several pieces a lane, whose registers they share.
 template <typename Tin, typename Tout>
 int pick_step(const DeltaStepDims& d, const DeltaStepPtrs& p, bool vec, cudaStream_t s) {
   const int nv = vec ? d.N / 4 : d.N;
