@@ -419,8 +419,10 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 2 ? (BWD ? 4 : 6) :
     float bb[2], hi[2], lo[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // 2^-150 is 0 in fp32: a bound that changes no decay keeps the sums finite
-      hi[j] = 2 * lane + j < rv ? fmaxf(softplus(zt[j]) * (A[pl.h] * lm::kLog2e), -150.f) : 0.f;
+      // 2^-150 is 0 in fp32: a bound that changes no decay keeps the sums finite.  By a
+      // comparison that is false for NaN, so that a NaN gate stays one
+      const float log_a = softplus(zt[j]) * (A[pl.h] * lm::kLog2e);
+      hi[j] = 2 * lane + j < rv ? (log_a < -150.f ? -150.f : log_a) : 0.f;
       bb[j] = 2 * lane + j < rv ? sigmoid(zb[j]) : 0.f;
     }
     auto plus = [](float& h, float& l, float h2, float l2) {

@@ -1,0 +1,48 @@
+"""The gated delta rule at values where it can go wrong -- gates that are not numbers, decays
+that are 0, outliers, infinities, states that live long -- against the fp64 oracle
+(``oracle/delta_ops.py``) on a GPU.  Tolerances are those of ``test_delta_ops`` (1e-5 in relative
+L2 for fp32 outputs) unless a test derives its own."""
+import numpy as np
+import pytest
+
+from oracle import delta_ops as do
+from test_delta_ops import delta_case, dev, on_gpu, types
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("name", ["dt", "beta", "dt_bias", "A"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [150, 1300])  # whole, and cut into segments
+def test_a_gate_that_is_nan_reaches_what_it_should(cuda_lib, name, dtype, T):
+    """From its token on, the head's outputs, its final state and what its gradients are sums
+    over are NaN, and no other head's bits change."""
+    import torch
+    it, _ = types(dtype)
+    a, init, dy, df, _ = delta_case(2, T, 2, 2, 24, 40, dtype, True, None)
+    gy, more = dev(dy, it), dict(init_states=dev(init))
+    want = cuda_lib.gated_delta_fwd(*on_gpu(a, it), **more)
+    back = cuda_lib.gated_delta_bwd(*on_gpu(a, it), gy, dfinal_states=dev(df), **more)
+    at = 70 if name in ("dt", "beta") else 0
+    rows = slice(0, 1) if name in ("dt", "beta") else slice(0, 2)  # batch rows that it reaches
+    if name in ("dt", "beta"):
+        a[name][0, at, 1] = np.nan
+    else:
+        a[name][1] = np.nan
+    x = on_gpu(a, it)
+    y, fin = cuda_lib.gated_delta_fwd(*x, **more)
+    got = cuda_lib.gated_delta_bwd(*x, gy, dfinal_states=dev(df), **more)
+    assert bool(y[rows, at:, 1].isnan().all()) and bool(fin[rows, 1].isnan().all())
+    assert torch.equal(y[:, :, 0], want[0][:, :, 0]) and torch.equal(fin[:, 0], want[1][:, 0])
+    assert torch.equal(y[rows, :at // 64 * 64, 1], want[0][rows, :at // 64 * 64, 1])
+    assert bool(got["ddt"][rows, :, 1].isnan().all()) and bool(got["dinit_states"][rows, 1].isnan().all())
+    for n in ("dA", "ddt_bias"):
+        assert bool(got[n][1].isnan()) and torch.equal(got[n][0], back[n][0])
+    for n in ("dv", "ddt", "dbeta"):
+        assert torch.equal(got[n][:, :, 0], back[n][:, :, 0])
+    assert torch.equal(got["dinit_states"][:, 0], back["dinit_states"][:, 0])
+    one = {n: m[:, at] if m.ndim > 2 else m for n, m in a.items()}
+    state = dev(init)
+    y1 = cuda_lib.gated_delta_step(*on_gpu(one, it), state)  # the token by itself agrees
+    assert bool(y1[rows, 1].isnan().all()) and bool(state[rows, 1].isnan().all())
+    assert bool(y1[:, 0].isfinite().all()) and bool(state[:, 0].isfinite().all())
