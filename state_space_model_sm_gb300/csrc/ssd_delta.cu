@@ -1361,8 +1361,9 @@ struct GradSmem {
 //     dv = b dR,   dbeta = (1 - b) dR . U   (as b_i dL/db_i = W_ii)
 // and the gradient of G_i is the row sum less the column sum of dAqk Aqk - W M, plus
 // scale e^G q . (dY S0) - dR . (b e^G S0 k) - U . (e^(G63 - G) dS k), where what the
-// last token's G takes from the state behind the chunk is added.  Row and column sums
-// are of the same products, so that what cancels in their difference cancels exactly.
+// last token's G takes from the state behind the chunk is added.  Row and column sums are
+// of the same products, each sum rounded by itself: 2^-24 of their terms is left of what
+// cancels in their difference, which a step whose decay is 0 does not pass on (gates_of).
 // Twelve products of 64 x 64 x 64 to 128 a tile of value rows, whose operands each become
 // planes in shared memory first: 700 us, 32 thousand clocks a head and chunk of an SM where
 // the products alone take 11.  Issue slots are 44 % used, the tensor cores 26 %; a second
@@ -1490,8 +1491,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const float v = dg[x] + after;
       const int64_t o = (tok + i) * d.H + h;
       if (i < rv) {
-        const float dz = v * A[h] * sigmoid(zd[x]);
-        sa = fmaf(v, softplus(zd[x]), sa);
+        // a decay that is 0 in fp32 (ex2 of less than -126) does not move with its gate; the
+        // difference of sums leaves their rounding there, and a step has no bound
+        const float delta = softplus(zd[x]);
+        const bool gone = delta * (A[h] * lm::kLog2e) < -126.f && v == v;
+        const float dz = gone ? 0.f : v * A[h] * sigmoid(zd[x]);
+        if (!gone) sa = fmaf(v, delta, sa);
         sb += dz;
         ddt[o] = from_f<TO>(dz);
         dbeta[o] = from_f<TO>((1.f - bd[x]) * wii[x]);

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import delta_ops as do
-from test_delta_ops import delta_case, dev, on_gpu, types
+from test_delta_ops import close, delta_case, dev, on_gpu, small, stored, types
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,24 @@ def test_a_gate_that_is_nan_reaches_what_it_should(cuda_lib, name, dtype, T):
     y1 = cuda_lib.gated_delta_step(*on_gpu(one, it), state)  # the token by itself agrees
     assert bool(y1[rows, 1].isnan().all()) and bool(state[rows, 1].isnan().all())
     assert bool(y1[:, 0].isfinite().all()) and bool(state[:, 0].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("step", [300.0, 3e4, np.inf])
+def test_gates_of_decays_that_are_zero(cuda_lib, dtype, step):
+    """Steps that forget everything next to ordinary ones: their gates' gradients are 0, and
+    the parameters' sums, which multiply by the step, are those of the others."""
+    import torch
+    it, _ = types(dtype)
+    a, init, dy, df, _ = delta_case(1, 192, 2, 2, 16, 32, dtype, True, None)
+    a["A"] = stored(np.array([-0.7, -2.0]), torch.float32)  # 300 steps: 2^-300 and less
+    hard = np.random.default_rng(1).random((1, 192, 2)) < 0.1
+    a["dt"] = stored(np.where(hard, step, a["dt"]), it)
+    got = cuda_lib.gated_delta_bwd(*on_gpu(a, it), dev(dy, it), init_states=dev(init), dfinal_states=dev(df))
+    # (the oracle multiplies by the step: a finite one whose decay is 0 as well)
+    ref = do.delta_bwd(*dict(a, dt=np.where(hard, 3e4, a["dt"])).values(), dy, init, dfinal=df)
+    close("ddt", got["ddt"], ref["ddt"])
+    terms = np.sqrt((ref["ddt"] ** 2).sum())
+    for n in ("dA", "ddt_bias"):
+        small(n, got[n], ref[n], terms)
+    assert not got["ddt"].cpu()[torch.from_numpy(hard)].any()
