@@ -521,7 +521,10 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
  * needs.  Long sequences of few heads are cut into segments that run at once and are
  * joined by products of their transitions: keys that let a state grow past f32's range
  * between two joins give infinities or NaN there.  A step's decay below
- * 2^-150 counts as 2^-150, 0 in f32; one that is NaN stays NaN.  Workspace of the size query's bytes (0 for a
+ * 2^-150 counts as 2^-150, 0 in f32; one that is NaN stays NaN.
+ * Operands of a chunk's products hold 2^-22 of a value, or 2^-39 of the largest of
+ * its row (a token's keys, a value channel over 64 tokens, a state's row): tokens
+ * next to one that is 10^6 (10^8) times larger are good to 5e-7 (5e-5).  Workspace of the size query's bytes (0 for a
  * rejected shape), 16-byte aligned, caller-owned. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;

@@ -15,8 +15,9 @@
 // Numerics: all matrix products run on the tensor cores with planes of fp32 values
 // (warp_mma.cuh).  What reaches a state, a state's gradient or a parameter's gradient is
 // three planes of bf16 (X and the pairs' gradients) or two of fp16 with rows scaled (the
-// chains), 2^-23 of a row's largest value; what only reaches a bf16 output is two planes
-// of bf16, 2^-16.  Sums and states are fp32.  Log decays are summed and kept as two floats,
+// chains), 2^-22 of a value or 2^-39 of its row's largest, so that a token stays good next
+// to others of its chunk that are up to 10^6 times larger; what only reaches a bf16 output
+// is two planes of bf16, 2^-16 of each value.  Sums and states are fp32.  Log decays are summed and kept as two floats,
 // so that a strong decay early in a chunk takes nothing from the differences behind it.
 //
 // 64 tokens a chunk: X takes 64^2 / 2 products a token, and the chain's length is the
@@ -314,8 +315,8 @@ struct PrepSmem {
   static constexpr size_t total = sizeof(Gates) + one + dy;
 };
 
-// The scale that brings row tid / 2 of a tile (two threads a row) to at most 2, and, with
-// `to`, the scaled row as fp16 planes.  Returns the inverse.
+// The scale of row tid / 2 of a tile (two threads a row) and, with `to`, the scaled row as
+// fp16 planes.  Returns the inverse.
 template <int NI, int NIMG, int NP>
 __device__ __forceinline__ float row_image(const bf16* tile, bf16* to) {
   constexpr int LD = NP + 8, W = NP / 2;
@@ -747,13 +748,14 @@ __device__ __forceinline__ void scale_rows(float (&c)[NT][4], float f0, float f1
     c[t][0] = a.x, c[t][1] = a.y, c[t][2] = b.x, c[t][3] = b.y;
   }
 }
-// Its columns (tokens 8 t + t2, + 1) times the tokens' factors.
+// Its columns (tokens 8 t + t2, + 1) times the tokens' factors, then its rows times g0 and
+// g1: a state's or a gradient's size, which may be any, comes last.
 __device__ __forceinline__ void scale_tokens(float (&c)[8][4], const float* f, int t2, float g0, float g1) {
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
     const float2 x = *reinterpret_cast<const float2*>(f + 8 * t + t2);
-    const float2 a = __fmul2_rn(make_float2(c[t][0], c[t][1]), __fmul2_rn(x, make_float2(g0, g0)));
-    const float2 b = __fmul2_rn(make_float2(c[t][2], c[t][3]), __fmul2_rn(x, make_float2(g1, g1)));
+    const float2 a = __fmul2_rn(__fmul2_rn(make_float2(c[t][0], c[t][1]), x), make_float2(g0, g0));
+    const float2 b = __fmul2_rn(__fmul2_rn(make_float2(c[t][2], c[t][3]), x), make_float2(g1, g1));
     c[t][0] = a.x, c[t][1] = a.y, c[t][2] = b.x, c[t][3] = b.y;
   }
 }

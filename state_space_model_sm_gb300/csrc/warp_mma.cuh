@@ -10,7 +10,9 @@
 // left operand of the next product.
 //
 // Where rows can be scaled by a power of two first, two planes of fp16 do what three of
-// bf16 do: rn(v) and rn(v - p0) leave 2^-23 of the row's largest value, and a product
+// bf16 do: with the row's largest value at the top of fp16's range, rn(v) and rn(v - p0)
+// leave 2^-22 of v, or 2^-39 of the largest value where v is under 2^-17 of it (fp16's
+// smallest step; with the largest at 1 that would begin 2^14 times higher), and a product
 // of two such values takes three instructions (the lower planes' product is below).
 //
 // Operand tiles in shared memory are rows of 16-bit values with a pitch of an odd number of 16
@@ -158,16 +160,16 @@ __device__ __forceinline__ void mma_planes(float (&c0)[4], float (&c1)[4], const
 
 // ----------------------------------------------------------- fp16, rows scaled
 
-// Power of two that brings the largest value m of a row to [1, 2), and its inverse; 1
-// for a row of zeros.
+// Power of two that brings the largest value m of a row to [2^14, 2^15), the top of fp16's
+// range, and its inverse (m under 2^-112: 2^126).
 struct Scale {
   float s, inv;
 };
 __device__ __forceinline__ Scale scale_of(float m) {
-  const int e = min((int)(__float_as_uint(m) >> 23), 253);
+  const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
   Scale r;
-  r.s = __uint_as_float((uint32_t)(e > 0 ? 254 - e : 127) << 23);
-  r.inv = __uint_as_float((uint32_t)(e > 0 ? e : 127) << 23);
+  r.s = __uint_as_float((268 - e) << 23);
+  r.inv = __uint_as_float((e - 14) << 23);
   return r;
 }
 // The planes of a pair of values times f.

@@ -67,3 +67,51 @@ def test_gates_of_decays_that_are_zero(cuda_lib, dtype, step):
     for n in ("dA", "ddt_bias"):
         small(n, got[n], ref[n], terms)
     assert not got["ddt"].cpu()[torch.from_numpy(hard)].any()
+
+
+def relative(got, ref):
+    g = got.double().cpu().numpy()
+    assert np.isfinite(g).all()
+    return np.linalg.norm(g - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "mixed", "bf16"])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6])
+@pytest.mark.parametrize("N", [40, 128])
+def test_a_token_next_to_a_larger_one(cuda_lib, dtype, size, N):
+    """What a token's outputs (gradients) do not depend on takes nothing from them: later
+    (earlier) tokens of its chunk that are 1e6 times larger.  Operands hold 2^-39 of their row's
+    largest value, 3 size: 5e-6 of a value at most and, uniform, 1.6e-6 in the mean square,
+    which the usual 1e-5 covers.  bf16 outputs add half a step in the 8th bit, 2^-8."""
+    import torch
+    it, ot = types(dtype)
+    a, init, dy, df, _ = delta_case(1, 100, 2, 1, 24, N, dtype, True, None)
+    a["v"][0, 50] = stored(a["v"][0, 50] * size, it)
+    dy[0, 10] = stored(dy[0, 10] * size, it)
+    x, more = on_gpu(a, it), dict(init_states=dev(init), out_dtype=ot)
+    y, _ = cuda_lib.gated_delta_fwd(*x, **more)
+    yr, _ = do.delta_fwd(*a.values(), init)
+    tol = 1e-5 + (2.0 ** -8 if ot == torch.bfloat16 else 0.0)
+    assert relative(y[:, :50], yr[:, :50]) <= tol
+    got = cuda_lib.gated_delta_bwd(*x, dev(dy, it), dfinal_states=dev(df), **more)
+    ref = do.delta_bwd(*a.values(), dy, init, dfinal=df)
+    assert relative(got["dv"][:, 11:], ref["dv"][:, 11:]) <= tol
+
+
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6])
+def test_columns_of_a_state_next_to_larger_ones(cuda_lib, size):
+    """Keys along the axes: each column of a state holds its own values, of sizes that differ,
+    and keeps them for the queries that read it alone (bounds as above)."""
+    import torch
+    a, init, _, _, _ = delta_case(1, 200, 2, 1, 24, 32, "f32", True, None)
+    at = np.random.default_rng(0).integers(0, 32, 200)
+    a["k"][0, :, 0] = a["q"][0, :, 0] = np.eye(32)[at]
+    scale = np.where(np.arange(32) < 3, size, 1.0)
+    a["v"] = stored(a["v"] * scale[at][None, :, None, None], torch.float32)
+    init = stored(init * scale, torch.float32)
+    y, fin = cuda_lib.gated_delta_fwd(*on_gpu(a, None), init_states=dev(init))
+    yr, fr = do.delta_fwd(*a.values(), init)
+    for big in (True, False):
+        t, c = (at < 3) == big, (np.arange(32) < 3) == big
+        assert relative(y[:, t], yr[:, t]) <= 1e-5
+        assert relative(fin[..., c], fr[..., c]) <= 1e-5
