@@ -524,7 +524,9 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
  * 2^-150 counts as 2^-150, 0 in f32; one that is NaN stays NaN.
  * Operands of a chunk's products hold 2^-22 of a value, or 2^-39 of the largest of
  * its row (a token's keys, a value channel over 64 tokens, a state's row): tokens
- * next to one that is 10^6 (10^8) times larger are good to 5e-7 (5e-5).  Workspace of the size query's bytes (0 for a
+ * next to one that is 10^6 (10^8) times larger are good to 5e-7 (5e-5).  An infinity or NaN
+ * at a token may also make NaN what its chunk holds of earlier tokens (in the
+ * gradients: of later ones).  Workspace of the size query's bytes (0 for a
  * rejected shape), 16-byte aligned, caller-owned. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;

@@ -161,7 +161,8 @@ __device__ __forceinline__ void mma_planes(float (&c0)[4], float (&c1)[4], const
 // ----------------------------------------------------------- fp16, rows scaled
 
 // Power of two that brings the largest value m of a row to [2^14, 2^15), the top of fp16's
-// range, and its inverse (m under 2^-112: 2^126).
+// range, and its inverse (m under 2^-112: 2^126).  An infinite value leaves nothing of the
+// others of its row: the inverse is NaN, and so are the row's products.
 struct Scale {
   float s, inv;
 };
@@ -169,7 +170,7 @@ __device__ __forceinline__ Scale scale_of(float m) {
   const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
   Scale r;
   r.s = __uint_as_float((268 - e) << 23);
-  r.inv = __uint_as_float((e - 14) << 23);
+  r.inv = __uint_as_float(e < 255 ? (e - 14) << 23 : 0x7fffffffu);
   return r;
 }
 // The planes of a pair of values times f.

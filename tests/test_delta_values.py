@@ -115,3 +115,33 @@ def test_columns_of_a_state_next_to_larger_ones(cuda_lib, size):
         t, c = (at < 3) == big, (np.arange(32) < 3) == big
         assert relative(y[:, t], yr[:, t]) <= 1e-5
         assert relative(fin[..., c], fr[..., c]) <= 1e-5
+
+
+@pytest.mark.parametrize("name,where", [
+    ("v", (0, 60, 1, 3)), ("v", (0, 100, 0, 0)), ("k", (0, 60, 0, 5)), ("q", (0, 60, 0, 5)),
+    ("dy", (0, 20, 1, 3)), ("init", (0, 1, 3, 5)), ("dfinal", (0, 1, 3, 5))])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_infinity_leaves_nothing_wrong(cuda_lib, name, where, value, dtype):
+    """Results that are finite are right, and what the definition makes infinite or NaN is not
+    finite."""
+    import torch
+    it, _ = types(dtype)
+    a, init, dy, df, _ = delta_case(1, 150, 2, 1, 16, 32, dtype, True, None)
+    dict(a, dy=dy, init=init, dfinal=df)[name][where] = value
+    x, more = on_gpu(a, it), dict(init_states=dev(init), out_dtype=torch.float32)
+    y, fin = cuda_lib.gated_delta_fwd(*x, **more)
+    got = cuda_lib.gated_delta_bwd(*x, dev(dy, it), dfinal_states=dev(df), **more)
+    with np.errstate(all="ignore"):
+        yr, fr = do.delta_fwd(*a.values(), init)
+        ref = do.delta_bwd(*a.values(), dy, init, dfinal=df)
+    for n, g, r in [("y", y, yr), ("final", fin, fr)] + [(n, got[n], ref[n]) for n in got]:
+        g = g.double().cpu().numpy()
+        both = np.isfinite(g) & np.isfinite(r)
+        assert not (np.isfinite(g) & ~np.isfinite(r)).any(), n
+        if both.any():  # (dA, ddt_bias: 5e-5 of their terms, as in test_delta_ops)
+            tol = 5e-5 if n in ("dA", "ddt_bias") else 1e-5
+            top = np.linalg.norm(r[both])
+            if n in ("dA", "ddt_bias"):
+                top = max(top, np.linalg.norm(ref["ddt"][np.isfinite(ref["ddt"])]))
+            assert np.linalg.norm((g - r)[both]) <= tol * top, n
