@@ -722,20 +722,45 @@ __device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (
       });
   }
 }
-// S += the product of the tokens of c (rows scaled) with their rows of the tile.
+// S <- keep S + the product of the tokens of c with their rows of the tile.  The products are
+// summed from zero, four tiles of columns at a time, and added to the state by one rounded
+// operation: an accumulation truncates, and with the state as the accumulator a long-lived
+// one lost 3e-7 of itself every chunk (7e-5 over 256).
 template <int NI, int NP>
-__device__ __forceinline__ void add_outer(float (&S)[NP / 8][4], const float (&c)[8][4],
-                                          const bf16* kt, float f0, float f1, int lane) {
+__device__ __forceinline__ void add_outer(float (&S)[NP / 8][4], float keep, const float (&c)[8][4],
+                                          const bf16* kt, Scale s0, Scale s1, int lane) {
   constexpr int LD = NP + 8;
+  uint32_t a[4][2][4];
 #pragma unroll
-  for (int kb = 0; kb < 4; ++kb) {
-    uint32_t a[2][4];
-    a_from_acc_h(a, c, kb, f0, f1);
+  for (int kb = 0; kb < 4; ++kb) a_from_acc_h(a[kb], c, kb, s0.s, s1.s);
 #pragma unroll
-    for (int np = 0; np < NP / 16; ++np)
-      mma_planes_h<NI>(S[2 * np], S[2 * np + 1], a, [&](int j, uint32_t(&x)[4]) {
-        b_cols<LD>(x, kt + j * kC * LD, np * 16, kb * 16, lane);
-      });
+  for (int n = 0; n < NP / 8; n += 4) {
+    float t[4][4] = {};
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+      for (int j = NI - 1; j >= 0; --j) {
+        uint32_t x[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          b_cols<LD>(x[h], kt + j * kC * LD, n * 8 + h * 16, kb * 16, lane);
+#pragma unroll
+        for (int i = 1; i >= 0; --i)
+          if (i + j < 2)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              mma16816h(t[h], a[kb][i], x[h >> 1][(h & 1) * 2], x[h >> 1][(h & 1) * 2 + 1]);
+      }
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const float f = o ? s1.inv : s0.inv;
+        const float2 was = make_float2(S[n + h][2 * o], S[n + h][2 * o + 1]);
+        const float2 v = __ffma2_rn(make_float2(t[h][2 * o], t[h][2 * o + 1]), make_float2(f, f),
+                                    __fmul2_rn(was, make_float2(keep, keep)));
+        S[n + h][2 * o] = v.x, S[n + h][2 * o + 1] = v.y;
+      }
   }
 }
 // A strip's rows times f0 and f1.
@@ -765,7 +790,6 @@ __device__ __forceinline__ void store_strip(float* m, int64_t strip, const float
 #pragma unroll
   for (int t = 0; t < NT; ++t) p[t * 32] = as4(c[t]);
 }
-constexpr float kBelow = 5.9604644775390625e-8f;  // 2^-24
 
 // A block of a chain: 64 rows (value rows, or rows of a segment's move) of one segment.
 struct Piece {
@@ -999,16 +1023,10 @@ __global__ void __launch_bounds__(192, 2)
     scale_rows(u, q0.inv, q1.inv);
     if constexpr (!SEG) store_strip<8>(w.U, srow, u, lane);
     scale_tokens(u, g.fu, t2, 1.f, 1.f);
-    // the state takes the products in the scale of U's rows, or of its own where that is
-    // 2^24 larger (what U would lose there is below the state's own rounding)
     row_max<8>(u, a0, a1);
-    const Scale u0 = scale_of(fmaxf(a0, m0 * kBelow)), u1 = scale_of(fmaxf(a1, m1 * kBelow));
-    const float end = ex2(g.gh[kC - 1]);
-    scale_rows(S, end * u0.s, end * u1.s);
-    add_outer<NI, NP>(S, u, kt, u0.s, u1.s, lane);
+    add_outer<NI, NP>(S, ex2(g.gh[kC - 1]), u, kt, scale_of(a0), scale_of(a1), lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
-    scale_rows(S, u0.inv, u1.inv);
   }
   end_state<NP, SEG>(S, d, pc, row, pc.last ? final_states : nullptr, w, lane);
 }
@@ -1312,18 +1330,12 @@ __global__ void __launch_bounds__(kChainThreads)
     scale_tokens(u, g.fz, t2, -1.f, -1.f);
     raw_strip<T>(r, yt, strip, lane);
     scale_tokens(r, g.fq, t2, 1.f, 1.f);
-    float b0, b1;
     row_max<8>(r, a0, a1);
-    row_max<8>(u, b0, b1);
-    const Scale u0 = scale_of(fmaxf(fmaxf(a0, b0), m0 * kBelow)),
-                u1 = scale_of(fmaxf(fmaxf(a1, b1), m1 * kBelow));
-    const float keep = ex2(g.gh[kC - 1]);
-    scale_rows(S, keep * u0.s, keep * u1.s);
-    add_outer<NI, NP>(S, r, qt, u0.s, u1.s, lane);
-    add_outer<NI, NP>(S, u, kt, u0.s, u1.s, lane);
+    add_outer<NI, NP>(S, ex2(g.gh[kC - 1]), r, qt, scale_of(a0), scale_of(a1), lane);
+    row_max<8>(u, a0, a1);
+    add_outer<NI, NP>(S, 1.f, u, kt, scale_of(a0), scale_of(a1), lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
-    scale_rows(S, u0.inv, u1.inv);
   }
   end_state<NP, SEG>(S, d, pc, row, pc.seg == 0 ? dinit : nullptr, w, lane);
 }

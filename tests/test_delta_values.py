@@ -145,3 +145,32 @@ def test_an_infinity_leaves_nothing_wrong(cuda_lib, name, where, value, dtype):
             if n in ("dA", "ddt_bias"):
                 top = max(top, np.linalg.norm(ref["ddt"][np.isfinite(ref["ddt"])]))
             assert np.linalg.norm((g - r)[both]) <= tol * top, n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "mixed"])
+@pytest.mark.parametrize("H", [2, 64])  # cut into segments, and one chain over all chunks
+def test_states_that_live_long(cuda_lib, dtype, H):
+    """Slow decays and small strengths: the state of the last token holds what 8192 tokens of one
+    sign added, so a bias of an addition would count 128 chunks' times.  A rounded addition a
+    chunk, 2^-24 each and independent, is sqrt(128) of them, 7e-7, beside the usual errors."""
+    import torch
+    it, _ = types(dtype)
+    T, G, P, N = 8192, 1, 4, 32
+    g = np.random.default_rng(H)
+    n = g.standard_normal
+    unit = lambda m: m / np.linalg.norm(m, axis=-1, keepdims=True)  # noqa: E731
+    a = dict(q=stored(unit(np.abs(n((1, T, G, N)))), it), k=stored(unit(np.abs(n((1, T, G, N)))), it),
+             v=stored(1 + 0.3 * n((1, T, H, P)), it), dt=stored(n((1, T, H)) - 9, it),
+             dt_bias=stored(0.1 * n(H), torch.float32), A=stored(-0.1 * np.exp(0.1 * n(H)), torch.float32),
+             beta=stored(n((1, T, H)) - 9, it))
+    init = stored(3 + 0.1 * n((1, H, P, N)), torch.float32)
+    dy = stored(np.abs(n((1, T, H, P))), it)
+    x, more = on_gpu(a, it), dict(init_states=dev(init), out_dtype=torch.float32)
+    y, fin = cuda_lib.gated_delta_fwd(*x, **more)
+    yr, fr = do.delta_fwd(*a.values(), init)
+    close("y", y, yr)
+    close("final", fin, fr)
+    got = cuda_lib.gated_delta_bwd(*x, dev(dy, it), **more)
+    ref = do.delta_bwd(*a.values(), dy, init)
+    for n in ("dq", "dk", "dv", "ddt", "dbeta", "dinit_states"):
+        close(n, got[n], ref[n])
