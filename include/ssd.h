@@ -513,7 +513,8 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
  * q, k (batch, seqlen, ngroups, dstate), v, y (batch, seqlen, nheads, headdim),
  * dt, beta (batch, seqlen, nheads); q, k, v, dt, beta in_dtype, y out_dtype;
  * dt_bias (nheads) f32 or NULL, A (nheads) f32 (negative: decay); init_states,
- * final_states (batch, nheads, headdim, dstate) f32 or NULL.  Keys of a length up
+ * final_states (batch, nheads, headdim, dstate) f32 or NULL, which must not overlap
+ * (SSD_ERR_INVALID_ARG; nor dfinal_states and dinit_states).  Keys of a length up
  * to 1 keep the state bounded (ssd_qk_norm_fwd with l2); the call does not
  * normalise them.  dstate <= 128, headdim <= 256, batch and nheads < 65536,
  * seqlen < 2^30, batch * nheads < 2^29, batch * nheads * ceil(seqlen / 64) < 2^31.

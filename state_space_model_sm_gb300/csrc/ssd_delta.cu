@@ -2131,6 +2131,13 @@ int check_in(const ssd_delta_shape* shape, DeltaDims* d, const DeltaIn& in) {
   return SSD_OK;
 }
 
+// Whether two tensors of states share memory: blocks of later segments write the last state
+// while those of the first may still read the initial one.
+bool overlap(const DeltaDims& d, const float* a, const float* b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x > y ? x - y : y - x) < (uintptr_t)d.B * d.H * d.P * d.N * sizeof(float);
+}
+
 int check_ws(const DeltaWs& w, const void* workspace, size_t bytes) {
   return !workspace || off(workspace, 16) || bytes < w.total ? SSD_ERR_WORKSPACE : SSD_OK;
 }
@@ -2169,7 +2176,8 @@ int ssd_gated_delta_fwd(const ssd_delta_shape* shape, const void* q, const void*
   const DeltaIn in{q, k, v, dt, dt_bias, A, beta, init_states, lengths};
   int st = check_in(shape, &d, in);
   if (st != SSD_OK) return st;
-  if (!y || off(y, shape->out_dtype == SSD_BF16 ? 2 : 4) || off(final_states, 4))
+  if (!y || off(y, shape->out_dtype == SSD_BF16 ? 2 : 4) || off(final_states, 4) ||
+      overlap(d, init_states, final_states))
     return SSD_ERR_INVALID_ARG;
   d.wide = d.P % 2 == 0 && !off(y, shape->out_dtype == SSD_BF16 ? 4 : 8);
   const DeltaWs w = delta_ws(d, workspace, false);
@@ -2191,7 +2199,7 @@ int ssd_gated_delta_bwd(const ssd_delta_shape* shape, const void* q, const void*
   const int e = shape->in_dtype == SSD_BF16 ? 2 : 4, o = shape->out_dtype == SSD_BF16 ? 2 : 4;
   if (!dy || !dq || !dk || !dv || !ddt || !dbeta || off(dy, e) || off(dq, o) || off(dk, o) ||
       off(dv, o) || off(ddt, o) || off(dbeta, o) || off(dA, 4) || off(ddt_bias, 4) ||
-      off(dfinal_states, 4) || off(dinit_states, 4))
+      off(dfinal_states, 4) || off(dinit_states, 4) || overlap(d, dfinal_states, dinit_states))
     return SSD_ERR_INVALID_ARG;
   d.wide = d.P % 2 == 0 && !off(dv, 2 * o);
   d.wide_k = d.N % 2 == 0 && !off(dq, 2 * o) && !off(dk, 2 * o);

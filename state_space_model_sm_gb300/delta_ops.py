@@ -52,7 +52,8 @@ def gated_delta_fwd(q, k, v, dt, dt_bias, A, beta, init_states=None, lengths=Non
     nheads, headdim, dstate) float32; lengths (batch,) int32: positions from lengths[b] on
     are padding.  dstate <= 128, headdim <= 256.  Keys longer than 1 let the state grow;
     ``qk_norm_fwd(..., l2=True)`` makes unit keys.  y is in ``out_dtype`` (v's type).
-    final_states is what ``gated_delta_step`` goes on from."""
+    final_states is what ``gated_delta_step`` goes on from (a given one must not overlap
+    init_states)."""
     lib = _native_lib()
     dev, shape, (B, T, H, P, N, G), odt, p = _delta_inputs(q, k, v, dt, dt_bias, A, beta, 4, scale,
                                                            out_dtype)
@@ -75,7 +76,8 @@ def gated_delta_bwd(q, k, v, dt, dt_bias, A, beta, dy, init_states=None, lengths
                     scale: float = 1.0, dfinal_states=None, out_dtype=None, workspace=None, out=None):
     """Gradients of <dy, y> + <dfinal_states, final_states> of ``gated_delta_fwd``
     (``ssd_gated_delta_bwd``): a dict with dq, dk, dv, ddt and dbeta in ``out_dtype`` (v's
-    type), and dA, ddt_bias and, with init_states, dinit_states in float32."""
+    type), and dA, ddt_bias and, with init_states, dinit_states in float32 (a given one must
+    not overlap dfinal_states)."""
     lib = _native_lib()
     dev, shape, (B, T, H, P, N, G), odt, p = _delta_inputs(q, k, v, dt, dt_bias, A, beta, 4, scale,
                                                            out_dtype)
