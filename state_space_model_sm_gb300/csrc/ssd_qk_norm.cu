@@ -15,9 +15,10 @@
 // 99 us, 4.6 TB/s; 2 x 8192 tokens of 32 heads without weights and rotation 52 us, 5.2 TB/s.
 //
 // Angles: position * freq loses the fraction of a turn in fp32 from some thousand
-// radians on.  Here freq / 2 pi is a 64-bit fraction of a turn, formed once a lane from
+// radians on.  Here freq / 2 pi is a 64-bit fraction of a turn, formed once a block from
 // the bits of freq and of 1 / 2 pi, and the angle is the 64-bit integer product with
-// the position, whose overflow is whole turns: exact to 2^-31 turns for every int32.
+// the position, whose overflow is whole turns: exact to 2^-31 turns for every int32, and
+// then rounded to a float's 24 bits, 2^-26 turns at most.
 #include <cuda_bf16.h>
 
 #include "layer_math.cuh"
@@ -49,7 +50,7 @@ __device__ __forceinline__ uint64_t turns(float f) {
   const uint32_t m = ex ? (w & 0x7fffffu) | 0x800000u : w & 0x7fffffu;
   const int e = (ex ? ex : 1) - 150;
   // m / 2 pi * 2^128 in five words
-  constexpr uint32_t c[4] = {0x4d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
+  constexpr uint32_t c[4] = {0x7d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
   uint32_t p[5];
   uint64_t carry = 0;
 #pragma unroll
