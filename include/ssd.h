@@ -575,9 +575,10 @@ int ssd_gated_delta_step(const ssd_delta_shape* shape, const void* q, const void
  * where pair i is columns (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved.
  * rows = batch * seqlen; positions (rows) int32 device memory, or NULL: row r is at
  * position r % seqlen.  freq (rotary / 2) f32 device memory (NULL with rotary 0).
- * Angles are reduced before they are rounded, at every int32 position.  q_out, k_out dense.
- * headdim <= 1024, q_heads, k_heads < 65536, rows * (q_heads + k_heads) < 2^31;
- * rotary even, <= headdim; eps > 0; |freq| < 2^20. */
+ * Angles are reduced before they are rounded, at every int32 position.  q_out, k_out
+ * dense.  headdim <= 1024, q_heads, k_heads < 65536, rows * (q_heads + k_heads) <
+ * 2^31; rotary even, <= headdim; eps > 0; |freq| < 2^20 (a pair whose frequency is
+ * not: NaN). */
 typedef struct {
   int64_t batch, seqlen, q_heads, k_heads, headdim, rotary;
   int64_t q_row_stride, k_row_stride, q_batch_stride, k_batch_stride;

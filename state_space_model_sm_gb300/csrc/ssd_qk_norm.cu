@@ -43,10 +43,13 @@ constexpr int kQkThreads = 128;
 constexpr int kQkWarps = kQkThreads / 32;
 
 // f / 2 pi in turns, modulo 1, times 2^64: m 2^e / 2 pi with a 24-bit m, by the first
-// 128 bits of 1 / 2 pi.
+// 128 bits of 1 / 2 pi.  They reach as far as |f| < 2^20; a larger, infinite or NaN
+// frequency is kNoTurn, whose angles are NaN.
+constexpr uint64_t kNoTurn = 0x8000000000000001u;
 __device__ __forceinline__ uint64_t turns(float f) {
   const uint32_t w = __float_as_uint(f);
   const int ex = (int)((w >> 23) & 0xffu);
+  if (ex >= 147) return kNoTurn;
   const uint32_t m = ex ? (w & 0x7fffffu) | 0x800000u : w & 0x7fffffu;
   const int e = (ex ? ex : 1) - 150;
   // m / 2 pi * 2^128 in five words
@@ -76,11 +79,16 @@ __device__ __forceinline__ uint64_t turns(float f) {
     const uint32_t lo = __funnelshift_r(x[0], x[1], o), hi = __funnelshift_r(x[1], x[2], o);
     r = (uint64_t)hi << 32 | lo;
   }
-  return w >> 31 ? 0 - r : r;
+  r = w >> 31 ? 0 - r : r;
+  return r == kNoTurn ? r + 1 : r;  // (2^-64 of a turn off)
 }
 
 __device__ __forceinline__ void rotation(uint64_t turn, int pos, float* sn, float* cs) {
   const uint64_t t = turn * (uint64_t)(int64_t)pos;
+  if (turn == kNoTurn) {
+    *sn = *cs = __int_as_float(0x7fffffff);
+    return;
+  }
   sincospif((float)(int32_t)(uint32_t)(t >> 32) * 4.656612873077393e-10f, sn, cs);  // 2^-31
 }
 

@@ -9,6 +9,26 @@ from test_delta_ops import close, dev
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf, 2.0 ** 20, -2.0 ** 100])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D", [64, 70])  # pieces of 16 bytes, single columns
+def test_a_frequency_out_of_range_is_nan(cuda_lib, value, interleaved, D):
+    """Its pair is NaN at every position but nothing else, forward and backward."""
+    g = np.random.default_rng(D)
+    x, dy = g.standard_normal((1, 5, 2, D)), g.standard_normal((1, 5, 2, D))
+    freq, pairs = g.uniform(0.1, 1.0, D // 2), D // 2
+    i = 3
+    hit = np.zeros(D, bool)
+    hit[[2 * i, 2 * i + 1] if interleaved else [i, i + pairs]] = True
+    kw = dict(interleaved=interleaved, l2=True)
+    want = cuda_lib.qk_norm_fwd(dev(x), dev(x), freq=dev(freq), **kw)[0].cpu().numpy()
+    freq[i] = value
+    got = cuda_lib.qk_norm_fwd(dev(x), dev(x), freq=dev(freq), **kw)[0].cpu().numpy()
+    assert np.isnan(got[..., hit]).all() and np.array_equal(got[..., ~hit], want[..., ~hit])
+    b = cuda_lib.qk_norm_bwd(dev(x), dev(x), None, None, dev(freq), None, dev(dy), dev(dy), **kw)
+    assert bool(b["dq"].isnan().all())  # each value's gradient holds the row's sum
+
+
 def test_the_largest_frequencies(cuda_lib):
     """Just under the limit and at the far positions: the fraction of a turn is what is left of
     2^51 radians.  The oracle's angle, a product of doubles, is good to 2^-53 of it, 2^-2
