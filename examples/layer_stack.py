@@ -291,11 +291,11 @@ class DeltaLayer:
         z, u, dt, beta = self._split(h)
         u = ssd.causal_conv_step(u, cache[0], p["conv"], p["conv_bias"], slots=slots)
         q, k, v = self._qkv(u)
-        at = cache[2][slots.long()]
-        q, k = ssd.qk_norm_fwd(q, k, p["w_q"], p["w_k"], self.freq, at, l2=True)
+        row = slots.clamp(min=0).long()  # an empty row reads slot 0's position and moves none
+        q, k = ssd.qk_norm_fwd(q, k, p["w_q"], p["w_k"], self.freq, cache[2][row], l2=True)
         y = ssd.gated_delta_step(q, k, v, dt.contiguous(), p["dt_bias"], -torch.exp(p["A_log"]),
                                  beta.contiguous(), cache[1], slots=slots)
-        cache[2][slots.long()] = at + 1
+        cache[2].index_add_(0, row, (slots >= 0).int())
         return ssd.gated_norm_fwd(y.flatten(-2), z.contiguous(), p["norm"], self.inner,
                                   return_rstd=False)[0] @ p["w_out"]
 
