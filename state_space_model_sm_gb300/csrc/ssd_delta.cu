@@ -723,10 +723,11 @@ __device__ __forceinline__ void state_times_keys(float (&z)[8][4], const float (
   }
 }
 // S <- keep S + the product of the tokens of c with their rows of the tile.  The products are
-// summed from zero, four tiles of columns at a time, and added to the state by one rounded
+// summed from zero, W tiles of columns at a time, and added to the state by one rounded
 // operation: an accumulation truncates, and with the state as the accumulator a long-lived
-// one lost 3e-7 of itself every chunk (7e-5 over 256).
-template <int NI, int NP>
+// one lost 3e-7 of itself every chunk (7e-5 over 256).  W 8 in the backward's chain (4: 303
+// us for 288), 4 in the forward's, whose registers two blocks an SM share.
+template <int NI, int NP, int W = 4>
 __device__ __forceinline__ void add_outer(float (&S)[NP / 8][4], float keep, const float (&c)[8][4],
                                           const bf16* kt, Scale s0, Scale s1, int lane) {
   constexpr int LD = NP + 8;
@@ -734,25 +735,25 @@ __device__ __forceinline__ void add_outer(float (&S)[NP / 8][4], float keep, con
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) a_from_acc_h(a[kb], c, kb, s0.s, s1.s);
 #pragma unroll
-  for (int n = 0; n < NP / 8; n += 4) {
-    float t[4][4] = {};
+  for (int n = 0; n < NP / 8; n += W) {
+    float t[W][4] = {};
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int j = NI - 1; j >= 0; --j) {
-        uint32_t x[2][4];
+        uint32_t x[W / 2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < W / 2; ++h)
           b_cols<LD>(x[h], kt + j * kC * LD, n * 8 + h * 16, kb * 16, lane);
 #pragma unroll
         for (int i = 1; i >= 0; --i)
           if (i + j < 2)
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+            for (int h = 0; h < W; ++h)
               mma16816h(t[h], a[kb][i], x[h >> 1][(h & 1) * 2], x[h >> 1][(h & 1) * 2 + 1]);
       }
 #pragma unroll
-    for (int h = 0; h < 4; ++h)
+    for (int h = 0; h < W; ++h)
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         const float f = o ? s1.inv : s0.inv;
@@ -1217,9 +1218,10 @@ constexpr size_t back_smem() { return sizeof(ChainBars) + 2 * back_stage<T, NP>(
 // The chain of the backward, from the last chunk to the first, with the gradient of the
 // state behind the chunk in registers:
 //     dU^T = E^T + (dS K^T) e^(G63 - G),   dR^T = dU^T X,
-//     dS <- e^G63 dS + (scale e^G dY)^T Q - (b e^G dR)^T K,
-// in the manner of k_delta_chain: 444 products a chunk, 284 us (96 chains of 64 chunks,
-// 4.4 us each).
+//     dS <- e^G63 dS - (b e^G dR)^T K + (scale e^G dY)^T Q,
+// in the manner of k_delta_chain: 444 products a chunk, 288 us (96 chains of 64 chunks,
+// 4.5 us each).  dR's part is added before dY's rows are taken up: both at once would be
+// 178 registers with 64 key columns, and a block an SM where two fit (138).
 template <typename T, int NP, bool SEG>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
@@ -1326,14 +1328,13 @@ __global__ void __launch_bounds__(kChainThreads)
     }
     scale_tokens(u, g.fx, t2, q0.inv, q1.inv);
     if constexpr (!SEG) store_strip<8>(w.dR, srow, u, lane);
-    // r = scale e^G dY^T 2^q, u = -b e^G dR^T 2^k
-    scale_tokens(u, g.fz, t2, -1.f, -1.f);
-    raw_strip<T>(r, yt, strip, lane);
-    scale_tokens(r, g.fq, t2, 1.f, 1.f);
-    row_max<8>(r, a0, a1);
-    add_outer<NI, NP>(S, ex2(g.gh[kC - 1]), r, qt, scale_of(a0), scale_of(a1), lane);
+    scale_tokens(u, g.fz, t2, -1.f, -1.f);  // -b e^G dR^T 2^k
     row_max<8>(u, a0, a1);
-    add_outer<NI, NP>(S, 1.f, u, kt, scale_of(a0), scale_of(a1), lane);
+    add_outer<NI, NP, 8>(S, ex2(g.gh[kC - 1]), u, kt, scale_of(a0), scale_of(a1), lane);
+    raw_strip<T>(r, yt, strip, lane);
+    scale_tokens(r, g.fq, t2, 1.f, 1.f);  // scale e^G dY^T 2^q
+    row_max<8>(r, a0, a1);
+    add_outer<NI, NP, 8>(S, 1.f, r, qt, scale_of(a0), scale_of(a1), lane);
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
   }
