@@ -1221,7 +1221,7 @@ constexpr size_t back_smem() { return sizeof(ChainBars) + 2 * back_stage<T, NP>(
 //     dS <- e^G63 dS - (b e^G dR)^T K + (scale e^G dY)^T Q,
 // in the manner of k_delta_chain: 444 products a chunk, 288 us (96 chains of 64 chunks,
 // 4.5 us each).  dR's part is added before dY's rows are taken up: both at once would be
-// 178 registers with 64 key columns, and a block an SM where two fit (138).
+// 178 registers with 64 key columns, and a block an SM where two fit (144).
 template <typename T, int NP, bool SEG>
 __global__ void __launch_bounds__(kChainThreads)
     k_delta_back(DeltaDims d, const T* __restrict__ dy, const float* __restrict__ dfinal,
@@ -1957,7 +1957,14 @@ int delta_dims(const ssd_delta_shape* s, DeltaDims* d) {
   if (bh * d->nc >= 0x7fffffff || bh * 4 >= 0x7fffffff) return SSD_ERR_UNSUPPORTED;
   segments(d);
   const int64_t blocks = (int64_t)d->B * d->G * d->nc;
-  const int64_t nb = (kGradBlocks + blocks - 1) / blocks;
+  int64_t nb = (kGradBlocks + blocks - 1) / blocks;
+  if (s->out_dtype == SSD_F32) {
+    // dk's accumulators take 12 accumulations a head and 8 for each 64 value rows, and each
+    // truncates: 64 heads of bf16 inputs in one block were 2.7e-5 off, 8 are 4e-6, which
+    // is the most here (a bf16 result's rounding is 2e-3)
+    const int64_t most = 160 / (12 + 8 * ((d->Ps + kC - 1) / kC)), need = (d->rep + most - 1) / most;
+    nb = nb > need ? nb : need;
+  }
   d->nb = (int)(nb < d->rep ? nb : d->rep);
   const int64_t no = (kOutBlocks + blocks - 1) / blocks;
   d->no = (int)(no < d->rep ? no : d->rep);

@@ -32,7 +32,10 @@ def ragged(B, T, seed=0):
     (64, 65, 5, 1, 40, 72, "f32", True, ragged(64, 65, 2)),
     # two groups, one block each in outputs and gradient (1280 blocks), three heads a group
     (80, 500, 6, 2, 16, 16, "bf16", True, ragged(80, 500, 3)),
-    (80, 500, 6, 2, 16, 16, "f32", True, ragged(80, 500, 3))])
+    (80, 500, 6, 2, 16, 16, "f32", True, ragged(80, 500, 3)),
+    # many heads that share their keys, whose gradients are summed in several blocks
+    (160, 65, 64, 1, 8, 16, "mixed", True, None), (160, 65, 64, 1, 8, 16, "f32", False, None),
+    (160, 65, 16, 1, 130, 16, "mixed", False, None), (160, 65, 64, 1, 8, 16, "bf16", False, None)])
 def test_delta_of_several_heads_a_block(cuda_lib, case):
     ops.test_delta_matches_oracle(cuda_lib, case)
 
