@@ -527,8 +527,13 @@ int ssd_block_norm_bwd(const ssd_block_norm_shape* shape, const void* residual, 
  * its row (a token's keys, a value channel over 64 tokens, a state's row): tokens
  * next to one that is 10^6 (10^8) times larger are good to 5e-7 (5e-5).  An infinity or NaN
  * at a token may also make NaN what its chunk holds of earlier tokens (in the
- * gradients: of later ones).  Workspace of the size query's bytes (0 for a
- * rejected shape), 16-byte aligned, caller-owned. */
+ * gradients: of later ones).  bf16 results are made of operands good to 2^-16.
+ * Workspace of the size query's bytes (0 for a rejected shape), 16-byte aligned,
+ * caller-owned.  It grows with the sequence: with P = headdim up to a multiple of 16
+ * and N = 64 or 128, for each 64 tokens and head 4 P (N + 64) bytes forward and
+ * 4 P (2 N + 320) backward, and about 20 KB, and the keys' (and queries') images of
+ * each group, 128 (N + 8) bytes a plane; a long prompt can be taken in parts, each
+ * from the last one's final states. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
   int64_t q_row_stride, k_row_stride, v_row_stride;

@@ -21,11 +21,12 @@
 // so that a strong decay early in a chunk takes nothing from the differences behind it.
 //
 // 64 tokens a chunk: X takes 64^2 / 2 products a token, and the chain's length is the
-// number of chunks.  tcgen05 was left aside: tiles of 64 rows run at half its rate, every
-// operand is an fp32 value split into planes first, and the chain's three dependent
-// products a chunk would each go through tensor memory and back, where mma.sync takes the
-// accumulators as its next left operand where they are.  Its rate, measured as 8 clocks an
-// instruction and SM quarter, is what the products' bounds below are of.
+// number of chunks.  tcgen05 is not used: the chain's three dependent products a chunk would
+// each go through tensor memory and back, where mma.sync takes the accumulators as its
+// next left operand where they are.  The other kernels could stack two products with the
+// same right operand to its 128 rows (64 tokens are half its rate); that was not tried.
+// mma.sync's rate, measured as 8 clocks an instruction and SM quarter, is what the
+// products' bounds below are of.
 //
 // Times below are, unless said, of a training step's sequences: 4 x 4096 tokens of 24 heads
 // in 12 groups, 64 value rows, 128 key columns, bf16, that is 6144 chunks of a head.
@@ -900,10 +901,11 @@ __global__ void __launch_bounds__(4 * NP) k_delta_join(DeltaDims d, DeltaWs w) {
 // Left operands are two fp16 planes of rows scaled by their largest value, K is one
 // (bf16 inputs) and X two: 316 products of 16 x 8 x 16 a chunk, where three planes of
 // bf16 take 504.  A warp issues its strip's at 8 clocks each, which bounds a chunk by 1.3 us;
-// it takes 2.9 with a block an SM and 5.1 with two (168 registers a thread, so that two
-// fit), the rest of which is the accumulators' way into operands: maxima, scales, planes.
-// 200 us a pass (96 chains of 64 chunks); two warps a strip, which exchange halves, were
-// slower (3.3).  KEEP: also writes b e^G Z, for the backward.
+// it takes 3.2 with a block an SM and 5.0 with two, the rest of which is the accumulators'
+// way into operands: maxima, scales, planes.  209 us a pass (96 chains of 64 chunks); two
+// warps a strip, which exchange halves, were slower.  KEEP: also writes b e^G Z, for the
+// backward.  (Two blocks of five warps put three on one quarter of the SM, which holds three of
+// 168 registers a thread: the bound that the compiler takes from two blocks of six warps.)
 //
 // Few heads leave most of the machine idle, so a long sequence is cut into W segments of cs
 // chunks.  A chunk's step is linear in the state and the values, row by row: the state
@@ -1381,7 +1383,7 @@ struct GradSmem {
 // cancels in their difference, which a step whose decay is 0 does not pass on (gates_of).
 // Twelve products of 64 x 64 x 64 to 128 a tile of value rows, whose operands each become
 // planes in shared memory first: 700 us, 32 thousand clocks a head and chunk of an SM where
-// the products alone take 11.  Issue slots are 44 % used, the tensor cores 26 %; a second
+// the products alone take 11.  Issue slots are 40 % used, the tensor cores 28 %; a second
 // block does not fit (shared memory), and fetching the next head's tiles into registers
 // spills.
 template <typename T, typename TO, int NP>
@@ -1901,21 +1903,24 @@ __global__ void __launch_bounds__(256)
 // the machine; each block sums its heads in registers.  Blocks, and forward and backward
 // of 1 x 1024 and 1 x 256 tokens of 64 heads in 8 groups: gradient 152, outputs 608: 403 and
 // 150 us; 304 and 1216: 409 and 135; 608 and 2432: 412 and 136.
-constexpr int kGradBlocks = 2 * 152, kOutBlocks = 8 * 152;
+constexpr int kGradBlocks = 2 * kRuleSms, kOutBlocks = 8 * kRuleSms;
 
 // Segments of the chains: as many, up to 32 of at least 8 chunks, as make the modelled time
-// shortest.  Measured with 128 key columns: a chunk of the chain takes 2.9 us with a block
-// an SM and 5.1 with two (which fit); of the extra pass, which has the blocks of the moves
-// as well and writes nothing on its way, 3.2 with few blocks, 4.5 with up to two an SM and
-// 3.8 for every two from there; a segment's join 3.8 us, more where the machine is full.
-// 8192 tokens, the three together against one segment: 1 head of 64 x 128 116 and 357 us,
-// 16 heads 162 and 373, 24 heads 225 and 373, 48 heads (not cut) 395 in four.
+// shortest.  The model is of the forward's chain of bf16 inputs with 128 key columns, and every
+// type, size and direction takes its choice, so that the states that the backward forms
+// again are the forward's: a chunk of the chain takes 2.9 us with a block an SM and 5.1
+// with two (which fit; 3.2 and 5.0 since a chunk's part of the state is summed apart); of the
+// extra pass, which has the blocks of the moves as well and writes nothing on its way, 3.2
+// with few blocks, 4.5 with up to two an SM and 3.8 for every two from there; a segment's
+// join 3.8 us, more where the machine is full.  8192 tokens of 64 value rows, the three
+// together: 8 heads 153 us, 16 163, 24 238; one segment takes 391, as of 48 heads, which are
+// not cut.
 void segments(DeltaDims* d) {
   const double heads = (double)d->B * d->H, vt = (d->Ps + kC - 1) / kC, mt = d->NP / kC;
-  auto waves = [](double blocks) { return ceil(blocks / (2 * 152)); };
-  auto chain = [&](double blocks) { return blocks <= 152 ? 2.9 : 5.1 * waves(blocks); };
+  auto waves = [](double blocks) { return ceil(blocks / (2 * kRuleSms)); };
+  auto chain = [&](double blocks) { return blocks <= kRuleSms ? 2.9 : 5.1 * waves(blocks); };
   auto ends = [&](double blocks) {
-    return blocks <= 100 ? 3.2 : blocks <= 2 * 152 ? 4.5 : 3.8 * waves(blocks);
+    return blocks <= 100 ? 3.2 : blocks <= 2 * kRuleSms ? 4.5 : 3.8 * waves(blocks);
   };
   d->W = 1, d->cs = d->nc;
   double best = d->nc * chain(heads * vt);
@@ -2107,8 +2112,8 @@ int delta_backward(const DeltaDims& d, const DeltaIn& in, const DeltaGrads& g, c
                static_cast<TO*>(g.dbeta));
   if (d.nb > 1) {
     const int64_t m = (int64_t)d.B * d.T * d.G * d.N, blocks = (m + 255) / 256;
-    DELTA_LAUNCH("k_delta_sum", k_delta_sum<TO>, blocks < 152 * 8 ? blocks : 152 * 8, 256, 0, w.dqp,
-                 w.dkp, d.nb, m, dq, dk);
+    DELTA_LAUNCH("k_delta_sum", k_delta_sum<TO>, blocks < kRuleSms * 8 ? blocks : kRuleSms * 8, 256, 0,
+                 w.dqp, w.dkp, d.nb, m, dq, dk);
   }
   DELTA_LAUNCH("k_delta_params", k_delta_params, d.H, 256, 0, w.part, d.B, d.H, d.nc, g.dA,
                g.ddt_bias);

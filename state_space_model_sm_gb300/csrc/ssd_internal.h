@@ -24,12 +24,16 @@ struct Dims {
 // ssd_api.cu).  Kernels whose bounded waits expire store SSD_ERR_TIMEOUT there.
 int* device_status_ptr();
 
-// SM count of the current device (152, the GB300's, where the query fails).
+// SMs that the rules are of which decide how a sum is split or how large a workspace is:
+// the GB300's, whatever the device, so that neither results nor sizes depend on it.
+constexpr int kRuleSms = 152;
+
+// SM count of the current device (the GB300's where the query fails).
 inline int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 152;
+    return kRuleSms;
   return sms;
 }
 

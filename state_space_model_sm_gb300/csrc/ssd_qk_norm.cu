@@ -526,7 +526,7 @@ int qk_dims(const ssd_qk_norm_shape* s, QkDims* d) {
 // whole; 1024 tokens of 32: 6.2 and 8.2).
 void split(QkDims* d, int per) {
   const int64_t rows = (int64_t)d->B * d->T, n = d->HQ + d->HK;
-  int64_t parts = 152 * 16 / rows;
+  int64_t parts = kRuleSms * 16 / rows;
   const int64_t most = (n + per - 1) / per;
   parts = parts < 1 ? 1 : parts > most ? most : parts;
   d->parts = (int)parts;
